@@ -59,12 +59,16 @@ typedef int pkv_status;
 #define PKV_DEVERR_SLOT 0x2u      /* slot outside [0, num_blocks * 16) */
 #define PKV_DEVERR_CONTEXT 0x4u   /* context_len > 16 * max_blocks_per_seq */
 #define PKV_DEVERR_TIMEOUT 0x8u   /* an internal wait gave up; the output is invalid */
+#define PKV_DEVERR_QUERY 0x10u    /* query_starts decreases, leaves [0, num_tokens], or gives a tree over 64 drafts */
+#define PKV_DEVERR_POSITION 0x20u /* position outside [0, max_positions) of a row that is not padding */
 
 #define PKV_BLOCK_TOKENS 16
 #define PKV_ATTN_HEAD_DIM 128   /* head_dim of pkv_attn_decode */
 #define PKV_ATTN_MAX_GROUP 8    /* max num_q_heads / num_kv_heads */
 #define PKV_ATTN_MAX_SEQS 4096  /* max num_seqs of one pkv_attn_decode call */
 #define PKV_ATTN_MAX_CTAS 2048  /* max num_ctas of one pkv_attn_decode call */
+#define PKV_TREE_MAX_DRAFTS 64  /* max drafted tokens of one sequence in pkv_attn_tree */
+#define PKV_ROPE_MAX_HEAD_DIM 256 /* max head_dim of pkv_qk_norm_rope_append */
 
 /* Library version (major * 10000 + minor * 100 + patch). */
 int pkv_version(void);
@@ -253,6 +257,118 @@ pkv_status pkv_attn_decode_ex(const void* q, const void* k_cache, const void* v_
                               const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
                               int head_dim, int num_blocks, int block_tokens, float scale, int num_ctas,
                               void* workspace, size_t workspace_bytes, void* out, void* stream);
+
+/*
+ * pkv_qk_norm_rope_append -- a layer's way from its q, k, v projections into
+ * the cache in one pass: the RMS norm of every query and key head (optional),
+ * the rotary position embedding of both, and pkv_append of the keys and
+ * values. Per token t and head row x of head_dim values, in fp32 with one
+ * rounding at the end:
+ *   y = x / sqrt(mean(x^2) + eps) * weight        (y = x when weight is NULL)
+ *   (a, b) -> (a cos - b sin, a sin + b cos)       for each rotated pair of y
+ * Angle i of position p: cos_sin[p][i] is its cosine, cos_sin[p][rotary_dim /
+ * 2 + i] its sine. Pair i is (y[i], y[i + rotary_dim / 2]), or (y[2 i], y[2 i
+ * + 1]) when interleaved != 0; values from rotary_dim on are not rotated.
+ *   q, k, v       : device bf16, [num_tokens] rows of num_q_heads (k, v:
+ *                   num_kv_heads) * head_dim contiguous values, one row every
+ *                   q_stride (k_stride, v_stride) values -- views of one fused
+ *                   projection as they are; strides are multiples of 8 and no
+ *                   shorter than the row
+ *   q_weight, k_weight : device bf16 [head_dim], or NULL for no norm
+ *   cos_sin       : device fp32 [max_positions][rotary_dim]; may be NULL when
+ *                   rotary_dim is 0 (no rotation)
+ *   positions     : device int32 [num_tokens] (may be NULL when rotary_dim is
+ *                   0); outside [0, max_positions) sets PKV_DEVERR_POSITION
+ *                   unless the row is padding, and is clamped
+ *   slot_mapping  : as in pkv_append: a negative slot marks a padding row,
+ *                   whose key and value are not written (its q_out row is); a
+ *                   slot past the pool is skipped and sets PKV_DEVERR_SLOT
+ *   q_out         : device bf16 [num_tokens][num_q_heads][head_dim]; must not
+ *                   overlap q, k or v
+ *   k_cache, v_cache, block_tokens : as in pkv_append_ex
+ * head_dim: a multiple of 8 up to 256; rotary_dim: a multiple of 16 up to
+ * head_dim (PKV_EUNSUPPORTED otherwise). bf16 pointers and cos_sin are 16-byte
+ * aligned. Slots must be distinct. cs2680 Lecture 10, §10.3 (the append).
+ */
+pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                   const void* v, int64_t v_stride, const void* q_weight,
+                                   const void* k_weight, float eps, const float* cos_sin,
+                                   int max_positions, int rotary_dim, int interleaved,
+                                   const int32_t* positions, const int64_t* slot_mapping, int num_tokens,
+                                   int num_q_heads, int num_kv_heads, int head_dim, void* q_out,
+                                   void* k_cache, void* v_cache, int num_blocks, int block_tokens,
+                                   uint32_t* device_error, void* stream);
+
+/*
+ * pkv_attn_prefill -- causal attention of whole prompts, or of chunks of
+ * them, over the cache that already holds their tokens (pkv_append first).
+ *
+ * The batch's query rows are packed: sequence s owns rows query_starts[s] ..
+ * query_starts[s + 1] of q and out (n_s rows, possibly none), its last n_s
+ * tokens; context_lens[s] counts all its tokens in the cache, these included.
+ * Row i of the sequence is the token at position p = context_lens[s] - n_s + i
+ * and sees the keys of positions 0 .. p:
+ *   x_j = scale * <q[row, h], K[table[s][j / b]][g][j % b]>,  j <= p
+ *   out[row, h] = sum_j softmax(x)_j * V[table[s][j / b]][g][j % b]
+ * with b = block_tokens and KV head g = h / (Hq / Hkv), so a first prompt, a
+ * later chunk of one, the rest of a prompt whose prefix was cached, and decode
+ * rows (n_s = 1) mix in one call (cs2680 Lecture 10, §10.3, step three, for
+ * many query rows). bf16 inputs and output, fp32 sums and softmax.
+ *   q, out        : device bf16 [num_tokens][num_q_heads][128]
+ *   query_starts  : device int32 [num_seqs + 1], non-decreasing; rows of q
+ *                   outside [query_starts[0], query_starts[num_seqs]) belong
+ *                   to no sequence and their out rows are left as they were
+ *   block_tables, context_lens, caches : as in pkv_attn_decode_ex
+ *   workspace     : device scratch of pkv_attn_prefill_workspace_size() bytes,
+ *                   256-byte aligned, its first 256 bytes zeroed once
+ *                   (pkv_attn_workspace_init); the first 4 bytes are the
+ *                   device error word, the rest carries nothing from one call
+ *                   to the next. Calls that share a workspace must not
+ *                   overlap on the GPU.
+ * What a row does not see never reaches it: keys and values behind p, rows of
+ * the last block past the context and unused blocks may hold anything, NaN
+ * included. A row that sees nothing gives zeros.
+ * Limits: as pkv_attn_decode_ex, num_tokens >= 0 and scale >= 0. Device-side
+ * errors are handled as there; besides, query_starts out of order or range is
+ * clamped and sets PKV_DEVERR_QUERY, and a chunk longer than its context sets
+ * PKV_DEVERR_CONTEXT (rows before position 0 see nothing).
+ */
+pkv_status pkv_attn_prefill(const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                            const int32_t* query_starts, int num_seqs, int num_tokens, int num_q_heads,
+                            int num_kv_heads, int head_dim, int num_blocks, int block_tokens, float scale,
+                            void* workspace, size_t workspace_bytes, void* out, void* stream);
+
+/* Bytes of device scratch for pkv_attn_prefill and pkv_attn_tree on the
+ * current device, whatever the batch; 0 when no device is present. */
+size_t pkv_attn_prefill_workspace_size(void);
+
+/*
+ * pkv_attn_tree -- attention of drafted token trees over the cache: the
+ * verification step of speculative decoding. Sequence s has the drafted
+ * tokens query_starts[s] .. query_starts[s + 1] (n_s of them, at most 64) of
+ * the packed q, k_draft, v_draft and out; they are not in the cache. Draft i
+ * sees every token of the sequence's context in the cache (context_lens[s],
+ * not counting drafts) and the drafts j of its own sequence whose bit j is
+ * set in tree_masks -- its ancestors and, normally, itself:
+ *   x = scale * <q[i, h], k>  over the context's keys and the seen k_draft[j]
+ *   out[i, h] = the softmax-weighted sum of the same tokens' values.
+ * The cache and the block manager's state stay as they were: once the caller
+ * has chosen a path, pkv_append with slot -1 for the other drafts writes the
+ * accepted tokens' keys and values.
+ *   k_draft, v_draft : device bf16 [num_tokens][num_kv_heads][128]
+ *   tree_masks    : device int64 [num_tokens]; bits at or above n_s are
+ *                   ignored
+ * Everything else, NaN in what a draft does not see included, as in
+ * pkv_attn_prefill; a sequence with more than 64 drafts sets PKV_DEVERR_QUERY
+ * and its first 64 are computed.
+ */
+pkv_status pkv_attn_tree(const void* q, const void* k_draft, const void* v_draft, const int64_t* tree_masks,
+                         const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                         int max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_starts,
+                         int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                         int num_blocks, int block_tokens, float scale, void* workspace,
+                         size_t workspace_bytes, void* out, void* stream);
 
 /*
  * Cascade attention -- pkv_attn_decode for a batch whose sequences share

@@ -6,6 +6,7 @@ module fails loudly if libpkv.so has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -26,12 +27,15 @@ DEVERR_BLOCK_ID = 0x1
 DEVERR_SLOT = 0x2
 DEVERR_CONTEXT = 0x4
 DEVERR_TIMEOUT = 0x8
+DEVERR_QUERY = 0x10
+DEVERR_POSITION = 0x20
 
 BLOCK_TOKENS = 16
 HEAD_DIM = 128
 MAX_GROUP = 8
 MAX_SEQS = 4096
 MAX_CTAS = 2048
+TREE_MAX_DRAFTS = 64
 
 EXPORTED = [
     "pkv_version", "pkv_status_string", "pkv_last_cuda_error", "pkv_read_device_error",
@@ -44,7 +48,8 @@ EXPORTED = [
     "pkv_bm_newest_running", "pkv_bm_slots", "pkv_step_layout", "pkv_decode_step_host",
     "pkv_attn_cascade_workspace_size", "pkv_cascade_staging_size", "pkv_cascade_plan", "pkv_attn_decode_cascade",
     "pkv_attn_decode_wait_test", "pkv_attn_decode_cuda_cores", "pkv_attn_workspace_fixed_bytes",
-    "pkv_attn_launch_ctas",
+    "pkv_attn_launch_ctas", "pkv_attn_prefill", "pkv_attn_prefill_workspace_size", "pkv_attn_tree",
+    "pkv_qk_norm_rope_append",
 ]
 BLOCK_SIZES = (8, 16, 32, 64)
 
@@ -137,6 +142,13 @@ def _load() -> ctypes.CDLL:
         "pkv_cascade_plan": (i32, [i32, i32, i32, i32, vp, vp, vp, vp, sz, vp, sz, vp]),
         "pkv_attn_decode_cascade": (i32, [vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, f32, i32, vp, vp, vp, sz,
                                           vp, vp]),
+        "pkv_attn_prefill_workspace_size": (sz, []),
+        "pkv_attn_prefill": (i32, [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, vp, sz, vp,
+                                   vp]),
+        "pkv_attn_tree": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, vp,
+                                sz, vp, vp]),
+        "pkv_qk_norm_rope_append": (i32, [vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, i32, i32, i32, vp, vp, i32, i32,
+                                          i32, i32, vp, vp, vp, i32, i32, vp, vp]),
         "pkv_decode_step_host": (i32, [vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz, vp, vp,
                                        vp, vp]),
     }
@@ -144,7 +156,6 @@ def _load() -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    del i64
     return lib
 
 
@@ -489,6 +500,221 @@ def attn_decode_static(q, k_cache, v_cache, block_tables, context_lens, scale, o
                                        float(scale), _ptr(device_error), _ptr(out), _stream(stream)),
            "pkv_attn_decode_static")
     return out
+
+
+# ---------------------------------------------------------------------------
+# many query rows per sequence: prompts, draft trees, and the way into the cache
+
+
+@contextlib.contextmanager
+def _launch_on(stream, **tensors):
+    """Checks that the named tensors share one CUDA device; inside, that device
+    is current and new tensors belong to `stream` (default: the device's
+    current stream). Yields the stream's handle."""
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{name} is on {t.device}, other tensors on {device}")
+    if stream is None and torch.cuda.current_device() == device.index:
+        yield torch.cuda.current_stream().cuda_stream
+        return
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+            return
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+        if s.device != device:
+            raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
+        with torch.cuda.stream(s):
+            yield s.cuda_stream
+
+
+class PrefillWorkspace:
+    """Device scratch for attn_prefill and attn_tree, of any batch: the error
+    word, then the partial results of rows whose keys are split. Calls that
+    share one must not overlap on the GPU."""
+
+    def __init__(self, device=None, stream=None):
+        dev = torch.device(device or "cuda")
+        with torch.cuda.device(dev):
+            self.nbytes = int(_lib.pkv_attn_prefill_workspace_size())
+            if self.nbytes == 0:
+                raise PkvError(PKV_ECUDA, "pkv_attn_prefill_workspace_size")
+            self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=dev)
+            off = (-self.buffer.data_ptr()) % 256
+            self.tensor = self.buffer[off : off + self.nbytes]
+            # only the header has to hold zeros
+            _check(_lib.pkv_attn_workspace_init(self.tensor.data_ptr(), 256, _stream(stream)),
+                   "pkv_attn_workspace_init")
+
+    @property
+    def ptr(self) -> int:
+        return self.tensor.data_ptr()
+
+    def read_error(self, clear: bool = True, stream=None) -> int:
+        return read_device_error(self.tensor[:4].view(torch.int32), clear, stream)
+
+
+def _rows_shapes(q, k_cache, v_cache, block_tables, context_lens, query_starts, out):
+    for t, dt, name in ((q, torch.bfloat16, "q"), (k_cache, torch.bfloat16, "k_cache"),
+                        (v_cache, torch.bfloat16, "v_cache"), (block_tables, torch.int32, "block_tables"),
+                        (context_lens, torch.int32, "context_lens"), (query_starts, torch.int32, "query_starts")):
+        _need(t, dt, name)
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [T, Hq, D] and caches [NB, Hkv, block_tokens, D]")
+    T, hq, d = q.shape
+    nb, hkv, bt, d2 = k_cache.shape
+    if d != d2 or v_cache.shape != k_cache.shape or bt not in BLOCK_SIZES:
+        raise ValueError("q [T, Hq, D] and caches [NB, Hkv, block_tokens in (8, 16, 32, 64), D] must agree")
+    if block_tables.dim() != 2 or context_lens.shape != (block_tables.shape[0],):
+        raise ValueError("block_tables must be [B, W] and context_lens [B]")
+    B, width = block_tables.shape
+    if query_starts.shape != (B + 1,):
+        raise ValueError("query_starts must be [B + 1]")
+    if out is not None:
+        _need(out, torch.bfloat16, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must be shaped like q")
+    return T, hq, d, nb, hkv, bt, B, width
+
+
+def attn_prefill(q, k_cache, v_cache, block_tables, context_lens, query_starts, scale, out=None, workspace=None,
+                 stream=None):
+    """Causal attention of packed prompt chunks over the cache that holds their
+    tokens: rows query_starts[s] .. query_starts[s + 1] of q [T, Hq, 128] are
+    the last tokens of sequence s, whose context_lens[s] tokens are all in the
+    cache. Returns out [T, Hq, 128]; rows of no sequence are left as they were
+    (zeros in an `out` made here)."""
+    T, hq, d, nb, hkv, bt, B, width = _rows_shapes(q, k_cache, v_cache, block_tables, context_lens, query_starts, out)
+    with _launch_on(stream, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
+                    query_starts=query_starts, out=out, workspace=workspace and workspace.tensor) as st:
+        if out is None:
+            out = torch.zeros_like(q)
+        if workspace is None:
+            workspace = PrefillWorkspace(q.device)
+        _check(_lib.pkv_attn_prefill(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), width,
+                                     _ptr(context_lens), _ptr(query_starts), B, T, hq, hkv, d, nb, bt, float(scale),
+                                     workspace.ptr, workspace.nbytes, _ptr(out), st), "pkv_attn_prefill")
+    return out
+
+
+def attn_tree(q, k_draft, v_draft, tree_masks, k_cache, v_cache, block_tables, context_lens, query_starts, scale,
+              out=None, workspace=None, stream=None):
+    """Attention of drafted token trees: draft i (row i of q [T, Hq, 128],
+    k_draft, v_draft [T, Hkv, 128], packed by query_starts) sees the
+    context_lens[s] tokens of its sequence in the cache and the drafts j of the
+    sequence whose bit j is set in tree_masks[i] (int64, see tree_masks()).
+    Returns out [T, Hq, 128]; the cache is not written."""
+    T, hq, d, nb, hkv, bt, B, width = _rows_shapes(q, k_cache, v_cache, block_tables, context_lens, query_starts, out)
+    _need(k_draft, torch.bfloat16, "k_draft")
+    _need(v_draft, torch.bfloat16, "v_draft")
+    _need(tree_masks, torch.int64, "tree_masks")
+    if k_draft.shape != (T, hkv, d) or v_draft.shape != (T, hkv, d) or tree_masks.shape != (T,):
+        raise ValueError("k_draft, v_draft must be [T, Hkv, D] and tree_masks [T]")
+    with _launch_on(stream, q=q, k_draft=k_draft, v_draft=v_draft, tree_masks=tree_masks, k_cache=k_cache,
+                    v_cache=v_cache, block_tables=block_tables, context_lens=context_lens, query_starts=query_starts,
+                    out=out, workspace=workspace and workspace.tensor) as st:
+        if out is None:
+            out = torch.zeros_like(q)
+        if workspace is None:
+            workspace = PrefillWorkspace(q.device)
+        _check(_lib.pkv_attn_tree(_ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(tree_masks), _ptr(k_cache), _ptr(v_cache),
+                                  _ptr(block_tables), width, _ptr(context_lens), _ptr(query_starts), B, T, hq, hkv, d,
+                                  nb, bt, float(scale), workspace.ptr, workspace.nbytes, _ptr(out), st),
+               "pkv_attn_tree")
+    return out
+
+
+def tree_masks(parents) -> list[int]:
+    """One sequence's rows of attn_tree's tree_masks from its drafts' parents:
+    parents[i] is the index of an earlier draft, or -1 for a draft that follows
+    the context. Row i has the bits of i and of its ancestors, as int64 values
+    (bit 63 is the sign)."""
+    if len(parents) > TREE_MAX_DRAFTS:
+        raise ValueError(f"a tree has at most {TREE_MAX_DRAFTS} drafts")
+    rows: list[int] = []
+    for i, p in enumerate(parents):
+        if not -1 <= p < i:
+            raise ValueError("a draft's parent is an earlier draft, or -1")
+        rows.append((rows[p] if p >= 0 else 0) | (1 << i))
+    return [r - (1 << 64) if r >> 63 else r for r in rows]
+
+
+def rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """cos and sin of every position's angles p * base^(-2 i / rotary_dim), fp32
+    [max_positions, rotary_dim] (cosines, then sines), computed in 64 bits: at
+    position 100,000 a 32-bit angle is off by up to 0.004."""
+    if max_positions < 1 or rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rope_table needs at least one position and an even rotary_dim")
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    angle = torch.arange(max_positions, dtype=torch.float64)[:, None] * float(base) ** (-2.0 * i / rotary_dim)
+    return torch.cat([angle.cos(), angle.sin()], dim=1).float().contiguous().to(device or "cuda")
+
+
+def _need_rows(t: torch.Tensor, name: str, shape) -> int:
+    """bf16 [T, H, D] whose rows are contiguous; returns the stride of a token."""
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    T, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0) if T > 1 else h * d
+
+
+def qk_norm_rope_append(q, k, v, cos_sin, positions, slot_mapping, k_cache, v_cache, q_weight=None, k_weight=None,
+                        eps: float = 1e-6, interleaved: bool = False, q_out=None, device_error=None, stream=None):
+    """RMS norm of every head of q [T, Hq, D] and k [T, Hkv, D] (skipped where
+    the weight is None), rotation by cos_sin[positions] (fp32 [positions,
+    rotary_dim], see rope_table(); None: no rotation), and the append of k and
+    v to slot_mapping's slots of the caches. q, k, v may be views of one fused
+    projection. Returns the normed, rotated queries [T, Hq, D]."""
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [T, Hq, D] and caches [NB, Hkv, block_tokens, D]")
+    T, hq, d = q.shape
+    nb, hkv, bt, d2 = k_cache.shape
+    if d != d2 or v_cache.shape != k_cache.shape or bt not in BLOCK_SIZES:
+        raise ValueError("q [T, Hq, D] and caches [NB, Hkv, block_tokens in (8, 16, 32, 64), D] must agree")
+    strides = [_need_rows(t, name, (T, h, d)) for t, name, h in ((q, "q", hq), (k, "k", hkv), (v, "v", hkv))]
+    _need(k_cache, torch.bfloat16, "k_cache")
+    _need(v_cache, torch.bfloat16, "v_cache")
+    _need(slot_mapping, torch.int64, "slot_mapping")
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [T]")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, torch.bfloat16, name)
+            if w.shape != (d,):
+                raise ValueError(f"{name} must be [D]")
+    max_positions = rotary = 0
+    if cos_sin is not None:
+        _need(cos_sin, torch.float32, "cos_sin")
+        _need(positions, torch.int32, "positions")
+        if cos_sin.dim() != 2 or positions.shape != (T,):
+            raise ValueError("cos_sin must be [positions, rotary_dim] and positions [T]")
+        max_positions, rotary = cos_sin.shape
+    if q_out is not None:
+        _need(q_out, torch.bfloat16, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must be shaped like q")
+    with _launch_on(stream, q=q, k=k, v=v, cos_sin=cos_sin, positions=positions if rotary else None,
+                    slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache, q_weight=q_weight, k_weight=k_weight,
+                    q_out=q_out, device_error=device_error) as st:
+        if q_out is None:
+            q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
+        _check(_lib.pkv_qk_norm_rope_append(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
+                                            _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), max_positions,
+                                            rotary, int(interleaved), _ptr(positions) if rotary else None,
+                                            _ptr(slot_mapping), T, hq, hkv, d, _ptr(q_out), _ptr(k_cache),
+                                            _ptr(v_cache), nb, bt, _ptr(device_error), st), "pkv_qk_norm_rope_append")
+    return q_out
 
 
 # ---------------------------------------------------------------------------

@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libpkv.so")
-SOURCES = ["pkv_attn.cu", "pkv_cache_ops.cu", "pkv_block_manager.cpp"]
+SOURCES = ["pkv_attn.cu", "pkv_prefill.cu", "pkv_qk_write.cu", "pkv_cache_ops.cu", "pkv_block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
