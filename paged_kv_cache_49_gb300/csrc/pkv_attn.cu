@@ -19,15 +19,9 @@
 #include "pkv_decode_kernel.cuh"
 
 namespace pkv {
-namespace attn {
 
-// ---------------------------------------------------------------------------
-// host side
-
-using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
         void* ptr = nullptr;
@@ -35,10 +29,15 @@ EncodeTiledFn encode_fn() {
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
                 cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
     });
     return fn;
 }
+
+namespace attn {
+
+// ---------------------------------------------------------------------------
+// host side
 
 // View of a cache as token rows (num_blocks * Hkv * block_tokens rows of 128
 // bf16), 3-D: {64 columns, rows, 2 column halves} with the halves 128 bytes
@@ -47,7 +46,7 @@ EncodeTiledFn encode_fn() {
 // in shared memory as the two halves one after the other, each in the
 // 128-byte swizzle.
 bool make_cache_map(CUtensorMap* map, const void* base, int num_blocks, int hkv, int block_tokens) {
-    EncodeTiledFn enc = encode_fn();
+    const auto enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t rows = static_cast<cuuint64_t>(num_blocks) * hkv * block_tokens;
     cuuint64_t dims[3] = {64, rows, 2};

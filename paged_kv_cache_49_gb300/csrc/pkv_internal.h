@@ -1,6 +1,8 @@
 // Host-side helpers shared by the library's translation units.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -11,6 +13,9 @@ namespace pkv {
 
 // Record a CUDA error for pkv_last_cuda_error (per host thread).
 void record_cuda_error(cudaError_t e);
+
+// The driver's tensor-map encoder, null if it has none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -1,128 +1,103 @@
 // Attention of many query rows per sequence over the paged cache: causal
 // prompt attention (pkv_attn_prefill) and draft-tree attention
 // (pkv_attn_tree).
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <mutex>
+#include <vector>
 
 #include "pkv_internal.h"
-#include "pkv_ptx.cuh"
+#include "pkv_prefill_kernel.cuh"
 
 namespace pkv {
 namespace prefill {
 
-constexpr int kDim = PKV_ATTN_HEAD_DIM;
-constexpr size_t kWsHeader = 256;
-
-struct Params {
-    const __nv_bfloat16* q;
-    const __nv_bfloat16* k_cache;
-    const __nv_bfloat16* v_cache;
-    const __nv_bfloat16* k_draft;  // null: prefill
-    const __nv_bfloat16* v_draft;
-    const int64_t* masks;
-    __nv_bfloat16* out;
-    const int32_t* block_tables;
-    const int32_t* context_lens;
-    const int32_t* query_starts;
-    uint32_t* err;
-    int num_seqs, num_tokens, hq, hkv, group, max_blocks, num_blocks, bt;
-    float scale_log2;
+// Per device, once: its SMs, and leave for the kernels' shared memory.
+struct DeviceInfo {
+    bool ok = false;
+    int grid = 0;
 };
 
-constexpr int kWarps = 8;
-
-// One warp per (token, query head), four head dims per lane, one key at a
-// time with the running maximum and sum of the softmax.
-template <bool kTree>
-__global__ void __launch_bounds__(kWarps * 32) rows_kernel(const Params p) {
-    const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int tok = static_cast<int>(w / p.hq);
-    if (tok >= p.num_tokens) return;
-    const int h = static_cast<int>(w - static_cast<long long>(tok) * p.hq);
-    const int g = h / p.group;
-    // last sequence that starts at or before the token
-    int lo = 0, hi = p.num_seqs;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(p.query_starts + mid + 1) > tok) hi = mid; else lo = mid + 1;
+DeviceInfo device_info() {
+    static std::mutex mu;
+    static std::vector<DeviceInfo> cache;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (static_cast<int>(cache.size()) <= dev) cache.resize(dev + 1);
+    DeviceInfo& d = cache[dev];
+    if (d.ok) return d;
+    int sms = 0;
+    cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(rows_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(rows_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        return {};
     }
-    const int s = lo;
-    if (s >= p.num_seqs) return;
-    const int start = __ldg(p.query_starts + s), end = __ldg(p.query_starts + s + 1);
-    if (tok < start) return;
-    uint32_t bad = 0;
-    if (start < 0 || end > p.num_tokens) bad |= PKV_DEVERR_QUERY;
-    const int first = max(start, 0), last = min(end, p.num_tokens);
-    const int n = last - first, i = tok - first;
-    if (kTree && n > PKV_TREE_MAX_DRAFTS) bad |= PKV_DEVERR_QUERY;
-    if (kTree && i >= PKV_TREE_MAX_DRAFTS) return;
-    int ctx = __ldg(p.context_lens + s);
-    const long long cap = static_cast<long long>(p.max_blocks) * p.bt;
-    if (ctx > cap) {
-        bad |= PKV_DEVERR_CONTEXT;
-        ctx = static_cast<int>(cap);
-    }
-    ctx = max(ctx, 0);
-    if (!kTree && n > ctx) bad |= PKV_DEVERR_CONTEXT;
-    const int seen = kTree ? ctx : max(0, ctx - n + i + 1);
-
-    float q[4];
-    const uint2 qv = *reinterpret_cast<const uint2*>(p.q + (static_cast<long long>(tok) * p.hq + h) * kDim + lane * 4);
-    q[0] = bf16_lo(qv.x); q[1] = bf16_hi(qv.x); q[2] = bf16_lo(qv.y); q[3] = bf16_hi(qv.y);
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    bool any = false;
-    auto add = [&](const __nv_bfloat16* kr, const __nv_bfloat16* vr) {
-        const uint2 kv = *reinterpret_cast<const uint2*>(kr + lane * 4);
-        const uint2 vv = *reinterpret_cast<const uint2*>(vr + lane * 4);
-        float x = q[0] * bf16_lo(kv.x) + q[1] * bf16_hi(kv.x) + q[2] * bf16_lo(kv.y) + q[3] * bf16_hi(kv.y);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-        x *= p.scale_log2;
-        const float m2 = fmaxf(m, x);
-        const float ref = m2 == -INFINITY ? 0.f : m2;
-        const float a = exp2f(m - ref), e = exp2f(x - ref);
-        m = m2;
-        l = l * a + e;
-        o[0] = o[0] * a + e * bf16_lo(vv.x);
-        o[1] = o[1] * a + e * bf16_hi(vv.x);
-        o[2] = o[2] * a + e * bf16_lo(vv.y);
-        o[3] = o[3] * a + e * bf16_hi(vv.y);
-        any = true;
-    };
-    for (int j = 0; j < seen; ++j) {
-        int blk = __ldg(p.block_tables + static_cast<long long>(s) * p.max_blocks + j / p.bt);
-        if (blk < 0 || blk >= p.num_blocks) {
-            bad |= PKV_DEVERR_BLOCK_ID;
-            blk = 0;
-        }
-        const long long row = (static_cast<long long>(blk) * p.hkv + g) * p.bt + j % p.bt;
-        add(p.k_cache + row * kDim, p.v_cache + row * kDim);
-    }
-    if (kTree) {
-        const uint64_t bits = static_cast<uint64_t>(__ldg(reinterpret_cast<const long long*>(p.masks) + tok));
-        for (int j = 0; j < min(n, PKV_TREE_MAX_DRAFTS); ++j)
-            if (bits >> j & 1) {
-                const long long row = static_cast<long long>(first + j) * p.hkv + g;
-                add(p.k_draft + row * kDim, p.v_draft + row * kDim);
-            }
-    }
-    const float inv = any ? 1.f / l : 0.f;
-    uint2 r;
-    r.x = pack_bf16x2(o[0] * inv, o[1] * inv);
-    r.y = pack_bf16x2(o[2] * inv, o[3] * inv);
-    *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(tok) * p.hq + h) * kDim + lane * 4) = r;
-    if (bad && lane == 0) atomicOr(p.err, bad);
+    d.grid = std::min(sms, kMaxGrid);
+    d.ok = true;
+    return d;
 }
 
-pkv_status run(const Params& p0, const void* q, const void* k_cache, const void* v_cache, const void* k_draft,
-               const void* v_draft, const int64_t* masks, bool tree, const int32_t* block_tables, int max_blocks_per_seq,
+// Workspace: header (error word), split items, then each range's two slots of
+// 256 row states and 256 rows of 128 fp32 values.
+constexpr size_t kWsSplits = kWsHeader, kWsStates = kWsSplits + sizeof(Split) * kMaxGrid;
+static_assert(kWsStates % 256 == 0, "alignment of the partial results");
+
+size_t workspace_bytes(int grid) {
+    return kWsStates + static_cast<size_t>(grid) * 2 * 2 * kRows * (sizeof(float2) + kDim * sizeof(float));
+}
+
+bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    const auto enc = tensor_map_encoder();
+    return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, ones,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Query rows: {64 columns, group heads, tokens, 2 column halves, KV heads};
+// a box is one half of a tile's tokens with their heads, one 128-byte row each.
+bool query_map(CUtensorMap* map, const void* q, int tokens, int hq, int hkv, int tpt) {
+    const cuuint64_t g = hq / hkv;
+    const cuuint64_t dims[5] = {64, g, static_cast<cuuint64_t>(tokens), 2, static_cast<cuuint64_t>(hkv)};
+    const cuuint64_t strides[4] = {256, static_cast<cuuint64_t>(hq) * 256, 128, g * 256};
+    const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(g), static_cast<cuuint32_t>(tpt), 1, 1};
+    return encode(map, q, 5, dims, strides, box);
+}
+
+// A cache as groups of 8 rows: {64 columns, 8 rows, 2 column halves, groups}.
+// A box is one block of one KV head; each of its row groups lands as its two
+// halves, one 1024-byte swizzle atom each.
+bool cache_map(CUtensorMap* map, const void* cache, int num_blocks, int hkv, int bt) {
+    const cuuint64_t dims[4] = {64, 8, 2, static_cast<cuuint64_t>(num_blocks) * hkv * (bt / 8)};
+    const cuuint64_t strides[3] = {256, 128, 2048};
+    const cuuint32_t box[4] = {64, 8, 2, static_cast<cuuint32_t>(bt / 8)};
+    return encode(map, cache, 4, dims, strides, box);
+}
+
+// Drafted keys or values, 8 tokens of one KV head a box, landing likewise.
+bool draft_map(CUtensorMap* map, const void* rows, int tokens, int hkv) {
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(tokens), 2, static_cast<cuuint64_t>(hkv)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(hkv) * 256, 128, 256};
+    const cuuint32_t box[4] = {64, 8, 2, 1};
+    return encode(map, rows, 4, dims, strides, box);
+}
+
+pkv_status run(const void* q, const void* k_cache, const void* v_cache, const void* k_draft, const void* v_draft,
+               const int64_t* masks, bool tree, const int32_t* block_tables, int max_blocks_per_seq,
                const int32_t* context_lens, const int32_t* query_starts, int num_seqs, int num_tokens, int num_q_heads,
                int num_kv_heads, int head_dim, int num_blocks, int block_tokens, float scale, void* workspace,
-               size_t workspace_bytes, void* out, cudaStream_t stream) {
+               size_t ws_bytes, void* out, cudaStream_t stream) {
     if (block_tokens != 8 && block_tokens != 16 && block_tokens != 32 && block_tokens != 64) return PKV_EUNSUPPORTED;
     if (num_tokens < 0 || num_seqs < 1 || num_q_heads < 1 || num_kv_heads < 1 || num_blocks < 1 ||
         max_blocks_per_seq < 1 || !std::isfinite(scale) || scale < 0.f)
@@ -141,34 +116,67 @@ pkv_status run(const Params& p0, const void* q, const void* k_cache, const void*
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(k_draft) ||
         !aligned16(v_draft) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return PKV_EINVAL;
-    if (workspace_bytes < kWsHeader) return PKV_EINVAL;
-    Params p = p0;
-    p.q = static_cast<const __nv_bfloat16*>(q);
-    p.k_cache = static_cast<const __nv_bfloat16*>(k_cache);
+    if (ws_bytes < workspace_bytes(1)) return PKV_EINVAL;
+    const DeviceInfo d = device_info();
+    if (!d.ok) return PKV_ECUDA;
+    const size_t per_cta = workspace_bytes(1) - workspace_bytes(0);
+    const int grid = static_cast<int>(std::min<size_t>(d.grid, (ws_bytes - workspace_bytes(0)) / per_cta));
+    Params p = {};
+    p.out = static_cast<__nv_bfloat16*>(out);
     p.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
-    p.k_draft = static_cast<const __nv_bfloat16*>(k_draft);
     p.v_draft = static_cast<const __nv_bfloat16*>(v_draft);
     p.masks = masks;
-    p.out = static_cast<__nv_bfloat16*>(out);
     p.block_tables = block_tables;
     p.context_lens = context_lens;
     p.query_starts = query_starts;
-    p.err = static_cast<uint32_t*>(workspace);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.err = reinterpret_cast<uint32_t*>(ws);
+    p.splits = reinterpret_cast<Split*>(ws + kWsSplits);
+    p.part_ml = reinterpret_cast<float2*>(ws + kWsStates);
+    p.part_o = reinterpret_cast<float*>(ws + kWsStates + static_cast<size_t>(grid) * 2 * 2 * kRows * sizeof(float2));
     p.num_seqs = num_seqs;
     p.num_tokens = num_tokens;
     p.hq = num_q_heads;
     p.hkv = num_kv_heads;
     p.group = num_q_heads / num_kv_heads;
+    p.tpt = kRows / p.group;
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = num_blocks;
     p.bt = block_tokens;
-    p.scale_log2 = scale * 1.4426950408889634f;
-    const long long warps = static_cast<long long>(num_tokens) * num_q_heads;
-    const long long grid = (warps + kWarps - 1) / kWarps;
-    if (grid >= (1ll << 31)) return PKV_ERANGE;
-    if (tree) rows_kernel<true><<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(p);
-    else rows_kernel<false><<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    // a scale of zero weighs every seen key alike: as does any scale this
+    // small, without 0 * -infinity at the masked ones
+    p.scale_log2 = std::max(scale * 1.4426950408889634f, 1e-30f);
+    CUtensorMap tm_q, tm_k, tm_v, tm_kd, tm_vd;
+    if (!query_map(&tm_q, q, num_tokens, num_q_heads, num_kv_heads, p.tpt) ||
+        !cache_map(&tm_k, k_cache, num_blocks, num_kv_heads, block_tokens) ||
+        !cache_map(&tm_v, v_cache, num_blocks, num_kv_heads, block_tokens))
+        return PKV_ECUDA;
+    if (tree) {
+        if (!draft_map(&tm_kd, k_draft, num_tokens, num_kv_heads) || !draft_map(&tm_vd, v_draft, num_tokens, num_kv_heads))
+            return PKV_ECUDA;
+    } else {
+        tm_kd = tm_k;  // not read
+        tm_vd = tm_v;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, tree ? rows_kernel<true> : rows_kernel<false>, tm_q, tm_k, tm_v, tm_kd, tm_vd, p);
+    if (e == cudaSuccess) {
+        // launched early, so that it is there when the last CTA ends
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3(grid, 8);
+        cfg.blockDim = dim3(kMergeWarps * 32);
+        cfg.dynamicSmemBytes = 0;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, merge_kernel, p);
+    }
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return PKV_ECUDA;
@@ -184,9 +192,8 @@ using namespace pkv;
 extern "C" {
 
 size_t pkv_attn_prefill_workspace_size(void) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    return prefill::kWsHeader;
+    const prefill::DeviceInfo d = prefill::device_info();
+    return d.ok ? prefill::workspace_bytes(d.grid) : 0;
 }
 
 pkv_status pkv_attn_prefill(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
@@ -194,7 +201,7 @@ pkv_status pkv_attn_prefill(const void* q, const void* k_cache, const void* v_ca
                             int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
                             int num_blocks, int block_tokens, float scale, void* workspace, size_t workspace_bytes,
                             void* out, void* stream) {
-    return prefill::run({}, q, k_cache, v_cache, nullptr, nullptr, nullptr, false, block_tables, max_blocks_per_seq,
+    return prefill::run(q, k_cache, v_cache, nullptr, nullptr, nullptr, false, block_tables, max_blocks_per_seq,
                         context_lens, query_starts, num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim,
                         num_blocks, block_tokens, scale, workspace, workspace_bytes, out, as_stream(stream));
 }
@@ -204,7 +211,7 @@ pkv_status pkv_attn_tree(const void* q, const void* k_draft, const void* v_draft
                          const int32_t* context_lens, const int32_t* query_starts, int num_seqs, int num_tokens,
                          int num_q_heads, int num_kv_heads, int head_dim, int num_blocks, int block_tokens,
                          float scale, void* workspace, size_t workspace_bytes, void* out, void* stream) {
-    return prefill::run({}, q, k_cache, v_cache, k_draft, v_draft, tree_masks, true, block_tables, max_blocks_per_seq,
+    return prefill::run(q, k_cache, v_cache, k_draft, v_draft, tree_masks, true, block_tables, max_blocks_per_seq,
                         context_lens, query_starts, num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim,
                         num_blocks, block_tokens, scale, workspace, workspace_bytes, out, as_stream(stream));
 }

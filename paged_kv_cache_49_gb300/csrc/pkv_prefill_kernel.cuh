@@ -1,0 +1,954 @@
+// Attention of many query rows per sequence over the paged cache, on the
+// fifth-generation tensor cores: causal prompt chunks and draft trees.
+//
+// A tile is 128 query rows of one KV head -- 128 / group tokens with all
+// their query heads, so a K or V byte serves the whole group -- against 128
+// keys: S = Q K^T into tensor memory, an online softmax in registers, P as
+// bf16 back into tensor memory over S, O += P V in tensor memory.
+//
+// An item is up to two tiles of one (sequence, KV head) against all their
+// keys. Its two streams (one accumulator and one softmax warpgroup each) run
+// in turn on the tensor core, so that one multiplies while the other takes
+// exponentials:
+//   - two tiles: each stream has its own query tile, both share every K and V
+//     tile;
+//   - one tile: the streams share the query tile and take the even and the
+//     odd key tiles; their states are joined at the end.
+//
+// The items of the batch, laid end to end by cost, are cut into one range per
+// CTA (one persistent CTA per SM), planned by every CTA from the lengths on
+// the device. A cut near an item's end moves there; any other leaves fp32
+// partial results that merge_kernel joins in a fixed order.
+//
+// What no row sees never enters a sum: masked scores are replaced before the
+// softmax, and of the value tiles that only some rows see in full, a warp
+// pair zeroes the rows past the end and the non-finite values before the
+// product; those are added to the rows that do see them at the end.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "pkv_ptx.cuh"
+#include "pkv_tcgen05.cuh"
+
+namespace pkv {
+namespace prefill {
+
+constexpr int kDim = PKV_ATTN_HEAD_DIM;
+constexpr int kRows = 128;    // query rows of a tile
+constexpr int kKeys = 128;    // keys of a tile
+constexpr int kStages = 5;    // K or V tiles in flight
+constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpClean = 10;  // and 11
+constexpr int kCleanBars = 8;  // more than the ring can hold
+
+constexpr uint32_t kTileBytes = kKeys * kDim * 2;
+constexpr uint32_t kTmemColumns = 512;
+constexpr uint32_t kTmemO = 256;  // S0, S1, O0, O1 of 128 columns each
+
+// Cost units of the work line: one key of an item's two tiles is 8, of a
+// single tile 5; an item's fixed work is kItemCost.
+constexpr int kCostTwo = 8, kCostOne = 5, kItemCost = 8 * 256;
+constexpr int kSnap = 8 * 256;      // a cut this near an item's end moves there
+constexpr int kMinRange = 8 * 256;  // least cost of a CTA's range
+
+constexpr size_t kWsHeader = 256;
+constexpr int kMaxGrid = 1024;
+
+struct Params {
+    __nv_bfloat16* out;
+    const __nv_bfloat16* v_cache;
+    const __nv_bfloat16* v_draft;
+    const int64_t* masks;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* query_starts;
+    uint32_t* err;
+    struct Split* splits;   // [grid]
+    float2* part_ml;        // [2 * grid][256]
+    float* part_o;          // [2 * grid][256][128]
+    int num_seqs, num_tokens, hq, hkv, group, tpt;  // tpt: tokens of a tile
+    int max_blocks, num_blocks, bt;
+    float scale_log2;
+};
+
+// An item cut among CTAs, described by the CTA that has its first piece.
+struct Split {
+    long long start;   // the item's place on the cost line
+    long long total;   // the line's length
+    long long cost;
+    int ntiles;        // 0: nothing to join
+    int ranges;        // ranges the line is cut into
+    int tok0, ntok, head0;
+};
+
+struct __align__(16) Misc {
+    uint64_t q_full, q_empty;
+    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t part_full[kCleanBars], clean[kCleanBars];  // value tiles to be cleaned: landed, cleaned
+    uint64_t s_full[2], p_full[2], o_full[2], item_done[2];
+    uint64_t join[2];         // one-tile items: both streams' states are there; both accumulators are read
+    long long scan[kThreads / 32];
+    int cut[2][4];            // sequence, head, item, tile of the range's ends
+    uint32_t tmem;
+    int abort;
+    uint32_t bad[2][4][4];    // [item parity][masked tile][key / 32]: non-finite values taken out
+    float2 ml[2][kRows];
+};
+
+constexpr size_t kSmemQ = 0, kSmemRing = 2 * kTileBytes, kSmemMisc = kSmemRing + kStages * kTileBytes;
+constexpr size_t kSmemBytes = kSmemMisc + sizeof(Misc);
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+
+// ---- the work line -----------------------------------------------------------
+
+struct Seq {
+    int n, ctx, tok0;  // query rows, tokens in the cache, first row
+};
+
+template <bool kTree>
+__device__ __forceinline__ Seq load_seq(const Params& p, int s, uint32_t* bad) {
+    const int a = __ldg(p.query_starts + s), b = __ldg(p.query_starts + s + 1);
+    int ctx = __ldg(p.context_lens + s);
+    Seq q;
+    q.tok0 = min(max(a, 0), p.num_tokens);
+    const int end = min(max(b, 0), p.num_tokens);
+    q.n = max(end - q.tok0, 0);
+    if (bad && (a != q.tok0 || b != end || end < q.tok0)) *bad |= PKV_DEVERR_QUERY;
+    if (kTree && q.n > PKV_TREE_MAX_DRAFTS) {
+        q.n = PKV_TREE_MAX_DRAFTS;
+        if (bad) *bad |= PKV_DEVERR_QUERY;
+    }
+    const long long cap = static_cast<long long>(p.max_blocks) * p.bt;
+    if (ctx > cap) {
+        ctx = static_cast<int>(cap);
+        if (bad) *bad |= PKV_DEVERR_CONTEXT;
+    }
+    q.ctx = max(ctx, 0);
+    if (bad && !kTree && q.n > q.ctx) *bad |= PKV_DEVERR_CONTEXT;
+    return q;
+}
+
+// Cost of the first `items` items of one head of a sequence, all of two full tiles.
+template <bool kTree>
+__device__ __forceinline__ long long full_cost(const Seq& q, int tpt, long long items) {
+    if (kTree) return items * (kCostTwo * (q.ctx + static_cast<long long>(kKeys)) + kItemCost);
+    // keys of item i: ctx - n + (i + 1) * 2 tpt (below zero only for a chunk longer than its context)
+    const long long base = q.ctx - q.n;
+    return items * (kCostTwo * max(base, 0ll) + kItemCost) + static_cast<long long>(kCostTwo) * tpt * items * (items + 1);
+}
+
+template <bool kTree>
+__device__ __forceinline__ long long last_cost(const Seq& q, int rest, int tpt) {
+    const long long keys = kTree ? q.ctx + static_cast<long long>(kKeys) : q.ctx;
+    return (rest > tpt ? kCostTwo : kCostOne) * keys + kItemCost;
+}
+
+template <bool kTree>
+__device__ __forceinline__ long long head_cost(const Seq& q, int tpt) {
+    const int full = q.n / (2 * tpt), rest = q.n - full * 2 * tpt;
+    return full_cost<kTree>(q, tpt, full) + (rest ? last_cost<kTree>(q, rest, tpt) : 0);
+}
+
+// Tiles of an item that belong to ranges before a cut `off` cost units into it.
+__device__ __forceinline__ int cut_tile(long long off, long long cost, int ntiles) {
+    if (off <= kSnap) return 0;
+    if (cost - off <= kSnap) return ntiles;
+    const int t = static_cast<int>((off * ntiles + cost / 2) / cost);
+    return min(max(t, 0), ntiles);
+}
+
+// One item: the tiles of one (sequence, KV head) from token i * 2 tpt on.
+struct Item {
+    int s, h, i;
+    Seq q;
+    int tok0, ntok;   // rows of q / out
+    int pos0;         // prefill: position of the first row
+    int kend;         // keys in the cache it may need
+    int nct, nt;      // tiles of the cache; with the draft tile
+    int first_masked; // first tile that not every row sees in full
+    bool two;
+
+    __device__ __forceinline__ int cut_tiles() const { return max(nt, 1); }
+};
+
+template <bool kTree>
+__device__ __forceinline__ void set_item(const Params& p, Item& it) {
+    const int off = it.i * 2 * p.tpt;
+    it.tok0 = it.q.tok0 + off;
+    it.ntok = min(2 * p.tpt, it.q.n - off);
+    it.two = it.ntok > p.tpt;
+    it.pos0 = it.q.ctx - it.q.n + off;
+    it.kend = kTree ? it.q.ctx : max(it.pos0 + it.ntok, 0);
+    it.nct = (it.kend + kKeys - 1) / kKeys;
+    it.nt = it.nct + (kTree ? 1 : 0);
+    it.first_masked = (kTree ? it.q.ctx : max(it.pos0 + 1, 0)) / kKeys;
+}
+
+template <bool kTree>
+__device__ __forceinline__ long long item_cost(const Params& p, const Item& it) {
+    const int full = it.q.n / (2 * p.tpt);
+    return it.i < full ? full_cost<kTree>(it.q, p.tpt, it.i + 1) - full_cost<kTree>(it.q, p.tpt, it.i)
+                       : last_cost<kTree>(it.q, it.q.n - full * 2 * p.tpt, p.tpt);
+}
+
+// A CTA's walk over its range: next() yields its pieces of items in order.
+template <bool kTree>
+struct Walk {
+    const Params& p;
+    Item it;
+    int s1, h1, i1, t1;  // the range's end
+    int ta, tb;          // tiles of the piece
+    bool first;
+
+    __device__ __forceinline__ Walk(const Params& prm, const int (&cut)[2][4]) : p(prm), first(true) {
+        it.s = cut[0][0];
+        it.h = cut[0][1];
+        it.i = cut[0][2];
+        ta = cut[0][3];
+        s1 = cut[1][0];
+        h1 = cut[1][1];
+        i1 = cut[1][2];
+        t1 = cut[1][3];
+    }
+    __device__ __forceinline__ bool next() {
+        bool step = !first;
+        if (first) {
+            first = false;
+            if (it.s >= p.num_seqs) return false;
+            it.q = load_seq<kTree>(p, it.s, nullptr);
+            set_item<kTree>(p, it);
+            step = ta >= it.cut_tiles();  // the range starts behind this item
+        }
+        if (step) {
+            ta = 0;
+            ++it.i;
+            if (it.i * 2 * p.tpt >= it.q.n) {
+                it.i = 0;
+                if (++it.h == p.hkv) {
+                    it.h = 0;
+                    do {
+                        if (++it.s >= p.num_seqs) return false;
+                        it.q = load_seq<kTree>(p, it.s, nullptr);
+                    } while (it.q.n == 0);
+                }
+            }
+            set_item<kTree>(p, it);
+        }
+        if (it.s > s1 || (it.s == s1 && (it.h > h1 || (it.h == h1 && it.i > i1)))) return false;
+        const bool last = it.s == s1 && it.h == h1 && it.i == i1;
+        if (last && t1 <= ta) return false;
+        tb = last ? t1 : it.cut_tiles();
+        return true;
+    }
+    __device__ __forceinline__ bool whole() const { return ta == 0 && tb == it.cut_tiles(); }
+    // key tiles of the piece, and of each stream
+    __device__ __forceinline__ int count() const { return min(tb, it.nt) - ta; }
+    __device__ __forceinline__ int stream_count(int stream) const {
+        const int c = max(count(), 0);
+        if (!it.two) return (c + 1 - stream) >> 1;
+        if (stream == 1 || kTree) return c;
+        const int own = (max(it.pos0 + p.tpt, 0) + kKeys - 1) / kKeys;  // tiles the first tile's rows see
+        return max(min(own - ta, c), 0);
+    }
+    // place of the piece's j-th K or V tile in the ring's order
+    __device__ __forceinline__ int ring_k(int j) const { return it.two ? 2 * j : max(2 * j - 1, 0); }
+    __device__ __forceinline__ int ring_v(int j) const { return it.two || j == count() - 1 ? 2 * j + 1 : 2 * j + 2; }
+};
+
+// Every thread of the CTA: the ends of this CTA's range, and the description
+// of the item that its end cuts.
+template <bool kTree>
+__device__ void plan(const Params& p, Misc& m) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
+    long long sum = 0;
+    uint32_t bad = 0;
+    for (int s = s0; s < s1; ++s) {
+        const Seq q = load_seq<kTree>(p, s, &bad);
+        sum += head_cost<kTree>(q, p.tpt) * p.hkv;
+    }
+    if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
+    long long incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) m.scan[warp] = incl;
+    if (tid < 8) m.cut[tid >> 2][tid & 3] = (tid & 3) == 0 ? p.num_seqs : 0;
+    if (tid == 0) p.splits[blockIdx.x].ntiles = 0;
+    __syncthreads();
+    long long before = incl - sum, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const long long v = m.scan[w];
+        if (w < warp) before += v;
+        total += v;
+    }
+    const long long fit = total / kMinRange;
+    const int ranges = static_cast<int>(min(static_cast<long long>(gridDim.x), max(fit, 1ll)));
+    const int b = blockIdx.x;
+    if (b >= ranges || total == 0) return;  // the ends stay behind the last sequence
+    for (int e = 0; e < 2; ++e) {
+        if (b + e >= ranges) break;
+        const long long x = total * (b + e) / ranges;
+        if (x < before || x >= before + sum) continue;
+        long long at = before;
+        for (int s = s0; s < s1; ++s) {
+            const Seq q = load_seq<kTree>(p, s, nullptr);
+            const long long hc = head_cost<kTree>(q, p.tpt);
+            if (x >= at + hc * p.hkv) {
+                at += hc * p.hkv;
+                continue;
+            }
+            Item it;
+            it.s = s;
+            it.q = q;
+            it.h = static_cast<int>((x - at) / hc);
+            const long long base = at + it.h * hc, off = x - base;
+            // the last item that starts at or before off
+            int lo = 0, hi = (q.n + 2 * p.tpt - 1) / (2 * p.tpt) - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (full_cost<kTree>(q, p.tpt, mid) <= off) lo = mid; else hi = mid - 1;
+            }
+            it.i = lo;
+            set_item<kTree>(p, it);
+            const long long start = base + full_cost<kTree>(q, p.tpt, lo), cost = item_cost<kTree>(p, it);
+            const int t = cut_tile(x - start, cost, it.cut_tiles());
+            m.cut[e][0] = s;
+            m.cut[e][1] = it.h;
+            m.cut[e][2] = it.i;
+            m.cut[e][3] = t;
+            // this CTA has the item's first piece and not its last
+            if (e == 1 && t > 0 && t < it.cut_tiles() &&
+                (b == 0 || total * b / ranges <= start || cut_tile(total * b / ranges - start, cost, it.cut_tiles()) == 0)) {
+                Split sp;
+                sp.start = start;
+                sp.total = total;
+                sp.cost = cost;
+                sp.ntiles = it.cut_tiles();
+                sp.ranges = ranges;
+                sp.tok0 = it.tok0;
+                sp.ntok = it.ntok;
+                sp.head0 = it.h * p.group;
+                p.splits[b] = sp;
+            }
+            break;
+        }
+    }
+}
+
+// ---- the kernel ---------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t non_finite2(uint32_t w) {  // a set sign bit for each non-finite bf16 half
+    return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+
+// Rows [0, valid) of a value tile in the ring: non-finite values become zero;
+// rows behind them become zero whole. Returns this lane's verdict on a row.
+__device__ __forceinline__ bool clean_row(uint8_t* tile, int row, int lane, bool valid) {
+    uint8_t* base = tile + (row >> 3) * 2048 + (row & 7) * 128;
+    bool bad = false;
+#pragma unroll
+    for (int panel = 0; panel < 2; ++panel)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // lanes start at different 16-byte chunks of their rows: no bank conflicts
+            uint4* c = reinterpret_cast<uint4*>(base + panel * 1024 + ((i + lane) & 7) * 16);
+            if (!valid) {
+                *c = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            uint4 v = *c;
+            const uint32_t x = non_finite2(v.x), y = non_finite2(v.y), z = non_finite2(v.z), w = non_finite2(v.w);
+            if (x | y | z | w) {
+                bad = true;
+                v.x &= ~((x >> 15) * 0xFFFFu);
+                v.y &= ~((y >> 15) * 0xFFFFu);
+                v.z &= ~((z >> 15) * 0xFFFFu);
+                v.w &= ~((w >> 15) * 0xFFFFu);
+                *c = v;
+            }
+        }
+    return bad;
+}
+
+// The keys of a masked tile that a row sees, as four words of 32.
+template <bool kTree>
+__device__ __forceinline__ void seen_words(const Item& it, int tile, int vis, uint64_t draft_mask, uint32_t (&w)[4]) {
+    if (kTree && tile == it.nct) {
+        w[0] = static_cast<uint32_t>(draft_mask);
+        w[1] = static_cast<uint32_t>(draft_mask >> 32);
+        w[2] = w[3] = 0;
+        return;
+    }
+    const int limit = vis - tile * kKeys;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int l = limit - 32 * k;
+        w[k] = l <= 0 ? 0u : l >= 32 ? 0xFFFFFFFFu : (1u << l) - 1u;
+    }
+}
+
+// Adds to 32 columns of a row the non-finite values that were taken out of the
+// product for keys the row sees (their weight is positive, so the weighted
+// value is the value itself).
+template <bool kTree>
+__device__ __noinline__ void add_non_finite(const Params& p, const Item& it, int t_lo, int t_hi, const uint32_t (*bad)[4],
+                                            int vis, uint64_t draft_mask, int col0, float* o) {
+    for (int t = t_lo; t < t_hi; ++t) {
+        uint32_t w[4];
+        seen_words<kTree>(it, t, vis, draft_mask, w);
+        for (int k = 0; k < 4; ++k) {
+            uint32_t bits = bad[t - t_lo][k] & w[k];
+            while (bits) {
+                const int key = __ffs(bits) - 1 + 32 * k;
+                bits &= bits - 1;
+                const __nv_bfloat16* row;
+                if (kTree && t == it.nct) {
+                    row = p.v_draft + (static_cast<long long>(it.q.tok0 + key) * p.hkv + it.h) * kDim;
+                } else {
+                    const int pos = t * kKeys + key;
+                    int blk = __ldg(p.block_tables + static_cast<long long>(it.s) * p.max_blocks + pos / p.bt);
+                    if (blk < 0 || blk >= p.num_blocks) blk = 0;
+                    row = p.v_cache + ((static_cast<long long>(blk) * p.hkv + it.h) * p.bt + pos % p.bt) * kDim;
+                }
+                for (int c = 0; c < 32; ++c) {
+                    const float v = __bfloat162float(row[col0 + c]);
+                    if (!isfinite(v)) o[c] += v;
+                }
+            }
+        }
+    }
+}
+
+template <bool kTree>
+__global__ void __launch_bounds__(kThreads, 1)
+rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kd,
+            const __grid_constant__ CUtensorMap tm_vd, const __grid_constant__ Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Misc& m = *reinterpret_cast<Misc*>(smem + kSmemMisc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t smem_base = smem_u32(smem);
+    volatile int* abort_flag = &m.abort;
+
+    griddep_launch_dependents();
+    if (smem_base & 1023) {  // the swizzle atoms need it; dynamic shared memory starts so, with no static beside it
+        if (tid == 0) {
+            p.splits[blockIdx.x].ntiles = 0;
+            atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+        }
+        return;
+    }
+    if (tid == 0) {
+        m.abort = 0;
+        mbar_init(smem_u32(&m.q_full), 1);
+        mbar_init(smem_u32(&m.q_empty), 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&m.kv_full[i]), 1);
+            mbar_init(smem_u32(&m.kv_empty[i]), 1);
+        }
+        for (int i = 0; i < kCleanBars; ++i) {
+            mbar_init(smem_u32(&m.part_full[i]), 1);
+            mbar_init(smem_u32(&m.clean[i]), 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&m.s_full[i]), 1);
+            mbar_init(smem_u32(&m.p_full[i]), 4);
+            mbar_init(smem_u32(&m.o_full[i]), 1);
+            mbar_init(smem_u32(&m.item_done[i]), kSoftmaxWarps);
+            mbar_init(smem_u32(&m.join[i]), kSoftmaxWarps);
+        }
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) tmem_alloc(smem_u32(&m.tmem), kTmemColumns);
+    tc_fence_before();
+    plan<kTree>(p, m);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m.tmem;
+    Walk<kTree> walk(p, m.cut);
+
+    if (warp < kSoftmaxWarps) {
+        // ---- softmax and epilogue: thread = row of the stream's tile
+        const int stream = warp >> 2;
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 tensor-memory lanes
+        const uint32_t t_s = tmem + lanes + stream * 128, t_o = tmem + lanes + kTmemO + stream * 128;
+        const int row_tok = row / p.group, row_head = row - row_tok * p.group;
+        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
+        uint32_t n_s = 0, n_o = 0, n_join = 0, n_item = 0;
+        for (; walk.next(); ++n_item) {
+            const Item& it = walk.it;
+            const int tile_tok = it.two ? stream * p.tpt : 0;
+            const int tok = it.tok0 + tile_tok + row_tok;
+            const bool valid = row_tok < p.tpt && tile_tok + row_tok < it.ntok;
+            const bool warp_valid = __any_sync(0xFFFFFFFFu, valid);
+            const int vis = kTree ? it.q.ctx : valid ? it.pos0 + tile_tok + row_tok + 1 : 0;
+            uint64_t draft_mask = 0;
+            if (kTree && valid) {
+                draft_mask = static_cast<uint64_t>(__ldg(reinterpret_cast<const long long*>(p.masks) + tok));
+                if (it.q.n < 64) draft_mask &= (1ull << it.q.n) - 1ull;
+            }
+            const int count = walk.stream_count(stream);
+            float mx = -INFINITY;  // reference of the exponentials, unscaled
+            float l = 0.f;
+            bool any = false;
+            bool ok = true;
+            for (int i = 0; i < count; ++i) {
+                const int tile = walk.ta + (it.two ? i : 2 * i + stream);
+                ok = mbar_wait(smem_u32(&m.s_full[stream]), n_s & 1, abort_flag, p.err);
+                ++n_s;
+                if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+                tc_fence_after();
+                if (warp_valid) {
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tmem_ld32(s[k], t_s + 32 * k);
+                    tmem_wait_ld(s[0]);
+                    hold(s[1]);
+                    hold(s[2]);
+                    hold(s[3]);
+                    if (tile >= it.first_masked) {
+                        uint32_t w[4];
+                        seen_words<kTree>(it, tile, vis, draft_mask, w);
+                        any |= (w[0] | w[1] | w[2] | w[3]) != 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(w[k] >> c & 1)) s[k][c] = 0xFF800000u;
+                    } else {
+                        any = true;
+                    }
+                    float m4[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        m4[k] = __uint_as_float(s[k][0]);
+#pragma unroll
+                        for (int c = 1; c < 32; ++c) m4[k] = fmaxf(m4[k], __uint_as_float(s[k][c]));
+                    }
+                    const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    // The reference only has to keep the exponentials in range: it
+                    // follows the maximum when that has grown by more than 8 (a
+                    // factor of 256 in the sums), which spares most rescalings of O.
+                    float factor = 1.f;
+                    const bool grow = mx == -INFINITY ? top != -INFINITY : (top - mx) * p.scale_log2 > 8.f;
+                    if (grow) {
+                        factor = mx == -INFINITY ? 0.f : ex2((mx - top) * p.scale_log2);
+                        mx = top;
+                    }
+                    const float ref = mx == -INFINITY ? 0.f : -mx * p.scale_log2;
+                    const uint64_t ref2 = pair(ref, ref);
+                    uint64_t sum2 = pair(l * factor, 0.f);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2) {
+                            const uint32_t* sk = s[2 * half + (c >> 5)];
+                            float a, b;
+                            unpair(fma2(pair(__uint_as_float(sk[c & 31]), __uint_as_float(sk[(c & 31) + 1])), scale2, ref2), a, b);
+                            a = ex2(a);
+                            b = ex2(b);
+                            sum2 = add2(sum2, pair(a, b));
+                            // the weights enter the product as bf16, as the tensor
+                            // core takes them; their sum stays in fp32
+                            pk[c >> 1] = pack_bf16x2(a, b);
+                        }
+                        tmem_st32(t_s + 32 * half, pk);
+                    }
+                    float s0, s1;
+                    unpair(sum2, s0, s1);
+                    l = s0 + s1;
+                    // S of this tile being complete, so is the stream's previous product
+                    if (i > 0 && __any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t o[32];
+                            tmem_ld32(o, t_o + 32 * k);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * factor);
+                            tmem_st32(t_o + 32 * k, o);
+                        }
+                    }
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&m.p_full[stream]));
+            }
+            if (!ok) break;
+            if (count > 0) {
+                ok = mbar_wait(smem_u32(&m.o_full[stream]), n_o & 1, abort_flag, p.err);
+                ++n_o;
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                tc_fence_after();
+            }
+
+            // the row's state: maximum (log2 units; any finite value says that the row sees a key) and sum
+            float2 st = make_float2(any ? (mx == -INFINITY ? -FLT_MAX : mx * p.scale_log2) : -INFINITY, l);
+            const bool whole = walk.whole();
+            const int t_lo = max(it.first_masked, walk.ta), t_hi = min(walk.tb, it.nt);
+            const uint32_t(*bad)[4] = m.bad[n_item & 1];
+            const long long slot = 2ll * blockIdx.x + (walk.ta == 0 ? 1 : 0);
+
+            // 32 columns of the row, out or into the partial results
+            auto put = [&](float (&o)[32], int col, float inv, long long prow) {
+                if (whole) {
+                    __nv_bfloat16* dst = p.out + (static_cast<long long>(tok) * p.hq + it.h * p.group + row_head) * kDim + col;
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8)
+                        *reinterpret_cast<uint4*>(dst + c) =
+                            make_uint4(pack_bf16x2(o[c] * inv, o[c + 1] * inv), pack_bf16x2(o[c + 2] * inv, o[c + 3] * inv),
+                                       pack_bf16x2(o[c + 4] * inv, o[c + 5] * inv), pack_bf16x2(o[c + 6] * inv, o[c + 7] * inv));
+                } else {
+                    float* dst = p.part_o + (slot * 2 * kRows + prow) * kDim + col;
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(o[c + e]);
+                        st_global_32b(dst + c, v);
+                    }
+                }
+            };
+            // what the sum is divided by; no key seen: zeros; only keys of weight zero: NaN, as 0 / 0
+            auto inverse = [](const float2& s) {
+                return s.y == 0.f ? (s.x == -INFINITY ? 0.f : __int_as_float(0x7FC00000)) : 1.f / s.y;
+            };
+
+            if (it.two) {
+                if (warp_valid) {
+                    const float inv = inverse(st);
+                    uint32_t bad_any = 0;
+                    for (int t = t_lo; t < min(t_hi, walk.ta + count); ++t)
+                        for (int k = 0; k < 4; ++k) bad_any |= bad[t - t_lo][k];
+#pragma unroll 1
+                    for (int col = 0; col < kDim; col += 32) {
+                        uint32_t r[32];
+                        float o[32];
+                        if (count > 0) {
+                            tmem_ld32(r, t_o + col);
+                            tmem_wait_ld(r);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __uint_as_float(r[c]);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = 0.f;
+                        }
+                        if (bad_any && valid) {
+                            float f[32];
+                            for (int c = 0; c < 32; ++c) f[c] = o[c];
+                            add_non_finite<kTree>(p, it, t_lo, min(t_hi, walk.ta + count), bad, vis, draft_mask, col, f);
+                            for (int c = 0; c < 32; ++c) o[c] = f[c];
+                        }
+                        if (valid) put(o, col, inv, stream * kRows + row);
+                    }
+                    if (valid && !whole) p.part_ml[slot * 2 * kRows + stream * kRows + row] = st;
+                }
+            } else {
+                // join the streams: each warpgroup takes half of the columns of both accumulators
+                m.ml[stream][row] = st;
+                auto meet = [&](int k) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&m.join[k]));
+                    const bool met = mbar_wait(smem_u32(&m.join[k]), n_join & 1, abort_flag, p.err);
+                    tc_fence_after();
+                    return __all_sync(0xFFFFFFFFu, met) != 0;
+                };
+                if (!meet(0)) break;
+                if (warp_valid) {
+                    const float2 s0 = m.ml[0][row], s1 = m.ml[1][row];
+                    const bool one = walk.stream_count(1) == 0, none = walk.stream_count(0) == 0;
+                    float2 js;
+                    js.x = fmaxf(s0.x, s1.x);
+                    const float a0 = s0.x == js.x ? 1.f : ex2(s0.x - js.x), a1 = s1.x == js.x ? 1.f : ex2(s1.x - js.x);
+                    js.y = s0.y * a0 + s1.y * a1;
+                    const float inv = inverse(js);
+                    uint32_t bad_any = 0;
+                    for (int t = t_lo; t < t_hi; ++t)
+                        for (int k = 0; k < 4; ++k) bad_any |= bad[t - t_lo][k];
+#pragma unroll 1
+                    for (int col = stream * 64; col < stream * 64 + 64; col += 32) {
+                        uint32_t r0[32], r1[32];
+                        float o[32];
+                        if (!none) {
+                            tmem_ld32(r0, tmem + lanes + kTmemO + col);
+                            if (!one) tmem_ld32(r1, tmem + lanes + kTmemO + 128 + col);
+                            tmem_wait_ld(r0);
+                            hold(r1);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            o[c] = none ? 0.f : one ? __uint_as_float(r0[c]) : __uint_as_float(r0[c]) * a0 + __uint_as_float(r1[c]) * a1;
+                        if (bad_any && valid) {
+                            float f[32];
+                            for (int c = 0; c < 32; ++c) f[c] = o[c];
+                            add_non_finite<kTree>(p, it, t_lo, t_hi, bad, vis, draft_mask, col, f);
+                            for (int c = 0; c < 32; ++c) o[c] = f[c];
+                        }
+                        if (valid) put(o, col, inv, row);
+                    }
+                    if (valid && !whole && stream == 0) p.part_ml[slot * 2 * kRows + row] = js;
+                }
+                // both accumulators are read before either is written again
+                if (!meet(1)) break;
+                ++n_join;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&m.item_done[n_item & 1]));
+        }
+    } else if (warp == kWarpLoad) {
+        // ---- loader: query tiles, then K and V tiles in the order of their use
+        if (lane == 0) {
+            prefetch_tensormap(&tm_q);
+            prefetch_tensormap(&tm_k);
+            prefetch_tensormap(&tm_v);
+            if (kTree) {
+                prefetch_tensormap(&tm_kd);
+                prefetch_tensormap(&tm_vd);
+            }
+        }
+        uint32_t ring = 0, n_q = 0, n_clean = 0;
+        const int blocks_per_tile = kKeys / p.bt;
+        bool ok = true;
+        while (ok && walk.next()) {
+            const Item& it = walk.it;
+            const int count = walk.count();
+            if (count <= 0) continue;
+            ok = mbar_wait(smem_u32(&m.q_empty), (n_q & 1) ^ 1, abort_flag, p.err);
+            ++n_q;
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            const int tiles = it.two ? 2 : 1;
+            const int masked0 = max(it.first_masked, walk.ta) - walk.ta;  // first masked tile of the piece
+            if (lane == 0) mbar_arrive_expect_tx(smem_u32(&m.q_full), tiles * 2 * 128 * p.group * p.tpt);
+            __syncwarp();
+            if (lane < 2 * tiles) {
+                const int t = lane >> 1, panel = lane & 1;
+                tma_load_5d(smem_base + kSmemQ + t * kTileBytes + panel * (kTileBytes / 2), &tm_q, 0, 0,
+                            it.tok0 + t * p.tpt, panel, it.h, smem_u32(&m.q_full));
+            }
+            // this lane's box of a tile: its last coordinate in the map
+            auto coordinate = [&](int j) {
+                const int t = walk.ta + j;
+                if (kTree && t == it.nct) return it.q.tok0 + lane * 8;
+                const int idx = t * blocks_per_tile + lane;
+                if (lane >= blocks_per_tile || idx * p.bt >= it.kend) return 0;
+                int blk = __ldg(p.block_tables + static_cast<long long>(it.s) * p.max_blocks + idx);
+                if (blk < 0 || blk >= p.num_blocks) {
+                    atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+                    blk = 0;
+                }
+                return (blk * p.hkv + it.h) * (p.bt >> 3);
+            };
+            auto load = [&](bool is_v, int j, int pos, int coord) {
+                const uint32_t at = ring + pos;
+                const uint32_t st = at % kStages, ph = (at / kStages) & 1;
+                ok = mbar_wait(smem_u32(&m.kv_empty[st]), ph ^ 1, abort_flag, p.err);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) return;
+                const int t = walk.ta + j;
+                uint32_t full = smem_u32(&m.kv_full[st]);
+                if (is_v && j >= masked0) {
+                    // a value tile to be cleaned lands on a barrier of its own: the
+                    // cleaning warps see no other tile, and could not follow the
+                    // ring's phases
+                    if (lane == 0) mbar_arrive(full);
+                    full = smem_u32(&m.part_full[(n_clean + (j - masked0)) % kCleanBars]);
+                }
+                const uint32_t dst = smem_base + kSmemRing + st * kTileBytes;
+                const bool draft = kTree && t == it.nct;
+                const int boxes = draft ? (it.q.n + 7) >> 3 : (min(kKeys, it.kend - t * kKeys) + p.bt - 1) / p.bt;
+                const uint32_t box_bytes = draft ? 2048 : p.bt * 256;
+                if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_bytes);
+                __syncwarp();
+                if (lane < boxes) {
+                    if (draft) tma_load_4d(dst + lane * box_bytes, is_v ? &tm_vd : &tm_kd, 0, coord, 0, it.h, full);
+                    else tma_load_4d(dst + lane * box_bytes, is_v ? &tm_v : &tm_k, 0, 0, 0, coord, full);
+                }
+            };
+            int cur = coordinate(0);
+            load(false, 0, walk.ring_k(0), cur);
+            for (int j = 0; ok && j < count; ++j) {
+                int next = 0;
+                if (j + 1 < count) next = coordinate(j + 1);
+                if (!it.two && j + 1 < count) load(false, j + 1, walk.ring_k(j + 1), next);
+                if (ok) load(true, j, walk.ring_v(j), cur);
+                if (ok && it.two && j + 1 < count) load(false, j + 1, walk.ring_k(j + 1), next);
+                cur = next;
+            }
+            ring += 2 * count;
+            n_clean += max(count - masked0, 0);
+        }
+    } else if (warp == kWarpMma) {
+        // ---- tensor core: one thread issues every product
+        if (lane == 0) {
+            constexpr uint32_t kIdescS = mma_idesc(kRows, kKeys, false), kIdescO = mma_idesc(kRows, kDim, true);
+            uint32_t ring = 0, n_q = 0, n_clean = 0, n_p[2] = {0, 0};
+            bool ok = true;
+            while (ok && walk.next()) {
+                const Item& it = walk.it;
+                const int count = walk.count();
+                if (count <= 0) continue;
+                const int cnt[2] = {walk.stream_count(0), walk.stream_count(1)};
+                const int masked0 = max(it.first_masked, walk.ta) - walk.ta;  // first masked tile of the piece
+                ok = mbar_wait(smem_u32(&m.q_full), n_q & 1, abort_flag, p.err);
+                ++n_q;
+                if (!ok) break;
+                const int last_k = count - 1;
+
+                // S of the stream's i-th key tile
+                auto scores = [&](int stream, int i) {
+                    const int j = it.two ? i : 2 * i + stream;
+                    const uint32_t at = ring + walk.ring_k(j), st = at % kStages;
+                    ok = mbar_wait(smem_u32(&m.kv_full[st]), (at / kStages) & 1, abort_flag, p.err);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t a = smem_base + kSmemQ + (it.two ? stream * kTileBytes : 0);
+                    const uint32_t b = smem_base + kSmemRing + st * kTileBytes;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ss(tmem + stream * 128, smem_desc(a + (k >> 2) * (kTileBytes / 2) + (k & 3) * 32, 16, 1024),
+                               smem_desc(b + (k >> 2) * 1024 + (k & 3) * 32, 16, 2048), kIdescS, k > 0);
+                    mma_commit(smem_u32(&m.s_full[stream]));
+                    if (!it.two || stream == 1) mma_commit(smem_u32(&m.kv_empty[st]));
+                    if (j == last_k && (!it.two || stream == 1)) mma_commit(smem_u32(&m.q_empty));
+                };
+                // O += P V for the stream's i-th key tile
+                auto values = [&](int stream, int i) {
+                    const int j = it.two ? i : 2 * i + stream;
+                    const uint32_t at = ring + walk.ring_v(j), st = at % kStages;
+                    if (j >= masked0) {
+                        const uint32_t c = n_clean + (j - masked0);
+                        ok = mbar_wait(smem_u32(&m.clean[c % kCleanBars]), (c / kCleanBars) & 1, abort_flag, p.err);
+                    } else {
+                        ok = mbar_wait(smem_u32(&m.kv_full[st]), (at / kStages) & 1, abort_flag, p.err);
+                    }
+                    if (ok) ok = mbar_wait(smem_u32(&m.p_full[stream]), n_p[stream] & 1, abort_flag, p.err);
+                    ++n_p[stream];
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t b = smem_base + kSmemRing + st * kTileBytes;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ts(tmem + kTmemO + stream * 128, tmem + stream * 128 + k * 8, smem_desc(b + k * 4096, 1024, 2048),
+                               kIdescO, i > 0 || k > 0);
+                    if (!it.two || stream == 1) mma_commit(smem_u32(&m.kv_empty[st]));
+                    if (i == cnt[stream] - 1) mma_commit(smem_u32(&m.o_full[stream]));
+                };
+
+                if (cnt[0] > 0) scores(0, 0);
+                if (ok && cnt[1] > 0) scores(1, 0);
+                const int rounds = max(cnt[0], cnt[1]);
+                for (int i = 0; ok && i < rounds; ++i)
+                    for (int stream = 0; ok && stream < 2; ++stream) {
+                        if (i >= cnt[stream]) continue;
+                        values(stream, i);
+                        if (ok && i + 1 < cnt[stream]) scores(stream, i + 1);
+                    }
+                ring += 2 * count;
+                n_clean += max(count - masked0, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- value tiles that not every row sees in full
+        const int half = warp - kWarpClean;
+        uint32_t ring = 0, n_clean = 0, n_item = 0;
+        bool ok = true;
+        for (; ok && walk.next(); ++n_item) {
+            const Item& it = walk.it;
+            const int count = walk.count();
+            // the epilogue of the item before the last has read its words
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&m.item_done[n_item & 1]), ((n_item >> 1) & 1) ^ 1, abort_flag, p.err));
+            if (count <= 0) continue;
+            const int masked0 = max(it.first_masked, walk.ta) - walk.ta;
+            for (int j = masked0; ok && j < count; ++j, ++n_clean) {
+                const uint32_t at = ring + walk.ring_v(j), st = at % kStages;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&m.part_full[n_clean % kCleanBars]),
+                                                       (n_clean / kCleanBars) & 1, abort_flag, p.err));
+                if (!ok) break;
+                const int t = walk.ta + j;
+                const int valid = kTree && t == it.nct ? it.q.n : min(kKeys, it.kend - t * kKeys);
+                uint8_t* tile = smem + kSmemRing + st * kTileBytes;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int row = half * 64 + r * 32 + lane;
+                    const bool bad = clean_row(tile, row, lane, row < valid);
+                    const uint32_t word = __ballot_sync(0xFFFFFFFFu, bad);
+                    if (lane == 0) m.bad[n_item & 1][j - masked0][half * 2 + r] = word;
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&m.clean[n_clean % kCleanBars]));
+            }
+            ring += 2 * count;
+        }
+    }
+    __syncthreads();
+    if (*abort_flag) {
+        // copies and products of a broken pipeline may still be under way
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) {}
+        __syncthreads();
+    }
+    if (warp == kWarpMma) tmem_free(tmem, kTmemColumns);
+}
+
+// Joins the pieces of the items that cuts split: block x serves the item whose
+// first piece CTA x computed, a warp per row.
+constexpr int kMergeWarps = 8;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Params p) {
+    griddep_wait();
+    const Split sp = p.splits[blockIdx.x];
+    if (sp.ntiles == 0) return;
+    const int lane = threadIdx.x & 31;
+    const int c0 = blockIdx.x;
+    for (int r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); r < 2 * kRows; r += gridDim.y * kMergeWarps) {
+        const int tile = r >> 7, rr = r & 127;
+        const int row_tok = rr / p.group, tok = tile * p.tpt + row_tok;
+        if (row_tok >= p.tpt || tok >= sp.ntok) continue;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        int t = 0;
+        for (int c = c0; t < sp.ntiles && c < sp.ranges; ++c) {
+            const long long end = sp.total * (c + 1) / sp.ranges - sp.start;
+            const int t_end = c + 1 >= sp.ranges || end >= sp.cost ? sp.ntiles : cut_tile(end, sp.cost, sp.ntiles);
+            if (t_end <= t) continue;  // no piece in this range
+            t = t_end;
+            const long long prow = (2ll * c + (c == c0 ? 1 : 0)) * 2 * kRows + r;
+            const float2 st = p.part_ml[prow];
+            if (st.x == -INFINITY) continue;
+            const float4 v = *reinterpret_cast<const float4*>(p.part_o + prow * kDim + lane * 4);
+            const float top = fmaxf(m, st.x);
+            const float a = m == top ? 1.f : ex2(m - top), b = st.x == top ? 1.f : ex2(st.x - top);
+            m = top;
+            l = l * a + st.y * b;
+            o.x = o.x * a + v.x * b;
+            o.y = o.y * a + v.y * b;
+            o.z = o.z * a + v.z * b;
+            o.w = o.w * a + v.w * b;
+        }
+        const float inv = l == 0.f ? (m == -INFINITY ? 0.f : __int_as_float(0x7FC00000)) : 1.f / l;
+        uint2 u;
+        u.x = pack_bf16x2(o.x * inv, o.y * inv);
+        u.y = pack_bf16x2(o.z * inv, o.w * inv);
+        const int head = sp.head0 + rr - row_tok * p.group;
+        *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(sp.tok0 + tok) * p.hq + head) * kDim + lane * 4) = u;
+    }
+}
+
+}  // namespace prefill
+}  // namespace pkv
