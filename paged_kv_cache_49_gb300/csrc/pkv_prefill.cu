@@ -38,6 +38,13 @@ DeviceInfo device_info() {
         e = cudaFuncSetAttribute(rows_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(rows_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+    // the kernels move registers between their warpgroups: a launch with fewer
+    // than they count on would wait for ever
+    for (const auto fn : {rows_kernel<false>, rows_kernel<true>}) {
+        cudaFuncAttributes at = {};
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, fn);
+        if (e == cudaSuccess && at.numRegs < kRegsLaunch) e = cudaErrorInvalidDeviceFunction;
+    }
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return {};

@@ -45,6 +45,9 @@ constexpr int kStages = 5;    // K or V tiles in flight
 constexpr int kThreads = 384;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpClean = 10;  // and 11
+// Registers: what the block is launched with, moved from the third warpgroup to the softmax's two.
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch, "register split");
 constexpr int kCleanBars = 8;  // more than the ring can hold
 
 constexpr uint32_t kTileBytes = kKeys * kDim * 2;
@@ -397,15 +400,16 @@ __device__ __forceinline__ void seen_words(const Item& it, int tile, int vis, ui
     }
 }
 
-// Adds to 32 columns of a row the non-finite values that were taken out of the
-// product for keys the row sees (their weight is positive, so the weighted
-// value is the value itself).
-template <bool kTree>
-__device__ __noinline__ void add_non_finite(const Params& p, const Item& it, int t_lo, int t_hi, const uint32_t (*bad)[4],
-                                            int vis, uint64_t draft_mask, int col0, float* o) {
+// Adds to columns [lo, hi) of a finished row the non-finite values that were
+// taken out of the product for keys the row sees (their weights are positive,
+// so each weighted value is the value itself). bad: the words of tiles t_lo ..
+template <bool kTree, typename T>
+__device__ void add_non_finite(const Params& p, const Item& it, int t_lo, int t_hi, const uint32_t (*bad)[4], int vis,
+                               uint64_t draft_mask, int lo, int hi, T* out_row) {
     for (int t = t_lo; t < t_hi; ++t) {
         uint32_t w[4];
         seen_words<kTree>(it, t, vis, draft_mask, w);
+#pragma unroll
         for (int k = 0; k < 4; ++k) {
             uint32_t bits = bad[t - t_lo][k] & w[k];
             while (bits) {
@@ -420,9 +424,10 @@ __device__ __noinline__ void add_non_finite(const Params& p, const Item& it, int
                     if (blk < 0 || blk >= p.num_blocks) blk = 0;
                     row = p.v_cache + ((static_cast<long long>(blk) * p.hkv + it.h) * p.bt + pos % p.bt) * kDim;
                 }
-                for (int c = 0; c < 32; ++c) {
-                    const float v = __bfloat162float(row[col0 + c]);
-                    if (!isfinite(v)) o[c] += v;
+#pragma unroll 1
+                for (int c = lo; c < hi; ++c) {
+                    const float v = __bfloat162float(row[c]);
+                    if (!isfinite(v)) out_row[c] = static_cast<T>(static_cast<float>(out_row[c]) + v);
                 }
             }
         }
@@ -478,6 +483,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     Walk<kTree> walk(p, m.cut);
 
     if (warp < kSoftmaxWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---- softmax and epilogue: thread = row of the stream's tile
         const int stream = warp >> 2;
         const int row = (warp & 3) * 32 + lane;
@@ -603,21 +609,20 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const long long slot = 2ll * blockIdx.x + (walk.ta == 0 ? 1 : 0);
 
             // 32 columns of the row, out or into the partial results
-            auto put = [&](float (&o)[32], int col, float inv, long long prow) {
+            __nv_bfloat16* out_row = p.out + (static_cast<long long>(tok) * p.hq + it.h * p.group + row_head) * kDim;
+            auto put = [&](uint32_t (&o)[32], int col, float inv, long long prow) {
                 if (whole) {
-                    __nv_bfloat16* dst = p.out + (static_cast<long long>(tok) * p.hq + it.h * p.group + row_head) * kDim + col;
+                    auto two = [&](int c) { return pack_bf16x2(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv); };
 #pragma unroll
                     for (int c = 0; c < 32; c += 8)
-                        *reinterpret_cast<uint4*>(dst + c) =
-                            make_uint4(pack_bf16x2(o[c] * inv, o[c + 1] * inv), pack_bf16x2(o[c + 2] * inv, o[c + 3] * inv),
-                                       pack_bf16x2(o[c + 4] * inv, o[c + 5] * inv), pack_bf16x2(o[c + 6] * inv, o[c + 7] * inv));
+                        *reinterpret_cast<uint4*>(out_row + col + c) = make_uint4(two(c), two(c + 2), two(c + 4), two(c + 6));
                 } else {
                     float* dst = p.part_o + (slot * 2 * kRows + prow) * kDim + col;
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
                         uint32_t v[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(o[c + e]);
+                        for (int e = 0; e < 8; ++e) v[e] = o[c + e];
                         st_global_32b(dst + c, v);
                     }
                 }
@@ -627,37 +632,31 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 return s.y == 0.f ? (s.x == -INFINITY ? 0.f : __int_as_float(0x7FC00000)) : 1.f / s.y;
             };
 
+            int col_lo = 0, col_hi = kDim, t_end = t_hi;  // this thread's columns; its stream's tiles
+            long long prow = row;
             if (it.two) {
+                t_end = min(t_hi, walk.ta + count);
+                prow += stream * kRows;
                 if (warp_valid) {
                     const float inv = inverse(st);
-                    uint32_t bad_any = 0;
-                    for (int t = t_lo; t < min(t_hi, walk.ta + count); ++t)
-                        for (int k = 0; k < 4; ++k) bad_any |= bad[t - t_lo][k];
 #pragma unroll 1
                     for (int col = 0; col < kDim; col += 32) {
                         uint32_t r[32];
-                        float o[32];
                         if (count > 0) {
                             tmem_ld32(r, t_o + col);
                             tmem_wait_ld(r);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) o[c] = __uint_as_float(r[c]);
                         } else {
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) o[c] = 0.f;
+                            for (int c = 0; c < 32; ++c) r[c] = 0;
                         }
-                        if (bad_any && valid) {
-                            float f[32];
-                            for (int c = 0; c < 32; ++c) f[c] = o[c];
-                            add_non_finite<kTree>(p, it, t_lo, min(t_hi, walk.ta + count), bad, vis, draft_mask, col, f);
-                            for (int c = 0; c < 32; ++c) o[c] = f[c];
-                        }
-                        if (valid) put(o, col, inv, stream * kRows + row);
+                        if (valid) put(r, col, inv, prow);
                     }
-                    if (valid && !whole) p.part_ml[slot * 2 * kRows + stream * kRows + row] = st;
+                    if (valid && !whole) p.part_ml[slot * 2 * kRows + prow] = st;
                 }
             } else {
                 // join the streams: each warpgroup takes half of the columns of both accumulators
+                col_lo = stream * 64;
+                col_hi = col_lo + 64;
                 m.ml[stream][row] = st;
                 auto meet = [&](int k) {
                     tc_fence_before();
@@ -676,40 +675,49 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     const float a0 = s0.x == js.x ? 1.f : ex2(s0.x - js.x), a1 = s1.x == js.x ? 1.f : ex2(s1.x - js.x);
                     js.y = s0.y * a0 + s1.y * a1;
                     const float inv = inverse(js);
-                    uint32_t bad_any = 0;
-                    for (int t = t_lo; t < t_hi; ++t)
-                        for (int k = 0; k < 4; ++k) bad_any |= bad[t - t_lo][k];
 #pragma unroll 1
-                    for (int col = stream * 64; col < stream * 64 + 64; col += 32) {
-                        uint32_t r0[32], r1[32];
-                        float o[32];
-                        if (!none) {
-                            tmem_ld32(r0, tmem + lanes + kTmemO + col);
-                            if (!one) tmem_ld32(r1, tmem + lanes + kTmemO + 128 + col);
-                            tmem_wait_ld(r0);
-                            hold(r1);
-                        }
+                    for (int col = col_lo; col < col_hi; col += 32) {
+                        uint32_t r[32], r1[32];
+                        if (none) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            o[c] = none ? 0.f : one ? __uint_as_float(r0[c]) : __uint_as_float(r0[c]) * a0 + __uint_as_float(r1[c]) * a1;
-                        if (bad_any && valid) {
-                            float f[32];
-                            for (int c = 0; c < 32; ++c) f[c] = o[c];
-                            add_non_finite<kTree>(p, it, t_lo, t_hi, bad, vis, draft_mask, col, f);
-                            for (int c = 0; c < 32; ++c) o[c] = f[c];
+                            for (int c = 0; c < 32; ++c) r[c] = 0;
+                        } else {
+                            tmem_ld32(r, tmem + lanes + kTmemO + col);
+                            if (!one) tmem_ld32(r1, tmem + lanes + kTmemO + 128 + col);
+                            tmem_wait_ld(r);
+                            if (!one) {
+                                hold(r1);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    r[c] = __float_as_uint(__uint_as_float(r[c]) * a0 + __uint_as_float(r1[c]) * a1);
+                            }
                         }
-                        if (valid) put(o, col, inv, row);
+                        if (valid) put(r, col, inv, prow);
                     }
-                    if (valid && !whole && stream == 0) p.part_ml[slot * 2 * kRows + row] = js;
+                    if (valid && !whole && stream == 0) p.part_ml[slot * 2 * kRows + prow] = js;
                 }
                 // both accumulators are read before either is written again
                 if (!meet(1)) break;
                 ++n_join;
             }
+            if (valid && t_lo < t_end) {
+                uint32_t any_bad = 0;
+                for (int t = t_lo; t < t_end; ++t)
+                    any_bad |= bad[t - t_lo][0] | bad[t - t_lo][1] | bad[t - t_lo][2] | bad[t - t_lo][3];
+                if (any_bad) {
+                    if (whole)
+                        add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi, out_row);
+                    else
+                        add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi,
+                                              p.part_o + (slot * 2 * kRows + prow) * kDim);
+                }
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&m.item_done[n_item & 1]));
         }
-    } else if (warp == kWarpLoad) {
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+      if (warp == kWarpLoad) {
         // ---- loader: query tiles, then K and V tiles in the order of their use
         if (lane == 0) {
             prefetch_tensormap(&tm_q);
@@ -895,6 +903,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
             ring += 2 * count;
         }
+      }
     }
     __syncthreads();
     if (*abort_flag) {
