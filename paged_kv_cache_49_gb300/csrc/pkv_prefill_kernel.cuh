@@ -41,7 +41,7 @@ namespace prefill {
 constexpr int kDim = PKV_ATTN_HEAD_DIM;
 constexpr int kRows = 128;    // query rows of a tile
 constexpr int kKeys = 128;    // keys of a tile
-constexpr int kStages = 5;    // K or V tiles in flight
+constexpr int kStages = 4;    // K or V tiles in flight
 constexpr int kThreads = 384;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpClean = 10;  // and 11
@@ -56,9 +56,10 @@ constexpr uint32_t kTmemO = 256;  // S0, S1, O0, O1 of 128 columns each
 
 // Cost units of the work line: one key of an item's two tiles is 8, of a
 // single tile 5; an item's fixed work is kItemCost.
-constexpr int kCostTwo = 8, kCostOne = 5, kItemCost = 8 * 256;
+constexpr int kCostTwo = 8, kCostOne = 5, kItemCost = 8 * 160;
 constexpr int kSnap = 8 * 256;      // a cut this near an item's end moves there
 constexpr int kMinRange = 8 * 256;  // least cost of a CTA's range
+constexpr int kPieces = 4;          // pieces described ahead
 
 constexpr size_t kWsHeader = 256;
 constexpr int kMaxGrid = 1024;
@@ -82,37 +83,59 @@ struct Params {
 
 // An item cut among CTAs, described by the CTA that has its first piece.
 struct Split {
-    long long start;   // the item's place on the cost line
-    long long total;   // the line's length
-    long long cost;
-    int ntiles;        // 0: nothing to join
-    int ranges;        // ranges the line is cut into
+    long long start, cost;  // the item's place and length on the cost line
+    long long chunk;        // the length of a range
+    int ntiles;             // 0: nothing to join
     int tok0, ntok, head0;
+};
+
+struct Seq {
+    int n, ctx, tok0;  // query rows, tokens in the cache, first row
+};
+
+// A CTA's piece of an item, as the loader describes it to the other warps.
+struct __align__(16) Piece {
+    int count;          // key tiles; below zero: no more pieces
+    int ta;             // the first of them
+    int cnt[2];         // key tiles of each stream
+    int two;            // two query tiles, or one
+    int whole;          // the piece is its whole item
+    int tok0, ntok;     // rows of q / out
+    int pos0;           // prefill: position of the first row
+    int first_masked;   // first tile that not every row sees in full
+    int kend, nct;      // keys in the cache it needs; their tiles
+    int s, h;           // sequence, KV head
+    int seq_n, seq_tok0, ctx;  // query rows and first row of the sequence, its tokens in the cache
 };
 
 struct __align__(16) Misc {
     uint64_t q_full, q_empty;
     uint64_t kv_full[kStages], kv_empty[kStages];
     uint64_t part_full[kCleanBars], clean[kCleanBars];  // value tiles to be cleaned: landed, cleaned
-    uint64_t s_full[2], p_full[2], o_full[2], item_done[2];
+    uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t join[2];         // one-tile items: both streams' states are there; both accumulators are read
-    long long scan[kThreads / 32];
-    int cut[2][4];            // sequence, head, item, tile of the range's ends
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
+    Piece piece[kPieces];
+    uint32_t bad[kPieces][4][4];  // [piece][masked tile][key / 32]: non-finite values taken out
     uint32_t tmem;
     int abort;
-    uint32_t bad[2][4][4];    // [item parity][masked tile][key / 32]: non-finite values taken out
-    float2 ml[2][kRows];
+    union {
+        struct {  // the plan; the loader has read it before it describes the first piece
+            long long scan[kThreads / 32];
+            int cut[2][4];  // sequence, head, item, tile of the range's ends
+            Seq cut_seq;    // the first sequence
+        };
+        float2 ml[2][kRows];  // one-tile items: the streams' row states
+    };
 };
 
-constexpr size_t kSmemQ = 0, kSmemRing = 2 * kTileBytes, kSmemMisc = kSmemRing + kStages * kTileBytes;
+constexpr size_t kSmemQ = 0, kSmemRing = 2 * kTileBytes, kSmemOut = kSmemRing + kStages * kTileBytes;
+constexpr uint32_t kOutBytes = 32 * 128;  // a softmax warp's staging: 32 rows of 128 bytes
+constexpr size_t kSmemMisc = kSmemOut + kSoftmaxWarps * kOutBytes;
 constexpr size_t kSmemBytes = kSmemMisc + sizeof(Misc);
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 // ---- the work line -----------------------------------------------------------
-
-struct Seq {
-    int n, ctx, tok0;  // query rows, tokens in the cache, first row
-};
 
 template <bool kTree>
 __device__ __forceinline__ Seq load_seq(const Params& p, int s, uint32_t* bad) {
@@ -158,11 +181,12 @@ __device__ __forceinline__ long long head_cost(const Seq& q, int tpt) {
     return full_cost<kTree>(q, tpt, full) + (rest ? last_cost<kTree>(q, rest, tpt) : 0);
 }
 
-// Tiles of an item that belong to ranges before a cut `off` cost units into it.
+// Tiles of an item that belong to ranges before a cut `off` cost units into
+// it; any monotone rule does that every reader computes alike.
 __device__ __forceinline__ int cut_tile(long long off, long long cost, int ntiles) {
     if (off <= kSnap) return 0;
     if (cost - off <= kSnap) return ntiles;
-    const int t = static_cast<int>((off * ntiles + cost / 2) / cost);
+    const int t = static_cast<int>(__ll2float_rn(off) / __ll2float_rn(cost) * ntiles + 0.5f);
     return min(max(t, 0), ntiles);
 }
 
@@ -200,31 +224,36 @@ __device__ __forceinline__ long long item_cost(const Params& p, const Item& it) 
                        : last_cost<kTree>(it.q, it.q.n - full * 2 * p.tpt, p.tpt);
 }
 
-// A CTA's walk over its range: next() yields its pieces of items in order.
+// The loader's walk over its CTA's range: next() yields the pieces in order.
 template <bool kTree>
 struct Walk {
     const Params& p;
     Item it;
+    Seq ahead;           // the sequence after it.s, read early
     int s1, h1, i1, t1;  // the range's end
     int ta, tb;          // tiles of the piece
     bool first;
 
-    __device__ __forceinline__ Walk(const Params& prm, const int (&cut)[2][4]) : p(prm), first(true) {
-        it.s = cut[0][0];
-        it.h = cut[0][1];
-        it.i = cut[0][2];
-        ta = cut[0][3];
-        s1 = cut[1][0];
-        h1 = cut[1][1];
-        i1 = cut[1][2];
-        t1 = cut[1][3];
+    __device__ __forceinline__ Walk(const Params& prm, const Misc& m) : p(prm), first(true) {
+        it.s = m.cut[0][0];
+        it.h = m.cut[0][1];
+        it.i = m.cut[0][2];
+        ta = m.cut[0][3];
+        it.q = m.cut_seq;
+        s1 = m.cut[1][0];
+        h1 = m.cut[1][1];
+        i1 = m.cut[1][2];
+        t1 = m.cut[1][3];
+    }
+    __device__ __forceinline__ void look_ahead() {
+        if (it.s + 1 < p.num_seqs) ahead = load_seq<kTree>(p, it.s + 1, nullptr);
     }
     __device__ __forceinline__ bool next() {
         bool step = !first;
         if (first) {
             first = false;
             if (it.s >= p.num_seqs) return false;
-            it.q = load_seq<kTree>(p, it.s, nullptr);
+            look_ahead();
             set_item<kTree>(p, it);
             step = ta >= it.cut_tiles();  // the range starts behind this item
         }
@@ -237,7 +266,8 @@ struct Walk {
                     it.h = 0;
                     do {
                         if (++it.s >= p.num_seqs) return false;
-                        it.q = load_seq<kTree>(p, it.s, nullptr);
+                        it.q = ahead;
+                        look_ahead();
                     } while (it.q.n == 0);
                 }
             }
@@ -249,20 +279,38 @@ struct Walk {
         tb = last ? t1 : it.cut_tiles();
         return true;
     }
-    __device__ __forceinline__ bool whole() const { return ta == 0 && tb == it.cut_tiles(); }
-    // key tiles of the piece, and of each stream
-    __device__ __forceinline__ int count() const { return min(tb, it.nt) - ta; }
-    __device__ __forceinline__ int stream_count(int stream) const {
-        const int c = max(count(), 0);
-        if (!it.two) return (c + 1 - stream) >> 1;
-        if (stream == 1 || kTree) return c;
-        const int own = (max(it.pos0 + p.tpt, 0) + kKeys - 1) / kKeys;  // tiles the first tile's rows see
-        return max(min(own - ta, c), 0);
+    __device__ __forceinline__ void describe(Piece& d) const {
+        d.ta = ta;
+        const int c = max(min(tb, it.nt) - ta, 0);
+        d.count = c;
+        if (!it.two) {
+            d.cnt[0] = (c + 1) >> 1;
+            d.cnt[1] = c >> 1;
+        } else {
+            // the first tile's rows see no tile past their own last token's
+            const int own = kTree ? it.nt : (max(it.pos0 + p.tpt, 0) + kKeys - 1) / kKeys;
+            d.cnt[0] = max(min(own - ta, c), 0);
+            d.cnt[1] = c;
+        }
+        d.two = it.two;
+        d.whole = ta == 0 && tb == it.cut_tiles();
+        d.tok0 = it.tok0;
+        d.ntok = it.ntok;
+        d.pos0 = it.pos0;
+        d.first_masked = it.first_masked;
+        d.kend = it.kend;
+        d.nct = it.nct;
+        d.s = it.s;
+        d.h = it.h;
+        d.seq_n = it.q.n;
+        d.seq_tok0 = it.q.tok0;
+        d.ctx = it.q.ctx;
     }
-    // place of the piece's j-th K or V tile in the ring's order
-    __device__ __forceinline__ int ring_k(int j) const { return it.two ? 2 * j : max(2 * j - 1, 0); }
-    __device__ __forceinline__ int ring_v(int j) const { return it.two || j == count() - 1 ? 2 * j + 1 : 2 * j + 2; }
 };
+
+// Place of a piece's j-th K or V tile in the ring, in the order of their use.
+__device__ __forceinline__ int ring_k(bool two, int j) { return two ? 2 * j : max(2 * j - 1, 0); }
+__device__ __forceinline__ int ring_v(bool two, int j, int count) { return two || j == count - 1 ? 2 * j + 1 : 2 * j + 2; }
 
 // Every thread of the CTA: the ends of this CTA's range, and the description
 // of the item that its end cuts.
@@ -273,8 +321,10 @@ __device__ void plan(const Params& p, Misc& m) {
     const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
     long long sum = 0;
     uint32_t bad = 0;
+    Seq seq0 = {0, 0, 0};
     for (int s = s0; s < s1; ++s) {
         const Seq q = load_seq<kTree>(p, s, &bad);
+        if (s == s0) seq0 = q;
         sum += head_cost<kTree>(q, p.tpt) * p.hkv;
     }
     if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
@@ -294,50 +344,51 @@ __device__ void plan(const Params& p, Misc& m) {
         if (w < warp) before += v;
         total += v;
     }
-    const long long fit = total / kMinRange;
-    const int ranges = static_cast<int>(min(static_cast<long long>(gridDim.x), max(fit, 1ll)));
+    const int ranges = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total / kMinRange, 1ll)));
+    const long long chunk = (total + ranges - 1) / ranges;
     const int b = blockIdx.x;
-    if (b >= ranges || total == 0) return;  // the ends stay behind the last sequence
     for (int e = 0; e < 2; ++e) {
-        if (b + e >= ranges) break;
-        const long long x = total * (b + e) / ranges;
-        if (x < before || x >= before + sum) continue;
+        const long long x = chunk * (b + e);
+        if (x < before || x >= before + sum) continue;  // at or past the line's end: behind the last sequence
         long long at = before;
         for (int s = s0; s < s1; ++s) {
-            const Seq q = load_seq<kTree>(p, s, nullptr);
-            const long long hc = head_cost<kTree>(q, p.tpt);
+            Item it;
+            it.q = s == s0 ? seq0 : load_seq<kTree>(p, s, nullptr);
+            const long long hc = head_cost<kTree>(it.q, p.tpt);
             if (x >= at + hc * p.hkv) {
                 at += hc * p.hkv;
                 continue;
             }
-            Item it;
             it.s = s;
-            it.q = q;
-            it.h = static_cast<int>((x - at) / hc);
-            const long long base = at + it.h * hc, off = x - base;
-            // the last item that starts at or before off
-            int lo = 0, hi = (q.n + 2 * p.tpt - 1) / (2 * p.tpt) - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (full_cost<kTree>(q, p.tpt, mid) <= off) lo = mid; else hi = mid - 1;
-            }
-            it.i = lo;
+            // estimates, then the exact head and item
+            it.h = min(static_cast<int>(__ll2float_rn(x - at) / __ll2float_rn(hc)), p.hkv - 1);
+            while (it.h > 0 && hc * it.h > x - at) --it.h;
+            while (it.h + 1 < p.hkv && hc * (it.h + 1) <= x - at) ++it.h;
+            const long long base = at + hc * it.h, off = x - base;
+            const int items = (it.q.n + 2 * p.tpt - 1) / (2 * p.tpt);
+            const float one = __ll2float_rn(full_cost<kTree>(it.q, p.tpt, 1)), bend = kTree ? 0.f : static_cast<float>(kCostTwo) * p.tpt;
+            // cost of i items: bend * i^2 + (one - bend) * i
+            const float lin = one - bend, o = __ll2float_rn(off);
+            const float guess = 2.f * o / (lin + sqrtf(lin * lin + 4.f * bend * o));
+            it.i = min(static_cast<int>(guess), items - 1);
+            while (it.i > 0 && full_cost<kTree>(it.q, p.tpt, it.i) > off) --it.i;
+            while (it.i + 1 < items && full_cost<kTree>(it.q, p.tpt, it.i + 1) <= off) ++it.i;
             set_item<kTree>(p, it);
-            const long long start = base + full_cost<kTree>(q, p.tpt, lo), cost = item_cost<kTree>(p, it);
+            const long long start = base + full_cost<kTree>(it.q, p.tpt, it.i), cost = item_cost<kTree>(p, it);
             const int t = cut_tile(x - start, cost, it.cut_tiles());
             m.cut[e][0] = s;
             m.cut[e][1] = it.h;
             m.cut[e][2] = it.i;
             m.cut[e][3] = t;
+            if (e == 0) m.cut_seq = it.q;
             // this CTA has the item's first piece and not its last
             if (e == 1 && t > 0 && t < it.cut_tiles() &&
-                (b == 0 || total * b / ranges <= start || cut_tile(total * b / ranges - start, cost, it.cut_tiles()) == 0)) {
+                (x - chunk <= start || cut_tile(x - chunk - start, cost, it.cut_tiles()) == 0)) {
                 Split sp;
                 sp.start = start;
-                sp.total = total;
                 sp.cost = cost;
+                sp.chunk = chunk;
                 sp.ntiles = it.cut_tiles();
-                sp.ranges = ranges;
                 sp.tok0 = it.tok0;
                 sp.ntok = it.ntok;
                 sp.head0 = it.h * p.group;
@@ -354,38 +405,33 @@ __device__ __forceinline__ uint32_t non_finite2(uint32_t w) {  // a set sign bit
     return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 
-// Rows [0, valid) of a value tile in the ring: non-finite values become zero;
-// rows behind them become zero whole. Returns this lane's verdict on a row.
-__device__ __forceinline__ bool clean_row(uint8_t* tile, int row, int lane, bool valid) {
-    uint8_t* base = tile + (row >> 3) * 2048 + (row & 7) * 128;
-    bool bad = false;
+// One 128-byte half of a row of a value tile in the ring: its non-finite values
+// become zero; whether there were any.
+__device__ __forceinline__ bool clean_half_row(uint8_t* half, int lane) {
+    uint4 v[8];
+    uint32_t any = 0;
+    // lanes start at different 16-byte chunks of their rows: no bank conflicts
 #pragma unroll
-    for (int panel = 0; panel < 2; ++panel)
+    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(half + ((i + lane) & 7) * 16);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // lanes start at different 16-byte chunks of their rows: no bank conflicts
-            uint4* c = reinterpret_cast<uint4*>(base + panel * 1024 + ((i + lane) & 7) * 16);
-            if (!valid) {
-                *c = make_uint4(0, 0, 0, 0);
-                continue;
-            }
-            uint4 v = *c;
-            const uint32_t x = non_finite2(v.x), y = non_finite2(v.y), z = non_finite2(v.z), w = non_finite2(v.w);
-            if (x | y | z | w) {
-                bad = true;
-                v.x &= ~((x >> 15) * 0xFFFFu);
-                v.y &= ~((y >> 15) * 0xFFFFu);
-                v.z &= ~((z >> 15) * 0xFFFFu);
-                v.w &= ~((w >> 15) * 0xFFFFu);
-                *c = v;
-            }
-        }
-    return bad;
+    for (int i = 0; i < 8; ++i) any |= non_finite2(v[i].x) | non_finite2(v[i].y) | non_finite2(v[i].z) | non_finite2(v[i].w);
+    if (any == 0) return false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        auto finite = [](uint32_t w) { return w & ~((non_finite2(w) >> 15) * 0xFFFFu); };
+        *reinterpret_cast<uint4*>(half + ((i + lane) & 7) * 16) = make_uint4(finite(v[i].x), finite(v[i].y), finite(v[i].z), finite(v[i].w));
+    }
+    return true;
+}
+
+__device__ __forceinline__ void zero_half_row(uint8_t* half, int lane) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(half + ((i + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
 }
 
 // The keys of a masked tile that a row sees, as four words of 32.
 template <bool kTree>
-__device__ __forceinline__ void seen_words(const Item& it, int tile, int vis, uint64_t draft_mask, uint32_t (&w)[4]) {
+__device__ __forceinline__ void seen_words(const Piece& it, int tile, int vis, uint64_t draft_mask, uint32_t (&w)[4]) {
     if (kTree && tile == it.nct) {
         w[0] = static_cast<uint32_t>(draft_mask);
         w[1] = static_cast<uint32_t>(draft_mask >> 32);
@@ -404,7 +450,7 @@ __device__ __forceinline__ void seen_words(const Item& it, int tile, int vis, ui
 // taken out of the product for keys the row sees (their weights are positive,
 // so each weighted value is the value itself). bad: the words of tiles t_lo ..
 template <bool kTree, typename T>
-__device__ void add_non_finite(const Params& p, const Item& it, int t_lo, int t_hi, const uint32_t (*bad)[4], int vis,
+__device__ void add_non_finite(const Params& p, const Piece& it, int t_lo, int t_hi, const uint32_t (*bad)[4], int vis,
                                uint64_t draft_mask, int lo, int hi, T* out_row) {
     for (int t = t_lo; t < t_hi; ++t) {
         uint32_t w[4];
@@ -417,7 +463,7 @@ __device__ void add_non_finite(const Params& p, const Item& it, int t_lo, int t_
                 bits &= bits - 1;
                 const __nv_bfloat16* row;
                 if (kTree && t == it.nct) {
-                    row = p.v_draft + (static_cast<long long>(it.q.tok0 + key) * p.hkv + it.h) * kDim;
+                    row = p.v_draft + (static_cast<long long>(it.seq_tok0 + key) * p.hkv + it.h) * kDim;
                 } else {
                     const int pos = t * kKeys + key;
                     int blk = __ldg(p.block_tables + static_cast<long long>(it.s) * p.max_blocks + pos / p.bt);
@@ -469,10 +515,22 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             mbar_init(smem_u32(&m.s_full[i]), 1);
             mbar_init(smem_u32(&m.p_full[i]), 4);
             mbar_init(smem_u32(&m.o_full[i]), 1);
-            mbar_init(smem_u32(&m.item_done[i]), kSoftmaxWarps);
             mbar_init(smem_u32(&m.join[i]), kSoftmaxWarps);
         }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(smem_u32(&m.piece_full[i]), 1);
+            mbar_init(smem_u32(&m.piece_empty[i]), kSoftmaxWarps + 3);
+        }
         fence_barrier_init();
+    }
+    if (tid == kWarpLoad * 32) {
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+        if (kTree) {
+            prefetch_tensormap(&tm_kd);
+            prefetch_tensormap(&tm_vd);
+        }
     }
     if (warp == kWarpMma) tmem_alloc(smem_u32(&m.tmem), kTmemColumns);
     tc_fence_before();
@@ -480,7 +538,16 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m.tmem;
-    Walk<kTree> walk(p, m.cut);
+    // A reader of the pieces: the n-th, or null when there are no more (or the pipeline broke).
+    auto get_piece = [&](uint32_t n) -> const Piece* {
+        const bool ok = mbar_wait(smem_u32(&m.piece_full[n % kPieces]), (n / kPieces) & 1, abort_flag, p.err);
+        const Piece& d = m.piece[n % kPieces];
+        return __all_sync(0xFFFFFFFFu, ok) && d.count >= 0 ? &d : nullptr;
+    };
+    auto done_piece = [&](uint32_t n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&m.piece_empty[n % kPieces]));
+    };
 
     if (warp < kSoftmaxWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -492,25 +559,28 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const int row_tok = row / p.group, row_head = row - row_tok * p.group;
         const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
         uint32_t n_s = 0, n_o = 0, n_join = 0, n_item = 0;
-        for (; walk.next(); ++n_item) {
-            const Item& it = walk.it;
+        for (;; ++n_item) {
+            const Piece* const piece = get_piece(n_item);
+            if (!piece) break;
+            const Piece& it = *piece;
             const int tile_tok = it.two ? stream * p.tpt : 0;
             const int tok = it.tok0 + tile_tok + row_tok;
             const bool valid = row_tok < p.tpt && tile_tok + row_tok < it.ntok;
             const bool warp_valid = __any_sync(0xFFFFFFFFu, valid);
-            const int vis = kTree ? it.q.ctx : valid ? it.pos0 + tile_tok + row_tok + 1 : 0;
+            const int vis = kTree ? it.ctx : valid ? it.pos0 + tile_tok + row_tok + 1 : 0;
             uint64_t draft_mask = 0;
             if (kTree && valid) {
                 draft_mask = static_cast<uint64_t>(__ldg(reinterpret_cast<const long long*>(p.masks) + tok));
-                if (it.q.n < 64) draft_mask &= (1ull << it.q.n) - 1ull;
+                if (it.seq_n < 64) draft_mask &= (1ull << it.seq_n) - 1ull;
             }
-            const int count = walk.stream_count(stream);
+            const int count = it.cnt[stream];
+            const int first_masked = it.first_masked, tile0 = it.two ? it.ta : it.ta + stream, tile_step = it.two ? 1 : 2;
             float mx = -INFINITY;  // reference of the exponentials, unscaled
             float l = 0.f;
             bool any = false;
             bool ok = true;
             for (int i = 0; i < count; ++i) {
-                const int tile = walk.ta + (it.two ? i : 2 * i + stream);
+                const int tile = tile0 + i * tile_step;
                 ok = mbar_wait(smem_u32(&m.s_full[stream]), n_s & 1, abort_flag, p.err);
                 ++n_s;
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
@@ -523,7 +593,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     hold(s[1]);
                     hold(s[2]);
                     hold(s[3]);
-                    if (tile >= it.first_masked) {
+                    if (tile >= first_masked) {
                         uint32_t w[4];
                         seen_words<kTree>(it, tile, vis, draft_mask, w);
                         any |= (w[0] | w[1] | w[2] | w[3]) != 0;
@@ -538,9 +608,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     float m4[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        m4[k] = __uint_as_float(s[k][0]);
+                        m4[k] = fmaxf(__uint_as_float(s[k][0]), __uint_as_float(s[k][1]));
 #pragma unroll
-                        for (int c = 1; c < 32; ++c) m4[k] = fmaxf(m4[k], __uint_as_float(s[k][c]));
+                        for (int c = 2; c < 32; c += 2)
+                            m4[k] = fmaxf(m4[k], fmaxf(__uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1])));
                     }
                     const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     // The reference only has to keep the exponentials in range: it
@@ -554,7 +625,19 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     }
                     const float ref = mx == -INFINITY ? 0.f : -mx * p.scale_log2;
                     const uint64_t ref2 = pair(ref, ref);
-                    uint64_t sum2 = pair(l * factor, 0.f);
+                    uint64_t sum2[4] = {pair(l * factor, 0.f), pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f)};
+                    // S of this tile being complete, so is the stream's previous product
+                    if (i > 0 && __any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t o[32];
+                            tmem_ld32(o, t_o + 32 * k);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * factor);
+                            tmem_st32(t_o + 32 * k, o);
+                        }
+                    }
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         uint32_t pk[32];
@@ -565,7 +648,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                             unpair(fma2(pair(__uint_as_float(sk[c & 31]), __uint_as_float(sk[(c & 31) + 1])), scale2, ref2), a, b);
                             a = ex2(a);
                             b = ex2(b);
-                            sum2 = add2(sum2, pair(a, b));
+                            sum2[(c >> 1) & 3] = add2(sum2[(c >> 1) & 3], pair(a, b));
                             // the weights enter the product as bf16, as the tensor
                             // core takes them; their sum stays in fp32
                             pk[c >> 1] = pack_bf16x2(a, b);
@@ -573,20 +656,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                         tmem_st32(t_s + 32 * half, pk);
                     }
                     float s0, s1;
-                    unpair(sum2, s0, s1);
+                    unpair(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])), s0, s1);
                     l = s0 + s1;
-                    // S of this tile being complete, so is the stream's previous product
-                    if (i > 0 && __any_sync(0xFFFFFFFFu, grow)) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t o[32];
-                            tmem_ld32(o, t_o + 32 * k);
-                            tmem_wait_ld(o);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * factor);
-                            tmem_st32(t_o + 32 * k, o);
-                        }
-                    }
                     tmem_wait_st();
                 }
                 tc_fence_before();
@@ -603,29 +674,43 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 
             // the row's state: maximum (log2 units; any finite value says that the row sees a key) and sum
             float2 st = make_float2(any ? (mx == -INFINITY ? -FLT_MAX : mx * p.scale_log2) : -INFINITY, l);
-            const bool whole = walk.whole();
-            const int t_lo = max(it.first_masked, walk.ta), t_hi = min(walk.tb, it.nt);
-            const uint32_t(*bad)[4] = m.bad[n_item & 1];
-            const long long slot = 2ll * blockIdx.x + (walk.ta == 0 ? 1 : 0);
+            const bool whole = it.whole;
+            const int t_lo = max(first_masked, it.ta), t_hi = it.ta + it.count;
+            const uint32_t(*bad)[4] = m.bad[n_item % kPieces];
+            const long long slot = 2ll * blockIdx.x + (it.ta == 0 ? 1 : 0);
 
-            // 32 columns of the row, out or into the partial results
-            __nv_bfloat16* out_row = p.out + (static_cast<long long>(tok) * p.hq + it.h * p.group + row_head) * kDim;
-            auto put = [&](uint32_t (&o)[32], int col, float inv, long long prow) {
+            // The results leave through shared memory, 128 bytes of each of the
+            // warp's 32 rows at a time (64 columns of the output, 32 of a partial
+            // result), so that a store covers whole lines: straight from the
+            // accumulator's rows each store would touch 32 of them, which took
+            // 1.5-3.5 us an item.
+            uint8_t* const staging = smem + kSmemOut + warp * kOutBytes;
+            auto chunk = [&](int r, int c) { return reinterpret_cast<uint4*>(staging + r * 128 + ((c ^ (r & 7)) << 4)); };
+            const int out_row = valid ? tok * p.hq + it.h * p.group + row_head : -1;  // below 2^31: 256 bytes each
+            const long long part_row0 = slot * 2 * kRows + (it.two ? stream * kRows : 0) + (warp & 3) * 32;
+            auto put = [&](uint32_t (&o)[32], int col, float inv) {
                 if (whole) {
                     auto two = [&](int c) { return pack_bf16x2(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv); };
+                    const int c0 = (col >> 3) & 4;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 8)
-                        *reinterpret_cast<uint4*>(out_row + col + c) = make_uint4(two(c), two(c + 2), two(c + 4), two(c + 6));
+                    for (int c = 0; c < 4; ++c)
+                        *chunk(lane, c0 + c) = make_uint4(two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
+                    if (c0 == 0) return;  // the other half of the 64 columns follows
                 } else {
-                    float* dst = p.part_o + (slot * 2 * kRows + prow) * kDim + col;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 8) {
-                        uint32_t v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = o[c + e];
-                        st_global_32b(dst + c, v);
-                    }
+                    for (int c = 0; c < 8; ++c) *chunk(lane, c) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                 }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int r = 4 * k + (lane >> 3);
+                    const int orow = __shfl_sync(0xFFFFFFFFu, out_row, r);
+                    if (orow < 0) continue;
+                    const uint4 v = *chunk(r, lane & 7);
+                    if (whole) *reinterpret_cast<uint4*>(p.out + static_cast<long long>(orow) * kDim + (col & ~63) + (lane & 7) * 8) = v;
+                    else *reinterpret_cast<uint4*>(p.part_o + (part_row0 + r) * kDim + col + (lane & 7) * 4) = v;
+                }
+                __syncwarp();
             };
             // what the sum is divided by; no key seen: zeros; only keys of weight zero: NaN, as 0 / 0
             auto inverse = [](const float2& s) {
@@ -635,7 +720,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             int col_lo = 0, col_hi = kDim, t_end = t_hi;  // this thread's columns; its stream's tiles
             long long prow = row;
             if (it.two) {
-                t_end = min(t_hi, walk.ta + count);
+                t_end = min(t_hi, it.ta + count);
                 prow += stream * kRows;
                 if (warp_valid) {
                     const float inv = inverse(st);
@@ -649,7 +734,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
                             for (int c = 0; c < 32; ++c) r[c] = 0;
                         }
-                        if (valid) put(r, col, inv, prow);
+                        put(r, col, inv);
                     }
                     if (valid && !whole) p.part_ml[slot * 2 * kRows + prow] = st;
                 }
@@ -669,7 +754,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 if (!meet(0)) break;
                 if (warp_valid) {
                     const float2 s0 = m.ml[0][row], s1 = m.ml[1][row];
-                    const bool one = walk.stream_count(1) == 0, none = walk.stream_count(0) == 0;
+                    const bool one = it.cnt[1] == 0, none = it.cnt[0] == 0;
                     float2 js;
                     js.x = fmaxf(s0.x, s1.x);
                     const float a0 = s0.x == js.x ? 1.f : ex2(s0.x - js.x), a1 = s1.x == js.x ? 1.f : ex2(s1.x - js.x);
@@ -692,7 +777,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                                     r[c] = __float_as_uint(__uint_as_float(r[c]) * a0 + __uint_as_float(r1[c]) * a1);
                             }
                         }
-                        if (valid) put(r, col, inv, prow);
+                        put(r, col, inv);
                     }
                     if (valid && !whole && stream == 0) p.part_ml[slot * 2 * kRows + prow] = js;
                 }
@@ -706,34 +791,35 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     any_bad |= bad[t - t_lo][0] | bad[t - t_lo][1] | bad[t - t_lo][2] | bad[t - t_lo][3];
                 if (any_bad) {
                     if (whole)
-                        add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi, out_row);
+                        add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi,
+                                              p.out + static_cast<long long>(out_row) * kDim);
                     else
                         add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi,
                                               p.part_o + (slot * 2 * kRows + prow) * kDim);
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&m.item_done[n_item & 1]));
+            done_piece(n_item);
         }
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
       if (warp == kWarpLoad) {
         // ---- loader: query tiles, then K and V tiles in the order of their use
-        if (lane == 0) {
-            prefetch_tensormap(&tm_q);
-            prefetch_tensormap(&tm_k);
-            prefetch_tensormap(&tm_v);
-            if (kTree) {
-                prefetch_tensormap(&tm_kd);
-                prefetch_tensormap(&tm_vd);
-            }
-        }
-        uint32_t ring = 0, n_q = 0, n_clean = 0;
+        uint32_t ring = 0, n_q = 0, n_clean = 0, n_item = 0;
+        Walk<kTree> walk(p, m);
         const int blocks_per_tile = kKeys / p.bt;
         bool ok = true;
-        while (ok && walk.next()) {
+        for (bool more = true; more; ++n_item) {
+            more = walk.next();
+            ok = mbar_wait(smem_u32(&m.piece_empty[n_item % kPieces]), ((n_item / kPieces) & 1) ^ 1, abort_flag, p.err);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (lane == 0) {
+                if (more) walk.describe(m.piece[n_item % kPieces]);
+                else m.piece[n_item % kPieces].count = -1;
+                mbar_arrive(smem_u32(&m.piece_full[n_item % kPieces]));
+            }
+            if (!more) break;
             const Item& it = walk.it;
-            const int count = walk.count();
+            const int count = min(walk.tb, it.nt) - walk.ta;
             if (count <= 0) continue;
             ok = mbar_wait(smem_u32(&m.q_empty), (n_q & 1) ^ 1, abort_flag, p.err);
             ++n_q;
@@ -787,121 +873,140 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 }
             };
             int cur = coordinate(0);
-            load(false, 0, walk.ring_k(0), cur);
+            load(false, 0, 0, cur);
             for (int j = 0; ok && j < count; ++j) {
                 int next = 0;
                 if (j + 1 < count) next = coordinate(j + 1);
-                if (!it.two && j + 1 < count) load(false, j + 1, walk.ring_k(j + 1), next);
-                if (ok) load(true, j, walk.ring_v(j), cur);
-                if (ok && it.two && j + 1 < count) load(false, j + 1, walk.ring_k(j + 1), next);
+                if (!it.two && j + 1 < count) load(false, j + 1, ring_k(it.two, j + 1), next);
+                if (ok) load(true, j, ring_v(it.two, j, count), cur);
+                if (ok && it.two && j + 1 < count) load(false, j + 1, ring_k(it.two, j + 1), next);
                 cur = next;
             }
             ring += 2 * count;
             n_clean += max(count - masked0, 0);
+            if (!ok) break;
         }
     } else if (warp == kWarpMma) {
-        // ---- tensor core: one thread issues every product
-        if (lane == 0) {
-            constexpr uint32_t kIdescS = mma_idesc(kRows, kKeys, false), kIdescO = mma_idesc(kRows, kDim, true);
-            uint32_t ring = 0, n_q = 0, n_clean = 0, n_p[2] = {0, 0};
-            bool ok = true;
-            while (ok && walk.next()) {
-                const Item& it = walk.it;
-                const int count = walk.count();
-                if (count <= 0) continue;
-                const int cnt[2] = {walk.stream_count(0), walk.stream_count(1)};
-                const int masked0 = max(it.first_masked, walk.ta) - walk.ta;  // first masked tile of the piece
-                ok = mbar_wait(smem_u32(&m.q_full), n_q & 1, abort_flag, p.err);
-                ++n_q;
-                if (!ok) break;
-                const int last_k = count - 1;
+        // ---- tensor core: one elected thread issues every product. The warp
+        // stays converged and its counters provably uniform: with the loop in
+        // one diverged lane, issuing the 8 products of a tile took 620-900
+        // cycles against the 512 they run for.
+        constexpr uint32_t kIdescS = mma_idesc(kRows, kKeys, false), kIdescO = mma_idesc(kRows, kDim, true);
+        const uint32_t tm = uniform(tmem), base = uniform(smem_base);
+        uint32_t ring = 0, n_q = 0, n_clean = 0, n_p[2] = {0, 0};
+        bool ok = true;
+        for (uint32_t n_item = 0; ok; ++n_item) {
+            const Piece* const piece = get_piece(n_item);
+            if (!piece) break;
+            const int count = uniform(piece->count);
+            const bool two = uniform(piece->two) != 0;
+            const int cnt[2] = {static_cast<int>(uniform(piece->cnt[0])), static_cast<int>(uniform(piece->cnt[1]))};
+            const int masked0 = uniform(max(piece->first_masked - piece->ta, 0));  // first masked tile of the piece
+            done_piece(n_item);
+            if (count == 0) continue;
+            ok = mbar_wait(smem_u32(&m.q_full), n_q & 1, abort_flag, p.err);
+            ++n_q;
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
 
-                // S of the stream's i-th key tile
-                auto scores = [&](int stream, int i) {
-                    const int j = it.two ? i : 2 * i + stream;
-                    const uint32_t at = ring + walk.ring_k(j), st = at % kStages;
-                    ok = mbar_wait(smem_u32(&m.kv_full[st]), (at / kStages) & 1, abort_flag, p.err);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint32_t a = smem_base + kSmemQ + (it.two ? stream * kTileBytes : 0);
-                    const uint32_t b = smem_base + kSmemRing + st * kTileBytes;
+            // S of the stream's i-th key tile
+            auto scores = [&](int stream, int i) {
+                const int j = two ? i : 2 * i + stream;
+                const uint32_t at = ring + ring_k(two, j), st = at % kStages;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&m.kv_full[st]), (at / kStages) & 1, abort_flag, p.err));
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t a = smem_desc(base + kSmemQ + (two ? stream * kTileBytes : 0), 16, 1024);
+                const uint64_t b = smem_desc(base + kSmemRing + st * kTileBytes, 16, 2048);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_ss(tmem + stream * 128, smem_desc(a + (k >> 2) * (kTileBytes / 2) + (k & 3) * 32, 16, 1024),
-                               smem_desc(b + (k >> 2) * 1024 + (k & 3) * 32, 16, 2048), kIdescS, k > 0);
+                        mma_ss(tm + stream * 128, a + (((k >> 2) * (kTileBytes / 2) + (k & 3) * 32) >> 4),
+                               b + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), kIdescS, k > 0);
                     mma_commit(smem_u32(&m.s_full[stream]));
-                    if (!it.two || stream == 1) mma_commit(smem_u32(&m.kv_empty[st]));
-                    if (j == last_k && (!it.two || stream == 1)) mma_commit(smem_u32(&m.q_empty));
-                };
-                // O += P V for the stream's i-th key tile
-                auto values = [&](int stream, int i) {
-                    const int j = it.two ? i : 2 * i + stream;
-                    const uint32_t at = ring + walk.ring_v(j), st = at % kStages;
-                    if (j >= masked0) {
-                        const uint32_t c = n_clean + (j - masked0);
-                        ok = mbar_wait(smem_u32(&m.clean[c % kCleanBars]), (c / kCleanBars) & 1, abort_flag, p.err);
-                    } else {
-                        ok = mbar_wait(smem_u32(&m.kv_full[st]), (at / kStages) & 1, abort_flag, p.err);
-                    }
-                    if (ok) ok = mbar_wait(smem_u32(&m.p_full[stream]), n_p[stream] & 1, abort_flag, p.err);
-                    ++n_p[stream];
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint32_t b = smem_base + kSmemRing + st * kTileBytes;
+                    if (!two || stream == 1) mma_commit(smem_u32(&m.kv_empty[st]));
+                    if (j == count - 1 && (!two || stream == 1)) mma_commit(smem_u32(&m.q_empty));
+                }
+                __syncwarp();
+            };
+            // O += P V for the stream's i-th key tile
+            auto values = [&](int stream, int i) {
+                const int j = two ? i : 2 * i + stream;
+                const uint32_t at = ring + ring_v(two, j, count), st = at % kStages;
+                if (j >= masked0) {
+                    const uint32_t c = n_clean + (j - masked0);
+                    ok = mbar_wait(smem_u32(&m.clean[c % kCleanBars]), (c / kCleanBars) & 1, abort_flag, p.err);
+                } else {
+                    ok = mbar_wait(smem_u32(&m.kv_full[st]), (at / kStages) & 1, abort_flag, p.err);
+                }
+                if (ok) ok = mbar_wait(smem_u32(&m.p_full[stream]), n_p[stream] & 1, abort_flag, p.err);
+                ++n_p[stream];
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t b = smem_desc(base + kSmemRing + st * kTileBytes, 1024, 2048);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_ts(tmem + kTmemO + stream * 128, tmem + stream * 128 + k * 8, smem_desc(b + k * 4096, 1024, 2048),
-                               kIdescO, i > 0 || k > 0);
-                    if (!it.two || stream == 1) mma_commit(smem_u32(&m.kv_empty[st]));
+                        mma_ts(tm + kTmemO + stream * 128, tm + stream * 128 + k * 8, b + ((k * 4096) >> 4), kIdescO,
+                               i > 0 || k > 0);
+                    if (!two || stream == 1) mma_commit(smem_u32(&m.kv_empty[st]));
                     if (i == cnt[stream] - 1) mma_commit(smem_u32(&m.o_full[stream]));
-                };
+                }
+                __syncwarp();
+            };
 
-                if (cnt[0] > 0) scores(0, 0);
-                if (ok && cnt[1] > 0) scores(1, 0);
-                const int rounds = max(cnt[0], cnt[1]);
-                for (int i = 0; ok && i < rounds; ++i)
-                    for (int stream = 0; ok && stream < 2; ++stream) {
-                        if (i >= cnt[stream]) continue;
-                        values(stream, i);
-                        if (ok && i + 1 < cnt[stream]) scores(stream, i + 1);
-                    }
-                ring += 2 * count;
-                n_clean += max(count - masked0, 0);
-            }
+            if (cnt[0] > 0) scores(0, 0);
+            if (ok && cnt[1] > 0) scores(1, 0);
+            const int rounds = max(cnt[0], cnt[1]);
+            for (int i = 0; ok && i < rounds; ++i)
+#pragma unroll
+                for (int stream = 0; stream < 2; ++stream) {
+                    if (!ok || i >= cnt[stream]) continue;
+                    values(stream, i);
+                    if (ok && i + 1 < cnt[stream]) scores(stream, i + 1);
+                }
+            ring += 2 * count;
+            n_clean += max(count - masked0, 0);
         }
-        __syncwarp();
     } else {
         // ---- value tiles that not every row sees in full
         const int half = warp - kWarpClean;
-        uint32_t ring = 0, n_clean = 0, n_item = 0;
+        uint32_t n_clean = 0;
         bool ok = true;
-        for (; ok && walk.next(); ++n_item) {
-            const Item& it = walk.it;
-            const int count = walk.count();
-            // the epilogue of the item before the last has read its words
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&m.item_done[n_item & 1]), ((n_item >> 1) & 1) ^ 1, abort_flag, p.err));
-            if (count <= 0) continue;
-            const int masked0 = max(it.first_masked, walk.ta) - walk.ta;
+        for (uint32_t n_item = 0, ring = 0; ok; ++n_item) {
+            const Piece* const piece = get_piece(n_item);
+            if (!piece) break;
+            const int count = piece->count;
+            const int masked0 = max(piece->first_masked - piece->ta, 0);
             for (int j = masked0; ok && j < count; ++j, ++n_clean) {
-                const uint32_t at = ring + walk.ring_v(j), st = at % kStages;
+                const uint32_t st = (ring + ring_v(piece->two, j, count)) % kStages;
+                const int t = piece->ta + j;
+                const int valid = kTree && t == piece->nct ? piece->seq_n : min(kKeys, piece->kend - t * kKeys);
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&m.part_full[n_clean % kCleanBars]),
                                                        (n_clean / kCleanBars) & 1, abort_flag, p.err));
                 if (!ok) break;
-                const int t = walk.ta + j;
-                const int valid = kTree && t == it.nct ? it.q.n : min(kKeys, it.kend - t * kKeys);
                 uint8_t* tile = smem + kSmemRing + st * kTileBytes;
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int row = half * 64 + r * 32 + lane;
-                    const bool bad = clean_row(tile, row, lane, row < valid);
+                    uint8_t* const halves = tile + (row >> 3) * 2048 + (row & 7) * 128;
+                    bool bad = false;
+                    if (row < valid) {
+                        bad = clean_half_row(halves, lane);
+                        bad |= clean_half_row(halves + 1024, lane);
+                    } else {
+                        zero_half_row(halves, lane);
+                        zero_half_row(halves + 1024, lane);
+                    }
                     const uint32_t word = __ballot_sync(0xFFFFFFFFu, bad);
-                    if (lane == 0) m.bad[n_item & 1][j - masked0][half * 2 + r] = word;
+                    if (lane == 0) m.bad[n_item % kPieces][j - masked0][half * 2 + r] = word;
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&m.clean[n_clean % kCleanBars]));
             }
             ring += 2 * count;
+            done_piece(n_item);
         }
       }
     }
@@ -932,9 +1037,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Params p)
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         int t = 0;
-        for (int c = c0; t < sp.ntiles && c < sp.ranges; ++c) {
-            const long long end = sp.total * (c + 1) / sp.ranges - sp.start;
-            const int t_end = c + 1 >= sp.ranges || end >= sp.cost ? sp.ntiles : cut_tile(end, sp.cost, sp.ntiles);
+        for (int c = c0; t < sp.ntiles; ++c) {
+            const long long end = sp.chunk * (c + 1) - sp.start;
+            const int t_end = end >= sp.cost ? sp.ntiles : cut_tile(end, sp.cost, sp.ntiles);
             if (t_end <= t) continue;  // no piece in this range
             t = t_end;
             const long long prow = (2ll * c + (c == c0 ? 1 : 0)) * 2 * kRows + r;
