@@ -506,33 +506,56 @@ def attn_decode_static(q, k_cache, v_cache, block_tables, context_lens, scale, o
 # many query rows per sequence: prompts, draft trees, and the way into the cache
 
 
-@contextlib.contextmanager
-def _launch_on(stream, **tensors):
-    """Checks that the named tensors share one CUDA device; inside, that device
-    is current and new tensors belong to `stream` (default: the device's
-    current stream). Yields the stream's handle."""
-    device = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, other tensors on {device}")
-    if stream is None and torch.cuda.current_device() == device.index:
-        yield torch.cuda.current_stream().cuda_stream
-        return
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
-            return
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
-        if s.device != device:
-            raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
-        with torch.cuda.stream(s):
-            yield s.cuda_stream
+def _need_all(device: int, tensors) -> None:
+    """Each (tensor, dtype, name): that dtype, contiguous, on that CUDA device."""
+    for t, dtype, name in tensors:
+        if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or device < 0:
+            _need(t, dtype, name)
+            raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{device}")
+
+
+class _LaunchOn:
+    """Makes a device current, and `stream` where one is given, so that new
+    tensors belong to it; yields the stream's handle."""
+
+    def __init__(self, device: int, stream):
+        self.device, self.stream = device, stream
+
+    def __enter__(self) -> int:
+        self.guards = contextlib.ExitStack()
+        self.guards.enter_context(torch.cuda.device(self.device))
+        if self.stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device)
+        s = self.stream
+        if not isinstance(s, torch.cuda.Stream):
+            s = torch.cuda.ExternalStream(int(s), device=self.device)
+        if s.device.index != self.device:
+            self.guards.close()
+            raise ValueError(f"the stream is on {s.device}, the tensors on cuda:{self.device}")
+        self.guards.enter_context(torch.cuda.stream(s))
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        self.guards.close()
+
+
+class _LaunchHere:
+    """The same for the current device and its current stream: nothing to do."""
+
+    def __init__(self, device: int):
+        self.device = device
+
+    def __enter__(self) -> int:
+        return torch._C._cuda_getCurrentRawStream(self.device)
+
+    def __exit__(self, *exc):
+        pass
+
+
+def _launch_on(device: int, stream):
+    if stream is None and torch.cuda.current_device() == device:
+        return _LaunchHere(device)
+    return _LaunchOn(device, stream)
 
 
 class PrefillWorkspace:
@@ -549,39 +572,40 @@ class PrefillWorkspace:
             self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=dev)
             off = (-self.buffer.data_ptr()) % 256
             self.tensor = self.buffer[off : off + self.nbytes]
+            self.ptr, self.device = self.tensor.data_ptr(), self.tensor.get_device()
             # only the header has to hold zeros
-            _check(_lib.pkv_attn_workspace_init(self.tensor.data_ptr(), 256, _stream(stream)),
-                   "pkv_attn_workspace_init")
-
-    @property
-    def ptr(self) -> int:
-        return self.tensor.data_ptr()
+            _check(_lib.pkv_attn_workspace_init(self.ptr, 256, _stream(stream)), "pkv_attn_workspace_init")
 
     def read_error(self, clear: bool = True, stream=None) -> int:
         return read_device_error(self.tensor[:4].view(torch.int32), clear, stream)
 
 
-def _rows_shapes(q, k_cache, v_cache, block_tables, context_lens, query_starts, out):
-    for t, dt, name in ((q, torch.bfloat16, "q"), (k_cache, torch.bfloat16, "k_cache"),
-                        (v_cache, torch.bfloat16, "v_cache"), (block_tables, torch.int32, "block_tables"),
-                        (context_lens, torch.int32, "context_lens"), (query_starts, torch.int32, "query_starts")):
-        _need(t, dt, name)
+_BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+
+
+def _rows_shapes(q, k_cache, v_cache, block_tables, context_lens, query_starts, out, workspace):
+    device = q.get_device()
+    _need_all(device, ((q, _BF16, "q"), (k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache"),
+                       (block_tables, _I32, "block_tables"), (context_lens, _I32, "context_lens"),
+                       (query_starts, _I32, "query_starts")))
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [T, Hq, D] and caches [NB, Hkv, block_tokens, D]")
     T, hq, d = q.shape
     nb, hkv, bt, d2 = k_cache.shape
     if d != d2 or v_cache.shape != k_cache.shape or bt not in BLOCK_SIZES:
         raise ValueError("q [T, Hq, D] and caches [NB, Hkv, block_tokens in (8, 16, 32, 64), D] must agree")
-    if block_tables.dim() != 2 or context_lens.shape != (block_tables.shape[0],):
+    if block_tables.dim() != 2 or context_lens.shape != block_tables.shape[:1]:
         raise ValueError("block_tables must be [B, W] and context_lens [B]")
     B, width = block_tables.shape
-    if query_starts.shape != (B + 1,):
+    if query_starts.dim() != 1 or query_starts.shape[0] != B + 1:
         raise ValueError("query_starts must be [B + 1]")
     if out is not None:
-        _need(out, torch.bfloat16, "out")
+        _need_all(device, ((out, _BF16, "out"),))
         if out.shape != q.shape:
             raise ValueError("out must be shaped like q")
-    return T, hq, d, nb, hkv, bt, B, width
+    if workspace is not None and workspace.device != device:
+        raise ValueError(f"the workspace is on cuda:{workspace.device}, the tensors on cuda:{device}")
+    return device, (T, hq, hkv, d, nb, bt), B, width
 
 
 def attn_prefill(q, k_cache, v_cache, block_tables, context_lens, query_starts, scale, out=None, workspace=None,
@@ -591,16 +615,15 @@ def attn_prefill(q, k_cache, v_cache, block_tables, context_lens, query_starts, 
     the last tokens of sequence s, whose context_lens[s] tokens are all in the
     cache. Returns out [T, Hq, 128]; rows of no sequence are left as they were
     (zeros in an `out` made here)."""
-    T, hq, d, nb, hkv, bt, B, width = _rows_shapes(q, k_cache, v_cache, block_tables, context_lens, query_starts, out)
-    with _launch_on(stream, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
-                    query_starts=query_starts, out=out, workspace=workspace and workspace.tensor) as st:
+    device, shape, B, width = _rows_shapes(q, k_cache, v_cache, block_tables, context_lens, query_starts, out, workspace)
+    with _launch_on(device, stream) as st:
         if out is None:
             out = torch.zeros_like(q)
         if workspace is None:
             workspace = PrefillWorkspace(q.device)
-        _check(_lib.pkv_attn_prefill(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), width,
-                                     _ptr(context_lens), _ptr(query_starts), B, T, hq, hkv, d, nb, bt, float(scale),
-                                     workspace.ptr, workspace.nbytes, _ptr(out), st), "pkv_attn_prefill")
+        _check(_lib.pkv_attn_prefill(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+                                     width, context_lens.data_ptr(), query_starts.data_ptr(), B, *shape, float(scale),
+                                     workspace.ptr, workspace.nbytes, out.data_ptr(), st), "pkv_attn_prefill")
     return out
 
 
@@ -611,23 +634,20 @@ def attn_tree(q, k_draft, v_draft, tree_masks, k_cache, v_cache, block_tables, c
     context_lens[s] tokens of its sequence in the cache and the drafts j of the
     sequence whose bit j is set in tree_masks[i] (int64, see tree_masks()).
     Returns out [T, Hq, 128]; the cache is not written."""
-    T, hq, d, nb, hkv, bt, B, width = _rows_shapes(q, k_cache, v_cache, block_tables, context_lens, query_starts, out)
-    _need(k_draft, torch.bfloat16, "k_draft")
-    _need(v_draft, torch.bfloat16, "v_draft")
-    _need(tree_masks, torch.int64, "tree_masks")
+    device, shape, B, width = _rows_shapes(q, k_cache, v_cache, block_tables, context_lens, query_starts, out, workspace)
+    _need_all(device, ((k_draft, _BF16, "k_draft"), (v_draft, _BF16, "v_draft"), (tree_masks, _I64, "tree_masks")))
+    T, _, hkv, d = shape[:4]
     if k_draft.shape != (T, hkv, d) or v_draft.shape != (T, hkv, d) or tree_masks.shape != (T,):
         raise ValueError("k_draft, v_draft must be [T, Hkv, D] and tree_masks [T]")
-    with _launch_on(stream, q=q, k_draft=k_draft, v_draft=v_draft, tree_masks=tree_masks, k_cache=k_cache,
-                    v_cache=v_cache, block_tables=block_tables, context_lens=context_lens, query_starts=query_starts,
-                    out=out, workspace=workspace and workspace.tensor) as st:
+    with _launch_on(device, stream) as st:
         if out is None:
             out = torch.zeros_like(q)
         if workspace is None:
             workspace = PrefillWorkspace(q.device)
-        _check(_lib.pkv_attn_tree(_ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(tree_masks), _ptr(k_cache), _ptr(v_cache),
-                                  _ptr(block_tables), width, _ptr(context_lens), _ptr(query_starts), B, T, hq, hkv, d,
-                                  nb, bt, float(scale), workspace.ptr, workspace.nbytes, _ptr(out), st),
-               "pkv_attn_tree")
+        _check(_lib.pkv_attn_tree(q.data_ptr(), k_draft.data_ptr(), v_draft.data_ptr(), tree_masks.data_ptr(),
+                                  k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), width,
+                                  context_lens.data_ptr(), query_starts.data_ptr(), B, *shape, float(scale),
+                                  workspace.ptr, workspace.nbytes, out.data_ptr(), st), "pkv_attn_tree")
     return out
 
 
@@ -657,16 +677,18 @@ def rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0, devic
     return torch.cat([angle.cos(), angle.sin()], dim=1).float().contiguous().to(device or "cuda")
 
 
-def _need_rows(t: torch.Tensor, name: str, shape) -> int:
+def _need_rows(device: int, t: torch.Tensor, name: str, T: int, h: int, d: int) -> int:
     """bf16 [T, H, D] whose rows are contiguous; returns the stride of a token."""
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    T, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    if t.dtype is not _BF16:
+        raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
+    if t.shape != (T, h, d):
+        raise ValueError(f"{name} must be {[T, h, d]}, got {list(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0) if T > 1 else h * d
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name} is on {t.device}: all tensors must be on one CUDA device")
+    return s0 if T > 1 else h * d
 
 
 def qk_norm_rope_append(q, k, v, cos_sin, positions, slot_mapping, k_cache, v_cache, q_weight=None, k_weight=None,
@@ -678,42 +700,47 @@ def qk_norm_rope_append(q, k, v, cos_sin, positions, slot_mapping, k_cache, v_ca
     projection. Returns the normed, rotated queries [T, Hq, D]."""
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [T, Hq, D] and caches [NB, Hkv, block_tokens, D]")
+    device = q.get_device()
     T, hq, d = q.shape
     nb, hkv, bt, d2 = k_cache.shape
     if d != d2 or v_cache.shape != k_cache.shape or bt not in BLOCK_SIZES:
         raise ValueError("q [T, Hq, D] and caches [NB, Hkv, block_tokens in (8, 16, 32, 64), D] must agree")
-    strides = [_need_rows(t, name, (T, h, d)) for t, name, h in ((q, "q", hq), (k, "k", hkv), (v, "v", hkv))]
-    _need(k_cache, torch.bfloat16, "k_cache")
-    _need(v_cache, torch.bfloat16, "v_cache")
-    _need(slot_mapping, torch.int64, "slot_mapping")
+    qs = _need_rows(device, q, "q", T, hq, d)
+    ks = _need_rows(device, k, "k", T, hkv, d)
+    vs = _need_rows(device, v, "v", T, hkv, d)
+    _need_all(device, ((k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache"), (slot_mapping, _I64, "slot_mapping")))
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [T]")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, torch.bfloat16, name)
-            if w.shape != (d,):
-                raise ValueError(f"{name} must be [D]")
+    qw = kw = cs = ps = None
+    if q_weight is not None:
+        _need_all(device, ((q_weight, _BF16, "q_weight"),))
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _need_all(device, ((k_weight, _BF16, "k_weight"),))
+        kw = k_weight.data_ptr()
+    if (qw and q_weight.shape != (d,)) or (kw and k_weight.shape != (d,)):
+        raise ValueError("q_weight and k_weight must be [D]")
     max_positions = rotary = 0
     if cos_sin is not None:
-        _need(cos_sin, torch.float32, "cos_sin")
-        _need(positions, torch.int32, "positions")
+        _need_all(device, ((cos_sin, _F32, "cos_sin"), (positions, _I32, "positions")))
         if cos_sin.dim() != 2 or positions.shape != (T,):
             raise ValueError("cos_sin must be [positions, rotary_dim] and positions [T]")
         max_positions, rotary = cos_sin.shape
+        cs, ps = cos_sin.data_ptr(), positions.data_ptr()
     if q_out is not None:
-        _need(q_out, torch.bfloat16, "q_out")
+        _need_all(device, ((q_out, _BF16, "q_out"),))
         if q_out.shape != q.shape:
             raise ValueError("q_out must be shaped like q")
-    with _launch_on(stream, q=q, k=k, v=v, cos_sin=cos_sin, positions=positions if rotary else None,
-                    slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache, q_weight=q_weight, k_weight=k_weight,
-                    q_out=q_out, device_error=device_error) as st:
+    if device_error is not None:
+        _need_all(device, ((device_error, _I32, "device_error"),))
+    with _launch_on(device, stream) as st:
         if q_out is None:
-            q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
-        _check(_lib.pkv_qk_norm_rope_append(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
-                                            _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), max_positions,
-                                            rotary, int(interleaved), _ptr(positions) if rotary else None,
-                                            _ptr(slot_mapping), T, hq, hkv, d, _ptr(q_out), _ptr(k_cache),
-                                            _ptr(v_cache), nb, bt, _ptr(device_error), st), "pkv_qk_norm_rope_append")
+            q_out = torch.empty((T, hq, d), dtype=_BF16, device=q.device)
+        _check(_lib.pkv_qk_norm_rope_append(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, qw, kw, float(eps), cs,
+                                            max_positions, rotary, 1 if interleaved else 0, ps,
+                                            slot_mapping.data_ptr(), T, hq, hkv, d, q_out.data_ptr(),
+                                            k_cache.data_ptr(), v_cache.data_ptr(), nb, bt, _ptr(device_error), st),
+               "pkv_qk_norm_rope_append")
     return q_out
 
 

@@ -7,16 +7,22 @@
 // the rotation would each read, round and write the rows again). Bound by
 // bandwidth: every value is read once and written once.
 //
-// A row of head_dim values is held by a group of lanes, 8 values (16 bytes)
-// each, so every access is a whole 32-byte sector or more, the sum of squares
-// is a shuffle reduction, and a half-split pair's other half sits in a fixed
-// partner lane. A group walks the heads of one token, so the token's angles
-// are loaded once, into registers.
+// A row of head_dim values is held by a group of lanes, 16 values each: of the
+// rotated values the 8 first halves and the 8 second halves of the same pairs
+// (so a pair never crosses lanes), elsewhere 16 in a row. The groups of a
+// resident grid take the (token, head) rows in turn and read the next turn's
+// row, position and slot before they work on this one's, so that a turn waits
+// for memory once. 16,411 tokens of 64 + 16 heads of 128: 127 us, 5.4 TB/s
+// (211 us with a block per token and nothing read ahead, 175 us with three
+// heads read together; two or three heads a turn, two or four blocks an SM,
+// streaming stores: 127-139 us). 64 tokens of 32 + 16 heads: 2.7 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <mutex>
+#include <vector>
 
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
@@ -36,105 +42,144 @@ struct Params {
     uint32_t* err;
     long long slot_limit;
     float eps;
-    int max_positions, rot, num_tokens, hq, hkv, dim, bt;
-    int head_chunks;  // blocks per token
+    int max_positions, rot, num_tokens, hq, hkv, dim, bt_shift;
+    int step_tok, step_head;  // the grid's groups, as tokens and heads
 };
+
+// 16 bytes that are read once
+__device__ __forceinline__ uint4 ld_streaming(const __nv_bfloat16* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
     x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
     x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
 }
 
-// kLanes: lanes per head row (a power of two, at least head_dim / 8).
+constexpr int kBlocksPerSm = 3;
+
+// kLanes: lanes per head row (a power of two, at least head_dim / 16).
 template <int kLanes, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) qk_write_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) qk_write_kernel(const Params p) {
     constexpr int kGroups = kThreads / kLanes;
     const int lane = threadIdx.x & (kLanes - 1);
-    const int tok = blockIdx.x / p.head_chunks;
-    const int chunk = blockIdx.x - tok * p.head_chunks;
-    const bool live = lane * 8 < p.dim;  // lanes past a head_dim that is no power of two hold nothing
-
-    const long long slot = __ldg(p.slots + tok);
-    const bool store_kv = slot >= 0 && slot < p.slot_limit;
-    uint32_t bad = slot >= p.slot_limit ? PKV_DEVERR_SLOT : 0u;
-    const bool turned = lane * 8 < p.rot;
-    const int half_lanes = p.rot >> 4;                       // lanes of the first half of the rotated values
-    const bool upper = !kInterleaved && lane >= half_lanes;  // this lane holds the pairs' second values
-    float c[8], s[8];
-    if (p.rot > 0) {
-        int pos = __ldg(p.positions + tok);
-        if (pos < 0 || pos >= p.max_positions) {
-            if (slot >= 0) bad |= PKV_DEVERR_POSITION;
-            pos = min(max(pos, 0), p.max_positions - 1);
-        }
-        if (turned) {
-            const float* row = p.cos_sin + static_cast<long long>(pos) * p.rot;
-            const int a0 = kInterleaved ? lane * 4 : (upper ? lane - half_lanes : lane) * 8;
-#pragma unroll
-            for (int i = 0; i < (kInterleaved ? 4 : 8); i += 4) {
-                const float4 cv = __ldg(reinterpret_cast<const float4*>(row + a0 + i));
-                const float4 sv = __ldg(reinterpret_cast<const float4*>(row + (p.rot >> 1) + a0 + i));
-                c[i] = cv.x; c[i + 1] = cv.y; c[i + 2] = cv.z; c[i + 3] = cv.w;
-                s[i] = sv.x; s[i + 1] = sv.y; s[i + 2] = sv.z; s[i + 3] = sv.w;
-            }
-        }
-    }
-    if (bad && p.err && chunk == 0 && threadIdx.x == 0) atomicOr(p.err, bad);
-
-    const long long blk = store_kv ? slot / p.bt : 0;
-    const int in_blk = store_kv ? static_cast<int>(slot - blk * p.bt) : 0;
     const int heads = p.hq + 2 * p.hkv;
+
+    // this lane's two runs of 8 values
+    const bool turned = lane * 16 < p.rot;
+    const int at0 = kInterleaved || !turned ? lane * 16 : lane * 8;
+    const int at1 = kInterleaved || !turned ? at0 + 8 : at0 + (p.rot >> 1);
+    const bool live0 = at0 < p.dim, live1 = at1 < p.dim;  // a head_dim that is no multiple of 16 lanes' values
+
+    // this group's (token, head), heads of q, k and v in a row
+    const long long gid = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / kLanes;
+    int tok = static_cast<int>(gid / heads), h = static_cast<int>(gid - static_cast<long long>(tok) * heads);
+    uint4 ahead0, ahead1;
+    long long slot_ahead = -1;
+    int pos_ahead = 0;
+    auto read_ahead = [&](int t, int hd) {
+        ahead0 = ahead1 = make_uint4(0, 0, 0, 0);
+        if (t >= p.num_tokens) return;
+        const __nv_bfloat16* row = hd < p.hq ? p.q + t * p.q_stride
+                                 : hd < p.hq + p.hkv ? p.k + t * p.k_stride - static_cast<long long>(p.hq) * p.dim
+                                                     : p.v + t * p.v_stride - static_cast<long long>(p.hq + p.hkv) * p.dim;
+        row += static_cast<long long>(hd) * p.dim;
+        if (live0) ahead0 = ld_streaming(row + at0);
+        if (live1) ahead1 = ld_streaming(row + at1);
+        slot_ahead = __ldg(p.slots + t);
+        if (p.rot > 0) pos_ahead = __ldg(p.positions + t);
+    };
+    read_ahead(tok, h);
+
     // every lane of a warp takes the same number of turns (shuffles below)
-    for (int h0 = chunk * kGroups; h0 < heads; h0 += p.head_chunks * kGroups) {
-        const int h = h0 + threadIdx.x / kLanes;
-        const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv, is_v = !is_q && !is_k;
-        const int hh = is_q ? h : is_k ? h - p.hq : h - p.hq - p.hkv;
-        const bool here = live && h < heads;
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (here) {
-            const __nv_bfloat16* src = is_q ? p.q + tok * p.q_stride : is_k ? p.k + tok * p.k_stride : p.v + tok * p.v_stride;
-            u = __ldg(reinterpret_cast<const uint4*>(src + static_cast<long long>(hh) * p.dim + lane * 8));
+    while (__any_sync(0xFFFFFFFFu, tok < p.num_tokens)) {
+        const bool mine = tok < p.num_tokens;
+        uint4 u[2] = {ahead0, ahead1};
+        const long long slot = slot_ahead;
+        int pos = pos_ahead;
+        int tok2 = tok + p.step_tok, h2 = h + p.step_head;
+        if (h2 >= heads) {
+            h2 -= heads;
+            ++tok2;
         }
-        float x[8];
-        unpack8(u, x);
-        float sq = 0.f;
+        read_ahead(tok2, h2);
+        const bool store_kv = mine && slot >= 0 && slot < p.slot_limit;
+        uint32_t bad = mine && slot >= p.slot_limit ? PKV_DEVERR_SLOT : 0u;
+        float c[8], s[8];
+        if (p.rot > 0) {
+            if (pos < 0 || pos >= p.max_positions) {
+                if (mine && slot >= 0) bad |= PKV_DEVERR_POSITION;
+                pos = min(max(pos, 0), p.max_positions - 1);
+            }
+            if (turned && mine && h < p.hq + p.hkv) {
+                const float* row = p.cos_sin + static_cast<long long>(pos) * p.rot + lane * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sq += x[i] * x[i];
-#pragma unroll
-        for (int d = kLanes / 2; d; d >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, d, kLanes);
-        const __nv_bfloat16* weight = is_q ? p.q_weight : p.k_weight;
-        if (!is_v && weight && live) {
-            const float r = rsqrtf(sq / static_cast<float>(p.dim) + p.eps);
-            float w[8];
-            unpack8(__ldg(reinterpret_cast<const uint4*>(weight + lane * 8)), w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-        }
-        if (kInterleaved) {
-            if (turned) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = x[2 * i], b = x[2 * i + 1];
-                    x[2 * i] = a * c[i] - b * s[i];
-                    x[2 * i + 1] = a * s[i] + b * c[i];
+                for (int i = 0; i < 8; i += 4) {
+                    const float4 cv = __ldg(reinterpret_cast<const float4*>(row + i));
+                    const float4 sv = __ldg(reinterpret_cast<const float4*>(row + (p.rot >> 1) + i));
+                    c[i] = cv.x; c[i + 1] = cv.y; c[i + 2] = cv.z; c[i + 3] = cv.w;
+                    s[i] = sv.x; s[i + 1] = sv.y; s[i + 2] = sv.z; s[i + 3] = sv.w;
                 }
             }
-        } else {
-            const int partner = turned ? (upper ? lane - half_lanes : lane + half_lanes) : lane;
+        }
+        if (bad && p.err && lane == 0 && h == 0) atomicOr(p.err, bad);
+        const long long blk = store_kv ? slot >> p.bt_shift : 0;
+        const int in_blk = static_cast<int>(slot) & ((1 << p.bt_shift) - 1);
+
+        const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv, is_v = !is_q && !is_k;
+        float x[2][8];
+        unpack8(u[0], x[0]);
+        unpack8(u[1], x[1]);
+        const __nv_bfloat16* weight = is_q ? p.q_weight : is_k ? p.k_weight : nullptr;
+        if (p.q_weight || p.k_weight) {
+            float sq = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = __shfl_sync(0xFFFFFFFFu, x[i], partner, kLanes);
-                if (turned) x[i] = upper ? y * s[i] + x[i] * c[i] : x[i] * c[i] - y * s[i];
+            for (int e = 0; e < 16; ++e) sq += x[e >> 3][e & 7] * x[e >> 3][e & 7];
+#pragma unroll
+            for (int d = kLanes / 2; d; d >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, d, kLanes);
+            if (weight) {
+                const float r = rsqrtf(sq / static_cast<float>(p.dim) + p.eps);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (!(half ? live1 : live0)) continue;
+                    float w[8];
+                    unpack8(__ldg(reinterpret_cast<const uint4*>(weight + (half ? at1 : at0))), w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[half][e] = x[half][e] * r * w[e];
+                }
             }
         }
-        if (!here) continue;
-        if (!is_v) u = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-        if (is_q) {
-            *reinterpret_cast<uint4*>(p.q_out + (static_cast<long long>(tok) * p.hq + hh) * p.dim + lane * 8) = u;
-        } else if (store_kv) {
-            __nv_bfloat16* cache = is_k ? p.k_cache : p.v_cache;
-            *reinterpret_cast<uint4*>(cache + ((blk * p.hkv + hh) * p.bt + in_blk) * p.dim + lane * 8) = u;
+        if (!is_v) {
+            if (turned) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float& a = kInterleaved ? x[e >> 2][2 * (e & 3)] : x[0][e];
+                    float& b = kInterleaved ? x[e >> 2][2 * (e & 3) + 1] : x[1][e];
+                    const float a0 = a, b0 = b;
+                    a = a0 * c[e] - b0 * s[e];
+                    b = a0 * s[e] + b0 * c[e];
+                }
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                u[half] = make_uint4(pack_bf16x2(x[half][0], x[half][1]), pack_bf16x2(x[half][2], x[half][3]),
+                                     pack_bf16x2(x[half][4], x[half][5]), pack_bf16x2(x[half][6], x[half][7]));
         }
+        __nv_bfloat16* dst = nullptr;
+        if (is_q) {
+            if (mine) dst = p.q_out + (static_cast<long long>(tok) * p.hq + h) * p.dim;
+        } else if (store_kv) {
+            const int hh = is_k ? h - p.hq : h - p.hq - p.hkv;
+            dst = (is_k ? p.k_cache : p.v_cache) + (((blk * p.hkv + hh) << p.bt_shift) + in_blk) * p.dim;
+        }
+        if (dst && live0) *reinterpret_cast<uint4*>(dst + at0) = u[0];
+        if (dst && live1) *reinterpret_cast<uint4*>(dst + at1) = u[1];
+        tok = tok2;
+        h = h2;
     }
 }
 
@@ -144,9 +189,26 @@ KernelFn kernel_for(int lanes, bool interleaved) {
     switch (lanes) {
         case 4: return interleaved ? qk_write_kernel<4, true> : qk_write_kernel<4, false>;
         case 8: return interleaved ? qk_write_kernel<8, true> : qk_write_kernel<8, false>;
-        case 16: return interleaved ? qk_write_kernel<16, true> : qk_write_kernel<16, false>;
-        default: return interleaved ? qk_write_kernel<32, true> : qk_write_kernel<32, false>;
+        default: return interleaved ? qk_write_kernel<16, true> : qk_write_kernel<16, false>;
     }
+}
+
+// Blocks that run at once on the current device (three on an SM at the
+// kernel's 80 registers), read once per device.
+int resident_blocks() {
+    static std::mutex mu;
+    static std::vector<int> cache;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (static_cast<int>(cache.size()) <= dev) cache.resize(dev + 1);
+    if (cache[dev] > 0) return cache[dev];
+    const cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        return 0;
+    }
+    return cache[dev] = sms * kBlocksPerSm;
 }
 
 }  // namespace qkw
@@ -169,7 +231,7 @@ pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
         return PKV_EINVAL;
     if (head_dim % 8 != 0 || head_dim > PKV_ROPE_MAX_HEAD_DIM || rotary_dim % 16 != 0 || rotary_dim > head_dim)
         return PKV_EUNSUPPORTED;
-    if (num_q_heads > (1 << 16) || num_kv_heads > (1 << 16)) return PKV_ERANGE;
+    if (num_q_heads > (1 << 16) || num_kv_heads > (1 << 16) || num_tokens > (1 << 30)) return PKV_ERANGE;
     if (num_tokens == 0) return PKV_OK;
     if (!q || !k || !v || !slot_mapping || !q_out || !k_cache || !v_cache ||
         (rotary_dim > 0 && (!cos_sin || !positions || max_positions < 1)))
@@ -181,8 +243,9 @@ pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
                             static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
         if (!aligned16(ptr)) return PKV_EINVAL;
     int lanes = 4;
-    while (lanes * 8 < head_dim) lanes *= 2;
+    while (lanes * 16 < head_dim) lanes *= 2;
     qkw::Params p = {};
+    p.bt_shift = 3;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.k = static_cast<const __nv_bfloat16*>(k);
     p.v = static_cast<const __nv_bfloat16*>(v);
@@ -206,9 +269,16 @@ pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
     p.hq = num_q_heads;
     p.hkv = num_kv_heads;
     p.dim = head_dim;
-    p.bt = block_tokens;
-    p.head_chunks = 1;
-    qkw::kernel_for(lanes, interleaved != 0)<<<num_tokens, qkw::kThreads, 0, as_stream(stream)>>>(p);
+    while ((8 << (p.bt_shift - 3)) < block_tokens) ++p.bt_shift;
+    const int heads = num_q_heads + 2 * num_kv_heads, groups = qkw::kThreads / lanes;
+    const long long blocks = (static_cast<long long>(num_tokens) * heads + groups - 1) / groups;
+    const int resident = qkw::resident_blocks();
+    if (resident < 1) return PKV_ECUDA;
+    const int grid = static_cast<int>(std::min<long long>(blocks, resident));
+    const long long step = static_cast<long long>(grid) * groups;
+    p.step_tok = static_cast<int>(step / heads);
+    p.step_head = static_cast<int>(step % heads);
+    qkw::kernel_for(lanes, interleaved != 0)<<<grid, qkw::kThreads, 0, as_stream(stream)>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) {
         record_cuda_error(e);
