@@ -147,6 +147,7 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
     p.hkv = num_kv_heads;
     p.group = num_q_heads / num_kv_heads;
     p.tpt = kRows / p.group;
+    p.item_magic = ((1ull << 36) + 2 * p.tpt - 1) / (2 * p.tpt);
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = num_blocks;
     p.bt = block_tokens;

@@ -79,6 +79,7 @@ struct Params {
     int num_seqs, num_tokens, hq, hkv, group, tpt;  // tpt: tokens of a tile
     int max_blocks, num_blocks, bt;
     float scale_log2;
+    unsigned long long item_magic;  // ceil(2^36 / (2 tpt))
 };
 
 // An item cut among CTAs, described by the CTA that has its first piece.
@@ -91,6 +92,7 @@ struct Split {
 
 struct Seq {
     int n, ctx, tok0;  // query rows, tokens in the cache, first row
+    int full, rest;    // items of two full tiles, rows of the last, smaller one
 };
 
 // A CTA's piece of an item, as the loader describes it to the other warps.
@@ -157,6 +159,11 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int s, uint32_t* bad) {
     }
     q.ctx = max(ctx, 0);
     if (bad && !kTree && q.n > q.ctx) *bad |= PKV_DEVERR_CONTEXT;
+    // n / (2 tpt) by the host's ceil(2^36 / (2 tpt)): exact below 2^28, then corrected
+    const int item_rows = 2 * p.tpt;
+    q.full = static_cast<int>((static_cast<unsigned long long>(q.n) * p.item_magic) >> 36);
+    if (q.full * item_rows > q.n) --q.full;
+    q.rest = q.n - q.full * item_rows;
     return q;
 }
 
@@ -170,15 +177,14 @@ __device__ __forceinline__ long long full_cost(const Seq& q, int tpt, long long 
 }
 
 template <bool kTree>
-__device__ __forceinline__ long long last_cost(const Seq& q, int rest, int tpt) {
+__device__ __forceinline__ long long last_cost(const Seq& q, int tpt) {
     const long long keys = kTree ? q.ctx + static_cast<long long>(kKeys) : q.ctx;
-    return (rest > tpt ? kCostTwo : kCostOne) * keys + kItemCost;
+    return (q.rest > tpt ? kCostTwo : kCostOne) * keys + kItemCost;
 }
 
 template <bool kTree>
 __device__ __forceinline__ long long head_cost(const Seq& q, int tpt) {
-    const int full = q.n / (2 * tpt), rest = q.n - full * 2 * tpt;
-    return full_cost<kTree>(q, tpt, full) + (rest ? last_cost<kTree>(q, rest, tpt) : 0);
+    return full_cost<kTree>(q, tpt, q.full) + (q.rest ? last_cost<kTree>(q, tpt) : 0);
 }
 
 // Tiles of an item that belong to ranges before a cut `off` cost units into
@@ -219,9 +225,8 @@ __device__ __forceinline__ void set_item(const Params& p, Item& it) {
 
 template <bool kTree>
 __device__ __forceinline__ long long item_cost(const Params& p, const Item& it) {
-    const int full = it.q.n / (2 * p.tpt);
-    return it.i < full ? full_cost<kTree>(it.q, p.tpt, it.i + 1) - full_cost<kTree>(it.q, p.tpt, it.i)
-                       : last_cost<kTree>(it.q, it.q.n - full * 2 * p.tpt, p.tpt);
+    return it.i < it.q.full ? full_cost<kTree>(it.q, p.tpt, it.i + 1) - full_cost<kTree>(it.q, p.tpt, it.i)
+                            : last_cost<kTree>(it.q, p.tpt);
 }
 
 // The loader's walk over its CTA's range: next() yields the pieces in order.
@@ -313,15 +318,17 @@ __device__ __forceinline__ int ring_k(bool two, int j) { return two ? 2 * j : ma
 __device__ __forceinline__ int ring_v(bool two, int j, int count) { return two || j == count - 1 ? 2 * j + 1 : 2 * j + 2; }
 
 // Every thread of the CTA: the ends of this CTA's range, and the description
-// of the item that its end cuts.
+// of the item that its end cuts. Each half of the threads goes over all
+// sequences and finds one end.
 template <bool kTree>
 __device__ void plan(const Params& p, Misc& m) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    constexpr int kHalf = kThreads / 2, kHalfWarps = kHalf / 32;
+    const int e = threadIdx.x >= kHalf, tid = threadIdx.x - e * kHalf, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.num_seqs + kHalf - 1) / kHalf;
     const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
     long long sum = 0;
     uint32_t bad = 0;
-    Seq seq0 = {0, 0, 0};
+    Seq seq0 = {};
     for (int s = s0; s < s1; ++s) {
         const Seq q = load_seq<kTree>(p, s, &bad);
         if (s == s0) seq0 = q;
@@ -334,68 +341,66 @@ __device__ void plan(const Params& p, Misc& m) {
         const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
         if (lane >= d) incl += o;
     }
-    if (lane == 31) m.scan[warp] = incl;
-    if (tid < 8) m.cut[tid >> 2][tid & 3] = (tid & 3) == 0 ? p.num_seqs : 0;
-    if (tid == 0) p.splits[blockIdx.x].ntiles = 0;
+    if (lane == 31) m.scan[e * kHalfWarps + warp] = incl;
+    if (tid < 4) m.cut[e][tid] = tid == 0 ? p.num_seqs : 0;
+    if (threadIdx.x == 0) p.splits[blockIdx.x].ntiles = 0;
     __syncthreads();
     long long before = incl - sum, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const long long v = m.scan[w];
+    for (int w = 0; w < kHalfWarps; ++w) {
+        const long long v = m.scan[e * kHalfWarps + w];
         if (w < warp) before += v;
         total += v;
     }
     const int ranges = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total / kMinRange, 1ll)));
-    const long long chunk = (total + ranges - 1) / ranges;
+    // a range's length, no less than its share (by some 2^-20 more)
+    const long long chunk = static_cast<long long>(__ll2float_ru(total) / ranges * 1.000001f) + 1;
     const int b = blockIdx.x;
-    for (int e = 0; e < 2; ++e) {
-        const long long x = chunk * (b + e);
-        if (x < before || x >= before + sum) continue;  // at or past the line's end: behind the last sequence
-        long long at = before;
-        for (int s = s0; s < s1; ++s) {
-            Item it;
-            it.q = s == s0 ? seq0 : load_seq<kTree>(p, s, nullptr);
-            const long long hc = head_cost<kTree>(it.q, p.tpt);
-            if (x >= at + hc * p.hkv) {
-                at += hc * p.hkv;
-                continue;
-            }
-            it.s = s;
-            // estimates, then the exact head and item
-            it.h = min(static_cast<int>(__ll2float_rn(x - at) / __ll2float_rn(hc)), p.hkv - 1);
-            while (it.h > 0 && hc * it.h > x - at) --it.h;
-            while (it.h + 1 < p.hkv && hc * (it.h + 1) <= x - at) ++it.h;
-            const long long base = at + hc * it.h, off = x - base;
-            const int items = (it.q.n + 2 * p.tpt - 1) / (2 * p.tpt);
-            const float one = __ll2float_rn(full_cost<kTree>(it.q, p.tpt, 1)), bend = kTree ? 0.f : static_cast<float>(kCostTwo) * p.tpt;
-            // cost of i items: bend * i^2 + (one - bend) * i
-            const float lin = one - bend, o = __ll2float_rn(off);
-            const float guess = 2.f * o / (lin + sqrtf(lin * lin + 4.f * bend * o));
-            it.i = min(static_cast<int>(guess), items - 1);
-            while (it.i > 0 && full_cost<kTree>(it.q, p.tpt, it.i) > off) --it.i;
-            while (it.i + 1 < items && full_cost<kTree>(it.q, p.tpt, it.i + 1) <= off) ++it.i;
-            set_item<kTree>(p, it);
-            const long long start = base + full_cost<kTree>(it.q, p.tpt, it.i), cost = item_cost<kTree>(p, it);
-            const int t = cut_tile(x - start, cost, it.cut_tiles());
-            m.cut[e][0] = s;
-            m.cut[e][1] = it.h;
-            m.cut[e][2] = it.i;
-            m.cut[e][3] = t;
-            if (e == 0) m.cut_seq = it.q;
-            // this CTA has the item's first piece and not its last
-            if (e == 1 && t > 0 && t < it.cut_tiles() &&
-                (x - chunk <= start || cut_tile(x - chunk - start, cost, it.cut_tiles()) == 0)) {
-                Split sp;
-                sp.start = start;
-                sp.cost = cost;
-                sp.chunk = chunk;
-                sp.ntiles = it.cut_tiles();
-                sp.tok0 = it.tok0;
-                sp.ntok = it.ntok;
-                sp.head0 = it.h * p.group;
-                p.splits[b] = sp;
-            }
-            break;
+    const long long x = chunk * (b + e);
+    if (x < before || x >= before + sum) return;  // at or past the line's end: behind the last sequence
+    long long at = before;
+    for (int s = s0; s < s1; ++s) {
+        Item it;
+        it.q = s == s0 ? seq0 : load_seq<kTree>(p, s, nullptr);
+        const long long hc = head_cost<kTree>(it.q, p.tpt);
+        if (x >= at + hc * p.hkv) {
+            at += hc * p.hkv;
+            continue;
         }
+        it.s = s;
+        // estimates, then the exact head and item
+        it.h = min(static_cast<int>(__ll2float_rn(x - at) / __ll2float_rn(hc)), p.hkv - 1);
+        while (it.h > 0 && hc * it.h > x - at) --it.h;
+        while (it.h + 1 < p.hkv && hc * (it.h + 1) <= x - at) ++it.h;
+        const long long base = at + hc * it.h, off = x - base;
+        const int items = it.q.full + (it.q.rest > 0);
+        // cost of i items: bend * i^2 + lin * i
+        const float bend = kTree ? 0.f : static_cast<float>(kCostTwo) * p.tpt;
+        const float lin = __ll2float_rn(full_cost<kTree>(it.q, p.tpt, 1)) - bend, o = __ll2float_rn(off);
+        it.i = min(static_cast<int>(2.f * o / (lin + sqrtf(lin * lin + 4.f * bend * o))), items - 1);
+        while (it.i > 0 && full_cost<kTree>(it.q, p.tpt, it.i) > off) --it.i;
+        while (it.i + 1 < items && full_cost<kTree>(it.q, p.tpt, it.i + 1) <= off) ++it.i;
+        set_item<kTree>(p, it);
+        const long long start = base + full_cost<kTree>(it.q, p.tpt, it.i), cost = item_cost<kTree>(p, it);
+        const int t = cut_tile(x - start, cost, it.cut_tiles());
+        m.cut[e][0] = s;
+        m.cut[e][1] = it.h;
+        m.cut[e][2] = it.i;
+        m.cut[e][3] = t;
+        if (e == 0) m.cut_seq = it.q;
+        // this CTA has the item's first piece and not its last
+        if (e == 1 && t > 0 && t < it.cut_tiles() &&
+            (x - chunk <= start || cut_tile(x - chunk - start, cost, it.cut_tiles()) == 0)) {
+            Split sp;
+            sp.start = start;
+            sp.cost = cost;
+            sp.chunk = chunk;
+            sp.ntiles = it.cut_tiles();
+            sp.tok0 = it.tok0;
+            sp.ntok = it.ntok;
+            sp.head0 = it.h * p.group;
+            p.splits[b] = sp;
+        }
+        return;
     }
 }
 
@@ -433,6 +438,7 @@ __device__ __forceinline__ void zero_half_row(uint8_t* half, int lane) {
 template <bool kTree>
 __device__ __forceinline__ void seen_words(const Piece& it, int tile, int vis, uint64_t draft_mask, uint32_t (&w)[4]) {
     if (kTree && tile == it.nct) {
+        if (it.seq_n < 64) draft_mask &= (1ull << it.seq_n) - 1ull;
         w[0] = static_cast<uint32_t>(draft_mask);
         w[1] = static_cast<uint32_t>(draft_mask >> 32);
         w[2] = w[3] = 0;
@@ -559,6 +565,15 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const int row_tok = row / p.group, row_head = row - row_tok * p.group;
         const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
         uint32_t n_s = 0, n_o = 0, n_join = 0, n_item = 0;
+        // one-tile items: a meeting of both warpgroups
+        auto meet = [&](int k) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&m.join[k]));
+            const bool met = mbar_wait(smem_u32(&m.join[k]), n_join & 1, abort_flag, p.err);
+            tc_fence_after();
+            return __all_sync(0xFFFFFFFFu, met) != 0;
+        };
         for (;; ++n_item) {
             const Piece* const piece = get_piece(n_item);
             if (!piece) break;
@@ -571,7 +586,6 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             uint64_t draft_mask = 0;
             if (kTree && valid) {
                 draft_mask = static_cast<uint64_t>(__ldg(reinterpret_cast<const long long*>(p.masks) + tok));
-                if (it.seq_n < 64) draft_mask &= (1ull << it.seq_n) - 1ull;
             }
             const int count = it.cnt[stream];
             const int first_masked = it.first_masked, tile0 = it.two ? it.ta : it.ta + stream, tile_step = it.two ? 1 : 2;
@@ -679,108 +693,95 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const uint32_t(*bad)[4] = m.bad[n_item % kPieces];
             const long long slot = 2ll * blockIdx.x + (it.ta == 0 ? 1 : 0);
 
-            // The results leave through shared memory, 128 bytes of each of the
-            // warp's 32 rows at a time (64 columns of the output, 32 of a partial
-            // result), so that a store covers whole lines: straight from the
-            // accumulator's rows each store would touch 32 of them, which took
-            // 1.5-3.5 us an item.
-            uint8_t* const staging = smem + kSmemOut + warp * kOutBytes;
-            auto chunk = [&](int r, int c) { return reinterpret_cast<uint4*>(staging + r * 128 + ((c ^ (r & 7)) << 4)); };
-            const int out_row = valid ? tok * p.hq + it.h * p.group + row_head : -1;  // below 2^31: 256 bytes each
-            const long long part_row0 = slot * 2 * kRows + (it.two ? stream * kRows : 0) + (warp & 3) * 32;
-            auto put = [&](uint32_t (&o)[32], int col, float inv) {
-                if (whole) {
-                    auto two = [&](int c) { return pack_bf16x2(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv); };
-                    const int c0 = (col >> 3) & 4;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        *chunk(lane, c0 + c) = make_uint4(two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
-                    if (c0 == 0) return;  // the other half of the 64 columns follows
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) *chunk(lane, c) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int r = 4 * k + (lane >> 3);
-                    const int orow = __shfl_sync(0xFFFFFFFFu, out_row, r);
-                    if (orow < 0) continue;
-                    const uint4 v = *chunk(r, lane & 7);
-                    if (whole) *reinterpret_cast<uint4*>(p.out + static_cast<long long>(orow) * kDim + (col & ~63) + (lane & 7) * 8) = v;
-                    else *reinterpret_cast<uint4*>(p.part_o + (part_row0 + r) * kDim + col + (lane & 7) * 4) = v;
-                }
-                __syncwarp();
-            };
             // what the sum is divided by; no key seen: zeros; only keys of weight zero: NaN, as 0 / 0
-            auto inverse = [](const float2& s) {
-                return s.y == 0.f ? (s.x == -INFINITY ? 0.f : __int_as_float(0x7FC00000)) : 1.f / s.y;
+            auto inverse = [](const float2& v) {
+                return v.y == 0.f ? (v.x == -INFINITY ? 0.f : __int_as_float(0x7FC00000)) : 1.f / v.y;
             };
-
-            int col_lo = 0, col_hi = kDim, t_end = t_hi;  // this thread's columns; its stream's tiles
-            long long prow = row;
+            // The row's result is acc0 * f0 + acc1 * f1: of two tiles this stream's
+            // accumulator; of one tile both streams' accumulators joined, half of the
+            // columns in each warpgroup.
+            int col_lo = 0, col_hi = kDim, t_end = t_hi, prow = row;  // t_end: end of the tiles that it holds
+            uint32_t acc0 = t_o, acc1 = t_o;
+            float f0 = 1.f, f1 = 0.f;
+            bool has0 = count > 0, has1 = false;
             if (it.two) {
                 t_end = min(t_hi, it.ta + count);
                 prow += stream * kRows;
-                if (warp_valid) {
-                    const float inv = inverse(st);
-#pragma unroll 1
-                    for (int col = 0; col < kDim; col += 32) {
-                        uint32_t r[32];
-                        if (count > 0) {
-                            tmem_ld32(r, t_o + col);
-                            tmem_wait_ld(r);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) r[c] = 0;
-                        }
-                        put(r, col, inv);
-                    }
-                    if (valid && !whole) p.part_ml[slot * 2 * kRows + prow] = st;
-                }
             } else {
-                // join the streams: each warpgroup takes half of the columns of both accumulators
                 col_lo = stream * 64;
                 col_hi = col_lo + 64;
                 m.ml[stream][row] = st;
-                auto meet = [&](int k) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&m.join[k]));
-                    const bool met = mbar_wait(smem_u32(&m.join[k]), n_join & 1, abort_flag, p.err);
-                    tc_fence_after();
-                    return __all_sync(0xFFFFFFFFu, met) != 0;
-                };
                 if (!meet(0)) break;
-                if (warp_valid) {
-                    const float2 s0 = m.ml[0][row], s1 = m.ml[1][row];
-                    const bool one = it.cnt[1] == 0, none = it.cnt[0] == 0;
-                    float2 js;
-                    js.x = fmaxf(s0.x, s1.x);
-                    const float a0 = s0.x == js.x ? 1.f : ex2(s0.x - js.x), a1 = s1.x == js.x ? 1.f : ex2(s1.x - js.x);
-                    js.y = s0.y * a0 + s1.y * a1;
-                    const float inv = inverse(js);
-#pragma unroll 1
-                    for (int col = col_lo; col < col_hi; col += 32) {
-                        uint32_t r[32], r1[32];
-                        if (none) {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) r[c] = 0;
-                        } else {
-                            tmem_ld32(r, tmem + lanes + kTmemO + col);
-                            if (!one) tmem_ld32(r1, tmem + lanes + kTmemO + 128 + col);
-                            tmem_wait_ld(r);
-                            if (!one) {
-                                hold(r1);
-#pragma unroll
-                                for (int c = 0; c < 32; ++c)
-                                    r[c] = __float_as_uint(__uint_as_float(r[c]) * a0 + __uint_as_float(r1[c]) * a1);
-                            }
-                        }
-                        put(r, col, inv);
-                    }
-                    if (valid && !whole && stream == 0) p.part_ml[slot * 2 * kRows + prow] = js;
+                const float2 s0 = m.ml[0][row], s1 = m.ml[1][row];
+                st.x = fmaxf(s0.x, s1.x);
+                f0 = s0.x == st.x ? 1.f : ex2(s0.x - st.x);
+                f1 = s1.x == st.x ? 1.f : ex2(s1.x - st.x);
+                st.y = s0.y * f0 + s1.y * f1;
+                acc0 = tmem + lanes + kTmemO;
+                acc1 = acc0 + 128;
+                has0 = it.cnt[0] > 0;
+                has1 = it.cnt[1] > 0;
+            }
+            const int out_row = valid ? tok * p.hq + it.h * p.group + row_head : -1;  // below 2^31: 256 bytes each
+            const long long part_row0 = slot * 2 * kRows + (prow - lane);
+            if (warp_valid) {
+                if (whole) {
+                    const float inv = inverse(st);
+                    f0 *= inv;
+                    f1 *= inv;
+                } else if (valid && (it.two || stream == 0)) {
+                    p.part_ml[part_row0 + lane] = st;
                 }
+                // The results leave through shared memory, 32 columns of the warp's 32
+                // rows at a time, so that a store covers 64 or 128 bytes of a row where
+                // one from the accumulator's rows would touch 32 lines.
+                uint8_t* const staging = smem + kSmemOut + warp * kOutBytes;
+                auto chunk = [&](int r, int c) { return reinterpret_cast<uint4*>(staging + r * 128 + ((c ^ (r & 7)) << 4)); };
+#pragma unroll 1
+                for (int col = col_lo; col < col_hi; col += 32) {
+                    uint32_t r[32], r1[32];
+                    tmem_ld32(r, acc0 + col);
+                    tmem_ld32(r1, acc1 + col);
+                    tmem_wait_ld(r);
+                    hold(r1);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        float v = has0 ? __uint_as_float(r[c]) * f0 : 0.f;
+                        if (has1) v += __uint_as_float(r1[c]) * f1;
+                        r[c] = __float_as_uint(v);
+                    }
+                    if (whole) {
+                        auto two = [&](int c) { return pack_bf16x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])); };
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) *chunk(lane, c) = make_uint4(two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
+                        __syncwarp();
+                        uint4 v[4];
+                        int orow[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            v[k] = *chunk(8 * k + (lane >> 2), lane & 3);
+                            orow[k] = __shfl_sync(0xFFFFFFFFu, out_row, 8 * k + (lane >> 2));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (orow[k] >= 0)
+                                *reinterpret_cast<uint4*>(p.out + static_cast<long long>(orow[k]) * kDim + col + (lane & 3) * 8) = v[k];
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) *chunk(lane, c) = make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
+                        __syncwarp();
+                        uint4 v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = *chunk(4 * k + (lane >> 3), lane & 7);
+                        // rows that are none are written too: they are the workspace's
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<uint4*>(p.part_o + (part_row0 + 4 * k + (lane >> 3)) * kDim + col + (lane & 7) * 4) = v[k];
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!it.two) {
                 // both accumulators are read before either is written again
                 if (!meet(1)) break;
                 ++n_join;
@@ -795,7 +796,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                                               p.out + static_cast<long long>(out_row) * kDim);
                     else
                         add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi,
-                                              p.part_o + (slot * 2 * kRows + prow) * kDim);
+                                              p.part_o + (part_row0 + lane) * kDim);
                 }
             }
             done_piece(n_item);
@@ -808,35 +809,36 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         Walk<kTree> walk(p, m);
         const int blocks_per_tile = kKeys / p.bt;
         bool ok = true;
-        for (bool more = true; more; ++n_item) {
-            more = walk.next();
+        // One piece is described ahead of the one that is loaded, and its query rows
+        // are brought into L2 meanwhile.
+        auto describe = [&](bool more) {
             ok = mbar_wait(smem_u32(&m.piece_empty[n_item % kPieces]), ((n_item / kPieces) & 1) ^ 1, abort_flag, p.err);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) return;
             if (lane == 0) {
                 if (more) walk.describe(m.piece[n_item % kPieces]);
                 else m.piece[n_item % kPieces].count = -1;
                 mbar_arrive(smem_u32(&m.piece_full[n_item % kPieces]));
             }
-            if (!more) break;
-            const Item& it = walk.it;
-            const int count = min(walk.tb, it.nt) - walk.ta;
-            if (count <= 0) continue;
-            ok = mbar_wait(smem_u32(&m.q_empty), (n_q & 1) ^ 1, abort_flag, p.err);
-            ++n_q;
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            const int tiles = it.two ? 2 : 1;
-            const int masked0 = max(it.first_masked, walk.ta) - walk.ta;  // first masked tile of the piece
-            if (lane == 0) mbar_arrive_expect_tx(smem_u32(&m.q_full), tiles * 2 * 128 * p.group * p.tpt);
             __syncwarp();
-            if (lane < 2 * tiles) {
-                const int t = lane >> 1, panel = lane & 1;
-                tma_load_5d(smem_base + kSmemQ + t * kTileBytes + panel * (kTileBytes / 2), &tm_q, 0, 0,
-                            it.tok0 + t * p.tpt, panel, it.h, smem_u32(&m.q_full));
-            }
+            ++n_item;
+        };
+        bool more = walk.next();
+        describe(more);
+        while (ok && more) {
+            const Piece& it = m.piece[(n_item - 1) % kPieces];  // only this warp replaces it, kPieces later
+            more = walk.next();
+            describe(more);
+            if (!ok) break;
+            const int ta = it.ta, count = it.count;
+            if (more && lane < 4 && (walk.it.two || lane < 2))
+                tma_prefetch_5d(&tm_q, 0, 0, walk.it.tok0 + (lane >> 1) * p.tpt, lane & 1, walk.it.h);
+            if (count == 0) continue;
+            const int masked0 = max(it.first_masked, ta) - ta;  // first masked tile of the piece
             // this lane's box of a tile: its last coordinate in the map
             auto coordinate = [&](int j) {
-                const int t = walk.ta + j;
-                if (kTree && t == it.nct) return it.q.tok0 + lane * 8;
+                const int t = ta + j;
+                if (kTree && t == it.nct) return it.seq_tok0 + lane * 8;
                 const int idx = t * blocks_per_tile + lane;
                 if (lane >= blocks_per_tile || idx * p.bt >= it.kend) return 0;
                 int blk = __ldg(p.block_tables + static_cast<long long>(it.s) * p.max_blocks + idx);
@@ -852,7 +854,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 ok = mbar_wait(smem_u32(&m.kv_empty[st]), ph ^ 1, abort_flag, p.err);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) return;
-                const int t = walk.ta + j;
+                const int t = ta + j;
                 uint32_t full = smem_u32(&m.kv_full[st]);
                 if (is_v && j >= masked0) {
                     // a value tile to be cleaned lands on a barrier of its own: the
@@ -863,7 +865,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 }
                 const uint32_t dst = smem_base + kSmemRing + st * kTileBytes;
                 const bool draft = kTree && t == it.nct;
-                const int boxes = draft ? (it.q.n + 7) >> 3 : (min(kKeys, it.kend - t * kKeys) + p.bt - 1) / p.bt;
+                const int boxes = draft ? (it.seq_n + 7) >> 3 : (min(kKeys, it.kend - t * kKeys) + p.bt - 1) / p.bt;
                 const uint32_t box_bytes = draft ? 2048 : p.bt * 256;
                 if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_bytes);
                 __syncwarp();
@@ -874,6 +876,19 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             };
             int cur = coordinate(0);
             load(false, 0, 0, cur);
+            if (!ok) break;
+            ok = mbar_wait(smem_u32(&m.q_empty), (n_q & 1) ^ 1, abort_flag, p.err);
+            ++n_q;
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            const int tiles = it.two ? 2 : 1;
+            if (lane == 0) mbar_arrive_expect_tx(smem_u32(&m.q_full), tiles * 2 * 128 * p.group * p.tpt);
+            __syncwarp();
+            if (lane < 2 * tiles) {
+                const int t = lane >> 1, panel = lane & 1;
+                tma_load_5d(smem_base + kSmemQ + t * kTileBytes + panel * (kTileBytes / 2), &tm_q, 0, 0,
+                            it.tok0 + t * p.tpt, panel, it.h, smem_u32(&m.q_full));
+            }
             for (int j = 0; ok && j < count; ++j) {
                 int next = 0;
                 if (j + 1 < count) next = coordinate(j + 1);
@@ -884,7 +899,6 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
             ring += 2 * count;
             n_clean += max(count - masked0, 0);
-            if (!ok) break;
         }
     } else if (warp == kWarpMma) {
         // ---- tensor core: one elected thread issues every product. The warp

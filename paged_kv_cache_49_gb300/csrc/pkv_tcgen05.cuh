@@ -135,6 +135,13 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int 
         : "memory");
 }
 
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_5d(const void* tmap, int x, int y, int z, int w, int v) {
+    asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(tmap), "r"(x),
+                 "r"(y), "r"(z), "r"(w), "r"(v)
+                 : "memory");
+}
+
 // ---- pairs of floats -------------------------------------------------------------
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
     uint64_t r;
@@ -158,13 +165,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
-}
-
-// 32 bytes to a 32-byte aligned address.
-__device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&r)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
 }
 
 }  // namespace pkv
