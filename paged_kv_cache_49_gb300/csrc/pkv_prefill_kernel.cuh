@@ -54,9 +54,12 @@ constexpr uint32_t kTileBytes = kKeys * kDim * 2;
 constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kTmemO = 256;  // S0, S1, O0, O1 of 128 columns each
 
-// Cost units of the work line: one key of an item's two tiles is 8, of a
-// single tile 5; an item's fixed work is kItemCost.
-constexpr int kCostTwo = 8, kCostOne = 5, kItemCost = 8 * 160;
+// Cost units of the work line: one key of an item's two tiles is 8 (3,400
+// cycles for a key tile). One tile alone costs 2,300 where the products bound
+// it, but as much as two where its keys' bytes do, as over the long contexts
+// of trees. kItemCost: an item's fixed work.
+constexpr int kCostTwo = 8, kItemCost = 8 * 200;
+__host__ __device__ constexpr int cost_one(bool tree) { return tree ? 8 : 6; }
 constexpr int kSnap = 8 * 256;      // a cut this near an item's end moves there
 constexpr int kMinRange = 8 * 256;  // least cost of a CTA's range
 constexpr int kPieces = 4;          // pieces described ahead
@@ -108,6 +111,7 @@ struct __align__(16) Piece {
     int kend, nct;      // keys in the cache it needs; their tiles
     int s, h;           // sequence, KV head
     int seq_n, seq_tok0, ctx;  // query rows and first row of the sequence, its tokens in the cache
+    int any_bad;        // set by the cleaning warps: values were taken out
 };
 
 struct __align__(16) Misc {
@@ -179,7 +183,8 @@ __device__ __forceinline__ long long full_cost(const Seq& q, int tpt, long long 
 template <bool kTree>
 __device__ __forceinline__ long long last_cost(const Seq& q, int tpt) {
     const long long keys = kTree ? q.ctx + static_cast<long long>(kKeys) : q.ctx;
-    return (q.rest > tpt ? kCostTwo : kCostOne) * keys + kItemCost;
+    constexpr int kOne = cost_one(kTree);
+    return (q.rest > tpt ? kCostTwo : kOne) * keys + kItemCost;
 }
 
 template <bool kTree>
@@ -310,6 +315,7 @@ struct Walk {
         d.seq_n = it.q.n;
         d.seq_tok0 = it.q.tok0;
         d.ctx = it.q.ctx;
+        d.any_bad = 0;
     }
 };
 
@@ -612,10 +618,12 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                         seen_words<kTree>(it, tile, vis, draft_mask, w);
                         any |= (w[0] | w[1] | w[2] | w[3]) != 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                        for (int k = 0; k < 4; ++k) {
+                            if (__all_sync(0xFFFFFFFFu, w[k] == 0xFFFFFFFFu)) continue;
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
                                 if (!(w[k] >> c & 1)) s[k][c] = 0xFF800000u;
+                        }
                     } else {
                         any = true;
                     }
@@ -732,52 +740,87 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 } else if (valid && (it.two || stream == 0)) {
                     p.part_ml[part_row0 + lane] = st;
                 }
-                // The results leave through shared memory, 32 columns of the warp's 32
-                // rows at a time, so that a store covers 64 or 128 bytes of a row where
-                // one from the accumulator's rows would touch 32 lines.
+                // The results leave through shared memory, 64 bytes of each of the warp's
+                // 32 rows at a time (two places in turn), so that a store covers 8 rows'
+                // 64 bytes where one from the accumulator's rows would touch 32 lines.
                 uint8_t* const staging = smem + kSmemOut + warp * kOutBytes;
-                auto chunk = [&](int r, int c) { return reinterpret_cast<uint4*>(staging + r * 128 + ((c ^ (r & 7)) << 4)); };
-#pragma unroll 1
-                for (int col = col_lo; col < col_hi; col += 32) {
-                    uint32_t r[32], r1[32];
-                    tmem_ld32(r, acc0 + col);
-                    tmem_ld32(r1, acc1 + col);
-                    tmem_wait_ld(r);
-                    hold(r1);
+                auto chunk = [&](int place, int r, int c) {
+                    return reinterpret_cast<uint4*>(staging + place * (kOutBytes / 2) + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+                };
+                const int r0 = lane >> 2, c0 = lane & 3;  // the lane's rows r0 + 8 k and its 16 bytes of each
+                int orow[4];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        float v = has0 ? __uint_as_float(r[c]) * f0 : 0.f;
-                        if (has1) v += __uint_as_float(r1[c]) * f1;
-                        r[c] = __float_as_uint(v);
+                for (int k = 0; k < 4; ++k) orow[k] = __shfl_sync(0xFFFFFFFFu, out_row, r0 + 8 * k);
+                const uint64_t f0x2 = pair(f0, f0), f1x2 = pair(f1, f1);
+                auto columns = [&](int col) {
+                    uint32_t r[32];
+                    tmem_ld32(r, acc0 + col);
+                    if (has1) {
+                        uint32_t r1[32];
+                        tmem_ld32(r1, acc1 + col);
+                        tmem_wait_ld(r);
+                        hold(r1);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            float a, b;
+                            unpair(fma2(pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), f0x2,
+                                        mul2(pair(__uint_as_float(r1[c]), __uint_as_float(r1[c + 1])), f1x2)), a, b);
+                            r[c] = __float_as_uint(a);
+                            r[c + 1] = __float_as_uint(b);
+                        }
+                    } else if (has0) {
+                        tmem_wait_ld(r);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            float a, b;
+                            unpair(mul2(pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), f0x2), a, b);
+                            r[c] = __float_as_uint(a);
+                            r[c + 1] = __float_as_uint(b);
+                        }
+                    } else {
+                        tmem_wait_ld(r);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) r[c] = 0u;
                     }
                     if (whole) {
+                        const int place = (col >> 5) & 1;
                         auto two = [&](int c) { return pack_bf16x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])); };
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) *chunk(lane, c) = make_uint4(two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
+                        for (int c = 0; c < 4; ++c)
+                            *chunk(place, lane, c) = make_uint4(two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
                         __syncwarp();
                         uint4 v[4];
-                        int orow[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            v[k] = *chunk(8 * k + (lane >> 2), lane & 3);
-                            orow[k] = __shfl_sync(0xFFFFFFFFu, out_row, 8 * k + (lane >> 2));
-                        }
+                        for (int k = 0; k < 4; ++k) v[k] = *chunk(place, r0 + 8 * k, c0);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if (orow[k] >= 0)
-                                *reinterpret_cast<uint4*>(p.out + static_cast<long long>(orow[k]) * kDim + col + (lane & 3) * 8) = v[k];
+                                *reinterpret_cast<uint4*>(p.out + static_cast<long long>(orow[k]) * kDim + col + c0 * 8) = v[k];
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) *chunk(lane, c) = make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
+                        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                *chunk(q, lane, c) = make_uint4(r[16 * q + 4 * c], r[16 * q + 4 * c + 1], r[16 * q + 4 * c + 2], r[16 * q + 4 * c + 3]);
+                        }
                         __syncwarp();
-                        uint4 v[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = *chunk(4 * k + (lane >> 3), lane & 7);
-                        // rows that are none are written too: they are the workspace's
+                        for (int q = 0; q < 2; ++q) {
+                            uint4 v[4];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            *reinterpret_cast<uint4*>(p.part_o + (part_row0 + 4 * k + (lane >> 3)) * kDim + col + (lane & 7) * 4) = v[k];
+                            for (int k = 0; k < 4; ++k) v[k] = *chunk(q, r0 + 8 * k, c0);
+                            // rows that are none are written too: they are the workspace's
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                *reinterpret_cast<uint4*>(p.part_o + (part_row0 + r0 + 8 * k) * kDim + col + 16 * q + c0 * 4) = v[k];
+                        }
+                        __syncwarp();
                     }
+                };
+#pragma unroll 1
+                for (int col = col_lo; col < col_hi; col += 64) {
+                    columns(col);
+                    columns(col + 32);
                     __syncwarp();
                 }
             }
@@ -786,18 +829,13 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 if (!meet(1)) break;
                 ++n_join;
             }
-            if (valid && t_lo < t_end) {
-                uint32_t any_bad = 0;
-                for (int t = t_lo; t < t_end; ++t)
-                    any_bad |= bad[t - t_lo][0] | bad[t - t_lo][1] | bad[t - t_lo][2] | bad[t - t_lo][3];
-                if (any_bad) {
-                    if (whole)
-                        add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi,
-                                              p.out + static_cast<long long>(out_row) * kDim);
-                    else
-                        add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi,
-                                              p.part_o + (part_row0 + lane) * kDim);
-                }
+            if (*const_cast<const volatile int*>(&it.any_bad) && valid && t_lo < t_end) {
+                if (whole)
+                    add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi,
+                                          p.out + static_cast<long long>(out_row) * kDim);
+                else
+                    add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi,
+                                          p.part_o + (part_row0 + lane) * kDim);
             }
             done_piece(n_item);
         }
@@ -1013,7 +1051,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                         zero_half_row(halves + 1024, lane);
                     }
                     const uint32_t word = __ballot_sync(0xFFFFFFFFu, bad);
-                    if (lane == 0) m.bad[n_item % kPieces][j - masked0][half * 2 + r] = word;
+                    if (lane == 0) {
+                        m.bad[n_item % kPieces][j - masked0][half * 2 + r] = word;
+                        if (word) atomicOr(&m.piece[n_item % kPieces].any_bad, 1);
+                    }
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
