@@ -171,25 +171,25 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int s, uint32_t* bad) {
     return q;
 }
 
-// Cost of the first `items` items of one head of a sequence, all of two full tiles.
-template <bool kTree>
-__device__ __forceinline__ long long full_cost(const Seq& q, int tpt, long long items) {
-    if (kTree) return items * (kCostTwo * (q.ctx + static_cast<long long>(kKeys)) + kItemCost);
-    // keys of item i: ctx - n + (i + 1) * 2 tpt (below zero only for a chunk longer than its context)
-    const long long base = q.ctx - q.n;
-    return items * (kCostTwo * max(base, 0ll) + kItemCost) + static_cast<long long>(kCostTwo) * tpt * items * (items + 1);
-}
+// Costs of one head of a sequence: of the first i items, all of two full
+// tiles, i * (a + b i); of the smaller one behind them, last.
+struct Cost {
+    long long a, last;
+    int b;
+    __device__ __forceinline__ long long first(int i) const { return i * (a + static_cast<long long>(b) * i); }
+};
 
 template <bool kTree>
-__device__ __forceinline__ long long last_cost(const Seq& q, int tpt) {
-    const long long keys = kTree ? q.ctx + static_cast<long long>(kKeys) : q.ctx;
+__device__ __forceinline__ Cost cost_of(const Seq& q, int tpt) {
+    Cost c;
+    // keys of item i of a prompt: ctx - n + (i + 1) * 2 tpt (fewer than that in
+    // a chunk longer than its context: then only the balance is off)
+    const long long keys = kTree ? q.ctx + static_cast<long long>(kKeys) : max(q.ctx - q.n, 0);
+    c.b = kTree ? 0 : kCostTwo * tpt;
+    c.a = kCostTwo * keys + kItemCost + c.b;
     constexpr int kOne = cost_one(kTree);
-    return (q.rest > tpt ? kCostTwo : kOne) * keys + kItemCost;
-}
-
-template <bool kTree>
-__device__ __forceinline__ long long head_cost(const Seq& q, int tpt) {
-    return full_cost<kTree>(q, tpt, q.full) + (q.rest ? last_cost<kTree>(q, tpt) : 0);
+    c.last = q.rest ? (q.rest > tpt ? kCostTwo : kOne) * (kTree ? keys : static_cast<long long>(q.ctx)) + kItemCost : 0;
+    return c;
 }
 
 // Tiles of an item that belong to ranges before a cut `off` cost units into
@@ -228,12 +228,6 @@ __device__ __forceinline__ void set_item(const Params& p, Item& it) {
     it.first_masked = (kTree ? it.q.ctx : max(it.pos0 + 1, 0)) / kKeys;
 }
 
-template <bool kTree>
-__device__ __forceinline__ long long item_cost(const Params& p, const Item& it) {
-    return it.i < it.q.full ? full_cost<kTree>(it.q, p.tpt, it.i + 1) - full_cost<kTree>(it.q, p.tpt, it.i)
-                            : last_cost<kTree>(it.q, p.tpt);
-}
-
 // The loader's walk over its CTA's range: next() yields the pieces in order.
 template <bool kTree>
 struct Walk {
@@ -255,34 +249,37 @@ struct Walk {
         i1 = m.cut[1][2];
         t1 = m.cut[1][3];
     }
-    __device__ __forceinline__ void look_ahead() {
-        if (it.s + 1 < p.num_seqs) ahead = load_seq<kTree>(p, it.s + 1, nullptr);
-    }
     __device__ __forceinline__ bool next() {
-        bool step = !first;
+        bool enter = first, step = !first;  // a sequence was entered; go on to another item
         if (first) {
-            first = false;
             if (it.s >= p.num_seqs) return false;
-            look_ahead();
             set_item<kTree>(p, it);
             step = ta >= it.cut_tiles();  // the range starts behind this item
+            first = false;
         }
-        if (step) {
-            ta = 0;
-            ++it.i;
-            if (it.i * 2 * p.tpt >= it.q.n) {
-                it.i = 0;
-                if (++it.h == p.hkv) {
-                    it.h = 0;
-                    do {
+#pragma unroll 1
+        while (enter || step) {
+            if (enter) {
+                if (it.s + 1 < p.num_seqs) ahead = load_seq<kTree>(p, it.s + 1, nullptr);
+                enter = false;
+            }
+            if (step) {
+                step = false;
+                ta = 0;
+                ++it.i;
+                if (it.i * 2 * p.tpt >= it.q.n) {
+                    it.i = 0;
+                    if (it.q.n == 0 || ++it.h == p.hkv) {
+                        it.h = 0;
                         if (++it.s >= p.num_seqs) return false;
                         it.q = ahead;
-                        look_ahead();
-                    } while (it.q.n == 0);
+                        enter = true;
+                        step = it.q.n == 0;
+                    }
                 }
             }
-            set_item<kTree>(p, it);
         }
+        set_item<kTree>(p, it);
         if (it.s > s1 || (it.s == s1 && (it.h > h1 || (it.h == h1 && it.i > i1)))) return false;
         const bool last = it.s == s1 && it.h == h1 && it.i == i1;
         if (last && t1 <= ta) return false;
@@ -319,7 +316,17 @@ struct Walk {
     }
 };
 
-// Place of a piece's j-th K or V tile in the ring, in the order of their use.
+// The ring's entries of a piece in the order of their use: K0 V0 K1 V1 ... for
+// two query tiles, K0 K1 V0 K2 V1 ... for one, whose streams take turns; and
+// the places of the j-th K and V tile in it.
+struct RingEntry {
+    bool is_v;
+    int j;
+};
+__device__ __forceinline__ RingEntry ring_entry(bool two, int pos, int count) {
+    if (two || pos == 0 || pos == 2 * count - 1) return {(pos & 1) != 0, pos >> 1};
+    return (pos & 1) ? RingEntry{false, (pos >> 1) + 1} : RingEntry{true, (pos >> 1) - 1};
+}
 __device__ __forceinline__ int ring_k(bool two, int j) { return two ? 2 * j : max(2 * j - 1, 0); }
 __device__ __forceinline__ int ring_v(bool two, int j, int count) { return two || j == count - 1 ? 2 * j + 1 : 2 * j + 2; }
 
@@ -335,10 +342,12 @@ __device__ void plan(const Params& p, Misc& m) {
     long long sum = 0;
     uint32_t bad = 0;
     Seq seq0 = {};
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
         const Seq q = load_seq<kTree>(p, s, &bad);
         if (s == s0) seq0 = q;
-        sum += head_cost<kTree>(q, p.tpt) * p.hkv;
+        const Cost c = cost_of<kTree>(q, p.tpt);
+        sum += (c.first(q.full) + c.last) * p.hkv;
     }
     if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
     long long incl = sum;
@@ -352,6 +361,7 @@ __device__ void plan(const Params& p, Misc& m) {
     if (threadIdx.x == 0) p.splits[blockIdx.x].ntiles = 0;
     __syncthreads();
     long long before = incl - sum, total = 0;
+#pragma unroll 1
     for (int w = 0; w < kHalfWarps; ++w) {
         const long long v = m.scan[e * kHalfWarps + w];
         if (w < warp) before += v;
@@ -364,29 +374,37 @@ __device__ void plan(const Params& p, Misc& m) {
     const long long x = chunk * (b + e);
     if (x < before || x >= before + sum) return;  // at or past the line's end: behind the last sequence
     long long at = before;
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
         Item it;
         it.q = s == s0 ? seq0 : load_seq<kTree>(p, s, nullptr);
-        const long long hc = head_cost<kTree>(it.q, p.tpt);
+        const Cost c = cost_of<kTree>(it.q, p.tpt);
+        const long long hc = c.first(it.q.full) + c.last;
         if (x >= at + hc * p.hkv) {
             at += hc * p.hkv;
             continue;
         }
         it.s = s;
         // estimates, then the exact head and item
-        it.h = min(static_cast<int>(__ll2float_rn(x - at) / __ll2float_rn(hc)), p.hkv - 1);
-        while (it.h > 0 && hc * it.h > x - at) --it.h;
-        while (it.h + 1 < p.hkv && hc * (it.h + 1) <= x - at) ++it.h;
-        const long long base = at + hc * it.h, off = x - base;
-        const int items = it.q.full + (it.q.rest > 0);
-        // cost of i items: bend * i^2 + lin * i
-        const float bend = kTree ? 0.f : static_cast<float>(kCostTwo) * p.tpt;
-        const float lin = __ll2float_rn(full_cost<kTree>(it.q, p.tpt, 1)) - bend, o = __ll2float_rn(off);
-        it.i = min(static_cast<int>(2.f * o / (lin + sqrtf(lin * lin + 4.f * bend * o))), items - 1);
-        while (it.i > 0 && full_cost<kTree>(it.q, p.tpt, it.i) > off) --it.i;
-        while (it.i + 1 < items && full_cost<kTree>(it.q, p.tpt, it.i + 1) <= off) ++it.i;
+        long long off = x - at;
+        it.h = min(static_cast<int>(__ll2float_rn(off) / __ll2float_rn(hc)), p.hkv - 1);
+        off -= hc * it.h;
+        if (off < 0) {
+            off += hc;
+            --it.h;
+        } else if (off >= hc) {
+            off -= hc;
+            ++it.h;
+        }
+        const float fa = __ll2float_rn(c.a), fo = __ll2float_rn(off);
+        it.i = min(static_cast<int>(2.f * fo / (fa + sqrtf(fa * fa + 4.f * c.b * fo))), it.q.full - (it.q.rest == 0));
+#pragma unroll 1
+        while (c.first(it.i) > off) --it.i;
+#pragma unroll 1
+        while (it.i < it.q.full - (it.q.rest == 0) && c.first(it.i + 1) <= off) ++it.i;
         set_item<kTree>(p, it);
-        const long long start = base + full_cost<kTree>(it.q, p.tpt, it.i), cost = item_cost<kTree>(p, it);
+        const long long start = x - off + c.first(it.i);
+        const long long cost = it.i < it.q.full ? c.first(it.i + 1) - c.first(it.i) : c.last;
         const int t = cut_tile(x - start, cost, it.cut_tiles());
         m.cut[e][0] = s;
         m.cut[e][1] = it.h;
@@ -416,9 +434,10 @@ __device__ __forceinline__ uint32_t non_finite2(uint32_t w) {  // a set sign bit
     return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 
-// One 128-byte half of a row of a value tile in the ring: its non-finite values
-// become zero; whether there were any.
-__device__ __forceinline__ bool clean_half_row(uint8_t* half, int lane) {
+// One 128-byte half of a row of a value tile in the ring: non-finite values
+// become zero, a row behind the last (live false) becomes zero whole. Whether
+// a live row had non-finite values.
+__device__ __forceinline__ bool clean_half_row(uint8_t* half, int lane, bool live) {
     uint4 v[8];
     uint32_t any = 0;
     // lanes start at different 16-byte chunks of their rows: no bank conflicts
@@ -426,18 +445,15 @@ __device__ __forceinline__ bool clean_half_row(uint8_t* half, int lane) {
     for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(half + ((i + lane) & 7) * 16);
 #pragma unroll
     for (int i = 0; i < 8; ++i) any |= non_finite2(v[i].x) | non_finite2(v[i].y) | non_finite2(v[i].z) | non_finite2(v[i].w);
-    if (any == 0) return false;
-#pragma unroll
+    if (any == 0 && live) return false;
+#pragma unroll 1
     for (int i = 0; i < 8; ++i) {
-        auto finite = [](uint32_t w) { return w & ~((non_finite2(w) >> 15) * 0xFFFFu); };
-        *reinterpret_cast<uint4*>(half + ((i + lane) & 7) * 16) = make_uint4(finite(v[i].x), finite(v[i].y), finite(v[i].z), finite(v[i].w));
+        uint4* const at = reinterpret_cast<uint4*>(half + ((i + lane) & 7) * 16);
+        auto finite = [live](uint32_t w) { return live ? w & ~((non_finite2(w) >> 15) * 0xFFFFu) : 0u; };
+        const uint4 u = *at;
+        *at = make_uint4(finite(u.x), finite(u.y), finite(u.z), finite(u.w));
     }
-    return true;
-}
-
-__device__ __forceinline__ void zero_half_row(uint8_t* half, int lane) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(half + ((i + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+    return live;
 }
 
 // The keys of a masked tile that a row sees, as four words of 32.
@@ -458,35 +474,37 @@ __device__ __forceinline__ void seen_words(const Piece& it, int tile, int vis, u
     }
 }
 
-// Adds to columns [lo, hi) of a finished row the non-finite values that were
-// taken out of the product for keys the row sees (their weights are positive,
-// so each weighted value is the value itself). bad: the words of tiles t_lo ..
-template <bool kTree, typename T>
-__device__ void add_non_finite(const Params& p, const Piece& it, int t_lo, int t_hi, const uint32_t (*bad)[4], int vis,
-                               uint64_t draft_mask, int lo, int hi, T* out_row) {
-    for (int t = t_lo; t < t_hi; ++t) {
-        uint32_t w[4];
-        seen_words<kTree>(it, t, vis, draft_mask, w);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t bits = bad[t - t_lo][k] & w[k];
-            while (bits) {
-                const int key = __ffs(bits) - 1 + 32 * k;
-                bits &= bits - 1;
-                const __nv_bfloat16* row;
-                if (kTree && t == it.nct) {
-                    row = p.v_draft + (static_cast<long long>(it.seq_tok0 + key) * p.hkv + it.h) * kDim;
-                } else {
-                    const int pos = t * kKeys + key;
-                    int blk = __ldg(p.block_tables + static_cast<long long>(it.s) * p.max_blocks + pos / p.bt);
-                    if (blk < 0 || blk >= p.num_blocks) blk = 0;
-                    row = p.v_cache + ((static_cast<long long>(blk) * p.hkv + it.h) * p.bt + pos % p.bt) * kDim;
-                }
+// Adds to columns [lo, hi) of a finished row -- bf16 in out, or fp32 in part --
+// the non-finite values that were taken out of the product for keys the row
+// sees (their weights are positive, so each weighted value is the value
+// itself). bad: the words of tiles t_lo ..
+template <bool kTree>
+__device__ __forceinline__ void add_non_finite(const Params& p, const Piece& it, int t_lo, int t_hi, const uint32_t (*bad)[4],
+                                               int vis, uint64_t draft_mask, int lo, int hi, __nv_bfloat16* out, float* part) {
 #pragma unroll 1
-                for (int c = lo; c < hi; ++c) {
-                    const float v = __bfloat162float(row[c]);
-                    if (!isfinite(v)) out_row[c] = static_cast<T>(static_cast<float>(out_row[c]) + v);
-                }
+    for (int kk = 0; kk < 4 * (t_hi - t_lo); ++kk) {
+        const int t = t_lo + (kk >> 2), k = kk & 3;
+        uint32_t bits = bad[kk >> 2][k];
+#pragma unroll 1
+        for (; bits; bits &= bits - 1) {
+            const int key = __ffs(bits) - 1 + 32 * k;
+            const __nv_bfloat16* row;
+            if (kTree && t == it.nct) {
+                if (!(draft_mask >> key & 1)) continue;
+                row = p.v_draft + (static_cast<long long>(it.seq_tok0 + key) * p.hkv + it.h) * kDim;
+            } else {
+                const int pos = t * kKeys + key;
+                if (pos >= vis) continue;
+                int blk = __ldg(p.block_tables + static_cast<long long>(it.s) * p.max_blocks + pos / p.bt);
+                if (blk < 0 || blk >= p.num_blocks) blk = 0;
+                row = p.v_cache + ((static_cast<long long>(blk) * p.hkv + it.h) * p.bt + pos % p.bt) * kDim;
+            }
+#pragma unroll 1
+            for (int c = lo; c < hi; ++c) {
+                const float v = __bfloat162float(row[c]);
+                if (isfinite(v)) continue;
+                if (out) out[c] = __float2bfloat16(__bfloat162float(out[c]) + v);
+                else part[c] += v;
             }
         }
     }
@@ -552,7 +570,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const uint32_t tmem = m.tmem;
     // A reader of the pieces: the n-th, or null when there are no more (or the pipeline broke).
     auto get_piece = [&](uint32_t n) -> const Piece* {
-        const bool ok = mbar_wait(smem_u32(&m.piece_full[n % kPieces]), (n / kPieces) & 1, abort_flag, p.err);
+        const bool ok = wait_for(smem_u32(&m.piece_full[n % kPieces]), (n / kPieces) & 1, abort_flag, p.err);
         const Piece& d = m.piece[n % kPieces];
         return __all_sync(0xFFFFFFFFu, ok) && d.count >= 0 ? &d : nullptr;
     };
@@ -576,7 +594,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&m.join[k]));
-            const bool met = mbar_wait(smem_u32(&m.join[k]), n_join & 1, abort_flag, p.err);
+            const bool met = wait_for(smem_u32(&m.join[k]), n_join & 1, abort_flag, p.err);
             tc_fence_after();
             return __all_sync(0xFFFFFFFFu, met) != 0;
         };
@@ -601,7 +619,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             bool ok = true;
             for (int i = 0; i < count; ++i) {
                 const int tile = tile0 + i * tile_step;
-                ok = mbar_wait(smem_u32(&m.s_full[stream]), n_s & 1, abort_flag, p.err);
+                ok = wait_for(smem_u32(&m.s_full[stream]), n_s & 1, abort_flag, p.err);
                 ++n_s;
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 tc_fence_after();
@@ -688,7 +706,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
             if (!ok) break;
             if (count > 0) {
-                ok = mbar_wait(smem_u32(&m.o_full[stream]), n_o & 1, abort_flag, p.err);
+                ok = wait_for(smem_u32(&m.o_full[stream]), n_o & 1, abort_flag, p.err);
                 ++n_o;
                 if (!__all_sync(0xFFFFFFFFu, ok)) break;
                 tc_fence_after();
@@ -752,33 +770,32 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
                 for (int k = 0; k < 4; ++k) orow[k] = __shfl_sync(0xFFFFFFFFu, out_row, r0 + 8 * k);
                 const uint64_t f0x2 = pair(f0, f0), f1x2 = pair(f1, f1);
-                auto columns = [&](int col) {
+#pragma unroll 1
+                for (int col = col_lo; col < col_hi; col += 32) {
                     uint32_t r[32];
                     tmem_ld32(r, acc0 + col);
+                    tmem_wait_ld(r);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        float a, b;
+                        unpair(mul2(pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), f0x2), a, b);
+                        r[c] = __float_as_uint(a);
+                        r[c + 1] = __float_as_uint(b);
+                    }
                     if (has1) {
                         uint32_t r1[32];
                         tmem_ld32(r1, acc1 + col);
-                        tmem_wait_ld(r);
-                        hold(r1);
+                        tmem_wait_ld(r1);
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
                             float a, b;
-                            unpair(fma2(pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), f0x2,
-                                        mul2(pair(__uint_as_float(r1[c]), __uint_as_float(r1[c + 1])), f1x2)), a, b);
+                            unpair(fma2(pair(__uint_as_float(r1[c]), __uint_as_float(r1[c + 1])), f1x2,
+                                        pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1]))), a, b);
                             r[c] = __float_as_uint(a);
                             r[c + 1] = __float_as_uint(b);
                         }
-                    } else if (has0) {
-                        tmem_wait_ld(r);
-#pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            float a, b;
-                            unpair(mul2(pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), f0x2), a, b);
-                            r[c] = __float_as_uint(a);
-                            r[c + 1] = __float_as_uint(b);
-                        }
-                    } else {
-                        tmem_wait_ld(r);
+                    }
+                    if (!has0) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) r[c] = 0u;
                     }
@@ -804,24 +821,12 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                                 *chunk(q, lane, c) = make_uint4(r[16 * q + 4 * c], r[16 * q + 4 * c + 1], r[16 * q + 4 * c + 2], r[16 * q + 4 * c + 3]);
                         }
                         __syncwarp();
+                        float* const dst = p.part_o + (part_row0 + r0) * kDim + col + c0 * 4;
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint4 v[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) v[k] = *chunk(q, r0 + 8 * k, c0);
-                            // rows that are none are written too: they are the workspace's
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                *reinterpret_cast<uint4*>(p.part_o + (part_row0 + r0 + 8 * k) * kDim + col + 16 * q + c0 * 4) = v[k];
-                        }
+                        for (int k = 0; k < 8; ++k)  // rows that are none are written too: they are the workspace's
+                            *reinterpret_cast<uint4*>(dst + (k & 3) * 8 * kDim + (k >> 2) * 16) = *chunk(k >> 2, r0 + 8 * (k & 3), c0);
                         __syncwarp();
                     }
-                };
-#pragma unroll 1
-                for (int col = col_lo; col < col_hi; col += 64) {
-                    columns(col);
-                    columns(col + 32);
-                    __syncwarp();
                 }
             }
             if (!it.two) {
@@ -830,12 +835,9 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 ++n_join;
             }
             if (*const_cast<const volatile int*>(&it.any_bad) && valid && t_lo < t_end) {
-                if (whole)
-                    add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi,
-                                          p.out + static_cast<long long>(out_row) * kDim);
-                else
-                    add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi,
-                                          p.part_o + (part_row0 + lane) * kDim);
+                add_non_finite<kTree>(p, it, t_lo, t_end, bad, vis, draft_mask, col_lo, col_hi,
+                                      whole ? p.out + static_cast<long long>(out_row) * kDim : nullptr,
+                                      p.part_o + (part_row0 + lane) * kDim);
             }
             done_piece(n_item);
         }
@@ -850,7 +852,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         // One piece is described ahead of the one that is loaded, and its query rows
         // are brought into L2 meanwhile.
         auto describe = [&](bool more) {
-            ok = mbar_wait(smem_u32(&m.piece_empty[n_item % kPieces]), ((n_item / kPieces) & 1) ^ 1, abort_flag, p.err);
+            ok = wait_for(smem_u32(&m.piece_empty[n_item % kPieces]), ((n_item / kPieces) & 1) ^ 1, abort_flag, p.err);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) return;
             if (lane == 0) {
@@ -873,23 +875,26 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 tma_prefetch_5d(&tm_q, 0, 0, walk.it.tok0 + (lane >> 1) * p.tpt, lane & 1, walk.it.h);
             if (count == 0) continue;
             const int masked0 = max(it.first_masked, ta) - ta;  // first masked tile of the piece
-            // this lane's box of a tile: its last coordinate in the map
-            auto coordinate = [&](int j) {
-                const int t = ta + j;
-                if (kTree && t == it.nct) return it.seq_tok0 + lane * 8;
-                const int idx = t * blocks_per_tile + lane;
-                if (lane >= blocks_per_tile || idx * p.bt >= it.kend) return 0;
-                int blk = __ldg(p.block_tables + static_cast<long long>(it.s) * p.max_blocks + idx);
+            // this lane's block of a tile, read from the table a tile early; and its
+            // box's last coordinate in the map
+            auto table_entry = [&](int j) {
+                const int idx = (ta + j) * blocks_per_tile + lane;
+                if (j >= count || lane >= blocks_per_tile || idx * p.bt >= it.kend) return 0;
+                return __ldg(p.block_tables + static_cast<long long>(it.s) * p.max_blocks + idx);
+            };
+            auto coordinate = [&](int j, int blk) {
+                if (kTree && ta + j == it.nct) return it.seq_tok0 + lane * 8;
                 if (blk < 0 || blk >= p.num_blocks) {
                     atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
                     blk = 0;
                 }
                 return (blk * p.hkv + it.h) * (p.bt >> 3);
             };
+            int blk_next = table_entry(0), coord_k = 0, coord_v = 0;  // of K's tile; of the V tile to come
             auto load = [&](bool is_v, int j, int pos, int coord) {
                 const uint32_t at = ring + pos;
                 const uint32_t st = at % kStages, ph = (at / kStages) & 1;
-                ok = mbar_wait(smem_u32(&m.kv_empty[st]), ph ^ 1, abort_flag, p.err);
+                ok = wait_for(smem_u32(&m.kv_empty[st]), ph ^ 1, abort_flag, p.err);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) return;
                 const int t = ta + j;
@@ -912,111 +917,191 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     else tma_load_4d(dst + lane * box_bytes, is_v ? &tm_v : &tm_k, 0, 0, 0, coord, full);
                 }
             };
-            int cur = coordinate(0);
-            load(false, 0, 0, cur);
-            if (!ok) break;
-            ok = mbar_wait(smem_u32(&m.q_empty), (n_q & 1) ^ 1, abort_flag, p.err);
-            ++n_q;
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            const int tiles = it.two ? 2 : 1;
-            if (lane == 0) mbar_arrive_expect_tx(smem_u32(&m.q_full), tiles * 2 * 128 * p.group * p.tpt);
-            __syncwarp();
-            if (lane < 2 * tiles) {
-                const int t = lane >> 1, panel = lane & 1;
-                tma_load_5d(smem_base + kSmemQ + t * kTileBytes + panel * (kTileBytes / 2), &tm_q, 0, 0,
-                            it.tok0 + t * p.tpt, panel, it.h, smem_u32(&m.q_full));
-            }
-            for (int j = 0; ok && j < count; ++j) {
-                int next = 0;
-                if (j + 1 < count) next = coordinate(j + 1);
-                if (!it.two && j + 1 < count) load(false, j + 1, ring_k(it.two, j + 1), next);
-                if (ok) load(true, j, ring_v(it.two, j, count), cur);
-                if (ok && it.two && j + 1 < count) load(false, j + 1, ring_k(it.two, j + 1), next);
-                cur = next;
+#pragma unroll 1
+            for (int pos = 0; ok && pos < 2 * count; ++pos) {
+                const RingEntry en = ring_entry(it.two, pos, count);
+                if (!en.is_v) {
+                    const int c = coordinate(en.j, blk_next);
+                    blk_next = table_entry(en.j + 1);
+                    coord_v = it.two || pos == 0 ? c : coord_k;
+                    coord_k = c;
+                }
+                load(en.is_v, en.j, pos, en.is_v ? coord_v : coord_k);
+                if (en.is_v) coord_v = coord_k;
+                if (ok && pos == 0) {
+                    ok = wait_for(smem_u32(&m.q_empty), (n_q & 1) ^ 1, abort_flag, p.err);
+                    ++n_q;
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    const int tiles = it.two ? 2 : 1;
+                    if (lane == 0) mbar_arrive_expect_tx(smem_u32(&m.q_full), tiles * 2 * 128 * p.group * p.tpt);
+                    __syncwarp();
+                    if (lane < 2 * tiles) {
+                        const int t = lane >> 1, panel = lane & 1;
+                        tma_load_5d(smem_base + kSmemQ + t * kTileBytes + panel * (kTileBytes / 2), &tm_q, 0, 0,
+                                    it.tok0 + t * p.tpt, panel, it.h, smem_u32(&m.q_full));
+                    }
+                }
             }
             ring += 2 * count;
             n_clean += max(count - masked0, 0);
         }
     } else if (warp == kWarpMma) {
-        // ---- tensor core: one elected thread issues every product. The warp
-        // stays converged and its counters provably uniform: with the loop in
-        // one diverged lane, issuing the 8 products of a tile took 620-900
-        // cycles against the 512 they run for.
+        // ---- tensor core: one elected thread issues every product, P V of a
+        // stream's key tile and S of its next one in one go. The tensor core queues
+        // only two or three products, so whatever the issuer waits for between them
+        // shows as idle time; and issued from one place the streams take turns, one
+        // multiplying while the other takes exponentials (an issuer for each let
+        // both do the same at the same time). The warp stays converged and its
+        // counters provably uniform: in one diverged lane, issuing the 8 products of
+        // a tile took 620-900 cycles against the 512 they run for.
         constexpr uint32_t kIdescS = mma_idesc(kRows, kKeys, false), kIdescO = mma_idesc(kRows, kDim, true);
         const uint32_t tm = uniform(tmem), base = uniform(smem_base);
-        uint32_t ring = 0, n_q = 0, n_clean = 0, n_p[2] = {0, 0};
+        uint32_t ring = 0, n_q = 0, n_clean = 0, n_p0 = 0, n_p1 = 0;  // n_p: tiles of each stream so far
         bool ok = true;
         for (uint32_t n_item = 0; ok; ++n_item) {
             const Piece* const piece = get_piece(n_item);
             if (!piece) break;
             const int count = uniform(piece->count);
             const bool two = uniform(piece->two) != 0;
-            const int cnt[2] = {static_cast<int>(uniform(piece->cnt[0])), static_cast<int>(uniform(piece->cnt[1]))};
+            const int cnt0 = uniform(piece->cnt[0]), cnt1 = uniform(piece->cnt[1]);
             const int masked0 = uniform(max(piece->first_masked - piece->ta, 0));  // first masked tile of the piece
             done_piece(n_item);
             if (count == 0) continue;
-            ok = mbar_wait(smem_u32(&m.q_full), n_q & 1, abort_flag, p.err);
+            struct Step {
+                bool has_v, has_k, last_k;
+                uint32_t st_v, st_k, bar_v, bar_k, bar_p, par_v, par_k, par_p;
+            };
+            auto step_at = [&](int turn) {
+                const int stream = turn & 1, i = turn >> 1, n = stream ? cnt1 : cnt0;
+                const int jv = two ? i : 2 * i + stream, jk = two ? i + 1 : jv + 2;
+                const uint32_t at_v = ring + ring_v(two, jv, count), at_k = ring + ring_k(two, jk), c = n_clean + (jv - masked0);
+                Step x;
+                x.has_v = i >= 0 && i < n;
+                x.has_k = i + 1 < n;
+                x.last_k = jk == count - 1;
+                x.st_v = at_v % kStages;
+                x.st_k = at_k % kStages;
+                const bool cleaned = jv >= masked0;
+                x.bar_v = cleaned ? smem_u32(&m.clean[c % kCleanBars]) : smem_u32(&m.kv_full[x.st_v]);
+                x.par_v = cleaned ? (c / kCleanBars) & 1 : (at_v / kStages) & 1;
+                x.bar_k = smem_u32(&m.kv_full[x.st_k]);
+                x.par_k = (at_k / kStages) & 1;
+                x.bar_p = smem_u32(&m.p_full[stream]);
+                x.par_p = ((stream ? n_p1 : n_p0) + i) & 1;
+                return x;
+            };
+            ok = wait_for(smem_u32(&m.q_full), n_q & 1, abort_flag, p.err);
             ++n_q;
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-
-            // S of the stream's i-th key tile
-            auto scores = [&](int stream, int i) {
-                const int j = two ? i : 2 * i + stream;
-                const uint32_t at = ring + ring_k(two, j), st = at % kStages;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&m.kv_full[st]), (at / kStages) & 1, abort_flag, p.err));
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t a = smem_desc(base + kSmemQ + (two ? stream * kTileBytes : 0), 16, 1024);
-                const uint64_t b = smem_desc(base + kSmemRing + st * kTileBytes, 16, 2048);
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ss(tm + stream * 128, a + (((k >> 2) * (kTileBytes / 2) + (k & 3) * 32) >> 4),
-                               b + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), kIdescS, k > 0);
-                    mma_commit(smem_u32(&m.s_full[stream]));
-                    if (!two || stream == 1) mma_commit(smem_u32(&m.kv_empty[st]));
-                    if (j == count - 1 && (!two || stream == 1)) mma_commit(smem_u32(&m.q_empty));
-                }
-                __syncwarp();
+            // S of each stream's first tile, then P V of tile i with S of tile i + 1,
+            // the streams in turn. A step waits for its V and K tile and its P.
+            const int turns = 2 * max(cnt0, cnt1);
+            auto issue_s = [&](uint32_t t_s, uint32_t dq, uint32_t dk, int k) {
+                mma_ss<desc_high(1024), desc_high(2048), kIdescS>(t_s, dq + (((k >> 2) * (kTileBytes / 2) + (k & 3) * 32) >> 4),
+                       dk + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), k > 0);
             };
-            // O += P V for the stream's i-th key tile
-            auto values = [&](int stream, int i) {
-                const int j = two ? i : 2 * i + stream;
-                const uint32_t at = ring + ring_v(two, j, count), st = at % kStages;
-                if (j >= masked0) {
-                    const uint32_t c = n_clean + (j - masked0);
-                    ok = mbar_wait(smem_u32(&m.clean[c % kCleanBars]), (c / kCleanBars) & 1, abort_flag, p.err);
-                } else {
-                    ok = mbar_wait(smem_u32(&m.kv_full[st]), (at / kStages) & 1, abort_flag, p.err);
+            auto issue_o = [&](uint32_t t_s, uint32_t dv, int k, bool accumulate) {
+                mma_ts<desc_high(2048), kIdescO>(t_s + kTmemO, t_s + k * 8, dv + ((k * 4096) >> 4), accumulate);
+            };
+            auto tile_at = [&](uint32_t at) { return base + kSmemRing + (at % kStages) * kTileBytes; };
+            const uint32_t dq0 = desc_low(base + kSmemQ, 16), dq1 = two ? desc_low(base + kSmemQ + kTileBytes, 16) : dq0;
+            // Two query tiles, both with a tile to come that every row sees in full: the
+            // same steps in as little as it takes, since a scalar instruction of this
+            // warp costs up to 10 cycles beside the softmax warps', and what is not
+            // hidden behind the two or three queued products (a look at the next
+            // barriers before a step's last three) leaves the tensor core idle.
+            const int fast = two ? min(cnt0 - 1, masked0) : 0;
+            ok = __all_sync(0xFFFFFFFFu, ok);
+#pragma unroll 1
+            for (int turn = -2; ok && turn < turns; ++turn) {
+                if (turn == 0 && fast > 0) {
+                    const uint32_t p0 = smem_u32(&m.p_full[0]), p1 = smem_u32(&m.p_full[1]);
+                bool ready = false;
+#pragma unroll 1
+                for (int i = 0; i < fast; ++i) {
+                    const uint32_t at = ring + 2 * i + 1;  // V of tile i, then K of tile i + 1
+                    const uint32_t dv = desc_low(tile_at(at), 1024), dk = desc_low(tile_at(at + 1), 16);
+                    if (!ready) {
+                        ok = wait_for(smem_u32(&m.kv_full[at % kStages]), (at / kStages) & 1, abort_flag, p.err);
+                        if (ok) ok = wait_for(smem_u32(&m.kv_full[(at + 1) % kStages]), ((at + 1) / kStages) & 1, abort_flag, p.err);
+                        if (ok) ok = wait_for(p0, (n_p0 + i) & 1, abort_flag, p.err);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) issue_o(tm, dv, k, i > 0 || k > 0);
+#pragma unroll
+                        for (int k = 0; k < 5; ++k) issue_s(tm, dq0, dk, k);
+                    }
+                    __syncwarp();
+                    ready = __all_sync(0xFFFFFFFFu, mbar_test(p1, (n_p1 + i) & 1));
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 5; k < 8; ++k) issue_s(tm, dq0, dk, k);
+                        mma_commit(smem_u32(&m.s_full[0]));
+                    }
+                    __syncwarp();
+                    if (!ready) {
+                        ok = __all_sync(0xFFFFFFFFu, wait_for(p1, (n_p1 + i) & 1, abort_flag, p.err));
+                        if (!ok) break;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) issue_o(tm + 128, dv, k, i > 0 || k > 0);
+                        mma_commit(smem_u32(&m.kv_empty[at % kStages]));
+#pragma unroll
+                        for (int k = 0; k < 5; ++k) issue_s(tm + 128, dq1, dk, k);
+                    }
+                    __syncwarp();
+                    ready = mbar_test(p0, (n_p0 + i + 1) & 1) & mbar_test(smem_u32(&m.kv_full[(at + 2) % kStages]), ((at + 2) / kStages) & 1) &
+                            mbar_test(smem_u32(&m.kv_full[(at + 3) % kStages]), ((at + 3) / kStages) & 1);
+                    ready = __all_sync(0xFFFFFFFFu, ready) && i + 1 < fast;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 5; k < 8; ++k) issue_s(tm + 128, dq1, dk, k);
+                        mma_commit(smem_u32(&m.s_full[1]));
+                        mma_commit(smem_u32(&m.kv_empty[(at + 1) % kStages]));
+                        if (i + 2 == count) mma_commit(smem_u32(&m.q_empty));
+                    }
+                    __syncwarp();
                 }
-                if (ok) ok = mbar_wait(smem_u32(&m.p_full[stream]), n_p[stream] & 1, abort_flag, p.err);
-                ++n_p[stream];
+                    if (!ok) break;
+                    turn = 2 * fast;
+                }
+                const Step now = step_at(turn);
+                if (!now.has_v && !now.has_k) continue;
+                if (now.has_v) ok = wait_for(now.bar_v, now.par_v, abort_flag, p.err);
+                if (ok && now.has_k) ok = wait_for(now.bar_k, now.par_k, abort_flag, p.err);
+                if (ok && now.has_v) ok = wait_for(now.bar_p, now.par_p, abort_flag, p.err);
                 ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) return;
+                if (!ok) break;
                 tc_fence_after();
-                const uint64_t b = smem_desc(base + kSmemRing + st * kTileBytes, 1024, 2048);
+                const uint32_t t_s = tm + (turn & 1) * 128;
+                const bool last_user = !two || (turn & 1);  // of a key tile
                 if (elect_one()) {
+                    if (now.has_v) {
+                        const uint32_t dv = desc_low(base + kSmemRing + now.st_v * kTileBytes, 1024);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ts(tm + kTmemO + stream * 128, tm + stream * 128 + k * 8, b + ((k * 4096) >> 4), kIdescO,
-                               i > 0 || k > 0);
-                    if (!two || stream == 1) mma_commit(smem_u32(&m.kv_empty[st]));
-                    if (i == cnt[stream] - 1) mma_commit(smem_u32(&m.o_full[stream]));
+                        for (int k = 0; k < 8; ++k) issue_o(t_s, dv, k, turn >= 2 || k > 0);
+                        if (last_user) mma_commit(smem_u32(&m.kv_empty[now.st_v]));
+                        if (!now.has_k) mma_commit(smem_u32(&m.o_full[turn & 1]));
+                    }
+                    if (now.has_k) {
+                        const uint32_t dk = desc_low(base + kSmemRing + now.st_k * kTileBytes, 16), dq = turn & 1 ? dq1 : dq0;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) issue_s(t_s, dq, dk, k);
+                        mma_commit(smem_u32(&m.s_full[turn & 1]));
+                        if (last_user) mma_commit(smem_u32(&m.kv_empty[now.st_k]));
+                        if (last_user && now.last_k) mma_commit(smem_u32(&m.q_empty));
+                    }
                 }
                 __syncwarp();
-            };
-
-            if (cnt[0] > 0) scores(0, 0);
-            if (ok && cnt[1] > 0) scores(1, 0);
-            const int rounds = max(cnt[0], cnt[1]);
-            for (int i = 0; ok && i < rounds; ++i)
-#pragma unroll
-                for (int stream = 0; stream < 2; ++stream) {
-                    if (!ok || i >= cnt[stream]) continue;
-                    values(stream, i);
-                    if (ok && i + 1 < cnt[stream]) scores(stream, i + 1);
-                }
+            }
+            n_p0 += cnt0;
+            n_p1 += cnt1;
             ring += 2 * count;
             n_clean += max(count - masked0, 0);
         }
@@ -1030,26 +1115,22 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (!piece) break;
             const int count = piece->count;
             const int masked0 = max(piece->first_masked - piece->ta, 0);
+#pragma unroll 1
             for (int j = masked0; ok && j < count; ++j, ++n_clean) {
                 const uint32_t st = (ring + ring_v(piece->two, j, count)) % kStages;
                 const int t = piece->ta + j;
                 const int valid = kTree && t == piece->nct ? piece->seq_n : min(kKeys, piece->kend - t * kKeys);
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&m.part_full[n_clean % kCleanBars]),
+                ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&m.part_full[n_clean % kCleanBars]),
                                                        (n_clean / kCleanBars) & 1, abort_flag, p.err));
                 if (!ok) break;
                 uint8_t* tile = smem + kSmemRing + st * kTileBytes;
-#pragma unroll
+#pragma unroll 1
                 for (int r = 0; r < 2; ++r) {
                     const int row = half * 64 + r * 32 + lane;
-                    uint8_t* const halves = tile + (row >> 3) * 2048 + (row & 7) * 128;
+                    uint8_t* const row_at = tile + (row >> 3) * 2048 + (row & 7) * 128;
                     bool bad = false;
-                    if (row < valid) {
-                        bad = clean_half_row(halves, lane);
-                        bad |= clean_half_row(halves + 1024, lane);
-                    } else {
-                        zero_half_row(halves, lane);
-                        zero_half_row(halves + 1024, lane);
-                    }
+#pragma unroll 1
+                    for (int side = 0; side < 2; ++side) bad |= clean_half_row(row_at + side * 1024, lane, row < valid);
                     const uint32_t word = __ballot_sync(0xFFFFFFFFu, bad);
                     if (lane == 0) {
                         m.bad[n_item % kPieces][j - masked0][half * 2 + r] = word;

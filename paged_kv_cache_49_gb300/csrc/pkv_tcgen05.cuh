@@ -5,7 +5,51 @@
 
 #include <cstdint>
 
+#include "pkv_ptx.cuh"
+
 namespace pkv {
+
+// mbar_wait in fewer instructions
+template <bool kSpin = false>
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 1;; ++n) {
+        uint32_t done;
+        if (kSpin)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        else
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        if (done) return true;
+        if (n & 255) continue;
+        if (*abort_flag) return false;
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitLimitNs) break;
+    }
+    *abort_flag = 1;
+    if (err) atomicOr(err, PKV_DEVERR_TIMEOUT);
+    return false;
+}
+
+// Whether the phase of that parity is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
 
 // ---- tensor memory -------------------------------------------------------------
 // One warp allocates (and later frees) columns; the address lands in shared memory.
@@ -72,27 +116,33 @@ __host__ __device__ constexpr uint32_t mma_idesc(int m, int n, bool b_mn) {
 // Shared-memory operand descriptor, 128-byte swizzle: atoms of 8 rows x 128
 // bytes. K contiguous: stride = bytes from 8 rows to the next 8. M or N
 // contiguous: stride = bytes from 8 k to the next 8, lead = bytes from 64
-// values of M or N to the next 64.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
-           (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
+// values of M or N to the next 64. The low word holds the address and the
+// lead, so that stepping through a tile is one 32-bit addition; the high word
+// is a constant.
+__host__ __device__ constexpr uint32_t desc_high(uint32_t stride) { return (stride >> 4) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) { return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16); }
 
 // D[tensor memory] (+)= A[shared] * B[shared], K = 16.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+template <uint32_t kHighA, uint32_t kHighB, uint32_t kIdesc>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_low), "n"(kHighA), "r"(b_low), "n"(kHighB), "n"(kIdesc), "r"(static_cast<uint32_t>(accumulate))
         : "memory");
 }
 
 // D[tensor memory] (+)= A[tensor memory] * B[shared], K = 16.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+template <uint32_t kHighB, uint32_t kIdesc>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_low, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_low), "n"(kHighB), "n"(kIdesc), "r"(static_cast<uint32_t>(accumulate))
         : "memory");
 }
 
