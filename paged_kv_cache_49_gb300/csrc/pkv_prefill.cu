@@ -166,22 +166,25 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
         tm_kd = tm_k;  // not read
         tm_vd = tm_v;
     }
+    // Both kernels are launched early (programmatic stream serialization) and
+    // wait for the one before, so that they are set up when it ends.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, tree ? rows_kernel<true> : rows_kernel<false>, tm_q, tm_k, tm_v, tm_kd, tm_vd, p);
-    if (e == cudaSuccess) {
-        // launched early, so that it is there when the last CTA ends
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    // an item of no more keys than the tables hold is never cut: nothing to join
+    const long long most_keys = static_cast<long long>(max_blocks_per_seq) * block_tokens + (tree ? kKeys : 0);
+    if (e == cudaSuccess && kCostTwo * most_keys + kItemCost > kWhole) {
         cfg.gridDim = dim3(grid, 8);
         cfg.blockDim = dim3(kMergeWarps * 32);
         cfg.dynamicSmemBytes = 0;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
         e = cudaLaunchKernelEx(&cfg, merge_kernel, p);
     }
     if (e == cudaSuccess) e = cudaGetLastError();

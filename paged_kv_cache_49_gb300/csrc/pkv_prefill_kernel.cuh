@@ -61,6 +61,7 @@ constexpr uint32_t kTmemO = 256;  // S0, S1, O0, O1 of 128 columns each
 constexpr int kCostTwo = 8, kItemCost = 8 * 200;
 __host__ __device__ constexpr int cost_one(bool tree) { return tree ? 8 : 6; }
 constexpr int kSnap = 8 * 256;      // a cut this near an item's end moves there
+constexpr int kWhole = 8 * 768;     // an item of this cost is never cut
 constexpr int kMinRange = 8 * 256;  // least cost of a CTA's range
 constexpr int kPieces = 4;          // pieces described ahead
 
@@ -195,8 +196,8 @@ __device__ __forceinline__ Cost cost_of(const Seq& q, int tpt) {
 // Tiles of an item that belong to ranges before a cut `off` cost units into
 // it; any monotone rule does that every reader computes alike.
 __device__ __forceinline__ int cut_tile(long long off, long long cost, int ntiles) {
-    if (off <= kSnap) return 0;
-    if (cost - off <= kSnap) return ntiles;
+    if (off <= kSnap || (cost <= kWhole && 2 * off < cost)) return 0;
+    if (cost - off <= kSnap || cost <= kWhole) return ntiles;
     const int t = static_cast<int>(__ll2float_rn(off) / __ll2float_rn(cost) * ntiles + 0.5f);
     return min(max(t, 0), ntiles);
 }
@@ -523,6 +524,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 
     griddep_launch_dependents();
     if (smem_base & 1023) {  // the swizzle atoms need it; dynamic shared memory starts so, with no static beside it
+        griddep_wait();
         if (tid == 0) {
             p.splits[blockIdx.x].ntiles = 0;
             atomicOr(p.err, PKV_DEVERR_TIMEOUT);
@@ -564,6 +566,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
     if (warp == kWarpMma) tmem_alloc(smem_u32(&m.tmem), kTmemColumns);
     tc_fence_before();
+    griddep_wait();  // launched early: the earlier kernels' results and the last call's partial results
     plan<kTree>(p, m);
     __syncthreads();
     tc_fence_after();
@@ -1161,6 +1164,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 constexpr int kMergeWarps = 8;
 
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Params p) {
+    griddep_launch_dependents();
     griddep_wait();
     const Split sp = p.splits[blockIdx.x];
     if (sp.ntiles == 0) return;

@@ -65,6 +65,7 @@ constexpr int kBlocksPerSm = 3;
 // kLanes: lanes per head row (a power of two, at least head_dim / 16).
 template <int kLanes, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) qk_write_kernel(const Params p) {
+    griddep_launch_dependents();  // an attention launched early behind this one sets itself up, then waits
     constexpr int kGroups = kThreads / kLanes;
     const int lane = threadIdx.x & (kLanes - 1);
     const int heads = p.hq + 2 * p.hkv;
