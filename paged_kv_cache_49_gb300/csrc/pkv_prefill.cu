@@ -17,6 +17,15 @@
 namespace pkv {
 namespace prefill {
 
+using KernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Params);
+
+KernelFn kernel_for(bool tree, bool one) {
+    if (one) return tree ? rows_kernel<true, true> : rows_kernel<false, true>;
+    return tree ? rows_kernel<true, false> : rows_kernel<false, false>;
+}
+
+size_t smem_for(bool one) { return one ? Smem<true>::kBytes : Smem<false>::kBytes; }
+
 // Per device, once: its SMs, and leave for the kernels' shared memory.
 struct DeviceInfo {
     bool ok = false;
@@ -34,17 +43,17 @@ DeviceInfo device_info() {
     if (d.ok) return d;
     int sms = 0;
     cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(rows_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(rows_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
-    // the kernels move registers between their warpgroups: a launch with fewer
-    // than they count on would wait for ever
-    for (const auto fn : {rows_kernel<false>, rows_kernel<true>}) {
-        cudaFuncAttributes at = {};
-        if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, fn);
-        if (e == cudaSuccess && at.numRegs < kRegsLaunch) e = cudaErrorInvalidDeviceFunction;
-    }
+    for (const bool tree : {false, true})
+        for (const bool one : {false, true}) {
+            const KernelFn fn = kernel_for(tree, one);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_for(one)));
+            // the kernels move registers between their warpgroups: a launch with
+            // fewer than they count on would wait for ever
+            cudaFuncAttributes at = {};
+            if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, fn);
+            if (e == cudaSuccess && at.numRegs < kRegsLaunch) e = cudaErrorInvalidDeviceFunction;
+        }
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return {};
@@ -147,7 +156,11 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
     p.hkv = num_kv_heads;
     p.group = num_q_heads / num_kv_heads;
     p.tpt = kRows / p.group;
-    p.item_magic = ((1ull << 36) + 2 * p.tpt - 1) / (2 * p.tpt);
+    // Sequences of one query tile each on the average (decode rows, small trees):
+    // the kernel of one-tile items, whose ring is deeper.
+    const bool one = static_cast<long long>(num_tokens) * p.group <= static_cast<long long>(num_seqs) * kRows;
+    const int tokens = (one ? 1 : 2) * p.tpt;
+    p.item_magic = ((1ull << 36) + tokens - 1) / tokens;
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = num_blocks;
     p.bt = block_tokens;
@@ -174,11 +187,11 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = smem_for(one);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, tree ? rows_kernel<true> : rows_kernel<false>, tm_q, tm_k, tm_v, tm_kd, tm_vd, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_for(tree, one), tm_q, tm_k, tm_v, tm_kd, tm_vd, p);
     // an item of no more keys than the tables hold is never cut: nothing to join
     const long long most_keys = static_cast<long long>(max_blocks_per_seq) * block_tokens + (tree ? kKeys : 0);
     if (e == cudaSuccess && kCostTwo * most_keys + kItemCost > kWhole) {

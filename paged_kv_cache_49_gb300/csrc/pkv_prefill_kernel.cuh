@@ -41,7 +41,6 @@ namespace prefill {
 constexpr int kDim = PKV_ATTN_HEAD_DIM;
 constexpr int kRows = 128;    // query rows of a tile
 constexpr int kKeys = 128;    // keys of a tile
-constexpr int kStages = 4;    // K or V tiles in flight
 constexpr int kThreads = 384;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpClean = 10;  // and 11
@@ -50,6 +49,7 @@ constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch, "register split");
 constexpr int kCleanBars = 8;  // more than the ring can hold
 
+constexpr int kMaxStages = 5;
 constexpr uint32_t kTileBytes = kKeys * kDim * 2;
 constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kTmemO = 256;  // S0, S1, O0, O1 of 128 columns each
@@ -83,7 +83,7 @@ struct Params {
     int num_seqs, num_tokens, hq, hkv, group, tpt;  // tpt: tokens of a tile
     int max_blocks, num_blocks, bt;
     float scale_log2;
-    unsigned long long item_magic;  // ceil(2^36 / (2 tpt))
+    unsigned long long item_magic;  // ceil(2^36 / tokens of an item)
 };
 
 // An item cut among CTAs, described by the CTA that has its first piece.
@@ -96,7 +96,7 @@ struct Split {
 
 struct Seq {
     int n, ctx, tok0;  // query rows, tokens in the cache, first row
-    int full, rest;    // items of two full tiles, rows of the last, smaller one
+    int full, rest;    // full items, tokens of the last, smaller one
 };
 
 // A CTA's piece of an item, as the loader describes it to the other warps.
@@ -117,7 +117,7 @@ struct __align__(16) Piece {
 
 struct __align__(16) Misc {
     uint64_t q_full, q_empty;
-    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
     uint64_t part_full[kCleanBars], clean[kCleanBars];  // value tiles to be cleaned: landed, cleaned
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t join[2];         // one-tile items: both streams' states are there; both accumulators are read
@@ -136,15 +136,26 @@ struct __align__(16) Misc {
     };
 };
 
-constexpr size_t kSmemQ = 0, kSmemRing = 2 * kTileBytes, kSmemOut = kSmemRing + kStages * kTileBytes;
+// Shared memory of a kernel whose items have one query tile at most, or two.
+// The room of the second one is a fifth stage of the ring: with four, a stream
+// of one-tile items over long contexts waits for its loads (a K tile is held
+// for 600 cycles after it lands, a V tile for 2,500, and a load takes 3,300).
 constexpr uint32_t kOutBytes = 32 * 128;  // a softmax warp's staging: 32 rows of 128 bytes
-constexpr size_t kSmemMisc = kSmemOut + kSoftmaxWarps * kOutBytes;
-constexpr size_t kSmemBytes = kSmemMisc + sizeof(Misc);
-static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+template <bool kOne>
+struct Smem {
+    static constexpr int kStages = kOne ? 5 : 4;  // K or V tiles in flight
+    static constexpr uint32_t kQ = 0, kRing = (kOne ? 1 : 2) * kTileBytes, kOut = kRing + kStages * kTileBytes;
+    static constexpr uint32_t kMisc = kOut + kSoftmaxWarps * kOutBytes;
+    static constexpr size_t kBytes = kMisc + sizeof(Misc);
+    static_assert(kBytes <= 232448, "shared memory of one CTA");
+};
 
 // ---- the work line -----------------------------------------------------------
 
-template <bool kTree>
+template <bool kOne>
+__device__ __forceinline__ int item_tokens(int tpt) { return kOne ? tpt : 2 * tpt; }
+
+template <bool kTree, bool kOne>
 __device__ __forceinline__ Seq load_seq(const Params& p, int s, uint32_t* bad) {
     const int a = __ldg(p.query_starts + s), b = __ldg(p.query_starts + s + 1);
     int ctx = __ldg(p.context_lens + s);
@@ -164,32 +175,31 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int s, uint32_t* bad) {
     }
     q.ctx = max(ctx, 0);
     if (bad && !kTree && q.n > q.ctx) *bad |= PKV_DEVERR_CONTEXT;
-    // n / (2 tpt) by the host's ceil(2^36 / (2 tpt)): exact below 2^28, then corrected
-    const int item_rows = 2 * p.tpt;
+    // n / tokens by the host's ceil(2^36 / tokens): exact below 2^28, then corrected
+    const int tokens = item_tokens<kOne>(p.tpt);
     q.full = static_cast<int>((static_cast<unsigned long long>(q.n) * p.item_magic) >> 36);
-    if (q.full * item_rows > q.n) --q.full;
-    q.rest = q.n - q.full * item_rows;
+    if (q.full * tokens > q.n) --q.full;
+    q.rest = q.n - q.full * tokens;
     return q;
 }
 
-// Costs of one head of a sequence: of the first i items, all of two full
-// tiles, i * (a + b i); of the smaller one behind them, last.
+// Costs of one head of a sequence: of the first i items, all full, i * (a + b i); of the smaller one behind them, last.
 struct Cost {
     long long a, last;
     int b;
     __device__ __forceinline__ long long first(int i) const { return i * (a + static_cast<long long>(b) * i); }
 };
 
-template <bool kTree>
+template <bool kTree, bool kOne>
 __device__ __forceinline__ Cost cost_of(const Seq& q, int tpt) {
+    constexpr int kOneCost = cost_one(kTree), kFull = kOne ? kOneCost : kCostTwo;
     Cost c;
-    // keys of item i of a prompt: ctx - n + (i + 1) * 2 tpt (fewer than that in
-    // a chunk longer than its context: then only the balance is off)
+    // keys of item i of a prompt: ctx - n + (i + 1) * its tokens (fewer than that
+    // in a chunk longer than its context: then only the balance is off)
     const long long keys = kTree ? q.ctx + static_cast<long long>(kKeys) : max(q.ctx - q.n, 0);
-    c.b = kTree ? 0 : kCostTwo * tpt;
-    c.a = kCostTwo * keys + kItemCost + c.b;
-    constexpr int kOne = cost_one(kTree);
-    c.last = q.rest ? (q.rest > tpt ? kCostTwo : kOne) * (kTree ? keys : static_cast<long long>(q.ctx)) + kItemCost : 0;
+    c.b = kTree ? 0 : kFull * item_tokens<kOne>(tpt) / 2;
+    c.a = kFull * keys + kItemCost + c.b;
+    c.last = q.rest ? (q.rest > tpt ? kCostTwo : kOneCost) * (kTree ? keys : static_cast<long long>(q.ctx)) + kItemCost : 0;
     return c;
 }
 
@@ -216,12 +226,12 @@ struct Item {
     __device__ __forceinline__ int cut_tiles() const { return max(nt, 1); }
 };
 
-template <bool kTree>
+template <bool kTree, bool kOne>
 __device__ __forceinline__ void set_item(const Params& p, Item& it) {
-    const int off = it.i * 2 * p.tpt;
+    const int off = it.i * item_tokens<kOne>(p.tpt);
     it.tok0 = it.q.tok0 + off;
-    it.ntok = min(2 * p.tpt, it.q.n - off);
-    it.two = it.ntok > p.tpt;
+    it.ntok = min(item_tokens<kOne>(p.tpt), it.q.n - off);
+    it.two = !kOne && it.ntok > p.tpt;
     it.pos0 = it.q.ctx - it.q.n + off;
     it.kend = kTree ? it.q.ctx : max(it.pos0 + it.ntok, 0);
     it.nct = (it.kend + kKeys - 1) / kKeys;
@@ -230,7 +240,7 @@ __device__ __forceinline__ void set_item(const Params& p, Item& it) {
 }
 
 // The loader's walk over its CTA's range: next() yields the pieces in order.
-template <bool kTree>
+template <bool kTree, bool kOne>
 struct Walk {
     const Params& p;
     Item it;
@@ -254,21 +264,21 @@ struct Walk {
         bool enter = first, step = !first;  // a sequence was entered; go on to another item
         if (first) {
             if (it.s >= p.num_seqs) return false;
-            set_item<kTree>(p, it);
+            set_item<kTree, kOne>(p, it);
             step = ta >= it.cut_tiles();  // the range starts behind this item
             first = false;
         }
 #pragma unroll 1
         while (enter || step) {
             if (enter) {
-                if (it.s + 1 < p.num_seqs) ahead = load_seq<kTree>(p, it.s + 1, nullptr);
+                if (it.s + 1 < p.num_seqs) ahead = load_seq<kTree, kOne>(p, it.s + 1, nullptr);
                 enter = false;
             }
             if (step) {
                 step = false;
                 ta = 0;
                 ++it.i;
-                if (it.i * 2 * p.tpt >= it.q.n) {
+                if (it.i * item_tokens<kOne>(p.tpt) >= it.q.n) {
                     it.i = 0;
                     if (it.q.n == 0 || ++it.h == p.hkv) {
                         it.h = 0;
@@ -280,7 +290,7 @@ struct Walk {
                 }
             }
         }
-        set_item<kTree>(p, it);
+        set_item<kTree, kOne>(p, it);
         if (it.s > s1 || (it.s == s1 && (it.h > h1 || (it.h == h1 && it.i > i1)))) return false;
         const bool last = it.s == s1 && it.h == h1 && it.i == i1;
         if (last && t1 <= ta) return false;
@@ -334,7 +344,7 @@ __device__ __forceinline__ int ring_v(bool two, int j, int count) { return two |
 // Every thread of the CTA: the ends of this CTA's range, and the description
 // of the item that its end cuts. Each half of the threads goes over all
 // sequences and finds one end.
-template <bool kTree>
+template <bool kTree, bool kOne>
 __device__ void plan(const Params& p, Misc& m) {
     constexpr int kHalf = kThreads / 2, kHalfWarps = kHalf / 32;
     const int e = threadIdx.x >= kHalf, tid = threadIdx.x - e * kHalf, lane = tid & 31, warp = tid >> 5;
@@ -345,9 +355,9 @@ __device__ void plan(const Params& p, Misc& m) {
     Seq seq0 = {};
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
-        const Seq q = load_seq<kTree>(p, s, &bad);
+        const Seq q = load_seq<kTree, kOne>(p, s, &bad);
         if (s == s0) seq0 = q;
-        const Cost c = cost_of<kTree>(q, p.tpt);
+        const Cost c = cost_of<kTree, kOne>(q, p.tpt);
         sum += (c.first(q.full) + c.last) * p.hkv;
     }
     if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
@@ -378,8 +388,8 @@ __device__ void plan(const Params& p, Misc& m) {
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
         Item it;
-        it.q = s == s0 ? seq0 : load_seq<kTree>(p, s, nullptr);
-        const Cost c = cost_of<kTree>(it.q, p.tpt);
+        it.q = s == s0 ? seq0 : load_seq<kTree, kOne>(p, s, nullptr);
+        const Cost c = cost_of<kTree, kOne>(it.q, p.tpt);
         const long long hc = c.first(it.q.full) + c.last;
         if (x >= at + hc * p.hkv) {
             at += hc * p.hkv;
@@ -403,7 +413,7 @@ __device__ void plan(const Params& p, Misc& m) {
         while (c.first(it.i) > off) --it.i;
 #pragma unroll 1
         while (it.i < it.q.full - (it.q.rest == 0) && c.first(it.i + 1) <= off) ++it.i;
-        set_item<kTree>(p, it);
+        set_item<kTree, kOne>(p, it);
         const long long start = x - off + c.first(it.i);
         const long long cost = it.i < it.q.full ? c.first(it.i + 1) - c.first(it.i) : c.last;
         const int t = cut_tile(x - start, cost, it.cut_tiles());
@@ -511,13 +521,15 @@ __device__ __forceinline__ void add_non_finite(const Params& p, const Piece& it,
     }
 }
 
-template <bool kTree>
+template <bool kTree, bool kOne>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kd,
             const __grid_constant__ CUtensorMap tm_vd, const __grid_constant__ Params p) {
+    using L = Smem<kOne>;
+    constexpr int kStages = L::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
-    Misc& m = *reinterpret_cast<Misc*>(smem + kSmemMisc);
+    Misc& m = *reinterpret_cast<Misc*>(smem + L::kMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem_base = smem_u32(smem);
     volatile int* abort_flag = &m.abort;
@@ -567,7 +579,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (warp == kWarpMma) tmem_alloc(smem_u32(&m.tmem), kTmemColumns);
     tc_fence_before();
     griddep_wait();  // launched early: the earlier kernels' results and the last call's partial results
-    plan<kTree>(p, m);
+    plan<kTree, kOne>(p, m);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m.tmem;
@@ -733,7 +745,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             uint32_t acc0 = t_o, acc1 = t_o;
             float f0 = 1.f, f1 = 0.f;
             bool has0 = count > 0, has1 = false;
-            if (it.two) {
+            if (!kOne && it.two) {
                 t_end = min(t_hi, it.ta + count);
                 prow += stream * kRows;
             } else {
@@ -764,7 +776,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 // The results leave through shared memory, 64 bytes of each of the warp's
                 // 32 rows at a time (two places in turn), so that a store covers 8 rows'
                 // 64 bytes where one from the accumulator's rows would touch 32 lines.
-                uint8_t* const staging = smem + kSmemOut + warp * kOutBytes;
+                uint8_t* const staging = smem + L::kOut + warp * kOutBytes;
                 auto chunk = [&](int place, int r, int c) {
                     return reinterpret_cast<uint4*>(staging + place * (kOutBytes / 2) + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
                 };
@@ -849,7 +861,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       if (warp == kWarpLoad) {
         // ---- loader: query tiles, then K and V tiles in the order of their use
         uint32_t ring = 0, n_q = 0, n_clean = 0, n_item = 0;
-        Walk<kTree> walk(p, m);
+        Walk<kTree, kOne> walk(p, m);
         const int blocks_per_tile = kKeys / p.bt;
         bool ok = true;
         // One piece is described ahead of the one that is loaded, and its query rows
@@ -909,7 +921,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     if (lane == 0) mbar_arrive(full);
                     full = smem_u32(&m.part_full[(n_clean + (j - masked0)) % kCleanBars]);
                 }
-                const uint32_t dst = smem_base + kSmemRing + st * kTileBytes;
+                const uint32_t dst = smem_base + L::kRing + st * kTileBytes;
                 const bool draft = kTree && t == it.nct;
                 const int boxes = draft ? (it.seq_n + 7) >> 3 : (min(kKeys, it.kend - t * kKeys) + p.bt - 1) / p.bt;
                 const uint32_t box_bytes = draft ? 2048 : p.bt * 256;
@@ -941,7 +953,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     __syncwarp();
                     if (lane < 2 * tiles) {
                         const int t = lane >> 1, panel = lane & 1;
-                        tma_load_5d(smem_base + kSmemQ + t * kTileBytes + panel * (kTileBytes / 2), &tm_q, 0, 0,
+                        tma_load_5d(smem_base + L::kQ + t * kTileBytes + panel * (kTileBytes / 2), &tm_q, 0, 0,
                                     it.tok0 + t * p.tpt, panel, it.h, smem_u32(&m.q_full));
                     }
                 }
@@ -966,7 +978,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const Piece* const piece = get_piece(n_item);
             if (!piece) break;
             const int count = uniform(piece->count);
-            const bool two = uniform(piece->two) != 0;
+            const bool two = !kOne && uniform(piece->two) != 0;
             const int cnt0 = uniform(piece->cnt[0]), cnt1 = uniform(piece->cnt[1]);
             const int masked0 = uniform(max(piece->first_masked - piece->ta, 0));  // first masked tile of the piece
             done_piece(n_item);
@@ -1006,8 +1018,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             auto issue_o = [&](uint32_t t_s, uint32_t dv, int k, bool accumulate) {
                 mma_ts<desc_high(2048), kIdescO>(t_s + kTmemO, t_s + k * 8, dv + ((k * 4096) >> 4), accumulate);
             };
-            auto tile_at = [&](uint32_t at) { return base + kSmemRing + (at % kStages) * kTileBytes; };
-            const uint32_t dq0 = desc_low(base + kSmemQ, 16), dq1 = two ? desc_low(base + kSmemQ + kTileBytes, 16) : dq0;
+            auto tile_at = [&](uint32_t at) { return base + L::kRing + (at % kStages) * kTileBytes; };
+            const uint32_t dq0 = desc_low(base + L::kQ, 16), dq1 = two ? desc_low(base + L::kQ + kTileBytes, 16) : dq0;
             // Two query tiles, both with a tile to come that every row sees in full: the
             // same steps in as little as it takes, since a scalar instruction of this
             // warp costs up to 10 cycles beside the softmax warps', and what is not
@@ -1017,7 +1029,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             ok = __all_sync(0xFFFFFFFFu, ok);
 #pragma unroll 1
             for (int turn = -2; ok && turn < turns; ++turn) {
-                if (turn == 0 && fast > 0) {
+                if (!kOne && turn == 0 && fast > 0) {
                     const uint32_t p0 = smem_u32(&m.p_full[0]), p1 = smem_u32(&m.p_full[1]);
                 bool ready = false;
 #pragma unroll 1
@@ -1086,14 +1098,14 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 const bool last_user = !two || (turn & 1);  // of a key tile
                 if (elect_one()) {
                     if (now.has_v) {
-                        const uint32_t dv = desc_low(base + kSmemRing + now.st_v * kTileBytes, 1024);
+                        const uint32_t dv = desc_low(base + L::kRing + now.st_v * kTileBytes, 1024);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) issue_o(t_s, dv, k, turn >= 2 || k > 0);
                         if (last_user) mma_commit(smem_u32(&m.kv_empty[now.st_v]));
                         if (!now.has_k) mma_commit(smem_u32(&m.o_full[turn & 1]));
                     }
                     if (now.has_k) {
-                        const uint32_t dk = desc_low(base + kSmemRing + now.st_k * kTileBytes, 16), dq = turn & 1 ? dq1 : dq0;
+                        const uint32_t dk = desc_low(base + L::kRing + now.st_k * kTileBytes, 16), dq = turn & 1 ? dq1 : dq0;
 #pragma unroll
                         for (int k = 0; k < 8; ++k) issue_s(t_s, dq, dk, k);
                         mma_commit(smem_u32(&m.s_full[turn & 1]));
@@ -1126,7 +1138,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 ok = __all_sync(0xFFFFFFFFu, wait_for(smem_u32(&m.part_full[n_clean % kCleanBars]),
                                                        (n_clean / kCleanBars) & 1, abort_flag, p.err));
                 if (!ok) break;
-                uint8_t* tile = smem + kSmemRing + st * kTileBytes;
+                uint8_t* tile = smem + L::kRing + st * kTileBytes;
 #pragma unroll 1
                 for (int r = 0; r < 2; ++r) {
                     const int row = half * 64 + r * 32 + lane;
