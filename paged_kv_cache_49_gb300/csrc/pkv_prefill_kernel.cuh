@@ -57,9 +57,10 @@ constexpr uint32_t kTmemO = 256;  // S0, S1, O0, O1 of 128 columns each
 // Cost units of the work line: one key of an item's two tiles is 8 (3,400
 // cycles for a key tile). One tile alone costs 2,300 where the products bound
 // it, but as much as two where its keys' bytes do, as over the long contexts
-// of trees. kItemCost: an item's fixed work.
-constexpr int kCostTwo = 8, kItemCost = 8 * 200;
+// of trees. An item's fixed work is 7,000 cycles (of a tree 4,800).
+constexpr int kCostTwo = 8;
 __host__ __device__ constexpr int cost_one(bool tree) { return tree ? 8 : 6; }
+__host__ __device__ constexpr int cost_item(bool tree) { return tree ? 8 * 200 : 8 * 290; }
 constexpr int kSnap = 8 * 256;      // a cut this near an item's end moves there
 constexpr int kWhole = 8 * 768;     // an item of this cost is never cut
 constexpr int kMinRange = 8 * 256;  // least cost of a CTA's range
@@ -192,7 +193,7 @@ struct Cost {
 
 template <bool kTree, bool kOne>
 __device__ __forceinline__ Cost cost_of(const Seq& q, int tpt) {
-    constexpr int kOneCost = cost_one(kTree), kFull = kOne ? kOneCost : kCostTwo;
+    constexpr int kOneCost = cost_one(kTree), kFull = kOne ? kOneCost : kCostTwo, kItemCost = cost_item(kTree);
     Cost c;
     // keys of item i of a prompt: ctx - n + (i + 1) * its tokens (fewer than that
     // in a chunk longer than its context: then only the balance is off)
@@ -1088,23 +1089,33 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 }
                 const Step now = step_at(turn);
                 if (!now.has_v && !now.has_k) continue;
-                if (now.has_v) ok = wait_for(now.bar_v, now.par_v, abort_flag, p.err);
-                if (ok && now.has_k) ok = wait_for(now.bar_k, now.par_k, abort_flag, p.err);
-                if (ok && now.has_v) ok = wait_for(now.bar_p, now.par_p, abort_flag, p.err);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                tc_fence_after();
                 const uint32_t t_s = tm + (turn & 1) * 128;
                 const bool last_user = !two || (turn & 1);  // of a key tile
-                if (elect_one()) {
-                    if (now.has_v) {
+                if (now.has_v) {
+                    ok = wait_for(now.bar_v, now.par_v, abort_flag, p.err);
+                    // (one-tile items are bound by their loads: there the product that
+                    // frees a stage does not wait for the next key tile)
+                    if (!kOne && ok && now.has_k) ok = wait_for(now.bar_k, now.par_k, abort_flag, p.err);
+                    if (ok) ok = wait_for(now.bar_p, now.par_p, abort_flag, p.err);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
                         const uint32_t dv = desc_low(base + L::kRing + now.st_v * kTileBytes, 1024);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) issue_o(t_s, dv, k, turn >= 2 || k > 0);
                         if (last_user) mma_commit(smem_u32(&m.kv_empty[now.st_v]));
                         if (!now.has_k) mma_commit(smem_u32(&m.o_full[turn & 1]));
                     }
-                    if (now.has_k) {
+                    __syncwarp();
+                }
+                if (now.has_k) {
+                    if (kOne || !now.has_v) {
+                        ok = __all_sync(0xFFFFFFFFu, wait_for(now.bar_k, now.par_k, abort_flag, p.err));
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    if (elect_one()) {
                         const uint32_t dk = desc_low(base + L::kRing + now.st_k * kTileBytes, 16), dq = turn & 1 ? dq1 : dq0;
 #pragma unroll
                         for (int k = 0; k < 8; ++k) issue_s(t_s, dq, dk, k);
@@ -1112,8 +1123,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                         if (last_user) mma_commit(smem_u32(&m.kv_empty[now.st_k]));
                         if (last_user && now.last_k) mma_commit(smem_u32(&m.q_empty));
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             n_p0 += cnt0;
             n_p1 += cnt1;
