@@ -861,9 +861,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
       if (warp == kWarpLoad) {
         // ---- loader: query tiles, then K and V tiles in the order of their use
-        uint32_t ring = 0, n_q = 0, n_clean = 0, n_item = 0;
+        uint32_t stage = 0, phase = 0, n_q = 0, n_clean = 0, n_item = 0;
         Walk<kTree, kOne> walk(p, m);
-        const int blocks_per_tile = kKeys / p.bt;
+        const int bt_shift = 31 - __clz(p.bt), tile_shift = 7 - bt_shift;
+        const int blocks_per_tile = 1 << tile_shift, block_rows = p.hkv << (bt_shift - 3);  // row groups of a block
         bool ok = true;
         // One piece is described ahead of the one that is loaded, and its query rows
         // are brought into L2 meanwhile.
@@ -886,81 +887,81 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             more = walk.next();
             describe(more);
             if (!ok) break;
-            const int ta = it.ta, count = it.count;
             if (more && lane < 4 && (walk.it.two || lane < 2))
                 tma_prefetch_5d(&tm_q, 0, 0, walk.it.tok0 + (lane >> 1) * p.tpt, lane & 1, walk.it.h);
+            const int ta = it.ta, count = it.count;
             if (count == 0) continue;
+            // What a load needs, in registers: at 1,500 cycles a load, as a plain loop
+            // took, the loader bounds the kernel (two loads a key tile).
+            const bool two = !kOne && it.two;
             const int masked0 = max(it.first_masked, ta) - ta;  // first masked tile of the piece
+            const int head = it.h, draft_tile = kTree ? it.nct - ta : count, draft_row = it.seq_tok0 + lane * 8;
+            const int blocks = min(count, it.nct - ta) > 0 ? (it.kend - ta * kKeys + p.bt - 1) >> bt_shift : 0;  // from the piece's first on
+            const int draft_boxes = (it.seq_n + 7) >> 3, head_row = head << (bt_shift - 3);
+            const int32_t* const table = p.block_tables + static_cast<long long>(it.s) * p.max_blocks + (ta << tile_shift);
             // this lane's block of a tile, read from the table a tile early; and its
             // box's last coordinate in the map
             auto table_entry = [&](int j) {
-                const int idx = (ta + j) * blocks_per_tile + lane;
-                if (j >= count || lane >= blocks_per_tile || idx * p.bt >= it.kend) return 0;
-                return __ldg(p.block_tables + static_cast<long long>(it.s) * p.max_blocks + idx);
+                const int idx = (j << tile_shift) + lane;
+                return j < count && lane < blocks_per_tile && idx < blocks ? __ldg(table + idx) : 0;
             };
             auto coordinate = [&](int j, int blk) {
-                if (kTree && ta + j == it.nct) return it.seq_tok0 + lane * 8;
-                if (blk < 0 || blk >= p.num_blocks) {
+                if (kTree && j == draft_tile) return draft_row;
+                if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
                     atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
                     blk = 0;
                 }
-                return (blk * p.hkv + it.h) * (p.bt >> 3);
+                return blk * block_rows + head_row;
             };
             int blk_next = table_entry(0), coord_k = 0, coord_v = 0;  // of K's tile; of the V tile to come
-            auto load = [&](bool is_v, int j, int pos, int coord) {
-                const uint32_t at = ring + pos;
-                const uint32_t st = at % kStages, ph = (at / kStages) & 1;
-                ok = wait_for(smem_u32(&m.kv_empty[st]), ph ^ 1, abort_flag, p.err);
+#pragma unroll 1
+            for (int pos = 0; pos < 2 * count; ++pos) {
+                const RingEntry en = ring_entry(two, pos, count);
+                if (!en.is_v) {
+                    const int c = coordinate(en.j, blk_next);
+                    blk_next = table_entry(en.j + 1);
+                    coord_v = two || pos == 0 ? c : coord_k;
+                    coord_k = c;
+                }
+                const int coord = en.is_v ? coord_v : coord_k;
+                if (en.is_v) coord_v = coord_k;
+                const bool draft = kTree && en.j == draft_tile;
+                const int boxes = draft ? draft_boxes : min(blocks - (en.j << tile_shift), blocks_per_tile);
+                const uint32_t box_shift = draft ? 11 : bt_shift + 8;
+                uint32_t full = smem_u32(&m.kv_full[stage]);
+                ok = wait_for(smem_u32(&m.kv_empty[stage]), phase ^ 1, abort_flag, p.err);
                 ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) return;
-                const int t = ta + j;
-                uint32_t full = smem_u32(&m.kv_full[st]);
-                if (is_v && j >= masked0) {
+                if (!ok) break;
+                if (en.is_v && en.j >= masked0) {
                     // a value tile to be cleaned lands on a barrier of its own: the
                     // cleaning warps see no other tile, and could not follow the
                     // ring's phases
                     if (lane == 0) mbar_arrive(full);
-                    full = smem_u32(&m.part_full[(n_clean + (j - masked0)) % kCleanBars]);
+                    full = smem_u32(&m.part_full[n_clean % kCleanBars]);
+                    ++n_clean;
                 }
-                const uint32_t dst = smem_base + L::kRing + st * kTileBytes;
-                const bool draft = kTree && t == it.nct;
-                const int boxes = draft ? (it.seq_n + 7) >> 3 : (min(kKeys, it.kend - t * kKeys) + p.bt - 1) / p.bt;
-                const uint32_t box_bytes = draft ? 2048 : p.bt * 256;
-                if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_bytes);
-                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(full, boxes << box_shift);
                 if (lane < boxes) {
-                    if (draft) tma_load_4d(dst + lane * box_bytes, is_v ? &tm_vd : &tm_kd, 0, coord, 0, it.h, full);
-                    else tma_load_4d(dst + lane * box_bytes, is_v ? &tm_v : &tm_k, 0, 0, 0, coord, full);
+                    const uint32_t dst = smem_base + L::kRing + stage * kTileBytes + (lane << box_shift);
+                    if (draft) tma_load_4d(dst, en.is_v ? &tm_vd : &tm_kd, 0, coord, 0, head, full);
+                    else tma_load_4d(dst, en.is_v ? &tm_v : &tm_k, 0, 0, 0, coord, full);
                 }
-            };
-#pragma unroll 1
-            for (int pos = 0; ok && pos < 2 * count; ++pos) {
-                const RingEntry en = ring_entry(it.two, pos, count);
-                if (!en.is_v) {
-                    const int c = coordinate(en.j, blk_next);
-                    blk_next = table_entry(en.j + 1);
-                    coord_v = it.two || pos == 0 ? c : coord_k;
-                    coord_k = c;
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
                 }
-                load(en.is_v, en.j, pos, en.is_v ? coord_v : coord_k);
-                if (en.is_v) coord_v = coord_k;
-                if (ok && pos == 0) {
+                if (pos == 0) {
                     ok = wait_for(smem_u32(&m.q_empty), (n_q & 1) ^ 1, abort_flag, p.err);
                     ++n_q;
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    const int tiles = it.two ? 2 : 1;
-                    if (lane == 0) mbar_arrive_expect_tx(smem_u32(&m.q_full), tiles * 2 * 128 * p.group * p.tpt);
-                    __syncwarp();
-                    if (lane < 2 * tiles) {
-                        const int t = lane >> 1, panel = lane & 1;
-                        tma_load_5d(smem_base + L::kQ + t * kTileBytes + panel * (kTileBytes / 2), &tm_q, 0, 0,
-                                    it.tok0 + t * p.tpt, panel, it.h, smem_u32(&m.q_full));
-                    }
+                    const int halves = two ? 4 : 2;
+                    if (lane == 0) mbar_arrive_expect_tx(smem_u32(&m.q_full), halves * 128 * p.group * p.tpt);
+                    if (lane < halves)
+                        tma_load_5d(smem_base + L::kQ + lane * (kTileBytes / 2), &tm_q, 0, 0, it.tok0 + (lane >> 1) * p.tpt, lane & 1,
+                                    head, smem_u32(&m.q_full));
                 }
             }
-            ring += 2 * count;
-            n_clean += max(count - masked0, 0);
         }
     } else if (warp == kWarpMma) {
         // ---- tensor core: one elected thread issues every product, P V of a
