@@ -285,6 +285,10 @@ pkv_status pkv_attn_decode_ex(const void* q, const void* k_cache, const void* v_
  *                   slot past the pool is skipped and sets PKV_DEVERR_SLOT
  *   q_out         : device bf16 [num_tokens][num_q_heads][head_dim]; must not
  *                   overlap q, k or v
+ *   k_out         : NULL, or device bf16 [num_tokens][num_kv_heads][head_dim]
+ *                   for the normed, rotated keys of every row, padding
+ *                   included -- drafted tokens' keys, which pkv_attn_tree reads
+ *                   before any of them is appended; must not overlap q, k or v
  *   k_cache, v_cache, block_tokens : as in pkv_append_ex
  * head_dim: a multiple of 8 up to 256; rotary_dim: a multiple of 16 up to
  * head_dim (PKV_EUNSUPPORTED otherwise). bf16 pointers and cos_sin are 16-byte
@@ -296,7 +300,7 @@ pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
                                    int max_positions, int rotary_dim, int interleaved,
                                    const int32_t* positions, const int64_t* slot_mapping, int num_tokens,
                                    int num_q_heads, int num_kv_heads, int head_dim, void* q_out,
-                                   void* k_cache, void* v_cache, int num_blocks, int block_tokens,
+                                   void* k_out, void* k_cache, void* v_cache, int num_blocks, int block_tokens,
                                    uint32_t* device_error, void* stream);
 
 /*

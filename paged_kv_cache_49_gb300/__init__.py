@@ -13,7 +13,7 @@ from ._native import (  # noqa: F401
     new_error_word, qk_norm_rope_append, read_device_error, rope_table, step_layout, tree_masks,
 )
 from .engine import (  # noqa: F401
-    CASCADE_MIN_SAVED_BYTES, HostStep, PagedKVEngine, StepBuffers, bf16_from_bits, bits_from_bf16, cascade_saved_bytes,
-    shared_prefix_groups,
+    CASCADE_MIN_SAVED_BYTES, DraftBuffers, HostStep, PagedKVEngine, PromptBuffers, RopeSpec, StepBuffers, bf16_from_bits,
+    bits_from_bf16, cascade_saved_bytes, shared_prefix_groups,
 )
 from .graphs import GraphedDecoder, default_buckets  # noqa: F401

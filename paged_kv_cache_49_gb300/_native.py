@@ -148,7 +148,7 @@ def _load() -> ctypes.CDLL:
         "pkv_attn_tree": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, vp,
                                 sz, vp, vp]),
         "pkv_qk_norm_rope_append": (i32, [vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, i32, i32, i32, vp, vp, i32, i32,
-                                          i32, i32, vp, vp, vp, i32, i32, vp, vp]),
+                                          i32, i32, vp, vp, vp, vp, i32, i32, vp, vp]),
         "pkv_decode_step_host": (i32, [vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz, vp, vp,
                                        vp, vp]),
     }
@@ -692,12 +692,15 @@ def _need_rows(device: int, t: torch.Tensor, name: str, T: int, h: int, d: int) 
 
 
 def qk_norm_rope_append(q, k, v, cos_sin, positions, slot_mapping, k_cache, v_cache, q_weight=None, k_weight=None,
-                        eps: float = 1e-6, interleaved: bool = False, q_out=None, device_error=None, stream=None):
+                        eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None, device_error=None,
+                        stream=None):
     """RMS norm of every head of q [T, Hq, D] and k [T, Hkv, D] (skipped where
     the weight is None), rotation by cos_sin[positions] (fp32 [positions,
     rotary_dim], see rope_table(); None: no rotation), and the append of k and
     v to slot_mapping's slots of the caches. q, k, v may be views of one fused
-    projection. Returns the normed, rotated queries [T, Hq, D]."""
+    projection. k_out [T, Hkv, D], where given, receives the normed, rotated
+    keys of every row (drafted tokens: slot -1 and k_out). Returns the normed,
+    rotated queries [T, Hq, D]."""
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [T, Hq, D] and caches [NB, Hkv, block_tokens, D]")
     device = q.get_device()
@@ -731,6 +734,10 @@ def qk_norm_rope_append(q, k, v, cos_sin, positions, slot_mapping, k_cache, v_ca
         _need_all(device, ((q_out, _BF16, "q_out"),))
         if q_out.shape != q.shape:
             raise ValueError("q_out must be shaped like q")
+    if k_out is not None:
+        _need_all(device, ((k_out, _BF16, "k_out"),))
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must be shaped like k")
     if device_error is not None:
         _need_all(device, ((device_error, _I32, "device_error"),))
     with _launch_on(device, stream) as st:
@@ -738,7 +745,7 @@ def qk_norm_rope_append(q, k, v, cos_sin, positions, slot_mapping, k_cache, v_ca
             q_out = torch.empty((T, hq, d), dtype=_BF16, device=q.device)
         _check(_lib.pkv_qk_norm_rope_append(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, qw, kw, float(eps), cs,
                                             max_positions, rotary, 1 if interleaved else 0, ps,
-                                            slot_mapping.data_ptr(), T, hq, hkv, d, q_out.data_ptr(),
+                                            slot_mapping.data_ptr(), T, hq, hkv, d, q_out.data_ptr(), _ptr(k_out),
                                             k_cache.data_ptr(), v_cache.data_ptr(), nb, bt, _ptr(device_error), st),
                "pkv_qk_norm_rope_append")
     return q_out

@@ -38,7 +38,7 @@ struct Params {
     const float* cos_sin;
     const int32_t* positions;
     const int64_t* slots;
-    __nv_bfloat16 *q_out, *k_cache, *v_cache;
+    __nv_bfloat16 *q_out, *k_out, *k_cache, *v_cache;
     uint32_t* err;
     long long slot_limit;
     float eps;
@@ -179,6 +179,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) qk_write_kernel(const 
         }
         if (dst && live0) *reinterpret_cast<uint4*>(dst + at0) = u[0];
         if (dst && live1) *reinterpret_cast<uint4*>(dst + at1) = u[1];
+        if (p.k_out && is_k && mine) {
+            dst = p.k_out + (static_cast<long long>(tok) * p.hkv + (h - p.hq)) * p.dim;
+            if (live0) *reinterpret_cast<uint4*>(dst + at0) = u[0];
+            if (live1) *reinterpret_cast<uint4*>(dst + at1) = u[1];
+        }
         tok = tok2;
         h = h2;
     }
@@ -223,7 +228,7 @@ pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
                                    int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
                                    const float* cos_sin, int max_positions, int rotary_dim, int interleaved,
                                    const int32_t* positions, const int64_t* slot_mapping, int num_tokens,
-                                   int num_q_heads, int num_kv_heads, int head_dim, void* q_out, void* k_cache,
+                                   int num_q_heads, int num_kv_heads, int head_dim, void* q_out, void* k_out, void* k_cache,
                                    void* v_cache, int num_blocks, int block_tokens, uint32_t* device_error,
                                    void* stream) {
     if (block_tokens != 8 && block_tokens != 16 && block_tokens != 32 && block_tokens != 64) return PKV_EUNSUPPORTED;
@@ -240,7 +245,7 @@ pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
     if (q_stride < static_cast<int64_t>(num_q_heads) * head_dim || k_stride < static_cast<int64_t>(num_kv_heads) * head_dim ||
         v_stride < static_cast<int64_t>(num_kv_heads) * head_dim || q_stride % 8 || k_stride % 8 || v_stride % 8)
         return PKV_EINVAL;
-    for (const void* ptr : {q, k, v, q_weight, k_weight, static_cast<const void*>(cos_sin), static_cast<const void*>(q_out),
+    for (const void* ptr : {q, k, v, q_weight, k_weight, static_cast<const void*>(cos_sin), static_cast<const void*>(q_out), static_cast<const void*>(k_out),
                             static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
         if (!aligned16(ptr)) return PKV_EINVAL;
     int lanes = 4;
@@ -259,6 +264,7 @@ pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
     p.positions = positions;
     p.slots = slot_mapping;
     p.q_out = static_cast<__nv_bfloat16*>(q_out);
+    p.k_out = static_cast<__nv_bfloat16*>(k_out);
     p.k_cache = static_cast<__nv_bfloat16*>(k_cache);
     p.v_cache = static_cast<__nv_bfloat16*>(v_cache);
     p.err = device_error;

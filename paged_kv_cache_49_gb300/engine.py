@@ -10,6 +10,7 @@ copy, append, attention.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 import numpy as np
@@ -86,6 +87,42 @@ class StepBuffers:
         return int(self.pairs.shape[0])
 
 
+@dataclass
+class RopeSpec:
+    """How a layer's queries and keys enter the cache: rotation by a table of
+    rope_table() and the heads' norm weights (None: no norm)."""
+    cos_sin: torch.Tensor
+    q_weight: torch.Tensor | None = None
+    k_weight: torch.Tensor | None = None
+    eps: float = 1e-6
+    interleaved: bool = False
+
+
+@dataclass
+class PromptBuffers:
+    """Device inputs of one prefill call: packed rows of several sequences."""
+    seq_ids: list
+    counts: list
+    positions: torch.Tensor   # int32 [T]
+    tables: torch.Tensor      # int32 [B, W]
+    ctx: torch.Tensor         # int32 [B], the chunk included
+    starts: torch.Tensor      # int32 [B + 1]
+    slots: torch.Tensor       # int64 [T]
+
+
+@dataclass
+class DraftBuffers:
+    """Device inputs of one verification step of drafted trees."""
+    seq_ids: list
+    counts: list
+    positions: torch.Tensor   # int32 [T]
+    tables: torch.Tensor      # int32 [B, W]
+    ctx: torch.Tensor         # int32 [B], the drafts not included
+    starts: torch.Tensor      # int32 [B + 1]
+    masks: torch.Tensor       # int64 [T]
+    slots: torch.Tensor       # int64 [T], all -1: nothing is appended yet
+
+
 class PagedKVEngine:
     def __init__(self, num_blocks: int, num_q_heads: int, num_kv_heads: int, head_dim: int = 128,
                  device="cuda", free_order=None, block_tokens: int = nat.BLOCK_TOKENS, incremental: bool = False,
@@ -132,6 +169,117 @@ class PagedKVEngine:
         st = torch.tensor(slots, dtype=torch.int64).to(self.device, non_blocking=True)
         nat.append(k, v, st, self.k_cache, self.v_cache, self.error, stream)
         return slots
+
+    # ---- prompts and drafted tokens -------------------------------------------
+    def _on(self, stream):
+        """A context in which `stream` (default: the current one) is current, so
+        that what is allocated inside belongs to it."""
+        if stream is None:
+            return contextlib.nullcontext()
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        return torch.cuda.stream(stream)
+
+    def prepare_prefill(self, seq_ids, counts, first=None) -> PromptBuffers:
+        """Host bookkeeping of a prefill call: sequence seq_ids[i] brings its next
+        counts[i] prompt tokens, from position first[i] on (default: each
+        prompt's last counts[i] tokens, a whole prompt where that is all of
+        them). Their slots lie in the pages that admission reserved."""
+        seq_ids, counts = list(seq_ids), [int(c) for c in counts]
+        if first is None:
+            first = [self.bm.context_len(s) - c for s, c in zip(seq_ids, counts)]
+        if len(seq_ids) != len(counts) or len(first) != len(counts):
+            raise ValueError("one count and one first position per sequence")
+        slots, positions = [], []
+        for s, f, c in zip(seq_ids, first, counts):
+            slots += self.bm.slots(s, f, c) if c else []
+            positions += range(f, f + c)
+        return PromptBuffers(*self._rows(seq_ids, counts, [f + c for f, c in zip(first, counts)], positions),
+                             slots=torch.tensor(slots, dtype=torch.int64).to(self.device))
+
+    def _rows(self, seq_ids, counts, context_lens, positions):
+        if not seq_ids:
+            raise ValueError("at least one sequence")
+        tables, _ = self.bm.batch_tables(seq_ids, max(1, max(len(self.bm.table(s)) for s in seq_ids)))
+        starts = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        ints = lambda x: torch.tensor(x, dtype=torch.int32).to(self.device)
+        return seq_ids, counts, ints(positions), tables.to(self.device), ints(context_lens), torch.from_numpy(starts).to(self.device)
+
+    def run_prefill(self, pb: PromptBuffers, q, k, v, scale: float, workspace, rope=None, out=None, stream=None):
+        """The device part: the chunk's keys and values into the cache, then
+        causal attention of its rows. q [T, Hq, D], k, v [T, Hkv, D] (bf16 on the
+        device), packed in pb's order."""
+        with self._on(stream):
+            if rope is None:
+                nat.append(k, v, pb.slots, self.k_cache, self.v_cache, self.error)
+            else:
+                q = nat.qk_norm_rope_append(q, k, v, rope.cos_sin, pb.positions, pb.slots, self.k_cache, self.v_cache,
+                                            q_weight=rope.q_weight, k_weight=rope.k_weight, eps=rope.eps,
+                                            interleaved=rope.interleaved, device_error=self.error)
+            return nat.attn_prefill(q, self.k_cache, self.v_cache, pb.tables, pb.ctx, pb.starts, scale, out=out,
+                                    workspace=workspace)
+
+    def prepare_drafts(self, seq_ids, parents) -> DraftBuffers:
+        """Host bookkeeping of a verification step: sequence seq_ids[i] has the
+        drafted tree parents[i] (see tree_masks()). A draft's position follows
+        its parent's, or the context. Nothing is reserved or written."""
+        seq_ids, parents = list(seq_ids), [list(p) for p in parents]
+        ctx = [self.bm.context_len(s) for s in seq_ids]
+        masks, positions = [], []
+        for c, tree in zip(ctx, parents):
+            masks += nat.tree_masks(tree)
+            depth: list[int] = []
+            for p in tree:
+                depth.append(depth[p] + 1 if p >= 0 else 0)
+            positions += [c + d for d in depth]
+        rows = self._rows(seq_ids, [len(p) for p in parents], ctx, positions)
+        return DraftBuffers(*rows, masks=torch.tensor(masks, dtype=torch.int64).to(self.device),
+                            slots=torch.full((len(masks),), -1, dtype=torch.int64, device=self.device))
+
+    def run_drafts(self, db: DraftBuffers, q, k, v, scale: float, workspace, rope=None, out=None, stream=None):
+        """The device part: (attention of the drafts, their keys as the cache would
+        hold them); the cache stays as it was."""
+        with self._on(stream):
+            if rope is not None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+                q = nat.qk_norm_rope_append(q, k, v, rope.cos_sin, db.positions, db.slots, self.k_cache, self.v_cache,
+                                            q_weight=rope.q_weight, k_weight=rope.k_weight, eps=rope.eps,
+                                            interleaved=rope.interleaved, k_out=k_out, device_error=self.error)
+                k = k_out
+            out = nat.attn_tree(q, k, v.contiguous(), db.masks, self.k_cache, self.v_cache, db.tables, db.ctx, db.starts,
+                                scale, out=out, workspace=workspace)
+        return out, k
+
+    def accept_drafts(self, db: DraftBuffers, paths, k, v, stream=None):
+        """Append the accepted drafts, paths[i] = the chosen drafts of sequence i in
+        order, root first; k as run_drafts returned it. Returns the slots in
+        draft order, -1 for the drafts that were not accepted. Where the manager
+        refuses a token (PoolExhausted, ReservationExceeded), the drafts before
+        it are appended all the same and the error is raised."""
+        paths = [[int(x) for x in p] for p in paths]
+        if len(paths) != len(db.counts) or any(len(set(p)) != len(p) or any(not 0 <= x < n for x in p)
+                                               for p, n in zip(paths, db.counts)):
+            raise ValueError("one path per sequence, of different drafts of its own")
+        starts = np.concatenate([[0], np.cumsum(db.counts)])
+        slots = np.full(int(starts[-1]), -1, np.int64)
+        pairs, refused = [], None
+        for d in range(max((len(p) for p in paths), default=0)):
+            rows = [i for i, p in enumerate(paths) if len(p) > d]
+            try:
+                got, cow = self.bm.prepare_append([db.seq_ids[i] for i in rows])
+            except nat.PkvError as e:
+                refused = e
+                break
+            pairs += cow
+            for i, slot in zip(rows, got):
+                slots[starts[i] + paths[i][d]] = slot
+        with self._on(stream):
+            if pairs:
+                nat.block_copy(self.k_cache, self.v_cache, torch.tensor(pairs, dtype=torch.int32).to(self.device), self.error)
+            nat.append(k, v.contiguous(), torch.from_numpy(slots).to(self.device), self.k_cache, self.v_cache, self.error)
+        if refused is not None:
+            raise refused
+        return slots.tolist()
 
     def replay_events(self, w, with_content: bool = True):
         """Apply a workload's admit / fork / history events; history appends

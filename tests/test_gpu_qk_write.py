@@ -48,9 +48,10 @@ def _run(pkv, T, hq, hkv, d, rot, norm, interleaved, bt, padding=(), fused=True,
     vc = kc.clone()
     err = pkv.new_error_word()
     w = [None if x is None else pkv.bf16_from_bits(x).cuda() for x in (wq, wk)]
+    k_out = torch.full((T, hkv, d), 5.0, dtype=torch.bfloat16, device="cuda") if seed % 2 else None
     q = pkv.qk_norm_rope_append(dev["q"], dev["k"], dev["v"], table, torch.from_numpy(positions).cuda(),
                                 torch.from_numpy(slots).cuda(), kc, vc, q_weight=w[0], k_weight=w[1], eps=1e-5,
-                                interleaved=interleaved, device_error=err, stream=stream)
+                                interleaved=interleaved, k_out=k_out, device_error=err, stream=stream)
     torch.cuda.synchronize()
     assert pkv.read_device_error(err) == 0
     cs = table.cpu().numpy() if rot else None
@@ -61,6 +62,9 @@ def _run(pkv, T, hq, hkv, d, rot, norm, interleaved, bt, padding=(), fused=True,
     kb, vb = pkv.bits_from_bf16(kc), pkv.bits_from_bf16(vc)
     _near(kb[blk, :, r], po.norm_rope(bits["k"], wk, 1e-5, cs, at, interleaved)[kept])
     assert np.array_equal(vb[blk, :, r], bits["v"][kept])
+    if k_out is not None:  # every row's keys, padding included
+        _near(pkv.bits_from_bf16(k_out), po.norm_rope(bits["k"], wk, 1e-5, cs, at, interleaved))
+        assert np.array_equal(pkv.bits_from_bf16(k_out)[kept], kb[blk, :, r])
     untouched = np.ones((nb, bt), bool)
     untouched[blk, r] = False
     three = np.uint16(0x4040)

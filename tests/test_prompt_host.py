@@ -57,20 +57,20 @@ def test_tree_refusals(nat, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(q=None), "EINVAL"), (dict(v=None), "EINVAL"), (dict(slots=None), "EINVAL"), (dict(qo=None), "EINVAL"),
     (dict(table=None), "EINVAL"), (dict(pos=None), "EINVAL"), (dict(mp=0), "EINVAL"), (dict(qs=8 * 128 - 8), "EINVAL"),
-    (dict(ks=2 * 128 + 4), "EINVAL"), (dict(vs=0), "EINVAL"), (dict(q=P + 2), "EINVAL"), (dict(w=P + 8), "EINVAL"),
+    (dict(ks=2 * 128 + 4), "EINVAL"), (dict(vs=0), "EINVAL"), (dict(q=P + 2), "EINVAL"), (dict(w=P + 8), "EINVAL"), (dict(ko=P + 8), "EINVAL"),
     (dict(eps=-1.0), "EINVAL"), (dict(eps=float("nan")), "EINVAL"), (dict(tokens=-1), "EINVAL"),
     (dict(d=12), "EUNSUPPORTED"), (dict(d=264), "EUNSUPPORTED"), (dict(rot=8), "EUNSUPPORTED"),
     (dict(rot=144), "EUNSUPPORTED"), (dict(bt=24), "EUNSUPPORTED"), (dict(tokens=0), "OK"),
 ])
 def test_write_refusals(nat, kw, status):
     a = dict(q=P, qs=12 * 128, ks=12 * 128, v=P, vs=12 * 128, w=None, eps=1e-6, table=P, mp=100, rot=128, pos=P,
-             slots=P, tokens=5, d=128, qo=P, bt=16)
+             slots=P, tokens=5, d=128, qo=P, ko=None, bt=16)
     a.update(kw)
     if a["d"] > 128:
         a.update(qs=12 * a["d"], ks=12 * a["d"], vs=12 * a["d"])
     assert nat.lib.pkv_qk_norm_rope_append(a["q"], a["qs"], P, a["ks"], a["v"], a["vs"], a["w"], None, a["eps"],
                                            a["table"], a["mp"], a["rot"], 0, a["pos"], a["slots"], a["tokens"], 8, 2,
-                                           a["d"], a["qo"], P, P, 10, a["bt"], None, None) == getattr(nat, "PKV_" + status)
+                                           a["d"], a["qo"], a["ko"], P, P, 10, a["bt"], None, None) == getattr(nat, "PKV_" + status)
 
 
 def test_binding_refusals(nat):
