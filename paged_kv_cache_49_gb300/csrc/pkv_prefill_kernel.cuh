@@ -373,7 +373,7 @@ __device__ void plan(const Params& p, Misc& m) {
     if (threadIdx.x == 0) p.splits[blockIdx.x].ntiles = 0;
     __syncthreads();
     long long before = incl - sum, total = 0;
-#pragma unroll 1
+#pragma unroll
     for (int w = 0; w < kHalfWarps; ++w) {
         const long long v = m.scan[e * kHalfWarps + w];
         if (w < warp) before += v;
@@ -774,74 +774,75 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 } else if (valid && (it.two || stream == 0)) {
                     p.part_ml[part_row0 + lane] = st;
                 }
-                // The results leave through shared memory, 64 bytes of each of the warp's
-                // 32 rows at a time (two places in turn), so that a store covers 8 rows'
-                // 64 bytes where one from the accumulator's rows would touch 32 lines.
+                // The results leave through shared memory, 128 bytes of each of the warp's
+                // 32 rows at a time, so that a store covers whole lines of 4 rows where one
+                // from the accumulator's rows would touch 32 lines. 64 columns a turn: the
+                // turns' latencies are what an item's end waits for.
                 uint8_t* const staging = smem + L::kOut + warp * kOutBytes;
-                auto chunk = [&](int place, int r, int c) {
-                    return reinterpret_cast<uint4*>(staging + place * (kOutBytes / 2) + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-                };
-                const int r0 = lane >> 2, c0 = lane & 3;  // the lane's rows r0 + 8 k and its 16 bytes of each
-                int orow[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) orow[k] = __shfl_sync(0xFFFFFFFFu, out_row, r0 + 8 * k);
+                auto chunk = [&](int r, int c) { return reinterpret_cast<uint4*>(staging + r * 128 + ((c ^ (r & 7)) << 4)); };
+                const int r0 = lane >> 3, c0 = lane & 7;  // the lane's rows r0 + 4 k and its 16 bytes of each
                 const uint64_t f0x2 = pair(f0, f0), f1x2 = pair(f1, f1);
 #pragma unroll 1
-                for (int col = col_lo; col < col_hi; col += 32) {
-                    uint32_t r[32];
-                    tmem_ld32(r, acc0 + col);
-                    tmem_wait_ld(r);
+                for (int col = col_lo; col < col_hi; col += 64) {
+                    uint32_t r[2][32];
+                    tmem_ld32(r[0], acc0 + col);
+                    tmem_ld32(r[1], acc0 + col + 32);
+                    tmem_wait_ld(r[0]);
+                    hold(r[1]);
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
+                    for (int c = 0; c < 64; c += 2) {
+                        uint32_t* const x = &r[c >> 5][c & 31];
                         float a, b;
-                        unpair(mul2(pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), f0x2), a, b);
-                        r[c] = __float_as_uint(a);
-                        r[c + 1] = __float_as_uint(b);
+                        unpair(mul2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), f0x2), a, b);
+                        x[0] = __float_as_uint(a);
+                        x[1] = __float_as_uint(b);
                     }
                     if (has1) {
-                        uint32_t r1[32];
-                        tmem_ld32(r1, acc1 + col);
-                        tmem_wait_ld(r1);
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            float a, b;
-                            unpair(fma2(pair(__uint_as_float(r1[c]), __uint_as_float(r1[c + 1])), f1x2,
-                                        pair(__uint_as_float(r[c]), __uint_as_float(r[c + 1]))), a, b);
-                            r[c] = __float_as_uint(a);
-                            r[c + 1] = __float_as_uint(b);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t r1[32];
+                            tmem_ld32(r1, acc1 + col + 32 * h);
+                            tmem_wait_ld(r1);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 2) {
+                                float a, b;
+                                unpair(fma2(pair(__uint_as_float(r1[c]), __uint_as_float(r1[c + 1])), f1x2,
+                                            pair(__uint_as_float(r[h][c]), __uint_as_float(r[h][c + 1]))), a, b);
+                                r[h][c] = __float_as_uint(a);
+                                r[h][c + 1] = __float_as_uint(b);
+                            }
                         }
                     }
                     if (!has0) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) r[c] = 0u;
+                        for (int c = 0; c < 64; ++c) r[c >> 5][c & 31] = 0u;
                     }
                     if (whole) {
-                        const int place = (col >> 5) & 1;
-                        auto two = [&](int c) { return pack_bf16x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])); };
+                        auto two = [&](int c) { return pack_bf16x2(__uint_as_float(r[c >> 5][c & 31]), __uint_as_float(r[c >> 5][(c & 31) + 1])); };
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            *chunk(place, lane, c) = make_uint4(two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
+                        for (int c = 0; c < 8; ++c)
+                            *chunk(lane, c) = make_uint4(two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
                         __syncwarp();
-                        uint4 v[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] = *chunk(place, r0 + 8 * k, c0);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (orow[k] >= 0)
-                                *reinterpret_cast<uint4*>(p.out + static_cast<long long>(orow[k]) * kDim + col + c0 * 8) = v[k];
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                *chunk(q, lane, c) = make_uint4(r[16 * q + 4 * c], r[16 * q + 4 * c + 1], r[16 * q + 4 * c + 2], r[16 * q + 4 * c + 3]);
+                        for (int k = 0; k < 8; ++k) {
+                            const uint4 v = *chunk(r0 + 4 * k, c0);
+                            const int orow = __shfl_sync(0xFFFFFFFFu, out_row, r0 + 4 * k);
+                            if (orow >= 0) *reinterpret_cast<uint4*>(p.out + static_cast<long long>(orow) * kDim + col + c0 * 8) = v;
                         }
                         __syncwarp();
-                        float* const dst = p.part_o + (part_row0 + r0) * kDim + col + c0 * 4;
+                    } else {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)  // rows that are none are written too: they are the workspace's
-                            *reinterpret_cast<uint4*>(dst + (k & 3) * 8 * kDim + (k >> 2) * 16) = *chunk(k >> 2, r0 + 8 * (k & 3), c0);
-                        __syncwarp();
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                *chunk(lane, c) = make_uint4(r[h][4 * c], r[h][4 * c + 1], r[h][4 * c + 2], r[h][4 * c + 3]);
+                            __syncwarp();
+                            float* const dst = p.part_o + (part_row0 + r0) * kDim + col + 32 * h + c0 * 4;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)  // rows that are none are written too: they are the workspace's
+                                *reinterpret_cast<uint4*>(dst + 4 * k * kDim) = *chunk(r0 + 4 * k, c0);
+                            __syncwarp();
+                        }
                     }
                 }
             }
