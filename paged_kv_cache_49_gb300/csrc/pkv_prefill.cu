@@ -195,7 +195,7 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
     // an item of no more keys than the tables hold is never cut: nothing to join
     const long long most_keys = static_cast<long long>(max_blocks_per_seq) * block_tokens + (tree ? kKeys : 0);
     if (e == cudaSuccess && kCostTwo * most_keys + cost_item(tree) > kWhole) {
-        cfg.gridDim = dim3(grid, 8);
+        cfg.gridDim = dim3(grid, (one ? 1 : 2) * kRows / (kMergeWarps * kMergeRows));
         cfg.blockDim = dim3(kMergeWarps * 32);
         cfg.dynamicSmemBytes = 0;
         e = cudaLaunchKernelEx(&cfg, merge_kernel, p);

@@ -1185,46 +1185,77 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 }
 
 // Joins the pieces of the items that cuts split: block x serves the item whose
-// first piece CTA x computed, a warp per row.
-constexpr int kMergeWarps = 8;
+// first piece CTA x computed, a warp kMergeRows rows. The pieces of a row are
+// joined in their order, and read kMergeAhead at a time: with one at a time the
+// kernel was as long as their latencies (13 us behind the ragged prompts' 65).
+constexpr int kMergeWarps = 8, kMergeRows = 4, kMergeAhead = 2;
 
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Params p) {
     griddep_launch_dependents();
     griddep_wait();
     const Split sp = p.splits[blockIdx.x];
     if (sp.ntiles == 0) return;
-    const int lane = threadIdx.x & 31;
-    const int c0 = blockIdx.x;
-    for (int r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); r < 2 * kRows; r += gridDim.y * kMergeWarps) {
-        const int tile = r >> 7, rr = r & 127;
-        const int row_tok = rr / p.group, tok = tile * p.tpt + row_tok;
-        if (row_tok >= p.tpt || tok >= sp.ntok) continue;
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        int t = 0;
-        for (int c = c0; t < sp.ntiles; ++c) {
-            const long long end = sp.chunk * (c + 1) - sp.start;
-            const int t_end = end >= sp.cost ? sp.ntiles : cut_tile(end, sp.cost, sp.ntiles);
-            if (t_end <= t) continue;  // no piece in this range
-            t = t_end;
-            const long long prow = (2ll * c + (c == c0 ? 1 : 0)) * 2 * kRows + r;
-            const float2 st = p.part_ml[prow];
-            if (st.x == -INFINITY) continue;
-            const float4 v = *reinterpret_cast<const float4*>(p.part_o + prow * kDim + lane * 4);
-            const float top = fmaxf(m, st.x);
-            const float a = m == top ? 1.f : ex2(m - top), b = st.x == top ? 1.f : ex2(st.x - top);
-            m = top;
-            l = l * a + st.y * b;
-            o.x = o.x * a + v.x * b;
-            o.y = o.y * a + v.y * b;
-            o.z = o.z * a + v.z * b;
-            o.w = o.w * a + v.w * b;
+    const int lane = threadIdx.x & 31, c0 = blockIdx.x;
+    const int first = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * kMergeRows;
+    // rows of the second query tile start at 128, whatever the first one holds
+    if ((first >> 7) * p.tpt + (first & 127) / p.group >= sp.ntok) return;
+    float m[kMergeRows], l[kMergeRows];
+    float4 o[kMergeRows];
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    int t = 0, c = c0;
+    while (t < sp.ntiles) {
+        float2 st[kMergeAhead][kMergeRows];
+        float4 v[kMergeAhead][kMergeRows];
+#pragma unroll
+        for (int a = 0; a < kMergeAhead; ++a) {
+            // the next range that holds a piece
+            long long slot = -1;
+            while (t < sp.ntiles && slot < 0) {
+                const long long end = sp.chunk * (c + 1) - sp.start;
+                const int t_end = end >= sp.cost ? sp.ntiles : cut_tile(end, sp.cost, sp.ntiles);
+                if (t_end > t) slot = 2ll * c + (c == c0 ? 1 : 0);
+                t = max(t, t_end);
+                ++c;
+            }
+#pragma unroll
+            for (int i = 0; i < kMergeRows; ++i) {
+                st[a][i] = make_float2(-INFINITY, 0.f);
+                if (slot < 0) continue;
+                const long long row = slot * 2 * kRows + first + i;
+                st[a][i] = p.part_ml[row];
+                v[a][i] = *reinterpret_cast<const float4*>(p.part_o + row * kDim + lane * 4);
+            }
         }
-        const float inv = l == 0.f ? (m == -INFINITY ? 0.f : __int_as_float(0x7FC00000)) : 1.f / l;
+#pragma unroll
+        for (int a = 0; a < kMergeAhead; ++a)
+#pragma unroll
+            for (int i = 0; i < kMergeRows; ++i) {
+                const float2 s = st[a][i];
+                if (s.x == -INFINITY) continue;  // sees no key of the piece: nothing, or not a row
+                const float top = fmaxf(m[i], s.x);
+                const float fa = m[i] == top ? 1.f : ex2(m[i] - top), fb = s.x == top ? 1.f : ex2(s.x - top);
+                m[i] = top;
+                l[i] = l[i] * fa + s.y * fb;
+                o[i].x = o[i].x * fa + v[a][i].x * fb;
+                o[i].y = o[i].y * fa + v[a][i].y * fb;
+                o[i].z = o[i].z * fa + v[a][i].z * fb;
+                o[i].w = o[i].w * fa + v[a][i].w * fb;
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i) {
+        const int r = (first + i) & 127, row_tok = r / p.group, tok = ((first + i) >> 7) * p.tpt + row_tok;
+        if (row_tok >= p.tpt || tok >= sp.ntok) continue;
+        const float inv = l[i] != 0.f ? 1.f / l[i] : m[i] == -INFINITY ? 0.f : __int_as_float(0x7FC00000);
         uint2 u;
-        u.x = pack_bf16x2(o.x * inv, o.y * inv);
-        u.y = pack_bf16x2(o.z * inv, o.w * inv);
-        const int head = sp.head0 + rr - row_tok * p.group;
+        u.x = pack_bf16x2(o[i].x * inv, o[i].y * inv);
+        u.y = pack_bf16x2(o[i].z * inv, o[i].w * inv);
+        const int head = sp.head0 + r - row_tok * p.group;
         *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(sp.tok0 + tok) * p.hq + head) * kDim + lane * 4) = u;
     }
 }
