@@ -332,7 +332,8 @@ pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
  * What a row does not see never reaches it: keys and values behind p, rows of
  * the last block past the context and unused blocks may hold anything, NaN
  * included. A row that sees nothing gives zeros.
- * Limits: as pkv_attn_decode_ex, num_tokens >= 0 and scale >= 0. Device-side
+ * Limits: as pkv_attn_decode_ex; 0 <= num_tokens < 2^28, num_tokens *
+ * num_q_heads < 2^31 (PKV_ERANGE), scale >= 0. Device-side
  * errors are handled as there; besides, query_starts out of order or range is
  * clamped and sets PKV_DEVERR_QUERY, and a chunk longer than its context sets
  * PKV_DEVERR_CONTEXT (rows before position 0 see nothing).

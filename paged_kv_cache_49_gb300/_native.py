@@ -725,6 +725,8 @@ def qk_norm_rope_append(q, k, v, cos_sin, positions, slot_mapping, k_cache, v_ca
         raise ValueError("q_weight and k_weight must be [D]")
     max_positions = rotary = 0
     if cos_sin is not None:
+        if positions is None:
+            raise ValueError("positions must be given with cos_sin")
         _need_all(device, ((cos_sin, _F32, "cos_sin"), (positions, _I32, "positions")))
         if cos_sin.dim() != 2 or positions.shape != (T,):
             raise ValueError("cos_sin must be [positions, rotary_dim] and positions [T]")

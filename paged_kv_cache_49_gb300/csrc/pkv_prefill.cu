@@ -123,7 +123,8 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
         return PKV_EUNSUPPORTED;
     if (static_cast<long long>(num_blocks) * num_kv_heads * block_tokens >= (1ll << 31) ||
         static_cast<long long>(num_seqs) * max_blocks_per_seq >= (1ll << 31) ||
-        static_cast<long long>(max_blocks_per_seq) * block_tokens >= (1ll << 31))
+        static_cast<long long>(max_blocks_per_seq) * block_tokens >= (1ll << 31) || num_tokens >= (1 << 28) ||
+        static_cast<long long>(num_tokens) * num_q_heads >= (1ll << 31))
         return PKV_ERANGE;
     if (num_tokens == 0) return PKV_OK;
     if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !query_starts || !workspace || !out ||

@@ -184,7 +184,8 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int s, uint32_t* bad) {
     return q;
 }
 
-// Costs of one head of a sequence: of the first i items, all full, i * (a + b i); of the smaller one behind them, last.
+// Costs of one head of a sequence: of the first i items, all full, i * (a + b i);
+// of the smaller one behind them, last.
 struct Cost {
     long long a, last;
     int b;
@@ -213,7 +214,7 @@ __device__ __forceinline__ int cut_tile(long long off, long long cost, int ntile
     return min(max(t, 0), ntiles);
 }
 
-// One item: the tiles of one (sequence, KV head) from token i * 2 tpt on.
+// One item: the i-th of one (sequence, KV head).
 struct Item {
     int s, h, i;
     Seq q;
@@ -577,9 +578,13 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             prefetch_tensormap(&tm_vd);
         }
     }
+    // Launched early: behind this wait are the earlier kernels' results and the
+    // last call's partial results. The tensor memory too is taken only here: an
+    // earlier kernel may still be about to take its own, and this one would hold
+    // all of it while it waits for that kernel's end.
+    griddep_wait();
     if (warp == kWarpMma) tmem_alloc(smem_u32(&m.tmem), kTmemColumns);
     tc_fence_before();
-    griddep_wait();  // launched early: the earlier kernels' results and the last call's partial results
     plan<kTree, kOne>(p, m);
     __syncthreads();
     tc_fence_after();

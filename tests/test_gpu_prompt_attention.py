@@ -272,6 +272,35 @@ def test_repeats_graphs_streams_and_a_shared_workspace(pkv, tree):
     assert ws.read_error() == 0
 
 
+def test_calls_on_two_streams_at_once(pkv):
+    """Two calls whose kernels may run side by side, each with its workspace."""
+    a = Batch(28, [300, 40], [4000, 900], 8, 2, 16)
+    b = Batch(29, [64, 33, 5], [9000, 64, 700], 8, 2, 16)
+    da, db = _dev(pkv, a, False), _dev(pkv, b, True)
+    ra, rb = _call(pkv, da, a.scale).clone(), _call(pkv, db, b.scale).clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [pkv.PrefillWorkspace(), pkv.PrefillWorkspace()]
+    outs = [torch.zeros_like(ra), torch.zeros_like(rb)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for d, s, w, o, x in zip((da, db), streams, spaces, outs, (a, b)):
+            _call(pkv, d, x.scale, out=o, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], ra) and torch.equal(outs[1], rb)
+    assert spaces[0].read_error() == 0 and spaces[1].read_error() == 0
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="one device")
+def test_another_device_than_the_current_one(pkv):
+    b = Batch(30, [9, 64], [500, 64], 8, 2, 16)
+    for tree in (False, True):
+        d = {k: t.to("cuda:1") for k, t in _dev(pkv, b, tree).items()}
+        out = _call(pkv, d, b.scale)
+        torch.cuda.synchronize("cuda:1")
+        _check(out, _ref(b, tree))
+
+
 def test_a_single_draft_is_a_decode_step(pkv):
     """One draft that sees itself: decode attention once it has been appended."""
     held = [1, 16, 203, 700]

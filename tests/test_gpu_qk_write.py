@@ -144,3 +144,12 @@ def test_bad_positions_and_slots_set_their_bits(pkv):
     before = kc.clone(), vc.clone()
     assert run([5, 5, 5, 5], [-1, -1, -1, 32]) == pkv.DEVERR_SLOT
     assert torch.equal(kc, before[0]) and torch.equal(vc, before[1])
+    slots = torch.arange(4, device="cuda")
+    for bad in (dict(positions=None), dict(positions=torch.zeros(4, device="cuda")), dict(k=k[:, :1]), dict(k=k.cpu()),
+                dict(slot_mapping=slots[:3]), dict(q_weight=torch.ones(64, dtype=torch.bfloat16, device="cuda")),
+                dict(k_out=torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")), dict(v_cache=vc[:1])):
+        a = dict(q=q, k=k, v=k, cos_sin=table, positions=torch.arange(4, dtype=torch.int32, device="cuda"),
+                 slot_mapping=slots, k_cache=kc, v_cache=vc)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            pkv.qk_norm_rope_append(**a)

@@ -37,7 +37,8 @@ def _prefill(nat, **kw):
     (dict(scale=float("nan")), "EINVAL"), (dict(scale=-0.5), "EINVAL"), (dict(scale=float("inf")), "EINVAL"),
     (dict(seqs=4097), "EUNSUPPORTED"), (dict(d=64), "EUNSUPPORTED"), (dict(hq=9), "EUNSUPPORTED"),
     (dict(hq=18), "EUNSUPPORTED"), (dict(bt=12), "EUNSUPPORTED"), (dict(nb=1 << 27), "ERANGE"),
-    (dict(width=1 << 30), "ERANGE"), (dict(tokens=0, q=None, out=None), "OK"),
+    (dict(width=1 << 30), "ERANGE"), (dict(tokens=1 << 28), "ERANGE"),
+    (dict(tokens=1 << 27, hq=16), "ERANGE"), (dict(tokens=0, q=None, out=None), "OK"),
 ])
 def test_prefill_refusals(nat, kw, status):
     assert _prefill(nat, **kw) == getattr(nat, "PKV_" + status)
