@@ -15,7 +15,11 @@
 // for memory once. 16,411 tokens of 64 + 16 heads of 128: 127 us, 5.4 TB/s
 // (211 us with a block per token and nothing read ahead, 175 us with three
 // heads read together; two or three heads a turn, two or four blocks an SM,
-// streaming stores: 127-139 us). 64 tokens of 32 + 16 heads: 2.7 us.
+// streaming stores: 127-147 us). What bounds it now is the bytes under way, 24
+// KB an SM. Three turns ahead through shared memory gives 119 us there but
+// takes 8.3 us for 6.1 where the rows come from L2 (5,003 tokens of 24 heads
+// of 64), as they do behind a projection of a usual step. 64 tokens of 32 + 16
+// heads: 2.4 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -26,6 +30,7 @@
 
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
+#include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace qkw {
@@ -34,14 +39,14 @@ constexpr int kThreads = 256;
 
 struct Params {
     const __nv_bfloat16 *q, *k, *v, *q_weight, *k_weight;
-    long long q_stride, k_stride, v_stride;
+    int q_stride, k_stride, v_stride;
     const float* cos_sin;
     const int32_t* positions;
     const int64_t* slots;
     __nv_bfloat16 *q_out, *k_out, *k_cache, *v_cache;
     uint32_t* err;
     long long slot_limit;
-    float eps;
+    float eps, inv_dim;
     int max_positions, rot, num_tokens, hq, hkv, dim, bt_shift;
     int step_tok, step_head;  // the grid's groups, as tokens and heads
 };
@@ -55,9 +60,18 @@ __device__ __forceinline__ uint4 ld_streaming(const __nv_bfloat16* p) {
     return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-    x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
-    x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+// 8 bf16 values as four pairs of floats
+__device__ __forceinline__ void unpack8(const uint4& u, uint64_t (&x)[4]) {
+    x[0] = pair(bf16_lo(u.x), bf16_hi(u.x));
+    x[1] = pair(bf16_lo(u.y), bf16_hi(u.y));
+    x[2] = pair(bf16_lo(u.z), bf16_hi(u.z));
+    x[3] = pair(bf16_lo(u.w), bf16_hi(u.w));
+}
+
+__device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
+    float lo, hi;
+    unpair(x, lo, hi);
+    return pack_bf16x2(lo, hi);
 }
 
 constexpr int kBlocksPerSm = 3;
@@ -85,10 +99,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) qk_write_kernel(const 
     auto read_ahead = [&](int t, int hd) {
         ahead0 = ahead1 = make_uint4(0, 0, 0, 0);
         if (t >= p.num_tokens) return;
-        const __nv_bfloat16* row = hd < p.hq ? p.q + t * p.q_stride
-                                 : hd < p.hq + p.hkv ? p.k + t * p.k_stride - static_cast<long long>(p.hq) * p.dim
-                                                     : p.v + t * p.v_stride - static_cast<long long>(p.hq + p.hkv) * p.dim;
-        row += static_cast<long long>(hd) * p.dim;
+        const bool is_q = hd < p.hq, is_k = hd < p.hq + p.hkv;
+        const int hh = is_q ? hd : is_k ? hd - p.hq : hd - p.hq - p.hkv;
+        const __nv_bfloat16* row = (is_q ? p.q : is_k ? p.k : p.v) + hh * p.dim;
+        row += static_cast<long long>(t) * (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride);
         if (live0) ahead0 = ld_streaming(row + at0);
         if (live1) ahead1 = ld_streaming(row + at1);
         slot_ahead = __ldg(p.slots + t);
@@ -110,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) qk_write_kernel(const 
         read_ahead(tok2, h2);
         const bool store_kv = mine && slot >= 0 && slot < p.slot_limit;
         uint32_t bad = mine && slot >= p.slot_limit ? PKV_DEVERR_SLOT : 0u;
-        float c[8], s[8];
+        uint64_t c[4], s[4];  // of eight angles
         if (p.rot > 0) {
             if (pos < 0 || pos >= p.max_positions) {
                 if (mine && slot >= 0) bad |= PKV_DEVERR_POSITION;
@@ -119,11 +133,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) qk_write_kernel(const 
             if (turned && mine && h < p.hq + p.hkv) {
                 const float* row = p.cos_sin + static_cast<long long>(pos) * p.rot + lane * 8;
 #pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    const float4 cv = __ldg(reinterpret_cast<const float4*>(row + i));
-                    const float4 sv = __ldg(reinterpret_cast<const float4*>(row + (p.rot >> 1) + i));
-                    c[i] = cv.x; c[i + 1] = cv.y; c[i + 2] = cv.z; c[i + 3] = cv.w;
-                    s[i] = sv.x; s[i + 1] = sv.y; s[i + 2] = sv.z; s[i + 3] = sv.w;
+                for (int i = 0; i < 2; ++i) {
+                    const float4 cv = __ldg(reinterpret_cast<const float4*>(row + 4 * i));
+                    const float4 sv = __ldg(reinterpret_cast<const float4*>(row + (p.rot >> 1) + 4 * i));
+                    c[2 * i] = pair(cv.x, cv.y);
+                    c[2 * i + 1] = pair(cv.z, cv.w);
+                    s[2 * i] = pair(sv.x, sv.y);
+                    s[2 * i + 1] = pair(sv.z, sv.w);
                 }
             }
         }
@@ -132,43 +148,57 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) qk_write_kernel(const 
         const int in_blk = static_cast<int>(slot) & ((1 << p.bt_shift) - 1);
 
         const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv, is_v = !is_q && !is_k;
-        float x[2][8];
+        uint64_t x[2][4];
         unpack8(u[0], x[0]);
         unpack8(u[1], x[1]);
         const __nv_bfloat16* weight = is_q ? p.q_weight : is_k ? p.k_weight : nullptr;
         if (p.q_weight || p.k_weight) {
-            float sq = 0.f;
+            uint64_t sq2 = mul2(x[0][0], x[0][0]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) sq += x[e >> 3][e & 7] * x[e >> 3][e & 7];
+            for (int e = 1; e < 8; ++e) sq2 = fma2(x[e >> 2][e & 3], x[e >> 2][e & 3], sq2);
+            float sq, odd;
+            unpair(sq2, sq, odd);
+            sq += odd;
 #pragma unroll
             for (int d = kLanes / 2; d; d >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, d, kLanes);
             if (weight) {
-                const float r = rsqrtf(sq / static_cast<float>(p.dim) + p.eps);
+                const float r = rsqrtf(sq * p.inv_dim + p.eps);
+                const uint64_t r2 = pair(r, r);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (!(half ? live1 : live0)) continue;
-                    float w[8];
+                    uint64_t w[4];
                     unpack8(__ldg(reinterpret_cast<const uint4*>(weight + (half ? at1 : at0))), w);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[half][e] = x[half][e] * r * w[e];
+                    for (int e = 0; e < 4; ++e) x[half][e] = mul2(mul2(x[half][e], r2), w[e]);
                 }
             }
         }
         if (!is_v) {
             if (turned) {
+                if (kInterleaved) {
+                    // angle e turns the e-th pair of the lane's 16 values
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float& a = kInterleaved ? x[e >> 2][2 * (e & 3)] : x[0][e];
-                    float& b = kInterleaved ? x[e >> 2][2 * (e & 3) + 1] : x[1][e];
-                    const float a0 = a, b0 = b;
-                    a = a0 * c[e] - b0 * s[e];
-                    b = a0 * s[e] + b0 * c[e];
+                    for (int e = 0; e < 8; ++e) {
+                        float a, b, c0, c1, s0, s1;
+                        unpair(x[e >> 2][e & 3], a, b);
+                        unpair(c[e >> 1], c0, c1);
+                        unpair(s[e >> 1], s0, s1);
+                        const float ce = e & 1 ? c1 : c0, se = e & 1 ? s1 : s0;
+                        x[e >> 2][e & 3] = pair(a * ce - b * se, a * se + b * ce);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint64_t a = x[0][e], b = x[1][e];
+                        x[0][e] = sub2(mul2(a, c[e]), mul2(b, s[e]));
+                        x[1][e] = fma2(a, s[e], mul2(b, c[e]));
+                    }
                 }
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-                u[half] = make_uint4(pack_bf16x2(x[half][0], x[half][1]), pack_bf16x2(x[half][2], x[half][3]),
-                                     pack_bf16x2(x[half][4], x[half][5]), pack_bf16x2(x[half][6], x[half][7]));
+                u[half] = make_uint4(pack_pair(x[half][0]), pack_pair(x[half][1]), pack_pair(x[half][2]), pack_pair(x[half][3]));
         }
         __nv_bfloat16* dst = nullptr;
         if (is_q) {
@@ -245,6 +275,7 @@ pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
     if (q_stride < static_cast<int64_t>(num_q_heads) * head_dim || k_stride < static_cast<int64_t>(num_kv_heads) * head_dim ||
         v_stride < static_cast<int64_t>(num_kv_heads) * head_dim || q_stride % 8 || k_stride % 8 || v_stride % 8)
         return PKV_EINVAL;
+    if (q_stride > INT32_MAX || k_stride > INT32_MAX || v_stride > INT32_MAX) return PKV_ERANGE;
     for (const void* ptr : {q, k, v, q_weight, k_weight, static_cast<const void*>(cos_sin), static_cast<const void*>(q_out), static_cast<const void*>(k_out),
                             static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
         if (!aligned16(ptr)) return PKV_EINVAL;
@@ -257,9 +288,9 @@ pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
     p.v = static_cast<const __nv_bfloat16*>(v);
     p.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
     p.k_weight = static_cast<const __nv_bfloat16*>(k_weight);
-    p.q_stride = q_stride;
-    p.k_stride = k_stride;
-    p.v_stride = v_stride;
+    p.q_stride = static_cast<int>(q_stride);
+    p.k_stride = static_cast<int>(k_stride);
+    p.v_stride = static_cast<int>(v_stride);
     p.cos_sin = cos_sin;
     p.positions = positions;
     p.slots = slot_mapping;
@@ -270,6 +301,7 @@ pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
     p.err = device_error;
     p.slot_limit = static_cast<long long>(num_blocks) * block_tokens;
     p.eps = eps;
+    p.inv_dim = 1.f / static_cast<float>(head_dim);
     p.max_positions = max_positions;
     p.rot = rotary_dim;
     p.num_tokens = num_tokens;
