@@ -151,6 +151,7 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
     p.splits = reinterpret_cast<Split*>(ws + kWsSplits);
     p.part_ml = reinterpret_cast<float2*>(ws + kWsStates);
     p.part_o = reinterpret_cast<float*>(ws + kWsStates + static_cast<size_t>(grid) * 2 * 2 * kRows * sizeof(float2));
+    p.grid = grid;
     p.num_seqs = num_seqs;
     p.num_tokens = num_tokens;
     p.hq = num_q_heads;
@@ -160,6 +161,7 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
     // Sequences of one query tile each on the average (decode rows, small trees):
     // the kernel of one-tile items, whose ring is deeper.
     const bool one = static_cast<long long>(num_tokens) * p.group <= static_cast<long long>(num_seqs) * kRows;
+    p.one = one;
     const int tokens = (one ? 1 : 2) * p.tpt;
     p.item_magic = ((1ull << 36) + tokens - 1) / tokens;
     p.max_blocks = max_blocks_per_seq;
@@ -196,10 +198,18 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
     // an item of no more keys than the tables hold is never cut: nothing to join
     const long long most_keys = static_cast<long long>(max_blocks_per_seq) * block_tokens + (tree ? kKeys : 0);
     if (e == cudaSuccess && kCostTwo * most_keys + cost_item(tree) > kWhole) {
-        cfg.gridDim = dim3(grid, (one ? 1 : 2) * kRows / (kMergeWarps * kMergeRows));
+        // no more items than tiles of tokens and sequences allow; where that is
+        // fewer than the CTAs, 4 to 32 rows a block, for 3 to 6 blocks an SM,
+        // else 32 (2,000 rows of 8 heads, 64 items: 27.5 us with 32 rows, 30.5
+        // with 16; 16 items of 9 pieces: 72 us with 8 rows, 78 with 16)
+        const long long items = (num_tokens / tokens + static_cast<long long>(num_seqs)) * num_kv_heads;
+        const int most = static_cast<int>(std::min<long long>(items, grid)), rows = (one ? 1 : 2) * kRows;
+        int parts = rows / (kMergeWarps * kMergeRows);
+        while (parts < rows / kMergeRows && most < grid && parts * most <= 3 * grid) parts *= 2;
+        cfg.gridDim = dim3(most, parts);
         cfg.blockDim = dim3(kMergeWarps * 32);
         cfg.dynamicSmemBytes = 0;
-        e = cudaLaunchKernelEx(&cfg, merge_kernel, p);
+        e = cudaLaunchKernelEx(&cfg, most < grid ? merge_kernel<false> : merge_kernel<true>, p);
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {

@@ -81,6 +81,7 @@ struct Params {
     struct Split* splits;   // [grid]
     float2* part_ml;        // [2 * grid][256]
     float* part_o;          // [2 * grid][256][128]
+    int grid, one;          // CTAs; items of one query tile only
     int num_seqs, num_tokens, hq, hkv, group, tpt;  // tpt: tokens of a tile
     int max_blocks, num_blocks, bt;
     float scale_log2;
@@ -1189,79 +1190,152 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (warp == kWarpMma) tmem_free(tmem, kTmemColumns);
 }
 
-// Joins the pieces of the items that cuts split: block x serves the item whose
-// first piece CTA x computed, a warp kMergeRows rows. The pieces of a row are
-// joined in their order, and read kMergeAhead at a time: with one at a time the
-// kernel was as long as their latencies (13 us behind the ragged prompts' 65).
-constexpr int kMergeWarps = 8, kMergeRows = 4, kMergeAhead = 2;
+// Joins the pieces of the items that cuts split: kEvery, block x serves the item
+// that CTA x describes, if it does; else, where there are fewer items than CTAs,
+// the x-th of them, so that more blocks can share its rows (y). A warp takes
+// kMergeRows rows of all pieces, read kMergeAhead at a time (one row of one
+// piece at a time, the kernel was as long as their latencies: 13 us behind the
+// ragged prompts' 65); of an item in more than kMergeShare pieces -- few rows on
+// a long context -- the warps share the pieces instead and join their results.
+// 8 drafts on 60,000 keys of one head, 150 pieces: 25 us for both kernels, 118
+// when one warp read all pieces of its rows; where there are two or three pieces
+// an item the search costs 1 to 2 us. The order of the sums is the same in every
+// run.
+constexpr int kMergeWarps = 8, kMergeRows = 4, kMergeAhead = 2, kMergeShare = 8;
 
-__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Params p) {
+struct RowSums {
+    float m, l;  // maximum (log2 units), sum of weights
+    float4 o;    // this lane's 4 columns
+
+    __device__ __forceinline__ void add(float m2, float l2, const float4& o2) {
+        if (m2 == -INFINITY) return;  // sees no key of the piece, or is not a row
+        const float top = fmaxf(m, m2);
+        const float fa = m == top ? 1.f : ex2(m - top), fb = m2 == top ? 1.f : ex2(m2 - top);
+        m = top;
+        l = l * fa + l2 * fb;
+        o.x = o.x * fa + o2.x * fb;
+        o.y = o.y * fa + o2.y * fb;
+        o.z = o.z * fa + o2.z * fb;
+        o.w = o.w * fa + o2.w * fb;
+    }
+};
+
+template <bool kEvery>
+__global__ void __launch_bounds__(kMergeWarps * 32, kEvery ? 3 : 2) merge_kernel(const Params p) {
+    __shared__ int slots[kMaxGrid];  // of the ranges from the first piece's on; -1: no piece in it
+    __shared__ int last, item, marks[kMergeWarps];
+    __shared__ float4 shared_o[kMergeWarps][kMergeRows][32];
+    __shared__ float2 shared_ml[kMergeWarps][kMergeRows];
     griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) last = kMaxGrid, item = -1;
+    __syncthreads();
     griddep_wait();
-    const Split sp = p.splits[blockIdx.x];
-    if (sp.ntiles == 0) return;
-    const int lane = threadIdx.x & 31, c0 = blockIdx.x;
-    const int first = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * kMergeRows;
-    // rows of the second query tile start at 128, whatever the first one holds
-    if ((first >> 7) * p.tpt + (first & 127) / p.group >= sp.ntok) return;
-    float m[kMergeRows], l[kMergeRows];
-    float4 o[kMergeRows];
-#pragma unroll
-    for (int i = 0; i < kMergeRows; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    int t = 0, c = c0;
-    while (t < sp.ntiles) {
-        float2 st[kMergeAhead][kMergeRows];
-        float4 v[kMergeAhead][kMergeRows];
-#pragma unroll
-        for (int a = 0; a < kMergeAhead; ++a) {
-            // the next range that holds a piece
-            long long slot = -1;
-            while (t < sp.ntiles && slot < 0) {
-                const long long end = sp.chunk * (c + 1) - sp.start;
-                const int t_end = end >= sp.cost ? sp.ntiles : cut_tile(end, sp.cost, sp.ntiles);
-                if (t_end > t) slot = 2ll * c + (c == c0 ? 1 : 0);
-                t = max(t, t_end);
-                ++c;
+    // the CTA that describes this block's item
+    int c0 = blockIdx.x;
+    if (!kEvery) {
+        for (int base = 0, found = 0; base < p.grid; base += kMergeWarps * 32) {
+            const int c = base + threadIdx.x;
+            const bool split = c < p.grid && p.splits[c].ntiles != 0;
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, split);
+            if (lane == 0) marks[warp] = __popc(mask);
+            __syncthreads();
+            int rank = found + __popc(mask & ((1u << lane) - 1u));
+            for (int w = 0; w < kMergeWarps; ++w) {
+                if (w < warp) rank += marks[w];
+                found += marks[w];
             }
-#pragma unroll
-            for (int i = 0; i < kMergeRows; ++i) {
-                st[a][i] = make_float2(-INFINITY, 0.f);
-                if (slot < 0) continue;
-                const long long row = slot * 2 * kRows + first + i;
-                st[a][i] = p.part_ml[row];
-                v[a][i] = *reinterpret_cast<const float4*>(p.part_o + row * kDim + lane * 4);
-            }
+            if (split && rank == static_cast<int>(blockIdx.x)) item = c;
+            __syncthreads();
         }
-#pragma unroll
-        for (int a = 0; a < kMergeAhead; ++a)
-#pragma unroll
-            for (int i = 0; i < kMergeRows; ++i) {
-                const float2 s = st[a][i];
-                if (s.x == -INFINITY) continue;  // sees no key of the piece: nothing, or not a row
-                const float top = fmaxf(m[i], s.x);
-                const float fa = m[i] == top ? 1.f : ex2(m[i] - top), fb = s.x == top ? 1.f : ex2(s.x - top);
-                m[i] = top;
-                l[i] = l[i] * fa + s.y * fb;
-                o[i].x = o[i].x * fa + v[a][i].x * fb;
-                o[i].y = o[i].y * fa + v[a][i].y * fb;
-                o[i].z = o[i].z * fa + v[a][i].z * fb;
-                o[i].w = o[i].w * fa + v[a][i].w * fb;
-            }
+        c0 = item;
+        if (c0 < 0) return;
     }
+    const Split sp = p.splits[c0];
+    if (sp.ntiles == 0) return;
+    const int block_rows = (p.one ? 1 : 2) * kRows / gridDim.y;
+    auto row_token = [&](int r) { return (r >> 7) * p.tpt + (r & 127) / p.group; };  // the second query tile starts at row 128
+    if (row_token(blockIdx.y * block_rows) >= sp.ntok) return;
+    auto tiles_before = [&](int c) {  // tiles of the item in the ranges up to c0 + c
+        const long long end = sp.chunk * (c0 + c + 1) - sp.start;
+        return end >= sp.cost ? sp.ntiles : cut_tile(end, sp.cost, sp.ntiles);
+    };
+    // the piece in the c-th range from the first piece's on, -1 if there is none
+    auto slot_of = [&](int c, bool& ends) {
+        const int t = tiles_before(c), before = c == 0 ? 0 : tiles_before(c - 1);
+        ends = t == sp.ntiles || c0 + c == p.grid - 1;
+        return t > before ? 2 * (c0 + c) + (c == 0 ? 1 : 0) : -1;
+    };
+
+    RowSums sums[kMergeRows];
+    auto gather = [&](int first, int from, int to, auto slot_at) {
 #pragma unroll
-    for (int i = 0; i < kMergeRows; ++i) {
-        const int r = (first + i) & 127, row_tok = r / p.group, tok = ((first + i) >> 7) * p.tpt + row_tok;
-        if (row_tok >= p.tpt || tok >= sp.ntok) continue;
-        const float inv = l[i] != 0.f ? 1.f / l[i] : m[i] == -INFINITY ? 0.f : __int_as_float(0x7FC00000);
-        uint2 u;
-        u.x = pack_bf16x2(o[i].x * inv, o[i].y * inv);
-        u.y = pack_bf16x2(o[i].z * inv, o[i].w * inv);
+        for (int i = 0; i < kMergeRows; ++i) sums[i] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int c = from; c < to; c += kMergeAhead) {
+            float2 st[kMergeAhead][kMergeRows];
+            float4 v[kMergeAhead][kMergeRows];
+#pragma unroll
+            for (int a = 0; a < kMergeAhead; ++a) {
+                const int slot = c + a < to ? slot_at(c + a) : -1;
+#pragma unroll
+                for (int i = 0; i < kMergeRows; ++i) {
+                    st[a][i] = make_float2(-INFINITY, 0.f);
+                    v[a][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (slot < 0) continue;
+                    const long long row = static_cast<long long>(slot) * 2 * kRows + first + i;
+                    st[a][i] = p.part_ml[row];
+                    v[a][i] = *reinterpret_cast<const float4*>(p.part_o + row * kDim + lane * 4);
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < kMergeAhead; ++a)
+#pragma unroll
+                for (int i = 0; i < kMergeRows; ++i) sums[i].add(st[a][i].x, st[a][i].y, v[a][i]);
+        }
+    };
+    auto store = [&](int row, const RowSums& x) {
+        const int r = row & 127, row_tok = r / p.group, tok = row_token(row);
+        if (row_tok >= p.tpt || tok >= sp.ntok) return;
+        const float inv = x.l != 0.f ? 1.f / x.l : x.m == -INFINITY ? 0.f : __int_as_float(0x7FC00000);
         const int head = sp.head0 + r - row_tok * p.group;
-        *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(sp.tok0 + tok) * p.hq + head) * kDim + lane * 4) = u;
+        *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(sp.tok0 + tok) * p.hq + head) * kDim + lane * 4) =
+            make_uint2(pack_bf16x2(x.o.x * inv, x.o.y * inv), pack_bf16x2(x.o.z * inv, x.o.w * inv));
+    };
+    bool ends;
+    const int mine = slot_of(lane, ends);
+    const int few = __ffs(__ballot_sync(0xFFFFFFFFu, ends));
+    if (few != 0 && few <= kMergeShare) {
+        for (int g = warp; g < block_rows / kMergeRows; g += kMergeWarps) {
+            const int first = blockIdx.y * block_rows + g * kMergeRows;
+            gather(first, 0, few, [&](int c) { return __shfl_sync(0xFFFFFFFFu, mine, c); });
+#pragma unroll
+            for (int i = 0; i < kMergeRows; ++i) store(first + i, sums[i]);
+        }
+        return;
+    }
+    for (int c = threadIdx.x; c0 + c < p.grid; c += blockDim.x) {
+        slots[c] = slot_of(c, ends);
+        if (ends) atomicMin(&last, c);
+    }
+    __syncthreads();
+    const int pieces = last + 1;
+    for (int g = 0; g < block_rows / kMergeRows; ++g) {
+        const int first = blockIdx.y * block_rows + g * kMergeRows;
+        if (row_token(first) >= sp.ntok) break;
+        gather(first, pieces * warp / kMergeWarps, pieces * (warp + 1) / kMergeWarps,
+               [&](int c) { return slots[c]; });
+#pragma unroll
+        for (int i = 0; i < kMergeRows; ++i) {
+            shared_o[warp][i][lane] = sums[i].o;
+            if (lane == 0) shared_ml[warp][i] = make_float2(sums[i].m, sums[i].l);
+        }
+        __syncthreads();
+        if (warp < kMergeRows) {
+            RowSums x = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+            for (int w = 0; w < kMergeWarps; ++w) x.add(shared_ml[w][warp].x, shared_ml[w][warp].y, shared_o[w][warp][lane]);
+            store(first + warp, x);
+        }
+        __syncthreads();
     }
 }
 

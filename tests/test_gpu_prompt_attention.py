@@ -99,6 +99,18 @@ def test_few_rows_on_long_contexts(pkv, tree, new, held):
     _run(pkv, Batch(len(new) + new[0], new, held, 8, 2, 16), tree=tree)
 
 
+@pytest.mark.parametrize("tree,new,held,hq,hkv", [
+    (True, [60], [17003], 7, 1),                         # a tile of 126 rows and a short one, all in many pieces
+    (True, [64], [30001], 24, 3),                        # items of fewer pieces
+    (False, [40, 3], [20011, 40], 10, 2),
+    (False, [3] + [2] * 159, [50021] + [300] * 159, 8, 1),  # as many items as CTAs, one of them long
+    (True, [3] + [2] * 159, [50021] + [300] * 159, 8, 1),
+])
+def test_items_in_many_pieces(pkv, tree, new, held, hq, hkv):
+    """The warps of the join share the pieces of a row."""
+    _run(pkv, Batch(hq + new[0], new, held, hq, hkv, 16, first_row=1, rows_behind=1), tree=tree)
+
+
 def test_many_sequences(pkv):
     rng = np.random.default_rng(5)
     held = [int(x) for x in rng.integers(1, 60, size=700)]
