@@ -1,8 +1,8 @@
 """GB300-native paged KV cache decode.
 
 libpkv (C ABI, include/pkv.h) holds the CUDA kernels for sm_103a -- paged
-decode attention, KV append, copy-on-write block copy -- and the C++ host
-block manager. This package is the thin Python binding over it plus a small
+decode attention, attention of prompts and draft trees, norm, rotation and KV
+append, copy-on-write block copy -- and the C++ host block manager. This package is the thin Python binding over it plus a small
 engine that drives one attention layer's pool.
 """
 from ._native import (  # noqa: F401

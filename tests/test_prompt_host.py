@@ -151,3 +151,21 @@ def test_oracle_rotation_and_norm():
     one = bits_of(np.ones(8, np.float32))
     n = po.norm_rope(x, one, 0.0, None, None, False)
     assert np.abs((n * n).mean(axis=-1) - 1.0).max() <= 1e-12
+
+
+def test_drafts_are_taken_once_and_only_in_their_place(nat):
+    """Refusals that leave the block manager as it was; nothing is launched."""
+    import torch
+    from paged_kv_cache_49_gb300.engine import PagedKVEngine
+    eng = PagedKVEngine(8, 2, 1, device="cpu")
+    a, b = eng.bm.admit(14, 20), eng.bm.admit(3, 20)
+    k = torch.zeros(4, 1, 128, dtype=torch.bfloat16)
+    twice = eng.prepare_drafts([a, a], [[-1, 0], [-1, 0]])
+    with pytest.raises(ValueError, match="takes one path"):
+        eng.accept_drafts(twice, [[0], [0, 1]], k, k)
+    db = eng.prepare_drafts([a, b], [[-1, 0], [-1, 0]])
+    assert db.held == [14, 3] and db.positions.tolist() == [14, 15, 3, 4]
+    eng.bm.prepare_append([b])
+    with pytest.raises(ValueError, match="takes one path"):
+        eng.accept_drafts(db, [[0], [0, 1]], k, k)
+    assert [eng.bm.context_len(s) for s in (a, b)] == [14, 4]
