@@ -58,18 +58,18 @@ DeviceInfo device_info() {
         record_cuda_error(e);
         return {};
     }
-    d.grid = std::min(sms, kMaxGrid);
+    d.grid = std::min(sms, kMaxGrid / kRounds);
     d.ok = true;
     return d;
 }
 
 // Workspace: header (error word), split items, then each range's two slots of
 // 256 row states and 256 rows of 128 fp32 values.
-constexpr size_t kWsSplits = kWsHeader, kWsStates = kWsSplits + sizeof(Split) * kMaxGrid;
+constexpr size_t kWsRounds = 64, kWsSplits = kWsHeader, kWsStates = kWsSplits + sizeof(Split) * kMaxGrid;
 static_assert(kWsStates % 256 == 0, "alignment of the partial results");
 
 size_t workspace_bytes(int grid) {
-    return kWsStates + static_cast<size_t>(grid) * 2 * 2 * kRows * (sizeof(float2) + kDim * sizeof(float));
+    return kWsStates + static_cast<size_t>(grid) * kRounds * 2 * 2 * kRows * (sizeof(float2) + kDim * sizeof(float));
 }
 
 bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
@@ -150,7 +150,8 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
     p.err = reinterpret_cast<uint32_t*>(ws);
     p.splits = reinterpret_cast<Split*>(ws + kWsSplits);
     p.part_ml = reinterpret_cast<float2*>(ws + kWsStates);
-    p.part_o = reinterpret_cast<float*>(ws + kWsStates + static_cast<size_t>(grid) * 2 * 2 * kRows * sizeof(float2));
+    p.part_o = reinterpret_cast<float*>(ws + kWsStates + static_cast<size_t>(grid) * kRounds * 2 * 2 * kRows * sizeof(float2));
+    p.rounds = reinterpret_cast<int*>(ws + kWsRounds);
     p.grid = grid;
     p.num_seqs = num_seqs;
     p.num_tokens = num_tokens;
@@ -182,6 +183,16 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
         tm_kd = tm_k;  // not read
         tm_vd = tm_v;
     }
+    const long long most_keys = static_cast<long long>(max_blocks_per_seq) * block_tokens + (tree ? kKeys : 0);
+    // no more items than tiles of tokens and sequences allow
+    const long long items = (num_tokens / tokens + static_cast<long long>(num_seqs)) * num_kv_heads;
+    // The device takes rounds where the lengths ask for them; the join of a call
+    // that may take them is slower by 2 us, so a call of few items a sequence
+    // does not.
+    p.max_rounds = !tree && !one && num_tokens / tokens >= kRoundReads * num_seqs && items >= 4 * grid &&
+                           num_seqs * most_keys * num_kv_heads * (4ll * kDim) > kRoundBytes
+                       ? kRounds
+                       : 1;
     // Both kernels are launched early (programmatic stream serialization) and
     // wait for the one before, so that they are set up when it ends.
     cudaLaunchAttribute attr[1];
@@ -196,20 +207,17 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_for(tree, one), tm_q, tm_k, tm_v, tm_kd, tm_vd, p);
     // an item of no more keys than the tables hold is never cut: nothing to join
-    const long long most_keys = static_cast<long long>(max_blocks_per_seq) * block_tokens + (tree ? kKeys : 0);
     if (e == cudaSuccess && kCostTwo * most_keys + cost_item(tree) > kWhole) {
-        // no more items than tiles of tokens and sequences allow; where that is
-        // fewer than the CTAs, 4 to 32 rows a block, for 3 to 6 blocks an SM,
-        // else 32 (2,000 rows of 8 heads, 64 items: 27.5 us with 32 rows, 30.5
-        // with 16; 16 items of 9 pieces: 72 us with 8 rows, 78 with 16)
-        const long long items = (num_tokens / tokens + static_cast<long long>(num_seqs)) * num_kv_heads;
+        // where there can be fewer split items than CTAs, 4 to 32 rows a block, for
+        // 3 to 6 blocks an SM, else 32 (2,000 rows of 8 heads, 64 items: 27.5 us with
+        // 32 rows, 30.5 with 16; 16 items of 9 pieces: 72 us with 8 rows, 78 with 16)
         const int most = static_cast<int>(std::min<long long>(items, grid)), rows = (one ? 1 : 2) * kRows;
         int parts = rows / (kMergeWarps * kMergeRows);
         while (parts < rows / kMergeRows && most < grid && parts * most <= 3 * grid) parts *= 2;
         cfg.gridDim = dim3(most, parts);
         cfg.blockDim = dim3(kMergeWarps * 32);
         cfg.dynamicSmemBytes = 0;
-        e = cudaLaunchKernelEx(&cfg, most < grid ? merge_kernel<false> : merge_kernel<true>, p);
+        e = cudaLaunchKernelEx(&cfg, most < grid ? merge_kernel<false, false> : p.max_rounds > 1 ? merge_kernel<true, true> : merge_kernel<true, false>, p);
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {

@@ -16,8 +16,8 @@
 //     odd key tiles; their states are joined at the end.
 //
 // The items of the batch, laid end to end by cost, are cut into one range per
-// CTA (one persistent CTA per SM), planned by every CTA from the lengths on
-// the device. A cut near an item's end moves there; any other leaves fp32
+// CTA (one persistent CTA per SM; three one after the other where that keeps
+// the contexts in L2), planned by every CTA from the lengths on the device. A cut near an item's end moves there; any other leaves fp32
 // partial results that merge_kernel joins in a fixed order.
 //
 // What no row sees never enters a sum: masked scores are replaced before the
@@ -27,8 +27,8 @@
 //
 // A group of G heads and T rows do G T operations a byte of K and V: prompts
 // are bound by the tensor core (16,411 tokens of 64 / 8 heads: 2.6 to 2.9 ms,
-// 1.5 to 1.7 PFLOP/s of a measured 1.9; chunks of 1,000 tokens on 9,000 cached
-// ones 1.86 ms, 1.54 PFLOP/s), trees by bandwidth (64 trees of 16 drafts on
+// 1.5 to 1.7 PFLOP/s of a measured 1.7 under the power cap to 1.9; chunks of
+// 1,000 tokens on 9,000 cached ones 2.0 ms, 1.43 PFLOP/s), trees by bandwidth (64 trees of 16 drafts on
 // 1,024 tokens: 98 us, 4.6 of 6.8 TB/s), short items by their starts and ends
 // (16 packed prompts of 512 tokens: 99 us, 0.62 PFLOP/s).
 #pragma once
@@ -75,6 +75,13 @@ constexpr int kPieces = 4;          // pieces described ahead
 
 constexpr size_t kWsHeader = 256;
 constexpr int kMaxGrid = 1024;
+// Ranges of a CTA, one after the other: more than one where many items each
+// read the same long contexts, all heads' contexts at once would exceed L2, and
+// there are items enough (rounds_of). The CTAs then share a third of the heads
+// at a time.
+constexpr int kRounds = 3;
+constexpr float kRoundBytes = 96.f * (1 << 20);  // of L2's 129 MB
+constexpr float kRoundReads = 16.f;
 
 struct Params {
     __nv_bfloat16* out;
@@ -85,10 +92,12 @@ struct Params {
     const int32_t* context_lens;
     const int32_t* query_starts;
     uint32_t* err;
-    struct Split* splits;   // [grid]
-    float2* part_ml;        // [2 * grid][256]
-    float* part_o;          // [2 * grid][256][128]
+    struct Split* splits;   // [ranges], as are:
+    float2* part_ml;        // [2 * ranges][256]
+    float* part_o;          // [2 * ranges][256][128]
+    int* rounds;            // of this call, for the join
     int grid, one;          // CTAs; items of one query tile only
+    int max_rounds;         // kRounds where the call may take them, else 1
     int num_seqs, num_tokens, hq, hkv, group, tpt;  // tpt: tokens of a tile
     int max_blocks, num_blocks, bt;
     float scale_log2;
@@ -121,6 +130,7 @@ struct __align__(16) Piece {
     int kend, nct;      // keys in the cache it needs; their tiles
     int s, h;           // sequence, KV head
     int seq_n, seq_tok0, ctx;  // query rows and first row of the sequence, its tokens in the cache
+    int slot;           // of its partial results
     int any_bad;        // set by the cleaning warps: values were taken out
 };
 
@@ -138,8 +148,10 @@ struct __align__(16) Misc {
     union {
         struct {  // the plan; the loader has read it before it describes the first piece
             long long scan[kThreads / 32];
-            int cut[2][4];  // sequence, head, item, tile of the range's ends
-            Seq cut_seq;    // the first sequence
+            float keys[kThreads / 32], items[kThreads / 32];
+            int cut[kRounds][2][4];  // sequence, head, item, tile of the ranges' ends
+            Seq cut_seq;             // the first one's first sequence
+            int rounds;
         };
         float2 ml[2][kRows];  // one-tile items: the streams' row states
     };
@@ -258,19 +270,38 @@ struct Walk {
     int s1, h1, i1, t1;  // the range's end
     int ta, tb;          // tiles of the piece
     bool first;
+    int cuts, round, rounds;  // lane i: the i-th number of the ranges' ends
 
-    __device__ __forceinline__ Walk(const Params& prm, const Misc& m) : p(prm), first(true) {
-        it.s = m.cut[0][0];
-        it.h = m.cut[0][1];
-        it.i = m.cut[0][2];
-        ta = m.cut[0][3];
+    __device__ __forceinline__ Walk(const Params& prm, const Misc& m) : p(prm), round(0), rounds(m.rounds) {
+        const int lane = threadIdx.x & 31;
+        cuts = lane < kRounds * 8 ? (&m.cut[0][0][0])[lane] : 0;
         it.q = m.cut_seq;
-        s1 = m.cut[1][0];
-        h1 = m.cut[1][1];
-        i1 = m.cut[1][2];
-        t1 = m.cut[1][3];
+        open();
+    }
+    __device__ __forceinline__ void open() {
+        auto get = [&](int i) { return __shfl_sync(0xFFFFFFFFu, cuts, round * 8 + i); };
+        it.s = get(0);
+        it.h = get(1);
+        it.i = get(2);
+        ta = get(3);
+        s1 = get(4);
+        h1 = get(5);
+        i1 = get(6);
+        t1 = get(7);
+        first = true;
     }
     __device__ __forceinline__ bool next() {
+        if (next_of_range()) return true;
+#pragma unroll 1
+        while (round + 1 < rounds) {
+            ++round;
+            open();
+            if (it.s < p.num_seqs) it.q = load_seq<kTree, kOne>(p, it.s, nullptr);
+            if (next_of_range()) return true;
+        }
+        return false;
+    }
+    __device__ __forceinline__ bool next_of_range() {
         bool enter = first, step = !first;  // a sequence was entered; go on to another item
         if (first) {
             if (it.s >= p.num_seqs) return false;
@@ -333,6 +364,7 @@ struct Walk {
         d.seq_n = it.q.n;
         d.seq_tok0 = it.q.tok0;
         d.ctx = it.q.ctx;
+        d.slot = 2 * (round * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x)) + (ta == 0 ? 1 : 0);
         d.any_bad = 0;
     }
 };
@@ -351,6 +383,20 @@ __device__ __forceinline__ RingEntry ring_entry(bool two, int pos, int count) {
 __device__ __forceinline__ int ring_k(bool two, int j) { return two ? 2 * j : max(2 * j - 1, 0); }
 __device__ __forceinline__ int ring_v(bool two, int j, int count) { return two || j == count - 1 ? 2 * j + 1 : 2 * j + 2; }
 
+template <bool kTree, bool kOne>
+__host__ __device__ constexpr int rounds_max() { return kTree || kOne ? 1 : kRounds; }  // others read their contexts a few times at the most
+
+// The rounds of a call: keys that it reads and items that it has (of all KV
+// heads), and their cost. Chunks of 1,000 tokens on 9,000 cached ones, 64 / 8
+// heads, 0.5 GB of inputs, read 9 GB from memory in one round, which slows the
+// products where power bounds the clocks: call after call 2,210 us in one
+// round, 2,140 in two, 2,000 in three or four. Items read by few others gain
+// nothing, and each cut more costs a join.
+__device__ __forceinline__ int rounds_of(float keys, float items, float cost, int grid) {
+    const bool many = cost >= kRoundReads * kCostTwo * keys && items >= 4.f * grid;
+    return many && keys * (4 * kDim) > kRoundBytes ? kRounds : 1;
+}
+
 // Every thread of the CTA: the ends of this CTA's range, and the description
 // of the item that its end cuts. Each half of the threads goes over all
 // sequences and finds one end.
@@ -361,6 +407,7 @@ __device__ void plan(const Params& p, Misc& m) {
     const int per = (p.num_seqs + kHalf - 1) / kHalf;
     const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
     long long sum = 0;
+    float keys = 0.f, items = 0.f;  // read at least once; the same in every CTA
     uint32_t bad = 0;
     Seq seq0 = {};
 #pragma unroll 1
@@ -369,6 +416,10 @@ __device__ void plan(const Params& p, Misc& m) {
         if (s == s0) seq0 = q;
         const Cost c = cost_of<kTree, kOne>(q, p.tpt);
         sum += (c.first(q.full) + c.last) * p.hkv;
+        if (rounds_max<kTree, kOne>() > 1 && p.max_rounds > 1 && q.n > 0) {
+            keys += static_cast<float>(q.ctx);
+            items += static_cast<float>(q.full + (q.rest != 0));
+        }
     }
     if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
     long long incl = sum;
@@ -378,8 +429,19 @@ __device__ void plan(const Params& p, Misc& m) {
         if (lane >= d) incl += o;
     }
     if (lane == 31) m.scan[e * kHalfWarps + warp] = incl;
-    if (tid < 4) m.cut[e][tid] = tid == 0 ? p.num_seqs : 0;
-    if (threadIdx.x == 0) p.splits[blockIdx.x].ntiles = 0;
+    if (rounds_max<kTree, kOne>() > 1 && p.max_rounds > 1) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            keys += __shfl_xor_sync(0xFFFFFFFFu, keys, d);
+            items += __shfl_xor_sync(0xFFFFFFFFu, items, d);
+        }
+        if (lane == 0) {
+            m.keys[e * kHalfWarps + warp] = keys;
+            m.items[e * kHalfWarps + warp] = items;
+        }
+    }
+    if (tid < 4 * kRounds) m.cut[tid >> 2][e][tid & 3] = (tid & 3) == 0 ? p.num_seqs : 0;
+    if (threadIdx.x < p.max_rounds) p.splits[threadIdx.x * gridDim.x + blockIdx.x].ntiles = 0;
     __syncthreads();
     long long before = incl - sum, total = 0;
 #pragma unroll
@@ -388,64 +450,81 @@ __device__ void plan(const Params& p, Misc& m) {
         if (w < warp) before += v;
         total += v;
     }
-    const int ranges = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total / kMinRange, 1ll)));
+    int rounds = 1;
+    if (rounds_max<kTree, kOne>() > 1 && p.max_rounds > 1) {
+        keys = items = 0.f;
+#pragma unroll
+        for (int w = 0; w < kHalfWarps; ++w) {
+            keys += m.keys[e * kHalfWarps + w];
+            items += m.items[e * kHalfWarps + w];
+        }
+        rounds = rounds_of(keys * p.hkv, items * p.hkv, static_cast<float>(total), gridDim.x);
+    }
+    if (threadIdx.x == 0) {
+        m.rounds = rounds;
+        if (p.max_rounds > 1 && blockIdx.x == 0) *p.rounds = rounds;
+    }
+    const int ranges = static_cast<int>(min(static_cast<long long>(gridDim.x) * rounds, max(total / kMinRange, 1ll)));
     // a range's length, no less than its share (by some 2^-20 more)
     const long long chunk = static_cast<long long>(__ll2float_ru(total) / ranges * 1.000001f) + 1;
-    const int b = blockIdx.x;
-    const long long x = chunk * (b + e);
-    if (x < before || x >= before + sum) return;  // at or past the line's end: behind the last sequence
-    long long at = before;
 #pragma unroll 1
-    for (int s = s0; s < s1; ++s) {
-        Item it;
-        it.q = s == s0 ? seq0 : load_seq<kTree, kOne>(p, s, nullptr);
-        const Cost c = cost_of<kTree, kOne>(it.q, p.tpt);
-        const long long hc = c.first(it.q.full) + c.last;
-        if (x >= at + hc * p.hkv) {
-            at += hc * p.hkv;
-            continue;
-        }
-        it.s = s;
-        // estimates, then the exact head and item
-        long long off = x - at;
-        it.h = min(static_cast<int>(__ll2float_rn(off) / __ll2float_rn(hc)), p.hkv - 1);
-        off -= hc * it.h;
-        if (off < 0) {
-            off += hc;
-            --it.h;
-        } else if (off >= hc) {
-            off -= hc;
-            ++it.h;
-        }
-        const float fa = __ll2float_rn(c.a), fo = __ll2float_rn(off);
-        it.i = min(static_cast<int>(2.f * fo / (fa + sqrtf(fa * fa + 4.f * c.b * fo))), it.q.full - (it.q.rest == 0));
+    for (int r = 0; r < rounds; ++r) {
+        const int b = r * gridDim.x + blockIdx.x;
+        const long long x = chunk * (b + e);
+        if (x < before || x >= before + sum) continue;  // at or past the line's end: behind the last sequence
+        long long at = before;
 #pragma unroll 1
-        while (c.first(it.i) > off) --it.i;
+        for (int s = s0; s < s1; ++s) {
+            Item it;
+            it.q = s == s0 ? seq0 : load_seq<kTree, kOne>(p, s, nullptr);
+            const Cost c = cost_of<kTree, kOne>(it.q, p.tpt);
+            const long long hc = c.first(it.q.full) + c.last;
+            if (x >= at + hc * p.hkv) {
+                at += hc * p.hkv;
+                continue;
+            }
+            it.s = s;
+            // estimates, then the exact head and item
+            long long off = x - at;
+            it.h = min(static_cast<int>(__ll2float_rn(off) / __ll2float_rn(hc)), p.hkv - 1);
+            off -= hc * it.h;
+            if (off < 0) {
+                off += hc;
+                --it.h;
+            } else if (off >= hc) {
+                off -= hc;
+                ++it.h;
+            }
+            const float fa = __ll2float_rn(c.a), fo = __ll2float_rn(off);
+            it.i = min(static_cast<int>(2.f * fo / (fa + sqrtf(fa * fa + 4.f * c.b * fo))), it.q.full - (it.q.rest == 0));
 #pragma unroll 1
-        while (it.i < it.q.full - (it.q.rest == 0) && c.first(it.i + 1) <= off) ++it.i;
-        set_item<kTree, kOne>(p, it);
-        const long long start = x - off + c.first(it.i);
-        const long long cost = it.i < it.q.full ? c.first(it.i + 1) - c.first(it.i) : c.last;
-        const int t = cut_tile(x - start, cost, it.cut_tiles());
-        m.cut[e][0] = s;
-        m.cut[e][1] = it.h;
-        m.cut[e][2] = it.i;
-        m.cut[e][3] = t;
-        if (e == 0) m.cut_seq = it.q;
-        // this CTA has the item's first piece and not its last
-        if (e == 1 && t > 0 && t < it.cut_tiles() &&
-            (x - chunk <= start || cut_tile(x - chunk - start, cost, it.cut_tiles()) == 0)) {
-            Split sp;
-            sp.start = start;
-            sp.cost = cost;
-            sp.chunk = chunk;
-            sp.ntiles = it.cut_tiles();
-            sp.tok0 = it.tok0;
-            sp.ntok = it.ntok;
-            sp.head0 = it.h * p.group;
-            p.splits[b] = sp;
+            while (c.first(it.i) > off) --it.i;
+#pragma unroll 1
+            while (it.i < it.q.full - (it.q.rest == 0) && c.first(it.i + 1) <= off) ++it.i;
+            set_item<kTree, kOne>(p, it);
+            const long long start = x - off + c.first(it.i);
+            const long long cost = it.i < it.q.full ? c.first(it.i + 1) - c.first(it.i) : c.last;
+            const int t = cut_tile(x - start, cost, it.cut_tiles());
+            m.cut[r][e][0] = s;
+            m.cut[r][e][1] = it.h;
+            m.cut[r][e][2] = it.i;
+            m.cut[r][e][3] = t;
+            if (e == 0 && r == 0) m.cut_seq = it.q;
+            // this CTA has the item's first piece and not its last
+            if (e == 1 && t > 0 && t < it.cut_tiles() &&
+                (x - chunk <= start || cut_tile(x - chunk - start, cost, it.cut_tiles()) == 0)) {
+                Split sp;
+                sp.start = start;
+                sp.cost = cost;
+                sp.chunk = chunk;
+                sp.ntiles = it.cut_tiles();
+                sp.tok0 = it.tok0;
+                sp.ntok = it.ntok;
+                sp.head0 = it.h * p.group;
+                p.splits[b] = sp;
+            }
+            break;
         }
-        return;
     }
 }
 
@@ -548,7 +627,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (smem_base & 1023) {  // the swizzle atoms need it; dynamic shared memory starts so, with no static beside it
         griddep_wait();
         if (tid == 0) {
-            p.splits[blockIdx.x].ntiles = 0;
+            for (int r = 0; r < p.max_rounds; ++r) p.splits[r * gridDim.x + blockIdx.x].ntiles = 0;
+            if (blockIdx.x == 0) *p.rounds = 1;
             atomicOr(p.err, PKV_DEVERR_TIMEOUT);
         }
         return;
@@ -746,7 +826,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const bool whole = it.whole;
             const int t_lo = max(first_masked, it.ta), t_hi = it.ta + it.count;
             const uint32_t(*bad)[4] = m.bad[n_item % kPieces];
-            const long long slot = 2ll * blockIdx.x + (it.ta == 0 ? 1 : 0);
+            const long long slot = it.slot;
 
             // what the sum is divided by; no key seen: zeros; only keys of weight zero: NaN, as 0 / 0
             auto inverse = [](const float2& v) {
@@ -1227,8 +1307,8 @@ struct RowSums {
     }
 };
 
-template <bool kEvery>
-__global__ void __launch_bounds__(kMergeWarps * 32, kEvery ? 3 : 2) merge_kernel(const Params p) {
+template <bool kEvery, bool kLoop>
+__global__ void __launch_bounds__(kMergeWarps * 32, kEvery && !kLoop ? 3 : 2) merge_kernel(const Params p) {
     __shared__ int slots[kMaxGrid];  // of the ranges from the first piece's on; -1: no piece in it
     __shared__ int last, item, marks[kMergeWarps];
     __shared__ float4 shared_o[kMergeWarps][kMergeRows][32];
@@ -1239,7 +1319,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kEvery ? 3 : 2) merge_kernel
     __syncthreads();
     griddep_wait();
     // the CTA that describes this block's item
-    int c0 = blockIdx.x;
+    int c0 = blockIdx.x, ranges = p.grid;
+    if (kLoop) {
+        ranges *= *const_cast<const volatile int*>(p.rounds);
+    }
     if (!kEvery) {
         for (int base = 0, found = 0; base < p.grid; base += kMergeWarps * 32) {
             const int c = base + threadIdx.x;
@@ -1258,90 +1341,96 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kEvery ? 3 : 2) merge_kernel
         c0 = item;
         if (c0 < 0) return;
     }
-    const Split sp = p.splits[c0];
-    if (sp.ntiles == 0) return;
-    const int block_rows = (p.one ? 1 : 2) * kRows / gridDim.y;
-    auto row_token = [&](int r) { return (r >> 7) * p.tpt + (r & 127) / p.group; };  // the second query tile starts at row 128
-    if (row_token(blockIdx.y * block_rows) >= sp.ntok) return;
-    auto tiles_before = [&](int c) {  // tiles of the item in the ranges up to c0 + c
-        const long long end = sp.chunk * (c0 + c + 1) - sp.start;
-        return end >= sp.cost ? sp.ntiles : cut_tile(end, sp.cost, sp.ntiles);
-    };
-    // the piece in the c-th range from the first piece's on, -1 if there is none
-    auto slot_of = [&](int c, bool& ends) {
-        const int t = tiles_before(c), before = c == 0 ? 0 : tiles_before(c - 1);
-        ends = t == sp.ntiles || c0 + c == p.grid - 1;
-        return t > before ? 2 * (c0 + c) + (c == 0 ? 1 : 0) : -1;
-    };
+#pragma unroll 1
+    for (; c0 < ranges; c0 += kLoop ? static_cast<int>(gridDim.x) : ranges) {
+        const Split sp = p.splits[c0];
+        if (sp.ntiles == 0) continue;
+        const int block_rows = (p.one ? 1 : 2) * kRows / gridDim.y;
+        auto row_token = [&](int r) { return (r >> 7) * p.tpt + (r & 127) / p.group; };  // the second query tile starts at row 128
+        if (row_token(blockIdx.y * block_rows) >= sp.ntok) continue;
+        auto tiles_before = [&](int c) {  // tiles of the item in the ranges up to c0 + c
+            const long long end = sp.chunk * (c0 + c + 1) - sp.start;
+            return end >= sp.cost ? sp.ntiles : cut_tile(end, sp.cost, sp.ntiles);
+        };
+        // the piece in the c-th range from the first piece's on, -1 if there is none
+        auto slot_of = [&](int c, bool& ends) {
+            const int t = tiles_before(c), before = c == 0 ? 0 : tiles_before(c - 1);
+            ends = t == sp.ntiles || c0 + c == ranges - 1;
+            return t > before ? 2 * (c0 + c) + (c == 0 ? 1 : 0) : -1;
+        };
 
-    RowSums sums[kMergeRows];
-    auto gather = [&](int first, int from, int to, auto slot_at) {
+        RowSums sums[kMergeRows];
+        auto gather = [&](int first, int from, int to, auto slot_at) {
 #pragma unroll
-        for (int i = 0; i < kMergeRows; ++i) sums[i] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-        for (int c = from; c < to; c += kMergeAhead) {
-            float2 st[kMergeAhead][kMergeRows];
-            float4 v[kMergeAhead][kMergeRows];
+            for (int i = 0; i < kMergeRows; ++i) sums[i] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+            for (int c = from; c < to; c += kMergeAhead) {
+                float2 st[kMergeAhead][kMergeRows];
+                float4 v[kMergeAhead][kMergeRows];
 #pragma unroll
-            for (int a = 0; a < kMergeAhead; ++a) {
-                const int slot = c + a < to ? slot_at(c + a) : -1;
+                for (int a = 0; a < kMergeAhead; ++a) {
+                    const int slot = c + a < to ? slot_at(c + a) : -1;
 #pragma unroll
-                for (int i = 0; i < kMergeRows; ++i) {
-                    st[a][i] = make_float2(-INFINITY, 0.f);
-                    v[a][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (slot < 0) continue;
-                    const long long row = static_cast<long long>(slot) * 2 * kRows + first + i;
-                    st[a][i] = p.part_ml[row];
-                    v[a][i] = *reinterpret_cast<const float4*>(p.part_o + row * kDim + lane * 4);
+                    for (int i = 0; i < kMergeRows; ++i) {
+                        st[a][i] = make_float2(-INFINITY, 0.f);
+                        v[a][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (slot < 0) continue;
+                        const long long row = static_cast<long long>(slot) * 2 * kRows + first + i;
+                        st[a][i] = p.part_ml[row];
+                        v[a][i] = *reinterpret_cast<const float4*>(p.part_o + row * kDim + lane * 4);
+                    }
                 }
+#pragma unroll
+                for (int a = 0; a < kMergeAhead; ++a)
+#pragma unroll
+                    for (int i = 0; i < kMergeRows; ++i) sums[i].add(st[a][i].x, st[a][i].y, v[a][i]);
             }
+        };
+        auto store = [&](int row, const RowSums& x) {
+            const int r = row & 127, row_tok = r / p.group, tok = row_token(row);
+            if (row_tok >= p.tpt || tok >= sp.ntok) return;
+            const float inv = x.l != 0.f ? 1.f / x.l : x.m == -INFINITY ? 0.f : __int_as_float(0x7FC00000);
+            const int head = sp.head0 + r - row_tok * p.group;
+            *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(sp.tok0 + tok) * p.hq + head) * kDim + lane * 4) =
+                make_uint2(pack_bf16x2(x.o.x * inv, x.o.y * inv), pack_bf16x2(x.o.z * inv, x.o.w * inv));
+        };
+        bool ends;
+        const int mine = slot_of(lane, ends);
+        const int few = __ffs(__ballot_sync(0xFFFFFFFFu, ends));
+        if (few != 0 && few <= kMergeShare) {
+            for (int g = warp; g < block_rows / kMergeRows; g += kMergeWarps) {
+                const int first = blockIdx.y * block_rows + g * kMergeRows;
+                gather(first, 0, few, [&](int c) { return __shfl_sync(0xFFFFFFFFu, mine, c); });
 #pragma unroll
-            for (int a = 0; a < kMergeAhead; ++a)
-#pragma unroll
-                for (int i = 0; i < kMergeRows; ++i) sums[i].add(st[a][i].x, st[a][i].y, v[a][i]);
+                for (int i = 0; i < kMergeRows; ++i) store(first + i, sums[i]);
+            }
+            continue;
         }
-    };
-    auto store = [&](int row, const RowSums& x) {
-        const int r = row & 127, row_tok = r / p.group, tok = row_token(row);
-        if (row_tok >= p.tpt || tok >= sp.ntok) return;
-        const float inv = x.l != 0.f ? 1.f / x.l : x.m == -INFINITY ? 0.f : __int_as_float(0x7FC00000);
-        const int head = sp.head0 + r - row_tok * p.group;
-        *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(sp.tok0 + tok) * p.hq + head) * kDim + lane * 4) =
-            make_uint2(pack_bf16x2(x.o.x * inv, x.o.y * inv), pack_bf16x2(x.o.z * inv, x.o.w * inv));
-    };
-    bool ends;
-    const int mine = slot_of(lane, ends);
-    const int few = __ffs(__ballot_sync(0xFFFFFFFFu, ends));
-    if (few != 0 && few <= kMergeShare) {
-        for (int g = warp; g < block_rows / kMergeRows; g += kMergeWarps) {
-            const int first = blockIdx.y * block_rows + g * kMergeRows;
-            gather(first, 0, few, [&](int c) { return __shfl_sync(0xFFFFFFFFu, mine, c); });
-#pragma unroll
-            for (int i = 0; i < kMergeRows; ++i) store(first + i, sums[i]);
-        }
-        return;
-    }
-    for (int c = threadIdx.x; c0 + c < p.grid; c += blockDim.x) {
-        slots[c] = slot_of(c, ends);
-        if (ends) atomicMin(&last, c);
-    }
-    __syncthreads();
-    const int pieces = last + 1;
-    for (int g = 0; g < block_rows / kMergeRows; ++g) {
-        const int first = blockIdx.y * block_rows + g * kMergeRows;
-        if (row_token(first) >= sp.ntok) break;
-        gather(first, pieces * warp / kMergeWarps, pieces * (warp + 1) / kMergeWarps,
-               [&](int c) { return slots[c]; });
-#pragma unroll
-        for (int i = 0; i < kMergeRows; ++i) {
-            shared_o[warp][i][lane] = sums[i].o;
-            if (lane == 0) shared_ml[warp][i] = make_float2(sums[i].m, sums[i].l);
+        for (int c = threadIdx.x; c0 + c < ranges; c += blockDim.x) {
+            slots[c] = slot_of(c, ends);
+            if (ends) atomicMin(&last, c);
         }
         __syncthreads();
-        if (warp < kMergeRows) {
-            RowSums x = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-            for (int w = 0; w < kMergeWarps; ++w) x.add(shared_ml[w][warp].x, shared_ml[w][warp].y, shared_o[w][warp][lane]);
-            store(first + warp, x);
+        const int pieces = last + 1;
+        for (int g = 0; g < block_rows / kMergeRows; ++g) {
+            const int first = blockIdx.y * block_rows + g * kMergeRows;
+            if (row_token(first) >= sp.ntok) break;
+            gather(first, pieces * warp / kMergeWarps, pieces * (warp + 1) / kMergeWarps,
+                   [&](int c) { return slots[c]; });
+#pragma unroll
+            for (int i = 0; i < kMergeRows; ++i) {
+                shared_o[warp][i][lane] = sums[i].o;
+                if (lane == 0) shared_ml[warp][i] = make_float2(sums[i].m, sums[i].l);
+            }
+            __syncthreads();
+            if (warp < kMergeRows) {
+                RowSums x = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+                for (int w = 0; w < kMergeWarps; ++w) x.add(shared_ml[w][warp].x, shared_ml[w][warp].y, shared_o[w][warp][lane]);
+                store(first + warp, x);
+            }
+            __syncthreads();
         }
+        if (!kLoop) return;
+        if (threadIdx.x == 0) last = kMaxGrid;  // every warp has read it
         __syncthreads();
     }
 }

@@ -111,6 +111,32 @@ def test_items_in_many_pieces(pkv, tree, new, held, hq, hkv):
     _run(pkv, Batch(hq + new[0], new, held, hq, hkv, 16, first_row=1, rows_behind=1), tree=tree)
 
 
+@pytest.mark.parametrize("new,held", [([1500, 700, 0, 300], [26003, 9001, 17, 300]), ([2500], [26000])])
+def test_chunks_whose_contexts_exceed_the_l2_cache(pkv, new, held):
+    """Ranges in several rounds; some rows of each sequence, as decode rows of the oracle."""
+    b = Batch(new[0], new, held, 64, 8, 16, first_row=2, rows_behind=3)
+    d = _dev(pkv, b, False)
+    ws = pkv.PrefillWorkspace()
+    out = torch.full_like(d["q"], 7.0)
+    _call(pkv, d, b.scale, out=out, workspace=ws)
+    again = torch.full_like(d["q"], 5.0)
+    _call(pkv, d, b.scale, out=again, workspace=ws)
+    assert ws.read_error() == 0
+    lo, hi = int(b.starts[0]), int(b.starts[-1])
+    assert (out[:lo] == 7.0).all() and (out[hi:] == 7.0).all()
+    assert torch.equal(out[lo:hi], again[lo:hi])
+    assert torch.isfinite(out.float()).all()
+    rows, seqs, ctx = [], [], []
+    for s, n in enumerate(new):
+        for i in sorted({0, 1, 31, 32, n // 3, n // 2, n - 33, n - 2, n - 1} if n else ()):
+            rows.append(int(b.starts[s]) + i)
+            seqs.append(s)
+            ctx.append(held[s] - n + i + 1)
+    ref = po.prompt_attention(b.q[rows], b.k, b.v, b.tables[seqs], np.array(ctx, np.int32),
+                              np.arange(len(rows) + 1, dtype=np.int32), b.scale)
+    _check(out[rows], ref)
+
+
 def test_many_sequences(pkv):
     rng = np.random.default_rng(5)
     held = [int(x) for x in rng.integers(1, 60, size=700)]
