@@ -156,6 +156,7 @@ CASES = [
     ([(60, 131072)], 1, 8, True, False, 152),
     ([(1, 1 + s % 5) for s in range(500)], 1, 2, False, True, 152),
     ([(33, 30), (700, 700), (1, 9000)], 3, 3, False, False, 7),
+    ([(1500, 26003), (700, 9001), (0, 17), (300, 300)], 8, 8, False, False, 3 * 152),  # three ranges a CTA
 ]
 for k in range(12):
     r = np.random.default_rng(k)
