@@ -206,7 +206,8 @@ pkv_status run(const void* q, const void* k_cache, const void* v_cache, const vo
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_for(tree, one), tm_q, tm_k, tm_v, tm_kd, tm_vd, p);
-    // an item of no more keys than the tables hold is never cut: nothing to join
+    // an item costs no more than the keys of a table row (cost_of): where that is
+    // too little to be cut, there is nothing to join
     if (e == cudaSuccess && kCostTwo * most_keys + cost_item(tree) > kWhole) {
         // where there can be fewer split items than CTAs, 4 to 32 rows a block, for
         // 3 to 6 blocks an SM, else 32 (2,000 rows of 8 heads, 64 items: 27.5 us with

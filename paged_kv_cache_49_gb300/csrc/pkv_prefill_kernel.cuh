@@ -216,10 +216,12 @@ template <bool kTree, bool kOne>
 __device__ __forceinline__ Cost cost_of(const Seq& q, int tpt) {
     constexpr int kOneCost = cost_one(kTree), kFull = kOne ? kOneCost : kCostTwo, kItemCost = cost_item(kTree);
     Cost c;
-    // keys of item i of a prompt: ctx - n + (i + 1) * its tokens (fewer than that
-    // in a chunk longer than its context: then only the balance is off)
-    const long long keys = kTree ? q.ctx + static_cast<long long>(kKeys) : max(q.ctx - q.n, 0);
-    c.b = kTree ? 0 : kFull * item_tokens<kOne>(tpt) / 2;
+    // keys of item i of a prompt: ctx - n + (i + 1) * its tokens; of a chunk longer
+    // than its context, all of ctx for every item. So none costs more than the keys
+    // of its table row would, by which the host leaves out the join.
+    const bool flat = kTree || q.n > q.ctx;
+    const long long keys = kTree ? q.ctx + static_cast<long long>(kKeys) : flat ? q.ctx : q.ctx - q.n;
+    c.b = flat ? 0 : kFull * item_tokens<kOne>(tpt) / 2;
     c.a = kFull * keys + kItemCost + c.b;
     c.last = q.rest ? (q.rest > tpt ? kCostTwo : kOneCost) * (kTree ? keys : static_cast<long long>(q.ctx)) + kItemCost : 0;
     return c;
