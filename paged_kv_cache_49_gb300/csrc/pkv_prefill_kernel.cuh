@@ -1281,7 +1281,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 
 // Joins the pieces of the items that cuts split: kEvery, block x serves the item
 // that CTA x describes, if it does; else, where there are fewer items than CTAs,
-// the x-th of them, so that more blocks can share its rows (y). A warp takes
+// the x-th of them (and every gridDim.x-th behind it), so that more blocks can
+// share its rows (y). A warp takes
 // kMergeRows rows of all pieces, read kMergeAhead at a time (one row of one
 // piece at a time, the kernel was as long as their latencies: 13 us behind the
 // ragged prompts' 65); of an item in more than kMergeShare pieces -- few rows on
@@ -1317,7 +1318,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kEvery && !kLoop ? 3 : 2) me
     __shared__ float2 shared_ml[kMergeWarps][kMergeRows];
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (threadIdx.x == 0) last = kMaxGrid, item = -1;
+    if (threadIdx.x == 0) last = kMaxGrid;
     __syncthreads();
     griddep_wait();
     // the CTA that describes this block's item
@@ -1325,26 +1326,35 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kEvery && !kLoop ? 3 : 2) me
     if (kLoop) {
         ranges *= *const_cast<const volatile int*>(p.rounds);
     }
-    if (!kEvery) {
-        for (int base = 0, found = 0; base < p.grid; base += kMergeWarps * 32) {
+    int rank = blockIdx.x, found = 0;  // !kEvery: of the item among the split ones; how many those are
+    auto find = [&] {
+        found = 0;
+        for (int base = 0; base < p.grid; base += kMergeWarps * 32) {
             const int c = base + threadIdx.x;
             const bool split = c < p.grid && p.splits[c].ntiles != 0;
             const uint32_t mask = __ballot_sync(0xFFFFFFFFu, split);
             if (lane == 0) marks[warp] = __popc(mask);
             __syncthreads();
-            int rank = found + __popc(mask & ((1u << lane) - 1u));
+            int at = found + __popc(mask & ((1u << lane) - 1u));
             for (int w = 0; w < kMergeWarps; ++w) {
-                if (w < warp) rank += marks[w];
+                if (w < warp) at += marks[w];
                 found += marks[w];
             }
-            if (split && rank == static_cast<int>(blockIdx.x)) item = c;
+            if (split && at == rank) item = c;
             __syncthreads();
         }
-        c0 = item;
-        if (c0 < 0) return;
-    }
+        return rank < found ? item : ranges;
+    };
+    auto next = [&] {
+        if (kEvery) return c0 + (kLoop ? static_cast<int>(gridDim.x) : ranges);
+        // one turn, but where query_starts lays sequences over the same rows: then
+        // there are more items than the host counted
+        rank += gridDim.x;
+        return rank < found ? find() : ranges;
+    };
+    if (!kEvery) c0 = find();
 #pragma unroll 1
-    for (; c0 < ranges; c0 += kLoop ? static_cast<int>(gridDim.x) : ranges) {
+    for (; c0 < ranges; c0 = next()) {
         const Split sp = p.splits[c0];
         if (sp.ntiles == 0) continue;
         const int block_rows = (p.one ? 1 : 2) * kRows / gridDim.y;
@@ -1431,7 +1441,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kEvery && !kLoop ? 3 : 2) me
             }
             __syncthreads();
         }
-        if (!kLoop) return;
+        if (kEvery && !kLoop) return;
         if (threadIdx.x == 0) last = kMaxGrid;  // every warp has read it
         __syncthreads();
     }

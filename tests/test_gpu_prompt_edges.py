@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import prompt_attention as po
 from tests.prompt_batches import Batch
 from tests.test_gpu_prompt_attention import _call, _check, _dev, _ref, pkv  # noqa: F401
 
@@ -45,3 +46,19 @@ def test_a_context_clamped_to_its_table(pkv):  # noqa: F811
     assert ws.read_error() == pkv.DEVERR_CONTEXT
     _check(out, _ref(b, False))
     assert np.isfinite(out.float().cpu().numpy()).all()
+
+
+def test_sequences_laid_over_the_same_rows(pkv):  # noqa: F811
+    """query_starts that goes back: more items than the rows could have. The bit
+    is set, and the sequence that has its rows to itself is exact."""
+    held = [20011] * 10
+    b = Batch(32, [320] + [0] * 8 + [40], held, 8, 1, 16)
+    d = _dev(pkv, b, False)
+    d["starts"].copy_(torch.tensor([0, 320] * 5 + [360], dtype=torch.int32))
+    ws = pkv.PrefillWorkspace()
+    out = torch.full_like(d["q"], 7.0)
+    _call(pkv, d, b.scale, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    assert ws.read_error() == pkv.DEVERR_QUERY
+    ref = po.prompt_attention(b.q[320:], b.k, b.v, b.tables[9:], b.ctx[9:], np.array([0, 40]), b.scale)
+    _check(out[320:], ref)
