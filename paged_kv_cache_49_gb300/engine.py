@@ -122,6 +122,7 @@ class DraftBuffers:
     masks: torch.Tensor       # int64 [T]
     slots: torch.Tensor       # int64 [T], all -1: nothing is appended yet
     held: list                # the sequences' context lengths
+    parents: list             # the sequences' trees
 
 
 class PagedKVEngine:
@@ -235,7 +236,8 @@ class PagedKVEngine:
             positions += [c + d for d in depth]
         rows = self._rows(seq_ids, [len(p) for p in parents], ctx, positions)
         return DraftBuffers(*rows, masks=torch.tensor(masks, dtype=torch.int64).to(self.device),
-                            slots=torch.full((len(masks),), -1, dtype=torch.int64).to(self.device), held=ctx)
+                            slots=torch.full((len(masks),), -1, dtype=torch.int64).to(self.device), held=ctx,
+                            parents=parents)
 
     def run_drafts(self, db: DraftBuffers, q, k, v, scale: float, workspace, rope=None, out=None, stream=None):
         """The device part: (attention of the drafts, their keys as the cache would
@@ -253,15 +255,19 @@ class PagedKVEngine:
 
     def accept_drafts(self, db: DraftBuffers, paths, k, v, stream=None):
         """Append the accepted drafts, paths[i] = the chosen drafts of sequence i in
-        order, root first; k as run_drafts returned it. Returns the slots in
-        draft order, -1 for the drafts that were not accepted. Where the manager
-        refuses a token (PoolExhausted, ReservationExceeded), the drafts before
-        it are appended all the same and the error is raised. A sequence whose
-        context has grown since prepare_drafts takes no drafts (ValueError)."""
+        order: the first follows the context, each other one the draft before it
+        (their keys are rotated for those positions). k as run_drafts returned it.
+        Returns the slots in draft order, -1 for the drafts that were not
+        accepted. Where the manager refuses a token (PoolExhausted,
+        ReservationExceeded), the drafts before it are appended all the same and
+        the error is raised. A sequence whose context has grown since
+        prepare_drafts takes no drafts (ValueError)."""
         paths = [[int(x) for x in p] for p in paths]
         if len(paths) != len(db.counts) or any(len(set(p)) != len(p) or any(not 0 <= x < n for x in p)
                                                for p, n in zip(paths, db.counts)):
             raise ValueError("one path per sequence, of different drafts of its own")
+        if any(tree[x] != before for p, tree in zip(paths, db.parents) for before, x in zip([-1] + p, p)):
+            raise ValueError("a path's first draft follows the context, and each other one's parent is the draft before it")
         grows = [i for i, p in enumerate(paths) if p]
         if len({db.seq_ids[i] for i in grows}) != len(grows) or any(
                 self.bm.context_len(db.seq_ids[i]) != db.held[i] for i in grows):
