@@ -183,13 +183,18 @@ class PagedKVEngine:
         return torch.cuda.stream(stream)
 
     def prepare_prefill(self, seq_ids, counts, first=None) -> PromptBuffers:
-        """Host bookkeeping of a prefill call: sequence seq_ids[i] brings its next
-        counts[i] prompt tokens, from position first[i] on (default: each
-        prompt's last counts[i] tokens, a whole prompt where that is all of
-        them). Their slots lie in the pages that admission reserved."""
+        """Host bookkeeping of a prefill call: sequence seq_ids[i] brings counts[i]
+        tokens of its prompt, from position first[i] on. Without first they are
+        its last ones: the whole prompt, or the rest of one whose other tokens
+        admission found in the cache or shares with other sequences. A chunk of a
+        longer rest needs first (ValueError): the engine does not keep how far a
+        prompt has come. The slots lie in the pages that admission reserved."""
         seq_ids, counts = list(seq_ids), [int(c) for c in counts]
         if first is None:
             first = [self.bm.context_len(s) - c for s, c in zip(seq_ids, counts)]
+            for s, f, c in zip(seq_ids, first, counts):
+                if c and f > self._in_place(s):
+                    raise ValueError(f"a chunk of {c} of sequence {s}'s {f + c} tokens needs its first position")
         if len(seq_ids) != len(counts) or len(first) != len(counts):
             raise ValueError("one count and one first position per sequence")
         slots, positions = [], []
@@ -198,6 +203,13 @@ class PagedKVEngine:
             positions += range(f, f + c)
         return PromptBuffers(*self._rows(seq_ids, counts, [f + c for f, c in zip(first, counts)], positions),
                              slots=torch.tensor(slots, dtype=torch.int64).to(self.device))
+
+    def _in_place(self, seq_id) -> int:
+        """Leading tokens in blocks that admission found in the cache or that other
+        sequences hold too."""
+        table = self.bm.table(seq_id)
+        shared = next((i for i, b in enumerate(table) if self.bm.refcount(b) < 2), len(table))
+        return max(self.bm.reused.get(seq_id, 0), shared) * self.block_tokens
 
     def _rows(self, seq_ids, counts, context_lens, positions):
         if not seq_ids:

@@ -45,3 +45,42 @@ def test_paths_of_the_tree_pass_the_checks(engine, path, monkeypatch):
     assert called == [slots] and [i for i, s in enumerate(slots) if s >= 0] == sorted(path)
     assert eng.bm.context_len(a) == 14 + len(path)
     assert [slots[i] for i in path] == eng.bm.slots(a, 14, len(path))
+
+
+def test_a_chunk_behind_tokens_that_nothing_wrote_says_where_it_starts(engine):
+    """Without first a prompt's rows are its last ones: right for all of it, or for
+    what follows tokens that are in the cache, and not for its first chunk."""
+    eng = engine()
+    a, b = eng.bm.admit(100, 5), eng.bm.admit(40, 5)
+    for counts in ([33, 40], [99, 40], [100, 39]):
+        with pytest.raises(ValueError, match="first"):
+            eng.prepare_prefill([a, b], counts)
+    done = [0, 0]
+    for counts in ([33, 0], [0, 40], [67, 0]):
+        pb = eng.prepare_prefill([a, b], counts, done)
+        assert pb.positions.tolist() == [f + i for f, c in zip(done, counts) for i in range(c)]
+        done = [d + c for d, c in zip(done, counts)]
+        assert pb.ctx.tolist() == done
+    whole = eng.prepare_prefill([b, a], [40, 100])
+    assert whole.positions.tolist() == [*range(40), *range(100)] and whole.ctx.tolist() == [40, 100]
+    assert eng.prepare_prefill([a, b], [0, 40]).positions.tolist() == [*range(40)]
+
+
+def test_the_rest_behind_cached_and_shared_tokens_needs_no_start(engine):
+    eng = engine(prefix_cache=True)
+    tokens = list(range(100))
+    eng.bm.admit(100, 5, tokens=tokens)
+    c = eng.bm.admit(110, 5, tokens=tokens + list(range(10)))
+    assert eng.prepare_prefill([c], [14]).positions.tolist() == [*range(96, 110)]
+    with pytest.raises(ValueError, match="first"):
+        eng.prepare_prefill([c], [13])
+    eng = engine()
+    eng.bm.admit(70, 5, 0, 64)
+    d = eng.bm.admit(80, 5, 0, 64)
+    assert eng.prepare_prefill([d], [16]).positions.tolist() == [*range(64, 80)]
+    with pytest.raises(ValueError, match="first"):
+        eng.prepare_prefill([d], [15])
+    eng = engine()
+    e = eng.bm.admit(50, 5)
+    f, = eng.bm.fork(e, 1)
+    assert eng.prepare_prefill([f], [7]).positions.tolist() == [*range(43, 50)]
