@@ -197,6 +197,9 @@ class PagedKVEngine:
                     raise ValueError(f"a chunk of {c} of sequence {s}'s {f + c} tokens needs its first position")
         if len(seq_ids) != len(counts) or len(first) != len(counts):
             raise ValueError("one count and one first position per sequence")
+        for s, f, c in zip(seq_ids, first, counts):
+            if f < 0 or c < 0 or f + c > self.bm.context_len(s):
+                raise ValueError(f"positions {f} to {f + c} leave sequence {s}'s {self.bm.context_len(s)} tokens")
         slots, positions = [], []
         for s, f, c in zip(seq_ids, first, counts):
             slots += self.bm.slots(s, f, c) if c else []

@@ -84,3 +84,15 @@ def test_the_rest_behind_cached_and_shared_tokens_needs_no_start(engine):
     e = eng.bm.admit(50, 5)
     f, = eng.bm.fork(e, 1)
     assert eng.prepare_prefill([f], [7]).positions.tolist() == [*range(43, 50)]
+
+
+@pytest.mark.parametrize("counts,first", [([5, 1], [96, 0]), ([101, 1], [0, 0]), ([0, 1], [101, 0]), ([0, 1], [-1, 0]),
+                                          ([3, 1], [-1, 0]), ([-1, 1], [5, 0]), ([1, 40], None), ([4, 3], [100, 0])])
+def test_a_chunk_lies_within_its_sequence(engine, counts, first):
+    """Reserved pages behind the context are the next steps'."""
+    eng = engine()
+    a, b = eng.bm.admit(100, 30), eng.bm.admit(3, 20)
+    with pytest.raises(ValueError):
+        eng.prepare_prefill([a, b], counts, first)
+    with pytest.raises(ValueError):
+        eng.prepare_prefill([a, b], [100, 3], [0])
