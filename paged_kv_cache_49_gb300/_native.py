@@ -773,8 +773,12 @@ class BlockManager:
                                         int(prefix_cache))
         if not self._h:
             raise PkvError(PKV_EINVAL, "pkv_bm_create_ex")
-        self.num_blocks = num_blocks
+        self.num_blocks, self.block_tokens = num_blocks, block_tokens
         self.reused: dict[int, int] = {}
+        # a sequence's prompt tokens, and how many of them from the first on are in
+        # their slots or on their way (the engine counts these)
+        self.prompt: dict[int, int] = {}
+        self.written: dict[int, int] = {}
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -789,7 +793,7 @@ class BlockManager:
         if tokens is None:
             _check(_lib.pkv_bm_admit(self._h, prompt_len, max_new, group, prefix_len, ctypes.byref(sid)),
                    "pkv_bm_admit")
-            self.reused[sid.value] = 0
+            self.reused[sid.value], self.prompt[sid.value], self.written[sid.value] = 0, prompt_len, 0
             return sid.value
         if group >= 0 or len(tokens) != prompt_len:
             raise PkvError(PKV_EINVAL, "pkv_bm_admit_tokens: no group, one token per prompt position")
@@ -797,12 +801,15 @@ class BlockManager:
         reused = ctypes.c_int(0)
         _check(_lib.pkv_bm_admit_tokens(self._h, buf, prompt_len, max_new, ctypes.byref(sid),
                                         ctypes.byref(reused)), "pkv_bm_admit_tokens")
-        self.reused[sid.value] = reused.value
+        self.reused[sid.value], self.prompt[sid.value] = reused.value, prompt_len
+        self.written[sid.value] = reused.value * self.block_tokens
         return sid.value
 
     def fork(self, parent: int, n: int) -> list[int]:
         ids = (ctypes.c_int32 * max(n, 1))()
         _check(_lib.pkv_bm_fork(self._h, parent, n, ids), "pkv_bm_fork")
+        for i in ids[:n]:
+            self.prompt[i], self.written[i] = self.prompt[parent], self.written[parent]
         return list(ids[:n])
 
     def prepare_append(self, seq_ids):
@@ -818,11 +825,14 @@ class BlockManager:
 
     def free(self, seq_id: int) -> None:
         _check(_lib.pkv_bm_free(self._h, seq_id), "pkv_bm_free")
-        self.reused.pop(seq_id, None)
+        for kept in (self.reused, self.prompt, self.written):
+            kept.pop(seq_id, None)
 
     def preempt(self, seq_id: int) -> int:
         n = ctypes.c_int(0)
         _check(_lib.pkv_bm_preempt(self._h, seq_id, ctypes.byref(n)), "pkv_bm_preempt")
+        # all its tokens are to be recomputed
+        self.prompt[seq_id], self.written[seq_id] = self.context_len(seq_id), 0
         return n.value
 
     def resume(self, seq_id: int) -> None:

@@ -170,6 +170,7 @@ class PagedKVEngine:
         slots = self.bm.slots(seq_id, first, int(k.shape[0]))
         st = torch.tensor(slots, dtype=torch.int64).to(self.device, non_blocking=True)
         nat.append(k, v, st, self.k_cache, self.v_cache, self.error, stream)
+        self._wrote(seq_id, first, len(slots))
         return slots
 
     # ---- prompts and drafted tokens -------------------------------------------
@@ -185,15 +186,16 @@ class PagedKVEngine:
     def prepare_prefill(self, seq_ids, counts, first=None) -> PromptBuffers:
         """Host bookkeeping of a prefill call: sequence seq_ids[i] brings counts[i]
         tokens of its prompt, from position first[i] on. Without first they are
-        its last ones: the whole prompt, or the rest of one whose other tokens
-        admission found in the cache or shares with other sequences. A chunk of a
-        longer rest needs first (ValueError): the engine does not keep how far a
-        prompt has come. The slots lie in the pages that admission reserved."""
+        its last ones: the whole prompt, the rest of one, or a token that a decode
+        step's append made room for. Prompt tokens before them have to be in the
+        cache or on their way (an earlier chunk's, write_positions', a cached or
+        shared prefix's): a chunk that leaves some out needs first (ValueError).
+        The slots lie in the pages that admission reserved."""
         seq_ids, counts = list(seq_ids), [int(c) for c in counts]
         if first is None:
             first = [self.bm.context_len(s) - c for s, c in zip(seq_ids, counts)]
             for s, f, c in zip(seq_ids, first, counts):
-                if c and f > self._in_place(s):
+                if c and f > self._known(s):
                     raise ValueError(f"a chunk of {c} of sequence {s}'s {f + c} tokens needs its first position")
         if len(seq_ids) != len(counts) or len(first) != len(counts):
             raise ValueError("one count and one first position per sequence")
@@ -203,16 +205,23 @@ class PagedKVEngine:
         slots, positions = [], []
         for s, f, c in zip(seq_ids, first, counts):
             slots += self.bm.slots(s, f, c) if c else []
+            self._wrote(s, f, c)
             positions += range(f, f + c)
         return PromptBuffers(*self._rows(seq_ids, counts, [f + c for f, c in zip(first, counts)], positions),
                              slots=torch.tensor(slots, dtype=torch.int64).to(self.device))
 
-    def _in_place(self, seq_id) -> int:
-        """Leading tokens in blocks that admission found in the cache or that other
-        sequences hold too."""
+    def _known(self, seq_id) -> int:
+        """A sequence's tokens, from the first on, that are in the cache or on their
+        way: those written, those in blocks that other sequences hold too, and all
+        behind the prompt."""
         table = self.bm.table(seq_id)
         shared = next((i for i, b in enumerate(table) if self.bm.refcount(b) < 2), len(table))
-        return max(self.bm.reused.get(seq_id, 0), shared) * self.block_tokens
+        known = max(self.bm.written[seq_id], shared * self.block_tokens)
+        return self.bm.context_len(seq_id) if known >= self.bm.prompt[seq_id] else known
+
+    def _wrote(self, seq_id, first: int, n: int) -> None:
+        if n and self.bm.written[seq_id] < first + n and first <= self._known(seq_id):
+            self.bm.written[seq_id] = first + n
 
     def _rows(self, seq_ids, counts, context_lens, positions):
         if not seq_ids:

@@ -49,7 +49,7 @@ def test_paths_of_the_tree_pass_the_checks(engine, path, monkeypatch):
 
 def test_a_chunk_behind_tokens_that_nothing_wrote_says_where_it_starts(engine):
     """Without first a prompt's rows are its last ones: right for all of it, or for
-    what follows tokens that are in the cache, and not for its first chunk."""
+    what follows tokens that are in the cache, not for its first chunk."""
     eng = engine()
     a, b = eng.bm.admit(100, 5), eng.bm.admit(40, 5)
     for counts in ([33, 40], [99, 40], [100, 39]):
@@ -71,15 +71,15 @@ def test_the_rest_behind_cached_and_shared_tokens_needs_no_start(engine):
     tokens = list(range(100))
     eng.bm.admit(100, 5, tokens=tokens)
     c = eng.bm.admit(110, 5, tokens=tokens + list(range(10)))
-    assert eng.prepare_prefill([c], [14]).positions.tolist() == [*range(96, 110)]
     with pytest.raises(ValueError, match="first"):
         eng.prepare_prefill([c], [13])
+    assert eng.prepare_prefill([c], [14]).positions.tolist() == [*range(96, 110)]
     eng = engine()
     eng.bm.admit(70, 5, 0, 64)
     d = eng.bm.admit(80, 5, 0, 64)
-    assert eng.prepare_prefill([d], [16]).positions.tolist() == [*range(64, 80)]
     with pytest.raises(ValueError, match="first"):
         eng.prepare_prefill([d], [15])
+    assert eng.prepare_prefill([d], [16]).positions.tolist() == [*range(64, 80)]
     eng = engine()
     e = eng.bm.admit(50, 5)
     f, = eng.bm.fork(e, 1)
@@ -96,3 +96,40 @@ def test_a_chunk_lies_within_its_sequence(engine, counts, first):
         eng.prepare_prefill([a, b], counts, first)
     with pytest.raises(ValueError):
         eng.prepare_prefill([a, b], [100, 3], [0])
+
+
+def test_tokens_behind_a_prompt_that_has_come_need_no_start(engine):
+    """A decode row, or the last chunk: what precedes it has been brought."""
+    eng = engine()
+    a, b = eng.bm.admit(100, 30), eng.bm.admit(3, 20)
+    eng.prepare_prefill([a], [60], [0])
+    assert eng.prepare_prefill([a, b], [40, 3]).positions.tolist() == [*range(60, 100), 0, 1, 2]
+    child, = eng.bm.fork(a, 1)
+    for _ in range(3):  # their appends are the decode steps'
+        eng.bm.prepare_append([a, b, child])
+    assert eng.prepare_prefill([a, b, child], [1, 1, 2]).positions.tolist() == [102, 5, 101, 102]
+    # a chunk out of order does not count for what precedes it
+    c = eng.bm.admit(50, 5)
+    eng.prepare_prefill([c], [10], [40])
+    with pytest.raises(ValueError, match="first"):
+        eng.prepare_prefill([c], [20])
+    # a preempted sequence comes back on fresh pages, all its tokens to be recomputed
+    eng.bm.preempt(a)
+    eng.bm.resume(a)
+    for count in (1, 43):
+        with pytest.raises(ValueError, match="first"):
+            eng.prepare_prefill([a], [count])
+    assert eng.prepare_prefill([a], [103]).positions.tolist() == [*range(103)]
+    assert eng.prepare_prefill([a], [1]).positions.tolist() == [102]
+    eng.bm.free(a)
+    assert a not in eng.bm.prompt and a not in eng.bm.written
+
+
+def test_written_positions_count(engine, monkeypatch):
+    from paged_kv_cache_49_gb300 import _native as nat
+    monkeypatch.setattr(nat, "append", lambda *a, **kw: None)
+    eng = engine()
+    a = eng.bm.admit(100, 30)
+    k = torch.zeros(64, 1, 128, dtype=torch.bfloat16)
+    eng.write_positions(a, 0, k, k)
+    assert eng.prepare_prefill([a], [36]).positions.tolist() == [*range(64, 100)]
