@@ -152,15 +152,34 @@ class PagedKVEngine:
             self.load_pool(w.pool_blocks_range("k", lo, hi), w.pool_blocks_range("v", lo, hi), lo)
 
     # ---- host bookkeeping + device launches ---------------------------------
+    def _side(self, stream) -> torch.cuda.Stream:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        return stream
+
+    def _on(self, stream):
+        """A context in which `stream` (default: the current one) is current, so
+        that what is allocated inside belongs to it."""
+        return contextlib.nullcontext() if stream is None else torch.cuda.stream(self._side(stream))
+
+    def _keep(self, stream, *inputs) -> None:
+        """The memory of inputs that the caller made on another stream is not given
+        out anew before `stream` is done with them."""
+        if stream is not None:
+            for t in inputs:
+                t.record_stream(self._side(stream))
+
     def append_tokens(self, seq_ids, k: torch.Tensor, v: torch.Tensor, stream=None):
         """Append one token per sequence (k, v: [B, Hkv, D] bf16 on device);
         returns (slots, pairs) as the block manager decided them."""
         slots, pairs = self.bm.prepare_append(list(seq_ids))
-        if pairs:
-            pt = torch.tensor(pairs, dtype=torch.int32).to(self.device, non_blocking=True)
-            nat.block_copy(self.k_cache, self.v_cache, pt, self.error, stream)
-        st = torch.tensor(slots, dtype=torch.int64).to(self.device, non_blocking=True)
-        nat.append(k, v, st, self.k_cache, self.v_cache, self.error, stream)
+        with self._on(stream):
+            if pairs:
+                pt = torch.tensor(pairs, dtype=torch.int32).to(self.device, non_blocking=True)
+                nat.block_copy(self.k_cache, self.v_cache, pt, self.error)
+            st = torch.tensor(slots, dtype=torch.int64).to(self.device, non_blocking=True)
+            nat.append(k, v, st, self.k_cache, self.v_cache, self.error)
+        self._keep(stream, k, v)
         return slots, pairs
 
     def write_positions(self, seq_id: int, first: int, k: torch.Tensor, v: torch.Tensor, stream=None):
@@ -168,21 +187,14 @@ class PagedKVEngine:
         (k, v: [n, Hkv, D] bf16 on device) -- a prefill, or the recompute of a
         resumed sequence -- with the append kernel; returns the slots."""
         slots = self.bm.slots(seq_id, first, int(k.shape[0]))
-        st = torch.tensor(slots, dtype=torch.int64).to(self.device, non_blocking=True)
-        nat.append(k, v, st, self.k_cache, self.v_cache, self.error, stream)
+        with self._on(stream):
+            st = torch.tensor(slots, dtype=torch.int64).to(self.device, non_blocking=True)
+            nat.append(k, v, st, self.k_cache, self.v_cache, self.error)
+        self._keep(stream, k, v)
         self._wrote(seq_id, first, len(slots))
         return slots
 
     # ---- prompts and drafted tokens -------------------------------------------
-    def _on(self, stream):
-        """A context in which `stream` (default: the current one) is current, so
-        that what is allocated inside belongs to it."""
-        if stream is None:
-            return contextlib.nullcontext()
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        return torch.cuda.stream(stream)
-
     def prepare_prefill(self, seq_ids, counts, first=None) -> PromptBuffers:
         """Host bookkeeping of a prefill call: sequence seq_ids[i] brings counts[i]
         tokens of its prompt, from position first[i] on. Without first they are
@@ -235,6 +247,7 @@ class PagedKVEngine:
         """The device part: the chunk's keys and values into the cache, then
         causal attention of its rows. q [T, Hq, D], k, v [T, Hkv, D] (bf16 on the
         device), packed in pb's order."""
+        self._keep(stream, q, k, v, pb.positions, pb.tables, pb.ctx, pb.starts, pb.slots)
         with self._on(stream):
             if rope is None:
                 nat.append(k, v, pb.slots, self.k_cache, self.v_cache, self.error)
@@ -266,6 +279,7 @@ class PagedKVEngine:
     def run_drafts(self, db: DraftBuffers, q, k, v, scale: float, workspace, rope=None, out=None, stream=None):
         """The device part: (attention of the drafts, their keys as the cache would
         hold them); the cache stays as it was."""
+        self._keep(stream, q, k, v, db.positions, db.tables, db.ctx, db.starts, db.masks, db.slots)
         with self._on(stream):
             if rope is not None:
                 k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
@@ -309,6 +323,7 @@ class PagedKVEngine:
             pairs += cow
             for i, slot in zip(rows, got):
                 slots[starts[i] + paths[i][d]] = slot
+        self._keep(stream, k, v)
         with self._on(stream):
             if pairs:
                 nat.block_copy(self.k_cache, self.v_cache, torch.tensor(pairs, dtype=torch.int32).to(self.device), self.error)
