@@ -522,16 +522,15 @@ class _LaunchOn:
         self.device, self.stream = device, stream
 
     def __enter__(self) -> int:
+        s = self.stream
+        if s is not None and not isinstance(s, torch.cuda.Stream):
+            s = torch.cuda.ExternalStream(int(s), device=self.device)
+        if s is not None and s.device.index != self.device:
+            raise ValueError(f"the stream is on {s.device}, the tensors on cuda:{self.device}")
         self.guards = contextlib.ExitStack()
         self.guards.enter_context(torch.cuda.device(self.device))
-        if self.stream is None:
+        if s is None:
             return torch._C._cuda_getCurrentRawStream(self.device)
-        s = self.stream
-        if not isinstance(s, torch.cuda.Stream):
-            s = torch.cuda.ExternalStream(int(s), device=self.device)
-        if s.device.index != self.device:
-            self.guards.close()
-            raise ValueError(f"the stream is on {s.device}, the tensors on cuda:{self.device}")
         self.guards.enter_context(torch.cuda.stream(s))
         return s.cuda_stream
 

@@ -133,3 +133,25 @@ def test_written_positions_count(engine, monkeypatch):
     k = torch.zeros(64, 1, 128, dtype=torch.bfloat16)
     eng.write_positions(a, 0, k, k)
     assert eng.prepare_prefill([a], [36]).positions.tolist() == [*range(64, 100)]
+
+
+@pytest.mark.parametrize("stream,error", [("none", ValueError), (object(), TypeError)])
+def test_a_refused_stream_leaves_the_device_as_it_was(engine, monkeypatch, stream, error):
+    from paged_kv_cache_49_gb300 import _native as nat
+    entered = []
+
+    class Device:
+        def __init__(self, index):
+            pass
+
+        def __enter__(self):
+            entered.append(1)
+
+        def __exit__(self, *exc):
+            entered.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    with pytest.raises(error):
+        with nat._LaunchOn(1, stream):
+            pass
+    assert not entered
