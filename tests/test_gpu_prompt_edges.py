@@ -5,7 +5,7 @@ import torch
 
 from oracle import prompt_attention as po
 from tests.prompt_batches import Batch
-from tests.test_gpu_prompt_attention import _call, _check, _dev, _ref, pkv  # noqa: F401
+from tests.test_gpu_prompt_attention import _call, _check, _dev, _ref, _run, pkv  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,36 @@ def test_sequences_laid_over_the_same_rows(pkv):  # noqa: F811
     assert ws.read_error() == pkv.DEVERR_QUERY
     ref = po.prompt_attention(b.q[320:], b.k, b.v, b.tables[9:], b.ctx[9:], np.array([0, 40]), b.scale)
     _check(out[320:], ref)
+
+
+@pytest.mark.parametrize("ctas", [1, 5, 100])
+@pytest.mark.parametrize("tree", [False, True])
+def test_a_workspace_of_fewer_ranges(pkv, tree, ctas):  # noqa: F811
+    """Fewer CTAs do the work, and nothing behind the given bytes is touched."""
+    b = Batch(33, [64, 33, 1], [9000, 2033, 700], 16, 2, 16)
+    d = _dev(pkv, b, tree)
+    ws = pkv.PrefillWorkspace()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    # header and descriptions of split items, then as much for every CTA
+    for full in range(40_000, 44_000, 16):
+        if (ws.nbytes - full) % sms == 0 and (ws.nbytes - full) // sms % 256 == 0:
+            break
+    ws.nbytes = full + ctas * ((ws.nbytes - full) // sms)
+    ws.tensor[ws.nbytes :].fill_(0x5A)
+    out = torch.full_like(d["q"], 7.0)
+    _call(pkv, d, b.scale, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    assert ws.read_error() == 0 and bool((ws.tensor[ws.nbytes :] == 0x5A).all())
+    _check(out, _ref(b, tree))
+    ws.nbytes = full
+    with pytest.raises(pkv.PkvError):
+        _call(pkv, d, b.scale, out=out, workspace=ws)
+
+
+@pytest.mark.parametrize("hq,hkv,decode,chunks", [(16, 4, 24, [(180, 5000), (97, 97)]), (64, 8, 9, [(70, 8011)]),
+                                                  (8, 1, 60, [(333, 3001), (1, 9000)])])
+def test_a_step_of_chunks_and_decode_rows(pkv, hq, hkv, decode, chunks):  # noqa: F811
+    """Long chunks and many single rows of grouped heads in one call."""
+    lens = [(1, 500 + 37 * s % 1200) for s in range(decode)] + chunks
+    lens = lens[1::2] + lens[::2]
+    _run(pkv, Batch(hq + decode, [n for n, _ in lens], [c for _, c in lens], hq, hkv, 16, first_row=2, rows_behind=1), False)
