@@ -17,8 +17,9 @@
 //
 // The items of the batch, laid end to end by cost, are cut into one range per
 // CTA (one persistent CTA per SM; three one after the other where that keeps
-// the contexts in L2), planned by every CTA from the lengths on the device. A cut near an item's end moves there; any other leaves fp32
-// partial results that merge_kernel joins in a fixed order.
+// the contexts in L2), planned by every CTA from the lengths on the device. A
+// cut near an item's end moves there; any other leaves fp32 partial results that
+// merge_kernel joins in a fixed order.
 //
 // What no row sees never enters a sum: masked scores are replaced before the
 // softmax, and of the value tiles that only some rows see in full, a warp
@@ -28,9 +29,11 @@
 // A group of G heads and T rows do G T operations a byte of K and V: prompts
 // are bound by the tensor core (16,411 tokens of 64 / 8 heads: 2.6 to 2.9 ms,
 // 1.5 to 1.7 PFLOP/s of a measured 1.7 under the power cap to 1.9; chunks of
-// 1,000 tokens on 9,000 cached ones 2.0 ms, 1.43 PFLOP/s), trees by bandwidth (64 trees of 16 drafts on
-// 1,024 tokens: 98 us, 4.6 of 6.8 TB/s), short items by their starts and ends
-// (16 packed prompts of 512 tokens: 99 us, 0.62 PFLOP/s).
+// 1,000 tokens on 9,000 cached ones 2.0 ms, 1.43 PFLOP/s), trees by bandwidth
+// (64 trees of 16 drafts on 1,024 tokens: 98 us, 4.6 of 6.8 TB/s), short items
+// by their starts and ends (16 packed prompts of 512 tokens: 99 us, 0.62
+// PFLOP/s). A K or V byte is read once for an item's 256 rows: a tree of more
+// than 32 drafts at 8 heads is two items and reads its context twice.
 #pragma once
 
 #include <cuda.h>
@@ -801,7 +804,11 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                             b = ex2(b);
                             sum2[(c >> 1) & 3] = add2(sum2[(c >> 1) & 3], pair(a, b));
                             // the weights enter the product as bf16, as the tensor
-                            // core takes them; their sum stays in fp32
+                            // core takes them; their sum is of the unrounded ones.
+                            // (The sum of the rounded ones, as decode takes it, has
+                            // no better a bound than 2^-8 of the weighted values, for two
+                            // more operations a pair in the loop that the long
+                            // prompts wait for.)
                             pk[c >> 1] = pack_bf16x2(a, b);
                         }
                         tmem_st32(t_s + 32 * half, pk);
@@ -1129,58 +1136,58 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             for (int turn = -2; ok && turn < turns; ++turn) {
                 if (!kOne && turn == 0 && fast > 0) {
                     const uint32_t p0 = smem_u32(&m.p_full[0]), p1 = smem_u32(&m.p_full[1]);
-                bool ready = false;
+                    bool ready = false;
 #pragma unroll 1
-                for (int i = 0; i < fast; ++i) {
-                    const uint32_t at = ring + 2 * i + 1;  // V of tile i, then K of tile i + 1
-                    const uint32_t dv = desc_low(tile_at(at), 1024), dk = desc_low(tile_at(at + 1), 16);
-                    if (!ready) {
-                        ok = wait_for(smem_u32(&m.kv_full[at % kStages]), (at / kStages) & 1, abort_flag, p.err);
-                        if (ok) ok = wait_for(smem_u32(&m.kv_full[(at + 1) % kStages]), ((at + 1) / kStages) & 1, abort_flag, p.err);
-                        if (ok) ok = wait_for(p0, (n_p0 + i) & 1, abort_flag, p.err);
-                        ok = __all_sync(0xFFFFFFFFu, ok);
-                        if (!ok) break;
-                    }
-                    tc_fence_after();
-                    if (elect_one()) {
+                    for (int i = 0; i < fast; ++i) {
+                        const uint32_t at = ring + 2 * i + 1;  // V of tile i, then K of tile i + 1
+                        const uint32_t dv = desc_low(tile_at(at), 1024), dk = desc_low(tile_at(at + 1), 16);
+                        if (!ready) {
+                            ok = wait_for(smem_u32(&m.kv_full[at % kStages]), (at / kStages) & 1, abort_flag, p.err);
+                            if (ok) ok = wait_for(smem_u32(&m.kv_full[(at + 1) % kStages]), ((at + 1) / kStages) & 1, abort_flag, p.err);
+                            if (ok) ok = wait_for(p0, (n_p0 + i) & 1, abort_flag, p.err);
+                            ok = __all_sync(0xFFFFFFFFu, ok);
+                            if (!ok) break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) issue_o(tm, dv, k, i > 0 || k > 0);
+                            for (int k = 0; k < 8; ++k) issue_o(tm, dv, k, i > 0 || k > 0);
 #pragma unroll
-                        for (int k = 0; k < 5; ++k) issue_s(tm, dq0, dk, k);
-                    }
-                    __syncwarp();
-                    ready = __all_sync(0xFFFFFFFFu, mbar_test(p1, (n_p1 + i) & 1));
-                    if (elect_one()) {
+                            for (int k = 0; k < 5; ++k) issue_s(tm, dq0, dk, k);
+                        }
+                        __syncwarp();
+                        ready = __all_sync(0xFFFFFFFFu, mbar_test(p1, (n_p1 + i) & 1));
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 5; k < 8; ++k) issue_s(tm, dq0, dk, k);
-                        mma_commit(smem_u32(&m.s_full[0]));
-                    }
-                    __syncwarp();
-                    if (!ready) {
-                        ok = __all_sync(0xFFFFFFFFu, wait_for(p1, (n_p1 + i) & 1, abort_flag, p.err));
-                        if (!ok) break;
-                    }
-                    tc_fence_after();
-                    if (elect_one()) {
+                            for (int k = 5; k < 8; ++k) issue_s(tm, dq0, dk, k);
+                            mma_commit(smem_u32(&m.s_full[0]));
+                        }
+                        __syncwarp();
+                        if (!ready) {
+                            ok = __all_sync(0xFFFFFFFFu, wait_for(p1, (n_p1 + i) & 1, abort_flag, p.err));
+                            if (!ok) break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) issue_o(tm + 128, dv, k, i > 0 || k > 0);
-                        mma_commit(smem_u32(&m.kv_empty[at % kStages]));
+                            for (int k = 0; k < 8; ++k) issue_o(tm + 128, dv, k, i > 0 || k > 0);
+                            mma_commit(smem_u32(&m.kv_empty[at % kStages]));
 #pragma unroll
-                        for (int k = 0; k < 5; ++k) issue_s(tm + 128, dq1, dk, k);
-                    }
-                    __syncwarp();
-                    ready = mbar_test(p0, (n_p0 + i + 1) & 1) & mbar_test(smem_u32(&m.kv_full[(at + 2) % kStages]), ((at + 2) / kStages) & 1) &
-                            mbar_test(smem_u32(&m.kv_full[(at + 3) % kStages]), ((at + 3) / kStages) & 1);
-                    ready = __all_sync(0xFFFFFFFFu, ready) && i + 1 < fast;
-                    if (elect_one()) {
+                            for (int k = 0; k < 5; ++k) issue_s(tm + 128, dq1, dk, k);
+                        }
+                        __syncwarp();
+                        ready = mbar_test(p0, (n_p0 + i + 1) & 1) & mbar_test(smem_u32(&m.kv_full[(at + 2) % kStages]), ((at + 2) / kStages) & 1) &
+                                mbar_test(smem_u32(&m.kv_full[(at + 3) % kStages]), ((at + 3) / kStages) & 1);
+                        ready = __all_sync(0xFFFFFFFFu, ready) && i + 1 < fast;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 5; k < 8; ++k) issue_s(tm + 128, dq1, dk, k);
-                        mma_commit(smem_u32(&m.s_full[1]));
-                        mma_commit(smem_u32(&m.kv_empty[(at + 1) % kStages]));
-                        if (i + 2 == count) mma_commit(smem_u32(&m.q_empty));
+                            for (int k = 5; k < 8; ++k) issue_s(tm + 128, dq1, dk, k);
+                            mma_commit(smem_u32(&m.s_full[1]));
+                            mma_commit(smem_u32(&m.kv_empty[(at + 1) % kStages]));
+                            if (i + 2 == count) mma_commit(smem_u32(&m.q_empty));
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
                     if (!ok) break;
                     turn = 2 * fast;
                 }

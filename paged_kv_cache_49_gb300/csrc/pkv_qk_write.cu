@@ -229,8 +229,8 @@ KernelFn kernel_for(int lanes, bool interleaved) {
     }
 }
 
-// Blocks that run at once on the current device (three on an SM at the
-// kernel's 80 registers), read once per device.
+// Blocks that run at once on the current device (as many on an SM as the
+// kernel's launch bounds leave registers for), its SMs read once per device.
 int resident_blocks() {
     static std::mutex mu;
     static std::vector<int> cache;
