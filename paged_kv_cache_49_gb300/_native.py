@@ -558,9 +558,11 @@ def _launch_on(device: int, stream):
 
 
 class PrefillWorkspace:
-    """Device scratch for attn_prefill and attn_tree, of any batch: the error
-    word, then the partial results of rows whose keys are split. Calls that
-    share one must not overlap on the GPU."""
+    """Device scratch for attn_prefill and attn_tree, of any batch (120 MB on 152
+    SMs): the error word, then the partial results of rows whose keys are split.
+    Its header is zeroed on `stream` (default: the current one); calls on another
+    stream wait for that one first, as for any input made there. Calls that share
+    a workspace must not overlap on the GPU."""
 
     def __init__(self, device=None, stream=None):
         dev = torch.device(device or "cuda")
@@ -613,7 +615,9 @@ def attn_prefill(q, k_cache, v_cache, block_tables, context_lens, query_starts, 
     tokens: rows query_starts[s] .. query_starts[s + 1] of q [T, Hq, 128] are
     the last tokens of sequence s, whose context_lens[s] tokens are all in the
     cache. Returns out [T, Hq, 128]; rows of no sequence are left as they were
-    (zeros in an `out` made here)."""
+    (zeros in an `out` made here). Without a workspace the call makes one for
+    itself, and what the device finds wrong (bad block ids, lengths, row starts, a
+    wait that ran out) is not reported: pass one and read its read_error()."""
     device, shape, B, width = _rows_shapes(q, k_cache, v_cache, block_tables, context_lens, query_starts, out, workspace)
     with _launch_on(device, stream) as st:
         if out is None:
@@ -632,7 +636,8 @@ def attn_tree(q, k_draft, v_draft, tree_masks, k_cache, v_cache, block_tables, c
     k_draft, v_draft [T, Hkv, 128], packed by query_starts) sees the
     context_lens[s] tokens of its sequence in the cache and the drafts j of the
     sequence whose bit j is set in tree_masks[i] (int64, see tree_masks()).
-    Returns out [T, Hq, 128]; the cache is not written."""
+    Returns out [T, Hq, 128]; the cache is not written. Without a workspace as
+    attn_prefill: device errors are not reported."""
     device, shape, B, width = _rows_shapes(q, k_cache, v_cache, block_tables, context_lens, query_starts, out, workspace)
     _need_all(device, ((k_draft, _BF16, "k_draft"), (v_draft, _BF16, "v_draft"), (tree_masks, _I64, "tree_masks")))
     T, _, hkv, d = shape[:4]
