@@ -328,7 +328,9 @@ pkv_status pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
  *                   (pkv_attn_workspace_init); the first 4 bytes are the
  *                   device error word, the rest carries nothing from one call
  *                   to the next. Calls that share a workspace must not
- *                   overlap on the GPU.
+ *                   overlap on the GPU. Fewer bytes are taken as they are
+ *                   and make fewer CTAs do the work; less than one CTA's
+ *                   share is refused (PKV_EINVAL)
  * What a row does not see never reaches it: keys and values behind p, rows of
  * the last block past the context and unused blocks may hold anything, NaN
  * included. A row that sees nothing gives zeros.

@@ -167,7 +167,8 @@ class PagedKVEngine:
         out anew before `stream` is done with them."""
         if stream is not None:
             for t in inputs:
-                t.record_stream(self._side(stream))
+                if t.is_cuda:  # others are refused by the call itself
+                    t.record_stream(self._side(stream))
 
     def append_tokens(self, seq_ids, k: torch.Tensor, v: torch.Tensor, stream=None):
         """Append one token per sequence (k, v: [B, Hkv, D] bf16 on device);

@@ -89,3 +89,26 @@ def test_inputs_let_go_while_a_side_stream_waits(pkv):
     assert len(got) == len(want)
     for i, (g, w) in enumerate(zip(got, want)):
         assert torch.equal(g, w), i
+
+
+@pytest.mark.parametrize("handle", ["side", "default"])
+def test_streams_given_as_handles(pkv, handle):
+    """cudaStream_t values, the default stream's zero among them."""
+    side = torch.cuda.Stream() if handle == "side" else torch.cuda.default_stream()
+    raw = side.cuda_stream
+    assert raw == 0 or handle == "side"
+    rope = pkv.RopeSpec(pkv.rope_table(400, D))
+    results = []
+    for stream in (None, raw):
+        eng, ws = pkv.PagedKVEngine(40, HQ, HKV, D), pkv.PrefillWorkspace()
+        eng.k_cache.zero_(), eng.v_cache.zero_()
+        a, b = eng.bm.admit(T, 30), eng.bm.admit(1, 30)
+        torch.cuda.synchronize()
+        q, k, v = _inputs(T, 1)
+        torch.cuda.synchronize()
+        out = eng.run_prefill(eng.prepare_prefill([a], [T]), q, k, v, SCALE, ws, rope, stream=stream)
+        eng.write_positions(b, 0, k[:1].contiguous(), v[:1].contiguous(), stream=stream)
+        eng.append_tokens([a, b], k[:2].contiguous(), v[:2].contiguous(), stream=stream)
+        torch.cuda.synchronize()
+        results.append((out.clone(), eng.k_cache.clone(), eng.v_cache.clone()))
+    assert all(torch.equal(x, y) for x, y in zip(*results))

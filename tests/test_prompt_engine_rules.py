@@ -155,3 +155,14 @@ def test_a_refused_stream_leaves_the_device_as_it_was(engine, monkeypatch, strea
         with nat._LaunchOn(1, stream):
             pass
     assert not entered
+
+
+def test_inputs_on_the_host_are_refused_as_such(engine, monkeypatch):
+    import contextlib
+    eng = engine()
+    monkeypatch.setattr(eng, "_on", lambda stream: contextlib.nullcontext())
+    a = eng.bm.admit(10, 5)
+    x = torch.zeros(10, 2, 128, dtype=torch.bfloat16)
+    pb = eng.prepare_prefill([a], [10])
+    with pytest.raises(ValueError, match="CUDA"):
+        eng.run_prefill(pb, x, x[:, :1].contiguous(), x[:, :1].contiguous(), 0.1, None, stream=7)
