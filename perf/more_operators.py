@@ -179,8 +179,8 @@ def _paged(x, blocks, block_tokens):
 def _quantise(x, group_dims):
     """(codes, scales, minima) of rows of 128 values."""
     x = x.float().unflatten(-1, (-1, group_dims))
-    lo = x.amin(dim=-1, keepdim=True).clamp(min=-FP16_MAX)
-    hi = x.amax(dim=-1, keepdim=True).clamp(max=FP16_MAX)
+    lo = x.amin(dim=-1, keepdim=True).clamp(-FP16_MAX, FP16_MAX)
+    hi = x.amax(dim=-1, keepdim=True).clamp(-FP16_MAX, FP16_MAX)
     m = lo.half()
     s = ((hi - lo) / 15).half()
     c = torch.round((x - m.float()) / torch.where(s > 0, s, torch.ones_like(s)).float()).clamp(0, 15)
@@ -397,8 +397,8 @@ def _plain_beams(state):
 def _exact_rows(x, group_dims):
     """Rows of 128 values as a 4-bit cache gives them back."""
     rows = x.double().reshape(*x.shape[:-1], HEAD_DIM // group_dims, group_dims)
-    least = rows.min(-1)[0].clamp_min(-FP16_MAX)
-    span = rows.max(-1)[0].clamp_max(FP16_MAX) - least
+    least, most = (x.clamp(-FP16_MAX, FP16_MAX) for x in (rows.min(-1)[0], rows.max(-1)[0]))
+    span = most - least
     m = least.float().half().double()[..., None]
     s = (span / 15).float().half().double()[..., None]
     code = torch.clamp(((rows - m) / s).round(), 0, 15)
