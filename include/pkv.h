@@ -378,6 +378,67 @@ pkv_status pkv_attn_tree(const void* q, const void* k_draft, const void* v_draft
                          size_t workspace_bytes, void* out, void* stream);
 
 /*
+ * A cache held in 4 bits -- the pages' cache with rows of 4-bit codes in place
+ * of bf16 values: 3.2 to 3.8 times as many tokens in a pool, and as many fewer
+ * bytes for decode attention to read. (The pages hold 16-bit rows; block
+ * tables, slots and the block manager are the same here.) A row, the key or
+ * value of one token and KV head, is quantised in groups of group_dims = 32, 64
+ * or 128 of its 128 values, in fp32 with one rounding per step:
+ *   lo, hi = the group's least and greatest value, held to +-65504
+ *   m = fp16(lo), s = fp16((hi - lo) / 15)
+ *   c = rint((x - m) / s), held to 0 .. 15 (0 where s is 0)
+ * and stands for s * c + m: within s / 2 (and the rounding of s and m) of x.
+ * Infinite and larger values saturate; a NaN makes its whole group NaN. Scales
+ * and minima are fp16, so ranges under 15 * 2^-24 vanish.
+ *
+ * cache: device bytes [num_blocks][num_kv_heads][block_tokens / 8][unit], one
+ * unit of 1,024 + 64 * 128 / group_dims bytes per 8 tokens (codes, scales and
+ * minima of both keys and values, in the order in which the attention's lanes
+ * read them; csrc/pkv_int4.cuh states it byte by byte); 16-byte aligned. Zero
+ * bytes stand for zeros. Slots, tables and pairs are those of the bf16 cache.
+ *
+ * pkv_int4_block_bytes: bytes of one block, all KV heads (0 on invalid
+ *   arguments).
+ * pkv_append_int4: pkv_append into such a cache. k, v: device bf16, rows of
+ *   num_kv_heads * 128 contiguous values every k_stride (v_stride) values
+ *   (multiples of 8, no shorter than the row), so views of one fused
+ *   projection as they are. Negative slots mark padding rows; slots past the
+ *   pool are skipped and set PKV_DEVERR_SLOT; slots must be distinct. The
+ *   bytes of a token's neighbours are left alone.
+ * pkv_load_int4: for each pair (src, dst), block src of the cache as bf16 rows
+ *   (rounded once) into block dst of k_cache and v_cache, bf16 pools
+ *   [num_dst_blocks][num_kv_heads][block_tokens][128] -- what pkv_attn_prefill
+ *   and pkv_attn_tree read. Pairs with an id outside its pool are skipped and
+ *   set PKV_DEVERR_BLOCK_ID; destinations must be distinct.
+ * pkv_block_copy_int4: pkv_block_copy of such blocks.
+ * pkv_attn_decode_int4: pkv_attn_decode over such a cache: workspace (the same
+ *   kind: one serves both calls), block_tables, context_lens, q, out, num_ctas,
+ *   limits and errors as there, any block size. fp32 sums and softmax; the
+ *   weights enter the product with the values in fp16. What lies behind a
+ *   context in its last block, NaN scales included, never reaches the output.
+ */
+size_t pkv_int4_block_bytes(int num_kv_heads, int block_tokens, int group_dims);
+
+pkv_status pkv_append_int4(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const int64_t* slot_mapping, int num_tokens, void* cache, int num_blocks,
+                           int num_kv_heads, int head_dim, int block_tokens, int group_dims,
+                           uint32_t* device_error, void* stream);
+
+pkv_status pkv_load_int4(const void* cache, const int32_t* src_dst_pairs, int num_pairs, void* k_cache,
+                         void* v_cache, int num_blocks, int num_dst_blocks, int num_kv_heads, int head_dim,
+                         int block_tokens, int group_dims, uint32_t* device_error, void* stream);
+
+pkv_status pkv_block_copy_int4(void* cache, const int32_t* src_dst_pairs, int num_pairs, int num_blocks,
+                               int num_kv_heads, int head_dim, int block_tokens, int group_dims,
+                               uint32_t* device_error, void* stream);
+
+pkv_status pkv_attn_decode_int4(const void* q, const void* cache, const int32_t* block_tables,
+                                int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                                int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
+                                int block_tokens, int group_dims, float scale, int num_ctas, void* workspace,
+                                size_t workspace_bytes, void* out, void* stream);
+
+/*
  * Cascade attention -- pkv_attn_decode for a batch whose sequences share
  * leading blocks, reading each shared block once for all its sharers instead
  * of once per sequence. The pages share those blocks in memory ("KV cache

@@ -49,9 +49,11 @@ EXPORTED = [
     "pkv_attn_cascade_workspace_size", "pkv_cascade_staging_size", "pkv_cascade_plan", "pkv_attn_decode_cascade",
     "pkv_attn_decode_wait_test", "pkv_attn_decode_cuda_cores", "pkv_attn_workspace_fixed_bytes",
     "pkv_attn_launch_ctas", "pkv_attn_prefill", "pkv_attn_prefill_workspace_size", "pkv_attn_tree",
-    "pkv_qk_norm_rope_append",
+    "pkv_qk_norm_rope_append", "pkv_int4_block_bytes", "pkv_append_int4", "pkv_load_int4", "pkv_block_copy_int4",
+    "pkv_attn_decode_int4",
 ]
 BLOCK_SIZES = (8, 16, 32, 64)
+INT4_GROUP_DIMS = (32, 64, 128)
 
 
 class PkvError(RuntimeError):
@@ -149,6 +151,12 @@ def _load() -> ctypes.CDLL:
                                 sz, vp, vp]),
         "pkv_qk_norm_rope_append": (i32, [vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, i32, i32, i32, vp, vp, i32, i32,
                                           i32, i32, vp, vp, vp, vp, i32, i32, vp, vp]),
+        "pkv_int4_block_bytes": (sz, [i32, i32, i32]),
+        "pkv_append_int4": (i32, [vp, i64, vp, i64, vp, i32, vp, i32, i32, i32, i32, i32, vp, vp]),
+        "pkv_load_int4": (i32, [vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]),
+        "pkv_block_copy_int4": (i32, [vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]),
+        "pkv_attn_decode_int4": (i32, [vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz, vp,
+                                       vp]),
         "pkv_decode_step_host": (i32, [vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz, vp, vp,
                                        vp, vp]),
     }
@@ -755,6 +763,120 @@ def qk_norm_rope_append(q, k, v, cos_sin, positions, slot_mapping, k_cache, v_ca
                                             k_cache.data_ptr(), v_cache.data_ptr(), nb, bt, _ptr(device_error), st),
                "pkv_qk_norm_rope_append")
     return q_out
+
+
+# ---------------------------------------------------------------------------
+# a cache held in 4 bits
+
+
+class Int4Cache:
+    """A pool of pages whose keys and values are held in 4 bits (see
+    pkv_append_int4 in the header for the format): uint8 `data` [num_blocks,
+    num_kv_heads, bytes of a block and head], zeros at first. Rows of 128 values
+    are quantised in groups of group_dims."""
+
+    def __init__(self, num_blocks: int, num_kv_heads: int, block_tokens: int = BLOCK_TOKENS, group_dims: int = 64,
+                 device=None):
+        nbytes = int(_lib.pkv_int4_block_bytes(num_kv_heads, block_tokens, group_dims))
+        if num_blocks < 1 or nbytes == 0:
+            raise ValueError("Int4Cache needs blocks, heads, block_tokens in (8, 16, 32, 64) and group_dims in (32, 64, 128)")
+        self.num_blocks, self.num_kv_heads = num_blocks, num_kv_heads
+        self.block_tokens, self.group_dims = block_tokens, group_dims
+        self.data = torch.zeros((num_blocks, num_kv_heads, nbytes // num_kv_heads), dtype=torch.uint8,
+                                device=device or "cuda")
+
+    def _shape(self):
+        return self.num_kv_heads, HEAD_DIM, self.block_tokens, self.group_dims
+
+
+_U8 = torch.uint8
+
+
+def _need_pairs(device: int, pairs) -> int:
+    _need_all(device, ((pairs, _I32, "pairs"),))
+    if pairs.numel() and (pairs.dim() != 2 or pairs.shape[1] != 2):
+        raise ValueError("pairs must be [n, 2]")
+    return pairs.shape[0] if pairs.numel() else 0
+
+
+def append_int4(k, v, slot_mapping, cache: Int4Cache, device_error=None, stream=None) -> None:
+    """Quantise k[i], v[i] ([T, Hkv, 128] bf16, possibly views of one fused
+    projection) into slot slot_mapping[i] (int64; negative: a padding row)."""
+    device = cache.data.get_device()
+    T = slot_mapping.numel()
+    _need_all(device, ((cache.data, _U8, "the cache"), (slot_mapping, _I64, "slot_mapping")))
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError("k, v must be [T, Hkv, 128]")
+    ks = _need_rows(device, k, "k", T, cache.num_kv_heads, HEAD_DIM)
+    vs = _need_rows(device, v, "v", T, cache.num_kv_heads, HEAD_DIM)
+    if device_error is not None:
+        _need_all(device, ((device_error, _I32, "device_error"),))
+    with _launch_on(device, stream) as st:
+        _check(_lib.pkv_append_int4(k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T, cache.data.data_ptr(),
+                                    cache.num_blocks, *cache._shape(), _ptr(device_error), st), "pkv_append_int4")
+
+
+def load_int4(cache: Int4Cache, pairs, k_cache, v_cache, device_error=None, stream=None) -> None:
+    """Block pairs[i, 0] of the 4-bit cache as bf16 rows into block pairs[i, 1] of
+    k_cache and v_cache [blocks, Hkv, block_tokens, 128]."""
+    device = cache.data.get_device()
+    _need_all(device, ((cache.data, _U8, "the cache"), (k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache")))
+    n = _need_pairs(device, pairs)
+    hkv, d, bt, _ = cache._shape()
+    if k_cache.dim() != 4 or k_cache.shape[1:] != (hkv, bt, d) or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache, v_cache must be {['blocks', hkv, bt, d]} and alike")
+    if device_error is not None:
+        _need_all(device, ((device_error, _I32, "device_error"),))
+    if n == 0:
+        return
+    with _launch_on(device, stream) as st:
+        _check(_lib.pkv_load_int4(cache.data.data_ptr(), pairs.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(),
+                                  cache.num_blocks, k_cache.shape[0], *cache._shape(), _ptr(device_error), st),
+               "pkv_load_int4")
+
+
+def block_copy_int4(cache: Int4Cache, pairs, device_error=None, stream=None) -> None:
+    """Copy physical block pairs[i, 0] of the cache onto pairs[i, 1]."""
+    device = cache.data.get_device()
+    _need_all(device, ((cache.data, _U8, "the cache"),))
+    n = _need_pairs(device, pairs)
+    if device_error is not None:
+        _need_all(device, ((device_error, _I32, "device_error"),))
+    with _launch_on(device, stream) as st:
+        _check(_lib.pkv_block_copy_int4(cache.data.data_ptr(), pairs.data_ptr(), n, cache.num_blocks, *cache._shape(),
+                                        _ptr(device_error), st), "pkv_block_copy_int4")
+
+
+def attn_decode_int4(q, cache: Int4Cache, block_tables, context_lens, scale, out=None, workspace=None, num_ctas: int = 0,
+                     stream=None):
+    """attn_decode over a cache held in 4 bits; returns out [B, Hq, 128] bf16.
+    workspace: an AttentionWorkspace; without one the call makes it, and device
+    errors are not reported."""
+    device = q.get_device()
+    _need_all(device, ((q, _BF16, "q"), (cache.data, _U8, "the cache"), (block_tables, _I32, "block_tables"),
+                       (context_lens, _I32, "context_lens")))
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
+        raise ValueError("q must be [B, Hq, 128]")
+    B, hq, d = q.shape
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError("block_tables must be [B, W] and context_lens [B]")
+    if out is not None:
+        _need_all(device, ((out, _BF16, "out"),))
+        if out.shape != q.shape:
+            raise ValueError("out must be shaped like q")
+    if workspace is not None and workspace.tensor.get_device() != device:
+        raise ValueError(f"the workspace is on {workspace.tensor.device}, the tensors on cuda:{device}")
+    with _launch_on(device, stream) as st:
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            workspace = AttentionWorkspace(B, cache.num_kv_heads, device=q.device, stream=st)
+        hkv, _, bt, gd = cache._shape()
+        _check(_lib.pkv_attn_decode_int4(q.data_ptr(), cache.data.data_ptr(), block_tables.data_ptr(),
+                                         block_tables.shape[1], context_lens.data_ptr(), B, hq, hkv, d, cache.num_blocks,
+                                         bt, gd, float(scale), int(num_ctas), workspace.ptr, workspace.nbytes,
+                                         out.data_ptr(), st), "pkv_attn_decode_int4")
+    return out
 
 
 # ---------------------------------------------------------------------------

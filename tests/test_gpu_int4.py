@@ -1,0 +1,460 @@
+"""The 4-bit cache's kernels against the oracle: bytes and loaded pages exactly,
+attention within bounds that count its roundings."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import int4
+from oracle.paged_attention import widen_bf16
+from workloads import randn_bf16
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from tests.conftest import build_native
+    build_native()
+    import paged_kv_cache_49_gb300 as m
+    return m
+
+
+def _f32(bits):
+    return (bits.astype(np.uint32) << np.uint32(16)).view(np.float32)
+
+
+def _rows(rng, shape, offset=1.0):
+    """bf16 bits of values whose channels differ in mean."""
+    x = torch.from_numpy(widen_bf16(randn_bf16(rng, shape)) + offset * rng.standard_normal(shape[1:]))
+    return x.to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
+
+
+def _dev(pkv, bits):
+    return pkv.bf16_from_bits(bits).cuda()
+
+
+def _bf16(x):
+    """float64 -> the bits of its rounding to fp32, then to bf16."""
+    return torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
+
+
+class Pool:
+    """A cache whose slots have all been written, and what it holds."""
+
+    def __init__(self, pkv, rng, blocks, hkv, bt, gd, k=None, v=None):
+        self.cache = pkv.Int4Cache(blocks, hkv, bt, gd)
+        shape = (blocks * bt, hkv, 128)
+        self.k_bits, self.v_bits = (_rows(rng, shape, o) if x is None else x for x, o in ((k, 1.0), (v, 0.0)))
+        self.slots = rng.permutation(blocks * bt)
+        err = pkv.new_error_word()
+        pkv.append_int4(_dev(pkv, self.k_bits), _dev(pkv, self.v_bits), torch.from_numpy(self.slots).cuda(), self.cache, err)
+        assert pkv.read_device_error(err) == 0
+        self.k, self.v = (self._paged(b, blocks, hkv, bt, gd) for b in (self.k_bits, self.v_bits))
+
+    def _paged(self, bits, blocks, hkv, bt, gd):
+        rows = np.empty((blocks * bt, hkv, 128), np.float32)
+        rows[self.slots] = _f32(bits)
+        return int4.quantise(rows.reshape(blocks, bt, hkv, 128).swapaxes(1, 2), gd)
+
+
+# ---- append, load, copy -------------------------------------------------------
+
+
+@pytest.mark.parametrize("gd", [32, 64, 128])
+@pytest.mark.parametrize("bt", [8, 16, 32, 64])
+def test_every_byte_of_a_pool(pkv, bt, gd):
+    pool = Pool(pkv, np.random.default_rng(bt + gd), 5, 3, bt, gd)
+    assert np.array_equal(pool.cache.data.cpu().numpy(), int4.pack(pool.k, pool.v))
+
+
+@pytest.mark.parametrize("T,hkv,bt,gd", [(1, 1, 8, 128), (1, 8, 16, 64), (3, 1, 16, 32), (37, 2, 32, 64), (100, 5, 64, 128),
+                                         (513, 8, 16, 64)])
+def test_append_views_padding_and_neighbours(pkv, T, hkv, bt, gd):
+    """Views of a fused projection; padding rows; bytes of other slots stay."""
+    rng = np.random.default_rng(T)
+    blocks = T // bt + 2
+    kb, vb = _rows(rng, (T, hkv, 128)), _rows(rng, (T, hkv, 128))
+    fused = torch.zeros((T, 3 * hkv, 128), dtype=torch.bfloat16, device="cuda")
+    fused[:, hkv:2 * hkv], fused[:, 2 * hkv:] = _dev(pkv, kb), _dev(pkv, vb)
+    slots = rng.permutation(blocks * bt)[:T]
+    slots[::5] = -1 - np.arange(len(slots[::5]))
+    cache = pkv.Int4Cache(blocks, hkv, bt, gd)
+    before = rng.integers(0, 256, size=cache.data.shape, dtype=np.uint8)
+    cache.data.copy_(torch.from_numpy(before))
+    err = pkv.new_error_word()
+    pkv.append_int4(fused[:, hkv:2 * hkv], fused[:, 2 * hkv:], torch.from_numpy(slots).cuda(), cache, err)
+    assert pkv.read_device_error(err) == 0
+    # what pack() makes of the new rows where they are, the old bytes elsewhere
+    kept = slots >= 0
+    marks, want = np.zeros(before.shape, np.uint8), before.copy()
+    for name, fill in (("marks", True), ("rows", False)):
+        parts = []
+        for bits in (kb, vb):
+            rows = np.zeros((blocks * bt, hkv, 128), np.float32)
+            rows[slots[kept]] = _f32(bits)[kept]
+            c, s, m = int4.quantise(rows.reshape(blocks, bt, hkv, 128).swapaxes(1, 2), gd)
+            if fill:
+                live = np.zeros(blocks * bt, bool)
+                live[slots[kept]] = True
+                live = live.reshape(blocks, 1, bt, 1)
+                c = np.broadcast_to(np.where(live, 15, 0), c.shape).astype(np.uint8)
+                ones = np.array(0xFFFF, np.uint16).view(np.float16)
+                s = m = np.broadcast_to(np.where(live, ones, np.float16(0)), s.shape)
+            parts.append((c, s, m))
+        if fill:
+            marks = int4.pack(*parts)
+        else:
+            want = np.where(marks == 0xFF, int4.pack(*parts), before)
+    assert np.array_equal(cache.data.cpu().numpy(), want)
+
+
+def test_append_edge_values(pkv):
+    """Zeros, constants, infinities, NaN, tiny and huge ranges, exact halves."""
+    x = np.zeros((16, 1, 128), np.float32)
+    x[1] = 2.5
+    x[2, 0, ::2] = np.inf
+    x[3] = -np.inf
+    x[4, 0, 5] = np.nan
+    x[5, 0, 3] = 2.0 ** -30
+    x[6, 0, 0], x[6, 0, 1] = -0.9375, 0.9375
+    x[6, 0, 2:18] = -0.9375 + (np.arange(16) + 0.5) / 8
+    x[7] = np.float32(3.0e38) * np.sign(np.arange(128) % 3 - 1.0)
+    x[8] = np.arange(128) * np.float32(2.0 ** -24)
+    x[9] = np.linspace(-1, 1, 128)
+    x[10] = -np.linspace(0, 7, 128) ** 3
+    x[11] = np.nan
+    x[12, 0, :] = 65280.0
+    x[12, 0, 64:] = -65280.0
+    x[13] = 2.0 ** -14 * np.arange(128)
+    x[14] = -0.0
+    x[15, 0, 100] = -np.nan
+    bits = torch.from_numpy(x).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
+    for gd in (32, 64, 128):
+        cache = pkv.Int4Cache(2, 1, 8, gd)
+        pkv.append_int4(_dev(pkv, bits), _dev(pkv, bits[::-1].copy()), torch.arange(16, device="cuda"), cache)
+        rows = [int4.quantise(_f32(b).reshape(2, 8, 1, 128).swapaxes(1, 2), gd) for b in (bits, bits[::-1])]
+        got, want = cache.data.cpu().numpy(), int4.pack(*rows)
+        params = np.r_[1024:got.shape[-1]]  # a NaN has many forms
+        g, w = (a[..., params].copy().view(np.float16) for a in (got, want))
+        assert np.array_equal(g, w, equal_nan=True)
+        assert np.array_equal(got[..., :1024], want[..., :1024])
+
+
+@pytest.mark.parametrize("gd", [32, 64, 128])
+@pytest.mark.parametrize("bt", [8, 16, 32, 64])
+def test_load_is_the_values_rounded_once(pkv, bt, gd):
+    rng = np.random.default_rng(3)
+    pool = Pool(pkv, rng, 7, 3, bt, gd)
+    pairs = np.array([[6, 0], [0, 4], [3, 1], [3, 2]], np.int32)
+    k, v = (torch.full((6, 3, bt, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    err = pkv.new_error_word()
+    pkv.load_int4(pool.cache, torch.from_numpy(pairs).cuda(), k, v, err)
+    assert pkv.read_device_error(err) == 0
+    for got, held in ((k, pool.k), (v, pool.v)):
+        got, want = pkv.bits_from_bf16(got), _bf16(int4.values(*held))
+        assert np.array_equal(got[pairs[:, 1]], want[pairs[:, 0]])
+        assert (_f32(got[[3, 5]]) == 7.0).all()
+
+
+def test_load_and_copy_of_nothing_and_of_bad_pairs(pkv):
+    rng = np.random.default_rng(4)
+    pool = Pool(pkv, rng, 4, 2, 16, 64)
+    k, v = (torch.full((3, 2, 16, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    none = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    before = pool.cache.data.clone()
+    pkv.load_int4(pool.cache, none, k, v)
+    pkv.block_copy_int4(pool.cache, none)
+    err = pkv.new_error_word()
+    for bad in ([[0, 3]], [[4, 0]], [[-1, 0]], [[0, -2]]):
+        pkv.load_int4(pool.cache, torch.tensor(bad, dtype=torch.int32, device="cuda"), k, v, err)
+        assert pkv.read_device_error(err) == pkv.DEVERR_BLOCK_ID
+    for bad in ([[0, 4]], [[4, 0]], [[-1, 0]], [[0, -2]]):
+        pkv.block_copy_int4(pool.cache, torch.tensor(bad, dtype=torch.int32, device="cuda"), err)
+        assert pkv.read_device_error(err) == pkv.DEVERR_BLOCK_ID
+    assert (k == 7).all() and (v == 7).all() and torch.equal(before, pool.cache.data)
+    # a bad slot, among good ones
+    rows = _dev(pkv, _rows(rng, (3, 2, 128)))
+    pkv.append_int4(rows, rows, torch.tensor([5, 64, -1], device="cuda"), pool.cache, err)
+    assert pkv.read_device_error(err) == pkv.DEVERR_SLOT
+    assert torch.equal(before[1:], pool.cache.data[1:]) and not torch.equal(before[0], pool.cache.data[0])
+
+
+@pytest.mark.parametrize("bt,gd,hkv", [(8, 128, 1), (16, 64, 8), (64, 32, 3)])
+def test_copies_of_blocks(pkv, bt, gd, hkv):
+    rng = np.random.default_rng(5)
+    cache = pkv.Int4Cache(9, hkv, bt, gd)
+    before = rng.integers(0, 256, size=cache.data.shape, dtype=np.uint8)
+    cache.data.copy_(torch.from_numpy(before))
+    pkv.block_copy_int4(cache, torch.tensor([[0, 8], [0, 3], [5, 1]], dtype=torch.int32, device="cuda"))
+    before[[8, 3, 1]] = before[[0, 0, 5]]
+    assert np.array_equal(cache.data.cpu().numpy(), before)
+
+
+# ---- decode attention ---------------------------------------------------------
+
+
+def _near(got, want, a, e, n):
+    """bf16 out against float64. In turn: the output's rounding, 2^-8 of it; the
+    weights' rounding to fp16 (2^-11, in the values' sum and in the denominator)
+    and that of weight times scale (2^-11): 3 * 2^-11 of a; a score off by 2^-17
+    of the size of its terms e (128 products and the groups' sums in fp32), which
+    moves weight and denominator alike: 2 * 2^-17 e a; exp2 and the fp32 sums:
+    2^-14 a; weights below fp16's range, 2^-24 each at most: n 2^-24 of the
+    largest value, which a / 2^-24 bounds where it counts -- n 2^-20 max a."""
+    big = a.max(axis=-1, keepdims=True)
+    tol = 2.0 ** -8 * np.abs(want) + a * (3 * 2.0 ** -11 + 2.0 ** -16 * e[..., None] + 2.0 ** -14)
+    tol += np.asarray(n, float)[:, None, None] * 2.0 ** -20 * big
+    g = _f32(got).astype(np.float64)
+    assert np.isfinite(g).all() and (np.abs(g - want) <= tol).all(), (np.abs(g - want) - tol).max()
+
+
+def _batch(rng, lens, blocks, bt):
+    """Tables over a shuffled pool; unused entries are bad ids, never read."""
+    per = [-(-n // bt) for n in lens]
+    order = rng.permutation(blocks)
+    width = max(max(per), 1) + 1
+    tables = np.full((len(lens), width), -7, np.int32)
+    at = 0
+    for i, n in enumerate(per):
+        tables[i, :n] = order[at:at + n]
+        at += n
+    assert at <= blocks
+    return tables
+
+
+def _poison(pool, tables, lens, bt):
+    """NaN scales and full codes behind every context and in unused blocks."""
+    d = pool.cache.data
+    blocks, hkv, _ = d.shape
+    live = np.zeros((blocks, bt), bool)
+    for row, n in zip(tables, lens):
+        t = np.arange(n)
+        live[row[t // bt], t % bt] = True
+    live = np.broadcast_to(live[:, None], (blocks, hkv, bt))
+    c = np.where(live[..., None], 15, 0).astype(np.uint8).repeat(128, axis=-1)
+    ones = np.array(0xFFFF, np.uint16).view(np.float16)
+    p = np.where(live[..., None], ones, np.float16(0)).repeat(pool.k[1].shape[-1], axis=-1)
+    keep = torch.from_numpy(int4.pack((c, p, p), (c, p, p)) == 0xFF).cuda()
+    d.copy_(torch.where(keep, d, torch.full_like(d, 0xFF)))
+
+
+def _decode(pkv, rng, lens, hq, hkv, bt=16, gd=64, num_ctas=0, q_scale=1.0, scale=128 ** -0.5, poison=True, pool=None, ws=None):
+    blocks = sum(-(-n // bt) for n in lens) + 3
+    pool = pool or Pool(pkv, rng, blocks, hkv, bt, gd)
+    tables = _batch(rng, lens, blocks, bt)
+    if poison:
+        _poison(pool, tables, lens, bt)
+    q = torch.from_numpy(q_scale * rng.standard_normal((len(lens), hq, 128))).to(torch.bfloat16)
+    ws = ws or pkv.AttentionWorkspace(len(lens), hkv)
+    out = torch.full(q.shape, 9.0, dtype=torch.bfloat16, device="cuda")
+    args = (q.cuda(), pool.cache, torch.from_numpy(tables).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), scale)
+    got = pkv.attn_decode_int4(*args, out=out, workspace=ws, num_ctas=num_ctas)
+    assert got.data_ptr() == out.data_ptr() and ws.read_error() == 0
+    want, a, e = int4.decode(q.double().numpy(), pool.k, pool.v, tables, lens, scale)
+    _near(pkv.bits_from_bf16(got), want, a, e, lens)
+    return args, ws, got
+
+
+@pytest.mark.parametrize("gd", [32, 64, 128])
+@pytest.mark.parametrize("bt", [8, 16, 32, 64])
+def test_ragged_lengths(pkv, bt, gd):
+    lens = [1, 0, 2, 7, 8, 9, 15, 16, 17, 31, 33, 63, 64, 65, 100, 127, 129, 255, 257, 700]
+    _decode(pkv, np.random.default_rng(bt * gd), lens, 8, 2, bt, gd)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (2, 1), (3, 1), (8, 1), (5, 5), (14, 2), (24, 4), (32, 8), (64, 8), (16, 16)])
+def test_head_layouts(pkv, hq, hkv):
+    _decode(pkv, np.random.default_rng(hq), [1, 77, 300, 0, 513], hq, hkv)
+
+
+@pytest.mark.parametrize("num_ctas", [1, 2, 3, 7, 64, 151, 152, 300, 304])
+def test_every_grid(pkv, num_ctas):
+    """Pieces of all kinds: a context cut among many CTAs, CTAs of many contexts.
+    (Grids that the workspace has no room for are refused.)"""
+    _decode(pkv, np.random.default_rng(num_ctas), [1500, 3, 0, 40, 4097, 16], 8, 2, num_ctas=num_ctas)
+
+
+def test_one_long_context(pkv):
+    _decode(pkv, np.random.default_rng(8), [40001], 8, 1)
+
+
+def test_many_short_contexts(pkv):
+    rng = np.random.default_rng(9)
+    _decode(pkv, rng, rng.integers(0, 41, size=1000).tolist(), 4, 1, bt=8)
+
+
+def test_the_largest_batch(pkv):
+    rng = np.random.default_rng(10)
+    _decode(pkv, rng, rng.integers(0, 20, size=4096).tolist(), 2, 1)
+
+
+@pytest.mark.parametrize("q_scale", [2.0 ** -30, 2.0 ** -9, 30.0, 2.0 ** 17])
+def test_queries_of_any_size(pkv, q_scale):
+    """Scores of the usual size: what the queries gain the scale gives back."""
+    _decode(pkv, np.random.default_rng(11), [50, 300], 8, 2, q_scale=q_scale, scale=128 ** -0.5 / q_scale)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 0.6])
+def test_scales(pkv, scale):
+    _decode(pkv, np.random.default_rng(12), [50, 1000], 8, 2, scale=scale)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -12, 2.0 ** -6, 300.0, 5000.0])
+def test_values_of_any_size(pkv, size):
+    """Small and large values: their scales span most of fp16."""
+    rng = np.random.default_rng(13)
+    v = (size * rng.standard_normal((25 * 16, 2, 128))).astype(np.float32)
+    v[::3] *= np.float32(1 / 64)
+    v = torch.from_numpy(v).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
+    _decode(pkv, rng, [300, 33], 8, 2, pool=Pool(pkv, rng, 25, 2, 16, 64, v=v))
+
+
+def test_nan_where_it_is_seen(pkv):
+    """A NaN in a key reaches its heads, one in a group of a value those dims."""
+    rng = np.random.default_rng(14)
+    blocks, lens = 8, [60, 60]
+    k, v = _rows(rng, (blocks * 16, 2, 128)), _rows(rng, (blocks * 16, 2, 128))
+    pool = Pool(pkv, rng, blocks, 2, 16, 64, k, v)
+    tables = _batch(rng, lens, blocks, 16)
+    slot = lambda s, t: int(tables[s, t // 16]) * 16 + t % 16
+    at = {int(x): i for i, x in enumerate(pool.slots)}
+    k[at[slot(0, 59)], 1, 5] = 0x7FC0
+    v[at[slot(1, 3)], 0, 70] = 0x7FC0
+    pkv.append_int4(_dev(pkv, k), _dev(pkv, v), torch.from_numpy(pool.slots).cuda(), pool.cache)
+    q = torch.from_numpy(rng.standard_normal((2, 8, 128))).to(torch.bfloat16).cuda()
+    out = pkv.attn_decode_int4(q, pool.cache, torch.from_numpy(tables).cuda(),
+                               torch.tensor(lens, dtype=torch.int32, device="cuda"), 0.1).isnan().cpu()
+    assert out[0, 4:].all() and not out[0, :4].any()
+    assert out[1, :4, 64:].all() and not out[1, :4, :64].any() and not out[1, 4:].any()
+
+
+def test_bad_blocks_and_contexts_are_reported(pkv):
+    rng = np.random.default_rng(15)
+    pool = Pool(pkv, rng, 6, 2, 16, 64)
+    q = torch.zeros((2, 4, 128), dtype=torch.bfloat16, device="cuda")
+    ws = pkv.AttentionWorkspace(2, 2)
+    for bad in (6, -1, 1 << 30, -(1 << 31)):
+        tables = torch.tensor([[0, bad], [1, 2]], dtype=torch.int32, device="cuda")
+        pkv.attn_decode_int4(q, pool.cache, tables, torch.tensor([32, 32], dtype=torch.int32, device="cuda"), 0.1, workspace=ws)
+        assert ws.read_error() == pkv.DEVERR_BLOCK_ID
+    tables = torch.tensor([[0, 3], [1, 2]], dtype=torch.int32, device="cuda")
+    pkv.attn_decode_int4(q, pool.cache, tables, torch.tensor([33, -5], dtype=torch.int32, device="cuda"), 0.1, workspace=ws)
+    assert ws.read_error() == pkv.DEVERR_CONTEXT
+    out = pkv.attn_decode_int4(q, pool.cache, tables, torch.tensor([0, -5], dtype=torch.int32, device="cuda"), 0.1, workspace=ws)
+    assert ws.read_error() == 0 and not out.any()
+
+
+def test_one_workspace_for_both_caches(pkv):
+    """bf16 and 4-bit calls of different batches take turns on one workspace."""
+    rng = np.random.default_rng(16)
+    args, ws, first = _decode(pkv, rng, [900, 20, 333], 8, 2, num_ctas=100)
+    first = first.clone()
+    k = torch.randn((90, 2, 16, 128), device="cuda").to(torch.bfloat16)
+    tables = torch.arange(90, dtype=torch.int32, device="cuda").view(3, 30)
+    ctx = torch.tensor([480, 1, 77], dtype=torch.int32, device="cuda")
+    other = pkv.attn_decode(args[0], k, k, tables, ctx, 0.1, workspace=ws).clone()
+    for grid in (100, 1, 37):
+        got = pkv.attn_decode_int4(*args, workspace=ws, num_ctas=grid)
+        assert torch.equal(other, pkv.attn_decode(args[0], k, k, tables, ctx, 0.1, workspace=ws))
+        if grid == 100:
+            assert torch.equal(first, got)
+    assert ws.read_error() == 0
+
+
+def test_repeats_are_equal_to_the_bit(pkv):
+    args, ws, first = _decode(pkv, np.random.default_rng(17), [5000, 64, 1, 900], 16, 2)
+    first = first.clone()
+    for _ in range(20):
+        assert torch.equal(first, pkv.attn_decode_int4(*args, workspace=ws))
+
+
+def test_streams_and_graphs(pkv):
+    """Append and attention on a side stream, then captured; two graphs that share
+    a workspace replayed in turn with new inputs."""
+    rng = np.random.default_rng(18)
+    args, ws, first = _decode(pkv, rng, [500, 70], 8, 2)
+    q, cache, tables, ctx, scale = args
+    first = first.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = torch.zeros_like(first)
+    for stream in (side, side.cuda_stream):
+        pkv.attn_decode_int4(*args, out=out, workspace=ws, stream=stream)
+        side.synchronize()
+        assert torch.equal(out, first)
+        out.zero_()
+    rows = torch.randn((2, 2, 128), device="cuda").to(torch.bfloat16)
+    t = tables.cpu().tolist()
+    slots = torch.tensor([t[0][500 // 16] * 16 + 500 % 16, t[1][70 // 16] * 16 + 70 % 16], device="cuda")
+    outs = [torch.zeros_like(first) for _ in range(2)]
+    graphs = []
+    for o in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pkv.append_int4(rows, rows, slots, cache)
+            pkv.attn_decode_int4(q, cache, tables, ctx, scale, out=o, workspace=ws)
+        graphs.append(g)
+    ctx += 1
+    for i in range(6):
+        rows.copy_(torch.randn((2, 2, 128), device="cuda"))
+        graphs[i % 2].replay()
+        pkv.append_int4(rows, rows, slots, cache)
+        assert torch.equal(outs[i % 2], pkv.attn_decode_int4(q, cache, tables, ctx, scale))
+    assert ws.read_error() == 0
+
+
+def test_a_pool_past_four_gigabytes(pkv):
+    """Offsets beyond 32 bits: blocks at both ends of a pool of 5.4 GB."""
+    rng = np.random.default_rng(19)
+    blocks = 300_000
+    cache = pkv.Int4Cache(blocks, 8, 16, 64)
+    ids = [blocks - 1, 0, 233_017, 240_000]
+    kb, vb = _rows(rng, (64, 8, 128)), _rows(rng, (64, 8, 128))
+    slots = np.concatenate([np.arange(16) + 16 * b for b in ids[:2] + ids[3:] + ids[2:3]])
+    pkv.append_int4(_dev(pkv, kb), _dev(pkv, vb), torch.from_numpy(slots).cuda(), cache)
+    pkv.block_copy_int4(cache, torch.tensor([[ids[0], 250_001]], dtype=torch.int32, device="cuda"))
+    held = [int4.quantise(_f32(b).reshape(4, 16, 8, 128).swapaxes(1, 2), 64) for b in (kb, vb)]
+    k, v = (torch.empty((2, 8, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pkv.load_int4(cache, torch.tensor([[250_001, 1], [ids[2], 0]], dtype=torch.int32, device="cuda"), k, v)
+    for got, h in ((k, held[0]), (v, held[1])):
+        assert np.array_equal(pkv.bits_from_bf16(got), _bf16(int4.values(*h))[[3, 0]])
+    q = torch.from_numpy(rng.standard_normal((1, 32, 128))).to(torch.bfloat16)
+    lens = [61]
+    got = pkv.attn_decode_int4(q.cuda(), cache, torch.tensor([[250_001, 0, 240_000, 233_017]], dtype=torch.int32, device="cuda"),
+                               torch.tensor(lens, dtype=torch.int32, device="cuda"), 0.1)
+    want, a, e = int4.decode(q.double().numpy(), *held, [[0, 1, 2, 3]], lens, 0.1)
+    _near(pkv.bits_from_bf16(got), want, a, e, lens)
+
+
+def test_refusals_on_the_gpu(pkv):
+    c = pkv.Int4Cache(4, 2)
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device="cuda")
+    i32, i64 = torch.int32, torch.int64
+    ok = dict(k=z(3, 2, 128), v=z(3, 2, 128), slots=z(3, dtype=i64))
+    for bad in (dict(k=z(3, 2, 128, dtype=torch.float16)), dict(k=z(2, 2, 128)), dict(v=z(3, 4, 128)[:, ::2]), dict(v=z(3, 256)),
+                dict(slots=z(3, dtype=i32)), dict(slots=z(4, dtype=i64)), dict(k=ok["k"].cpu()),
+                dict(k=z(3, 1, 128).expand(3, 2, 128))):
+        a = {**ok, **bad}
+        with pytest.raises(ValueError):
+            pkv.append_int4(a["k"], a["v"], a["slots"], c)
+    with pytest.raises(pkv.PkvError):  # the rows of a broadcast tensor overlap: their stride is zero
+        pkv.append_int4(z(1, 2, 128).expand(3, 2, 128), ok["v"], ok["slots"], c)
+    for k, v, p in ((z(4, 2, 8, 128), z(4, 2, 8, 128), z(1, 2, dtype=i32)), (z(4, 2, 16, 128), z(5, 2, 16, 128), z(1, 2, dtype=i32)),
+                    (z(4, 2, 16, 128), z(4, 2, 16, 128), z(1, 2, dtype=i64)), (z(4, 2, 16, 128), z(4, 2, 16, 128), z(3, dtype=i32))):
+        with pytest.raises(ValueError):
+            pkv.load_int4(c, p, k, v)
+    ok = dict(q=z(2, 4, 128), tables=z(2, 3, dtype=i32), ctx=z(2, dtype=i32), out=None)
+    for bad in (dict(q=z(2, 4, 64)), dict(q=z(2, 128)), dict(tables=z(3, 3, dtype=i32)), dict(ctx=z(2, dtype=i64)),
+                dict(ctx=z(3, dtype=i32)), dict(out=z(2, 3, 128)), dict(out=z(2, 4, 128, dtype=torch.float32))):
+        a = {**ok, **bad}
+        with pytest.raises(ValueError):
+            pkv.attn_decode_int4(a["q"], c, a["tables"], a["ctx"], 0.1, out=a["out"])
+    for bad in (dict(q=z(2, 3, 128)), dict(q=z(2, 18, 128))):
+        a = {**ok, **bad}
+        with pytest.raises(pkv.PkvError):
+            pkv.attn_decode_int4(a["q"], c, a["tables"], a["ctx"], 0.1)
+    with pytest.raises(pkv.PkvError):
+        pkv.attn_decode_int4(ok["q"], c, ok["tables"], ok["ctx"], float("nan"))
+    with pytest.raises(pkv.PkvError):  # more CTAs than the workspace has room for
+        pkv.attn_decode_int4(ok["q"], c, ok["tables"], ok["ctx"], 0.1, num_ctas=2048)
