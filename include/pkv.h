@@ -68,6 +68,8 @@ typedef int pkv_status;
 #define PKV_ATTN_MAX_SEQS 4096  /* max num_seqs of one pkv_attn_decode call */
 #define PKV_ATTN_MAX_CTAS 2048  /* max num_ctas of one pkv_attn_decode call */
 #define PKV_TREE_MAX_DRAFTS 64  /* max drafted tokens of one sequence in pkv_attn_tree */
+#define PKV_BEAM_MAX_BEAMS 32       /* max beams of a group in pkv_beam_select */
+#define PKV_BEAM_MAX_CANDIDATES 64  /* max continuations taken per group */
 #define PKV_ROPE_MAX_HEAD_DIM 256 /* max head_dim of pkv_qk_norm_rope_append */
 
 /* Library version (major * 10000 + minor * 100 + patch). */
@@ -439,6 +441,58 @@ pkv_status pkv_attn_decode_int4(const void* q, const void* cache, const int32_t*
                                 size_t workspace_bytes, void* out, void* stream);
 
 /*
+ * pkv_beam_select -- beam search's selection: of each group of beams (the
+ * hypotheses of one request, whose sequences share blocks: cs2680 Lecture 10,
+ * §10.4) the best continuations over the vocabulary, and their token histories.
+ * The pages name beams among the uses of shared blocks and describe no
+ * selection. Beam k of group b, row b * num_beams + k of logits, has the
+ * candidates
+ *   (k, v) with score scores[b][k] + logits[row][v] - log sum_v exp logits[row][v]
+ * or, where finished[b][k] != 0, the single one (k, eos) with score scores[b][k]
+ * (its logits are not read). Of all candidates of the group the num_candidates
+ * with the highest scores are taken, equal scores in the order of k * vocab + v.
+ * A candidate whose score is NaN or -inf is none: barred tokens have logits of
+ * -inf, beams that do not exist yet scores of -inf (their logits are not read).
+ *   logits       : device, bf16 (logits_bytes = 2) or fp32 (4); num_groups *
+ *                  num_beams rows of vocab contiguous values, one every
+ *                  row_stride >= vocab values; any alignment
+ *   scores       : device fp32 [num_groups][num_beams]
+ *   finished     : device bytes [num_groups][num_beams], or NULL for none
+ *   eos          : the token that ends a beam, -1 for none (finished NULL)
+ *   history, lengths : device int32 [num_groups][num_beams][max_length] and
+ *                  [num_groups][num_beams], or both NULL (then so are the
+ *                  outputs): the first `length` tokens of a row count
+ *   scores_out, tokens_out, parents_out, finished_out : device fp32, int32,
+ *                  int32, bytes [num_groups][num_candidates], best first;
+ *                  parents_out is the beam k; finished_out says that the parent
+ *                  was finished or the token is eos. Where a group has fewer
+ *                  candidates the rest are (-inf, -1, -1, 0)
+ *   history_out, lengths_out : [num_groups][num_candidates][max_length] and
+ *                  [num_groups][num_candidates]: the parent's tokens, then the
+ *                  new one unless the parent was finished; what lies behind
+ *                  them stays as it was, a missing candidate has length 0. Must
+ *                  not overlap history. A parent that has max_length tokens
+ *                  takes no more and sets PKV_DEVERR_CONTEXT in device_error
+ *                  (which may be NULL); so does a length outside [0, max_length],
+ *                  which is clamped
+ *   workspace    : device scratch of pkv_beam_workspace_size bytes for the same
+ *                  four sizes, 256-byte aligned; it holds nothing between calls.
+ *                  Calls that share one must not overlap on the GPU
+ * Scores are formed and compared in 64 bits from sums of exponentials in 32.
+ * Limits: num_beams <= 32, num_candidates <= 64 (PKV_EUNSUPPORTED), num_beams *
+ * vocab < 2^31 (PKV_ERANGE).
+ */
+pkv_status pkv_beam_select(const void* logits, int64_t row_stride, int logits_bytes, const float* scores,
+                           const uint8_t* finished, int eos, int num_groups, int num_beams,
+                           int num_candidates, int vocab, const int32_t* history, const int32_t* lengths,
+                           int max_length, float* scores_out, int32_t* tokens_out, int32_t* parents_out,
+                           uint8_t* finished_out, int32_t* lengths_out, int32_t* history_out,
+                           void* workspace, size_t workspace_bytes, uint32_t* device_error, void* stream);
+
+/* Bytes of device scratch for pkv_beam_select; 0 on invalid arguments. */
+size_t pkv_beam_workspace_size(int num_groups, int num_beams, int num_candidates, int vocab);
+
+/*
  * Cascade attention -- pkv_attn_decode for a batch whose sequences share
  * leading blocks, reading each shared block once for all its sharers instead
  * of once per sequence. The pages share those blocks in memory ("KV cache
@@ -704,6 +758,17 @@ pkv_status pkv_bm_admit_tokens(pkv_bm* bm, const int32_t* tokens, int prompt_len
 
 /* child_ids: host int32 [n]. All-or-nothing. The parent must be running. */
 pkv_status pkv_bm_fork(pkv_bm* bm, int parent_seq, int n, int32_t* child_ids);
+
+/* Beam search's step: sequence seq_ids[i] goes on as sequence
+ * seq_ids[parents[i]] is now (host int32 arrays [n], distinct running ids,
+ * parents in [0, n)). Blocks are shared by reference, none is copied: a
+ * sequence that several go on as keeps its table under its own id where it is
+ * one of them (else under the first of theirs), the others are its children as
+ * of pkv_bm_fork, and one that nobody goes on as is released first; writes into
+ * what is shared then make copy-on-write pairs in pkv_bm_prepare_append (cs2680
+ * Lecture 10, §10.4: shared blocks, copied on divergence). PKV_ENOMEM, with no
+ * state change, when the children need more pages than are available then. */
+pkv_status pkv_bm_reorder(pkv_bm* bm, const int32_t* seq_ids, const int32_t* parents, int n);
 
 /* For each listed sequence (distinct ids, processed in order): the slot of
  * its next token and, where that token lands in a shared block, one

@@ -55,6 +55,8 @@ implementations share):
 """
 from __future__ import annotations
 
+import copy
+
 
 class BlockManagerError(Exception):
     pass
@@ -263,6 +265,38 @@ class BlockManager:
             self.reused[sid] = 0
             kids.append(sid)
         return kids
+
+    def reorder(self, seq_ids, parents) -> None:
+        """Sequence seq_ids[i] goes on as seq_ids[parents[i]] is (beam search's
+        step): first those that nobody goes on as are released, then each parent's
+        table goes to itself or else to the first that goes on as it, and the
+        others share its written blocks as a fork's children do."""
+        seq_ids, parents = [int(s) for s in seq_ids], [int(p) for p in parents]
+        n = len(seq_ids)
+        if len(set(seq_ids)) != n or len(parents) != n or any(not 0 <= p < n for p in parents) or any(
+                s not in self.seqs or not self.seqs[s].running for s in seq_ids):
+            raise InvalidRequest("unknown, preempted or repeated sequence id, or a parent outside the list")
+        was = [self.seqs[s] for s in seq_ids]
+        heirs = {p: p if parents[p] == p else parents.index(p) for p in set(parents)}
+        before = copy.deepcopy(self.__dict__)
+        try:
+            for p in range(n):
+                if p not in heirs:
+                    self._release(was[p].table)
+                    self._leave_group(was[p])
+            for i, p in enumerate(parents):
+                if heirs[p] == i:
+                    self.seqs[seq_ids[i]] = _Seq(list(was[p].table), was[p].ctx, was[p].group, was[p].max_len)
+                    continue
+                self.seqs[-1] = was[p]  # under a name of its own while it is forked
+                kid, = self.fork(-1, 1)
+                self.next_id -= 1
+                del self.reused[kid], self.seqs[-1]
+                self.seqs[seq_ids[i]] = self.seqs.pop(kid)
+        except PoolExhausted:
+            self.__dict__.clear()
+            self.__dict__.update(before)
+            raise
 
     # -- decode-step bookkeeping ------------------------------------------
     def prepare_append(self, seq_ids):

@@ -50,7 +50,7 @@ EXPORTED = [
     "pkv_attn_decode_wait_test", "pkv_attn_decode_cuda_cores", "pkv_attn_workspace_fixed_bytes",
     "pkv_attn_launch_ctas", "pkv_attn_prefill", "pkv_attn_prefill_workspace_size", "pkv_attn_tree",
     "pkv_qk_norm_rope_append", "pkv_int4_block_bytes", "pkv_append_int4", "pkv_load_int4", "pkv_block_copy_int4",
-    "pkv_attn_decode_int4",
+    "pkv_attn_decode_int4", "pkv_beam_select", "pkv_beam_workspace_size", "pkv_bm_reorder",
 ]
 BLOCK_SIZES = (8, 16, 32, 64)
 INT4_GROUP_DIMS = (32, 64, 128)
@@ -157,6 +157,10 @@ def _load() -> ctypes.CDLL:
         "pkv_block_copy_int4": (i32, [vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]),
         "pkv_attn_decode_int4": (i32, [vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz, vp,
                                        vp]),
+        "pkv_beam_workspace_size": (sz, [i32, i32, i32, i32]),
+        "pkv_beam_select": (i32, [vp, i64, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp,
+                                  sz, vp, vp]),
+        "pkv_bm_reorder": (i32, [vp, vp, vp, i32]),
         "pkv_decode_step_host": (i32, [vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz, vp, vp,
                                        vp, vp]),
     }
@@ -880,6 +884,97 @@ def attn_decode_int4(q, cache: Int4Cache, block_tables, context_lens, scale, out
 
 
 # ---------------------------------------------------------------------------
+# beam search
+
+
+class BeamBuffers:
+    """What beam_select leaves of each group's `candidates` best continuations,
+    best first: scores (fp32), tokens, parents (int32), finished (bool) [groups,
+    candidates]; with max_length also lengths (int32) and history (int32 [groups,
+    candidates, max_length])."""
+
+    def __init__(self, groups: int, candidates: int, max_length: int = 0, device=None):
+        new = lambda dtype, *more: torch.zeros((groups, candidates, *more), dtype=dtype, device=device or "cuda")
+        self.scores, self.tokens, self.parents = new(_F32), new(_I32), new(_I32)
+        self.finished = new(torch.bool)
+        self.lengths, self.history = (new(_I32), new(_I32, max_length)) if max_length else (None, None)
+
+
+class BeamWorkspace:
+    """Device scratch of beam_select for one shape; it holds nothing between calls."""
+
+    def __init__(self, groups: int, beams: int, candidates: int, vocab: int, device=None):
+        self.shape = groups, beams, candidates, vocab
+        self.nbytes = int(_lib.pkv_beam_workspace_size(*self.shape))
+        if self.nbytes == 0:
+            raise PkvError(PKV_EINVAL, "pkv_beam_workspace_size")
+        self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device or "cuda")
+        off = (-self.buffer.data_ptr()) % 256
+        self.tensor = self.buffer[off : off + self.nbytes]
+        self.ptr, self.device = self.tensor.data_ptr(), self.tensor.get_device()
+
+
+def beam_select(logits, scores, finished=None, eos: int = -1, history=None, lengths=None, candidates: int | None = None,
+                out: BeamBuffers | None = None, workspace: BeamWorkspace | None = None, device_error=None, stream=None):
+    """The best continuations of groups of beams: logits [groups * beams, vocab]
+    (bf16 or fp32, rows apart by any stride), scores fp32 [groups, beams]; finished
+    bool [groups, beams]; history int32 [groups, beams, max_length] and lengths
+    int32 [groups, beams], or neither. Takes out's number of candidates, or
+    `candidates` (default: one per beam). Returns the BeamBuffers."""
+    device = logits.get_device()
+    if logits.dtype not in (_BF16, _F32) or logits.dim() != 2:
+        raise ValueError(f"logits must be bf16 or fp32 [groups * beams, vocab], got {logits.dtype} {list(logits.shape)}")
+    _need_all(device, ((scores, _F32, "scores"),))
+    if scores.dim() != 2 or logits.shape[0] != scores.numel() or scores.numel() == 0:
+        raise ValueError("scores must be [groups, beams], a row of logits each")
+    (groups, beams), vocab = scores.shape, logits.shape[1]
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("a row of logits must be contiguous")
+    if finished is not None:
+        _need_all(device, ((finished, torch.bool, "finished"),))
+        if finished.shape != scores.shape:
+            raise ValueError("finished must be shaped like scores")
+    if (history is None) != (lengths is None):
+        raise ValueError("history and lengths come together")
+    room = 0
+    if history is not None:
+        _need_all(device, ((history, _I32, "history"), (lengths, _I32, "lengths")))
+        if history.dim() != 3 or history.shape[:2] != scores.shape or lengths.shape != scores.shape or history.shape[2] < 1:
+            raise ValueError("history must be [groups, beams, max_length] and lengths [groups, beams]")
+        room = history.shape[2]
+    n = candidates if candidates is not None else out.scores.shape[1] if out is not None else beams
+    if out is not None:
+        parts = [(out.scores, _F32, "out.scores"), (out.tokens, _I32, "out.tokens"), (out.parents, _I32, "out.parents"),
+                 (out.finished, torch.bool, "out.finished")]
+        if room:
+            if out.history is None or out.history.shape != (groups, n, room):
+                raise ValueError("out's histories must be [groups, candidates, max_length], as the beams'")
+            if out.history.data_ptr() == history.data_ptr():
+                raise ValueError("out's histories must not be the beams'")
+            parts += [(out.lengths, _I32, "out.lengths"), (out.history, _I32, "out.history")]
+        _need_all(device, parts)
+        if any(t.shape != (groups, n) for t, _, name in parts if name != "out.history"):
+            raise ValueError(f"out must hold {groups} groups of {n} candidates")
+    if workspace is not None and workspace.device != device:
+        raise ValueError(f"the workspace is on cuda:{workspace.device}, the tensors on cuda:{device}")
+    if device_error is not None:
+        _need_all(device, ((device_error, _I32, "device_error"),))
+    with _launch_on(device, stream) as st:
+        if out is None:
+            out = BeamBuffers(groups, n, room, device=logits.device)
+        if workspace is None:
+            workspace = BeamWorkspace(groups, beams, n, vocab, device=logits.device)
+        stride = logits.stride(0) if logits.shape[0] > 1 else vocab
+        _check(_lib.pkv_beam_select(logits.data_ptr(), stride, logits.element_size(), scores.data_ptr(), _ptr(finished),
+                                    int(eos), groups, beams, n, vocab, _ptr(history), _ptr(lengths), room,
+                                    out.scores.data_ptr(), out.tokens.data_ptr(), out.parents.data_ptr(),
+                                    out.finished.data_ptr(), _ptr(out.lengths) if room else None,
+                                    _ptr(out.history) if room else None, workspace.ptr, workspace.nbytes,
+                                    _ptr(device_error), st), "pkv_beam_select")
+    return out
+
+
+# ---------------------------------------------------------------------------
 # host block manager
 
 
@@ -937,6 +1032,19 @@ class BlockManager:
         for i in ids[:n]:
             self.prompt[i], self.written[i] = self.prompt[parent], self.written[parent]
         return list(ids[:n])
+
+    def reorder(self, seq_ids, parents) -> None:
+        """Sequence seq_ids[i] goes on as seq_ids[parents[i]] is now (beam search):
+        tables are shared by reference; PoolExhausted leaves all as it was."""
+        n = len(seq_ids)
+        if len(parents) != n:
+            raise ValueError("one parent per sequence")
+        ids = (ctypes.c_int32 * max(n, 1))(*[int(x) for x in seq_ids])
+        src = (ctypes.c_int32 * max(n, 1))(*[int(x) for x in parents])
+        _check(_lib.pkv_bm_reorder(self._h, ids, src, n), "pkv_bm_reorder")
+        for kept in (self.prompt, self.written):
+            was = [kept[s] for s in ids[:n]]
+            kept.update({s: was[p] for s, p in zip(ids[:n], src[:n])})
 
     def prepare_append(self, seq_ids):
         """Returns (slots list[int], pairs list[(src, dst)])."""

@@ -150,6 +150,34 @@ struct pkv_bm {
         }
     }
 
+    // Pages that a child of `parent` takes: private ones for the rest of its
+    // allowance, and a spare for the copy of a partial last block (none where
+    // pages are taken as they are needed).
+    int64_t written_blocks(const Sequence& parent) const { return ceil_div(parent.ctx, block_tokens); }
+    bool needs_spare(const Sequence& parent) const { return parent.ctx % block_tokens != 0 && !incremental; }
+    int64_t child_pages(const Sequence& parent) const {
+        return incremental ? 0 : (static_cast<int64_t>(parent.table.size()) - written_blocks(parent)) + (needs_spare(parent) ? 1 : 0);
+    }
+
+    // A sequence that shares the parent's written blocks (callers have checked
+    // available()).
+    Sequence child_of(const Sequence& parent) {
+        const int64_t written = written_blocks(parent);
+        Sequence child;
+        child.ctx = parent.ctx;
+        child.max_len = parent.max_len;
+        child.group = parent.group;
+        child.table.assign(parent.table.begin(), parent.table.begin() + written);
+        while (child.table.size() < parent.table.size()) child.table.push_back(alloc());
+        for (int32_t b : child.table) ref[b] += 1;
+        if (needs_spare(parent)) {
+            spares[parent.table[written - 1]].push_back(alloc());
+            spare_count += 1;
+        }
+        if (parent.group >= 0) groups[parent.group].members += 1;
+        return child;
+    }
+
     Sequence* running_seq(int id) {
         auto it = seqs.find(id);
         return it == seqs.end() || !it->second.running ? nullptr : &it->second;
@@ -302,27 +330,60 @@ pkv_status pkv_bm_fork(pkv_bm* bm, int parent_seq, int n, int32_t* child_ids) {
     const Sequence* p = bm->running_seq(parent_seq);
     if (!p) return PKV_EINVAL;
     const Sequence parent = *p;  // copy: emplacing children may rehash
-    const int64_t written = ceil_div(parent.ctx, bm->block_tokens);
-    const bool partial = parent.ctx % bm->block_tokens != 0 && !bm->incremental;
-    const int64_t per_child = bm->incremental
-        ? 0 : (static_cast<int64_t>(parent.table.size()) - written) + (partial ? 1 : 0);
-    if (static_cast<int64_t>(n) * per_child > bm->available()) return PKV_ENOMEM;
+    if (static_cast<int64_t>(n) * bm->child_pages(parent) > bm->available()) return PKV_ENOMEM;
     for (int i = 0; i < n; ++i) {
-        Sequence child;
-        child.ctx = parent.ctx;
-        child.max_len = parent.max_len;
-        child.group = parent.group;
-        child.table.assign(parent.table.begin(), parent.table.begin() + written);
-        while (child.table.size() < parent.table.size()) child.table.push_back(bm->alloc());
-        for (int32_t b : child.table) bm->ref[b] += 1;
-        if (partial) {
-            bm->spares[parent.table[written - 1]].push_back(bm->alloc());
-            bm->spare_count += 1;
-        }
-        if (parent.group >= 0) bm->groups[parent.group].members += 1;
         const int id = bm->next_id++;
-        bm->seqs.emplace(id, std::move(child));
+        bm->seqs.emplace(id, bm->child_of(parent));
         child_ids[i] = id;
+    }
+    return PKV_OK;
+}
+
+// A sequence that nobody goes on as is released; one of those that go on as a
+// parent (the parent itself, else the first) takes its table over, the others
+// are its children as of a fork.
+pkv_status pkv_bm_reorder(pkv_bm* bm, const int32_t* seq_ids, const int32_t* parents, int n) {
+    if (!bm || n < 0 || (n > 0 && (!seq_ids || !parents))) return PKV_EINVAL;
+    std::lock_guard<std::mutex> lock(bm->mu);
+    {
+        std::vector<int32_t> sorted(seq_ids, seq_ids + n);
+        std::sort(sorted.begin(), sorted.end());
+        if (std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end()) return PKV_EINVAL;
+    }
+    std::vector<int> heir(n, -1);
+    for (int i = 0; i < n; ++i) {
+        if (!bm->running_seq(seq_ids[i]) || parents[i] < 0 || parents[i] >= n) return PKV_EINVAL;
+        if (heir[parents[i]] < 0 || parents[i] == i) heir[parents[i]] = i;
+    }
+    // The pages that the children take and those that the released tables leave,
+    // before anything changes.
+    int64_t need = 0, freed = 0;
+    std::unordered_map<int32_t, int64_t> ref_left, spare_left;
+    for (int i = 0; i < n; ++i) {
+        if (heir[parents[i]] != i) need += bm->child_pages(*bm->running_seq(seq_ids[parents[i]]));
+        if (heir[i] >= 0) continue;
+        for (int32_t b : bm->running_seq(seq_ids[i])->table) {
+            auto r = ref_left.emplace(b, bm->ref[b]).first;
+            auto sp = spare_left.emplace(b, bm->spares[b].size()).first;
+            r->second -= 1;
+            if (sp->second > 0 && sp->second > r->second - 1) {
+                sp->second -= 1;
+                freed += 1;
+            }
+            freed += r->second == 0;
+        }
+    }
+    if (need > bm->available() + freed) return PKV_ENOMEM;
+    std::vector<Sequence> old;
+    for (int i = 0; i < n; ++i) old.push_back(std::move(*bm->running_seq(seq_ids[i])));
+    for (int i = 0; i < n; ++i) {
+        if (heir[i] >= 0) continue;
+        bm->release(old[i].table);
+        bm->leave_group(old[i]);
+    }
+    for (int i = 0; i < n; ++i) {
+        const Sequence& parent = old[parents[i]];
+        *bm->running_seq(seq_ids[i]) = heir[parents[i]] == i ? parent : bm->child_of(parent);
     }
     return PKV_OK;
 }
