@@ -14,8 +14,9 @@ from ._native import (  # noqa: F401
     decode_step_host, default_ctas, launch_ctas, load_int4, new_error_word, qk_norm_rope_append, read_device_error,
     rope_table, step_layout, tree_masks,
 )
+from .beams import BeamSearch  # noqa: F401
 from .engine import (  # noqa: F401
-    CASCADE_MIN_SAVED_BYTES, DraftBuffers, HostStep, PagedKVEngine, PromptBuffers, RopeSpec, StepBuffers, bf16_from_bits,
+    CASCADE_MIN_SAVED_BYTES, DraftBuffers, HostStep, Int4Pages, PagedKVEngine, PromptBuffers, RopeSpec, StepBuffers, bf16_from_bits,
     bits_from_bf16, cascade_saved_bytes, shared_prefix_groups,
 )
 from .graphs import GraphedDecoder, default_buckets  # noqa: F401

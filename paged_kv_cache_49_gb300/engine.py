@@ -99,6 +99,14 @@ class RopeSpec:
 
 
 @dataclass
+class Int4Pages:
+    """The pages of a batch's contexts in a 4-bit cache, and where they lie once they
+    are loaded as bf16 pages, each page once."""
+    pairs: torch.Tensor       # int32 [n, 2]: block, place
+    tables: torch.Tensor      # int32 [B, W] of places
+
+
+@dataclass
 class PromptBuffers:
     """Device inputs of one prefill call: packed rows of several sequences."""
     seq_ids: list
@@ -108,6 +116,7 @@ class PromptBuffers:
     ctx: torch.Tensor         # int32 [B], the chunk included
     starts: torch.Tensor      # int32 [B + 1]
     slots: torch.Tensor       # int64 [T]
+    pages: Int4Pages | None = None
 
 
 @dataclass
@@ -123,19 +132,32 @@ class DraftBuffers:
     slots: torch.Tensor       # int64 [T], all -1: nothing is appended yet
     held: list                # the sequences' context lengths
     parents: list             # the sequences' trees
+    pages: Int4Pages | None = None
 
 
 class PagedKVEngine:
+    """cache_bits 16: the pools k_cache and v_cache hold bf16. cache_bits 4: `cache`
+    (an Int4Cache) holds keys and values quantised in groups of group_dims; what
+    is attended, by decode steps, prompts and drafts alike, is what it holds."""
+
     def __init__(self, num_blocks: int, num_q_heads: int, num_kv_heads: int, head_dim: int = 128,
                  device="cuda", free_order=None, block_tokens: int = nat.BLOCK_TOKENS, incremental: bool = False,
-                 watermark: int = 0, prefix_cache: bool = False):
+                 watermark: int = 0, prefix_cache: bool = False, cache_bits: int = 16, group_dims: int = 64):
+        if cache_bits not in (4, 16):
+            raise ValueError("cache_bits is 4 or 16")
+        if cache_bits == 4 and head_dim != nat.HEAD_DIM:
+            raise ValueError(f"a 4-bit cache has heads of {nat.HEAD_DIM} values")
         self.num_blocks, self.num_q_heads, self.num_kv_heads, self.head_dim = (
             num_blocks, num_q_heads, num_kv_heads, head_dim)
         self.block_tokens = block_tokens
         self.device = torch.device(device)
-        shape = (num_blocks, num_kv_heads, block_tokens, head_dim)
-        self.k_cache = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        self.v_cache = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        self.k_cache = self.v_cache = self.cache = None
+        if cache_bits == 4:
+            self.cache = nat.Int4Cache(num_blocks, num_kv_heads, block_tokens, group_dims, device=self.device)
+        else:
+            shape = (num_blocks, num_kv_heads, block_tokens, head_dim)
+            self.k_cache = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            self.v_cache = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
         self.bm = nat.BlockManager(num_blocks, block_tokens, free_order, incremental=incremental,
                                    watermark=watermark, prefix_cache=prefix_cache)
         self.error = nat.new_error_word(self.device)
@@ -143,6 +165,12 @@ class PagedKVEngine:
     # ---- pool content ----------------------------------------------------
     def load_pool(self, k_bits: np.ndarray, v_bits: np.ndarray, lo: int = 0) -> None:
         n = k_bits.shape[0]
+        if self.cache is not None:
+            rows = [bf16_from_bits(b).to(self.device).transpose(1, 2).reshape(n * self.block_tokens, self.num_kv_heads, -1)
+                    for b in (k_bits, v_bits)]
+            first = lo * self.block_tokens
+            self._write(*rows, torch.arange(first, first + n * self.block_tokens, device=self.device))
+            return
         self.k_cache[lo : lo + n].copy_(bf16_from_bits(k_bits))
         self.v_cache[lo : lo + n].copy_(bf16_from_bits(v_bits))
 
@@ -170,6 +198,18 @@ class PagedKVEngine:
                 if t.is_cuda:  # others are refused by the call itself
                     t.record_stream(self._side(stream))
 
+    def _write(self, k, v, slots, stream=None) -> None:
+        if self.cache is not None:
+            nat.append_int4(k, v, slots, self.cache, self.error, stream)
+        else:
+            nat.append(k, v, slots, self.k_cache, self.v_cache, self.error, stream)
+
+    def _copy(self, pairs, stream=None) -> None:
+        if self.cache is not None:
+            nat.block_copy_int4(self.cache, pairs, self.error, stream)
+        else:
+            nat.block_copy(self.k_cache, self.v_cache, pairs, self.error, stream)
+
     def append_tokens(self, seq_ids, k: torch.Tensor, v: torch.Tensor, stream=None):
         """Append one token per sequence (k, v: [B, Hkv, D] bf16 on device);
         returns (slots, pairs) as the block manager decided them."""
@@ -177,9 +217,9 @@ class PagedKVEngine:
         with self._on(stream):
             if pairs:
                 pt = torch.tensor(pairs, dtype=torch.int32).to(self.device, non_blocking=True)
-                nat.block_copy(self.k_cache, self.v_cache, pt, self.error)
+                self._copy(pt)
             st = torch.tensor(slots, dtype=torch.int64).to(self.device, non_blocking=True)
-            nat.append(k, v, st, self.k_cache, self.v_cache, self.error)
+            self._write(k, v, st)
         self._keep(stream, k, v)
         return slots, pairs
 
@@ -190,7 +230,7 @@ class PagedKVEngine:
         slots = self.bm.slots(seq_id, first, int(k.shape[0]))
         with self._on(stream):
             st = torch.tensor(slots, dtype=torch.int64).to(self.device, non_blocking=True)
-            nat.append(k, v, st, self.k_cache, self.v_cache, self.error)
+            self._write(k, v, st)
         self._keep(stream, k, v)
         self._wrote(seq_id, first, len(slots))
         return slots
@@ -220,8 +260,9 @@ class PagedKVEngine:
             slots += self.bm.slots(s, f, c) if c else []
             self._wrote(s, f, c)
             positions += range(f, f + c)
-        return PromptBuffers(*self._rows(seq_ids, counts, [f + c for f, c in zip(first, counts)], positions),
-                             slots=torch.tensor(slots, dtype=torch.int64).to(self.device))
+        held = [f + c for f, c in zip(first, counts)]
+        return PromptBuffers(*self._rows(seq_ids, counts, held, positions),
+                             slots=torch.tensor(slots, dtype=torch.int64).to(self.device), pages=self._pages(seq_ids, held))
 
     def _known(self, seq_id) -> int:
         """A sequence's tokens, from the first on, that are in the cache or on their
@@ -244,11 +285,38 @@ class PagedKVEngine:
         ints = lambda x: torch.tensor(x, dtype=torch.int32).to(self.device)
         return seq_ids, counts, ints(positions), tables.to(self.device), ints(context_lens), torch.from_numpy(starts).to(self.device)
 
+    def _pages(self, seq_ids, context_lens) -> Int4Pages | None:
+        if self.cache is None:
+            return None
+        rows = [self.bm.table(s)[: -(-c // self.block_tokens)] for s, c in zip(seq_ids, context_lens)]
+        place = {b: i for i, b in enumerate(dict.fromkeys(b for row in rows for b in row))}
+        tables = torch.full((len(rows), max(1, max(len(row) for row in rows))), -1, dtype=torch.int32)
+        for i, row in enumerate(rows):
+            tables[i, : len(row)] = torch.tensor([place[b] for b in row], dtype=torch.int32)
+        pairs = torch.tensor(list(place.items()), dtype=torch.int32).reshape(-1, 2)
+        return Int4Pages(pairs.to(self.device), tables.to(self.device))
+
+    def _room(self, pages: Int4Pages):
+        """bf16 pools for the pages."""
+        shape = (max(1, pages.pairs.shape[0]), self.num_kv_heads, self.block_tokens, self.head_dim)
+        return [torch.empty(shape, dtype=torch.bfloat16, device=self.device) for _ in range(2)]
+
+    def _turn(self, rope, q, k, v, positions, pools):
+        """Normed, rotated queries and keys, nothing written to the pools."""
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        nowhere = torch.full((k.shape[0],), -1, dtype=torch.int64, device=k.device)
+        q = nat.qk_norm_rope_append(q, k, v, rope.cos_sin, positions, nowhere, *pools, q_weight=rope.q_weight,
+                                    k_weight=rope.k_weight, eps=rope.eps, interleaved=rope.interleaved, k_out=k_out,
+                                    device_error=self.error)
+        return q, k_out
+
     def run_prefill(self, pb: PromptBuffers, q, k, v, scale: float, workspace, rope=None, out=None, stream=None):
         """The device part: the chunk's keys and values into the cache, then
         causal attention of its rows. q [T, Hq, D], k, v [T, Hkv, D] (bf16 on the
         device), packed in pb's order."""
         self._keep(stream, q, k, v, pb.positions, pb.tables, pb.ctx, pb.starts, pb.slots)
+        if self.cache is not None:
+            return self._run_prefill_int4(pb, q, k, v, scale, workspace, rope, out, stream)
         with self._on(stream):
             if rope is None:
                 nat.append(k, v, pb.slots, self.k_cache, self.v_cache, self.error)
@@ -258,6 +326,18 @@ class PagedKVEngine:
                                             interleaved=rope.interleaved, device_error=self.error)
             return nat.attn_prefill(q, self.k_cache, self.v_cache, pb.tables, pb.ctx, pb.starts, scale, out=out,
                                     workspace=workspace)
+
+    def _run_prefill_int4(self, pb, q, k, v, scale, workspace, rope, out, stream):
+        """The chunk goes into the 4-bit cache, then the pages of its contexts, the
+        chunk's own among them, come back as bf16 pages for the attention."""
+        self._keep(stream, pb.pages.pairs, pb.pages.tables)
+        with self._on(stream):
+            pools = self._room(pb.pages)
+            if rope is not None:
+                q, k = self._turn(rope, q, k, v, pb.positions, pools)
+            nat.append_int4(k, v, pb.slots, self.cache, self.error)
+            nat.load_int4(self.cache, pb.pages.pairs, *pools, self.error)
+            return nat.attn_prefill(q, *pools, pb.pages.tables, pb.ctx, pb.starts, scale, out=out, workspace=workspace)
 
     def prepare_drafts(self, seq_ids, parents) -> DraftBuffers:
         """Host bookkeeping of a verification step: sequence seq_ids[i] has the
@@ -275,12 +355,14 @@ class PagedKVEngine:
         rows = self._rows(seq_ids, [len(p) for p in parents], ctx, positions)
         return DraftBuffers(*rows, masks=torch.tensor(masks, dtype=torch.int64).to(self.device),
                             slots=torch.full((len(masks),), -1, dtype=torch.int64).to(self.device), held=ctx,
-                            parents=parents)
+                            parents=parents, pages=self._pages(seq_ids, ctx))
 
     def run_drafts(self, db: DraftBuffers, q, k, v, scale: float, workspace, rope=None, out=None, stream=None):
         """The device part: (attention of the drafts, their keys as the cache would
         hold them); the cache stays as it was."""
         self._keep(stream, q, k, v, db.positions, db.tables, db.ctx, db.starts, db.masks, db.slots)
+        if self.cache is not None:
+            return self._run_drafts_int4(db, q, k, v, scale, workspace, rope, out, stream)
         with self._on(stream):
             if rope is not None:
                 k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
@@ -290,6 +372,17 @@ class PagedKVEngine:
                 k = k_out
             out = nat.attn_tree(q, k, v.contiguous(), db.masks, self.k_cache, self.v_cache, db.tables, db.ctx, db.starts,
                                 scale, out=out, workspace=workspace)
+        return out, k
+
+    def _run_drafts_int4(self, db, q, k, v, scale, workspace, rope, out, stream):
+        self._keep(stream, db.pages.pairs, db.pages.tables)
+        with self._on(stream):
+            pools = self._room(db.pages)
+            if rope is not None:
+                q, k = self._turn(rope, q, k, v, db.positions, pools)
+            nat.load_int4(self.cache, db.pages.pairs, *pools, self.error)
+            out = nat.attn_tree(q, k, v.contiguous(), db.masks, *pools, db.pages.tables, db.ctx, db.starts, scale, out=out,
+                                workspace=workspace)
         return out, k
 
     def accept_drafts(self, db: DraftBuffers, paths, k, v, stream=None):
@@ -327,11 +420,17 @@ class PagedKVEngine:
         self._keep(stream, k, v)
         with self._on(stream):
             if pairs:
-                nat.block_copy(self.k_cache, self.v_cache, torch.tensor(pairs, dtype=torch.int32).to(self.device), self.error)
-            nat.append(k, v.contiguous(), torch.from_numpy(slots).to(self.device), self.k_cache, self.v_cache, self.error)
+                self._copy(torch.tensor(pairs, dtype=torch.int32).to(self.device))
+            self._write(k, v.contiguous(), torch.from_numpy(slots).to(self.device))
         if refused is not None:
             raise refused
         return slots.tolist()
+
+    def reorder(self, seq_ids, parents) -> None:
+        """Sequence seq_ids[i] goes on as seq_ids[parents[i]] is now, as beam search
+        asks after each selection: pages are shared by reference, and copied where
+        prepare_step or append_tokens finds the next token in a shared one."""
+        self.bm.reorder(seq_ids, parents)
 
     def replay_events(self, w, with_content: bool = True):
         """Apply a workload's admit / fork / history events; history appends
@@ -381,8 +480,8 @@ class PagedKVEngine:
     def run_step(self, sb: StepBuffers, scale: float, num_ctas: int = 0, stream=None) -> torch.Tensor:
         """The device part of a decode step -- copy-on-write copies, append,
         attention -- as one library call (separate calls for block sizes
-        other than 16). Idempotent for fixed inputs."""
-        if self.block_tokens != nat.BLOCK_TOKENS:
+        other than 16 and for a 4-bit cache). Idempotent for fixed inputs."""
+        if self.cache is not None or self.block_tokens != nat.BLOCK_TOKENS:
             return self.run_step_separate(sb, scale, num_ctas, stream)
         return nat.decode_step(sb.q, sb.k, sb.v, sb.slots, sb.pairs, self.k_cache, self.v_cache, sb.tables,
                                sb.ctx, scale, sb.out, sb.workspace, self.error, num_ctas, stream)
@@ -390,16 +489,19 @@ class PagedKVEngine:
     def run_step_separate(self, sb: StepBuffers, scale: float, num_ctas: int = 0, stream=None) -> torch.Tensor:
         """The same step as three separate library calls."""
         if sb.num_pairs:
-            nat.block_copy(self.k_cache, self.v_cache, sb.pairs, self.error, stream)
-        nat.append(sb.k, sb.v, sb.slots, self.k_cache, self.v_cache, self.error, stream)
+            self._copy(sb.pairs, stream)
+        self._write(sb.k, sb.v, sb.slots, stream)
+        if self.cache is not None:
+            return nat.attn_decode_int4(sb.q, self.cache, sb.tables, sb.ctx, scale, sb.out, sb.workspace, num_ctas, stream)
         nat.attn_decode(sb.q, self.k_cache, self.v_cache, sb.tables, sb.ctx, scale, sb.out,
                         sb.workspace, num_ctas, stream)
         return sb.out
 
     def cascade_for(self, sb: StepBuffers, min_saved_bytes: int = CASCADE_MIN_SAVED_BYTES):
         """A cascade plan for the step's batch when its shared prefixes save
-        enough reads to pay for the extra launches, else None."""
-        if self.block_tokens != nat.BLOCK_TOKENS:
+        enough reads to pay for the extra launches, else None (as for a 4-bit
+        cache, whose shared pages are read by each sequence)."""
+        if self.cache is not None or self.block_tokens != nat.BLOCK_TOKENS:
             return None
         groups = shared_prefix_groups(sb.tables.cpu().numpy(), sb.ctx.cpu().numpy())
         if not groups or cascade_saved_bytes(groups, self.num_kv_heads, head_dim=self.head_dim) < min_saved_bytes:
@@ -409,6 +511,8 @@ class PagedKVEngine:
     def run_step_cascade(self, sb: StepBuffers, scale: float, cascade, stream=None) -> torch.Tensor:
         """run_step with the attention through a cascade plan (copy-on-write
         copies and the append first, as in run_step)."""
+        if self.cache is not None:
+            raise ValueError("cascade attention reads a bf16 cache")
         if sb.num_pairs:
             nat.block_copy(self.k_cache, self.v_cache, sb.pairs, self.error, stream)
         nat.append(sb.k, sb.v, sb.slots, self.k_cache, self.v_cache, self.error, stream)
@@ -432,8 +536,8 @@ class HostStep:
                "block_tables": torch.int32, "context_lens": torch.int32, "src_dst_pairs": torch.int32}
 
     def __init__(self, eng: PagedKVEngine, num_seqs: int, width: int, max_pairs: int = 0):
-        if eng.block_tokens != nat.BLOCK_TOKENS:
-            raise ValueError("host-buffer steps use 16-token blocks")
+        if eng.cache is not None or eng.block_tokens != nat.BLOCK_TOKENS:
+            raise ValueError("host-buffer steps use a bf16 cache of 16-token blocks")
         self.eng, self.num_seqs, self.width, self.max_pairs = eng, num_seqs, width, max_pairs
         hq, hkv, d = eng.num_q_heads, eng.num_kv_heads, eng.head_dim
         self.layout = nat.step_layout(num_seqs, hq, hkv, d, width, max_pairs)

@@ -64,6 +64,10 @@ class GraphedDecoder:
             self._capture(b)
 
     def _launch(self, b: _Bucket):
+        if self.eng.cache is not None:
+            nat.append_int4(b.k, b.v, b.slots, self.eng.cache, self.eng.error)
+            nat.attn_decode_int4(b.q, self.eng.cache, b.tables, b.ctx, self.scale, b.out, b.ws, self.num_ctas)
+            return
         nat.decode_step(b.q, b.k, b.v, b.slots, b.no_pairs, self.eng.k_cache, self.eng.v_cache, b.tables, b.ctx,
                         self.scale, b.out, b.ws, self.eng.error, self.num_ctas)
 
@@ -109,7 +113,7 @@ class GraphedDecoder:
         b.staged.record()
         if pairs:
             pt = torch.tensor(pairs, dtype=torch.int32).to(self.eng.device, non_blocking=True)
-            nat.block_copy(self.eng.k_cache, self.eng.v_cache, pt, self.eng.error)
+            self.eng._copy(pt)
         b.graph.replay()
         return b.out[:n], slots, pairs
 
