@@ -52,88 +52,102 @@ struct Params {
     uint8_t* finished_out;
     int32_t* lengths_out;
     int32_t* history_out;
-    float2* stats;  // [rows][chunks]: maximum, sum of exponentials
+    float2* stats;  // [rows][chunks]: maximum, sum of exponentials from it on
     uint2* lists;   // [rows][chunks][n]: logit bits, token (or -1)
     uint32_t* err;
     int eos, beams, n, vocab, max_length, chunks;
 };
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 // A beam that is read: neither finished nor without a score.
 __device__ __forceinline__ bool row_done(const Params& p, int row) { return p.finished && p.finished[row] != 0; }
 __device__ __forceinline__ bool row_live(const Params& p, int row) { return !row_done(p, row) && p.scores[row] > -INFINITY; }
 
-// ---- selection shared by both kernels -----------------------------------------
-
-template <class Key>
-__device__ __forceinline__ bool before(Key ka, int ia, Key kb, int ib) {
-    return ka > kb || (ka == kb && ia < ib);
+// Numbers that compare as unsigned integers as the keys do as floats.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
+__device__ __forceinline__ uint64_t ordered(double x) {
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x));
+    return u >> 63 ? ~u : u | (uint64_t(1) << 63);
+}
+__device__ __forceinline__ double unordered(uint64_t u) {
+    return __longlong_as_double(static_cast<long long>(u >> 63 ? u & ~(uint64_t(1) << 63) : ~u));
 }
 
-template <class Key>
+// ---- selection shared by both kernels -----------------------------------------
+
+// A candidate: its key in order, and its index; of equal keys the lower index
+// comes first.
+struct Candidate {
+    uint64_t key;
+    int at;
+    int pad;
+};
+
+__device__ __forceinline__ bool before(uint64_t ka, int ia, uint64_t kb, int ib) { return ka > kb || (ka == kb && ia < ib); }
+
 struct Selection {
-    Key key[kList];
-    int at[kList];
-    Key warp_key[kWarps];
-    int warp_at[kWarps];
+    Candidate list[kList];
+    uint32_t warp_key[kWarps];
+    Candidate warp_best[kWarps];
     int count;
 };
 
 // The least, over the warps, of each warp's ceil(n / 8)-th largest thread key:
 // at least n keys of the block reach it (or all that are above -inf).
-template <class Key>
-__device__ __forceinline__ Key threshold(Selection<Key>& sel, Key best, int n) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Key mine = best, top = -INFINITY;
+__device__ __forceinline__ float threshold(Selection& sel, float best, int n) {
+    uint32_t mine = ordered(best), top = 0;
     for (int i = 0; i < (n + kWarps - 1) / kWarps; ++i) {
-        top = mine;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = __reduce_max_sync(0xffffffffu, mine);
         const unsigned holders = __ballot_sync(0xffffffffu, mine == top);
-        if (lane == __ffs(holders) - 1) mine = -INFINITY;
+        if ((threadIdx.x & 31) == __ffs(holders) - 1) mine = 0;
     }
     if (threadIdx.x == 0) sel.count = 0;
-    if (lane == 0) sel.warp_key[warp] = top;
+    if ((threadIdx.x & 31) == 0) sel.warp_key[threadIdx.x >> 5] = max(top, ordered(-INFINITY));
     __syncthreads();
-    Key t = sel.warp_key[0];
+    uint32_t t = sel.warp_key[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) t = min(t, sel.warp_key[w]);
-    return t;
+    return unordered(t);
 }
 
-template <class Key>
-__device__ __forceinline__ void offer(Selection<Key>& sel, Key key, int at) {
+__device__ __forceinline__ void offer(Selection& sel, uint64_t key, int at) {
     const int i = atomicAdd(&sel.count, 1);
-    if (i < kList) {
-        sel.key[i] = key;
-        sel.at[i] = at;
-    }
+    if (i < kList) *reinterpret_cast<uint4*>(&sel.list[i]) = make_uint4(static_cast<uint32_t>(key), static_cast<uint32_t>(key >> 32), at, 0);
 }
 
 // Writes the n first of the list in order to put(rank, key, at), the missing
-// ones as (-inf, -1); where the list overflowed, finds them by n rounds over
-// items 0 .. items - 1, item(i, key, at) being false for no candidate.
-template <class Key, class Item, class Put>
-__device__ __forceinline__ void finish(Selection<Key>& sel, int n, int items, Item item, Put put) {
+// ones as (0, -1); where the list overflowed, finds them by n rounds over items
+// 0 .. items - 1, item(i, key, at) being false for no candidate.
+template <class Item, class Put>
+__device__ __forceinline__ void finish(Selection& sel, int n, int items, Item item, Put put) {
     __syncthreads();
     const int count = sel.count;
     if (count <= kList) {
         for (int i = threadIdx.x; i < count; i += kThreads) {
-            const Key k = sel.key[i];
-            const int at = sel.at[i];
+            const Candidate c = sel.list[i];
             int rank = 0;
-            for (int j = 0; j < count; ++j) rank += before(sel.key[j], sel.at[j], k, at);
-            if (rank < n) put(rank, k, at);
+#pragma unroll 4
+            for (int j = 0; j < count; ++j) {
+                const uint4 u = *reinterpret_cast<const uint4*>(&sel.list[j]);
+                rank += before(static_cast<uint64_t>(u.y) << 32 | u.x, static_cast<int>(u.z), c.key, c.at);
+            }
+            if (rank < n) put(rank, c.key, c.at);
         }
-        for (int i = count + threadIdx.x; i < n; i += kThreads) put(i, Key(-INFINITY), -1);
+        for (int i = count + threadIdx.x; i < n; i += kThreads) put(i, uint64_t(0), -1);
         return;
     }
-    Key last = INFINITY;
+    uint64_t last = ~uint64_t(0);
     int last_at = -1;
     for (int j = 0; j < n; ++j) {
-        Key best = -INFINITY;
+        uint64_t best = 0;
         int best_at = INT_MAX;
         for (int i = threadIdx.x; i < items; i += kThreads) {
-            Key k;
+            uint64_t k;
             int at;
             if (item(i, k, at) && before(last, last_at, k, at) && before(k, at, best, best_at)) {
                 best = k;
@@ -142,7 +156,7 @@ __device__ __forceinline__ void finish(Selection<Key>& sel, int n, int items, It
         }
 #pragma unroll
         for (int d = 16; d; d >>= 1) {
-            const Key k = __shfl_xor_sync(0xffffffffu, best, d);
+            const uint64_t k = __shfl_xor_sync(0xffffffffu, best, d);
             const int at = __shfl_xor_sync(0xffffffffu, best_at, d);
             if (before(k, at, best, best_at)) {
                 best = k;
@@ -150,18 +164,15 @@ __device__ __forceinline__ void finish(Selection<Key>& sel, int n, int items, It
             }
         }
         __syncthreads();
-        if ((threadIdx.x & 31) == 0) {
-            sel.warp_key[threadIdx.x >> 5] = best;
-            sel.warp_at[threadIdx.x >> 5] = best_at;
-        }
+        if ((threadIdx.x & 31) == 0) sel.warp_best[threadIdx.x >> 5] = {best, best_at, 0};
         __syncthreads();
-        last = sel.warp_key[0];
-        last_at = sel.warp_at[0];
+        last = sel.warp_best[0].key;
+        last_at = sel.warp_best[0].at;
 #pragma unroll
         for (int w = 1; w < kWarps; ++w)
-            if (before(sel.warp_key[w], sel.warp_at[w], last, last_at)) {
-                last = sel.warp_key[w];
-                last_at = sel.warp_at[w];
+            if (before(sel.warp_best[w].key, sel.warp_best[w].at, last, last_at)) {
+                last = sel.warp_best[w].key;
+                last_at = sel.warp_best[w].at;
             }
         if (threadIdx.x == 0) put(j, last, last_at);  // kList > n candidates are there
     }
@@ -181,6 +192,16 @@ struct Vector<__nv_bfloat16> {
         u[e / 2] = e & 1 ? (u[e / 2] & 0xffffu) | v << 16 : (u[e / 2] & 0xffff0000u) | v;
     }
     __device__ __forceinline__ float get(int e) const { return e & 1 ? bf16_hi(u[e / 2]) : bf16_lo(u[e / 2]); }
+    // the largest value (NaN passed over), pairs at a time
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    __device__ __forceinline__ float largest() const {
+        const uint32_t m = max2(max2(u[0], u[1]), max2(u[2], u[3]));
+        return fmaxf(bf16_lo(m), bf16_hi(m));
+    }
 };
 template <>
 struct Vector<float> {
@@ -189,6 +210,7 @@ struct Vector<float> {
     __device__ __forceinline__ void fill() { u[0] = u[1] = u[2] = u[3] = 0xff800000u; }
     __device__ __forceinline__ void set(int e, float x) { u[e] = __float_as_uint(x); }
     __device__ __forceinline__ float get(int e) const { return __uint_as_float(u[e]); }
+    __device__ __forceinline__ float largest() const { return fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3))); }
 };
 
 // kN logits from token `at` on, -inf behind the row's end. Which logits a thread
@@ -225,12 +247,11 @@ __device__ __forceinline__ Vector<T> load(const T* row, int at, int vocab, unsig
 
 // CTA (row, chunk).
 template <class T, int kVectors>
-__global__ void __launch_bounds__(kThreads) scan_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
     constexpr int kN = Vector<T>::kN;
-    griddep_launch_dependents();
     const int row = blockIdx.x / p.chunks, chunk = blockIdx.x - row * p.chunks;
     if (!row_live(p, row)) return;
-    __shared__ Selection<float> sel;
+    __shared__ Selection sel;
     __shared__ float warp_max[kWarps], warp_sum[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const T* logits = static_cast<const T*>(p.logits) + row * p.row_stride;
@@ -241,46 +262,60 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const Params p) {
     for (int i = 0; i < kVectors; ++i) v[i] = load(logits, first + i * kThreads * kN, p.vocab, shift);
     float best = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kVectors; ++i)
-#pragma unroll
-        for (int e = 0; e < kN; ++e) best = fmaxf(best, v[i].get(e));
-    float top = best;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (lane == 0) warp_max[warp] = top;
+    for (int i = 0; i < kVectors; ++i) best = fmaxf(best, v[i].largest());
+    const uint32_t warp_top = __reduce_max_sync(0xffffffffu, ordered(best));
+    if (lane == 0) warp_max[warp] = unordered(warp_top);
     const float cut = threshold(sel, best, p.n);  // behind its barrier the warps' maxima are there
+    float top = warp_max[0];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, warp_max[w]);
-    const float from = top > -INFINITY ? top : 0.f;
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, warp_max[w]);
+    // sum 2^(x log2(e) - from): its only error beside the sum's is that of the
+    // fp32 constant, by which the join divides again. A NaN makes the row's sum
+    // NaN, and then none of its scores is a number.
+    const int lo = chunk * kVectors * kThreads * kN, hi = min(lo + kVectors * kThreads * kN, p.vocab);
+    const float from = top > -INFINITY ? top * kLog2e : 0.f;
     float sum = 0.f;
+    if (fabsf(from) < INFINITY || fabsf(top) == INFINITY) {
 #pragma unroll
-    for (int i = 0; i < kVectors; ++i)
+        for (int i = 0; i < kVectors; ++i)
 #pragma unroll
-        for (int e = 0; e < kN; ++e) sum += ex2((v[i].get(e) - from) * 1.4426950408889634f);
-    // a NaN makes the row's sum NaN, and then none of its scores is a number
+            for (int e = 0; e < kN; ++e) sum += ex2(fmaf(v[i].get(e), kLog2e, -from));
+    } else {  // logits of more than 2e38
+        for (int i = lo + threadIdx.x; i < hi; i += kThreads) sum += ex2((static_cast<float>(logits[i]) - top) * kLog2e);
+    }
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane == 0) warp_sum[warp] = sum;
     if (best >= cut && best > -INFINITY) {
+        // the thread's logits that reach the cut, as bits, and then one by one
+        uint64_t hits = 0;
 #pragma unroll
         for (int i = 0; i < kVectors; ++i)
 #pragma unroll
-            for (int e = 0; e < kN; ++e) {
-                const float x = v[i].get(e);
-                if (x >= cut && x > -INFINITY) offer(sel, x, first + i * kThreads * kN + e);
-            }
+            for (int e = 0; e < kN; ++e)
+                if (v[i].get(e) >= cut) hits |= uint64_t(1) << (i * kN + e);
+        while (hits) {
+            const int bit = __ffsll(static_cast<long long>(hits)) - 1;
+            hits &= hits - 1;
+            const int at = first + bit / kN * kThreads * kN + bit % kN;
+            const float x = at < p.vocab ? static_cast<float>(logits[at]) : -INFINITY;
+            if (x > -INFINITY) offer(sel, ordered(x), at);
+        }
     }
+    griddep_launch_dependents();  // the join's CTAs need not take room before
     const size_t out = static_cast<size_t>(row) * p.chunks + chunk;
     uint2* list = p.lists + out * p.n;
-    const int lo = chunk * kVectors * kThreads * kN, hi = min(lo + kVectors * kThreads * kN, p.vocab);
     finish(
         sel, p.n, hi - lo,
-        [&](int i, float& k, int& at) {
+        [&](int i, uint64_t& k, int& at) {
             at = lo + i;
-            k = static_cast<float>(logits[at]);
-            return k > -INFINITY;
+            const float x = static_cast<float>(logits[at]);
+            k = ordered(x);
+            return x > -INFINITY;
         },
-        [&](int rank, float k, int at) { list[rank] = make_uint2(__float_as_uint(k), static_cast<uint32_t>(at)); });
+        [&](int rank, uint64_t k, int at) {
+            list[rank] = make_uint2(__float_as_uint(unordered(static_cast<uint32_t>(k))), static_cast<uint32_t>(at));
+        });
     if (threadIdx.x == 0) {
         float all = 0.f;
 #pragma unroll
@@ -292,64 +327,103 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const Params p) {
 // ---- join -----------------------------------------------------------------------
 
 // CTA (group, share): every share of a group finds its best n candidates, and
-// writes the results of every gridDim.y-th.
+// writes the results of every gridDim.y-th. Candidates are sifted by scores in
+// fp32, with room for their rounding, and ranked by scores in 64 bits.
 __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
-    __shared__ Selection<double> sel;
+    __shared__ Selection sel;
     __shared__ double lse[kMaxBeams];
-    __shared__ double won_key[kMaxCandidates];
+    __shared__ float size[kMaxBeams];
+    __shared__ uint64_t won_key[kMaxCandidates];
     __shared__ int won_at[kMaxCandidates];
     const int group = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row0 = group * p.beams;
     griddep_wait();
     for (int k = warp; k < p.beams; k += kWarps) {
         const int row = row0 + k;
-        if (!row_live(p, row)) continue;
+        if (!row_live(p, row)) {
+            if (lane == 0) size[k] = fabsf(p.scores[row]) < INFINITY ? fabsf(p.scores[row]) : 0.f;
+            continue;
+        }
         const float2* stats = p.stats + static_cast<size_t>(row) * p.chunks;
         float top = -INFINITY;
         for (int i = lane; i < p.chunks; i += 32) top = fmaxf(top, stats[i].x);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = unordered(__reduce_max_sync(0xffffffffu, ordered(top)));
+        // a chunk's sum counts from its largest logit, times the scan's fp32 log2(e)
+        auto from = [](float x) {
+            const float f = x * kLog2e;
+            return fabsf(f) < INFINITY ? static_cast<double>(f) : static_cast<double>(x) * static_cast<double>(kLog2e);
+        };
         double sum = 0.;
         for (int i = lane; i < p.chunks; i += 32)
-            sum += static_cast<double>(stats[i].y) * exp(static_cast<double>(stats[i].x) - static_cast<double>(top));
+            sum += static_cast<double>(stats[i].y) * static_cast<double>(exp2f(static_cast<float>(from(stats[i].x) - from(top))));
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0) lse[k] = static_cast<double>(top) + log(sum);
+        if (lane == 0) {
+            lse[k] = (from(top) + log2(sum)) / static_cast<double>(kLog2e);
+            size[k] = fabsf(p.scores[row]) + fabsf(static_cast<float>(lse[k]));
+        }
     }
     __syncthreads();
     // candidate i: entry i % (chunks * n) of beam i / (chunks * n)
     const int per_row = p.chunks * p.n, items = p.beams * per_row;
-    auto item = [&](int i, double& key, int& at) {
-        const int k = i / per_row, j = i - k * per_row, row = row0 + k;
-        const float s = p.scores[row];
+    // its beam, logit and index; false for none
+    auto entry = [&](int i, int& k, float& x, int& at) {
+        k = i / per_row;
+        const int j = i - k * per_row, row = row0 + k;
+        if (!(p.scores[row] > -INFINITY)) return false;
         if (row_done(p, row)) {
-            key = s;
             at = k * p.vocab + p.eos;
-            return j == 0 && s > -INFINITY;
+            x = 0.f;
+            return j == 0;
         }
-        if (!(s > -INFINITY)) return false;
         const uint2 c = p.lists[static_cast<size_t>(row) * per_row + j];
-        key = static_cast<double>(s) + (static_cast<double>(__uint_as_float(c.x)) - lse[k]);
+        x = __uint_as_float(c.x);
         at = k * p.vocab + static_cast<int>(c.y);
-        return static_cast<int>(c.y) >= 0 && key > -INFINITY;  // (false for NaN)
+        return static_cast<int>(c.y) >= 0;
     };
-    double best = -INFINITY;
+    auto rough = [&](int k, float x) {
+        const float s = p.scores[row0 + k];
+        return row_done(p, row0 + k) ? s : s + (x - static_cast<float>(lse[k]));
+    };
+    auto exact = [&](int k, float x) {
+        const double s = static_cast<double>(p.scores[row0 + k]);
+        return row_done(p, row0 + k) ? s : s + (static_cast<double>(x) - lse[k]);
+    };
+    float best = -INFINITY;
     for (int i = threadIdx.x; i < items; i += kThreads) {
-        double key;
-        int at;
-        if (item(i, key, at)) best = max(best, key);
+        int k, at;
+        float x;
+        if (entry(i, k, x, at)) best = fmaxf(best, rough(k, x));  // passes over NaN
     }
-    const double cut = threshold(sel, best, p.n);
-    if (best >= cut && best > -INFINITY)
-        for (int i = threadIdx.x; i < items; i += kThreads) {
-            double key;
-            int at;
-            if (item(i, key, at) && key >= cut) offer(sel, key, at);
-        }
-    finish(sel, p.n, items, item, [&](int rank, double key, int at) {
-        won_key[rank] = key;
-        won_at[rank] = at;
-    });
+    float cut = threshold(sel, best, p.n);
+    // Rounded sums are off by less than 2^-22 of their terms: those of a score at
+    // the cut are the beam's score, its logarithm of the sum, and the cut less
+    // these.
+    float terms = 0.f;
+    for (int k = 0; k < p.beams; ++k) terms = fmaxf(terms, size[k] < INFINITY ? size[k] : 0.f);
+    cut -= 0x1p-21f * (2.f * terms + fabsf(cut));
+    if (!(cut > -INFINITY)) cut = -INFINITY;
+    for (int i = threadIdx.x; i < items; i += kThreads) {
+        int k, at;
+        float x;
+        if (!entry(i, k, x, at) || !(rough(k, x) >= cut)) continue;
+        const double key = exact(k, x);
+        if (key > -INFINITY) offer(sel, ordered(key), at);
+    }
+    finish(
+        sel, p.n, items,
+        [&](int i, uint64_t& key, int& at) {
+            int k;
+            float x;
+            if (!entry(i, k, x, at)) return false;
+            const double score = exact(k, x);
+            key = ordered(score);
+            return score > -INFINITY;  // (false for NaN)
+        },
+        [&](int rank, uint64_t key, int at) {
+            won_key[rank] = key;
+            won_at[rank] = at;
+        });
     __syncthreads();
     for (int j = blockIdx.y; j < p.n; j += gridDim.y) {
         const int at = won_at[j];
@@ -367,7 +441,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
         }
         const bool grows = some && !done && length < p.max_length;
         if (threadIdx.x == 0) {
-            p.scores_out[out] = static_cast<float>(won_key[j]);
+            p.scores_out[out] = some ? static_cast<float>(unordered(won_key[j])) : -INFINITY;
             p.tokens_out[out] = token;
             p.parents_out[out] = k;
             p.finished_out[out] = done || (some && token == p.eos);
