@@ -478,7 +478,8 @@ pkv_status pkv_attn_decode_int4(const void* q, const void* cache, const int32_t*
  *   workspace    : device scratch of pkv_beam_workspace_size bytes for the same
  *                  four sizes, 256-byte aligned; it holds nothing between calls.
  *                  Calls that share one must not overlap on the GPU
- * Scores are formed and compared in 64 bits from sums of exponentials in 32.
+ * Scores are formed and compared in twice fp32's precision, from sums of
+ * exponentials in fp32.
  * Limits: num_beams <= 32, num_candidates <= 64 (PKV_EUNSUPPORTED), num_beams *
  * vocab < 2^31 (PKV_ERANGE).
  */

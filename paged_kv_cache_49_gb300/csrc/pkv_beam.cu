@@ -13,9 +13,9 @@
 // least n logits of the chunk reach the least of these 8, and hardly more do, so
 // those that reach it go into a list whose entries are ranked by comparing them
 // all. (A list that overflows, as of equal logits, is replaced by n rounds over
-// the chunk.) The join does the same with the chunks' candidates of a group,
-// whose scores it forms in 64 bits: neighbours of the last one taken may differ
-// by less than fp32 holds. The exponentials bound the scan from the other side:
+// the chunk.) The join merges the chunks' lists of a group by scores of twice
+// fp32's precision: neighbours of the last one taken may differ by less than
+// fp32 holds. The exponentials bound the scan from the other side:
 // at 16 a cycle and SM they take two thirds of the time of reading bf16 logits.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -52,7 +52,7 @@ struct Params {
     uint8_t* finished_out;
     int32_t* lengths_out;
     int32_t* history_out;
-    float2* stats;  // [rows][chunks]: maximum, sum of exponentials from it on
+    float2* stats;  // [rows][chunks][kWarps]: maximum, sum of exponentials from it on
     uint2* lists;   // [rows][chunks][n]: logit bits, token (or -1)
     uint32_t* err;
     int eos, beams, n, vocab, max_length, chunks;
@@ -64,21 +64,32 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ bool row_done(const Params& p, int row) { return p.finished && p.finished[row] != 0; }
 __device__ __forceinline__ bool row_live(const Params& p, int row) { return !row_done(p, row) && p.scores[row] > -INFINITY; }
 
-// Numbers that compare as unsigned integers as the keys do as floats.
+// Numbers that compare as unsigned integers as the keys do as floats (-0 as 0).
 __device__ __forceinline__ uint32_t ordered(float x) {
-    const uint32_t u = __float_as_uint(x);
+    const uint32_t u = __float_as_uint(__fadd_rn(x, 0.f));
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
-__device__ __forceinline__ uint64_t ordered(double x) {
-    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x));
-    return u >> 63 ? ~u : u | (uint64_t(1) << 63);
+// A number as the sum of two, the second below half a step of the first: 48 bits
+// or more from fp32 operations (64-bit ones run at 1/64 of their rate here).
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ double unordered(uint64_t u) {
-    return __longlong_as_double(static_cast<long long>(u >> 63 ? u & ~(uint64_t(1) << 63) : ~u));
+__device__ __forceinline__ Pair add(Pair a, float b) {
+    const Pair s = two_sum(a.hi, b);
+    return two_sum(s.hi, __fadd_rn(s.lo, a.lo));
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) { return add(add(a, b.hi), b.lo); }
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+    const float p = __fmul_rn(a.hi, b.hi);
+    return two_sum(p, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -p))));
 }
 
-// ---- selection shared by both kernels -----------------------------------------
+// ---- selection from a chunk ------------------------------------------------------
 
 // A candidate: its key in order, and its index; of equal keys the lower index
 // comes first.
@@ -216,8 +227,8 @@ struct Vector<float> {
 // kN logits from token `at` on, -inf behind the row's end. Which logits a thread
 // sums is a matter of their tokens alone, so rows that are alike have the same
 // sums wherever they lie: a row that does not begin on a 16-byte boundary is read
-// as neighbouring aligned vectors, shifted; its first and last logits, whose
-// vectors reach beyond the row, one by one.
+// in words (for bf16 rows on odd places, shifted by half a word); logits whose
+// words reach beyond the row are read one by one.
 template <class T>
 __device__ __forceinline__ Vector<T> load(const T* row, int at, int vocab, unsigned shift) {
     constexpr int kN = Vector<T>::kN;
@@ -225,17 +236,16 @@ __device__ __forceinline__ Vector<T> load(const T* row, int at, int vocab, unsig
     if (shift == 0 && at + kN <= vocab) {
         const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + at));
         v.u[0] = u.x, v.u[1] = u.y, v.u[2] = u.z, v.u[3] = u.w;
-    } else if (shift != 0 && at >= kN && at + 2 * kN <= vocab) {
-        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(row + at) - shift);
-        const uint4 a = __ldg(src), b = __ldg(src + 1);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        const unsigned bits = shift % 4 * 8;
+    } else if (shift != 0 && shift % 4 == 0 && at + kN <= vocab) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = shift < 4 ? w[i] : shift < 8 ? w[i + 1] : shift < 12 ? w[i + 2] : w[i + 3];
-            const uint32_t hi = shift < 4 ? w[i + 1] : shift < 8 ? w[i + 2] : shift < 12 ? w[i + 3] : w[i + 4];
-            v.u[i] = __funnelshift_r(lo, hi, bits);
-        }
+        for (int i = 0; i < 4; ++i) v.u[i] = __ldg(reinterpret_cast<const uint32_t*>(row + at) + i);
+    } else if (shift % 4 != 0 && at >= kN && at + kN < vocab) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(row + at - 1);
+        uint32_t w[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = __ldg(src + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.u[i] = __funnelshift_r(w[i], w[i + 1], 16);
     } else {
         v.fill();
 #pragma unroll
@@ -252,7 +262,6 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
     const int row = blockIdx.x / p.chunks, chunk = blockIdx.x - row * p.chunks;
     if (!row_live(p, row)) return;
     __shared__ Selection sel;
-    __shared__ float warp_max[kWarps], warp_sum[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const T* logits = static_cast<const T*>(p.logits) + row * p.row_stride;
     const unsigned shift = static_cast<unsigned>(reinterpret_cast<uintptr_t>(logits) & 15u);
@@ -263,47 +272,53 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
     float best = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) best = fmaxf(best, v[i].largest());
-    const uint32_t warp_top = __reduce_max_sync(0xffffffffu, ordered(best));
-    if (lane == 0) warp_max[warp] = unordered(warp_top);
-    const float cut = threshold(sel, best, p.n);  // behind its barrier the warps' maxima are there
-    float top = warp_max[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, warp_max[w]);
-    // sum 2^(x log2(e) - from): its only error beside the sum's is that of the
+    // Each warp sums from its own largest logit on, with no barrier before it:
+    // sum 2^(x log2(e) - from), whose only error beside the sum's is that of the
     // fp32 constant, by which the join divides again. A NaN makes the row's sum
     // NaN, and then none of its scores is a number.
     const int lo = chunk * kVectors * kThreads * kN, hi = min(lo + kVectors * kThreads * kN, p.vocab);
+    const float top = unordered(__reduce_max_sync(0xffffffffu, ordered(best)));
     const float from = top > -INFINITY ? top * kLog2e : 0.f;
     float sum = 0.f;
     if (fabsf(from) < INFINITY || fabsf(top) == INFINITY) {
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kVectors; ++i)
 #pragma unroll
-            for (int e = 0; e < kN; ++e) sum += ex2(fmaf(v[i].get(e), kLog2e, -from));
+            for (int e = 0; e < kN; ++e) part[e % 4] += ex2(fmaf(v[i].get(e), kLog2e, -from));
+        sum = (part[0] + part[1]) + (part[2] + part[3]);
     } else {  // logits of more than 2e38
-        for (int i = lo + threadIdx.x; i < hi; i += kThreads) sum += ex2((static_cast<float>(logits[i]) - top) * kLog2e);
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i)
+#pragma unroll 1
+            for (int e = 0; e < kN; ++e) {
+                const int at = first + i * kThreads * kN + e;
+                if (at < p.vocab) sum += ex2((static_cast<float>(logits[at]) - top) * kLog2e);
+            }
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) warp_sum[warp] = sum;
+    const size_t out = static_cast<size_t>(row) * p.chunks + chunk;
+    if (lane == 0) p.stats[out * kWarps + warp] = make_float2(top, sum);
+    const float cut = threshold(sel, best, p.n);
     if (best >= cut && best > -INFINITY) {
-        // the thread's logits that reach the cut, as bits, and then one by one
-        uint64_t hits = 0;
 #pragma unroll
-        for (int i = 0; i < kVectors; ++i)
+        for (int i = 0; i < kVectors; ++i) {
+            if (!(v[i].largest() >= cut)) continue;
+            // the vector's logits that reach the cut, as bits, and then one by one
+            unsigned hits = 0;
 #pragma unroll
             for (int e = 0; e < kN; ++e)
-                if (v[i].get(e) >= cut) hits |= uint64_t(1) << (i * kN + e);
-        while (hits) {
-            const int bit = __ffsll(static_cast<long long>(hits)) - 1;
-            hits &= hits - 1;
-            const int at = first + bit / kN * kThreads * kN + bit % kN;
-            const float x = at < p.vocab ? static_cast<float>(logits[at]) : -INFINITY;
-            if (x > -INFINITY) offer(sel, ordered(x), at);
+                if (v[i].get(e) >= cut) hits |= 1u << e;
+#pragma unroll 1
+            for (; hits; hits &= hits - 1) {
+                const int at = first + i * kThreads * kN + __ffs(static_cast<int>(hits)) - 1;
+                const float x = at < p.vocab ? static_cast<float>(logits[at]) : -INFINITY;
+                if (x > -INFINITY) offer(sel, ordered(x), at);
+            }
         }
     }
     griddep_launch_dependents();  // the join's CTAs need not take room before
-    const size_t out = static_cast<size_t>(row) * p.chunks + chunk;
     uint2* list = p.lists + out * p.n;
     finish(
         sel, p.n, hi - lo,
@@ -316,141 +331,173 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
         [&](int rank, uint64_t k, int at) {
             list[rank] = make_uint2(__float_as_uint(unordered(static_cast<uint32_t>(k))), static_cast<uint32_t>(at));
         });
-    if (threadIdx.x == 0) {
-        float all = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) all += warp_sum[w];
-        p.stats[out] = make_float2(top, all);
-    }
 }
 
 // ---- join -----------------------------------------------------------------------
 
 // CTA (group, share): every share of a group finds its best n candidates, and
-// writes the results of every gridDim.y-th. Candidates are sifted by scores in
-// fp32, with room for their rounding, and ranked by scores in 64 bits.
+// writes the results of every gridDim.y-th. The chunks' lists are in order, so
+// the candidates are merged: in each of n rounds the best of the lists' first
+// remaining entries is taken. (A cut as in the scan's does not bound the list:
+// where one beam leads, the best n are in a few chunks, and the other chunks'
+// first entries say nothing about them.)
 __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
-    __shared__ Selection sel;
-    __shared__ double lse[kMaxBeams];
-    __shared__ float size[kMaxBeams];
-    __shared__ uint64_t won_key[kMaxCandidates];
+    // In quarters, so that no sum of finite ones overflows: the beams' scores and
+    // the logarithms of their sums.
+    __shared__ float score[kMaxBeams];
+    __shared__ Pair lse[kMaxBeams];
+    __shared__ bool done[kMaxBeams];
+    __shared__ uint4 warp_best[2][kWarps];
+    __shared__ float won_score[kMaxCandidates];
     __shared__ int won_at[kMaxCandidates];
     const int group = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row0 = group * p.beams;
     griddep_wait();
     for (int k = warp; k < p.beams; k += kWarps) {
-        const int row = row0 + k;
-        if (!row_live(p, row)) {
-            if (lane == 0) size[k] = fabsf(p.scores[row]) < INFINITY ? fabsf(p.scores[row]) : 0.f;
-            continue;
+        const int row = row0 + k, parts = p.chunks * kWarps;
+        const bool live = row_live(p, row);
+        if (lane == 0) {
+            score[k] = 0.25f * p.scores[row];
+            done[k] = row_done(p, row);
         }
-        const float2* stats = p.stats + static_cast<size_t>(row) * p.chunks;
+        if (!live) continue;
+        const float2* stats = p.stats + static_cast<size_t>(row) * parts;
         float top = -INFINITY;
-        for (int i = lane; i < p.chunks; i += 32) top = fmaxf(top, stats[i].x);
+#pragma unroll 4
+        for (int i = lane; i < parts; i += 32) top = fmaxf(top, stats[i].x);
         top = unordered(__reduce_max_sync(0xffffffffu, ordered(top)));
-        // a chunk's sum counts from its largest logit, times the scan's fp32 log2(e)
-        auto from = [](float x) {
-            const float f = x * kLog2e;
-            return fabsf(f) < INFINITY ? static_cast<double>(f) : static_cast<double>(x) * static_cast<double>(kLog2e);
-        };
-        double sum = 0.;
-        for (int i = lane; i < p.chunks; i += 32)
-            sum += static_cast<double>(stats[i].y) * static_cast<double>(exp2f(static_cast<float>(from(stats[i].x) - from(top))));
+        // a part's sum counts from its largest logit, times the scan's fp32 log2(e)
+        const bool large = fabsf(top * kLog2e) == INFINITY;
+        float sum = 0.f;
+#pragma unroll 4
+        for (int i = lane; i < parts; i += 32) {
+            const float2 s = stats[i];
+            sum += s.y * exp2f(large ? (s.x - top) * kLog2e : __fmul_rn(s.x, kLog2e) - __fmul_rn(top, kLog2e));
+        }
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (lane == 0) {
-            lse[k] = (from(top) + log2(sum)) / static_cast<double>(kLog2e);
-            size[k] = fabsf(p.scores[row]) + fabsf(static_cast<float>(lse[k]));
+            // log2 of the sum by its exponent and the rest, then by 1 / kLog2e
+            const int e = ilogbf(sum);
+            const float rest = log2f(ldexpf(sum, -e));
+            const Pair by = {0x1.62e43p-1f, 0x1.f8ff94p-28f};
+            Pair l;
+            if (large) l = two_sum(top, 0.f);
+            else l = mul(add(two_sum(__fmul_rn(top, kLog2e), static_cast<float>(e)), rest), by);
+            if (!(sum < INFINITY) || !(fabsf(top) < INFINITY)) l.hi = l.lo = NAN;
+            lse[k] = {0.25f * l.hi, 0.25f * l.lo};
         }
     }
     __syncthreads();
-    // candidate i: entry i % (chunks * n) of beam i / (chunks * n)
-    const int per_row = p.chunks * p.n, items = p.beams * per_row;
-    // its beam, logit and index; false for none
-    auto entry = [&](int i, int& k, float& x, int& at) {
-        k = i / per_row;
-        const int j = i - k * per_row, row = row0 + k;
-        if (!(p.scores[row] > -INFINITY)) return false;
-        if (row_done(p, row)) {
-            at = k * p.vocab + p.eos;
-            x = 0.f;
-            return j == 0;
-        }
-        const uint2 c = p.lists[static_cast<size_t>(row) * per_row + j];
-        x = __uint_as_float(c.x);
+    // Entry j of list i (a chunk of a beam): its key, 0 for none, and index. A
+    // finished beam has one entry in all, whose score is the beam's.
+    const int lists = p.beams * p.chunks;
+    auto raw = [&](int i, int k, int j) {
+        if (!(score[k] > -INFINITY) || j >= p.n) return make_uint2(0u, 0xffffffffu);
+        if (done[k]) return make_uint2(0u, i == k * p.chunks && j == 0 ? static_cast<uint32_t>(p.eos) : 0xffffffffu);
+        return p.lists[(static_cast<size_t>(row0) * p.chunks + i) * p.n + j];
+    };
+    auto key_of = [&](int k, uint2 c, int& at) {
         at = k * p.vocab + static_cast<int>(c.y);
-        return static_cast<int>(c.y) >= 0;
+        if (static_cast<int>(c.y) < 0) return uint64_t(0);
+        const Pair l = lse[k];
+        const Pair s = done[k] ? Pair{score[k], 0.f}
+                               : add(add(two_sum(0.25f * __uint_as_float(c.x), -l.hi), -l.lo), score[k]);
+        if (!(s.hi > -INFINITY && s.hi < INFINITY)) return uint64_t(0);  // (none for NaN)
+        return static_cast<uint64_t>(ordered(s.hi)) << 32 | ordered(s.lo);
     };
-    auto rough = [&](int k, float x) {
-        const float s = p.scores[row0 + k];
-        return row_done(p, row0 + k) ? s : s + (x - static_cast<float>(lse[k]));
-    };
-    auto exact = [&](int k, float x) {
-        const double s = static_cast<double>(p.scores[row0 + k]);
-        return row_done(p, row0 + k) ? s : s + (static_cast<double>(x) - lse[k]);
-    };
-    float best = -INFINITY;
-    for (int i = threadIdx.x; i < items; i += kThreads) {
-        int k, at;
-        float x;
-        if (entry(i, k, x, at)) best = fmaxf(best, rough(k, x));  // passes over NaN
+    // The thread's list with its first remaining entry, and the one behind it;
+    // where it has more lists, how far each was taken is counted again from the
+    // last one taken, since its own entries are in order.
+    uint64_t key = 0, next_key = 0;
+    int at = INT_MAX, next_at = INT_MAX, taken = 0;
+    const bool single = lists <= kThreads;
+    const int list = min(static_cast<int>(threadIdx.x), lists - 1), beam = list / p.chunks;
+    if (single && list == threadIdx.x) {
+        const uint2 c0 = raw(list, beam, 0), c1 = raw(list, beam, 1);
+        key = key_of(beam, c0, at);
+        next_key = key_of(beam, c1, next_at);
     }
-    float cut = threshold(sel, best, p.n);
-    // Rounded sums are off by less than 2^-22 of their terms: those of a score at
-    // the cut are the beam's score, its logarithm of the sum, and the cut less
-    // these.
-    float terms = 0.f;
-    for (int k = 0; k < p.beams; ++k) terms = fmaxf(terms, size[k] < INFINITY ? size[k] : 0.f);
-    cut -= 0x1p-21f * (2.f * terms + fabsf(cut));
-    if (!(cut > -INFINITY)) cut = -INFINITY;
-    for (int i = threadIdx.x; i < items; i += kThreads) {
-        int k, at;
-        float x;
-        if (!entry(i, k, x, at) || !(rough(k, x) >= cut)) continue;
-        const double key = exact(k, x);
-        if (key > -INFINITY) offer(sel, ordered(key), at);
+    uint64_t last = ~uint64_t(0);
+    int last_at = -1;
+    auto search = [&] {  // the best entry of the thread's lists behind the last one taken
+        key = 0;
+        at = INT_MAX;
+        for (int i = threadIdx.x; i < lists; i += kThreads) {
+            const int k = i / p.chunks;
+            for (int j = 0; j < p.n; ++j) {
+                int a;
+                const uint64_t e = key_of(k, raw(i, k, j), a);
+                if (e == 0) break;
+                if (!before(last, last_at, e, a)) continue;
+                if (before(e, a, key, at)) {
+                    key = e;
+                    at = a;
+                }
+                break;
+            }
+        }
+    };
+    if (!single) search();
+    // the first of the warp's keys, and where it is
+    auto first_of = [](uint64_t k, int i) {
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(k >> 32));
+        const bool top = static_cast<uint32_t>(k >> 32) == hi;
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, top ? static_cast<uint32_t>(k) : 0u);
+        const int first = __reduce_min_sync(0xffffffffu, top && static_cast<uint32_t>(k) == lo ? i : INT_MAX);
+        return make_uint4(lo, hi, static_cast<uint32_t>(first), 0u);
+    };
+    for (int j = 0; j < p.n; ++j) {
+        const uint4 u = first_of(key, at);
+        if (lane == 0) warp_best[j & 1][warp] = u;
+        __syncthreads();
+        const uint4 w = warp_best[j & 1][lane % kWarps];
+        const uint4 best = first_of(static_cast<uint64_t>(w.y) << 32 | w.x, static_cast<int>(w.z));
+        last = static_cast<uint64_t>(best.y) << 32 | best.x;
+        last_at = static_cast<int>(best.z);
+        if (threadIdx.x == 0) {
+            won_score[j] = last ? 4.f * (unordered(best.y) + unordered(best.x)) : -INFINITY;
+            won_at[j] = last ? last_at : -1;
+        }
+        if (last && key == last && at == last_at) {
+            if (single) {
+                key = next_key;
+                at = next_at;
+                ++taken;
+                next_key = key_of(beam, raw(list, beam, taken + 1), next_at);
+            } else {
+                search();
+            }
+        }
     }
-    finish(
-        sel, p.n, items,
-        [&](int i, uint64_t& key, int& at) {
-            int k;
-            float x;
-            if (!entry(i, k, x, at)) return false;
-            const double score = exact(k, x);
-            key = ordered(score);
-            return score > -INFINITY;  // (false for NaN)
-        },
-        [&](int rank, uint64_t key, int at) {
-            won_key[rank] = key;
-            won_at[rank] = at;
-        });
     __syncthreads();
     for (int j = blockIdx.y; j < p.n; j += gridDim.y) {
         const int at = won_at[j];
         const bool some = at >= 0;
         const int k = some ? at / p.vocab : -1, token = some ? at - k * p.vocab : -1;
         const int row = row0 + max(k, 0);
-        const bool done = some && row_done(p, row);
+        const bool ended = some && done[k];
         const size_t out = static_cast<size_t>(group) * p.n + j;
         int length = 0;
         if (some && p.lengths) {
             const int given = p.lengths[row];
             length = min(max(given, 0), p.max_length);
-            if ((given != length || (!done && length == p.max_length)) && p.err && threadIdx.x == 0)
+            if ((given != length || (!ended && length == p.max_length)) && p.err && threadIdx.x == 0)
                 atomicOr(p.err, PKV_DEVERR_CONTEXT);
         }
-        const bool grows = some && !done && length < p.max_length;
+        const bool grows = some && !ended && length < p.max_length;
         if (threadIdx.x == 0) {
-            p.scores_out[out] = some ? static_cast<float>(unordered(won_key[j])) : -INFINITY;
+            p.scores_out[out] = won_score[j];
             p.tokens_out[out] = token;
             p.parents_out[out] = k;
-            p.finished_out[out] = done || (some && token == p.eos);
+            p.finished_out[out] = ended || (some && token == p.eos);
             if (p.lengths) p.lengths_out[out] = length + (grows ? 1 : 0);
             if (p.lengths && grows) p.history_out[out * p.max_length + length] = token;
         }
         if (p.lengths) {
             const int32_t* src = p.history + static_cast<size_t>(row) * p.max_length;
             int32_t* dst = p.history_out + out * p.max_length;
+#pragma unroll 4
             for (int i = threadIdx.x; i < length; i += kThreads) dst[i] = src[i];
         }
     }
@@ -494,7 +541,7 @@ pkv_status check(int groups, int beams, int candidates, int vocab) {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t workspace_for(long long rows, int candidates, int chunks) {
-    return align256(static_cast<size_t>(rows) * chunks * sizeof(float2)) +
+    return align256(static_cast<size_t>(rows) * chunks * kWarps * sizeof(float2)) +
            align256(static_cast<size_t>(rows) * chunks * candidates * sizeof(uint2));
 }
 
@@ -547,7 +594,7 @@ pkv_status pkv_beam_select(const void* logits, int64_t row_stride, int logits_by
     p.history_out = history_out;
     p.stats = static_cast<float2*>(workspace);
     p.lists = reinterpret_cast<uint2*>(static_cast<uint8_t*>(workspace) +
-                                       beam::align256(static_cast<size_t>(rows) * p.chunks * sizeof(float2)));
+                                       beam::align256(static_cast<size_t>(rows) * p.chunks * beam::kWarps * sizeof(float2)));
     p.err = device_error;
     p.eos = eos;
     p.beams = num_beams;

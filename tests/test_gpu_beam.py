@@ -132,6 +132,13 @@ def test_ties_go_to_the_lowest_index(pkv):
             rng = np.random.default_rng(4)
             logits = _logits(rng, 1, vocab, dtype).repeat(4, 1).contiguous()
             _check(pkv, logits, np.array([[-1.0, -1.0], [-1.0, -1.0]], np.float32), n=12)
+    # zeros of either sign are equal
+    for dtype in DTYPES:
+        logits = torch.zeros((2, 9000), dtype=dtype, device="cuda")
+        logits[:, :4000] = -0.0
+        logits[1, ::2] = -0.0
+        _check(pkv, logits, np.array([[-1.0, -1.0]], np.float32), n=20)
+        _check(pkv, logits - 3 * (torch.arange(9000, device="cuda") % 300 > 0).to(dtype), np.array([[0.0, -0.0]], np.float32), n=64)
     # logits of few values: thousands of ties with the last one taken
     coarse = torch.randint(0, 3, (6, 30_011), device="cuda").to(torch.bfloat16)
     _check(pkv, coarse, np.array([[-1.0, -1.5], [-2.0, -0.5], [0.0, 0.0]], np.float32), n=64)
