@@ -55,14 +55,17 @@ struct Params {
     float2* stats;  // [rows][chunks][kWarps]: maximum, sum of exponentials from it on
     uint2* lists;   // [rows][chunks][n]: logit bits, token (or -1)
     uint32_t* err;
-    int eos, beams, n, vocab, max_length, chunks;
+    int eos, beams, n, vocab, max_length, chunks, chunk_tokens;
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A beam that is read: neither finished nor without a score.
 __device__ __forceinline__ bool row_done(const Params& p, int row) { return p.finished && p.finished[row] != 0; }
-__device__ __forceinline__ bool row_live(const Params& p, int row) { return !row_done(p, row) && p.scores[row] > -INFINITY; }
+__device__ __forceinline__ bool row_live(const Params& p, int row) {
+    const bool done = row_done(p, row), some = p.scores[row] > -INFINITY;  // (both read at once)
+    return !done & some;
+}
 
 // Numbers that compare as unsigned integers as the keys do as floats (-0 as 0).
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -91,34 +94,33 @@ __device__ __forceinline__ Pair mul(Pair a, Pair b) {
 
 // ---- selection from a chunk ------------------------------------------------------
 
-// A candidate: its key in order, and its index; of equal keys the lower index
-// comes first.
-struct Candidate {
-    uint64_t key;
-    int at;
-    int pad;
+// Candidates as numbers: the key in order above what is left of 2^32 by the
+// index, so that of equal keys the lower index is the larger number.
+struct Selection {
+    uint64_t list[kList];
+    int at[kList];  // (of the join, whose keys take all 64 bits)
+    uint32_t warp_key[kWarps];
+    uint64_t warp_best[kWarps];
+    int warp_at[kWarps];
+    int count;
 };
 
 __device__ __forceinline__ bool before(uint64_t ka, int ia, uint64_t kb, int ib) { return ka > kb || (ka == kb && ia < ib); }
 
-struct Selection {
-    Candidate list[kList];
-    uint32_t warp_key[kWarps];
-    Candidate warp_best[kWarps];
-    int count;
-};
-
-// The least, over the warps, of each warp's ceil(n / 8)-th largest thread key:
-// at least n keys of the block reach it (or all that are above -inf).
-__device__ __forceinline__ float threshold(Selection& sel, float best, int n) {
+// The least, over the warps that have any (the first `warps`), of each warp's
+// ceil(n / warps)-th largest thread key: at least n keys of the block reach it
+// (or all that are above -inf).
+__device__ __forceinline__ float threshold(Selection& sel, float best, int n, int warps) {
+    const int warp = threadIdx.x >> 5;
     uint32_t mine = ordered(best), top = 0;
-    for (int i = 0; i < (n + kWarps - 1) / kWarps; ++i) {
-        top = __reduce_max_sync(0xffffffffu, mine);
-        const unsigned holders = __ballot_sync(0xffffffffu, mine == top);
-        if ((threadIdx.x & 31) == __ffs(holders) - 1) mine = 0;
-    }
+    if (warp < warps)
+        for (int i = 0; i < (n + warps - 1) / warps; ++i) {
+            top = __reduce_max_sync(0xffffffffu, mine);
+            const unsigned holders = __ballot_sync(0xffffffffu, mine == top);
+            if ((threadIdx.x & 31) == __ffs(holders) - 1) mine = 0;
+        }
     if (threadIdx.x == 0) sel.count = 0;
-    if ((threadIdx.x & 31) == 0) sel.warp_key[threadIdx.x >> 5] = max(top, ordered(-INFINITY));
+    if ((threadIdx.x & 31) == 0) sel.warp_key[warp] = warp < warps ? max(top, ordered(-INFINITY)) : 0xffffffffu;
     __syncthreads();
     uint32_t t = sel.warp_key[0];
 #pragma unroll
@@ -126,28 +128,27 @@ __device__ __forceinline__ float threshold(Selection& sel, float best, int n) {
     return unordered(t);
 }
 
-__device__ __forceinline__ void offer(Selection& sel, uint64_t key, int at) {
-    const int i = atomicAdd(&sel.count, 1);
-    if (i < kList) *reinterpret_cast<uint4*>(&sel.list[i]) = make_uint4(static_cast<uint32_t>(key), static_cast<uint32_t>(key >> 32), at, 0);
-}
-
 // Writes the n first of the list in order to put(rank, key, at), the missing
 // ones as (0, -1); where the list overflowed, finds them by n rounds over items
-// 0 .. items - 1, item(i, key, at) being false for no candidate.
-template <class Item, class Put>
+// 0 .. items - 1, item(i, key, at) being false for no candidate. kIndexed: the
+// keys leave no room for the index, which is in `at`.
+template <bool kIndexed, class Item, class Put>
 __device__ __forceinline__ void finish(Selection& sel, int n, int items, Item item, Put put) {
     __syncthreads();
     const int count = sel.count;
     if (count <= kList) {
-        for (int i = threadIdx.x; i < count; i += kThreads) {
-            const Candidate c = sel.list[i];
+        // four lanes a candidate
+        for (int i0 = 0; i0 < count; i0 += kThreads / 4) {
+            const int i = i0 + static_cast<int>(threadIdx.x) / 4;
+            const uint64_t key = i < count ? sel.list[i] : ~uint64_t(0);
+            const int at = kIndexed && i < count ? sel.at[i] : 0;
             int rank = 0;
 #pragma unroll 4
-            for (int j = 0; j < count; ++j) {
-                const uint4 u = *reinterpret_cast<const uint4*>(&sel.list[j]);
-                rank += before(static_cast<uint64_t>(u.y) << 32 | u.x, static_cast<int>(u.z), c.key, c.at);
-            }
-            if (rank < n) put(rank, c.key, c.at);
+            for (int j = threadIdx.x & 3; j < count; j += 4)
+                rank += kIndexed ? before(sel.list[j], sel.at[j], key, at) : sel.list[j] > key;
+            rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+            rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+            if (i < count && (threadIdx.x & 3) == 0 && rank < n) put(rank, key, at);
         }
         for (int i = count + threadIdx.x; i < n; i += kThreads) put(i, uint64_t(0), -1);
         return;
@@ -159,7 +160,7 @@ __device__ __forceinline__ void finish(Selection& sel, int n, int items, Item it
         int best_at = INT_MAX;
         for (int i = threadIdx.x; i < items; i += kThreads) {
             uint64_t k;
-            int at;
+            int at = 0;
             if (item(i, k, at) && before(last, last_at, k, at) && before(k, at, best, best_at)) {
                 best = k;
                 best_at = at;
@@ -175,17 +176,21 @@ __device__ __forceinline__ void finish(Selection& sel, int n, int items, Item it
             }
         }
         __syncthreads();
-        if ((threadIdx.x & 31) == 0) sel.warp_best[threadIdx.x >> 5] = {best, best_at, 0};
+        if ((threadIdx.x & 31) == 0) {
+            sel.warp_best[threadIdx.x >> 5] = best;
+            sel.warp_at[threadIdx.x >> 5] = best_at;
+        }
         __syncthreads();
-        last = sel.warp_best[0].key;
-        last_at = sel.warp_best[0].at;
+        last = sel.warp_best[0];
+        last_at = sel.warp_at[0];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w)
-            if (before(sel.warp_best[w].key, sel.warp_best[w].at, last, last_at)) {
-                last = sel.warp_best[w].key;
-                last_at = sel.warp_best[w].at;
+            if (before(sel.warp_best[w], sel.warp_at[w], last, last_at)) {
+                last = sel.warp_best[w];
+                last_at = sel.warp_at[w];
             }
         if (threadIdx.x == 0) put(j, last, last_at);  // kList > n candidates are there
+        if (!kIndexed) last_at = INT_MAX;  // equal keys are one candidate
     }
 }
 
@@ -203,6 +208,10 @@ struct Vector<__nv_bfloat16> {
         u[e / 2] = e & 1 ? (u[e / 2] & 0xffffu) | v << 16 : (u[e / 2] & 0xffff0000u) | v;
     }
     __device__ __forceinline__ float get(int e) const { return e & 1 ? bf16_hi(u[e / 2]) : bf16_lo(u[e / 2]); }
+    __device__ __forceinline__ float pick(int e) const {  // get(e) where e is not known in advance
+        const uint32_t w = e < 4 ? (e < 2 ? u[0] : u[1]) : (e < 6 ? u[2] : u[3]);
+        return e & 1 ? bf16_hi(w) : bf16_lo(w);
+    }
     // the largest value (NaN passed over), pairs at a time
     static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
         uint32_t d;
@@ -221,6 +230,7 @@ struct Vector<float> {
     __device__ __forceinline__ void fill() { u[0] = u[1] = u[2] = u[3] = 0xff800000u; }
     __device__ __forceinline__ void set(int e, float x) { u[e] = __float_as_uint(x); }
     __device__ __forceinline__ float get(int e) const { return __uint_as_float(u[e]); }
+    __device__ __forceinline__ float pick(int e) const { return __uint_as_float(e < 2 ? (e < 1 ? u[0] : u[1]) : (e < 3 ? u[2] : u[3])); }
     __device__ __forceinline__ float largest() const { return fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3))); }
 };
 
@@ -265,10 +275,12 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const T* logits = static_cast<const T*>(p.logits) + row * p.row_stride;
     const unsigned shift = static_cast<unsigned>(reinterpret_cast<uintptr_t>(logits) & 15u);
-    const int first = (chunk * kVectors * kThreads + threadIdx.x) * kN;  // token of the thread's first logit
+    // the chunk's tokens, and the thread's first one
+    const int lo = chunk * p.chunk_tokens, hi = min(lo + p.chunk_tokens, p.vocab);
+    const int first = lo + static_cast<int>(threadIdx.x) * kN;
     Vector<T> v[kVectors];
 #pragma unroll
-    for (int i = 0; i < kVectors; ++i) v[i] = load(logits, first + i * kThreads * kN, p.vocab, shift);
+    for (int i = 0; i < kVectors; ++i) v[i] = load(logits, first + i * kThreads * kN, hi, shift);
     float best = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) best = fmaxf(best, v[i].largest());
@@ -276,7 +288,6 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
     // sum 2^(x log2(e) - from), whose only error beside the sum's is that of the
     // fp32 constant, by which the join divides again. A NaN makes the row's sum
     // NaN, and then none of its scores is a number.
-    const int lo = chunk * kVectors * kThreads * kN, hi = min(lo + kVectors * kThreads * kN, p.vocab);
     const float top = unordered(__reduce_max_sync(0xffffffffu, ordered(best)));
     const float from = top > -INFINITY ? top * kLog2e : 0.f;
     float sum = 0.f;
@@ -293,14 +304,16 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
 #pragma unroll 1
             for (int e = 0; e < kN; ++e) {
                 const int at = first + i * kThreads * kN + e;
-                if (at < p.vocab) sum += ex2((static_cast<float>(logits[at]) - top) * kLog2e);
+                if (at < hi) sum += ex2((static_cast<float>(logits[at]) - top) * kLog2e);
             }
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     const size_t out = static_cast<size_t>(row) * p.chunks + chunk;
     if (lane == 0) p.stats[out * kWarps + warp] = make_float2(top, sum);
-    const float cut = threshold(sel, best, p.n);
+    const float cut = threshold(sel, best, p.n, min(kWarps, (hi - lo + 32 * kN - 1) / (32 * kN)));
+    // index `at` of the chunk's candidates, counted down, so that the lower is the larger
+    auto packed = [&](float x, int at) { return static_cast<uint64_t>(ordered(x)) << 32 | static_cast<uint32_t>(~at); };
     if (best >= cut && best > -INFINITY) {
 #pragma unroll
         for (int i = 0; i < kVectors; ++i) {
@@ -309,45 +322,44 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
             unsigned hits = 0;
 #pragma unroll
             for (int e = 0; e < kN; ++e)
-                if (v[i].get(e) >= cut) hits |= 1u << e;
+                if (v[i].get(e) >= cut && v[i].get(e) > -INFINITY) hits |= 1u << e;
+            if (hits == 0) continue;
+            int slot = atomicAdd(&sel.count, __popc(hits));
 #pragma unroll 1
-            for (; hits; hits &= hits - 1) {
-                const int at = first + i * kThreads * kN + __ffs(static_cast<int>(hits)) - 1;
-                const float x = at < p.vocab ? static_cast<float>(logits[at]) : -INFINITY;
-                if (x > -INFINITY) offer(sel, ordered(x), at);
+            for (; hits; hits &= hits - 1, ++slot) {
+                const int e = __ffs(static_cast<int>(hits)) - 1;
+                if (slot < kList) sel.list[slot] = packed(v[i].pick(e), first + i * kThreads * kN + e);
             }
         }
     }
     griddep_launch_dependents();  // the join's CTAs need not take room before
     uint2* list = p.lists + out * p.n;
-    finish(
+    finish<false>(
         sel, p.n, hi - lo,
-        [&](int i, uint64_t& k, int& at) {
-            at = lo + i;
-            const float x = static_cast<float>(logits[at]);
-            k = ordered(x);
+        [&](int i, uint64_t& k, int&) {
+            const float x = static_cast<float>(logits[lo + i]);
+            k = packed(x, lo + i);
             return x > -INFINITY;
         },
-        [&](int rank, uint64_t k, int at) {
-            list[rank] = make_uint2(__float_as_uint(unordered(static_cast<uint32_t>(k))), static_cast<uint32_t>(at));
+        [&](int rank, uint64_t k, int) {
+            list[rank] = k ? make_uint2(__float_as_uint(unordered(static_cast<uint32_t>(k >> 32))), ~static_cast<uint32_t>(k))
+                           : make_uint2(0xff800000u, 0xffffffffu);
         });
 }
 
 // ---- join -----------------------------------------------------------------------
 
 // CTA (group, share): every share of a group finds its best n candidates, and
-// writes the results of every gridDim.y-th. The chunks' lists are in order, so
-// the candidates are merged: in each of n rounds the best of the lists' first
-// remaining entries is taken. (A cut as in the scan's does not bound the list:
-// where one beam leads, the best n are in a few chunks, and the other chunks'
-// first entries say nothing about them.)
+// writes the results of every gridDim.y-th. Candidates are sifted by a cut as the
+// scan's, by scores in fp32 with room for their rounding; what is left is ranked
+// by scores in pairs.
 __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
+    __shared__ Selection sel;
     // In quarters, so that no sum of finite ones overflows: the beams' scores and
     // the logarithms of their sums.
     __shared__ float score[kMaxBeams];
     __shared__ Pair lse[kMaxBeams];
     __shared__ bool done[kMaxBeams];
-    __shared__ uint4 warp_best[2][kWarps];
     __shared__ float won_score[kMaxCandidates];
     __shared__ int won_at[kMaxCandidates];
     const int group = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -355,25 +367,33 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
     griddep_wait();
     for (int k = warp; k < p.beams; k += kWarps) {
         const int row = row0 + k, parts = p.chunks * kWarps;
-        const bool live = row_live(p, row);
-        if (lane == 0) {
-            score[k] = 0.25f * p.scores[row];
-            done[k] = row_done(p, row);
-        }
-        if (!live) continue;
         const float2* stats = p.stats + static_cast<size_t>(row) * parts;
+        constexpr int kHeld = 4;  // of the parts, a lane; the rest are read twice
+        float2 held[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) held[i] = lane + 32 * i < parts ? stats[lane + 32 * i] : make_float2(-INFINITY, 0.f);
+        const float s = p.scores[row];
+        const bool ended = row_done(p, row);
+        if (lane == 0) {
+            score[k] = 0.25f * s;
+            done[k] = ended;
+            lse[k] = {0.f, 0.f};
+        }
+        if (ended || !(s > -INFINITY)) continue;
         float top = -INFINITY;
-#pragma unroll 4
-        for (int i = lane; i < parts; i += 32) top = fmaxf(top, stats[i].x);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) top = fmaxf(top, held[i].x);
+        for (int i = lane + 32 * kHeld; i < parts; i += 32) top = fmaxf(top, stats[i].x);
         top = unordered(__reduce_max_sync(0xffffffffu, ordered(top)));
         // a part's sum counts from its largest logit, times the scan's fp32 log2(e)
         const bool large = fabsf(top * kLog2e) == INFINITY;
+        auto scaled = [&](float2 s) {
+            return s.y * exp2f(large ? (s.x - top) * kLog2e : __fmul_rn(s.x, kLog2e) - __fmul_rn(top, kLog2e));
+        };
         float sum = 0.f;
-#pragma unroll 4
-        for (int i = lane; i < parts; i += 32) {
-            const float2 s = stats[i];
-            sum += s.y * exp2f(large ? (s.x - top) * kLog2e : __fmul_rn(s.x, kLog2e) - __fmul_rn(top, kLog2e));
-        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) sum += lane + 32 * i < parts ? scaled(held[i]) : 0.f;
+        for (int i = lane + 32 * kHeld; i < parts; i += 32) sum += scaled(stats[i]);
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (lane == 0) {
@@ -389,87 +409,80 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
         }
     }
     __syncthreads();
-    // Entry j of list i (a chunk of a beam): its key, 0 for none, and index. A
-    // finished beam has one entry in all, whose score is the beam's.
-    const int lists = p.beams * p.chunks;
-    auto raw = [&](int i, int k, int j) {
-        if (!(score[k] > -INFINITY) || j >= p.n) return make_uint2(0u, 0xffffffffu);
-        if (done[k]) return make_uint2(0u, i == k * p.chunks && j == 0 ? static_cast<uint32_t>(p.eos) : 0xffffffffu);
-        return p.lists[(static_cast<size_t>(row0) * p.chunks + i) * p.n + j];
+    // Candidate i is entry i % (chunks * n) of beam i / (chunks * n); a finished
+    // beam has its first one alone, whose score is the beam's. Neighbours go to
+    // different warps, so that those of a few leading chunks do too.
+    const int per_row = p.chunks * p.n, items = p.beams * per_row;
+    const float by = 1.f / static_cast<float>(per_row);
+    const bool few = items < (1 << 20);  // quotients by fp32 are exact
+    auto beam_of = [&](int i) { return few ? static_cast<int>((static_cast<float>(i) + 0.5f) * by) : i / per_row; };
+    const uint2* lists = p.lists + static_cast<size_t>(row0) * per_row;
+    // the score's larger part (-inf or NaN for none)
+    auto rough = [&](int i, int k, uint2 c) {
+        if (done[k]) return i == k * per_row ? score[k] : -INFINITY;
+        const float s = score[k] + (0.25f * __uint_as_float(c.x) - lse[k].hi);
+        return static_cast<int>(c.y) < 0 || !(score[k] > -INFINITY) ? -INFINITY : s;
     };
-    auto key_of = [&](int k, uint2 c, int& at) {
-        at = k * p.vocab + static_cast<int>(c.y);
-        if (static_cast<int>(c.y) < 0) return uint64_t(0);
+    auto exact = [&](int i, int k, uint2 c, uint64_t& key, int& at) {
+        if (rough(i, k, c) == -INFINITY) return false;
+        at = k * p.vocab + (done[k] ? p.eos : static_cast<int>(c.y));
         const Pair l = lse[k];
         const Pair s = done[k] ? Pair{score[k], 0.f}
                                : add(add(two_sum(0.25f * __uint_as_float(c.x), -l.hi), -l.lo), score[k]);
-        if (!(s.hi > -INFINITY && s.hi < INFINITY)) return uint64_t(0);  // (none for NaN)
-        return static_cast<uint64_t>(ordered(s.hi)) << 32 | ordered(s.lo);
+        key = static_cast<uint64_t>(ordered(s.hi)) << 32 | ordered(s.lo);
+        return s.hi > -INFINITY && s.hi < INFINITY;  // (false for NaN)
     };
-    // The thread's list with its first remaining entry, and the one behind it;
-    // where it has more lists, how far each was taken is counted again from the
-    // last one taken, since its own entries are in order.
-    uint64_t key = 0, next_key = 0;
-    int at = INT_MAX, next_at = INT_MAX, taken = 0;
-    const bool single = lists <= kThreads;
-    const int list = min(static_cast<int>(threadIdx.x), lists - 1), beam = list / p.chunks;
-    if (single && list == threadIdx.x) {
-        const uint2 c0 = raw(list, beam, 0), c1 = raw(list, beam, 1);
-        key = key_of(beam, c0, at);
-        next_key = key_of(beam, c1, next_at);
+    constexpr int kAhead = 4;  // loads in flight
+    const int mine = lane * kWarps + warp;
+    float best = -INFINITY;
+    for (int i0 = mine; i0 < items; i0 += kAhead * kThreads) {
+        uint2 c[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i0 + u * kThreads < items) c[u] = lists[i0 + u * kThreads];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i < items) best = fmaxf(best, rough(i, beam_of(i), c[u]));  // passes over NaN
+        }
     }
-    uint64_t last = ~uint64_t(0);
-    int last_at = -1;
-    auto search = [&] {  // the best entry of the thread's lists behind the last one taken
-        key = 0;
-        at = INT_MAX;
-        for (int i = threadIdx.x; i < lists; i += kThreads) {
-            const int k = i / p.chunks;
-            for (int j = 0; j < p.n; ++j) {
-                int a;
-                const uint64_t e = key_of(k, raw(i, k, j), a);
-                if (e == 0) break;
-                if (!before(last, last_at, e, a)) continue;
-                if (before(e, a, key, at)) {
-                    key = e;
-                    at = a;
-                }
-                break;
-            }
-        }
-    };
-    if (!single) search();
-    // the first of the warp's keys, and where it is
-    auto first_of = [](uint64_t k, int i) {
-        const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(k >> 32));
-        const bool top = static_cast<uint32_t>(k >> 32) == hi;
-        const uint32_t lo = __reduce_max_sync(0xffffffffu, top ? static_cast<uint32_t>(k) : 0u);
-        const int first = __reduce_min_sync(0xffffffffu, top && static_cast<uint32_t>(k) == lo ? i : INT_MAX);
-        return make_uint4(lo, hi, static_cast<uint32_t>(first), 0u);
-    };
-    for (int j = 0; j < p.n; ++j) {
-        const uint4 u = first_of(key, at);
-        if (lane == 0) warp_best[j & 1][warp] = u;
-        __syncthreads();
-        const uint4 w = warp_best[j & 1][lane % kWarps];
-        const uint4 best = first_of(static_cast<uint64_t>(w.y) << 32 | w.x, static_cast<int>(w.z));
-        last = static_cast<uint64_t>(best.y) << 32 | best.x;
-        last_at = static_cast<int>(best.z);
-        if (threadIdx.x == 0) {
-            won_score[j] = last ? 4.f * (unordered(best.y) + unordered(best.x)) : -INFINITY;
-            won_at[j] = last ? last_at : -1;
-        }
-        if (last && key == last && at == last_at) {
-            if (single) {
-                key = next_key;
-                at = next_at;
-                ++taken;
-                next_key = key_of(beam, raw(list, beam, taken + 1), next_at);
-            } else {
-                search();
+    float cut = threshold(sel, best, p.n, min(items, kWarps));
+    // Rounded sums are off by less than 2^-22 of their terms: those of a score at
+    // the cut are the beam's score, its logarithm of the sum, and the cut less
+    // these.
+    float terms = 0.f;
+    for (int k = 0; k < p.beams; ++k) {
+        const float t = fabsf(score[k]) + fabsf(lse[k].hi);
+        if (t < INFINITY) terms = fmaxf(terms, t);
+    }
+    cut -= 0x1p-21f * (2.f * terms + fabsf(cut));
+    if (!(cut > -INFINITY)) cut = -INFINITY;
+    for (int i0 = mine; i0 < items; i0 += kAhead * kThreads) {
+        uint2 c[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i0 + u * kThreads < items) c[u] = lists[i0 + u * kThreads];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i >= items) continue;
+            const int k = beam_of(i);
+            uint64_t key;
+            int at;
+            if (!(rough(i, k, c[u]) >= cut) || !exact(i, k, c[u], key, at)) continue;
+            const int slot = atomicAdd(&sel.count, 1);
+            if (slot < kList) {
+                sel.list[slot] = key;
+                sel.at[slot] = at;
             }
         }
     }
+    finish<true>(
+        sel, p.n, items, [&](int i, uint64_t& key, int& at) { return exact(i, beam_of(i), lists[i], key, at); },
+        [&](int rank, uint64_t key, int at) {
+            won_score[rank] = at < 0 ? -INFINITY : 4.f * (unordered(static_cast<uint32_t>(key >> 32)) + unordered(static_cast<uint32_t>(key)));
+            won_at[rank] = at;
+        });
     __syncthreads();
     for (int j = blockIdx.y; j < p.n; j += gridDim.y) {
         const int at = won_at[j];
@@ -510,12 +523,16 @@ int vectors_for(long long rows, long long vectors) {
     return v;
 }
 
-// Chunks of a row of `vocab` logits of `size` bytes.
-int chunks_for(long long rows, int vocab, int size, int* vectors) {
+// Chunks of a row of `vocab` logits of `size` bytes, and their tokens: as even as
+// vectors allow, so that no chunk leaves most of its warps without logits.
+int chunks_for(long long rows, int vocab, int size, int* vectors, int* tokens) {
     const int n = 16 / size;
     const long long most = (static_cast<long long>(vocab) + n - 1) / n;
     *vectors = vectors_for(rows, most);
-    return static_cast<int>((most + *vectors * kThreads - 1) / (*vectors * kThreads));
+    const long long chunks = (most + *vectors * kThreads - 1) / (*vectors * kThreads);
+    const long long each = (most + chunks - 1) / chunks;
+    *tokens = static_cast<int>(each * n);
+    return static_cast<int>((most + each - 1) / each);
 }
 
 template <class T>
@@ -532,8 +549,8 @@ pkv_status check(int groups, int beams, int candidates, int vocab) {
     if (groups < 1 || beams < 1 || candidates < 1 || vocab < 1) return PKV_EINVAL;
     if (beams > kMaxBeams || candidates > kMaxCandidates) return PKV_EUNSUPPORTED;
     if (static_cast<long long>(beams) * vocab >= INT_MAX || vocab > (1 << 30) || groups > (1 << 20)) return PKV_ERANGE;
-    int v;
-    if (static_cast<long long>(groups) * beams * chunks_for(static_cast<long long>(groups) * beams, vocab, 4, &v) > INT_MAX)
+    int v, t;
+    if (static_cast<long long>(groups) * beams * chunks_for(static_cast<long long>(groups) * beams, vocab, 4, &v, &t) > INT_MAX)
         return PKV_ERANGE;
     return PKV_OK;
 }
@@ -555,9 +572,9 @@ extern "C" {
 size_t pkv_beam_workspace_size(int num_groups, int num_beams, int num_candidates, int vocab) {
     if (beam::check(num_groups, num_beams, num_candidates, vocab) != PKV_OK) return 0;
     const long long rows = static_cast<long long>(num_groups) * num_beams;
-    int v;
-    return std::max(beam::workspace_for(rows, num_candidates, beam::chunks_for(rows, vocab, 2, &v)),
-                    beam::workspace_for(rows, num_candidates, beam::chunks_for(rows, vocab, 4, &v)));
+    int v, t;
+    return std::max(beam::workspace_for(rows, num_candidates, beam::chunks_for(rows, vocab, 2, &v, &t)),
+                    beam::workspace_for(rows, num_candidates, beam::chunks_for(rows, vocab, 4, &v, &t)));
 }
 
 pkv_status pkv_beam_select(const void* logits, int64_t row_stride, int logits_bytes, const float* scores,
@@ -578,7 +595,7 @@ pkv_status pkv_beam_select(const void* logits, int64_t row_stride, int logits_by
     const long long rows = static_cast<long long>(num_groups) * num_beams;
     int vectors;
     beam::Params p = {};
-    p.chunks = beam::chunks_for(rows, vocab, logits_bytes, &vectors);
+    p.chunks = beam::chunks_for(rows, vocab, logits_bytes, &vectors, &p.chunk_tokens);
     if (workspace_bytes < beam::workspace_for(rows, num_candidates, p.chunks)) return PKV_EINVAL;
     p.logits = logits;
     p.row_stride = row_stride;
