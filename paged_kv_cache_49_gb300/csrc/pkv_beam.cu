@@ -67,6 +67,24 @@ __device__ __forceinline__ bool row_live(const Params& p, int row) {
     return !done & some;
 }
 
+// Pairs of fp32 numbers in one register pair, one instruction for both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // Numbers that compare as unsigned integers as the keys do as floats (-0 as 0).
 __device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t u = __float_as_uint(__fadd_rn(x, 0.f));
@@ -99,6 +117,7 @@ __device__ __forceinline__ Pair mul(Pair a, Pair b) {
 struct Selection {
     uint64_t list[kList];
     int at[kList];  // (of the join, whose keys take all 64 bits)
+    float deal[kThreads];
     uint32_t warp_key[kWarps];
     uint64_t warp_best[kWarps];
     int warp_at[kWarps];
@@ -201,6 +220,7 @@ struct Vector;  // 16 bytes of logits
 template <>
 struct Vector<__nv_bfloat16> {
     static constexpr int kN = 8;
+    static constexpr float kLeast = -0x1.fep127f;
     uint32_t u[4];
     __device__ __forceinline__ void fill() { u[0] = u[1] = u[2] = u[3] = 0xff80ff80u; }  // -inf
     __device__ __forceinline__ void set(int e, __nv_bfloat16 x) {
@@ -211,6 +231,18 @@ struct Vector<__nv_bfloat16> {
     __device__ __forceinline__ float pick(int e) const {  // get(e) where e is not known in advance
         const uint32_t w = e < 4 ? (e < 2 ? u[0] : u[1]) : (e < 6 ? u[2] : u[3]);
         return e & 1 ? bf16_hi(w) : bf16_lo(w);
+    }
+    // bit e: logit e reaches the cut, a bf16 number above -inf
+    __device__ __forceinline__ unsigned reach(float cut) const {
+        const __nv_bfloat162 c = __float2bfloat162_rn(cut);
+        unsigned m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = __hge2_mask(reinterpret_cast<const __nv_bfloat162&>(u[i]), c);
+        if ((m[0] | m[1] | m[2] | m[3]) == 0) return 0;
+        unsigned bits = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bits |= (m[i] & 1u) << (2 * i) | (m[i] >> 31) << (2 * i + 1);
+        return bits;
     }
     // the largest value (NaN passed over), pairs at a time
     static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
@@ -226,10 +258,17 @@ struct Vector<__nv_bfloat16> {
 template <>
 struct Vector<float> {
     static constexpr int kN = 4;
+    static constexpr float kLeast = -0x1.fffffep127f;
     uint32_t u[4];
     __device__ __forceinline__ void fill() { u[0] = u[1] = u[2] = u[3] = 0xff800000u; }
     __device__ __forceinline__ void set(int e, float x) { u[e] = __float_as_uint(x); }
     __device__ __forceinline__ float get(int e) const { return __uint_as_float(u[e]); }
+    __device__ __forceinline__ unsigned reach(float cut) const {
+        unsigned bits = 0;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) bits |= get(e) >= cut ? 1u << e : 0u;
+        return bits;
+    }
     __device__ __forceinline__ float pick(int e) const { return __uint_as_float(e < 2 ? (e < 1 ? u[0] : u[1]) : (e < 3 ? u[2] : u[3])); }
     __device__ __forceinline__ float largest() const { return fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3))); }
 };
@@ -292,12 +331,20 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
     const float from = top > -INFINITY ? top * kLog2e : 0.f;
     float sum = 0.f;
     if (fabsf(from) < INFINITY || fabsf(top) == INFINITY) {
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        // two at a time: x log2(e) - from, and the sums
+        uint64_t part[2] = {0, 0};
+        const uint64_t by = pair(kLog2e, kLog2e), less = pair(-from, -from);
 #pragma unroll
         for (int i = 0; i < kVectors; ++i)
 #pragma unroll
-            for (int e = 0; e < kN; ++e) part[e % 4] += ex2(fmaf(v[i].get(e), kLog2e, -from));
-        sum = (part[0] + part[1]) + (part[2] + part[3]);
+            for (int e = 0; e < kN; e += 2) {
+                float a, b;
+                unpair(fma2(pair(v[i].get(e), v[i].get(e + 1)), by, less), a, b);
+                part[e / 2 % 2] = add2(part[e / 2 % 2], pair(ex2(a), ex2(b)));
+            }
+        float a, b;
+        unpair(add2(part[0], part[1]), a, b);
+        sum = a + b;
     } else {  // logits of more than 2e38
 #pragma unroll
         for (int i = 0; i < kVectors; ++i)
@@ -311,18 +358,14 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     const size_t out = static_cast<size_t>(row) * p.chunks + chunk;
     if (lane == 0) p.stats[out * kWarps + warp] = make_float2(top, sum);
-    const float cut = threshold(sel, best, p.n, min(kWarps, (hi - lo + 32 * kN - 1) / (32 * kN)));
+    // (a cut of -inf is raised to the least finite number: -inf is no candidate)
+    const float cut = fmaxf(threshold(sel, best, p.n, min(kWarps, (hi - lo + 32 * kN - 1) / (32 * kN))), Vector<T>::kLeast);
     // index `at` of the chunk's candidates, counted down, so that the lower is the larger
     auto packed = [&](float x, int at) { return static_cast<uint64_t>(ordered(x)) << 32 | static_cast<uint32_t>(~at); };
-    if (best >= cut && best > -INFINITY) {
+    if (best >= cut) {
 #pragma unroll
         for (int i = 0; i < kVectors; ++i) {
-            if (!(v[i].largest() >= cut)) continue;
-            // the vector's logits that reach the cut, as bits, and then one by one
-            unsigned hits = 0;
-#pragma unroll
-            for (int e = 0; e < kN; ++e)
-                if (v[i].get(e) >= cut && v[i].get(e) > -INFINITY) hits |= 1u << e;
+            unsigned hits = v[i].reach(cut);
             if (hits == 0) continue;
             int slot = atomicAdd(&sel.count, __popc(hits));
 #pragma unroll 1
@@ -410,8 +453,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
     }
     __syncthreads();
     // Candidate i is entry i % (chunks * n) of beam i / (chunks * n); a finished
-    // beam has its first one alone, whose score is the beam's. Neighbours go to
-    // different warps, so that those of a few leading chunks do too.
+    // beam has its first one alone, whose score is the beam's.
     const int per_row = p.chunks * p.n, items = p.beams * per_row;
     const float by = 1.f / static_cast<float>(per_row);
     const bool few = items < (1 << 20);  // quotients by fp32 are exact
@@ -432,20 +474,29 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
         key = static_cast<uint64_t>(ordered(s.hi)) << 32 | ordered(s.lo);
         return s.hi > -INFINITY && s.hi < INFINITY;  // (false for NaN)
     };
+    // Every thread takes one of each 256 candidates, a different one in turn: the
+    // first entries of the lists, the best ones, come to all.
     constexpr int kAhead = 4;  // loads in flight
-    const int mine = lane * kWarps + warp;
-    float best = -INFINITY;
-    for (int i0 = mine; i0 < items; i0 += kAhead * kThreads) {
-        uint2 c[kAhead];
+    auto each = [&](auto take) {
+        for (int i0 = 0; i0 < items; i0 += kAhead * kThreads) {
+            uint2 c[kAhead];
+            int at[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (i0 + u * kThreads < items) c[u] = lists[i0 + u * kThreads];
+            for (int u = 0; u < kAhead; ++u) {
+                at[u] = i0 + u * kThreads + ((threadIdx.x + 37 * (i0 / kThreads + u)) & (kThreads - 1));
+                if (at[u] < items) c[u] = lists[at[u]];
+            }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int i = i0 + u * kThreads;
-            if (i < items) best = fmaxf(best, rough(i, beam_of(i), c[u]));  // passes over NaN
+            for (int u = 0; u < kAhead; ++u)
+                if (at[u] < items) take(at[u], beam_of(at[u]), c[u]);
         }
-    }
+    };
+    float best = -INFINITY;
+    each([&](int i, int k, uint2 c) { best = fmaxf(best, rough(i, k, c)); });  // passes over NaN
+    // the threads' best, dealt out anew: neighbours go to different warps
+    sel.deal[threadIdx.x] = best;
+    __syncthreads();
+    best = sel.deal[lane * kWarps + warp];
     float cut = threshold(sel, best, p.n, min(items, kWarps));
     // Rounded sums are off by less than 2^-22 of their terms: those of a score at
     // the cut are the beam's score, its logarithm of the sum, and the cut less
@@ -457,26 +508,16 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
     }
     cut -= 0x1p-21f * (2.f * terms + fabsf(cut));
     if (!(cut > -INFINITY)) cut = -INFINITY;
-    for (int i0 = mine; i0 < items; i0 += kAhead * kThreads) {
-        uint2 c[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (i0 + u * kThreads < items) c[u] = lists[i0 + u * kThreads];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int i = i0 + u * kThreads;
-            if (i >= items) continue;
-            const int k = beam_of(i);
-            uint64_t key;
-            int at;
-            if (!(rough(i, k, c[u]) >= cut) || !exact(i, k, c[u], key, at)) continue;
-            const int slot = atomicAdd(&sel.count, 1);
-            if (slot < kList) {
-                sel.list[slot] = key;
-                sel.at[slot] = at;
-            }
+    each([&](int i, int k, uint2 c) {
+        uint64_t key;
+        int at;
+        if (!(rough(i, k, c) >= cut) || !exact(i, k, c, key, at)) return;
+        const int slot = atomicAdd(&sel.count, 1);
+        if (slot < kList) {
+            sel.list[slot] = key;
+            sel.at[slot] = at;
         }
-    }
+    });
     finish<true>(
         sel, p.n, items, [&](int i, uint64_t& key, int& at) { return exact(i, beam_of(i), lists[i], key, at); },
         [&](int rank, uint64_t key, int at) {
