@@ -563,6 +563,12 @@ class _LaunchHere:
         pass
 
 
+def _here(device: int, stream) -> int | None:
+    """The current stream's handle where that is the one to launch on and `device`
+    the current device; None where _LaunchOn has to make them so first."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None and torch._C._cuda_getDevice() == device else None
+
+
 def _launch_on(device: int, stream):
     if stream is None and torch.cuda.current_device() == device:
         return _LaunchHere(device)
@@ -786,14 +792,21 @@ class Int4Cache:
             raise ValueError("Int4Cache needs blocks, heads, block_tokens in (8, 16, 32, 64) and group_dims in (32, 64, 128)")
         self.num_blocks, self.num_kv_heads = num_blocks, num_kv_heads
         self.block_tokens, self.group_dims = block_tokens, group_dims
-        self.data = torch.zeros((num_blocks, num_kv_heads, nbytes // num_kv_heads), dtype=torch.uint8,
-                                device=device or "cuda")
+        self._data = torch.zeros((num_blocks, num_kv_heads, nbytes // num_kv_heads), dtype=torch.uint8,
+                                 device=device or "cuda")
+        # of the calls' arguments: the pool's address, and the shape behind it
+        self._ptr, self._device = self._data.data_ptr(), self._data.get_device()
+        self._shape = num_kv_heads, HEAD_DIM, block_tokens, group_dims
 
-    def _shape(self):
-        return self.num_kv_heads, HEAD_DIM, self.block_tokens, self.group_dims
+    @property
+    def data(self) -> torch.Tensor:
+        return self._data
 
 
-_U8 = torch.uint8
+def _need_cache(cache: Int4Cache) -> int:
+    if cache._device < 0:
+        raise ValueError("the cache must be on a CUDA device")
+    return cache._device
 
 
 def _need_pairs(device: int, pairs) -> int:
@@ -803,52 +816,56 @@ def _need_pairs(device: int, pairs) -> int:
     return pairs.shape[0] if pairs.numel() else 0
 
 
+def _need_error_word(device: int, device_error) -> int | None:
+    if device_error is None:
+        return None
+    _need_all(device, ((device_error, _I32, "device_error"),))
+    return device_error.data_ptr()
+
+
 def append_int4(k, v, slot_mapping, cache: Int4Cache, device_error=None, stream=None) -> None:
     """Quantise k[i], v[i] ([T, Hkv, 128] bf16, possibly views of one fused
     projection) into slot slot_mapping[i] (int64; negative: a padding row)."""
-    device = cache.data.get_device()
-    T = slot_mapping.numel()
-    _need_all(device, ((cache.data, _U8, "the cache"), (slot_mapping, _I64, "slot_mapping")))
+    device = _need_cache(cache)
+    _need_all(device, ((slot_mapping, _I64, "slot_mapping"),))
     if k.dim() != 3 or v.dim() != 3:
         raise ValueError("k, v must be [T, Hkv, 128]")
-    ks = _need_rows(device, k, "k", T, cache.num_kv_heads, HEAD_DIM)
-    vs = _need_rows(device, v, "v", T, cache.num_kv_heads, HEAD_DIM)
-    if device_error is not None:
-        _need_all(device, ((device_error, _I32, "device_error"),))
-    with _launch_on(device, stream) as st:
-        _check(_lib.pkv_append_int4(k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T, cache.data.data_ptr(),
-                                    cache.num_blocks, *cache._shape(), _ptr(device_error), st), "pkv_append_int4")
+    T, hkv = slot_mapping.numel(), cache.num_kv_heads
+    ks = _need_rows(device, k, "k", T, hkv, HEAD_DIM)
+    vs = _need_rows(device, v, "v", T, hkv, HEAD_DIM)
+    err = _need_error_word(device, device_error)
+    st = _here(device, stream)
+    with contextlib.nullcontext(st) if st is not None else _LaunchOn(device, stream) as st:
+        _check(_lib.pkv_append_int4(k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T, cache._ptr,
+                                    cache.num_blocks, *cache._shape, err, st), "pkv_append_int4")
 
 
 def load_int4(cache: Int4Cache, pairs, k_cache, v_cache, device_error=None, stream=None) -> None:
     """Block pairs[i, 0] of the 4-bit cache as bf16 rows into block pairs[i, 1] of
     k_cache and v_cache [blocks, Hkv, block_tokens, 128]."""
-    device = cache.data.get_device()
-    _need_all(device, ((cache.data, _U8, "the cache"), (k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache")))
+    device = _need_cache(cache)
+    _need_all(device, ((k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache")))
     n = _need_pairs(device, pairs)
-    hkv, d, bt, _ = cache._shape()
+    hkv, d, bt, _ = cache._shape
     if k_cache.dim() != 4 or k_cache.shape[1:] != (hkv, bt, d) or v_cache.shape != k_cache.shape:
         raise ValueError(f"k_cache, v_cache must be {['blocks', hkv, bt, d]} and alike")
-    if device_error is not None:
-        _need_all(device, ((device_error, _I32, "device_error"),))
+    err = _need_error_word(device, device_error)
     if n == 0:
         return
-    with _launch_on(device, stream) as st:
-        _check(_lib.pkv_load_int4(cache.data.data_ptr(), pairs.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(),
-                                  cache.num_blocks, k_cache.shape[0], *cache._shape(), _ptr(device_error), st),
-               "pkv_load_int4")
+    st = _here(device, stream)
+    with contextlib.nullcontext(st) if st is not None else _LaunchOn(device, stream) as st:
+        _check(_lib.pkv_load_int4(cache._ptr, pairs.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(), cache.num_blocks,
+                                  k_cache.shape[0], *cache._shape, err, st), "pkv_load_int4")
 
 
 def block_copy_int4(cache: Int4Cache, pairs, device_error=None, stream=None) -> None:
     """Copy physical block pairs[i, 0] of the cache onto pairs[i, 1]."""
-    device = cache.data.get_device()
-    _need_all(device, ((cache.data, _U8, "the cache"),))
+    device = _need_cache(cache)
     n = _need_pairs(device, pairs)
-    if device_error is not None:
-        _need_all(device, ((device_error, _I32, "device_error"),))
+    err = _need_error_word(device, device_error)
     with _launch_on(device, stream) as st:
-        _check(_lib.pkv_block_copy_int4(cache.data.data_ptr(), pairs.data_ptr(), n, cache.num_blocks, *cache._shape(),
-                                        _ptr(device_error), st), "pkv_block_copy_int4")
+        _check(_lib.pkv_block_copy_int4(cache._ptr, pairs.data_ptr(), n, cache.num_blocks, *cache._shape, err, st),
+               "pkv_block_copy_int4")
 
 
 def attn_decode_int4(q, cache: Int4Cache, block_tables, context_lens, scale, out=None, workspace=None, num_ctas: int = 0,
@@ -857,29 +874,31 @@ def attn_decode_int4(q, cache: Int4Cache, block_tables, context_lens, scale, out
     workspace: an AttentionWorkspace; without one the call makes it, and device
     errors are not reported."""
     device = q.get_device()
-    _need_all(device, ((q, _BF16, "q"), (cache.data, _U8, "the cache"), (block_tables, _I32, "block_tables"),
-                       (context_lens, _I32, "context_lens")))
-    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
+    _need_all(device, ((q, _BF16, "q"), (block_tables, _I32, "block_tables"), (context_lens, _I32, "context_lens")))
+    if cache._device != device:
+        raise ValueError(f"the cache is on {cache.data.device}, other tensors on cuda:{device}")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != HEAD_DIM:
         raise ValueError("q must be [B, Hq, 128]")
-    B, hq, d = q.shape
+    B, hq, d = shape
     if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [B, W] and context_lens [B]")
     if out is not None:
         _need_all(device, ((out, _BF16, "out"),))
-        if out.shape != q.shape:
+        if out.shape != shape:
             raise ValueError("out must be shaped like q")
     if workspace is not None and workspace.tensor.get_device() != device:
         raise ValueError(f"the workspace is on {workspace.tensor.device}, the tensors on cuda:{device}")
-    with _launch_on(device, stream) as st:
+    st = _here(device, stream)
+    with contextlib.nullcontext(st) if st is not None else _LaunchOn(device, stream) as st:
         if out is None:
             out = torch.empty_like(q)
         if workspace is None:
             workspace = AttentionWorkspace(B, cache.num_kv_heads, device=q.device, stream=st)
-        hkv, _, bt, gd = cache._shape()
-        _check(_lib.pkv_attn_decode_int4(q.data_ptr(), cache.data.data_ptr(), block_tables.data_ptr(),
-                                         block_tables.shape[1], context_lens.data_ptr(), B, hq, hkv, d, cache.num_blocks,
-                                         bt, gd, float(scale), int(num_ctas), workspace.ptr, workspace.nbytes,
-                                         out.data_ptr(), st), "pkv_attn_decode_int4")
+        hkv, _, bt, gd = cache._shape
+        _check(_lib.pkv_attn_decode_int4(q.data_ptr(), cache._ptr, block_tables.data_ptr(), block_tables.shape[1],
+                                         context_lens.data_ptr(), B, hq, hkv, d, cache.num_blocks, bt, gd, scale, num_ctas,
+                                         workspace.ptr, workspace.nbytes, out.data_ptr(), st), "pkv_attn_decode_int4")
     return out
 
 
@@ -895,9 +914,17 @@ class BeamBuffers:
 
     def __init__(self, groups: int, candidates: int, max_length: int = 0, device=None):
         new = lambda dtype, *more: torch.zeros((groups, candidates, *more), dtype=dtype, device=device or "cuda")
-        self.scores, self.tokens, self.parents = new(_F32), new(_I32), new(_I32)
-        self.finished = new(torch.bool)
-        self.lengths, self.history = (new(_I32), new(_I32, max_length)) if max_length else (None, None)
+        self.shape = groups, candidates, max_length
+        self._tensors = [new(_F32), new(_I32), new(_I32), new(torch.bool)]
+        self._tensors += [new(_I32), new(_I32, max_length)] if max_length else [None, None]
+        self._ptrs, self._device = [_ptr(t) for t in self._tensors], self._tensors[0].get_device()
+
+    scores = property(lambda self: self._tensors[0])
+    tokens = property(lambda self: self._tensors[1])
+    parents = property(lambda self: self._tensors[2])
+    finished = property(lambda self: self._tensors[3])
+    lengths = property(lambda self: self._tensors[4])
+    history = property(lambda self: self._tensors[5])
 
 
 class BeamWorkspace:
@@ -925,52 +952,47 @@ def beam_select(logits, scores, finished=None, eos: int = -1, history=None, leng
     if logits.dtype not in (_BF16, _F32) or logits.dim() != 2:
         raise ValueError(f"logits must be bf16 or fp32 [groups * beams, vocab], got {logits.dtype} {list(logits.shape)}")
     _need_all(device, ((scores, _F32, "scores"),))
-    if scores.dim() != 2 or logits.shape[0] != scores.numel() or scores.numel() == 0:
+    rows, vocab = logits.shape
+    shape = scores.shape
+    if len(shape) != 2 or rows != shape[0] * shape[1] or rows == 0:
         raise ValueError("scores must be [groups, beams], a row of logits each")
-    (groups, beams), vocab = scores.shape, logits.shape[1]
+    groups, beams = shape
     if vocab > 1 and logits.stride(1) != 1:
         raise ValueError("a row of logits must be contiguous")
     if finished is not None:
         _need_all(device, ((finished, torch.bool, "finished"),))
-        if finished.shape != scores.shape:
+        if finished.shape != shape:
             raise ValueError("finished must be shaped like scores")
     if (history is None) != (lengths is None):
         raise ValueError("history and lengths come together")
     room = 0
     if history is not None:
         _need_all(device, ((history, _I32, "history"), (lengths, _I32, "lengths")))
-        if history.dim() != 3 or history.shape[:2] != scores.shape or lengths.shape != scores.shape or history.shape[2] < 1:
+        if history.dim() != 3 or history.shape[:2] != shape or lengths.shape != shape or history.shape[2] < 1:
             raise ValueError("history must be [groups, beams, max_length] and lengths [groups, beams]")
         room = history.shape[2]
-    n = candidates if candidates is not None else out.scores.shape[1] if out is not None else beams
+    n = candidates if candidates is not None else out.shape[1] if out is not None else beams
     if out is not None:
-        parts = [(out.scores, _F32, "out.scores"), (out.tokens, _I32, "out.tokens"), (out.parents, _I32, "out.parents"),
-                 (out.finished, torch.bool, "out.finished")]
-        if room:
-            if out.history is None or out.history.shape != (groups, n, room):
-                raise ValueError("out's histories must be [groups, candidates, max_length], as the beams'")
-            if out.history.data_ptr() == history.data_ptr():
-                raise ValueError("out's histories must not be the beams'")
-            parts += [(out.lengths, _I32, "out.lengths"), (out.history, _I32, "out.history")]
-        _need_all(device, parts)
-        if any(t.shape != (groups, n) for t, _, name in parts if name != "out.history"):
-            raise ValueError(f"out must hold {groups} groups of {n} candidates")
+        if out._device != device or out.shape[:2] != (groups, n):
+            raise ValueError(f"out must hold {groups} groups of {n} candidates on cuda:{device}")
+        if room and out.shape[2] != room:
+            raise ValueError("out's histories must be [groups, candidates, max_length], as the beams'")
+        if room and out._ptrs[5] == history.data_ptr():
+            raise ValueError("out's histories must not be the beams'")
     if workspace is not None and workspace.device != device:
         raise ValueError(f"the workspace is on cuda:{workspace.device}, the tensors on cuda:{device}")
-    if device_error is not None:
-        _need_all(device, ((device_error, _I32, "device_error"),))
-    with _launch_on(device, stream) as st:
+    err = _need_error_word(device, device_error)
+    st = _here(device, stream)
+    with contextlib.nullcontext(st) if st is not None else _LaunchOn(device, stream) as st:
         if out is None:
             out = BeamBuffers(groups, n, room, device=logits.device)
         if workspace is None:
             workspace = BeamWorkspace(groups, beams, n, vocab, device=logits.device)
-        stride = logits.stride(0) if logits.shape[0] > 1 else vocab
-        _check(_lib.pkv_beam_select(logits.data_ptr(), stride, logits.element_size(), scores.data_ptr(), _ptr(finished),
-                                    int(eos), groups, beams, n, vocab, _ptr(history), _ptr(lengths), room,
-                                    out.scores.data_ptr(), out.tokens.data_ptr(), out.parents.data_ptr(),
-                                    out.finished.data_ptr(), _ptr(out.lengths) if room else None,
-                                    _ptr(out.history) if room else None, workspace.ptr, workspace.nbytes,
-                                    _ptr(device_error), st), "pkv_beam_select")
+        so, to, po, fo, lo, ho = out._ptrs
+        _check(_lib.pkv_beam_select(logits.data_ptr(), logits.stride(0) if groups * beams > 1 else vocab,
+                                    2 if logits.dtype is _BF16 else 4, scores.data_ptr(), _ptr(finished), eos, groups, beams, n,
+                                    vocab, _ptr(history), _ptr(lengths), room, so, to, po, fo, lo if room else None,
+                                    ho if room else None, workspace.ptr, workspace.nbytes, err, st), "pkv_beam_select")
     return out
 
 

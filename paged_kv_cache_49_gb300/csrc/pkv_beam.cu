@@ -36,7 +36,6 @@ constexpr int kMaxBeams = PKV_BEAM_MAX_BEAMS;
 constexpr int kMaxCandidates = PKV_BEAM_MAX_CANDIDATES;
 constexpr int kList = 512;     // candidates that are ranked
 constexpr int kMaxVectors = 8;  // 16-byte vectors a thread holds
-// Chunks are made smaller (fewer vectors a thread) while this many CTAs are not reached.
 constexpr int kWantCtas = 304;
 
 struct Params {
@@ -400,7 +399,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
     __shared__ Selection sel;
     // In quarters, so that no sum of finite ones overflows: the beams' scores and
     // the logarithms of their sums.
-    __shared__ float score[kMaxBeams];
+    __shared__ float score[kMaxBeams], less[kMaxBeams];  // (less: the score less the logarithm, -inf for a beam not read)
     __shared__ Pair lse[kMaxBeams];
     __shared__ bool done[kMaxBeams];
     __shared__ float won_score[kMaxCandidates];
@@ -421,6 +420,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
             score[k] = 0.25f * s;
             done[k] = ended;
             lse[k] = {0.f, 0.f};
+            less[k] = -INFINITY;
         }
         if (ended || !(s > -INFINITY)) continue;
         float top = -INFINITY;
@@ -449,55 +449,55 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
             else l = mul(add(two_sum(__fmul_rn(top, kLog2e), static_cast<float>(e)), rest), by);
             if (!(sum < INFINITY) || !(fabsf(top) < INFINITY)) l.hi = l.lo = NAN;
             lse[k] = {0.25f * l.hi, 0.25f * l.lo};
+            less[k] = score[k] - lse[k].hi;
         }
     }
     __syncthreads();
-    // Candidate i is entry i % (chunks * n) of beam i / (chunks * n); a finished
-    // beam has its first one alone, whose score is the beam's.
+    // Candidate i is entry i % (chunks * n) of beam i / (chunks * n), or, from
+    // `items` on, the one of the finished beam i - items.
     const int per_row = p.chunks * p.n, items = p.beams * per_row;
     const float by = 1.f / static_cast<float>(per_row);
     const bool few = items < (1 << 20);  // quotients by fp32 are exact
     auto beam_of = [&](int i) { return few ? static_cast<int>((static_cast<float>(i) + 0.5f) * by) : i / per_row; };
     const uint2* lists = p.lists + static_cast<size_t>(row0) * per_row;
-    // the score's larger part (-inf or NaN for none)
-    auto rough = [&](int i, int k, uint2 c) {
-        if (done[k]) return i == k * per_row ? score[k] : -INFINITY;
-        const float s = score[k] + (0.25f * __uint_as_float(c.x) - lse[k].hi);
-        return static_cast<int>(c.y) < 0 || !(score[k] > -INFINITY) ? -INFINITY : s;
-    };
-    auto exact = [&](int i, int k, uint2 c, uint64_t& key, int& at) {
-        if (rough(i, k, c) == -INFINITY) return false;
-        at = k * p.vocab + (done[k] ? p.eos : static_cast<int>(c.y));
+    // the score in fp32: -inf or NaN where there is no candidate
+    auto rough = [&](int i) { return fmaf(0.25f, __uint_as_float(lists[i].x), less[beam_of(i)]); };
+    auto exact = [&](int i, uint64_t& key, int& at) {
+        const bool ended = i >= items;
+        const int k = ended ? i - items : beam_of(i);
+        if (ended ? !done[k] : !(less[k] > -INFINITY)) return false;
+        const uint2 c = ended ? make_uint2(0u, static_cast<uint32_t>(p.eos)) : lists[i];
+        at = k * p.vocab + static_cast<int>(c.y);
         const Pair l = lse[k];
-        const Pair s = done[k] ? Pair{score[k], 0.f}
-                               : add(add(two_sum(0.25f * __uint_as_float(c.x), -l.hi), -l.lo), score[k]);
+        const Pair s = ended ? Pair{score[k], 0.f} : add(add(two_sum(0.25f * __uint_as_float(c.x), -l.hi), -l.lo), score[k]);
         key = static_cast<uint64_t>(ordered(s.hi)) << 32 | ordered(s.lo);
-        return s.hi > -INFINITY && s.hi < INFINITY;  // (false for NaN)
+        return static_cast<int>(c.y) >= 0 && s.hi > -INFINITY && s.hi < INFINITY;  // (false for NaN)
     };
     // Every thread takes one of each 256 candidates, a different one in turn: the
-    // first entries of the lists, the best ones, come to all.
-    constexpr int kAhead = 4;  // loads in flight
-    auto each = [&](auto take) {
-        for (int i0 = 0; i0 < items; i0 += kAhead * kThreads) {
-            uint2 c[kAhead];
-            int at[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                at[u] = i0 + u * kThreads + ((threadIdx.x + 37 * (i0 / kThreads + u)) & (kThreads - 1));
-                if (at[u] < items) c[u] = lists[at[u]];
-            }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (at[u] < items) take(at[u], beam_of(at[u]), c[u]);
-        }
-    };
+    // first entries of the lists, the best ones, come to all. The first kHeld
+    // scores of a thread stay in registers, any others are formed again.
+    constexpr int kHeld = 32;
+    auto index = [&](int u) { return u * kThreads + static_cast<int>((threadIdx.x + 37u * u) & (kThreads - 1)); };
+    float held[kHeld];
     float best = -INFINITY;
-    each([&](int i, int k, uint2 c) { best = fmaxf(best, rough(i, k, c)); });  // passes over NaN
+#pragma unroll
+    for (int u0 = 0; u0 < kHeld; u0 += 8) {
+        if (u0 * kThreads >= items) break;
+#pragma unroll
+        for (int u = u0; u < u0 + 8; ++u) {
+            held[u] = index(u) < items ? rough(index(u)) : -INFINITY;
+            best = fmaxf(best, held[u]);  // passes over NaN
+        }
+    }
+    for (int u = kHeld; u * kThreads < items; ++u)
+        if (index(u) < items) best = fmaxf(best, rough(index(u)));
+    const bool ended = threadIdx.x < p.beams && done[threadIdx.x];
+    if (ended) best = fmaxf(best, score[threadIdx.x]);
     // the threads' best, dealt out anew: neighbours go to different warps
     sel.deal[threadIdx.x] = best;
     __syncthreads();
     best = sel.deal[lane * kWarps + warp];
-    float cut = threshold(sel, best, p.n, min(items, kWarps));
+    float cut = threshold(sel, best, p.n, kWarps);
     // Rounded sums are off by less than 2^-22 of their terms: those of a score at
     // the cut are the beam's score, its logarithm of the sum, and the cut less
     // these.
@@ -507,25 +507,37 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
         if (t < INFINITY) terms = fmaxf(terms, t);
     }
     cut -= 0x1p-21f * (2.f * terms + fabsf(cut));
-    if (!(cut > -INFINITY)) cut = -INFINITY;
-    each([&](int i, int k, uint2 c) {
+    cut = fmaxf(cut, -0x1.fffffep127f);  // (-inf is no candidate)
+    auto take = [&](int i) {
         uint64_t key;
         int at;
-        if (!(rough(i, k, c) >= cut) || !exact(i, k, c, key, at)) return;
+        if (!exact(i, key, at)) return;
         const int slot = atomicAdd(&sel.count, 1);
         if (slot < kList) {
             sel.list[slot] = key;
             sel.at[slot] = at;
         }
-    });
+    };
+#pragma unroll
+    for (int u0 = 0; u0 < kHeld; u0 += 8) {
+        if (u0 * kThreads >= items) break;
+        unsigned hits = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) hits |= held[u0 + u] >= cut ? 1u << u : 0u;
+        for (; hits; hits &= hits - 1) take(index(u0 + __ffs(static_cast<int>(hits)) - 1));
+    }
+    for (int u = kHeld; u * kThreads < items; ++u)
+        if (index(u) < items && rough(index(u)) >= cut) take(index(u));
+    if (ended && score[threadIdx.x] >= cut) take(items + static_cast<int>(threadIdx.x));
     finish<true>(
-        sel, p.n, items, [&](int i, uint64_t& key, int& at) { return exact(i, beam_of(i), lists[i], key, at); },
+        sel, p.n, items + p.beams, [&](int i, uint64_t& key, int& at) { return exact(i, key, at); },
         [&](int rank, uint64_t key, int at) {
             won_score[rank] = at < 0 ? -INFINITY : 4.f * (unordered(static_cast<uint32_t>(key >> 32)) + unordered(static_cast<uint32_t>(key)));
             won_at[rank] = at;
         });
     __syncthreads();
-    for (int j = blockIdx.y; j < p.n; j += gridDim.y) {
+    // a warp a result
+    for (int j = blockIdx.y * kWarps + warp; j < p.n; j += gridDim.y * kWarps) {
         const int at = won_at[j];
         const bool some = at >= 0;
         const int k = some ? at / p.vocab : -1, token = some ? at - k * p.vocab : -1;
@@ -536,11 +548,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
         if (some && p.lengths) {
             const int given = p.lengths[row];
             length = min(max(given, 0), p.max_length);
-            if ((given != length || (!ended && length == p.max_length)) && p.err && threadIdx.x == 0)
-                atomicOr(p.err, PKV_DEVERR_CONTEXT);
+            if ((given != length || (!ended && length == p.max_length)) && p.err && lane == 0) atomicOr(p.err, PKV_DEVERR_CONTEXT);
         }
         const bool grows = some && !ended && length < p.max_length;
-        if (threadIdx.x == 0) {
+        if (lane == 0) {
             p.scores_out[out] = won_score[j];
             p.tokens_out[out] = token;
             p.parents_out[out] = k;
@@ -551,29 +562,27 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
         if (p.lengths) {
             const int32_t* src = p.history + static_cast<size_t>(row) * p.max_length;
             int32_t* dst = p.history_out + out * p.max_length;
-#pragma unroll 4
-            for (int i = threadIdx.x; i < length; i += kThreads) dst[i] = src[i];
+#pragma unroll 8
+            for (int i = lane; i < length; i += 32) dst[i] = src[i];
         }
     }
 }
 
-// Vectors a thread holds, of a row's `vectors`: as many as leave kWantCtas CTAs.
-int vectors_for(long long rows, long long vectors) {
-    int v = kMaxVectors;
-    while (v > 1 && rows * ((vectors + v * kThreads - 1) / (v * kThreads)) < kWantCtas) v /= 2;
-    return v;
-}
-
-// Chunks of a row of `vocab` logits of `size` bytes, and their tokens: as even as
-// vectors allow, so that no chunk leaves most of its warps without logits.
+// Chunks of a row of `vocab` logits of `size` bytes, their tokens, and the
+// vectors a thread holds: as many as leave kWantCtas CTAs (a CTA's fixed part,
+// 3,600 cycles of the 8,600 with 8 vectors a thread, is then paid least often),
+// and chunks as even as vectors allow, so that none leaves most of its warps
+// without logits.
 int chunks_for(long long rows, int vocab, int size, int* vectors, int* tokens) {
     const int n = 16 / size;
-    const long long most = (static_cast<long long>(vocab) + n - 1) / n;
-    *vectors = vectors_for(rows, most);
-    const long long chunks = (most + *vectors * kThreads - 1) / (*vectors * kThreads);
-    const long long each = (most + chunks - 1) / chunks;
+    const long long all = (static_cast<long long>(vocab) + n - 1) / n;  // vectors of a row
+    auto chunks = [&](int v) { return (all + v * kThreads - 1) / (v * kThreads); };
+    int v = kMaxVectors;
+    while (v > 1 && rows * chunks(v) < kWantCtas) v /= 2;
+    const long long each = (all + chunks(v) - 1) / chunks(v);
+    *vectors = v;
     *tokens = static_cast<int>(each * n);
-    return static_cast<int>((most + each - 1) / each);
+    return static_cast<int>((all + each - 1) / each);
 }
 
 template <class T>
@@ -665,7 +674,7 @@ pkv_status pkv_beam_select(const void* logits, int64_t row_stride, int logits_by
     if (e == cudaSuccess) {
         // launched early: it waits for the scan before it reads anything
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(num_groups, static_cast<unsigned>(std::max(1, std::min(num_candidates, beam::kWantCtas / num_groups))));
+        cfg.gridDim = dim3(num_groups, static_cast<unsigned>(std::max(1, std::min((num_candidates + beam::kWarps - 1) / beam::kWarps, 152 / num_groups))));
         cfg.blockDim = dim3(beam::kThreads);
         cfg.stream = as_stream(stream);
         cudaLaunchAttribute attr[1];
