@@ -51,7 +51,7 @@ struct Params {
     uint8_t* finished_out;
     int32_t* lengths_out;
     int32_t* history_out;
-    float2* stats;  // [rows][chunks][kWarps]: maximum, sum of exponentials from it on
+    float2* stats;  // [rows][chunks]: maximum, sum of exponentials from it on
     uint2* lists;   // [rows][chunks][n]: logit bits, token (or -1)
     uint32_t* err;
     int eos, beams, n, vocab, max_length, chunks, chunk_tokens;
@@ -64,6 +64,16 @@ __device__ __forceinline__ bool row_done(const Params& p, int row) { return p.fi
 __device__ __forceinline__ bool row_live(const Params& p, int row) {
     const bool done = row_done(p, row), some = p.scores[row] > -INFINITY;  // (both read at once)
     return !done & some;
+}
+
+// A sum of powers of two counts from its largest logit, times kLog2e in fp32: one
+// from s.x on as one from `top` on. (Products that overflow stand for logits of
+// more than 2e38, whose differences count alone.) One without a logit above -inf
+// is 0, or NaN.
+__device__ __forceinline__ float scaled(float2 s, float top) {
+    if (!(s.x > -INFINITY)) return s.y;
+    const float a = __fmul_rn(s.x, kLog2e), b = __fmul_rn(top, kLog2e);
+    return s.y * exp2f(fabsf(b) < INFINITY ? a - b : (s.x - top) * kLog2e);
 }
 
 // Pairs of fp32 numbers in one register pair, one instruction for both.
@@ -116,7 +126,10 @@ __device__ __forceinline__ Pair mul(Pair a, Pair b) {
 struct Selection {
     uint64_t list[kList];
     int at[kList];  // (of the join, whose keys take all 64 bits)
-    float deal[kThreads];
+    union {
+        float deal[kThreads];
+        float2 part[kWarps];
+    };
     uint32_t warp_key[kWarps];
     uint64_t warp_best[kWarps];
     int warp_at[kWarps];
@@ -227,22 +240,6 @@ struct Vector<__nv_bfloat16> {
         u[e / 2] = e & 1 ? (u[e / 2] & 0xffffu) | v << 16 : (u[e / 2] & 0xffff0000u) | v;
     }
     __device__ __forceinline__ float get(int e) const { return e & 1 ? bf16_hi(u[e / 2]) : bf16_lo(u[e / 2]); }
-    __device__ __forceinline__ float pick(int e) const {  // get(e) where e is not known in advance
-        const uint32_t w = e < 4 ? (e < 2 ? u[0] : u[1]) : (e < 6 ? u[2] : u[3]);
-        return e & 1 ? bf16_hi(w) : bf16_lo(w);
-    }
-    // bit e: logit e reaches the cut, a bf16 number above -inf
-    __device__ __forceinline__ unsigned reach(float cut) const {
-        const __nv_bfloat162 c = __float2bfloat162_rn(cut);
-        unsigned m[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m[i] = __hge2_mask(reinterpret_cast<const __nv_bfloat162&>(u[i]), c);
-        if ((m[0] | m[1] | m[2] | m[3]) == 0) return 0;
-        unsigned bits = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) bits |= (m[i] & 1u) << (2 * i) | (m[i] >> 31) << (2 * i + 1);
-        return bits;
-    }
     // the largest value (NaN passed over), pairs at a time
     static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
         uint32_t d;
@@ -262,15 +259,32 @@ struct Vector<float> {
     __device__ __forceinline__ void fill() { u[0] = u[1] = u[2] = u[3] = 0xff800000u; }
     __device__ __forceinline__ void set(int e, float x) { u[e] = __float_as_uint(x); }
     __device__ __forceinline__ float get(int e) const { return __uint_as_float(u[e]); }
-    __device__ __forceinline__ unsigned reach(float cut) const {
-        unsigned bits = 0;
-#pragma unroll
-        for (int e = 0; e < kN; ++e) bits |= get(e) >= cut ? 1u << e : 0u;
-        return bits;
-    }
-    __device__ __forceinline__ float pick(int e) const { return __uint_as_float(e < 2 ? (e < 1 ? u[0] : u[1]) : (e < 3 ? u[2] : u[3])); }
     __device__ __forceinline__ float largest() const { return fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3))); }
 };
+
+// Which of a thread's logits reach the cut: bits, and the vector and place that a
+// bit stands for.
+template <int kVectors>
+__device__ __forceinline__ uint64_t reach(const Vector<__nv_bfloat16> (&v)[kVectors], float cut) {
+    const __nv_bfloat162 c = __float2bfloat162_rn(cut);  // (a logit, or the least finite one)
+    uint32_t bits[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4 * kVectors; ++i)  // word i: bits i % 16 and 16 more
+        bits[i / 16] |= __hge2_mask(reinterpret_cast<const __nv_bfloat162&>(v[i / 4].u[i % 4]), c) & (0x00010001u << (i % 16));
+    return static_cast<uint64_t>(bits[1]) << 32 | bits[0];
+}
+__device__ __forceinline__ int2 place(int bit, __nv_bfloat16) {
+    const int word = bit / 32 * 16 + bit % 16;
+    return make_int2(word / 4, word % 4 * 2 + bit / 16 % 2);
+}
+template <int kVectors>
+__device__ __forceinline__ uint64_t reach(const Vector<float> (&v)[kVectors], float cut) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * kVectors; ++i) bits |= v[i / 4].get(i % 4) >= cut ? 1u << i : 0u;
+    return bits;
+}
+__device__ __forceinline__ int2 place(int bit, float) { return make_int2(bit / 4, bit % 4); }
 
 // kN logits from token `at` on, -inf behind the row's end. Which logits a thread
 // sums is a matter of their tokens alone, so rows that are alike have the same
@@ -355,23 +369,28 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    const size_t out = static_cast<size_t>(row) * p.chunks + chunk;
-    if (lane == 0) p.stats[out * kWarps + warp] = make_float2(top, sum);
+    if (lane == 0) sel.part[warp] = make_float2(top, sum);
     // (a cut of -inf is raised to the least finite number: -inf is no candidate)
     const float cut = fmaxf(threshold(sel, best, p.n, min(kWarps, (hi - lo + 32 * kN - 1) / (32 * kN))), Vector<T>::kLeast);
+    const size_t out = static_cast<size_t>(row) * p.chunks + chunk;
+    if (warp == 0) {  // the warps' sums, behind the cut's barrier
+        const float2 mine = sel.part[lane % kWarps];
+        const float most = unordered(__reduce_max_sync(0xffffffffu, ordered(mine.x)));
+        float all = scaled(mine, most);
+#pragma unroll
+        for (int d = 1; d < kWarps; d <<= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+        if (lane == 0) p.stats[out] = make_float2(most, all);
+    }
     // index `at` of the chunk's candidates, counted down, so that the lower is the larger
     auto packed = [&](float x, int at) { return static_cast<uint64_t>(ordered(x)) << 32 | static_cast<uint32_t>(~at); };
     if (best >= cut) {
-#pragma unroll
-        for (int i = 0; i < kVectors; ++i) {
-            unsigned hits = v[i].reach(cut);
-            if (hits == 0) continue;
-            int slot = atomicAdd(&sel.count, __popc(hits));
-#pragma unroll 1
-            for (; hits; hits &= hits - 1, ++slot) {
-                const int e = __ffs(static_cast<int>(hits)) - 1;
-                if (slot < kList) sel.list[slot] = packed(v[i].pick(e), first + i * kThreads * kN + e);
-            }
+        uint64_t hits = reach(v, cut);
+        int slot = atomicAdd(&sel.count, __popcll(hits));
+        for (; hits; hits &= hits - 1, ++slot) {
+            const int2 at = place(__ffsll(static_cast<long long>(hits)) - 1, T());
+            const int token = first + at.x * kThreads * kN + at.y;
+            // (at hand in L1; a bit behind the row's end would be a fill's, below any cut)
+            if (slot < kList) sel.list[slot] = packed(static_cast<float>(logits[token]), token);
         }
     }
     griddep_launch_dependents();  // the join's CTAs need not take room before
@@ -392,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
 // ---- join -----------------------------------------------------------------------
 
 // CTA (group, share): every share of a group finds its best n candidates, and
-// writes the results of every gridDim.y-th. Candidates are sifted by a cut as the
+// copies its part of the histories. Candidates are sifted by a cut as the
 // scan's, by scores in fp32 with room for their rounding; what is left is ranked
 // by scores in pairs.
 __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
@@ -408,12 +427,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
     const int row0 = group * p.beams;
     griddep_wait();
     for (int k = warp; k < p.beams; k += kWarps) {
-        const int row = row0 + k, parts = p.chunks * kWarps;
-        const float2* stats = p.stats + static_cast<size_t>(row) * parts;
-        constexpr int kHeld = 4;  // of the parts, a lane; the rest are read twice
-        float2 held[kHeld];
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) held[i] = lane + 32 * i < parts ? stats[lane + 32 * i] : make_float2(-INFINITY, 0.f);
+        const int row = row0 + k;
+        const float2* stats = p.stats + static_cast<size_t>(row) * p.chunks;
+        const float2 first = lane < p.chunks ? stats[lane] : make_float2(-INFINITY, 0.f);
         const float s = p.scores[row];
         const bool ended = row_done(p, row);
         if (lane == 0) {
@@ -423,20 +439,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
             less[k] = -INFINITY;
         }
         if (ended || !(s > -INFINITY)) continue;
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) top = fmaxf(top, held[i].x);
-        for (int i = lane + 32 * kHeld; i < parts; i += 32) top = fmaxf(top, stats[i].x);
+        float top = first.x;
+        for (int i = lane + 32; i < p.chunks; i += 32) top = fmaxf(top, stats[i].x);
         top = unordered(__reduce_max_sync(0xffffffffu, ordered(top)));
-        // a part's sum counts from its largest logit, times the scan's fp32 log2(e)
         const bool large = fabsf(top * kLog2e) == INFINITY;
-        auto scaled = [&](float2 s) {
-            return s.y * exp2f(large ? (s.x - top) * kLog2e : __fmul_rn(s.x, kLog2e) - __fmul_rn(top, kLog2e));
-        };
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) sum += lane + 32 * i < parts ? scaled(held[i]) : 0.f;
-        for (int i = lane + 32 * kHeld; i < parts; i += 32) sum += scaled(stats[i]);
+        float sum = lane < p.chunks ? scaled(first, top) : 0.f;
+        for (int i = lane + 32; i < p.chunks; i += 32) sum += scaled(stats[i], top);
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (lane == 0) {
@@ -481,10 +489,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
     float held[kHeld];
     float best = -INFINITY;
 #pragma unroll
-    for (int u0 = 0; u0 < kHeld; u0 += 8) {
+    for (int u0 = 0; u0 < kHeld; u0 += 16) {
         if (u0 * kThreads >= items) break;
 #pragma unroll
-        for (int u = u0; u < u0 + 8; ++u) {
+        for (int u = u0; u < u0 + 16; ++u) {
             held[u] = index(u) < items ? rough(index(u)) : -INFINITY;
             best = fmaxf(best, held[u]);  // passes over NaN
         }
@@ -536,34 +544,46 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
             won_at[rank] = at;
         });
     __syncthreads();
-    // a warp a result
-    for (int j = blockIdx.y * kWarps + warp; j < p.n; j += gridDim.y * kWarps) {
-        const int at = won_at[j];
+    __shared__ int from[kMaxCandidates], length[kMaxCandidates];  // of the histories
+    if (threadIdx.x < p.n) {
+        const int j = threadIdx.x, at = won_at[j];
         const bool some = at >= 0;
         const int k = some ? at / p.vocab : -1, token = some ? at - k * p.vocab : -1;
         const int row = row0 + max(k, 0);
         const bool ended = some && done[k];
         const size_t out = static_cast<size_t>(group) * p.n + j;
-        int length = 0;
+        int held = 0;
+        bool grows = false;
         if (some && p.lengths) {
             const int given = p.lengths[row];
-            length = min(max(given, 0), p.max_length);
-            if ((given != length || (!ended && length == p.max_length)) && p.err && lane == 0) atomicOr(p.err, PKV_DEVERR_CONTEXT);
+            held = min(max(given, 0), p.max_length);
+            grows = !ended && held < p.max_length;
+            if ((given != held || (!ended && !grows)) && p.err) atomicOr(p.err, PKV_DEVERR_CONTEXT);
         }
-        const bool grows = some && !ended && length < p.max_length;
-        if (lane == 0) {
+        from[j] = row;
+        length[j] = held;
+        if (blockIdx.y == 0) {
             p.scores_out[out] = won_score[j];
             p.tokens_out[out] = token;
             p.parents_out[out] = k;
             p.finished_out[out] = ended || (some && token == p.eos);
-            if (p.lengths) p.lengths_out[out] = length + (grows ? 1 : 0);
-            if (p.lengths && grows) p.history_out[out * p.max_length + length] = token;
+            if (p.lengths) p.lengths_out[out] = held + (grows ? 1 : 0);
+            if (grows) p.history_out[out * p.max_length + held] = token;
         }
-        if (p.lengths) {
-            const int32_t* src = p.history + static_cast<size_t>(row) * p.max_length;
-            int32_t* dst = p.history_out + out * p.max_length;
-#pragma unroll 8
-            for (int i = lane; i < length; i += 32) dst[i] = src[i];
+    }
+    if (!p.lengths) return;
+    __syncthreads();
+    for (int j = blockIdx.y; j < p.n; j += gridDim.y) {
+        const int32_t* src = p.history + static_cast<size_t>(from[j]) * p.max_length;
+        int32_t* dst = p.history_out + (static_cast<size_t>(group) * p.n + j) * p.max_length;
+        for (int i0 = threadIdx.x; i0 < length[j]; i0 += 4 * kThreads) {
+            int32_t v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i0 + u * kThreads < length[j]) v[u] = src[i0 + u * kThreads];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i0 + u * kThreads < length[j]) dst[i0 + u * kThreads] = v[u];
         }
     }
 }
@@ -608,7 +628,7 @@ pkv_status check(int groups, int beams, int candidates, int vocab) {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t workspace_for(long long rows, int candidates, int chunks) {
-    return align256(static_cast<size_t>(rows) * chunks * kWarps * sizeof(float2)) +
+    return align256(static_cast<size_t>(rows) * chunks * sizeof(float2)) +
            align256(static_cast<size_t>(rows) * chunks * candidates * sizeof(uint2));
 }
 
@@ -661,7 +681,7 @@ pkv_status pkv_beam_select(const void* logits, int64_t row_stride, int logits_by
     p.history_out = history_out;
     p.stats = static_cast<float2*>(workspace);
     p.lists = reinterpret_cast<uint2*>(static_cast<uint8_t*>(workspace) +
-                                       beam::align256(static_cast<size_t>(rows) * p.chunks * beam::kWarps * sizeof(float2)));
+                                       beam::align256(static_cast<size_t>(rows) * p.chunks * sizeof(float2)));
     p.err = device_error;
     p.eos = eos;
     p.beams = num_beams;
@@ -674,7 +694,7 @@ pkv_status pkv_beam_select(const void* logits, int64_t row_stride, int logits_by
     if (e == cudaSuccess) {
         // launched early: it waits for the scan before it reads anything
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(num_groups, static_cast<unsigned>(std::max(1, std::min((num_candidates + beam::kWarps - 1) / beam::kWarps, 152 / num_groups))));
+        cfg.gridDim = dim3(num_groups, static_cast<unsigned>(std::max(1, std::min(num_candidates, beam::kWantCtas / num_groups))));
         cfg.blockDim = dim3(beam::kThreads);
         cfg.stream = as_stream(stream);
         cudaLaunchAttribute attr[1];
