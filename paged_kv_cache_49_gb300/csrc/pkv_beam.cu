@@ -26,6 +26,7 @@
 
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
+#include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace beam {
@@ -74,24 +75,6 @@ __device__ __forceinline__ float scaled(float2 s, float top) {
     if (!(s.x > -INFINITY)) return s.y;
     const float a = __fmul_rn(s.x, kLog2e), b = __fmul_rn(top, kLog2e);
     return s.y * exp2f(fabsf(b) < INFINITY ? a - b : (s.x - top) * kLog2e);
-}
-
-// Pairs of fp32 numbers in one register pair, one instruction for both.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
 }
 
 // Numbers that compare as unsigned integers as the keys do as floats (-0 as 0).

@@ -9,6 +9,7 @@
 #include "pkv_int4.cuh"
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
+#include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace kv4 {
@@ -24,81 +25,95 @@ __device__ __forceinline__ uint4 ld_streaming(const uint4* p) {
                  : "l"(p));
     return v;
 }
+// 1 / x to the last bit but one.
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Of both halves; NaN where either is.
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
 
 struct Append {
     const uint4* k;
     const uint4* v;
-    int64_t k_stride, v_stride;  // of a token, in 8-value vectors
+    uint32_t k_stride, v_stride;  // of a token, in 8-value vectors
     const int64_t* slots;
-    long long tokens;
-    int hkv, bt_shift;
+    uint32_t tokens, magic;  // (i * magic) >> (32 + magic_shift) is i / hkv
+    int magic_shift, hkv, bt_shift;
     long long slot_limit;
     uint8_t* cache;
     uint32_t* err;
 };
 
-// A row's 8 values of this lane as codes (value e in bits 4 e .. + 3), and its
-// group's scale and minimum, over which the group's kLanes lanes agree.
-//
-// Rounding is by adding 1.5 * 2^23, whose last bit counts ones: t / s by the
-// reciprocal and one rounding. That is off by less than 2^-18 of a step within
-// the range, so where the quotient is not near a half it rounds as the true one
-// does; near one (one lane in 3,000 values) the division itself decides.
+// The codes of this lane's 8 values (value e in bits 4 e .. + 3) by the
+// definition, one division and one rounding each.
+__device__ __noinline__ uint32_t codes_by_division(uint4 raw, float m, float s) {
+    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t word = 0;
+    for (int e = 0; e < 8; ++e) {
+        const float x = __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+        word |= static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x, m), s)), 0.f), 15.f)) << (4 * e);
+    }
+    return word;
+}
+
+// A row's 8 values of this lane as codes, and its group's scale and minimum, over
+// which the group's kLanes lanes agree: what bounds the append is the number of
+// its operations (27 a value as first written, 41 us for 16,411 tokens of 8
+// heads; 12 as below), so
+//  * least and greatest value go through the reduction as one pair of bf16
+//    numbers, the greatest negated, and NaN goes with them;
+//  * (hi - lo) / 15 is by Markstein's correction of a product with 1 / 15, which
+//    rounds as the division does;
+//  * t / s is t by the reciprocal, rounded by adding 1.5 * 2^23, whose last bit
+//    counts ones, and the codes are collected from the sums' bits. That is off by
+//    less than 2^-18 of a step, so where the quotient is not near a half it
+//    rounds as the true one does; near one (one lane in 2,000), or where
+//    saturated values leave the range, the division itself decides.
 template <int kLanes>
 __device__ __forceinline__ uint32_t quantise(const uint4& raw, __half& s, __half& m) {
-    constexpr float kOne = 12582912.f;
-    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t lo2 = u[0], hi2 = u[0], nan = 0;
+    constexpr float kOne = 12582912.f;  // 0x4b400000
+    const uint32_t lo2 = min_bf16x2(min_bf16x2(raw.x, raw.y), min_bf16x2(raw.z, raw.w));
+    const uint32_t hi2 = max_bf16x2(max_bf16x2(raw.x, raw.y), max_bf16x2(raw.z, raw.w)) ^ 0x80008000u;
+    uint32_t range = min_bf16x2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));  // (lo, -hi)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        lo2 = min_bf16x2(lo2, u[i]);
-        hi2 = max_bf16x2(hi2, u[i]);
-        // a NaN's magnitude is above 0x7f80: its sum with 0x7f carries into the sign's place
-        nan |= ((u[i] & 0x7fff7fffu) + 0x007f007fu) & 0x80008000u;
-    }
-    float lo = fminf(bf16_lo(lo2), bf16_hi(lo2)), hi = fmaxf(bf16_lo(hi2), bf16_hi(hi2));
-#pragma unroll
-    for (int d = kLanes / 2; d; d >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-    }
-    const unsigned lane = threadIdx.x & 31, group = ((1u << kLanes) - 1) << (lane / kLanes * kLanes);
-    const bool none = (__ballot_sync(0xffffffffu, nan != 0) & group) != 0;
-    lo = fminf(fmaxf(lo, -kHalfMax), kHalfMax);
-    hi = fminf(fmaxf(hi, -kHalfMax), kHalfMax);
+    for (int d = kLanes / 2; d; d >>= 1) range = min_bf16x2(range, __shfl_xor_sync(0xffffffffu, range, d));
+    const float least = bf16_lo(range), most = -bf16_hi(range);
+    const float lo = fminf(fmaxf(least, -kHalfMax), kHalfMax), span = fminf(fmaxf(most, -kHalfMax), kHalfMax) - lo;
+    const float third = span * (1.f / 15.f);
     m = __float2half_rn(lo);
-    s = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+    s = __float2half_rn(__fmaf_rn(__fmaf_rn(-15.f, third, span), 1.f / 15.f, third));
     const float mf = __half2float(m), sf = __half2float(s);
-    const float r = sf > 0.f ? __frcp_rn(sf) : 0.f;
+    const float r = sf > 0.f ? rcp(sf) : 0.f;
+    const uint64_t less = pair(-mf, -mf), by = pair(r, r), one = pair(kOne, kOne), minus = pair(-1.f, -1.f);
+    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
     uint32_t word = 0;
     float off = 0.f;  // the largest distance from a whole number
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float t = __fsub_rn(e & 1 ? bf16_hi(u[e / 2]) : bf16_lo(u[e / 2]), mf);
-        const float y = __fmaf_rn(t, r, kOne);
-        off = fmaxf(off, fabsf(__fmaf_rn(t, r, -__fsub_rn(y, kOne))));
-        word |= static_cast<uint32_t>(__vimin_s32_relu(__float_as_int(y) - __float_as_int(kOne), 15)) << (4 * e);
+    for (int i = 3; i >= 0; --i) {
+        const uint64_t t = add2(pair(bf16_lo(u[i]), bf16_hi(u[i])), less);
+        const uint64_t y = fma2(t, by, one);
+        float y0, y1, d0, d1;
+        unpair(y, y0, y1);
+        unpair(fma2(t, by, fma2(y, minus, one)), d0, d1);
+        off = fmaxf(off, fmaxf(fabsf(d0), fabsf(d1)));
+        word = word * 256u + __float_as_uint(y1) * 16u + __float_as_uint(y0);
     }
-    if (off > 0.5f - 0x1p-14f) {
-        word = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float t = __fsub_rn(e & 1 ? bf16_hi(u[e / 2]) : bf16_lo(u[e / 2]), mf);
-            word |= static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(t, sf)), 0.f), 15.f)) << (4 * e);
-        }
-    }
+    word -= 0x3f400000u;  // what the sums' 0x4b400000 are, at each of eight places, modulo 2^32
+    const bool inside = (least - mf) * r > -0.25f && (most - mf) * r < 15.25f;
     if (!(sf > 0.f)) word = 0;
-    if (none) {
+    else if (off > 0.5f - 0x1p-14f || !inside) word = codes_by_division(raw, mf, sf);
+    if (least != least) {  // a NaN
         s = m = __ushort_as_half(0x7fff);
         word = 0;
     }
@@ -109,63 +124,64 @@ __device__ __forceinline__ uint32_t quantise(const uint4& raw, __half& s, __half
 // both a lane, so four loads in flight. Tokens next to one another in a unit
 // (a prompt's) share the 4-byte words of its values' codes and parameters.
 template <int kGroups>
-__global__ void __launch_bounds__(kThreads) append_kernel(const Append p) {
+__global__ void __launch_bounds__(kThreads, 5) append_kernel(const Append p) {
     using U = Unit<kGroups>;
     constexpr int kLanes = 16 / kGroups;
     const int part = threadIdx.x & 15, w = part >> 2, c = part & 3, g = part / kLanes;
-    const long long i = static_cast<long long>(blockIdx.x) * (kThreads / 16) + threadIdx.x / 16;
-    const long long pr = i / p.hkv;
+    const uint32_t i = blockIdx.x * (kThreads / 16) + threadIdx.x / 16;
+    const uint32_t pr = p.magic ? __umulhi(i, p.magic) >> p.magic_shift : i;  // i / hkv
     const int head = static_cast<int>(i - pr * p.hkv);
-    const long long tok = 2 * pr;
+    const uint32_t tok = 2 * pr;
     uint4 raw[2][2] = {};  // [key, value][token]
-    long long slot[2] = {-1, -1};
+    int slot[2] = {-1, -1};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if (tok + j >= p.tokens) continue;
-        raw[0][j] = ld_streaming(p.k + (tok + j) * p.k_stride + head * 16 + part);
-        raw[1][j] = ld_streaming(p.v + (tok + j) * p.v_stride + head * 16 + part);
-        slot[j] = __ldg(p.slots + tok + j);
+        raw[0][j] = ld_streaming(p.k + static_cast<uint64_t>(tok + j) * p.k_stride + (head * 16 + part));
+        raw[1][j] = ld_streaming(p.v + static_cast<uint64_t>(tok + j) * p.v_stride + (head * 16 + part));
+        const long long at = __ldg(p.slots + tok + j);
+        if (at >= p.slot_limit && p.err && part == 0 && head == 0) atomicOr(p.err, PKV_DEVERR_SLOT);
+        slot[j] = at >= 0 && at < p.slot_limit ? static_cast<int>(at) : -1;
     }
-    __half s[2][2], m[2][2];
-    uint32_t word[2][2];
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) word[kv][j] = quantise<kLanes>(raw[kv][j], s[kv][j], m[kv][j]);
-    uint8_t* unit[2];
-    int t[2];
+    auto unit_of = [&](int at) {
+        const int unit = (((at >> p.bt_shift) * p.hkv + head) << (p.bt_shift - 3)) + ((at & ((1 << p.bt_shift) - 1)) >> 3);
+        return p.cache + static_cast<size_t>(unit) * U::kBytes;
+    };
+    const bool first = part % kLanes == 0;
+    __half s[2], m[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        if (slot[j] >= p.slot_limit) {
-            if (p.err && part == 0 && head == 0) atomicOr(p.err, PKV_DEVERR_SLOT);
-            slot[j] = -1;
-        }
-        const long long blk = slot[j] >> p.bt_shift;
-        const int pos = static_cast<int>(slot[j] & ((1 << p.bt_shift) - 1));
-        t[j] = pos & 7;
-        unit[j] = p.cache + (((blk * p.hkv + head) << (p.bt_shift - 3)) + (pos >> 3)) * U::kBytes;
+        const uint32_t word = quantise<kLanes>(raw[0][j], s[0], m[0]);
         if (slot[j] < 0) continue;
-        *reinterpret_cast<uint32_t*>(unit[j] + key_word(t[j], w, c)) = word[0][j];
-        if (part % kLanes == 0)
-            *reinterpret_cast<__half2*>(unit[j] + U::kKeyParams + (t[j] * kGroups + g) * 4) = __halves2half2(s[0][j], m[0][j]);
+        uint8_t* unit = unit_of(slot[j]);
+        const int t = slot[j] & 7;
+        *reinterpret_cast<uint32_t*>(unit + key_word(t, w, c)) = word;
+        if (first) *reinterpret_cast<__half2*>(unit + U::kKeyParams + (t * kGroups + g) * 4) = __halves2half2(s[0], m[0]);
     }
+    uint32_t word[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) word[j] = quantise<kLanes>(raw[1][j], s[j], m[j]);
     if (slot[0] >= 0 && slot[1] == slot[0] + 1 && (slot[0] & 1) == 0) {
-        *reinterpret_cast<uint32_t*>(unit[0] + value_piece(t[0], w, 2 * c)) = __byte_perm(word[1][0], word[1][1], 0x5410);
-        *reinterpret_cast<uint32_t*>(unit[0] + value_piece(t[0], w, 2 * c + 1)) = __byte_perm(word[1][0], word[1][1], 0x7632);
-        if (part % kLanes == 0) {
-            *reinterpret_cast<__half2*>(unit[0] + U::kValueScales + (g * kUnit + t[0]) * 2) = __halves2half2(s[1][0], s[1][1]);
-            *reinterpret_cast<__half2*>(unit[0] + U::kValueMins + (g * kUnit + t[0]) * 2) = __halves2half2(m[1][0], m[1][1]);
+        uint8_t* unit = unit_of(slot[0]);
+        const int t = slot[0] & 7;
+        *reinterpret_cast<uint32_t*>(unit + value_piece(t, w, 2 * c)) = __byte_perm(word[0], word[1], 0x5410);
+        *reinterpret_cast<uint32_t*>(unit + value_piece(t, w, 2 * c + 1)) = __byte_perm(word[0], word[1], 0x7632);
+        if (first) {
+            *reinterpret_cast<__half2*>(unit + U::kValueScales + (g * kUnit + t) * 2) = __halves2half2(s[0], s[1]);
+            *reinterpret_cast<__half2*>(unit + U::kValueMins + (g * kUnit + t) * 2) = __halves2half2(m[0], m[1]);
         }
         return;
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if (slot[j] < 0) continue;
-        *reinterpret_cast<uint16_t*>(unit[j] + value_piece(t[j], w, 2 * c)) = static_cast<uint16_t>(word[1][j]);
-        *reinterpret_cast<uint16_t*>(unit[j] + value_piece(t[j], w, 2 * c + 1)) = static_cast<uint16_t>(word[1][j] >> 16);
-        if (part % kLanes == 0) {
-            *reinterpret_cast<__half*>(unit[j] + U::kValueScales + (g * kUnit + t[j]) * 2) = s[1][j];
-            *reinterpret_cast<__half*>(unit[j] + U::kValueMins + (g * kUnit + t[j]) * 2) = m[1][j];
+        uint8_t* unit = unit_of(slot[j]);
+        const int t = slot[j] & 7;
+        *reinterpret_cast<uint16_t*>(unit + value_piece(t, w, 2 * c)) = static_cast<uint16_t>(word[j]);
+        *reinterpret_cast<uint16_t*>(unit + value_piece(t, w, 2 * c + 1)) = static_cast<uint16_t>(word[j] >> 16);
+        if (first) {
+            *reinterpret_cast<__half*>(unit + U::kValueScales + (g * kUnit + t) * 2) = s[j];
+            *reinterpret_cast<__half*>(unit + U::kValueMins + (g * kUnit + t) * 2) = m[j];
         }
     }
 }
@@ -300,18 +316,23 @@ pkv_status pkv_append_int4(const void* k, int64_t k_stride, const void* v, int64
     kv4::Append p = {};
     p.k = static_cast<const uint4*>(k);
     p.v = static_cast<const uint4*>(v);
-    p.k_stride = k_stride / 8;
-    p.v_stride = v_stride / 8;
+    p.k_stride = static_cast<uint32_t>(k_stride / 8);
+    p.v_stride = static_cast<uint32_t>(v_stride / 8);
     p.slots = slot_mapping;
-    p.tokens = num_tokens;
+    p.tokens = static_cast<uint32_t>(num_tokens);
     p.hkv = num_kv_heads;
     p.bt_shift = block_tokens == 8 ? 3 : block_tokens == 16 ? 4 : block_tokens == 32 ? 5 : 6;
     p.slot_limit = static_cast<long long>(num_blocks) * block_tokens;
     p.cache = static_cast<uint8_t*>(cache);
     p.err = device_error;
     const long long pairs = (static_cast<long long>(num_tokens) + 1) / 2 * num_kv_heads;
+    if (pairs >= (1ll << 31) - kv4::kThreads) return PKV_ERANGE;
+    // i / hkv for i < 2^31: with 2^shift < hkv <= 2^(shift + 1), the magic number
+    // ceil(2^(32 + shift) / hkv) is off by less than one part in 2^31 (0: hkv is 1; Granlund
+    // and Montgomery's division by an invariant)
+    while ((2ll << p.magic_shift) < num_kv_heads) ++p.magic_shift;
+    p.magic = static_cast<uint32_t>(((1ull << (32 + p.magic_shift)) + num_kv_heads - 1) / num_kv_heads);
     const long long blocks = (pairs + kv4::kThreads / 16 - 1) / (kv4::kThreads / 16);
-    if (blocks > INT32_MAX) return PKV_ERANGE;
     const int grid = static_cast<int>(blocks);
     switch (kv4::groups_of(group_dims)) {
         case 1: kv4::append_kernel<1><<<grid, kv4::kThreads, 0, as_stream(stream)>>>(p); break;
