@@ -55,14 +55,26 @@ struct Append {
     uint32_t* err;
 };
 
-// The codes of this lane's 8 values (value e in bits 4 e .. + 3) by the
-// definition, one division and one rounding each.
-__device__ __noinline__ uint32_t codes_by_division(uint4 raw, float m, float s) {
+constexpr float kNear = 0.5f - 0x1p-14f;
+
+// The codes (value e in bits 4 e .. + 3) of which some may be off, by the
+// definition -- one division and one rounding -- where the quotient by the
+// reciprocal r is near a half. One that leaves the range spoils the others' places.
+__device__ __noinline__ uint32_t corrected(uint32_t word, uint4 raw, float m, float s, float r) {
     const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t word = 0;
+    unsigned which = 0;
+#pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float x = __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
-        word |= static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x, m), s)), 0.f), 15.f)) << (4 * e);
+        const float q = __fsub_rn(e & 1 ? bf16_hi(u[e / 2]) : bf16_lo(u[e / 2]), m) * r;
+        if (!(fabsf(q - rintf(q)) < kNear)) which |= 1u << e;
+        if (!(q > -0.25f && q < 15.25f)) which |= 0xffu;
+    }
+    for (; which; which &= which - 1) {
+        const int e = __ffs(static_cast<int>(which)) - 1;
+        const uint32_t pair = e < 4 ? (e < 2 ? u[0] : u[1]) : (e < 6 ? u[2] : u[3]);
+        const float t = __fsub_rn(e & 1 ? bf16_hi(pair) : bf16_lo(pair), m);
+        const uint32_t code = static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(t, s)), 0.f), 15.f));
+        word = (word & ~(15u << (4 * e))) | code << (4 * e);
     }
     return word;
 }
@@ -78,8 +90,9 @@ __device__ __noinline__ uint32_t codes_by_division(uint4 raw, float m, float s) 
 //  * t / s is t by the reciprocal, rounded by adding 1.5 * 2^23, whose last bit
 //    counts ones, and the codes are collected from the sums' bits. That is off by
 //    less than 2^-18 of a step, so where the quotient is not near a half it
-//    rounds as the true one does; near one (one lane in 2,000), or where
-//    saturated values leave the range, the division itself decides.
+//    rounds as the true one does; near one (one lane in 170: bf16 values
+//    lie on few points), or where saturated values leave the range, the division
+//    itself decides.
 template <int kLanes>
 __device__ __forceinline__ uint32_t quantise(const uint4& raw, __half& s, __half& m) {
     constexpr float kOne = 12582912.f;  // 0x4b400000
@@ -112,7 +125,7 @@ __device__ __forceinline__ uint32_t quantise(const uint4& raw, __half& s, __half
     word -= 0x3f400000u;  // what the sums' 0x4b400000 are, at each of eight places, modulo 2^32
     const bool inside = (least - mf) * r > -0.25f && (most - mf) * r < 15.25f;
     if (!(sf > 0.f)) word = 0;
-    else if (off > 0.5f - 0x1p-14f || !inside) word = codes_by_division(raw, mf, sf);
+    else if (!(off < kNear) || !inside) word = corrected(word, raw, mf, sf, r);
     if (least != least) {  // a NaN
         s = m = __ushort_as_half(0x7fff);
         word = 0;
