@@ -17,37 +17,51 @@ using KernelFn = void (*)(Decode);
 
 KernelFn kernel_for(int groups) { return groups == 1 ? decode_kernel<1> : groups == 2 ? decode_kernel<2> : decode_kernel<4>; }
 
-size_t smem_for(int groups, int num_seqs) {
-    return groups == 1 ? Smem<1>::bytes(num_seqs) : groups == 2 ? Smem<2>::bytes(num_seqs) : Smem<4>::bytes(num_seqs);
+size_t smem_for(int groups, int num_seqs, int slots) {
+    return groups == 1 ? Smem<1>::bytes(num_seqs, slots) : groups == 2 ? Smem<2>::bytes(num_seqs, slots) : Smem<4>::bytes(num_seqs, slots);
 }
 
-// CTAs that fit at once on the current device; 0 on error. Kept per device,
-// group count and shared memory size.
-int resident_ctas(int groups, int num_seqs) {
-    struct Entry {
-        int dev, groups;
-        size_t smem;
-        int ctas;
-    };
+// A launch's shape: every CTA that fits at once, with room for the states of two
+// pieces, or of one where that keeps two CTAs on an SM.
+struct Shape {
+    int dev = -1, groups = 0, num_seqs = 0;
+    int ctas = 0, slots = 0;  // ctas 0 on error
+    size_t smem = 0;
+};
+
+// Kept per device, group count and number of sequences.
+Shape shape_for(int groups, int num_seqs) {
     static std::mutex mu;
-    static std::vector<Entry> cache;
-    int dev = 0, sms = 0, per_sm = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    const size_t smem = smem_for(groups, num_seqs);
+    static std::vector<Shape> cache;
+    Shape s;
+    if (cudaGetDevice(&s.dev) != cudaSuccess) return s;
+    s.groups = groups;
+    s.num_seqs = (num_seqs + 63) / 64 * 64;
     std::lock_guard<std::mutex> lock(mu);
-    for (const Entry& e : cache)
-        if (e.dev == dev && e.groups == groups && e.smem == smem) return e.ctas;
+    for (const Shape& e : cache)
+        if (e.dev == s.dev && e.groups == groups && e.num_seqs == s.num_seqs) return e;
     const KernelFn fn = kernel_for(groups);
+    int sms = 0, best = 0;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem_for(groups, PKV_ATTN_MAX_SEQS)));
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, smem);
+                                         static_cast<int>(smem_for(groups, PKV_ATTN_MAX_SEQS, 2)));
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, s.dev);
+    for (int slots = 2; slots >= 1 && e == cudaSuccess; --slots) {
+        int per_sm = 0;
+        const size_t smem = smem_for(groups, s.num_seqs, slots);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, smem);
+        if (e == cudaSuccess && per_sm > best) {
+            best = per_sm;
+            s.slots = slots;
+            s.smem = smem;
+        }
+    }
     if (e != cudaSuccess) {
         record_cuda_error(e);
-        return 0;
+        return s;
     }
-    cache.push_back({dev, groups, smem, std::min(sms * per_sm, kMaxCtas)});
-    return cache.back().ctas;
+    s.ctas = std::min(sms * best, kMaxCtas);
+    cache.push_back(s);
+    return s;
 }
 
 }  // namespace kv4
@@ -76,11 +90,11 @@ extern "C" pkv_status pkv_attn_decode_int4(const void* q, const void* cache, con
         return PKV_ERANGE;
     if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return PKV_EINVAL;
-    const int resident = kv4::resident_ctas(groups, num_seqs);
-    if (resident < 1) return PKV_ECUDA;
+    const kv4::Shape shape = kv4::shape_for(groups, num_seqs);
+    if (shape.ctas < 1) return PKV_ECUDA;
     // No more CTAs than the tables can hold work for: a run's cost each.
     int grid = num_ctas > 0 ? num_ctas
-                            : static_cast<int>(std::max<long long>(1, std::min<long long>(resident, cost / (kv4::kRunCost + 1))));
+                            : static_cast<int>(std::max<long long>(1, std::min<long long>(shape.ctas, cost / (kv4::kRunCost + 1))));
     if (workspace_bytes < attn::workspace_bytes(1)) return PKV_EINVAL;
     const long long fit = static_cast<long long>((workspace_bytes - attn::kWsFixed) / attn::kWsPerCta);
     if (grid > fit) {
@@ -104,10 +118,11 @@ extern "C" pkv_status pkv_attn_decode_int4(const void* q, const void* cache, con
     p.scale_log2 = scale * 1.4426950408889634f;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.err = reinterpret_cast<uint32_t*>(ws);
-    p.counters = reinterpret_cast<unsigned long long*>(ws + attn::kWsHeader);
+    p.counters = reinterpret_cast<int*>(ws + attn::kWsHeader);
     p.group_counters = p.counters + kv4::kMaxCtas;
     p.partials = reinterpret_cast<float*>(ws + attn::kWsFixed);
-    kv4::kernel_for(groups)<<<grid, kv4::kThreads, kv4::smem_for(groups, num_seqs), as_stream(stream)>>>(p);
+    p.slots = shape.slots;
+    kv4::kernel_for(groups)<<<grid, kv4::kThreads, shape.smem, as_stream(stream)>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) {
         record_cuda_error(e);

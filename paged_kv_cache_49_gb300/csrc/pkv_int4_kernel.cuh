@@ -27,11 +27,12 @@
 //
 // Work: as the bf16 cache's decode kernel (pkv_decode_kernel.cuh): all
 // (sequence, KV head) runs laid end to end in tiles of kTile tokens, cut into
-// gridDim.x ranges of equal cost. A producer warp copies tiles (one bulk copy a
-// block) into a ring; consumer warp i takes every kWarps-th. At the end of a
-// piece the warps leave their states in shared memory and each combines the
-// states of its own heads; pieces of a run that is cut among CTAs are combined
-// by whichever CTA finishes last, head by head.
+// gridDim.x ranges of equal cost. A producer warp copies tiles
+// into a ring; consumer warp i takes every kWarps-th, whatever piece it
+// belongs to. A helper warp goes with them, so that none waits for another: it
+// has the next piece's queries ready as the products take them, and combines the
+// states that the consumers leave of a piece; pieces of a run that is cut among
+// CTAs are combined by whichever helper finishes last.
 #pragma once
 
 #include "pkv_decode_kernel.cuh"
@@ -45,30 +46,34 @@ constexpr int kTile = 64;   // tokens
 constexpr int kWarps = 4;   // consumers
 constexpr int kStages = 8;
 static_assert(kStages % kWarps == 0, "each stage is always the same warp's");
-constexpr int kConsumers = kWarps * 32;
-constexpr int kThreads = kConsumers + 32;
+constexpr int kProducers = 2;  // producer i copies every tile whose place in the stream is i modulo their number
+constexpr int kHelper = kWarps + kProducers;
+constexpr int kThreads = (kHelper + 1) * 32;
+static_assert(kStages % kProducers == 0, "each stage is always the same producer's");
 constexpr int kSubs = kTile / 16;
 // Work partition: what a run costs beyond its tiles, in tiles.
 constexpr int kRunCost = 3;
 // Runs of more pieces than this are combined in two levels.
 constexpr int kMergeGroup = 16;
-// Counters of a launch, 64 bits with one byte a head, in the workspace's region
-// of counters: per CTA one for the cut run, and one for the group of its pieces,
-// whose first piece is the CTA's (at most one: the last run of its range).
-constexpr int kMaxCtas = static_cast<int>(attn::kWsCounterBytes / 16);
-static_assert(kMaxCtas / kMergeGroup < 256 && kMergeGroup < 256, "a count fits a byte");
+constexpr int kMaxCtas = attn::kMaxCtas;
 
 constexpr int kORow = attn::kORow;
 constexpr int kStateFloats = kWarps * kMaxG * kORow;  // output, max and sum of every warp's heads
+constexpr int kQSlots = 2;
 
+// Shared memory: the ring, queries, states of one or two pieces (one where two
+// would keep a second CTA off the SM), barriers, the plan.
 template <int kGroups>
 struct Smem {
     static constexpr int kStage = kTile / kUnit * Unit<kGroups>::kBytes;
-    static constexpr int kStates = kStages * kStage;
-    static constexpr int kBars = kStates + 2 * kStateFloats * 4;
-    static constexpr int kMisc = kBars + 2 * kStages * 8;
-    static constexpr int kScan = kMisc + 64;
-    static constexpr size_t bytes(int num_seqs) { return 128 + kScan + 4 * static_cast<size_t>(num_seqs); }
+    static constexpr int kQueries = kStages * kStage;
+    static constexpr int kQBytes = (16 + 2 + 2 * kGroups) * 32 * 4;
+    static constexpr int kBars = kQueries + kQSlots * kQBytes;
+    static constexpr int kNumBars = 2 * kStages + 2 * kQSlots + 4;
+    static constexpr int kMisc = kBars + kNumBars * 8;
+    static constexpr int kStates = (kMisc + 64 + 15) / 16 * 16;
+    static __host__ __device__ constexpr int scan(int slots) { return kStates + slots * kStateFloats * 4; }
+    static constexpr size_t bytes(int num_seqs, int slots) { return 128 + scan(slots) + 4 * static_cast<size_t>(num_seqs); }
 };
 
 struct Decode {
@@ -80,10 +85,31 @@ struct Decode {
     int num_seqs, width, cap, hq, hkv, group, num_blocks, bt_shift;
     float scale_log2;
     uint32_t* err;
-    unsigned long long* counters;        // [kMaxCtas]
-    unsigned long long* group_counters;  // [kMaxCtas]
-    float* partials;                     // [grid][2][kMaxG][kORow]
+    int* counters;        // [kMaxCtas]: pieces counted of the cut run whose first piece is the CTA's
+    int* group_counters;  // [kMaxCtas]: likewise, of a group of its pieces
+    float* partials;      // [grid][2][kMaxG][kORow]
+    int slots;            // pieces whose states fit in shared memory
 };
+
+// True in one thread of the warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one = 0;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t@p mov.u32 %0, 1;\n\t}" : "+r"(one));
+    return one != 0;
+}
+
+// Products and transposes that the compiler may schedule among others.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
 
 __device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ uint32_t lds32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
@@ -158,6 +184,28 @@ struct Queries {
             for (int i = 0; i < kGroups; ++i) sum[i][h] = __shfl_sync(0xffffffffu, sums[i], lane) * 0x1p-24f;
         }
     }
+
+    // Into and out of shared memory, as the lanes hold them.
+    __device__ __forceinline__ void store(uint8_t* slot, int lane) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4*>(slot)[i * 32 + lane] = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
+        float2* rest = reinterpret_cast<float2*>(slot + 2048) + lane;
+        rest[0] = make_float2(factor[0], factor[1]);
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) rest[32 * (i + 1)] = make_float2(sum[i][0], sum[i][1]);
+    }
+    __device__ __forceinline__ void fetch(const uint8_t* slot, int lane) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 u = reinterpret_cast<const uint4*>(slot)[i * 32 + lane];
+            b[4 * i] = u.x, b[4 * i + 1] = u.y, b[4 * i + 2] = u.z, b[4 * i + 3] = u.w;
+        }
+        const float2* rest = reinterpret_cast<const float2*>(slot + 2048) + lane;
+        factor[0] = rest[0].x, factor[1] = rest[0].y;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) sum[i][0] = rest[32 * (i + 1)].x, sum[i][1] = rest[32 * (i + 1)].y;
+    }
 };
 
 // A warp's softmax state of a piece. Lane 4 r + c holds heads 2 c, 2 c + 1:
@@ -220,32 +268,35 @@ __device__ __forceinline__ void add_tile(uint8_t* tile, int valid, const Queries
     float x[kSubs][4];
 #pragma unroll
     for (int i = 0; i < kSubs; ++i) {
-        if (16 * i >= valid) {
-            x[i][0] = x[i][1] = x[i][2] = x[i][3] = -INFINITY;
-            continue;
-        }
         const uint8_t* u0 = tile + 2 * i * U::kBytes;
         const uint8_t* u1 = u0 + U::kBytes;
         const uint4 k0 = lds128(u0 + lane * 16), k1 = lds128(u1 + lane * 16);
-        float acc[kGroups][4];
+        // two chains of products a group (one for four groups)
+        constexpr int kChains = kGroups == 4 ? 1 : 2;
+        float acc[kGroups][kChains][4];
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+            for (int j = 0; j < kChains; ++j) acc[g][j][0] = acc[g][j][1] = acc[g][j][2] = acc[g][j][3] = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const uint32_t a = word(k0, w), b = word(k1, w), ah = a >> 8, bh = b >> 8;
-            float(&d)[4] = acc[w * kGroups / 4];
-            mma_f16_16816(d, a & kEven, b & kEven, a & kOdd, b & kOdd, q.b[4 * w], q.b[4 * w + 1]);
-            mma_f16_16816(d, ah & kEven, bh & kEven, ah & kOdd, bh & kOdd, q.b[4 * w + 2], q.b[4 * w + 3]);
+            const int g = w * kGroups / 4;
+            mma(acc[g][0], a & kEven, b & kEven, a & kOdd, b & kOdd, q.b[4 * w], q.b[4 * w + 1]);
+            mma(acc[g][kChains - 1], ah & kEven, bh & kEven, ah & kOdd, bh & kOdd, q.b[4 * w + 2], q.b[4 * w + 3]);
         }
         float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
             const uint32_t p0 = lds32(u0 + U::kKeyParams + (r * kGroups + g) * 4);
             const uint32_t p1 = lds32(u1 + U::kKeyParams + (r * kGroups + g) * 4);
+            float d[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) d[h] = kChains == 2 ? acc[g][0][h] + acc[g][kChains - 1][h] : acc[g][0][h];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                t[h] = fmaf(half_lo(p0), acc[g][h], fmaf(half_hi(p0), q.sum[g][h], t[h]));
-                t[h + 2] = fmaf(half_lo(p1), acc[g][h + 2], fmaf(half_hi(p1), q.sum[g][h], t[h + 2]));
+                t[h] = fmaf(half_lo(p0), d[h], fmaf(half_hi(p0), q.sum[g][h], t[h]));
+                t[h + 2] = fmaf(half_lo(p1), d[h + 2], fmaf(half_hi(p1), q.sum[g][h], t[h + 2]));
             }
         }
 #pragma unroll
@@ -299,11 +350,10 @@ __device__ __forceinline__ void add_tile(uint8_t* tile, int valid, const Queries
     // ---- values ----
 #pragma unroll
     for (int i = 0; i < kSubs; ++i) {
-        if (16 * i >= valid) break;
         const uint8_t* u0 = tile + 2 * i * U::kBytes;
         const uint8_t* u1 = u0 + U::kBytes;
-        const uint32_t p0 = movmatrix_trans(pack_f16x2(ex2(x[i][0] - base[0]), ex2(x[i][1] - base[1])));
-        const uint32_t p1 = movmatrix_trans(pack_f16x2(ex2(x[i][2] - base[0]), ex2(x[i][3] - base[1])));
+        const uint32_t p0 = transposed(pack_f16x2(ex2(x[i][0] - base[0]), ex2(x[i][1] - base[1])));
+        const uint32_t p1 = transposed(pack_f16x2(ex2(x[i][2] - base[0]), ex2(x[i][3] - base[1])));
         uint32_t m0 = 0, m1 = 0;
         if (r < kGroups) {
             m0 = lds32(u0 + U::kValueMins + (r * kUnit + 2 * c) * 2);
@@ -311,7 +361,7 @@ __device__ __forceinline__ void add_tile(uint8_t* tile, int valid, const Queries
         } else if (r == kGroups) {
             m0 = m1 = 0x3c003c00u;  // ones
         }
-        mma_f16_16816(st.e, m0, 0u, m1, 0u, p0, p1);
+        mma(st.e, m0, 0u, m1, 0u, p0, p1);
         const uint4 v0 = lds128(u0 + U::kValues + lane * 16), v1 = lds128(u1 + U::kValues + lane * 16);
         uint32_t b0 = 0, b1 = 0;
 #pragma unroll
@@ -322,48 +372,71 @@ __device__ __forceinline__ void add_tile(uint8_t* tile, int valid, const Queries
                 b1 = hmul2(p1, lds32(u1 + U::kValueScales + (g * kUnit + 2 * c) * 2));
             }
             const uint32_t a = word(v0, w), b = word(v1, w), ah = a >> 8, bh = b >> 8;
-            mma_f16_16816(st.o[2 * w], a & kEven, a & kOdd, b & kEven, b & kOdd, b0, b1);
-            mma_f16_16816(st.o[2 * w + 1], ah & kEven, ah & kOdd, bh & kEven, bh & kOdd, b0, b1);
+            mma(st.o[2 * w], a & kEven, a & kOdd, b & kEven, b & kOdd, b0, b1);
+            mma(st.o[2 * w + 1], ah & kEven, ah & kOdd, bh & kEven, bh & kOdd, b0, b1);
         }
     }
 }
 
-// `count` partial results of one head, `stride` CTAs apart from CTA `first` on,
-// combined: lane l owns dims 4 l .. + 3. A run's last CTA i1 has its piece in
-// slot 0, the others in slot 1.
-__device__ __forceinline__ float4 combine(const Decode& p, int first, int stride, int count, int i1, int h, int lane, float& M,
-                                          float& L) {
-    constexpr int kBatch = 8;  // loads in flight
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    M = -INFINITY;
-    L = 0.f;
-    for (int n = 0; n < count; n += kBatch) {
-        float m[kBatch], l[kBatch];
-        float4 o[kBatch];
+// A run's pieces leave their partial results with their CTAs: slot 0 for the
+// run's last, slot 1 for the others (a CTA holds at most two pieces of cut runs,
+// one that goes on in the next CTA and the end of one from an earlier CTA).
+__device__ __forceinline__ float* partial(const Decode& p, int cta, int last, int h) {
+    return p.partials + ((static_cast<size_t>(cta) * 2 + (cta == last ? 0 : 1)) * kMaxG + h) * kORow;
+}
+
+// `count` partial results, `stride` CTAs apart from CTA `first` on, combined by
+// head; emit(h, four dims from 4 lane on, max, sum). Four heads and four partial
+// results are on their way at a time.
+template <class Emit>
+__device__ __forceinline__ void combine(const Decode& p, int first, int stride, int count, int last, int lane, Emit emit) {
+#pragma unroll 1
+    for (int h0 = 0; h0 < p.group; h0 += 4) {
+        float M[4], L[4];
+        float4 acc[4];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int cta = first + (n + k) * stride;
-            const float* src = p.partials + ((static_cast<size_t>(cta) * 2 + (cta == i1 ? 0 : 1)) * kMaxG + h) * kORow;
-            const bool live = n + k < count;
-            m[k] = live ? __ldcg(src + kDim) : -INFINITY;
-            l[k] = live ? __ldcg(src + kDim + 1) : 0.f;
-            o[k] = live ? __ldcg(reinterpret_cast<const float4*>(src + 4 * lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int h = 0; h < 4; ++h) {
+            M[h] = -INFINITY;
+            L[h] = 0.f;
+            acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        float top = M;
+#pragma unroll 1
+        for (int n = 0; n < count; n += 4) {
+            float m[4][4], l[4][4];
+            float4 o[4][4];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) top = fmaxf(top, m[k]);
-        const float a = ex2(M - top);
-        acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
-        L *= a;
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const float f = ex2(m[k] - top);
-            L = fmaf(f, l[k], L);
-            acc = make_float4(fmaf(f, o[k].x, acc.x), fmaf(f, o[k].y, acc.y), fmaf(f, o[k].z, acc.z), fmaf(f, o[k].w, acc.w));
+                for (int h = 0; h < 4; ++h) {
+                    const bool live = n + k < count && h0 + h < p.group;
+                    const float* src = partial(p, live ? first + (n + k) * stride : first, last, live ? h0 + h : h0);
+                    m[k][h] = live ? __ldcg(src + kDim) : -INFINITY;
+                    l[k][h] = live ? __ldcg(src + kDim + 1) : 0.f;
+                    o[k][h] = live ? __ldcg(reinterpret_cast<const float4*>(src + 4 * lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                float top = M[h];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = fmaxf(top, m[k][h]);
+                const float a = ex2(M[h] - top);
+                acc[h] = make_float4(acc[h].x * a, acc[h].y * a, acc[h].z * a, acc[h].w * a);
+                L[h] *= a;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float f = ex2(m[k][h] - top);
+                    L[h] = fmaf(f, l[k][h], L[h]);
+                    acc[h] = make_float4(fmaf(f, o[k][h].x, acc[h].x), fmaf(f, o[k][h].y, acc[h].y), fmaf(f, o[k][h].z, acc[h].z),
+                                         fmaf(f, o[k][h].w, acc[h].w));
+                }
+                M[h] = top;
+            }
         }
-        M = top;
+        __syncwarp();  // every lane's reads, before what emit() may put in their place
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            if (h0 + h < p.group) emit(h0 + h, acc[h], M[h], L[h]);
     }
-    return acc;
 }
 
 __device__ __forceinline__ uint2 rounded(float4 o, float inv) {
@@ -378,17 +451,33 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
     uint8_t* smem = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = p.num_seqs, hkv = p.hkv;
-    int* scan = reinterpret_cast<int*>(smem + L::kScan);
+    int* scan = reinterpret_cast<int*>(smem + L::scan(p.slots));
     int* misc = reinterpret_cast<int*>(smem + L::kMisc);
     volatile int* abort_flag = misc;
     int* ends = misc + 1;
     int* unknown = misc + 3;  // the walk's first piece: left to its search
     int* warp_total = misc + 4;
+    static_assert(4 + kThreads / 32 <= 16, "the warps' totals fit");
     const uint32_t bar0 = smem_u32(smem + L::kBars);
     auto full_bar = [&](int i) { return bar0 + 8u * i; };
     auto empty_bar = [&](int i) { return bar0 + 8u * (kStages + i); };
+    auto qfull_bar = [&](int i) { return bar0 + 8u * (2 * kStages + i); };
+    auto qempty_bar = [&](int i) { return bar0 + 8u * (2 * kStages + kQSlots + i); };
+    auto mfull_bar = [&](int i) { return bar0 + 8u * (2 * kStages + 2 * kQSlots + i); };
+    auto mempty_bar = [&](int i) { return bar0 + 8u * (2 * kStages + 2 * kQSlots + 2 + i); };
     if (tid == 0) {
-        for (int i = 0; i < 2 * kStages; ++i) mbar_init(bar0 + 8u * i, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full_bar(i), 1);
+            mbar_init(empty_bar(i), 1);
+        }
+        for (int i = 0; i < kQSlots; ++i) {
+            mbar_init(qfull_bar(i), 1);
+            mbar_init(qempty_bar(i), kWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(mfull_bar(i), kWarps);
+            mbar_init(mempty_bar(i), 1);
+        }
         misc[0] = 0;
         *unknown = -1;
         fence_barrier_init();
@@ -396,7 +485,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
 
     // ---- plan: prefix sums of the runs' tiles, then this CTA's range ----
     // Tile x of run i = s * hkv + g sits at cost position x + kRunCost * i; a
-    // CTA takes the tiles of an equal share of positions.
+    // CTA takes the tiles of an equal share of positions. An end of its range is
+    // found by the thread that holds the sequence.
     const int per = (B + kThreads - 1) / kThreads;
     const int lo = min(B, tid * per), hi = min(B, lo + per);
     int local = 0;
@@ -421,22 +511,22 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
         tiles += t;
         if (w < warp) before += t;
     }
-    for (int s = lo; s < hi; ++s) scan[s] += before;
-    __syncthreads();
     const int cost = hkv * (tiles + kRunCost * B);
     const int share = (cost + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-    if (warp < 2) {
-        const int y = min((static_cast<int>(blockIdx.x) + warp) * share, cost);
-        int at = hkv * tiles;
-        if (y < cost) {
-            const int s = attn::warp_first_true(B, [&](int i) { return hkv * (scan[i] + kRunCost * (i + 1)) > y; });
-            const int nb = attn::run_blocks(scan, s), first = hkv * (scan[s] - nb);
-            const int off = y - first - hkv * kRunCost * s;
-            const int g = off / (nb + kRunCost);
-            at = first + g * nb + min(off - g * (nb + kRunCost), nb);
+    for (int s = lo, start = before; s < hi; ++s) {
+        const int end = before + scan[s], nb = end - start;
+        scan[s] = end;
+        const int c0 = hkv * (start + kRunCost * s), c1 = c0 + hkv * (nb + kRunCost);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int y = (static_cast<int>(blockIdx.x) + i) * share;
+            if (y < c0 || y >= c1) continue;
+            const int g = attn::div_small(y - c0, nb + kRunCost);
+            ends[i] = hkv * start + g * nb + min(y - c0 - g * (nb + kRunCost), nb);
         }
-        if (lane == 0) ends[warp] = at;
+        start = end;
     }
+    if (tid < 2 && (static_cast<int>(blockIdx.x) + tid) * share >= cost) ends[tid] = hkv * tiles;
     __syncthreads();
     const int range_lo = ends[0], range_hi = ends[1];
 
@@ -448,49 +538,60 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
     }
     if (range_lo >= range_hi) return;
 
+    const int r = lane >> 2, c = lane & 3;
+    float* states = reinterpret_cast<float*>(smem + L::kStates);
     attn::PieceWalk walk(scan, B, hkv, range_lo, range_hi, unknown);
     attn::Piece pc;
-    if (warp == kWarps) {
-        // ======================= producer warp =======================
+    if (warp >= kWarps && warp < kHelper) {
+        // ====================== producer warps =======================
+        // A copy costs the warp that issues it 100 to 150 cycles, and one producer
+        // took 860 a tile of four: more than the tile's time in HBM.
         const uint64_t policy = policy_evict_first();
         const int bt = 1 << p.bt_shift;
-        const int tokens = min(bt, kTile);             // of one copy
-        const int copies = kTile / tokens;             // of one tile
-        const int round = 32 / copies;                 // tiles whose copies the lanes hold at a time
-        const int mine = lane / copies, part = lane % copies;
-        int gi = 0, issued = 0;
+        const int tokens = min(bt, kTile);  // of one copy
+        const int copies = kTile / tokens;  // of one tile
+        const int ahead = 32 / copies;      // tiles whose copies' places the lanes hold
+        const uint32_t copy_bytes = tokens / kUnit * U::kBytes;
+        constexpr int kMaxCopies = kTile / 8;
+        int gi = 0, last_issued = -1;
         while (walk.next(pc)) {
             const int ctx = min(__ldg(p.context_lens + pc.s), p.cap);
             const int32_t* row = p.tables + static_cast<size_t>(pc.s) * p.width;
-            for (int j0 = 0; j0 < pc.len; j0 += round) {
-                const int n = min(round, pc.len - j0);
-                const int first = (pc.blk + j0 + mine) * kTile + part * tokens;
-                int units = 0;
-                const uint8_t* src = p.cache;
-                if (mine < n && first < ctx) {
-                    units = (min(tokens, ctx - first) + kUnit - 1) / kUnit;
-                    int id = __ldg(row + (first >> p.bt_shift));
+            for (int j0 = 0; j0 < pc.len; j0 += ahead) {
+                const int n = min(ahead, pc.len - j0);
+                const int token = (pc.blk + j0) * kTile + lane * tokens;
+                uint64_t src = 0;
+                if (lane < n * copies && token < ctx) {
+                    int id = __ldg(row + (token >> p.bt_shift));
                     if (id < 0 || id >= p.num_blocks) {
                         atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
                         id = 0;  // a valid block in its place; the output is flagged invalid
                     }
-                    src += (((static_cast<size_t>(id) * hkv + pc.g) << (p.bt_shift - 3)) + (first & (bt - 1)) / kUnit) * U::kBytes;
+                    src = reinterpret_cast<uint64_t>(p.cache) +
+                          (((static_cast<size_t>(id) * hkv + pc.g) << (p.bt_shift - 3)) + (token & (bt - 1)) / kUnit) * U::kBytes;
                 }
                 for (int j = 0; j < n; ++j, ++gi) {
+                    if (gi % kProducers != warp - kWarps) continue;
                     const int st = gi % kStages;
-                    bool ok = false;
-                    if (lane == 0) {
-                        ok = mbar_wait(empty_bar(st), static_cast<uint32_t>((gi / kStages) & 1) ^ 1u, abort_flag, p.err);
-                        if (ok) {
-                            const int left = min(kTile, ctx - (pc.blk + j0 + j) * kTile);
-                            mbar_arrive_expect_tx(full_bar(st), static_cast<uint32_t>((left + kUnit - 1) / kUnit * U::kBytes));
-                            ++issued;
+                    const int left = min(kTile, ctx - (pc.blk + j0 + j) * kTile);
+                    const uint32_t bytes = (left + kUnit - 1) / kUnit * U::kBytes;
+                    const uint32_t full = full_bar(st), dst = smem_u32(smem + st * L::kStage);
+                    const bool ok = mbar_wait(empty_bar(st), static_cast<uint32_t>((gi / kStages) & 1) ^ 1u, abort_flag, p.err);
+                    if (!__all_sync(0xffffffffu, ok)) continue;
+                    last_issued = gi;
+                    uint64_t from[kMaxCopies];
+#pragma unroll
+                    for (int i = 0; i < kMaxCopies; ++i)
+                        if (i < copies) from[i] = __shfl_sync(0xffffffffu, src, j * copies + i);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(full, bytes);
+#pragma unroll
+                        for (int i = 0; i < kMaxCopies; ++i) {
+                            const uint32_t at = i * copy_bytes;
+                            if (at >= bytes) break;
+                            bulk_load(dst + at, reinterpret_cast<const void*>(from[i]), min(bytes - at, copy_bytes), full, policy);
                         }
                     }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (ok && mine == j && units > 0)
-                        bulk_load(smem_u32(smem + st * L::kStage + part * (tokens / kUnit) * U::kBytes), src,
-                                  static_cast<uint32_t>(units * U::kBytes), full_bar(st), policy);
                 }
             }
         }
@@ -505,61 +606,169 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
                 }
             }
             volatile int never = 0;
-            for (int i = max(0, issued - kStages); i < issued; ++i)
+            for (int i = last_issued; i > last_issued - kStages && i >= 0; i -= kProducers)
                 mbar_wait(full_bar(i % kStages), static_cast<uint32_t>((i / kStages) & 1), &never, nullptr);
         }
         return;
     }
 
+    if (warp == kHelper) {
+        // ======================== helper warp ========================
+        // The next piece's queries, then this one's results. Consumers that have
+        // few tiles of a piece read its queries themselves.
+        int slot = 0, qslot = 0;
+        uint32_t phase = 0, qphase = 0;
+        int turn = 0;  // the consumer that has the piece's first tile
+        auto prepare = [&](const attn::Piece& piece) {
+            if (piece.len < kWarps) return;
+            Queries<kGroups> q;
+            q.load(p, piece.s, piece.g, r, c);
+            if (mbar_wait(qempty_bar(qslot), qphase ^ 1u, abort_flag, p.err)) q.store(smem + L::kQueries + qslot * L::kQBytes, lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull_bar(qslot));
+            if (++qslot == kQSlots) {
+                qslot = 0;
+                qphase ^= 1u;
+            }
+        };
+        attn::Piece next;
+        bool more = walk.next(next);
+        prepare(next);
+        while (more) {
+            pc = next;
+            more = walk.next(next);
+            if (more) prepare(next);
+            const int s = pc.s, g = pc.g, nb = pc.nb, some = min(kWarps, pc.len), from = turn;
+            turn = (turn + pc.len) % kWarps;
+            if (nb == 1) continue;  // its consumer writes the rows
+            const int seg = hkv * (scan[s] - nb) + g * nb + kRunCost * (s * hkv + g);
+            const int i0 = seg / share, i1 = (seg + nb - 1) / share, pieces = i1 - i0 + 1;
+            const int cta = static_cast<int>(blockIdx.x);
+            uint2* out = reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(s) * p.hq + static_cast<size_t>(g) * p.group) * kDim) + lane;
+            auto finish = [&](int h, float4 o, float, float l) { out[h * (kDim / 4)] = rounded(o, 1.f / l); };
+            auto leave = [&](float* dst, float4 o, float m, float l) {
+                *reinterpret_cast<float4*>(dst + 4 * lane) = o;
+                if (lane == 0) {
+                    dst[kDim] = m;
+                    dst[kDim + 1] = l;
+                }
+            };
+            mbar_wait(mfull_bar(slot), phase, abort_flag, p.err);
+            const float* held = states + slot * kStateFloats;
+#pragma unroll 2
+            for (int h = 0; h < p.group; ++h) {
+                float m[kWarps], M = -INFINITY, l = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k) {  // consumers from, from + 1, ... hold tiles of the piece
+                    const int w = from + k < kWarps ? from + k : from + k - kWarps;
+                    m[k] = k < some ? held[(w * kMaxG + h) * kORow + kDim] : -INFINITY;
+                    M = fmaxf(M, m[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k) {
+                    if (k >= some) continue;
+                    const int w = from + k < kWarps ? from + k : from + k - kWarps;
+                    const float* src = held + (w * kMaxG + h) * kORow;
+                    const float f = ex2(m[k] - M);
+                    const float4 v = *reinterpret_cast<const float4*>(src + 4 * lane);
+                    l = fmaf(f, src[kDim + 1], l);
+                    o = make_float4(fmaf(f, v.x, o.x), fmaf(f, v.y, o.y), fmaf(f, v.z, o.z), fmaf(f, v.w, o.w));
+                }
+                if (pieces == 1) finish(h, o, M, l);
+                else leave(partial(p, cta, i1, h), o, M, l);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(mempty_bar(slot));
+            if (++slot == p.slots) {
+                slot = 0;
+                phase ^= 1u;
+            }
+            if (pieces == 1) continue;
+            // true for the last of `count` that come here
+            auto last = [&](int* ctr, int count) {
+                __syncwarp();  // every lane's stores, before lane 0's release
+                int old = 0;
+                if (lane == 0) {
+                    old = atom_add_acq_rel_gpu(ctr, 1);
+                    if (old == count - 1) *ctr = 0;  // ready for the next launch
+                }
+                old = __shfl_sync(0xffffffffu, old, 0);
+                __syncwarp();
+                return old == count - 1;
+            };
+            int stride = 1;
+            if (pieces > kMergeGroup) {
+                stride = kMergeGroup;
+                const int base = i0 + (cta - i0) / kMergeGroup * kMergeGroup;
+                const int count = min(kMergeGroup, i1 - base + 1);
+                if (count > 1) {  // else a lone piece, its group's result already
+                    if (!last(p.group_counters + base, count)) continue;
+                    combine(p, base, 1, count, i1, lane,
+                            [&](int h, float4 o, float m, float l) { leave(partial(p, base, i1, h), o, m, l); });
+                }
+            }
+            const int count = (pieces + stride - 1) / stride;
+            if (last(p.counters + i0, count)) combine(p, i0, stride, count, i1, lane, finish);
+        }
+        return;
+    }
+
     // ======================= consumer warps =======================
-    const int r = lane >> 2, c = lane & 3;
-    float* states = reinterpret_cast<float*>(smem + L::kStates);
-    int gidx = 0, slot = 0;
+    int gidx = 0, slot = 0, qslot = 0;
+    uint32_t phase = 0, qphase = 0;
     while (walk.next(pc)) {
-        const int s = pc.s, g = pc.g, nb = pc.nb;
+        const int s = pc.s, g = pc.g;
         const int ctx = min(__ldg(p.context_lens + s), p.cap);
         const int turn = gidx % kWarps;
         const int first = warp >= turn ? warp - turn : warp + kWarps - turn;
         const bool mine = first < pc.len;
-        State<kGroups> st;
-        if (mine) {
-            Queries<kGroups> q;
-            q.load(p, s, g, r, c);
-            st.clear();
-            for (int j = first; j < pc.len; j += kWarps) {
-                const int gi = gidx + j, stage = gi % kStages;
-                const bool landed = mbar_wait(full_bar(stage), static_cast<uint32_t>((gi / kStages) & 1), abort_flag, p.err);
-                add_tile<kGroups>(smem + stage * L::kStage, min(kTile, ctx - (pc.blk + j) * kTile), q, st, lane);
-                fence_proxy_async_shared();  // this lane's accesses of the stage, before the copy that will replace it
-                __syncwarp();
-                if (lane == 0 && landed) mbar_arrive(empty_bar(stage));
+        Queries<kGroups> q;
+        if (pc.len >= kWarps) {
+            const bool landed = mbar_wait(qfull_bar(qslot), qphase, abort_flag, p.err);
+            q.fetch(smem + L::kQueries + qslot * L::kQBytes, lane);
+            __syncwarp();
+            if (lane == 0 && landed) mbar_arrive(qempty_bar(qslot));
+            if (++qslot == kQSlots) {
+                qslot = 0;
+                qphase ^= 1u;
             }
+        } else if (mine) {
+            q.load(p, s, g, r, c);
+        }
+        State<kGroups> st;
+        st.clear();
+        for (int j = first; j < pc.len; j += kWarps) {
+            const int gi = gidx + j, stage = gi % kStages;
+            const bool landed = mbar_wait(full_bar(stage), static_cast<uint32_t>((gi / kStages) & 1), abort_flag, p.err);
+            add_tile<kGroups>(smem + stage * L::kStage, min(kTile, ctx - (pc.blk + j) * kTile), q, st, lane);
+            fence_proxy_async_shared();  // this lane's accesses of the stage, before the copy that will replace it
+            __syncwarp();
+            if (lane == 0 && landed) mbar_arrive(empty_bar(stage));
         }
         gidx += pc.len;
-        float mins[kGroups][2], sums[2];
-        if (mine) st.rows(c, mins, sums);
-        const size_t row0 = static_cast<size_t>(s) * p.hq + static_cast<size_t>(g) * p.group;
-        if (nb == 1) {  // a run of one tile: its warp writes the rows
-            if (mine) {
+        if (pc.nb == 1) {  // a run of one tile: its warp writes the rows
+            if (!mine) continue;
+            float mins[kGroups][2], sums[2];
+            st.rows(c, mins, sums);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (2 * c + h >= p.group) continue;
-                    const float inv = 1.f / sums[h];
+            for (int h = 0; h < 2; ++h) {
+                if (2 * c + h >= p.group) continue;
+                const float inv = 1.f / sums[h];
+                __nv_bfloat16* row = p.out + (static_cast<size_t>(s) * p.hq + static_cast<size_t>(g) * p.group + 2 * c + h) * kDim;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        *reinterpret_cast<uint2*>(p.out + (row0 + 2 * c + h) * kDim + 32 * w + 4 * r) = rounded(st.row(w, h, mins), inv);
-                }
+                for (int w = 0; w < 4; ++w)
+                    *reinterpret_cast<uint2*>(row + 32 * w + 4 * r) = rounded(st.row(w, h, mins), inv);
             }
             continue;
         }
-        // Every warp's state into this piece's slot; behind the barrier the
-        // other slot is free (all have read it), and warp w combines head w.
-        float* held = states + slot * kStateFloats;
-        slot ^= 1;
+        mbar_wait(mempty_bar(slot), phase ^ 1u, abort_flag, p.err);
         if (mine) {
+            float mins[kGroups][2], sums[2];
+            st.rows(c, mins, sums);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float* dst = held + (warp * kMaxG + 2 * c + h) * kORow;
+                float* dst = states + slot * kStateFloats + (warp * kMaxG + 2 * c + h) * kORow;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) *reinterpret_cast<float4*>(dst + 32 * w + 4 * r) = st.row(w, h, mins);
                 if (r == 0) {
@@ -568,71 +777,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
                 }
             }
         }
-        named_barrier_sync(1, kConsumers);
-        const int seg = hkv * (scan[s] - nb) + g * nb + kRunCost * (s * hkv + g);
-        const int i0 = seg / share, i1 = (seg + nb - 1) / share, pieces = i1 - i0 + 1;
-        for (int h = warp; h < p.group; h += kWarps) {
-            float M = -INFINITY, sum_h = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int some = min(kWarps, pc.len);  // warps turn, turn + 1, ... hold tiles of the piece
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k)
-                if (k < some) M = fmaxf(M, held[((turn + k) % kWarps * kMaxG + h) * kORow + kDim]);
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                if (k >= some) continue;
-                const float* src = held + ((turn + k) % kWarps * kMaxG + h) * kORow;
-                const float f = ex2(src[kDim] - M);
-                const float4 o = *reinterpret_cast<const float4*>(src + 4 * lane);
-                sum_h = fmaf(f, src[kDim + 1], sum_h);
-                acc = make_float4(fmaf(f, o.x, acc.x), fmaf(f, o.y, acc.y), fmaf(f, o.z, acc.z), fmaf(f, o.w, acc.w));
-            }
-            uint2* out = reinterpret_cast<uint2*>(p.out + (row0 + h) * kDim) + lane;
-            if (pieces == 1) {
-                *out = rounded(acc, 1.f / sum_h);
-                continue;
-            }
-            // A CTA holds at most two pieces of cut runs: one that goes on in
-            // the next CTA (slot 1) and the end of one from an earlier CTA.
-            const int cta = static_cast<int>(blockIdx.x);
-            auto slot_of = [&](int i) { return p.partials + ((static_cast<size_t>(i) * 2 + (i == i1 ? 0 : 1)) * kMaxG + h) * kORow; };
-            auto leave = [&](float* dst) {
-                *reinterpret_cast<float4*>(dst + 4 * lane) = acc;
-                if (lane == 0) {
-                    dst[kDim] = M;
-                    dst[kDim + 1] = sum_h;
-                }
-                __syncwarp();
-            };
-            // true for the last of `count` warps that come here for head h
-            auto last = [&](unsigned long long* ctr, int count) {
-                uint64_t old = 0;
-                if (lane == 0) {
-                    old = atom_add_acq_rel_gpu(ctr, uint64_t(1) << (8 * h));
-                    old = (old >> (8 * h)) & 255u;
-                    if (static_cast<int>(old) == count - 1) atomicAdd(ctr, 0ull - (static_cast<unsigned long long>(count) << (8 * h)));
-                }
-                const int seen = __shfl_sync(0xffffffffu, static_cast<int>(old), 0);
-                __syncwarp();
-                return seen == count - 1;
-            };
-            leave(slot_of(cta));
-            int stride = 1;
-            if (pieces > kMergeGroup) {
-                stride = kMergeGroup;
-                const int base = i0 + (cta - i0) / kMergeGroup * kMergeGroup;
-                const int count = min(kMergeGroup, i1 - base + 1);
-                if (count > 1) {  // else a lone piece, its group's result already
-                    if (!last(p.group_counters + base, count)) continue;
-                    acc = combine(p, base, 1, count, i1, h, lane, M, sum_h);
-                    __syncwarp();
-                    leave(slot_of(base));
-                }
-            }
-            const int count = (pieces + stride - 1) / stride;
-            if (!last(p.counters + i0, count)) continue;
-            acc = combine(p, i0, stride, count, i1, h, lane, M, sum_h);
-            *out = rounded(acc, 1.f / sum_h);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(mfull_bar(slot));
+        if (++slot == p.slots) {
+            slot = 0;
+            phase ^= 1u;
         }
     }
 }
