@@ -393,11 +393,12 @@ pkv_status pkv_attn_tree(const void* q, const void* k_draft, const void* v_draft
  * Infinite and larger values saturate; a NaN makes its whole group NaN. Scales
  * and minima are fp16, so ranges under 15 * 2^-24 vanish.
  *
- * cache: device bytes [num_blocks][num_kv_heads][block_tokens / 8][unit], one
- * unit of 1,024 + 64 * 128 / group_dims bytes per 8 tokens (codes, scales and
- * minima of both keys and values, in the order in which the attention's lanes
- * read them; csrc/pkv_int4.cuh states it byte by byte); 16-byte aligned. Zero
- * bytes stand for zeros. Slots, tables and pairs are those of the bf16 cache.
+ * cache: device bytes [num_blocks][block_tokens / 16][num_kv_heads][2][unit]
+ * (blocks of 8 tokens: [num_blocks][num_kv_heads][unit]), one unit of 1,024 +
+ * 64 * 128 / group_dims bytes per 8 tokens (codes, scales and minima of both keys
+ * and values, in the order in which the attention's lanes read them;
+ * csrc/pkv_int4.cuh states it byte by byte); 16-byte aligned. Zero bytes stand
+ * for zeros. Slots, tables and pairs are those of the bf16 cache.
  *
  * pkv_int4_block_bytes: bytes of one block, all KV heads (0 on invalid
  *   arguments).
@@ -413,13 +414,19 @@ pkv_status pkv_attn_tree(const void* q, const void* k_draft, const void* v_draft
  *   and pkv_attn_tree read. Pairs with an id outside its pool are skipped and
  *   set PKV_DEVERR_BLOCK_ID; destinations must be distinct.
  * pkv_block_copy_int4: pkv_block_copy of such blocks.
- * pkv_attn_decode_int4: pkv_attn_decode over such a cache: workspace (the same
- *   kind: one serves both calls), block_tables, context_lens, q, out, num_ctas,
- *   limits and errors as there, any block size. fp32 sums and softmax; the
+ * pkv_attn_decode_int4: pkv_attn_decode over such a cache: block_tables,
+ *   context_lens, q, out, limits and errors as there, any block size. workspace:
+ *   as there (one serves both calls), with room for the partial results of as
+ *   many CTAs as run at once in pkv_attn_int4_workspace_size() bytes, whatever
+ *   the batch (0 when no device is present); fewer bytes are taken as they are
+ *   and make fewer CTAs do the work, less than one CTA's share is refused
+ *   (PKV_EINVAL). num_ctas: as there, at most 1,536. fp32 sums and softmax; the
  *   weights enter the product with the values in fp16. What lies behind a
  *   context in its last block, NaN scales included, never reaches the output.
  */
 size_t pkv_int4_block_bytes(int num_kv_heads, int block_tokens, int group_dims);
+
+size_t pkv_attn_int4_workspace_size(void);
 
 pkv_status pkv_append_int4(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                            const int64_t* slot_mapping, int num_tokens, void* cache, int num_blocks,

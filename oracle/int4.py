@@ -6,7 +6,8 @@ Per group of G of a row's 128 values, in fp32 with one rounding per step:
     c = rint((x - m) / s), held to 0 .. 15 (0 where s is 0)
 and the row stands for s c + m. A NaN makes its group's s and m NaN.
 
-pack() lays a block of one KV head out in bytes: units of 8 tokens, each
+pack() lays a block's rows out in bytes: slabs of 16 tokens (8 where the block has
+no more), in each the KV heads, in each of these units of 8 tokens, each
     key codes    word 4 c + w of a token's 16: dims 32 w + 8 c .. + 7
     value codes  16-bit piece (r, t / 2, w, t % 2): dims 32 w + 4 r .. + 3
     keys' (s, m) by token and group, values' s by group and token, values' m.
@@ -44,7 +45,15 @@ def values(codes, s, m):
 
 
 def pack(k, v):
-    """k, v: (codes, s, m) of rows [..., tokens, 128] -> bytes [..., tokens / 8 * unit]."""
+    """k, v: (codes, s, m) of rows [..., heads, tokens, 128] -> bytes [..., slabs, heads,
+    slab tokens / 8 * unit]."""
+    slab = min(16, k[0].shape[-2])
+    by_slab = lambda x: np.moveaxis(x.reshape(*x.shape[:-2], -1, slab, x.shape[-1]), -3, -4)
+    return _pack_rows([by_slab(x) for x in k], [by_slab(x) for x in v])
+
+
+def _pack_rows(k, v):
+    """Rows [..., tokens, 128] of one head -> bytes [..., tokens / 8 * unit]."""
     (kc, ks, km), (vc, vs, vm) = k, v
     lead, tokens, groups = kc.shape[:-2], kc.shape[-2], ks.shape[-1]
     u = tokens // 8

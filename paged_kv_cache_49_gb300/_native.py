@@ -50,7 +50,7 @@ EXPORTED = [
     "pkv_attn_decode_wait_test", "pkv_attn_decode_cuda_cores", "pkv_attn_workspace_fixed_bytes",
     "pkv_attn_launch_ctas", "pkv_attn_prefill", "pkv_attn_prefill_workspace_size", "pkv_attn_tree",
     "pkv_qk_norm_rope_append", "pkv_int4_block_bytes", "pkv_append_int4", "pkv_load_int4", "pkv_block_copy_int4",
-    "pkv_attn_decode_int4", "pkv_beam_select", "pkv_beam_workspace_size", "pkv_bm_reorder",
+    "pkv_attn_decode_int4", "pkv_attn_int4_workspace_size", "pkv_beam_select", "pkv_beam_workspace_size", "pkv_bm_reorder",
 ]
 BLOCK_SIZES = (8, 16, 32, 64)
 INT4_GROUP_DIMS = (32, 64, 128)
@@ -152,6 +152,7 @@ def _load() -> ctypes.CDLL:
         "pkv_qk_norm_rope_append": (i32, [vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, i32, i32, i32, vp, vp, i32, i32,
                                           i32, i32, vp, vp, vp, vp, i32, i32, vp, vp]),
         "pkv_int4_block_bytes": (sz, [i32, i32, i32]),
+        "pkv_attn_int4_workspace_size": (sz, []),
         "pkv_append_int4": (i32, [vp, i64, vp, i64, vp, i32, vp, i32, i32, i32, i32, i32, vp, vp]),
         "pkv_load_int4": (i32, [vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]),
         "pkv_block_copy_int4": (i32, [vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]),
@@ -281,7 +282,9 @@ class AttentionWorkspace:
         if nbytes == 0:
             raise PkvError(PKV_EINVAL, "pkv_attn_workspace_size")
         self.num_seqs, self.num_kv_heads, self.nbytes = num_seqs, num_kv_heads, nbytes
-        self.buffer = torch.empty(nbytes + 256, dtype=torch.uint8, device=device or "cuda")
+        # attn_decode_int4 leaves more partial results a CTA, behind the same counters
+        self.int4_nbytes = max(nbytes, int(_lib.pkv_attn_int4_workspace_size()))
+        self.buffer = torch.empty(self.int4_nbytes + 256, dtype=torch.uint8, device=device or "cuda")
         off = (-self.buffer.data_ptr()) % 256
         self.tensor = self.buffer[off : off + nbytes]
         _check(_lib.pkv_attn_workspace_init(self.tensor.data_ptr(), nbytes, _stream(stream)),
@@ -781,9 +784,9 @@ def qk_norm_rope_append(q, k, v, cos_sin, positions, slot_mapping, k_cache, v_ca
 
 class Int4Cache:
     """A pool of pages whose keys and values are held in 4 bits (see
-    pkv_append_int4 in the header for the format): uint8 `data` [num_blocks,
-    num_kv_heads, bytes of a block and head], zeros at first. Rows of 128 values
-    are quantised in groups of group_dims."""
+    pkv_append_int4 in the header for the format): uint8 `data` [num_blocks, slabs of
+    a block, num_kv_heads, bytes of a slab and head], zeros at first. Rows of 128
+    values are quantised in groups of group_dims."""
 
     def __init__(self, num_blocks: int, num_kv_heads: int, block_tokens: int = BLOCK_TOKENS, group_dims: int = 64,
                  device=None):
@@ -792,7 +795,8 @@ class Int4Cache:
             raise ValueError("Int4Cache needs blocks, heads, block_tokens in (8, 16, 32, 64) and group_dims in (32, 64, 128)")
         self.num_blocks, self.num_kv_heads = num_blocks, num_kv_heads
         self.block_tokens, self.group_dims = block_tokens, group_dims
-        self._data = torch.zeros((num_blocks, num_kv_heads, nbytes // num_kv_heads), dtype=torch.uint8,
+        slabs = max(1, block_tokens // 16)
+        self._data = torch.zeros((num_blocks, slabs, num_kv_heads, nbytes // slabs // num_kv_heads), dtype=torch.uint8,
                                  device=device or "cuda")
         # of the calls' arguments: the pool's address, and the shape behind it
         self._ptr, self._device = self._data.data_ptr(), self._data.get_device()
@@ -898,7 +902,7 @@ def attn_decode_int4(q, cache: Int4Cache, block_tables, context_lens, scale, out
         hkv, _, bt, gd = cache._shape
         _check(_lib.pkv_attn_decode_int4(q.data_ptr(), cache._ptr, block_tables.data_ptr(), block_tables.shape[1],
                                          context_lens.data_ptr(), B, hq, hkv, d, cache.num_blocks, bt, gd, scale, num_ctas,
-                                         workspace.ptr, workspace.nbytes, out.data_ptr(), st), "pkv_attn_decode_int4")
+                                         workspace.ptr, workspace.int4_nbytes, out.data_ptr(), st), "pkv_attn_decode_int4")
     return out
 
 

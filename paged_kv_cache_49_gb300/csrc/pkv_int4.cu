@@ -49,7 +49,8 @@ struct Append {
     uint32_t k_stride, v_stride;  // of a token, in 8-value vectors
     const int64_t* slots;
     uint32_t tokens, magic;  // (i * magic) >> (32 + magic_shift) is i / hkv
-    int magic_shift, hkv, bt_shift;
+    int magic_shift, hkv;
+    bool blocks_of_8;
     long long slot_limit;
     uint8_t* cache;
     uint32_t* err;
@@ -156,17 +157,14 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const Append p) {
         if (at >= p.slot_limit && p.err && part == 0 && head == 0) atomicOr(p.err, PKV_DEVERR_SLOT);
         slot[j] = at >= 0 && at < p.slot_limit ? static_cast<int>(at) : -1;
     }
-    auto unit_of = [&](int at) {
-        const int unit = (((at >> p.bt_shift) * p.hkv + head) << (p.bt_shift - 3)) + ((at & ((1 << p.bt_shift) - 1)) >> 3);
-        return p.cache + static_cast<size_t>(unit) * U::kBytes;
-    };
+    auto unit_at = [&](int at) { return p.cache + static_cast<size_t>(unit_of(at, head, p.hkv, p.blocks_of_8)) * U::kBytes; };
     const bool first = part % kLanes == 0;
     __half s[2], m[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const uint32_t word = quantise<kLanes>(raw[0][j], s[0], m[0]);
         if (slot[j] < 0) continue;
-        uint8_t* unit = unit_of(slot[j]);
+        uint8_t* unit = unit_at(slot[j]);
         const int t = slot[j] & 7;
         *reinterpret_cast<uint32_t*>(unit + key_word(t, w, c)) = word;
         if (first) *reinterpret_cast<__half2*>(unit + U::kKeyParams + (t * kGroups + g) * 4) = __halves2half2(s[0], m[0]);
@@ -175,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const Append p) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) word[j] = quantise<kLanes>(raw[1][j], s[j], m[j]);
     if (slot[0] >= 0 && slot[1] == slot[0] + 1 && (slot[0] & 1) == 0) {
-        uint8_t* unit = unit_of(slot[0]);
+        uint8_t* unit = unit_at(slot[0]);
         const int t = slot[0] & 7;
         *reinterpret_cast<uint32_t*>(unit + value_piece(t, w, 2 * c)) = __byte_perm(word[0], word[1], 0x5410);
         *reinterpret_cast<uint32_t*>(unit + value_piece(t, w, 2 * c + 1)) = __byte_perm(word[0], word[1], 0x7632);
@@ -188,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const Append p) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if (slot[j] < 0) continue;
-        uint8_t* unit = unit_of(slot[j]);
+        uint8_t* unit = unit_at(slot[j]);
         const int t = slot[j] & 7;
         *reinterpret_cast<uint16_t*>(unit + value_piece(t, w, 2 * c)) = static_cast<uint16_t>(word[j]);
         *reinterpret_cast<uint16_t*>(unit + value_piece(t, w, 2 * c + 1)) = static_cast<uint16_t>(word[j] >> 16);
@@ -206,7 +204,8 @@ struct Load {
     uint8_t* v;
     long long units;  // pairs * heads * block tokens / 8
     int per_block;    // units of a block
-    int num_src, num_dst;
+    int slab_units;   // of one head
+    int num_src, num_dst, hkv;
     uint32_t* err;
 };
 
@@ -234,7 +233,10 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const Load p) {
         return;
     }
     const uint8_t* unit = p.cache + (static_cast<long long>(src) * p.per_block + at) * U::kBytes;
-    const long long out = (static_cast<long long>(dst) * p.per_block + at) * (kUnit * kDim * 2);
+    // where its 8 rows are in a bf16 block: [head][position]
+    const int per_slab = p.slab_units * p.hkv, slab = at / per_slab, rest = at - slab * per_slab;
+    const int head = rest / p.slab_units, first = slab * p.slab_units + rest % p.slab_units;
+    const long long out = (static_cast<long long>(dst) * p.per_block + head * (p.per_block / p.hkv) + first) * (kUnit * kDim * 2);
     const uint4 kc = ld_streaming(reinterpret_cast<const uint4*>(unit) + lane);
     const uint4 vc = ld_streaming(reinterpret_cast<const uint4*>(unit + U::kValues) + lane);
     __half2 kp[kGroups], vs[kGroups], vm[kGroups];
@@ -334,7 +336,7 @@ pkv_status pkv_append_int4(const void* k, int64_t k_stride, const void* v, int64
     p.slots = slot_mapping;
     p.tokens = static_cast<uint32_t>(num_tokens);
     p.hkv = num_kv_heads;
-    p.bt_shift = block_tokens == 8 ? 3 : block_tokens == 16 ? 4 : block_tokens == 32 ? 5 : 6;
+    p.blocks_of_8 = block_tokens == 8;
     p.slot_limit = static_cast<long long>(num_blocks) * block_tokens;
     p.cache = static_cast<uint8_t*>(cache);
     p.err = device_error;
@@ -372,6 +374,8 @@ pkv_status pkv_load_int4(const void* cache, const int32_t* src_dst_pairs, int nu
     p.v = static_cast<uint8_t*>(v_cache);
     p.per_block = num_kv_heads * (block_tokens / kv4::kUnit);
     p.units = static_cast<long long>(num_pairs) * p.per_block;
+    p.slab_units = block_tokens == 8 ? 1 : 2;
+    p.hkv = num_kv_heads;
     p.num_src = num_blocks;
     p.num_dst = num_dst_blocks;
     p.err = device_error;

@@ -10,9 +10,11 @@
 // matrix products of the attention as they are; bf16 keys and values convert to
 // m without loss from 2^-14 on. A NaN in a group makes its s and m NaN.
 //
-// A block of one KV head is block_tokens / 8 units of 8 tokens, one after the
-// other, so that a run of tokens is one contiguous copy whatever the block
-// size. A unit (1,024 + 64 * 128 / G bytes) holds, in this order,
+// A block is slabs of 16 tokens (of 8 where it has but 8), one after the other; a
+// slab has its KV heads' rows one after the other, so that the rows of a slab of
+// several heads are one contiguous copy; and a head's part of a slab is one or
+// two units of 8 tokens. A unit (1,024 + 64 * 128 / G bytes) holds, in this
+// order,
 //   512 bytes  key codes: token t at 64 t; its 16 words in the order 4 c + w,
 //              word (w, c) the dims 32 w + 8 c .. + 7, lowest dim lowest
 //   512 bytes  value codes: 16-bit pieces of 4 dims at
@@ -56,6 +58,11 @@ struct Unit {
 inline int groups_of(int group_dims) { return group_dims == 32 ? 4 : group_dims == 64 ? 2 : group_dims == 128 ? 1 : 0; }
 
 inline bool block_tokens_ok(int bt) { return bt == 8 || bt == 16 || bt == 32 || bt == 64; }
+
+// The unit that holds a slot's token (slot = block * block tokens + position).
+__host__ __device__ __forceinline__ long long unit_of(long long slot, int head, int hkv, bool blocks_of_8) {
+    return blocks_of_8 ? (slot >> 3) * hkv + head : ((slot >> 4) * hkv + head) * 2 + ((slot >> 3) & 1);
+}
 
 // Byte of token t's key word (w, c), and of its value piece (w, r), in a unit.
 __device__ __forceinline__ int key_word(int t, int w, int c) { return t * 64 + (4 * c + w) * 4; }

@@ -25,56 +25,63 @@
 //    weight times scale to stay in range. A third product with rows of the
 //    values' minima and of ones gives sum p m and the softmax's denominator.
 //
-// Work: as the bf16 cache's decode kernel (pkv_decode_kernel.cuh): all
-// (sequence, KV head) runs laid end to end in tiles of kTile tokens, cut into
-// gridDim.x ranges of equal cost. A producer warp copies tiles
-// into a ring; consumer warp i takes every kWarps-th, whatever piece it
-// belongs to. A helper warp goes with them, so that none waits for another: it
-// has the next piece's queries ready as the products take them, and combines the
-// states that the consumers leave of a piece; pieces of a run that is cut among
-// CTAs are combined by whichever helper finishes last.
+// Work. A run is one sequence and up to 8 of its KV heads (the most of 8, 4, 2, 1
+// that divide their number), in tiles of 16 tokens a consumer warp: with 8 heads
+// a warp has a head of its own, with fewer the warps of a head share its tokens.
+// A tile's bytes are one copy then, or few, since a slab holds its heads'
+// rows next to one another -- with a copy a block and head, issuing them (100 to
+// 150 cycles each) was what bounded the kernel. All runs are laid end to end, as
+// in the bf16 cache's decode kernel (pkv_decode_kernel.cuh), and cut into
+// gridDim.x ranges of equal cost, one CTA an SM. Producer warps copy tiles into a
+// ring; the consumers take up to four tiles at a time, 64 tokens each where they
+// have a head of their own. At the end of a piece a warp has its head's result;
+// warps that share a head combine theirs through shared memory first. Pieces of a
+// run that is cut among CTAs are combined by whichever warp (of those with the
+// same rows) finishes last.
 #pragma once
 
 #include "pkv_decode_kernel.cuh"
 #include "pkv_int4.cuh"
+#include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace kv4 {
 
 constexpr int kMaxG = PKV_ATTN_MAX_GROUP;
-constexpr int kTile = 64;   // tokens
-constexpr int kWarps = 4;   // consumers
-constexpr int kStages = 8;
-static_assert(kStages % kWarps == 0, "each stage is always the same warp's");
+constexpr int kWarps = 4;      // consumers, and heads of a run at most
+constexpr int kTok = 16;       // tokens of a tile, a warp
+constexpr int kSubs = 4;       // tiles a warp takes at a time
+constexpr int kStages = 8;     // tiles of the ring
 constexpr int kProducers = 2;  // producer i copies every tile whose place in the stream is i modulo their number
-constexpr int kHelper = kWarps + kProducers;
-constexpr int kThreads = (kHelper + 1) * 32;
-static_assert(kStages % kProducers == 0, "each stage is always the same producer's");
-constexpr int kSubs = kTile / 16;
+static_assert(kStages % kSubs == 0 && kStages % kProducers == 0, "each stage is always the same producer's");
+constexpr int kConsumers = kWarps * 32;
+constexpr int kThreads = kConsumers + kProducers * 32;
 // Work partition: what a run costs beyond its tiles, in tiles.
-constexpr int kRunCost = 3;
+constexpr int kRunCost = 2;
 // Runs of more pieces than this are combined in two levels.
 constexpr int kMergeGroup = 16;
-constexpr int kMaxCtas = attn::kMaxCtas;
+// Counters of a launch, 64 bits with one byte a warp, in the workspace's region
+// of counters: per CTA one for the cut run, and one for the group of its pieces,
+// whose first piece is the CTA's (at most one: the last run of its range).
+constexpr int kMaxCtas = static_cast<int>(attn::kWsCounterBytes / 16);
+static_assert(kMaxCtas / kMergeGroup < 256 && kMergeGroup < 256, "a count fits a byte");
 
 constexpr int kORow = attn::kORow;
-constexpr int kStateFloats = kWarps * kMaxG * kORow;  // output, max and sum of every warp's heads
-constexpr int kQSlots = 2;
+constexpr int kStateFloats = kWarps * kMaxG * kORow;  // output, max and sum of every warp's rows
 
-// Shared memory: the ring, queries, states of one or two pieces (one where two
-// would keep a second CTA off the SM), barriers, the plan.
 template <int kGroups>
 struct Smem {
-    static constexpr int kStage = kTile / kUnit * Unit<kGroups>::kBytes;
-    static constexpr int kQueries = kStages * kStage;
-    static constexpr int kQBytes = (16 + 2 + 2 * kGroups) * 32 * 4;
-    static constexpr int kBars = kQueries + kQSlots * kQBytes;
-    static constexpr int kNumBars = 2 * kStages + 2 * kQSlots + 4;
-    static constexpr int kMisc = kBars + kNumBars * 8;
-    static constexpr int kStates = (kMisc + 64 + 15) / 16 * 16;
-    static __host__ __device__ constexpr int scan(int slots) { return kStates + slots * kStateFloats * 4; }
-    static constexpr size_t bytes(int num_seqs, int slots) { return 128 + scan(slots) + 4 * static_cast<size_t>(num_seqs); }
+    static constexpr int kStage = kWarps * 2 * Unit<kGroups>::kBytes;
+    static constexpr int kStates = kStages * kStage;
+    static constexpr int kBars = kStates + kStateFloats * 4;
+    static constexpr int kMisc = kBars + 2 * kStages * 8;
+    static constexpr int kScan = kMisc + 64;
+    static constexpr size_t bytes(int num_seqs) { return 128 + kScan + 4 * static_cast<size_t>(num_seqs); }
 };
+
+// A CTA's partial results: two pieces, up to 32 rows each.
+constexpr int kRows = kWarps * kMaxG;
+constexpr size_t partial_bytes(int rows) { return 2 * static_cast<size_t>(rows) * kORow * 4; }
 
 struct Decode {
     const __nv_bfloat16* q;
@@ -82,22 +89,15 @@ struct Decode {
     const int32_t* tables;
     const int32_t* context_lens;
     __nv_bfloat16* out;
-    int num_seqs, width, cap, hq, hkv, group, num_blocks, bt_shift;
+    int num_seqs, width, cap, hq, hkv, group, num_blocks, bt_shift;  // (log2 of block tokens)
+    int heads, runs, rows;    // KV heads of a run, runs of a sequence, query rows of a run
+    int copy_tokens, copies;  // of a copy, and copies of a tile
     float scale_log2;
     uint32_t* err;
-    int* counters;        // [kMaxCtas]: pieces counted of the cut run whose first piece is the CTA's
-    int* group_counters;  // [kMaxCtas]: likewise, of a group of its pieces
-    float* partials;      // [grid][2][kMaxG][kORow]
-    int slots;            // pieces whose states fit in shared memory
+    unsigned long long* counters;        // [kMaxCtas]
+    unsigned long long* group_counters;  // [kMaxCtas]
+    float* partials;                     // [grid][2][rows][kORow]
 };
-
-// True in one thread of the warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t one = 0;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t@p mov.u32 %0, 1;\n\t}" : "+r"(one));
-    return one != 0;
-}
 
 // Products and transposes that the compiler may schedule among others.
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -118,6 +118,8 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+// The larger of two non-negative fp16 numbers, of both halves (a NaN is larger).
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 __device__ __forceinline__ float half_lo(uint32_t v) { return __half2float(__ushort_as_half(static_cast<unsigned short>(v))); }
 __device__ __forceinline__ float half_hi(uint32_t v) { return __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16))); }
 __device__ __forceinline__ uint32_t word(const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
@@ -184,28 +186,6 @@ struct Queries {
             for (int i = 0; i < kGroups; ++i) sum[i][h] = __shfl_sync(0xffffffffu, sums[i], lane) * 0x1p-24f;
         }
     }
-
-    // Into and out of shared memory, as the lanes hold them.
-    __device__ __forceinline__ void store(uint8_t* slot, int lane) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            reinterpret_cast<uint4*>(slot)[i * 32 + lane] = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
-        float2* rest = reinterpret_cast<float2*>(slot + 2048) + lane;
-        rest[0] = make_float2(factor[0], factor[1]);
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) rest[32 * (i + 1)] = make_float2(sum[i][0], sum[i][1]);
-    }
-    __device__ __forceinline__ void fetch(const uint8_t* slot, int lane) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint4 u = reinterpret_cast<const uint4*>(slot)[i * 32 + lane];
-            b[4 * i] = u.x, b[4 * i + 1] = u.y, b[4 * i + 2] = u.z, b[4 * i + 3] = u.w;
-        }
-        const float2* rest = reinterpret_cast<const float2*>(slot + 2048) + lane;
-        factor[0] = rest[0].x, factor[1] = rest[0].y;
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) sum[i][0] = rest[32 * (i + 1)].x, sum[i][1] = rest[32 * (i + 1)].y;
-    }
 };
 
 // A warp's softmax state of a piece. Lane 4 r + c holds heads 2 c, 2 c + 1:
@@ -246,30 +226,35 @@ struct State {
     }
 };
 
-// One tile into a warp's state; `valid` of its tokens count.
-template <int kGroups>
-__device__ __forceinline__ void add_tile(uint8_t* tile, int valid, const Queries<kGroups>& q, State<kGroups>& st, int lane) {
+// Up to kSubs tiles into a warp's state: unit 0 of tile i at `at[i]`, unit 1 `second`
+// bytes behind it; valid[i] of its 16 tokens count, and at least one in all.
+// kWhole: all of them do, and with no branch between them the tiles' products and
+// loads overlap.
+template <int kGroups, bool kWhole>
+__device__ __forceinline__ void add_tiles(uint8_t* const (&at)[kSubs], const int (&valid)[kSubs], int second,
+                                          const Queries<kGroups>& q, State<kGroups>& st, int lane) {
     using U = Unit<kGroups>;
     const int r = lane >> 2, c = lane & 3;
-    if (valid < kTile) {
-        // scales and minima behind the context, which may be anything, are zeros to the values' products
-        for (int t = valid + lane; t < kTile; t += 32) {
-            uint8_t* unit = tile + t / kUnit * U::kBytes;
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                *reinterpret_cast<uint16_t*>(unit + U::kValueScales + (g * kUnit + t % kUnit) * 2) = 0;
-                *reinterpret_cast<uint16_t*>(unit + U::kValueMins + (g * kUnit + t % kUnit) * 2) = 0;
-            }
-        }
-        __syncwarp();
-    }
-
-    // ---- scores ----
     float x[kSubs][4];
+    uint32_t scales = 0;  // the largest of the values', a lane's two tokens at a time
 #pragma unroll
     for (int i = 0; i < kSubs; ++i) {
-        const uint8_t* u0 = tile + 2 * i * U::kBytes;
-        const uint8_t* u1 = u0 + U::kBytes;
+        x[i][0] = x[i][1] = x[i][2] = x[i][3] = -INFINITY;
+        if (!kWhole && valid[i] <= 0) continue;
+        uint8_t* u0 = at[i];
+        uint8_t* u1 = u0 + second;
+        if (!kWhole && valid[i] < kTok) {
+            // scales and minima behind the context, which may be anything, are zeros to the values' products
+            if (lane >= valid[i] && lane < kTok) {
+                uint8_t* unit = lane < kUnit ? u0 : u1;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    *reinterpret_cast<uint16_t*>(unit + U::kValueScales + (g * kUnit + lane % kUnit) * 2) = 0;
+                    *reinterpret_cast<uint16_t*>(unit + U::kValueMins + (g * kUnit + lane % kUnit) * 2) = 0;
+                }
+            }
+            __syncwarp();
+        }
         const uint4 k0 = lds128(u0 + lane * 16), k1 = lds128(u1 + lane * 16);
         // two chains of products a group (one for four groups)
         constexpr int kChains = kGroups == 4 ? 1 : 2;
@@ -298,15 +283,14 @@ __device__ __forceinline__ void add_tile(uint8_t* tile, int valid, const Queries
                 t[h] = fmaf(half_lo(p0), d[h], fmaf(half_hi(p0), q.sum[g][h], t[h]));
                 t[h + 2] = fmaf(half_lo(p1), d[h + 2], fmaf(half_hi(p1), q.sum[g][h], t[h + 2]));
             }
+            scales = max_u16x2(scales, max_u16x2(lds32(u0 + U::kValueScales + (g * kUnit + 2 * c) * 2),
+                                                 lds32(u1 + U::kValueScales + (g * kUnit + 2 * c) * 2)));
         }
 #pragma unroll
         for (int h = 0; h < 4; ++h) x[i][h] = t[h] * q.factor[h & 1];
-    }
-    if (valid < kTile) {
-#pragma unroll
-        for (int i = 0; i < kSubs; ++i) {
-            if (16 * i + r >= valid) x[i][0] = x[i][1] = -INFINITY;
-            if (16 * i + 8 + r >= valid) x[i][2] = x[i][3] = -INFINITY;
+        if (!kWhole && valid[i] < kTok) {
+            if (r >= valid[i]) x[i][0] = x[i][1] = -INFINITY;
+            if (kUnit + r >= valid[i]) x[i][2] = x[i][3] = -INFINITY;
         }
     }
 
@@ -319,17 +303,7 @@ __device__ __forceinline__ void add_tile(uint8_t* tile, int valid, const Queries
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], d));
     }
-    bool large = false;
-    constexpr int kWords = kTile / kUnit * kGroups * 4;
-#pragma unroll
-    for (int i = 0; i < (kWords + 31) / 32; ++i) {
-        const int at = i * 32 + lane;
-        if (kWords % 32 == 0 || at < kWords) {
-            const uint32_t v = lds32(tile + at / (kGroups * 4) * U::kBytes + U::kValueScales + at % (kGroups * 4) * 4);
-            large |= (v & 0xffffu) >= 0x5000u || (v >> 16) >= 0x5000u;  // 32 in fp16
-        }
-    }
-    if (__any_sync(0xffffffffu, large)) st.offset = 2.f;
+    if (__any_sync(0xffffffffu, (scales & 0xffffu) >= 0x5000u || (scales >> 16) >= 0x5000u)) st.offset = 2.f;  // 32 in fp16
     const float base[2] = {top[0] - st.offset, top[1] - st.offset};
     if (__any_sync(0xffffffffu, base[0] != st.base[0] || base[1] != st.base[1])) {
         const float f[2] = {ex2(st.base[0] - base[0]), ex2(st.base[1] - base[1])};
@@ -350,8 +324,9 @@ __device__ __forceinline__ void add_tile(uint8_t* tile, int valid, const Queries
     // ---- values ----
 #pragma unroll
     for (int i = 0; i < kSubs; ++i) {
-        const uint8_t* u0 = tile + 2 * i * U::kBytes;
-        const uint8_t* u1 = u0 + U::kBytes;
+        if (!kWhole && valid[i] <= 0) continue;
+        const uint8_t* u0 = at[i];
+        const uint8_t* u1 = u0 + second;
         const uint32_t p0 = transposed(pack_f16x2(ex2(x[i][0] - base[0]), ex2(x[i][1] - base[1])));
         const uint32_t p1 = transposed(pack_f16x2(ex2(x[i][2] - base[0]), ex2(x[i][3] - base[1])));
         uint32_t m0 = 0, m1 = 0;
@@ -381,49 +356,51 @@ __device__ __forceinline__ void add_tile(uint8_t* tile, int valid, const Queries
 // A run's pieces leave their partial results with their CTAs: slot 0 for the
 // run's last, slot 1 for the others (a CTA holds at most two pieces of cut runs,
 // one that goes on in the next CTA and the end of one from an earlier CTA).
-__device__ __forceinline__ float* partial(const Decode& p, int cta, int last, int h) {
-    return p.partials + ((static_cast<size_t>(cta) * 2 + (cta == last ? 0 : 1)) * kMaxG + h) * kORow;
+__device__ __forceinline__ float* partial(const Decode& p, int cta, int last, int row) {
+    return p.partials + ((static_cast<size_t>(cta) * 2 + (cta == last ? 0 : 1)) * p.rows + row) * kORow;
 }
 
-// `count` partial results, `stride` CTAs apart from CTA `first` on, combined by
-// head; emit(h, four dims from 4 lane on, max, sum). Four heads and four partial
-// results are on their way at a time.
+// `count` partial results of rows row, row + step, ... (`rows` of them), `stride`
+// CTAs apart from CTA `first` on, combined; emit(row, four dims from 4 lane on,
+// max, sum). Four of two rows are on their way at a time.
 template <class Emit>
-__device__ __forceinline__ void combine(const Decode& p, int first, int stride, int count, int last, int lane, Emit emit) {
+__device__ __forceinline__ void combine(const Decode& p, int first, int stride, int count, int last, int row, int step, int rows,
+                                        int lane, Emit emit) {
+    constexpr int kAhead = 4, kAbreast = 2;
 #pragma unroll 1
-    for (int h0 = 0; h0 < p.group; h0 += 4) {
-        float M[4], L[4];
-        float4 acc[4];
+    for (int j = 0; j < rows; j += kAbreast) {
+        float M[kAbreast], L[kAbreast];
+        float4 acc[kAbreast];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < kAbreast; ++h) {
             M[h] = -INFINITY;
             L[h] = 0.f;
             acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll 1
-        for (int n = 0; n < count; n += 4) {
-            float m[4][4], l[4][4];
-            float4 o[4][4];
+        for (int n = 0; n < count; n += kAhead) {
+            float m[kAhead][kAbreast], l[kAhead][kAbreast];
+            float4 o[kAhead][kAbreast];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const bool live = n + k < count && h0 + h < p.group;
-                    const float* src = partial(p, live ? first + (n + k) * stride : first, last, live ? h0 + h : h0);
+                for (int h = 0; h < kAbreast; ++h) {
+                    const bool live = n + k < count && j + h < rows;
+                    const float* src = partial(p, live ? first + (n + k) * stride : first, last, row + (live ? j + h : j) * step);
                     m[k][h] = live ? __ldcg(src + kDim) : -INFINITY;
                     l[k][h] = live ? __ldcg(src + kDim + 1) : 0.f;
                     o[k][h] = live ? __ldcg(reinterpret_cast<const float4*>(src + 4 * lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
+            for (int h = 0; h < kAbreast; ++h) {
                 float top = M[h];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) top = fmaxf(top, m[k][h]);
+                for (int k = 0; k < kAhead; ++k) top = fmaxf(top, m[k][h]);
                 const float a = ex2(M[h] - top);
                 acc[h] = make_float4(acc[h].x * a, acc[h].y * a, acc[h].z * a, acc[h].w * a);
                 L[h] *= a;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kAhead; ++k) {
                     const float f = ex2(m[k][h] - top);
                     L[h] = fmaf(f, l[k][h], L[h]);
                     acc[h] = make_float4(fmaf(f, o[k][h].x, acc[h].x), fmaf(f, o[k][h].y, acc[h].y), fmaf(f, o[k][h].z, acc[h].z),
@@ -434,8 +411,8 @@ __device__ __forceinline__ void combine(const Decode& p, int first, int stride, 
         }
         __syncwarp();  // every lane's reads, before what emit() may put in their place
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-            if (h0 + h < p.group) emit(h0 + h, acc[h], M[h], L[h]);
+        for (int h = 0; h < kAbreast; ++h)
+            if (j + h < rows) emit(row + (j + h) * step, acc[h], M[h], L[h]);
     }
 }
 
@@ -450,8 +427,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int B = p.num_seqs, hkv = p.hkv;
-    int* scan = reinterpret_cast<int*>(smem + L::scan(p.slots));
+    const int B = p.num_seqs, runs = p.runs;
+    const int parts = kWarps / p.heads, tile_tokens = kTok * parts;  // warps of a head, tokens of a tile
+    int* scan = reinterpret_cast<int*>(smem + L::kScan);
     int* misc = reinterpret_cast<int*>(smem + L::kMisc);
     volatile int* abort_flag = misc;
     int* ends = misc + 1;
@@ -461,22 +439,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
     const uint32_t bar0 = smem_u32(smem + L::kBars);
     auto full_bar = [&](int i) { return bar0 + 8u * i; };
     auto empty_bar = [&](int i) { return bar0 + 8u * (kStages + i); };
-    auto qfull_bar = [&](int i) { return bar0 + 8u * (2 * kStages + i); };
-    auto qempty_bar = [&](int i) { return bar0 + 8u * (2 * kStages + kQSlots + i); };
-    auto mfull_bar = [&](int i) { return bar0 + 8u * (2 * kStages + 2 * kQSlots + i); };
-    auto mempty_bar = [&](int i) { return bar0 + 8u * (2 * kStages + 2 * kQSlots + 2 + i); };
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full_bar(i), 1);
-            mbar_init(empty_bar(i), 1);
-        }
-        for (int i = 0; i < kQSlots; ++i) {
-            mbar_init(qfull_bar(i), 1);
-            mbar_init(qempty_bar(i), kWarps);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(mfull_bar(i), kWarps);
-            mbar_init(mempty_bar(i), 1);
+            mbar_init(empty_bar(i), kWarps);
         }
         misc[0] = 0;
         *unknown = -1;
@@ -484,16 +450,17 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
     }
 
     // ---- plan: prefix sums of the runs' tiles, then this CTA's range ----
-    // Tile x of run i = s * hkv + g sits at cost position x + kRunCost * i; a
+    // Tile x of run i = s * runs + g sits at cost position x + kRunCost * i; a
     // CTA takes the tiles of an equal share of positions. An end of its range is
     // found by the thread that holds the sequence.
     const int per = (B + kThreads - 1) / kThreads;
     const int lo = min(B, tid * per), hi = min(B, lo + per);
+    const int tile_shift = 31 - __clz(tile_tokens);
     int local = 0;
     for (int s = lo; s < hi; ++s) {
         const int n = __ldg(p.context_lens + s);
         if (n > p.cap) atomicOr(p.err, PKV_DEVERR_CONTEXT);
-        local += (max(min(n, p.cap), 0) + kTile - 1) / kTile;
+        local += (max(min(n, p.cap), 0) + tile_tokens - 1) >> tile_shift;
         scan[s] = local;
     }
     int sum = local;
@@ -511,22 +478,22 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
         tiles += t;
         if (w < warp) before += t;
     }
-    const int cost = hkv * (tiles + kRunCost * B);
+    const int cost = runs * (tiles + kRunCost * B);
     const int share = (cost + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
     for (int s = lo, start = before; s < hi; ++s) {
         const int end = before + scan[s], nb = end - start;
         scan[s] = end;
-        const int c0 = hkv * (start + kRunCost * s), c1 = c0 + hkv * (nb + kRunCost);
+        const int c0 = runs * (start + kRunCost * s), c1 = c0 + runs * (nb + kRunCost);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int y = (static_cast<int>(blockIdx.x) + i) * share;
             if (y < c0 || y >= c1) continue;
             const int g = attn::div_small(y - c0, nb + kRunCost);
-            ends[i] = hkv * start + g * nb + min(y - c0 - g * (nb + kRunCost), nb);
+            ends[i] = runs * start + g * nb + min(y - c0 - g * (nb + kRunCost), nb);
         }
         start = end;
     }
-    if (tid < 2 && (static_cast<int>(blockIdx.x) + tid) * share >= cost) ends[tid] = hkv * tiles;
+    if (tid < 2 && (static_cast<int>(blockIdx.x) + tid) * share >= cost) ends[tid] = runs * tiles;
     __syncthreads();
     const int range_lo = ends[0], range_hi = ends[1];
 
@@ -538,65 +505,56 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
     }
     if (range_lo >= range_hi) return;
 
-    const int r = lane >> 2, c = lane & 3;
-    float* states = reinterpret_cast<float*>(smem + L::kStates);
-    attn::PieceWalk walk(scan, B, hkv, range_lo, range_hi, unknown);
+    attn::PieceWalk walk(scan, B, runs, range_lo, range_hi, unknown);
     attn::Piece pc;
-    if (warp >= kWarps && warp < kHelper) {
+    const bool blocks_of_8 = p.bt_shift == 3;
+    if (warp >= kWarps) {
         // ====================== producer warps =======================
-        // A copy costs the warp that issues it 100 to 150 cycles, and one producer
-        // took 860 a tile of four: more than the tile's time in HBM.
+        // Lanes look up where a round of copies come from, each tile's then go out
+        // from one thread, chosen by elect.sync: knowing it to be one, the compiler
+        // hands a copy its operands at once.
         const uint64_t policy = policy_evict_first();
-        const int bt = 1 << p.bt_shift;
-        const int tokens = min(bt, kTile);  // of one copy
-        const int copies = kTile / tokens;  // of one tile
-        const int ahead = 32 / copies;      // tiles whose copies' places the lanes hold
-        const uint32_t copy_bytes = tokens / kUnit * U::kBytes;
-        constexpr int kMaxCopies = kTile / 8;
+        const int ahead = 32 / p.copies;  // tiles whose copies' places the lanes hold
+        const uint32_t unit_row = static_cast<uint32_t>(p.heads) * U::kBytes;  // a unit of every head of the run
         int gi = 0, last_issued = -1;
         while (walk.next(pc)) {
             const int ctx = min(__ldg(p.context_lens + pc.s), p.cap);
             const int32_t* row = p.tables + static_cast<size_t>(pc.s) * p.width;
             for (int j0 = 0; j0 < pc.len; j0 += ahead) {
                 const int n = min(ahead, pc.len - j0);
-                const int token = (pc.blk + j0) * kTile + lane * tokens;
+                const int token = (pc.blk + j0) * tile_tokens + lane * p.copy_tokens;
                 uint64_t src = 0;
-                if (lane < n * copies && token < ctx) {
+                if (lane < n * p.copies && token < ctx) {
                     int id = __ldg(row + (token >> p.bt_shift));
                     if (id < 0 || id >= p.num_blocks) {
                         atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
                         id = 0;  // a valid block in its place; the output is flagged invalid
                     }
-                    src = reinterpret_cast<uint64_t>(p.cache) +
-                          (((static_cast<size_t>(id) * hkv + pc.g) << (p.bt_shift - 3)) + (token & (bt - 1)) / kUnit) * U::kBytes;
+                    const long long slot = (static_cast<long long>(id) << p.bt_shift) + (token & ((1 << p.bt_shift) - 1));
+                    src = reinterpret_cast<uint64_t>(p.cache) + unit_of(slot, pc.g * p.heads, p.hkv, blocks_of_8) * U::kBytes;
                 }
                 for (int j = 0; j < n; ++j, ++gi) {
                     if (gi % kProducers != warp - kWarps) continue;
                     const int st = gi % kStages;
-                    const int left = min(kTile, ctx - (pc.blk + j0 + j) * kTile);
-                    const uint32_t bytes = (left + kUnit - 1) / kUnit * U::kBytes;
+                    // whole slabs: 16 tokens (8 in blocks of 8)
+                    const int left = min(tile_tokens, ctx - (pc.blk + j0 + j) * tile_tokens);
+                    const uint32_t slabs = blocks_of_8 ? (left + 7) >> 3 : (left + 15) >> 4;
+                    const uint32_t slab_bytes = blocks_of_8 ? unit_row : 2 * unit_row;
+                    const uint32_t bytes = slabs * slab_bytes, copy_bytes = p.copy_tokens / 8 * unit_row;
                     const uint32_t full = full_bar(st), dst = smem_u32(smem + st * L::kStage);
                     const bool ok = mbar_wait(empty_bar(st), static_cast<uint32_t>((gi / kStages) & 1) ^ 1u, abort_flag, p.err);
                     if (!__all_sync(0xffffffffu, ok)) continue;
                     last_issued = gi;
-                    uint64_t from[kMaxCopies];
-#pragma unroll
-                    for (int i = 0; i < kMaxCopies; ++i)
-                        if (i < copies) from[i] = __shfl_sync(0xffffffffu, src, j * copies + i);
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(full, bytes);
-#pragma unroll
-                        for (int i = 0; i < kMaxCopies; ++i) {
-                            const uint32_t at = i * copy_bytes;
-                            if (at >= bytes) break;
-                            bulk_load(dst + at, reinterpret_cast<const void*>(from[i]), min(bytes - at, copy_bytes), full, policy);
-                        }
+                    if (elect_one()) mbar_arrive_expect_tx(full, bytes);
+                    for (uint32_t at = 0, i = j * p.copies; at < bytes; at += copy_bytes, ++i) {
+                        const uint64_t a = __shfl_sync(0xffffffffu, src, i);
+                        if (elect_one()) bulk_load(dst + at, reinterpret_cast<const void*>(a), min(bytes - at, copy_bytes), full, policy);
                     }
                 }
             }
         }
         // No copy may land after the CTA has ended. Without an abort every copy
-        // was waited for by its consumer and these waits return at once; after
+        // was waited for by its consumers and these waits return at once; after
         // one (a wait that ran out) the copies issued need not be a prefix, so
         // a grace period far longer than any copy takes comes first.
         if (lane == 0) {
@@ -612,177 +570,154 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
         return;
     }
 
-    if (warp == kHelper) {
-        // ======================== helper warp ========================
-        // The next piece's queries, then this one's results. Consumers that have
-        // few tiles of a piece read its queries themselves.
-        int slot = 0, qslot = 0;
-        uint32_t phase = 0, qphase = 0;
-        int turn = 0;  // the consumer that has the piece's first tile
-        auto prepare = [&](const attn::Piece& piece) {
-            if (piece.len < kWarps) return;
-            Queries<kGroups> q;
-            q.load(p, piece.s, piece.g, r, c);
-            if (mbar_wait(qempty_bar(qslot), qphase ^ 1u, abort_flag, p.err)) q.store(smem + L::kQueries + qslot * L::kQBytes, lane);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(qfull_bar(qslot));
-            if (++qslot == kQSlots) {
-                qslot = 0;
-                qphase ^= 1u;
+    // ======================= consumer warps =======================
+    const int r = lane >> 2, c = lane & 3;
+    const int head = warp & (p.heads - 1), part = warp / p.heads;
+    // the warp's two units in a stage
+    const int second = blocks_of_8 ? p.heads * U::kBytes : U::kBytes;
+    const int own = blocks_of_8 ? (part * 2 * p.heads + head) * U::kBytes : (part * p.heads + head) * 2 * U::kBytes;
+    float* states = reinterpret_cast<float*>(smem + L::kStates);
+    const int cta = static_cast<int>(blockIdx.x);
+    int gidx = 0;
+    while (walk.next(pc)) {
+        const int s = pc.s, nb = pc.nb;
+        const int ctx = min(__ldg(p.context_lens + s), p.cap);
+        Queries<kGroups> q;
+        q.load(p, s, pc.g * p.heads + head, r, c);
+        State<kGroups> st;
+        st.clear();
+        bool some = false;  // whether the warp has tokens of the piece
+        for (int j = 0; j < pc.len; j += kSubs) {
+            const int n = min(kSubs, pc.len - j);
+            uint8_t* at[kSubs];
+            int valid[kSubs];
+            bool landed = true, any = false, whole = true;
+#pragma unroll
+            for (int i = 0; i < kSubs; ++i) {
+                const int gi = gidx + j + i;
+                at[i] = smem + gi % kStages * L::kStage + own;
+                valid[i] = i < n ? min(kTok, ctx - (pc.blk + j + i) * tile_tokens - part * kTok) : 0;
+                any |= valid[i] > 0;
+                whole &= valid[i] == kTok;
+                if (i < n) landed &= mbar_wait(full_bar(gi % kStages), static_cast<uint32_t>((gi / kStages) & 1), abort_flag, p.err);
             }
-        };
-        attn::Piece next;
-        bool more = walk.next(next);
-        prepare(next);
-        while (more) {
-            pc = next;
-            more = walk.next(next);
-            if (more) prepare(next);
-            const int s = pc.s, g = pc.g, nb = pc.nb, some = min(kWarps, pc.len), from = turn;
-            turn = (turn + pc.len) % kWarps;
-            if (nb == 1) continue;  // its consumer writes the rows
-            const int seg = hkv * (scan[s] - nb) + g * nb + kRunCost * (s * hkv + g);
-            const int i0 = seg / share, i1 = (seg + nb - 1) / share, pieces = i1 - i0 + 1;
-            const int cta = static_cast<int>(blockIdx.x);
-            uint2* out = reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(s) * p.hq + static_cast<size_t>(g) * p.group) * kDim) + lane;
-            auto finish = [&](int h, float4 o, float, float l) { out[h * (kDim / 4)] = rounded(o, 1.f / l); };
-            auto leave = [&](float* dst, float4 o, float m, float l) {
-                *reinterpret_cast<float4*>(dst + 4 * lane) = o;
-                if (lane == 0) {
-                    dst[kDim] = m;
-                    dst[kDim + 1] = l;
+            if (whole) add_tiles<kGroups, true>(at, valid, second, q, st, lane);
+            else if (any) add_tiles<kGroups, false>(at, valid, second, q, st, lane);
+            some |= any;
+            fence_proxy_async_shared();  // this lane's accesses of the stages, before the copies that will replace them
+            __syncwarp();
+            if (lane < n && landed) mbar_arrive(empty_bar((gidx + j + lane) % kStages));
+        }
+        gidx += pc.len;
+
+        // ---- the piece's result, row by row ----
+        const int seg = runs * (scan[s] - nb) + pc.g * nb + kRunCost * (s * runs + pc.g);
+        const int i0 = seg / share, i1 = (seg + nb - 1) / share, pieces = i1 - i0 + 1;
+        __nv_bfloat16* out = p.out + (static_cast<size_t>(s) * p.hq + static_cast<size_t>(pc.g) * p.rows) * kDim;
+        // rows of this warp from here on: its head's, or every eighth of the run's
+        int row = head * p.group, step = 1, rows = p.group;
+        float mins[kGroups][2], sums[2];
+        st.rows(c, mins, sums);
+        if (parts == 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (2 * c + h >= p.group) continue;
+                const int mine = row + 2 * c + h;
+                if (pieces == 1) {
+                    const float inv = 1.f / sums[h];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        *reinterpret_cast<uint2*>(out + mine * kDim + 32 * w + 4 * r) = rounded(st.row(w, h, mins), inv);
+                } else {
+                    float* dst = partial(p, cta, i1, mine);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) *reinterpret_cast<float4*>(dst + 32 * w + 4 * r) = st.row(w, h, mins);
+                    if (r == 0) {
+                        dst[kDim] = st.base[h];
+                        dst[kDim + 1] = sums[h];
+                    }
                 }
-            };
-            mbar_wait(mfull_bar(slot), phase, abort_flag, p.err);
-            const float* held = states + slot * kStateFloats;
-#pragma unroll 2
-            for (int h = 0; h < p.group; ++h) {
-                float m[kWarps], M = -INFINITY, l = 0.f;
+            }
+        } else {
+            // the warps of a head through shared memory; all have read the last piece's states
+            named_barrier_sync(1, kConsumers);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float* dst = states + (warp * kMaxG + 2 * c + h) * kORow;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) *reinterpret_cast<float4*>(dst + 32 * w + 4 * r) = st.row(w, h, mins);
+                if (r == 0) {
+                    dst[kDim] = some ? st.base[h] : -INFINITY;
+                    dst[kDim + 1] = some ? sums[h] : 0.f;
+                }
+            }
+            named_barrier_sync(1, kConsumers);
+            row = warp;
+            step = kWarps;
+            rows = (p.rows - warp + kWarps - 1) / kWarps;
+            for (int j = 0; j < rows; ++j) {
+                const int mine = row + j * step, of = mine / p.group, h = mine - of * p.group;
+                float M = -INFINITY, l = 0.f;
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) {  // consumers from, from + 1, ... hold tiles of the piece
-                    const int w = from + k < kWarps ? from + k : from + k - kWarps;
-                    m[k] = k < some ? held[(w * kMaxG + h) * kORow + kDim] : -INFINITY;
-                    M = fmaxf(M, m[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    if (k >= some) continue;
-                    const int w = from + k < kWarps ? from + k : from + k - kWarps;
-                    const float* src = held + (w * kMaxG + h) * kORow;
-                    const float f = ex2(m[k] - M);
+                for (int k = 0; k < parts; ++k) M = fmaxf(M, states[((k * p.heads + of) * kMaxG + h) * kORow + kDim]);
+                for (int k = 0; k < parts; ++k) {
+                    const float* src = states + ((k * p.heads + of) * kMaxG + h) * kORow;
+                    if (src[kDim + 1] == 0.f) continue;  // a part without tokens
+                    const float f = ex2(src[kDim] - M);
                     const float4 v = *reinterpret_cast<const float4*>(src + 4 * lane);
                     l = fmaf(f, src[kDim + 1], l);
                     o = make_float4(fmaf(f, v.x, o.x), fmaf(f, v.y, o.y), fmaf(f, v.z, o.z), fmaf(f, v.w, o.w));
                 }
-                if (pieces == 1) finish(h, o, M, l);
-                else leave(partial(p, cta, i1, h), o, M, l);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(mempty_bar(slot));
-            if (++slot == p.slots) {
-                slot = 0;
-                phase ^= 1u;
-            }
-            if (pieces == 1) continue;
-            // true for the last of `count` that come here
-            auto last = [&](int* ctr, int count) {
-                __syncwarp();  // every lane's stores, before lane 0's release
-                int old = 0;
-                if (lane == 0) {
-                    old = atom_add_acq_rel_gpu(ctr, 1);
-                    if (old == count - 1) *ctr = 0;  // ready for the next launch
-                }
-                old = __shfl_sync(0xffffffffu, old, 0);
-                __syncwarp();
-                return old == count - 1;
-            };
-            int stride = 1;
-            if (pieces > kMergeGroup) {
-                stride = kMergeGroup;
-                const int base = i0 + (cta - i0) / kMergeGroup * kMergeGroup;
-                const int count = min(kMergeGroup, i1 - base + 1);
-                if (count > 1) {  // else a lone piece, its group's result already
-                    if (!last(p.group_counters + base, count)) continue;
-                    combine(p, base, 1, count, i1, lane,
-                            [&](int h, float4 o, float m, float l) { leave(partial(p, base, i1, h), o, m, l); });
+                if (pieces == 1) {
+                    reinterpret_cast<uint2*>(out + mine * kDim)[lane] = rounded(o, 1.f / l);
+                } else {
+                    float* dst = partial(p, cta, i1, mine);
+                    *reinterpret_cast<float4*>(dst + 4 * lane) = o;
+                    if (lane == 0) {
+                        dst[kDim] = M;
+                        dst[kDim + 1] = l;
+                    }
                 }
             }
-            const int count = (pieces + stride - 1) / stride;
-            if (last(p.counters + i0, count)) combine(p, i0, stride, count, i1, lane, finish);
         }
-        return;
-    }
+        if (pieces == 1) continue;
 
-    // ======================= consumer warps =======================
-    int gidx = 0, slot = 0, qslot = 0;
-    uint32_t phase = 0, qphase = 0;
-    while (walk.next(pc)) {
-        const int s = pc.s, g = pc.g;
-        const int ctx = min(__ldg(p.context_lens + s), p.cap);
-        const int turn = gidx % kWarps;
-        const int first = warp >= turn ? warp - turn : warp + kWarps - turn;
-        const bool mine = first < pc.len;
-        Queries<kGroups> q;
-        if (pc.len >= kWarps) {
-            const bool landed = mbar_wait(qfull_bar(qslot), qphase, abort_flag, p.err);
-            q.fetch(smem + L::kQueries + qslot * L::kQBytes, lane);
+        // ---- a run that is cut: the last of the warps with these rows combines them ----
+        auto last = [&](unsigned long long* ctr, int count) {
+            __syncwarp();  // every lane's stores, before lane 0's release
+            uint64_t old = 0;
+            if (lane == 0) {
+                old = atom_add_acq_rel_gpu(ctr, uint64_t(1) << (8 * warp));
+                old = (old >> (8 * warp)) & 255u;
+                if (static_cast<int>(old) == count - 1)  // ready for the next launch
+                    atomicAdd(ctr, 0ull - (static_cast<unsigned long long>(count) << (8 * warp)));
+            }
+            const int seen = __shfl_sync(0xffffffffu, static_cast<int>(old), 0);
             __syncwarp();
-            if (lane == 0 && landed) mbar_arrive(qempty_bar(qslot));
-            if (++qslot == kQSlots) {
-                qslot = 0;
-                qphase ^= 1u;
-            }
-        } else if (mine) {
-            q.load(p, s, g, r, c);
-        }
-        State<kGroups> st;
-        st.clear();
-        for (int j = first; j < pc.len; j += kWarps) {
-            const int gi = gidx + j, stage = gi % kStages;
-            const bool landed = mbar_wait(full_bar(stage), static_cast<uint32_t>((gi / kStages) & 1), abort_flag, p.err);
-            add_tile<kGroups>(smem + stage * L::kStage, min(kTile, ctx - (pc.blk + j) * kTile), q, st, lane);
-            fence_proxy_async_shared();  // this lane's accesses of the stage, before the copy that will replace it
-            __syncwarp();
-            if (lane == 0 && landed) mbar_arrive(empty_bar(stage));
-        }
-        gidx += pc.len;
-        if (pc.nb == 1) {  // a run of one tile: its warp writes the rows
-            if (!mine) continue;
-            float mins[kGroups][2], sums[2];
-            st.rows(c, mins, sums);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (2 * c + h >= p.group) continue;
-                const float inv = 1.f / sums[h];
-                __nv_bfloat16* row = p.out + (static_cast<size_t>(s) * p.hq + static_cast<size_t>(g) * p.group + 2 * c + h) * kDim;
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    *reinterpret_cast<uint2*>(row + 32 * w + 4 * r) = rounded(st.row(w, h, mins), inv);
-            }
-            continue;
-        }
-        mbar_wait(mempty_bar(slot), phase ^ 1u, abort_flag, p.err);
-        if (mine) {
-            float mins[kGroups][2], sums[2];
-            st.rows(c, mins, sums);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float* dst = states + slot * kStateFloats + (warp * kMaxG + 2 * c + h) * kORow;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) *reinterpret_cast<float4*>(dst + 32 * w + 4 * r) = st.row(w, h, mins);
-                if (r == 0) {
-                    dst[kDim] = st.base[h];
-                    dst[kDim + 1] = sums[h];
-                }
+            return seen == count - 1;
+        };
+        int stride = 1;
+        if (pieces > kMergeGroup) {
+            stride = kMergeGroup;
+            const int base = i0 + (cta - i0) / kMergeGroup * kMergeGroup;
+            const int count = min(kMergeGroup, i1 - base + 1);
+            if (count > 1) {  // else a lone piece, its group's result already
+                if (!last(p.group_counters + base, count)) continue;
+                combine(p, base, 1, count, i1, row, step, rows, lane, [&](int i, float4 o, float m, float l) {
+                    float* dst = partial(p, base, i1, i);
+                    *reinterpret_cast<float4*>(dst + 4 * lane) = o;
+                    if (lane == 0) {
+                        dst[kDim] = m;
+                        dst[kDim + 1] = l;
+                    }
+                });
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(mfull_bar(slot));
-        if (++slot == p.slots) {
-            slot = 0;
-            phase ^= 1u;
-        }
+        const int count = (pieces + stride - 1) / stride;
+        if (!last(p.counters + i0, count)) continue;
+        combine(p, i0, stride, count, i1, row, step, rows, lane, [&](int i, float4 o, float, float l) {
+            reinterpret_cast<uint2*>(out + i * kDim)[lane] = rounded(o, 1.f / l);
+        });
     }
 }
 

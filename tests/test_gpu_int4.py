@@ -226,7 +226,7 @@ def _batch(rng, lens, blocks, bt):
 def _poison(pool, tables, lens, bt):
     """NaN scales and full codes behind every context and in unused blocks."""
     d = pool.cache.data
-    blocks, hkv, _ = d.shape
+    blocks, hkv = d.shape[0], d.shape[2]
     live = np.zeros((blocks, bt), bool)
     for row, n in zip(tables, lens):
         t = np.arange(n)

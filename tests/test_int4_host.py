@@ -68,7 +68,8 @@ def _cache(pkv, blocks=4, hkv=2, bt=16, gd=64):
 
 def test_the_cache_object(pkv):
     c = _cache(pkv)
-    assert c.data.shape == (4, 2, 2 * 1152) and c.data.dtype == torch.uint8 and not c.data.any()
+    assert _cache(pkv, bt=64).data.shape == (4, 4, 2, 2 * 1152) and _cache(pkv, bt=8, gd=128).data.shape == (4, 1, 2, 1088)
+    assert c.data.shape == (4, 1, 2, 2 * 1152) and c.data.dtype == torch.uint8 and not c.data.any()
     for bad in (dict(blocks=0), dict(hkv=0), dict(bt=24), dict(gd=48)):
         with pytest.raises(ValueError):
             _cache(pkv, **bad)

@@ -50,8 +50,19 @@ def test_halves_round_to_even():
 def test_bytes(group_dims):
     tokens, groups = 16, 128 // group_dims
     k, v = (int4.quantise(_rows(seed, tokens, 128), group_dims) for seed in (1, 2))
-    got = int4.pack(k, v)
+    one = [[x[None] for x in kv] for kv in (k, v)]  # one head
+    got = int4.pack(*one)
     unit = 1024 + 64 * groups
+    assert got.shape == (1, 1, 2 * unit)
+    # slabs of 16 tokens (8 in a block of 8), in each the heads
+    heads = [[np.stack([x, x[::-1]]) for x in kv] for kv in (k, v)]
+    eight = int4.pack(*[[x[:, :8] for x in kv] for kv in heads])
+    assert eight.shape == (1, 2, unit) and np.array_equal(eight[0, 0], got[0, 0, :unit])
+    twice = int4.pack(*[[np.concatenate([x, x[:, ::-1]], axis=1) for x in kv] for kv in heads])
+    assert twice.shape == (2, 2, 2 * unit)
+    assert np.array_equal(twice[0, 0], got[0, 0]) and np.array_equal(twice[1, 1], got[0, 0])
+    assert np.array_equal(twice[0, 1], twice[1, 0]) and not np.array_equal(twice[0, 0], twice[0, 1])
+    got = got[0, 0]
     want = np.zeros(2 * unit, np.uint8)
 
     def nibble(byte, high, code):
