@@ -420,7 +420,7 @@ pkv_status pkv_attn_tree(const void* q, const void* k_draft, const void* v_draft
  *   many CTAs as run at once in pkv_attn_int4_workspace_size() bytes, whatever
  *   the batch (0 when no device is present); fewer bytes are taken as they are
  *   and make fewer CTAs do the work, less than one CTA's share is refused
- *   (PKV_EINVAL). num_ctas: as there, at most 1,536. fp32 sums and softmax; the
+ *   (PKV_EINVAL). num_ctas: as there, at most 512. fp32 sums and softmax; the
  *   weights enter the product with the values in fp16. What lies behind a
  *   context in its last block, NaN scales included, never reaches the output.
  */

@@ -91,9 +91,8 @@ pkv_status pkv_attn_decode_int4(const void* q, const void* cache, const int32_t*
         return PKV_EINVAL;
     const int resident = kv4::resident_ctas(groups, num_seqs);
     if (resident < 1) return PKV_ECUDA;
-    // No more CTAs than the tables can hold work for: a run's cost each.
-    int grid = num_ctas > 0 ? num_ctas
-                            : static_cast<int>(std::max<long long>(1, std::min<long long>(resident, cost / (kv4::kRunCost + 1))));
+    // No more CTAs than leave each the tiles that its consumers take at a time.
+    int grid = num_ctas > 0 ? num_ctas : static_cast<int>(std::min<long long>(resident, (cost + kv4::kSubs - 1) / kv4::kSubs));
     const size_t each = kv4::partial_bytes(p.rows);
     if (workspace_bytes < attn::kWsFixed + each) return PKV_EINVAL;
     const size_t fit = (workspace_bytes - attn::kWsFixed) / each;
@@ -123,8 +122,20 @@ pkv_status pkv_attn_decode_int4(const void* q, const void* cache, const int32_t*
     p.counters = reinterpret_cast<unsigned long long*>(ws + attn::kWsHeader);
     p.group_counters = p.counters + kv4::kMaxCtas;
     p.partials = reinterpret_cast<float*>(ws + attn::kWsFixed);
-    kv4::kernel_for(groups)<<<grid, kv4::kThreads, kv4::smem_for(groups, num_seqs), as_stream(stream)>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    // Launched early (programmatic stream serialization): the kernel sets itself up
+    // while the one before it ends, then waits for it.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kv4::kThreads);
+    cfg.dynamicSmemBytes = kv4::smem_for(groups, num_seqs);
+    cfg.stream = as_stream(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kv4::kernel_for(groups), p);
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return PKV_ECUDA;

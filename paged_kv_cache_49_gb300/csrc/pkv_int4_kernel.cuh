@@ -57,14 +57,14 @@ static_assert(kStages % kSubs == 0 && kStages % kProducers == 0, "each stage is 
 constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + kProducers * 32;
 // Work partition: what a run costs beyond its tiles, in tiles.
-constexpr int kRunCost = 2;
-// Runs of more pieces than this are combined in two levels.
+constexpr int kRunCost = 4;
+// Runs of more pieces than this are combined in two levels, each of up to 32.
 constexpr int kMergeGroup = 16;
 // Counters of a launch, 64 bits with one byte a warp, in the workspace's region
 // of counters: per CTA one for the cut run, and one for the group of its pieces,
 // whose first piece is the CTA's (at most one: the last run of its range).
-constexpr int kMaxCtas = static_cast<int>(attn::kWsCounterBytes / 16);
-static_assert(kMaxCtas / kMergeGroup < 256 && kMergeGroup < 256, "a count fits a byte");
+constexpr int kMaxCtas = 32 * kMergeGroup;
+static_assert(2 * kMaxCtas * 8 <= static_cast<int>(attn::kWsCounterBytes), "the counters fit their region");
 
 constexpr int kORow = attn::kORow;
 constexpr int kStateFloats = kWarps * kMaxG * kORow;  // output, max and sum of every warp's rows
@@ -360,53 +360,52 @@ __device__ __forceinline__ float* partial(const Decode& p, int cta, int last, in
     return p.partials + ((static_cast<size_t>(cta) * 2 + (cta == last ? 0 : 1)) * p.rows + row) * kORow;
 }
 
-// `count` partial results of rows row, row + step, ... (`rows` of them), `stride`
-// CTAs apart from CTA `first` on, combined; emit(row, four dims from 4 lane on,
-// max, sum). Four of two rows are on their way at a time.
+// `count` (at most 32) partial results of rows row, row + step, ... (`rows` of them),
+// `stride` CTAs apart from CTA `first` on, combined; emit(row, four dims from 4 lane
+// on, max, sum). Lane k holds partial result k's maxima and sums of all rows, which
+// come first; then four results of four rows are on their way at a time.
 template <class Emit>
 __device__ __forceinline__ void combine(const Decode& p, int first, int stride, int count, int last, int row, int step, int rows,
                                         int lane, Emit emit) {
-    constexpr int kAhead = 4, kAbreast = 2;
+    constexpr int kAhead = 4, kAbreast = 4;
+    const int cta = first + min(lane, count - 1) * stride;
 #pragma unroll 1
     for (int j = 0; j < rows; j += kAbreast) {
-        float M[kAbreast], L[kAbreast];
+        float2 ml[kAbreast];
+#pragma unroll
+        for (int h = 0; h < kAbreast; ++h)
+            ml[h] = __ldcg(reinterpret_cast<const float2*>(partial(p, cta, last, row + min(j + h, rows - 1) * step) + kDim));
+        float M[kAbreast], L[kAbreast], weight[kAbreast];
         float4 acc[kAbreast];
 #pragma unroll
         for (int h = 0; h < kAbreast; ++h) {
-            M[h] = -INFINITY;
-            L[h] = 0.f;
+            M[h] = lane < count ? ml[h].x : -INFINITY;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) M[h] = fmaxf(M[h], __shfl_xor_sync(0xffffffffu, M[h], d));
+            weight[h] = lane < count ? ex2(ml[h].x - M[h]) : 0.f;
+            L[h] = lane < count ? weight[h] * ml[h].y : 0.f;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) L[h] += __shfl_xor_sync(0xffffffffu, L[h], d);
             acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll 1
         for (int n = 0; n < count; n += kAhead) {
-            float m[kAhead][kAbreast], l[kAhead][kAbreast];
             float4 o[kAhead][kAbreast];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
 #pragma unroll
+                for (int h = 0; h < kAbreast; ++h)
+                    o[k][h] = __ldcg(reinterpret_cast<const float4*>(partial(p, first + min(n + k, count - 1) * stride, last,
+                                                                             row + min(j + h, rows - 1) * step) + 4 * lane));
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (n + k >= count) break;
+#pragma unroll
                 for (int h = 0; h < kAbreast; ++h) {
-                    const bool live = n + k < count && j + h < rows;
-                    const float* src = partial(p, live ? first + (n + k) * stride : first, last, row + (live ? j + h : j) * step);
-                    m[k][h] = live ? __ldcg(src + kDim) : -INFINITY;
-                    l[k][h] = live ? __ldcg(src + kDim + 1) : 0.f;
-                    o[k][h] = live ? __ldcg(reinterpret_cast<const float4*>(src + 4 * lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-#pragma unroll
-            for (int h = 0; h < kAbreast; ++h) {
-                float top = M[h];
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) top = fmaxf(top, m[k][h]);
-                const float a = ex2(M[h] - top);
-                acc[h] = make_float4(acc[h].x * a, acc[h].y * a, acc[h].z * a, acc[h].w * a);
-                L[h] *= a;
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    const float f = ex2(m[k][h] - top);
-                    L[h] = fmaf(f, l[k][h], L[h]);
+                    const float f = __shfl_sync(0xffffffffu, weight[h], n + k);
                     acc[h] = make_float4(fmaf(f, o[k][h].x, acc[h].x), fmaf(f, o[k][h].y, acc[h].y), fmaf(f, o[k][h].z, acc[h].z),
                                          fmaf(f, o[k][h].w, acc[h].w));
                 }
-                M[h] = top;
             }
         }
         __syncwarp();  // every lane's reads, before what emit() may put in their place
@@ -433,9 +432,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
     int* misc = reinterpret_cast<int*>(smem + L::kMisc);
     volatile int* abort_flag = misc;
     int* ends = misc + 1;
-    int* unknown = misc + 3;  // the walk's first piece: left to its search
-    int* warp_total = misc + 4;
-    static_assert(4 + kThreads / 32 <= 16, "the warps' totals fit");
+    int* first_piece = misc + 3;  // sequence (or -1), run, tile, place on the line
+    int* warp_total = misc + 7;
+    static_assert(7 + kThreads / 32 <= 16, "the warps' totals fit");
     const uint32_t bar0 = smem_u32(smem + L::kBars);
     auto full_bar = [&](int i) { return bar0 + 8u * i; };
     auto empty_bar = [&](int i) { return bar0 + 8u * (kStages + i); };
@@ -445,9 +444,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
             mbar_init(empty_bar(i), kWarps);
         }
         misc[0] = 0;
-        *unknown = -1;
+        first_piece[0] = -1;
         fence_barrier_init();
     }
+    // Launched early, behind kernels that may write what is read from here on.
+    griddep_launch_dependents();
+    griddep_wait();
 
     // ---- plan: prefix sums of the runs' tiles, then this CTA's range ----
     // Tile x of run i = s * runs + g sits at cost position x + kRunCost * i; a
@@ -484,12 +486,38 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
         const int end = before + scan[s], nb = end - start;
         scan[s] = end;
         const int c0 = runs * (start + kRunCost * s), c1 = c0 + runs * (nb + kRunCost);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int y = (static_cast<int>(blockIdx.x) + i) * share;
-            if (y < c0 || y >= c1) continue;
-            const int g = attn::div_small(y - c0, nb + kRunCost);
-            ends[i] = runs * start + g * nb + min(y - c0 - g * (nb + kRunCost), nb);
+        const int y0 = static_cast<int>(blockIdx.x) * share, y1 = y0 + share;
+        // the first tile at or behind cost position y, within this sequence: its run and its place in it
+        auto tile_at = [&](int y, int& g) {
+            g = attn::div_small(y - c0, nb + kRunCost);
+            return min(y - c0 - g * (nb + kRunCost), nb);
+        };
+        int g, at;
+        if (y0 >= c0 && y0 < c1) {
+            at = tile_at(y0, g);
+            ends[0] = runs * start + g * nb + at;
+        }
+        if (y1 >= c0 && y1 < c1) {
+            at = tile_at(y1, g);
+            const int end_tile = runs * start + g * nb + at;
+            ends[1] = end_tile;
+            // The walk's first piece is the part of the range in the run that holds
+            // its last tile; where that is this sequence's, nobody searches for it.
+            if (at == 0) --g;
+            if (nb > 0 && g >= 0) {
+                const int seg = runs * start + g * nb;
+                int split = seg, g0;
+                if (y0 >= c0) {
+                    const int in_run = tile_at(y0, g0);
+                    split = max(seg, runs * start + g0 * nb + in_run);
+                }
+                if (split < end_tile) {
+                    first_piece[0] = s;
+                    first_piece[1] = g;
+                    first_piece[2] = split - seg;
+                    first_piece[3] = split;
+                }
+            }
         }
         start = end;
     }
@@ -505,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
     }
     if (range_lo >= range_hi) return;
 
-    attn::PieceWalk walk(scan, B, runs, range_lo, range_hi, unknown);
+    attn::PieceWalk walk(scan, B, runs, range_lo, range_hi, first_piece);
     attn::Piece pc;
     const bool blocks_of_8 = p.bt_shift == 3;
     if (warp >= kWarps) {
