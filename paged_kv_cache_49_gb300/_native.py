@@ -813,63 +813,63 @@ def _need_cache(cache: Int4Cache) -> int:
     return cache._device
 
 
-def _need_pairs(device: int, pairs) -> int:
-    _need_all(device, ((pairs, _I32, "pairs"),))
-    if pairs.numel() and (pairs.dim() != 2 or pairs.shape[1] != 2):
+def _pairs(pairs) -> int:
+    n = pairs.numel()
+    if n and (pairs.dim() != 2 or pairs.shape[1] != 2):
         raise ValueError("pairs must be [n, 2]")
-    return pairs.shape[0] if pairs.numel() else 0
-
-
-def _need_error_word(device: int, device_error) -> int | None:
-    if device_error is None:
-        return None
-    _need_all(device, ((device_error, _I32, "device_error"),))
-    return device_error.data_ptr()
+    return n // 2
 
 
 def append_int4(k, v, slot_mapping, cache: Int4Cache, device_error=None, stream=None) -> None:
     """Quantise k[i], v[i] ([T, Hkv, 128] bf16, possibly views of one fused
     projection) into slot slot_mapping[i] (int64; negative: a padding row)."""
     device = _need_cache(cache)
-    _need_all(device, ((slot_mapping, _I64, "slot_mapping"),))
+    st = _here(device, stream)
+    if st is None:
+        with _LaunchOn(device, stream):
+            return append_int4(k, v, slot_mapping, cache, device_error)
+    tensors, err = ((slot_mapping, _I64, "slot_mapping"),), None
+    if device_error is not None:
+        tensors, err = tensors + ((device_error, _I32, "device_error"),), device_error.data_ptr()
+    _need_all(device, tensors)
     if k.dim() != 3 or v.dim() != 3:
         raise ValueError("k, v must be [T, Hkv, 128]")
-    T, hkv = slot_mapping.numel(), cache.num_kv_heads
-    ks = _need_rows(device, k, "k", T, hkv, HEAD_DIM)
-    vs = _need_rows(device, v, "v", T, hkv, HEAD_DIM)
-    err = _need_error_word(device, device_error)
-    st = _here(device, stream)
-    with contextlib.nullcontext(st) if st is not None else _LaunchOn(device, stream) as st:
-        _check(_lib.pkv_append_int4(k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T, cache._ptr,
-                                    cache.num_blocks, *cache._shape, err, st), "pkv_append_int4")
+    T, (hkv, d, bt, gd) = slot_mapping.numel(), cache._shape
+    ks, vs = _need_rows(device, k, "k", T, hkv, d), _need_rows(device, v, "v", T, hkv, d)
+    _check(_lib.pkv_append_int4(k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T, cache._ptr, cache.num_blocks,
+                                hkv, d, bt, gd, err, st), "pkv_append_int4")
 
 
 def load_int4(cache: Int4Cache, pairs, k_cache, v_cache, device_error=None, stream=None) -> None:
     """Block pairs[i, 0] of the 4-bit cache as bf16 rows into block pairs[i, 1] of
     k_cache and v_cache [blocks, Hkv, block_tokens, 128]."""
     device = _need_cache(cache)
-    _need_all(device, ((k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache")))
-    n = _need_pairs(device, pairs)
-    hkv, d, bt, _ = cache._shape
-    if k_cache.dim() != 4 or k_cache.shape[1:] != (hkv, bt, d) or v_cache.shape != k_cache.shape:
-        raise ValueError(f"k_cache, v_cache must be {['blocks', hkv, bt, d]} and alike")
-    err = _need_error_word(device, device_error)
-    if n == 0:
-        return
     st = _here(device, stream)
-    with contextlib.nullcontext(st) if st is not None else _LaunchOn(device, stream) as st:
+    if st is None:
+        with _LaunchOn(device, stream):
+            return load_int4(cache, pairs, k_cache, v_cache, device_error)
+    tensors, err = ((k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache"), (pairs, _I32, "pairs")), None
+    if device_error is not None:
+        tensors, err = tensors + ((device_error, _I32, "device_error"),), device_error.data_ptr()
+    _need_all(device, tensors)
+    n, (hkv, d, bt, gd), shape = _pairs(pairs), cache._shape, k_cache.shape
+    if len(shape) != 4 or shape[1:] != (hkv, bt, d) or v_cache.shape != shape:
+        raise ValueError(f"k_cache, v_cache must be {['blocks', hkv, bt, d]} and alike")
+    if n:
         _check(_lib.pkv_load_int4(cache._ptr, pairs.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(), cache.num_blocks,
-                                  k_cache.shape[0], *cache._shape, err, st), "pkv_load_int4")
+                                  shape[0], hkv, d, bt, gd, err, st), "pkv_load_int4")
 
 
 def block_copy_int4(cache: Int4Cache, pairs, device_error=None, stream=None) -> None:
     """Copy physical block pairs[i, 0] of the cache onto pairs[i, 1]."""
     device = _need_cache(cache)
-    n = _need_pairs(device, pairs)
-    err = _need_error_word(device, device_error)
+    _need_all(device, ((pairs, _I32, "pairs"),))
+    if device_error is not None:
+        _need_all(device, ((device_error, _I32, "device_error"),))
+    n = _pairs(pairs)
     with _launch_on(device, stream) as st:
-        _check(_lib.pkv_block_copy_int4(cache._ptr, pairs.data_ptr(), n, cache.num_blocks, *cache._shape, err, st),
-               "pkv_block_copy_int4")
+        _check(_lib.pkv_block_copy_int4(cache._ptr, pairs.data_ptr(), n, cache.num_blocks, *cache._shape, _ptr(device_error),
+                                        st), "pkv_block_copy_int4")
 
 
 def attn_decode_int4(q, cache: Int4Cache, block_tables, context_lens, scale, out=None, workspace=None, num_ctas: int = 0,
@@ -879,30 +879,32 @@ def attn_decode_int4(q, cache: Int4Cache, block_tables, context_lens, scale, out
     errors are not reported."""
     device = q.get_device()
     _need_all(device, ((q, _BF16, "q"), (block_tables, _I32, "block_tables"), (context_lens, _I32, "context_lens")))
+    st = _here(device, stream)
+    if st is None:
+        with _LaunchOn(device, stream):
+            return attn_decode_int4(q, cache, block_tables, context_lens, scale, out, workspace, num_ctas)
     if cache._device != device:
         raise ValueError(f"the cache is on {cache.data.device}, other tensors on cuda:{device}")
-    shape = q.shape
+    shape, tables = q.shape, block_tables.shape
     if len(shape) != 3 or shape[2] != HEAD_DIM:
         raise ValueError("q must be [B, Hq, 128]")
     B, hq, d = shape
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+    if len(tables) != 2 or tables[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [B, W] and context_lens [B]")
-    if out is not None:
+    hkv, _, bt, gd = cache._shape
+    if out is None:
+        out = torch.empty_like(q)
+    else:
         _need_all(device, ((out, _BF16, "out"),))
         if out.shape != shape:
             raise ValueError("out must be shaped like q")
-    if workspace is not None and workspace.tensor.get_device() != device:
+    if workspace is None:
+        workspace = AttentionWorkspace(B, hkv, device=q.device)
+    elif workspace.tensor.get_device() != device:
         raise ValueError(f"the workspace is on {workspace.tensor.device}, the tensors on cuda:{device}")
-    st = _here(device, stream)
-    with contextlib.nullcontext(st) if st is not None else _LaunchOn(device, stream) as st:
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None:
-            workspace = AttentionWorkspace(B, cache.num_kv_heads, device=q.device, stream=st)
-        hkv, _, bt, gd = cache._shape
-        _check(_lib.pkv_attn_decode_int4(q.data_ptr(), cache._ptr, block_tables.data_ptr(), block_tables.shape[1],
-                                         context_lens.data_ptr(), B, hq, hkv, d, cache.num_blocks, bt, gd, scale, num_ctas,
-                                         workspace.ptr, workspace.int4_nbytes, out.data_ptr(), st), "pkv_attn_decode_int4")
+    _check(_lib.pkv_attn_decode_int4(q.data_ptr(), cache._ptr, block_tables.data_ptr(), tables[1], context_lens.data_ptr(), B,
+                                     hq, hkv, d, cache.num_blocks, bt, gd, scale, num_ctas, workspace.ptr,
+                                     workspace.int4_nbytes, out.data_ptr(), st), "pkv_attn_decode_int4")
     return out
 
 
@@ -956,6 +958,10 @@ def beam_select(logits, scores, finished=None, eos: int = -1, history=None, leng
     if logits.dtype not in (_BF16, _F32) or logits.dim() != 2:
         raise ValueError(f"logits must be bf16 or fp32 [groups * beams, vocab], got {logits.dtype} {list(logits.shape)}")
     _need_all(device, ((scores, _F32, "scores"),))
+    st = _here(device, stream)
+    if st is None:
+        with _LaunchOn(device, stream):
+            return beam_select(logits, scores, finished, eos, history, lengths, candidates, out, workspace, device_error)
     rows, vocab = logits.shape
     shape = scores.shape
     if len(shape) != 2 or rows != shape[0] * shape[1] or rows == 0:
@@ -985,18 +991,17 @@ def beam_select(logits, scores, finished=None, eos: int = -1, history=None, leng
             raise ValueError("out's histories must not be the beams'")
     if workspace is not None and workspace.device != device:
         raise ValueError(f"the workspace is on cuda:{workspace.device}, the tensors on cuda:{device}")
-    err = _need_error_word(device, device_error)
-    st = _here(device, stream)
-    with contextlib.nullcontext(st) if st is not None else _LaunchOn(device, stream) as st:
-        if out is None:
-            out = BeamBuffers(groups, n, room, device=logits.device)
-        if workspace is None:
-            workspace = BeamWorkspace(groups, beams, n, vocab, device=logits.device)
-        so, to, po, fo, lo, ho = out._ptrs
-        _check(_lib.pkv_beam_select(logits.data_ptr(), logits.stride(0) if groups * beams > 1 else vocab,
-                                    2 if logits.dtype is _BF16 else 4, scores.data_ptr(), _ptr(finished), eos, groups, beams, n,
-                                    vocab, _ptr(history), _ptr(lengths), room, so, to, po, fo, lo if room else None,
-                                    ho if room else None, workspace.ptr, workspace.nbytes, err, st), "pkv_beam_select")
+    if device_error is not None:
+        _need_all(device, ((device_error, _I32, "device_error"),))
+    if out is None:
+        out = BeamBuffers(groups, n, room, device=logits.device)
+    if workspace is None:
+        workspace = BeamWorkspace(groups, beams, n, vocab, device=logits.device)
+    so, to, po, fo, lo, ho = out._ptrs
+    _check(_lib.pkv_beam_select(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, 2 if logits.dtype is _BF16 else 4,
+                                scores.data_ptr(), _ptr(finished), eos, groups, beams, n, vocab, _ptr(history), _ptr(lengths),
+                                room, so, to, po, fo, lo if room else None, ho if room else None, workspace.ptr,
+                                workspace.nbytes, _ptr(device_error), st), "pkv_beam_select")
     return out
 
 
