@@ -56,50 +56,81 @@ struct Append {
     uint32_t* err;
 };
 
-constexpr float kNear = 0.5f - 0x1p-14f;
+// Of both 16-bit halves, as whole numbers.
+__device__ __forceinline__ uint32_t min_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 
-// The codes (value e in bits 4 e .. + 3) of which some may be off, by the
-// definition -- one division and one rounding -- where the quotient by the
-// reciprocal r is near a half. One that leaves the range spoils the others' places.
-__device__ __noinline__ uint32_t corrected(uint32_t word, uint4 raw, float m, float s, float r) {
-    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-    unsigned which = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float q = __fsub_rn(e & 1 ? bf16_hi(u[e / 2]) : bf16_lo(u[e / 2]), m) * r;
-        if (!(fabsf(q - rintf(q)) < kNear)) which |= 1u << e;
-        if (!(q > -0.25f && q < 15.25f)) which |= 0xffu;
-    }
-    for (; which; which &= which - 1) {
-        const int e = __ffs(static_cast<int>(which)) - 1;
-        const uint32_t pair = e < 4 ? (e < 2 ? u[0] : u[1]) : (e < 6 ? u[2] : u[3]);
-        const float t = __fsub_rn(e & 1 ? bf16_hi(pair) : bf16_lo(pair), m);
-        const uint32_t code = static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(t, s)), 0.f), 15.f));
-        word = (word & ~(15u << (4 * e))) | code << (4 * e);
+constexpr float kMargin = 0x1p-14f;  // 4 of a quotient's 2^16 parts
+constexpr uint32_t kNear = 8;        // parts: twice the margin
+
+__device__ __forceinline__ float value_of(const uint4& raw, int e) {
+    const uint32_t u = e < 4 ? (e < 2 ? raw.x : raw.y) : (e < 6 ? raw.z : raw.w);
+    return e & 1 ? bf16_hi(u) : bf16_lo(u);
+}
+
+// All eight codes (value e in bits 4 e .. + 3) by the definition: one difference,
+// one division, one rounding.
+__device__ __noinline__ uint32_t divided(uint4 raw, float m, float s) {
+    uint32_t word = 0;
+#pragma unroll 1
+    for (int e = 7; e >= 0; --e) {
+        const float q = rintf(__fdiv_rn(__fsub_rn(value_of(raw, e), m), s));
+        word = word << 4 | static_cast<uint32_t>(fminf(fmaxf(q, 0.f), 15.f));
     }
     return word;
 }
 
-// A row's 8 values of this lane as codes, and its group's scale and minimum, over
-// which the group's kLanes lanes agree: what bounds the append is the number of
-// its operations (27 a value as first written, 41 us for 16,411 tokens of 8
-// heads; 12 as below), so
+// The codes whose sums y = x r + from (see below) are near a half: code c was
+// rounded up from about h = c - 1/2, and stays where t / s > h, or = h and c is
+// even. t and s h are fp32 numbers (s has 11 bits, h 5), and where they differ the
+// quotient differs from h by more than half a step, so t <=> s h decides as the
+// rounded division would.
+__device__ __noinline__ uint32_t corrected(uint32_t word, uint4 raw, float m, float s, float r, float from) {
+    unsigned which = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if ((__float_as_uint(__fmaf_rn(value_of(raw, e), r, from)) & 0xffffu) < kNear) which |= 1u << e;
+    for (; which; which &= which - 1) {
+        const int e = __ffs(static_cast<int>(which)) - 1;
+        // one too many at the most, and 16 at the most: 15.25 is not near a half
+        const uint32_t code = word >> (4 * e) & 15u;
+        const float over = __fmaf_rn(0.5f - static_cast<float>(code), s, __fsub_rn(value_of(raw, e), m));
+        if (code && (over < 0.f || (over == 0.f && (code & 1)))) word -= 1u << (4 * e);
+    }
+    return word;
+}
+
+// A row's 16 values of this lane as codes, and its group's scale and minimum, over
+// which the group's kLanes lanes agree. What bounds the append is the number of
+// its operations (19 a value and lane), so
 //  * least and greatest value go through the reduction as one pair of bf16
 //    numbers, the greatest negated, and NaN goes with them;
 //  * (hi - lo) / 15 is by Markstein's correction of a product with 1 / 15, which
 //    rounds as the division does;
-//  * t / s is t by the reciprocal, rounded by adding 1.5 * 2^23, whose last bit
-//    counts ones, and the codes are collected from the sums' bits. That is off by
-//    less than 2^-18 of a step, so where the quotient is not near a half it
-//    rounds as the true one does; near one (one lane in 170: bf16 values
-//    lie on few points), or where saturated values leave the range, the division
-//    itself decides.
+//  * a code comes from one fused product and sum with r = 1 / s,
+//      y = x r + (192.5 + margin - m r),
+//    in [192, 256), whose last bit counts 2^-16: the upper half of its bits is a
+//    constant and the code, the lower half how far the quotient is above the half
+//    (less the margin) that it was rounded up from. y is off by less than the
+//    margin: 2^-17 of its own rounding, 2^-15 of the sum's in brackets while
+//    |m r| < 512, 2^-19 of r's error, 2^-20 of the definition's own difference.
+//    A quotient within the margin of a half is looked at again (one lane in 170:
+//    bf16 values lie on few points), and where saturated values leave the range,
+//    or |m r| is 512 or more (groups all of whose values are within 3% of one
+//    number), the division itself decides.
 template <int kLanes>
-__device__ __forceinline__ uint32_t quantise(const uint4& raw, __half& s, __half& m) {
-    constexpr float kOne = 12582912.f;  // 0x4b400000
-    const uint32_t lo2 = min_bf16x2(min_bf16x2(raw.x, raw.y), min_bf16x2(raw.z, raw.w));
-    const uint32_t hi2 = max_bf16x2(max_bf16x2(raw.x, raw.y), max_bf16x2(raw.z, raw.w)) ^ 0x80008000u;
-    uint32_t range = min_bf16x2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));  // (lo, -hi)
+__device__ __forceinline__ void quantise(const uint4 (&raw)[2], uint32_t (&word)[2], __half& s, __half& m) {
+    uint32_t lo2[2], hi2[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        lo2[i] = min_bf16x2(min_bf16x2(raw[i].x, raw[i].y), min_bf16x2(raw[i].z, raw[i].w));
+        hi2[i] = max_bf16x2(max_bf16x2(raw[i].x, raw[i].y), max_bf16x2(raw[i].z, raw[i].w));
+    }
+    const uint32_t lows = min_bf16x2(lo2[0], lo2[1]), highs = max_bf16x2(hi2[0], hi2[1]) ^ 0x80008000u;
+    uint32_t range = min_bf16x2(__byte_perm(lows, highs, 0x5410), __byte_perm(lows, highs, 0x7632));  // (lo, -hi)
 #pragma unroll
     for (int d = kLanes / 2; d; d >>= 1) range = min_bf16x2(range, __shfl_xor_sync(0xffffffffu, range, d));
     const float least = bf16_lo(range), most = -bf16_hi(range);
@@ -109,50 +140,60 @@ __device__ __forceinline__ uint32_t quantise(const uint4& raw, __half& s, __half
     s = __float2half_rn(__fmaf_rn(__fmaf_rn(-15.f, third, span), 1.f / 15.f, third));
     const float mf = __half2float(m), sf = __half2float(s);
     const float r = sf > 0.f ? rcp(sf) : 0.f;
-    const uint64_t less = pair(-mf, -mf), by = pair(r, r), one = pair(kOne, kOne), minus = pair(-1.f, -1.f);
-    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t word = 0;
-    float off = 0.f;  // the largest distance from a whole number
+    const float from = __fmaf_rn(-mf, r, 192.5f + kMargin);
+    const uint64_t by = pair(r, r), add = pair(from, from);
+    const bool inside = __fmaf_rn(least, r, from) > 192.25f && __fmaf_rn(most, r, from) < 207.75f && fabsf(mf * r) < 512.f;
 #pragma unroll
-    for (int i = 3; i >= 0; --i) {
-        const uint64_t t = add2(pair(bf16_lo(u[i]), bf16_hi(u[i])), less);
-        const uint64_t y = fma2(t, by, one);
-        float y0, y1, d0, d1;
-        unpair(y, y0, y1);
-        unpair(fma2(t, by, fma2(y, minus, one)), d0, d1);
-        off = fmaxf(off, fmaxf(fabsf(d0), fabsf(d1)));
-        word = word * 256u + __float_as_uint(y1) * 16u + __float_as_uint(y0);
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t near = 0xffffffffu;
+        word[i] = 0;
+#pragma unroll
+        for (int j = 3; j >= 0; --j) {  // values j and j + 4
+            const uint32_t a = u[j / 2], b = u[j / 2 + 2];
+            float y0, y1;
+            unpair(fma2(j & 1 ? pair(bf16_hi(a), bf16_hi(b)) : pair(bf16_lo(a), bf16_lo(b)), by, add), y0, y1);
+            near = min_u16x2(near, __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x5410));
+            word[i] = word[i] * 16u + __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632);
+        }
+        // less what the upper halves' constant 0x4340 is, at each of eight places
+        word[i] -= 0x43404340u * 0x1111u;
+        if (!(sf > 0.f)) word[i] = 0;
+        else if (!inside) word[i] = divided(raw[i], mf, sf);
+        else if (min(near & 0xffffu, near >> 16) < kNear) word[i] = corrected(word[i], raw[i], mf, sf, r, from);
     }
-    word -= 0x3f400000u;  // what the sums' 0x4b400000 are, at each of eight places, modulo 2^32
-    const bool inside = (least - mf) * r > -0.25f && (most - mf) * r < 15.25f;
-    if (!(sf > 0.f)) word = 0;
-    else if (!(off < kNear) || !inside) word = corrected(word, raw, mf, sf, r);
     if (least != least) {  // a NaN
         s = m = __ushort_as_half(0x7fff);
-        word = 0;
+        word[0] = word[1] = 0;
     }
-    return word;
 }
 
-// Half a warp a pair of tokens and head: 8 values of the key and of the value of
-// both a lane, so four loads in flight. Tokens next to one another in a unit
-// (a prompt's) share the 4-byte words of its values' codes and parameters.
+// A quarter of a warp a pair of tokens and head: 16 values of the key and of the
+// value of both a lane, so eight loads in flight. Tokens next to one another in a
+// unit (a prompt's) share the 4-byte words of its values' codes and parameters.
+constexpr int kTeam = 8;  // lanes
+
 template <int kGroups>
-__global__ void __launch_bounds__(kThreads, 5) append_kernel(const Append p) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const Append p) {
     using U = Unit<kGroups>;
-    constexpr int kLanes = 16 / kGroups;
-    const int part = threadIdx.x & 15, w = part >> 2, c = part & 3, g = part / kLanes;
-    const uint32_t i = blockIdx.x * (kThreads / 16) + threadIdx.x / 16;
+    constexpr int kLanes = kTeam / kGroups;
+    const int part = threadIdx.x % kTeam, w = part >> 1, c = 2 * (part & 1), g = part / kLanes;  // (words c and c + 1)
+    const uint32_t i = blockIdx.x * (kThreads / kTeam) + threadIdx.x / kTeam;
     const uint32_t pr = p.magic ? __umulhi(i, p.magic) >> p.magic_shift : i;  // i / hkv
     const int head = static_cast<int>(i - pr * p.hkv);
     const uint32_t tok = 2 * pr;
-    uint4 raw[2][2] = {};  // [key, value][token]
+    uint4 raw[2][2][2] = {};  // [key, value][token][half]
     int slot[2] = {-1, -1};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if (tok + j >= p.tokens) continue;
-        raw[0][j] = ld_streaming(p.k + static_cast<uint64_t>(tok + j) * p.k_stride + (head * 16 + part));
-        raw[1][j] = ld_streaming(p.v + static_cast<uint64_t>(tok + j) * p.v_stride + (head * 16 + part));
+        const uint4* k = p.k + static_cast<uint64_t>(tok + j) * p.k_stride + (head * 16 + 2 * part);
+        const uint4* v = p.v + static_cast<uint64_t>(tok + j) * p.v_stride + (head * 16 + 2 * part);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            raw[0][j][h] = __ldg(k + h);
+            raw[1][j][h] = __ldg(v + h);
+        }
         const long long at = __ldg(p.slots + tok + j);
         if (at >= p.slot_limit && p.err && part == 0 && head == 0) atomicOr(p.err, PKV_DEVERR_SLOT);
         slot[j] = at >= 0 && at < p.slot_limit ? static_cast<int>(at) : -1;
@@ -160,23 +201,27 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const Append p) {
     auto unit_at = [&](int at) { return p.cache + static_cast<size_t>(unit_of(at, head, p.hkv, p.blocks_of_8)) * U::kBytes; };
     const bool first = part % kLanes == 0;
     __half s[2], m[2];
+    uint32_t word[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const uint32_t word = quantise<kLanes>(raw[0][j], s[0], m[0]);
+        quantise<kLanes>(raw[0][j], word[j], s[0], m[0]);
         if (slot[j] < 0) continue;
         uint8_t* unit = unit_at(slot[j]);
         const int t = slot[j] & 7;
-        *reinterpret_cast<uint32_t*>(unit + key_word(t, w, c)) = word;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint32_t*>(unit + key_word(t, w, c + h)) = word[j][h];
         if (first) *reinterpret_cast<__half2*>(unit + U::kKeyParams + (t * kGroups + g) * 4) = __halves2half2(s[0], m[0]);
     }
-    uint32_t word[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) word[j] = quantise<kLanes>(raw[1][j], s[j], m[j]);
+    for (int j = 0; j < 2; ++j) quantise<kLanes>(raw[1][j], word[j], s[j], m[j]);
     if (slot[0] >= 0 && slot[1] == slot[0] + 1 && (slot[0] & 1) == 0) {
         uint8_t* unit = unit_at(slot[0]);
         const int t = slot[0] & 7;
-        *reinterpret_cast<uint32_t*>(unit + value_piece(t, w, 2 * c)) = __byte_perm(word[0], word[1], 0x5410);
-        *reinterpret_cast<uint32_t*>(unit + value_piece(t, w, 2 * c + 1)) = __byte_perm(word[0], word[1], 0x7632);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            *reinterpret_cast<uint32_t*>(unit + value_piece(t, w, 2 * (c + h))) = __byte_perm(word[0][h], word[1][h], 0x5410);
+            *reinterpret_cast<uint32_t*>(unit + value_piece(t, w, 2 * (c + h) + 1)) = __byte_perm(word[0][h], word[1][h], 0x7632);
+        }
         if (first) {
             *reinterpret_cast<__half2*>(unit + U::kValueScales + (g * kUnit + t) * 2) = __halves2half2(s[0], s[1]);
             *reinterpret_cast<__half2*>(unit + U::kValueMins + (g * kUnit + t) * 2) = __halves2half2(m[0], m[1]);
@@ -188,8 +233,11 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const Append p) {
         if (slot[j] < 0) continue;
         uint8_t* unit = unit_at(slot[j]);
         const int t = slot[j] & 7;
-        *reinterpret_cast<uint16_t*>(unit + value_piece(t, w, 2 * c)) = static_cast<uint16_t>(word[j]);
-        *reinterpret_cast<uint16_t*>(unit + value_piece(t, w, 2 * c + 1)) = static_cast<uint16_t>(word[j] >> 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            *reinterpret_cast<uint16_t*>(unit + value_piece(t, w, 2 * (c + h))) = static_cast<uint16_t>(word[j][h]);
+            *reinterpret_cast<uint16_t*>(unit + value_piece(t, w, 2 * (c + h) + 1)) = static_cast<uint16_t>(word[j][h] >> 16);
+        }
         if (first) {
             *reinterpret_cast<__half*>(unit + U::kValueScales + (g * kUnit + t) * 2) = s[j];
             *reinterpret_cast<__half*>(unit + U::kValueMins + (g * kUnit + t) * 2) = m[j];
@@ -347,7 +395,7 @@ pkv_status pkv_append_int4(const void* k, int64_t k_stride, const void* v, int64
     // and Montgomery's division by an invariant)
     while ((2ll << p.magic_shift) < num_kv_heads) ++p.magic_shift;
     p.magic = static_cast<uint32_t>(((1ull << (32 + p.magic_shift)) + num_kv_heads - 1) / num_kv_heads);
-    const long long blocks = (pairs + kv4::kThreads / 16 - 1) / (kv4::kThreads / 16);
+    const long long blocks = (pairs + kv4::kThreads / kv4::kTeam - 1) / (kv4::kThreads / kv4::kTeam);
     const int grid = static_cast<int>(blocks);
     switch (kv4::groups_of(group_dims)) {
         case 1: kv4::append_kernel<1><<<grid, kv4::kThreads, 0, as_stream(stream)>>>(p); break;

@@ -141,6 +141,23 @@ def test_append_edge_values(pkv):
         assert np.array_equal(got[..., :1024], want[..., :1024])
 
 
+def test_codes_of_quotients_near_a_half(pkv):
+    """Groups of few bf16 steps far from zero (scales from a thousandth to 1/30 of the
+    values and less), groups that step by halves of their scale, wide ones: bytes exactly."""
+    rng = np.random.default_rng(77)
+    n, gd = 16384, 64
+    kinds = np.arange(n) % 4
+    steps = rng.integers(1, 64, n)[:, None]
+    few = 128.0 + rng.integers(0, 96, (n, 1)) + rng.integers(0, 64, (n, gd)) % (steps + 1)  # of 256 steps up to 256
+    halves = rng.integers(0, 31, (n, gd)) * 0.5
+    halves[:, 0], halves[:, 1] = 0, 15  # a scale of one: every other value on a half
+    wide = rng.standard_normal((n, gd)) * 2.0 ** rng.integers(-6, 6, (n, gd))
+    values = np.choose(kinds[:, None], [few, halves, wide, -few]) * 2.0 ** rng.integers(-10, 8, (n, 1))
+    x = torch.from_numpy(values.reshape(2, n // 16, 4, 128)).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
+    pool = Pool(pkv, rng, n // 16 // 16, 4, 16, gd, x[0], x[1])
+    assert np.array_equal(pool.cache.data.cpu().numpy(), int4.pack(pool.k, pool.v))
+
+
 @pytest.mark.parametrize("gd", [32, 64, 128])
 @pytest.mark.parametrize("bt", [8, 16, 32, 64])
 def test_load_is_the_values_rounded_once(pkv, bt, gd):
