@@ -304,6 +304,7 @@ __device__ __forceinline__ Vector<T> load(const T* row, int at, int vocab, unsig
 template <class T, int kVectors>
 __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
     constexpr int kN = Vector<T>::kN;
+    griddep_wait();
     const int row = blockIdx.x / p.chunks, chunk = blockIdx.x - row * p.chunks;
     if (!row_live(p, row)) return;
     __shared__ Selection sel;
@@ -408,6 +409,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
     __shared__ int won_at[kMaxCandidates];
     const int group = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row0 = group * p.beams;
+    griddep_launch_dependents();
     griddep_wait();
     for (int k = warp; k < p.beams; k += kWarps) {
         const int row = row0 + k;
@@ -672,21 +674,22 @@ pkv_status pkv_beam_select(const void* logits, int64_t row_stride, int logits_by
     p.vocab = vocab;
     p.max_length = max_length;
     const auto scan = logits_bytes == 2 ? beam::scan_for<__nv_bfloat16>(vectors) : beam::scan_for<float>(vectors);
-    scan<<<static_cast<unsigned>(rows * p.chunks), beam::kThreads, 0, as_stream(stream)>>>(p);
-    cudaError_t e = cudaGetLastError();
+    // both launched early: each waits for the kernel before it reads anything
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * p.chunks));
+    cfg.blockDim = dim3(beam::kThreads);
+    cfg.stream = as_stream(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, scan, p);
     if (e == cudaSuccess) {
-        // launched early: it waits for the scan before it reads anything
-        cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(num_groups, static_cast<unsigned>(std::max(1, std::min(num_candidates, beam::kWantCtas / num_groups))));
-        cfg.blockDim = dim3(beam::kThreads);
-        cfg.stream = as_stream(stream);
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
         e = cudaLaunchKernelEx(&cfg, beam::join_kernel, p);
     }
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return PKV_ECUDA;
