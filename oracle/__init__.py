@@ -10,6 +10,8 @@ Plain, slow CPU code that restates what the pages define:
   - cache_ops: the slot arithmetic of the block table, append and block copy;
   - block_manager: free list, refcounts, copy-on-write and page-rounded
     admission with full output reservation;
+  - int4: the 4-bit cache's rounding, layout and attention;
+  - beam: beam search's selection and histories;
   - accounting: the pages' closed-form memory arithmetic;
   - scenario: replays a workload's events with the pieces above.
 

@@ -345,6 +345,7 @@ pkv_status pkv_bm_fork(pkv_bm* bm, int parent_seq, int n, int32_t* child_ids) {
 pkv_status pkv_bm_reorder(pkv_bm* bm, const int32_t* seq_ids, const int32_t* parents, int n) {
     if (!bm || n < 0 || (n > 0 && (!seq_ids || !parents))) return PKV_EINVAL;
     std::lock_guard<std::mutex> lock(bm->mu);
+    if (static_cast<size_t>(n) > bm->seqs.size()) return PKV_EINVAL;
     {
         std::vector<int32_t> sorted(seq_ids, seq_ids + n);
         std::sort(sorted.begin(), sorted.end());

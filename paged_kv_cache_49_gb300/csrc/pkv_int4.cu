@@ -1,6 +1,10 @@
 // Ways into and out of a cache held in 4 bits (layout and formulas:
 // pkv_int4.cuh): the quantising append, pages back as bf16 pages, and copies of
-// whole blocks. All are data movement with a few operations a value.
+// whole blocks. All are data movement with a few operations a value. Of 16,411
+// tokens of 8 heads the append reads 67 MB and writes 19: 19 us, 4.5 TB/s, bound by
+// its operations (13 warp instructions for 32 values, 64% of the issue slots) and by
+// what the blocks of a wave wait for their first loads; loading them again takes
+// 14 us, 6.1 TB/s. A load of 0.47 GB in and out takes 72 us, 6.5 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -105,7 +109,7 @@ __device__ __noinline__ uint32_t corrected(uint32_t word, uint4 raw, float m, fl
 
 // A row's 16 values of this lane as codes, and its group's scale and minimum, over
 // which the group's kLanes lanes agree. What bounds the append is the number of
-// its operations (19 a value and lane), so
+// its operations (21 warp instructions for 32 values before the steps below), so
 //  * least and greatest value go through the reduction as one pair of bf16
 //    numbers, the greatest negated, and NaN goes with them;
 //  * (hi - lo) / 15 is by Markstein's correction of a product with 1 / 15, which
@@ -268,7 +272,8 @@ __device__ __forceinline__ uint32_t values2(uint32_t codes, float s24, float m0,
     return pack_bf16x2(fmaf(__low2float(h), s24, m0), fmaf(__high2float(h), s24b, m1));
 }
 
-// A warp a unit, lane 4 r + c: of the keys, token r's dims 32 w + 8 c .. + 7; of
+// A warp a unit, which is 1,024 bytes of codes in two loads a lane and 4,096 of
+// rows out; lane 4 r + c: of the keys, token r's dims 32 w + 8 c .. + 7; of
 // the values, dims 32 w + 4 r .. + 3 of tokens 2 c and 2 c + 1.
 template <int kGroups>
 __global__ void __launch_bounds__(kThreads) load_kernel(const Load p) {

@@ -18,6 +18,8 @@
 //  * S^T[16 tokens x 8 heads] = K Q^T and O^T[128 dims x 8 heads] += V^T P^T by
 //    mma.sync m16n8k16, whose N = 8 is a whole group of query heads; a unit's
 //    codes lie in shared memory as the lanes hold them (one 16-byte load each).
+//    (Register operands: tcgen05 would have the codes' fp16 numbers, four times
+//    their bytes, written back to shared or tensor memory for each product.)
 //    The queries are scaled by a power of two per head so that fp16 holds them
 //    without loss.
 //  * Weights are 2^(x - max + 10), so what fp16 drops of them is below 2^-35 of
@@ -25,19 +27,24 @@
 //    weight times scale to stay in range. A third product with rows of the
 //    values' minima and of ones gives sum p m and the softmax's denominator.
 //
-// Work. A run is one sequence and up to 8 of its KV heads (the most of 8, 4, 2, 1
-// that divide their number), in tiles of 16 tokens a consumer warp: with 8 heads
-// a warp has a head of its own, with fewer the warps of a head share its tokens.
-// A tile's bytes are one copy then, or few, since a slab holds its heads'
-// rows next to one another -- with a copy a block and head, issuing them (100 to
-// 150 cycles each) was what bounded the kernel. All runs are laid end to end, as
-// in the bf16 cache's decode kernel (pkv_decode_kernel.cuh), and cut into
-// gridDim.x ranges of equal cost, one CTA an SM. Producer warps copy tiles into a
-// ring; the consumers take up to four tiles at a time, 64 tokens each where they
-// have a head of their own. At the end of a piece a warp has its head's result;
-// warps that share a head combine theirs through shared memory first. Pieces of a
-// run that is cut among CTAs are combined by whichever warp (of those with the
-// same rows) finishes last.
+// Work. A run is one sequence and up to 4 of its KV heads (the most of 4, 2, 1
+// that divide their number), in tiles of 16 tokens a consumer warp: with 4 heads a
+// warp has a head of its own, with fewer the warps of a head share its tokens. A
+// tile's bytes are one copy then, or few, since a slab holds its heads' rows next
+// to one another -- with a copy a block and head, issuing them (100 to 150 cycles
+// each) was what bounded the kernel. All runs are laid end to end, as in the bf16
+// cache's decode kernel (pkv_decode_kernel.cuh), and cut into gridDim.x ranges of
+// equal cost, one a CTA, two CTAs an SM. Producer warps copy tiles into a ring;
+// the consumers take up to four tiles at a time. At the end of a piece a warp has
+// its head's result; warps that share a head combine theirs through shared memory
+// first. Pieces of a run that is cut among CTAs are combined by whichever warp (of
+// those with the same rows) finishes last.
+//
+// What bounds it: of 256 sequences of 11,200 tokens on average and 8 heads (3.3 GB)
+// the reading, 541 us, 6.1 TB/s; of 64 of 1,500 (111 MB, 32 us, 3.5 TB/s) the start
+// (5 us until the first tiles land) and the unequal ends of the ranges; the matrix
+// products and what feeds them, 2,300 cycles for 64 tokens of 4 heads, fill three
+// quarters of the time between.
 #pragma once
 
 #include "pkv_decode_kernel.cuh"
@@ -48,6 +55,11 @@ namespace pkv {
 namespace kv4 {
 
 constexpr int kMaxG = PKV_ATTN_MAX_GROUP;
+// With both sides measured, in us for one sequence / 64 / 256 / 200 of one KV head:
+// 8 warps and heads take 128 registers a thread at most and spill (10.5 / 34.3 /
+// 558 / 22.9 with 4, 13.3 / 52.9 / 965 / 29.7 with 8); two tiles at a time overlap
+// less (10.5 / 33.8 / 594 / 21.5); a second producer gives 10.4 / 33.5 / 542 / 21.9;
+// a ring of 12 tiles leaves one CTA an SM (10.0 / 39.2 / 764 / 25.9).
 constexpr int kWarps = 4;      // consumers, and heads of a run at most
 constexpr int kTok = 16;       // tokens of a tile, a warp
 constexpr int kSubs = 4;       // tiles a warp takes at a time
@@ -56,7 +68,8 @@ constexpr int kProducers = 2;  // producer i copies every tile whose place in th
 static_assert(kStages % kSubs == 0 && kStages % kProducers == 0, "each stage is always the same producer's");
 constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + kProducers * 32;
-// Work partition: what a run costs beyond its tiles, in tiles.
+// Work partition: what a run costs beyond its tiles, in tiles (200 sequences of one
+// KV head: 21.6 us with 1, 20.7 with 3, 19.4 with 4).
 constexpr int kRunCost = 4;
 // Runs of more pieces than this are combined in two levels, each of up to 32.
 constexpr int kMergeGroup = 16;
@@ -99,6 +112,24 @@ struct Decode {
     float* partials;                     // [grid][2][rows][kORow]
 };
 
+__device__ __forceinline__ uint64_t atom_add_acq_rel_gpu(unsigned long long* addr, uint64_t v) {
+    uint64_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;" : "=l"(old) : "l"(addr), "l"(v) : "memory");
+    return old;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            dst),
+        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+        : "memory");
+}
+// Two floats -> f16x2 (round to nearest even); lo in the low half.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 // Products and transposes that the compiler may schedule among others.
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"

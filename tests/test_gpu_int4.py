@@ -285,6 +285,15 @@ def test_head_layouts(pkv, hq, hkv):
     _decode(pkv, np.random.default_rng(hq), [1, 77, 300, 0, 513], hq, hkv)
 
 
+@pytest.mark.parametrize("gd", [32, 64, 128])
+@pytest.mark.parametrize("bt", [8, 32, 64])
+@pytest.mark.parametrize("hkv", [1, 6, 8, 12])
+def test_heads_blocks_and_groups_together(pkv, hkv, bt, gd):
+    """Runs of one, two and four heads (one warp, two, all of a head), of one run
+    and of several a sequence, cut at a few places."""
+    _decode(pkv, np.random.default_rng(hkv + bt + gd), [1, 200, 65, 0, 130, 23], 2 * hkv, hkv, bt, gd, num_ctas=5)
+
+
 @pytest.mark.parametrize("num_ctas", [1, 2, 3, 7, 64, 151, 152, 300, 304])
 def test_every_grid(pkv, num_ctas):
     """Pieces of all kinds: a context cut among many CTAs, CTAs of many contexts.
@@ -419,6 +428,40 @@ def test_streams_and_graphs(pkv):
         pkv.append_int4(rows, rows, slots, cache)
         assert torch.equal(outs[i % 2], pkv.attn_decode_int4(q, cache, tables, ctx, scale))
     assert ws.read_error() == 0
+
+
+def test_calls_in_turn_without_a_wait(pkv):
+    """Appends, loads, copies and attention, each launched while the one before may
+    still run, read and write the same pages: a token at a time, the results of
+    every call kept, against the same calls one by one."""
+    rng = np.random.default_rng(21)
+    n, hkv, bt = 48, 4, 16
+    kb, vb = _rows(rng, (n, 300, hkv, 128)), _rows(rng, (n, 300, hkv, 128))
+    k, v = _dev(pkv, kb), _dev(pkv, vb)
+    q = torch.randn((n, 2, 16, 128), device="cuda").to(torch.bfloat16)
+    slots = torch.arange(300, device="cuda")
+    pairs = torch.tensor([[i, i + 1] for i in range(19)], dtype=torch.int32, device="cuda")
+    copies = torch.tensor([[0, 20], [7, 21]], dtype=torch.int32, device="cuda")
+    tables = torch.stack([torch.arange(19), 21 - torch.arange(19)]).int().cuda()
+    ctx = torch.tensor([300, 290], dtype=torch.int32, device="cuda")
+
+    def run(wait):
+        cache, ws = pkv.Int4Cache(22, hkv, bt, 64), pkv.AttentionWorkspace(2, hkv)
+        loaded = torch.zeros((n, 2, 20, hkv, bt, 128), dtype=torch.bfloat16, device="cuda")
+        outs = torch.zeros_like(q)
+        torch.cuda.synchronize()
+        for i in range(n):
+            for call in (lambda: pkv.append_int4(k[i], v[i], slots, cache), lambda: pkv.load_int4(cache, pairs, *loaded[i]),
+                         lambda: pkv.block_copy_int4(cache, copies),
+                         lambda: pkv.attn_decode_int4(q[i], cache, tables, ctx, 0.09, out=outs[i], workspace=ws)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        assert ws.read_error() == 0
+        return loaded, outs
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
 
 
 def test_a_pool_past_four_gigabytes(pkv):
