@@ -9,10 +9,10 @@
 // Two launches. The scan reads each logit once: a CTA holds a chunk of a row in
 // registers, and leaves its maximum, the sum of its exponentials and its n
 // largest logits. These come without a sort: of the 8 warps' threads' maxima,
-// each warp's ceil(n / 8)-th largest is known after as many warp reductions; at
-// least n logits of the chunk reach the least of these 8, and hardly more do, so
-// those that reach it go into a list whose entries are ranked by comparing them
-// all. (A list that overflows, as of equal logits, is replaced by n rounds over
+// each warp's ceil(n / 8)-th largest is known after as many warp reductions; the
+// largest of these 8 that n threads' maxima reach is reached by hardly more than n
+// logits of the chunk, so those that reach it go into a list whose entries are
+// ranked by comparing them all. (A list that overflows, as of equal logits, is replaced by n rounds over
 // the chunk.) The join merges the chunks' lists of a group by scores of twice
 // fp32's precision: neighbours of the last one taken may differ by less than
 // fp32 holds. The exponentials bound the scan from the other side:
@@ -53,7 +53,7 @@ struct Params {
     int32_t* lengths_out;
     int32_t* history_out;
     float2* stats;  // [rows][chunks]: maximum, sum of exponentials from it on
-    uint2* lists;   // [rows][chunks][n]: logit bits, token (or -1)
+    uint2* lists;   // [groups][n][beams][chunks]: logit bits, token (or -1)
     uint32_t* err;
     int eos, beams, n, vocab, max_length, chunks, chunk_tokens;
 };
@@ -114,6 +114,7 @@ struct Selection {
         float2 part[kWarps];
     };
     uint32_t warp_key[kWarps];
+    int reached[kWarps];
     uint64_t warp_best[kWarps];
     int warp_at[kWarps];
     int count;
@@ -121,24 +122,39 @@ struct Selection {
 
 __device__ __forceinline__ bool before(uint64_t ka, int ia, uint64_t kb, int ib) { return ka > kb || (ka == kb && ia < ib); }
 
-// The least, over the warps that have any (the first `warps`), of each warp's
-// ceil(n / warps)-th largest thread key: at least n keys of the block reach it
-// (or all that are above -inf).
+// A cut that at least n keys of the block reach (or all that are above -inf), and
+// hardly more: of the warps that have any (the first `warps`), each warp's
+// ceil(n / warps)-th largest thread key; the least of these is such a cut, and the
+// largest that n threads' keys reach is the one taken.
 __device__ __forceinline__ float threshold(Selection& sel, float best, int n, int warps) {
-    const int warp = threadIdx.x >> 5;
-    uint32_t mine = ordered(best), top = 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t key = ordered(best);
+    uint32_t mine = key, top = 0;
     if (warp < warps)
         for (int i = 0; i < (n + warps - 1) / warps; ++i) {
             top = __reduce_max_sync(0xffffffffu, mine);
             const unsigned holders = __ballot_sync(0xffffffffu, mine == top);
-            if ((threadIdx.x & 31) == __ffs(holders) - 1) mine = 0;
+            if (lane == __ffs(holders) - 1) mine = 0;
         }
     if (threadIdx.x == 0) sel.count = 0;
-    if ((threadIdx.x & 31) == 0) sel.warp_key[warp] = warp < warps ? max(top, ordered(-INFINITY)) : 0xffffffffu;
+    if (lane == 0) {
+        sel.warp_key[warp] = warp < warps ? max(top, ordered(-INFINITY)) : 0xffffffffu;
+        sel.reached[warp] = 0;
+    }
     __syncthreads();
-    uint32_t t = sel.warp_key[0];
+    int reach = 0;
+    uint32_t t = 0xffffffffu;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) t = min(t, sel.warp_key[w]);
+    for (int w = 0; w < kWarps; ++w) {
+        const int reached = __popc(__ballot_sync(0xffffffffu, key >= sel.warp_key[w]));
+        if (lane == w) reach = reached;
+        t = min(t, sel.warp_key[w]);
+    }
+    if (lane < kWarps && reach > 0) atomicAdd(&sel.reached[lane], reach);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        if (sel.reached[w] >= n) t = max(t, sel.warp_key[w]);
     return unordered(t);
 }
 
@@ -151,9 +167,9 @@ __device__ __forceinline__ void finish(Selection& sel, int n, int items, Item it
     __syncthreads();
     const int count = sel.count;
     if (count <= kList) {
-        // four lanes a candidate
-        for (int i0 = 0; i0 < count; i0 += kThreads / 4) {
-            const int i = i0 + static_cast<int>(threadIdx.x) / 4;
+        // four lanes a candidate; warps without one have nothing to do
+        for (int i0 = static_cast<int>(threadIdx.x) / 32 * 8; i0 < count; i0 += kThreads / 4) {
+            const int i = i0 + static_cast<int>(threadIdx.x) % 32 / 4;
             const uint64_t key = i < count ? sel.list[i] : ~uint64_t(0);
             const int at = kIndexed && i < count ? sel.at[i] : 0;
             int rank = 0;
@@ -378,7 +394,8 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
         }
     }
     griddep_launch_dependents();  // the join's CTAs need not take room before
-    uint2* list = p.lists + out * p.n;
+    const int group = row / p.beams, all_lists = p.beams * p.chunks;
+    uint2* list = p.lists + static_cast<size_t>(group) * all_lists * p.n + (row - group * p.beams) * p.chunks + chunk;
     finish<false>(
         sel, p.n, hi - lo,
         [&](int i, uint64_t& k, int&) {
@@ -387,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
             return x > -INFINITY;
         },
         [&](int rank, uint64_t k, int) {
-            list[rank] = k ? make_uint2(__float_as_uint(unordered(static_cast<uint32_t>(k >> 32))), ~static_cast<uint32_t>(k))
+            list[static_cast<size_t>(rank) * all_lists] = k ? make_uint2(__float_as_uint(unordered(static_cast<uint32_t>(k >> 32))), ~static_cast<uint32_t>(k))
                            : make_uint2(0xff800000u, 0xffffffffu);
         });
 }
@@ -398,6 +415,8 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
 // copies its part of the histories. Candidates are sifted by a cut as the
 // scan's, by scores in fp32 with room for their rounding; what is left is ranked
 // by scores in pairs.
+constexpr int kHeld = 2;  // turns whose scores stay in registers
+
 __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
     __shared__ Selection sel;
     // In quarters, so that no sum of finite ones overflows: the beams' scores and
@@ -405,6 +424,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
     __shared__ float score[kMaxBeams], less[kMaxBeams];  // (less: the score less the logarithm, -inf for a beam not read)
     __shared__ Pair lse[kMaxBeams];
     __shared__ bool done[kMaxBeams];
+    __shared__ int order[kMaxBeams];
     __shared__ float won_score[kMaxCandidates];
     __shared__ int won_at[kMaxCandidates];
     const int group = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -446,44 +466,56 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
         }
     }
     __syncthreads();
-    // Candidate i is entry i % (chunks * n) of beam i / (chunks * n), or, from
-    // `items` on, the one of the finished beam i - items.
-    const int per_row = p.chunks * p.n, items = p.beams * per_row;
-    const float by = 1.f / static_cast<float>(per_row);
+    // The beams that are read, next to one another.
+    const unsigned read = __ballot_sync(0xffffffffu, lane < p.beams && !(less[lane % kMaxBeams] == -INFINITY));
+    if (warp == 0 && (read >> lane & 1)) order[__popc(read & ((1u << lane) - 1))] = lane;
+    __syncthreads();
+    // Candidate i is entry i / some of list i % some, of `some` lists that are read,
+    // each in order, or, from `items` on, the one of the finished beam i - items.
+    const int some = __popc(read) * p.chunks, items = some * p.n, stride = p.beams * p.chunks;
+    const float by_lists = 1.f / static_cast<float>(max(some, 1)), by_chunks = 1.f / static_cast<float>(p.chunks);
     const bool few = items < (1 << 20);  // quotients by fp32 are exact
-    auto beam_of = [&](int i) { return few ? static_cast<int>((static_cast<float>(i) + 0.5f) * by) : i / per_row; };
-    const uint2* lists = p.lists + static_cast<size_t>(row0) * per_row;
+    struct Place {
+        int beam;
+        size_t at;
+    };
+    auto place = [&](int i) {
+        const int entry = few ? static_cast<int>((static_cast<float>(i) + 0.5f) * by_lists) : i / some, list = i - entry * some;
+        const int nth = few ? static_cast<int>((static_cast<float>(list) + 0.5f) * by_chunks) : list / p.chunks, k = order[nth];
+        return Place{k, static_cast<size_t>(entry) * stride + k * p.chunks + (list - nth * p.chunks)};
+    };
+    const uint2* lists = p.lists + static_cast<size_t>(group) * stride * p.n;
     // the score in fp32: -inf or NaN where there is no candidate
-    auto rough = [&](int i) { return fmaf(0.25f, __uint_as_float(lists[i].x), less[beam_of(i)]); };
+    auto rough = [&](int i) {
+        const Place at = place(i);
+        return fmaf(0.25f, __uint_as_float(lists[at.at].x), less[at.beam]);
+    };
     auto exact = [&](int i, uint64_t& key, int& at) {
         const bool ended = i >= items;
-        const int k = ended ? i - items : beam_of(i);
-        if (ended ? !done[k] : !(less[k] > -INFINITY)) return false;
-        const uint2 c = ended ? make_uint2(0u, static_cast<uint32_t>(p.eos)) : lists[i];
+        const Place from = ended ? Place{i - items, 0} : place(i);
+        const int k = from.beam;
+        if (ended && !done[k]) return false;
+        const uint2 c = ended ? make_uint2(0u, static_cast<uint32_t>(p.eos)) : lists[from.at];
         at = k * p.vocab + static_cast<int>(c.y);
         const Pair l = lse[k];
         const Pair s = ended ? Pair{score[k], 0.f} : add(add(two_sum(0.25f * __uint_as_float(c.x), -l.hi), -l.lo), score[k]);
         key = static_cast<uint64_t>(ordered(s.hi)) << 32 | ordered(s.lo);
         return static_cast<int>(c.y) >= 0 && s.hi > -INFINITY && s.hi < INFINITY;  // (false for NaN)
     };
-    // Every thread takes one of each 256 candidates, a different one in turn: the
-    // first entries of the lists, the best ones, come to all. The first kHeld
-    // scores of a thread stay in registers, any others are formed again.
-    constexpr int kHeld = 32;
-    auto index = [&](int u) { return u * kThreads + static_cast<int>((threadIdx.x + 37u * u) & (kThreads - 1)); };
+    // The cut is from the lists' first entries: a turn of the threads takes 256
+    // candidates, and the first turns take those of every list.
+    const int turns = max(kHeld, (some + kThreads - 1) / kThreads);
     float held[kHeld];
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+        const int i = u * kThreads + static_cast<int>(threadIdx.x);
+        held[u] = i < items ? rough(i) : -INFINITY;
+    }
     float best = -INFINITY;
 #pragma unroll
-    for (int u0 = 0; u0 < kHeld; u0 += 16) {
-        if (u0 * kThreads >= items) break;
-#pragma unroll
-        for (int u = u0; u < u0 + 16; ++u) {
-            held[u] = index(u) < items ? rough(index(u)) : -INFINITY;
-            best = fmaxf(best, held[u]);  // passes over NaN
-        }
-    }
-    for (int u = kHeld; u * kThreads < items; ++u)
-        if (index(u) < items) best = fmaxf(best, rough(index(u)));
+    for (int u = 0; u < kHeld; ++u) best = fmaxf(best, held[u]);  // passes over NaN
+    for (int i = kHeld * kThreads + static_cast<int>(threadIdx.x); i < min(items, turns * kThreads); i += kThreads)
+        best = fmaxf(best, rough(i));
     const bool ended = threadIdx.x < p.beams && done[threadIdx.x];
     if (ended) best = fmaxf(best, score[threadIdx.x]);
     // the threads' best, dealt out anew: neighbours go to different warps
@@ -494,11 +526,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
     // Rounded sums are off by less than 2^-22 of their terms: those of a score at
     // the cut are the beam's score, its logarithm of the sum, and the cut less
     // these.
-    float terms = 0.f;
-    for (int k = 0; k < p.beams; ++k) {
-        const float t = fabsf(score[k]) + fabsf(lse[k].hi);
-        if (t < INFINITY) terms = fmaxf(terms, t);
-    }
+    const float t = lane < p.beams ? fabsf(score[lane]) + fabsf(lse[lane].hi) : 0.f;
+    const float terms = __uint_as_float(__reduce_max_sync(0xffffffffu, t < INFINITY ? __float_as_uint(t) : 0u));
     cut -= 0x1p-21f * (2.f * terms + fabsf(cut));
     cut = fmaxf(cut, -0x1.fffffep127f);  // (-inf is no candidate)
     auto take = [&](int i) {
@@ -511,16 +540,18 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
             sel.at[slot] = at;
         }
     };
-#pragma unroll
-    for (int u0 = 0; u0 < kHeld; u0 += 8) {
-        if (u0 * kThreads >= items) break;
-        unsigned hits = 0;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) hits |= held[u0 + u] >= cut ? 1u << u : 0u;
-        for (; hits; hits &= hits - 1) take(index(u0 + __ffs(static_cast<int>(hits)) - 1));
+    // Turns go on until as many candidates one after the other as there are lists,
+    // one of each, are below the cut: so are all behind them.
+    int below = 0;
+#pragma unroll 1
+    for (int u = 0; u * kThreads < items; ++u) {
+        const int i = u * kThreads + static_cast<int>(threadIdx.x);
+        const float x = u == 0 ? held[0] : u < kHeld ? held[kHeld - 1] : i < items ? rough(i) : -INFINITY;
+        if (x >= cut) take(i);
+        if (u + 1 < kHeld || (u + 1) * kThreads >= items) continue;
+        below = __syncthreads_or(x >= cut) ? 0 : below + kThreads;
+        if (below >= some) break;
     }
-    for (int u = kHeld; u * kThreads < items; ++u)
-        if (index(u) < items && rough(index(u)) >= cut) take(index(u));
     if (ended && score[threadIdx.x] >= cut) take(items + static_cast<int>(threadIdx.x));
     finish<true>(
         sel, p.n, items + p.beams, [&](int i, uint64_t& key, int& at) { return exact(i, key, at); },
