@@ -12,11 +12,15 @@
 // each warp's ceil(n / 8)-th largest is known after as many warp reductions; the
 // largest of these 8 that n threads' maxima reach is reached by hardly more than n
 // logits of the chunk, so those that reach it go into a list whose entries are
-// ranked by comparing them all. (A list that overflows, as of equal logits, is replaced by n rounds over
-// the chunk.) The join merges the chunks' lists of a group by scores of twice
-// fp32's precision: neighbours of the last one taken may differ by less than
-// fp32 holds. The exponentials bound the scan from the other side:
-// at 16 a cycle and SM they take two thirds of the time of reading bf16 logits.
+// ranked by comparing them all. (A list that overflows, as of equal logits, is
+// replaced by n rounds over the chunk.) The join merges the chunks' lists of a
+// group, as far into each as its entries reach the cut, by scores of twice fp32's
+// precision: neighbours of the last one taken may differ by less than fp32 holds.
+//
+// What bounds it: the scan of 64 groups of 4 beams over 131,072 tokens in bf16 (60
+// MB read) the exponentials, at 16 a cycle and SM two thirds of the time of
+// reading, and the instructions around them (12 for 32 logits, half of them a
+// CTA's for its cut and list): 14 us; the join, 7 us, a chain of latencies.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -37,7 +41,7 @@ constexpr int kMaxBeams = PKV_BEAM_MAX_BEAMS;
 constexpr int kMaxCandidates = PKV_BEAM_MAX_CANDIDATES;
 constexpr int kList = 512;     // candidates that are ranked
 constexpr int kMaxVectors = 8;  // 16-byte vectors a thread holds
-constexpr int kWantCtas = 304;
+constexpr int kWantCtas = 304;  // two an SM (152 to 608: the same)
 
 struct Params {
     const void* logits;
@@ -605,10 +609,11 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
 }
 
 // Chunks of a row of `vocab` logits of `size` bytes, their tokens, and the
-// vectors a thread holds: as many as leave kWantCtas CTAs (a CTA's fixed part,
-// 3,600 cycles of the 8,600 with 8 vectors a thread, is then paid least often),
-// and chunks as even as vectors allow, so that none leaves most of its warps
-// without logits.
+// vectors a thread holds: as many as leave kWantCtas CTAs (what a CTA does whatever
+// it holds is then done least often: 64 groups of 4 beams, 131,072 tokens in bf16,
+// take 28 us with 4 vectors a thread, 21 with 8, 21 to 23 with 16, whose registers
+// leave fewer CTAs an SM), and chunks as even as vectors allow, so that none leaves
+// most of its warps without logits.
 int chunks_for(long long rows, int vocab, int size, int* vectors, int* tokens) {
     const int n = 16 / size;
     const long long all = (static_cast<long long>(vocab) + n - 1) / n;  // vectors of a row
