@@ -41,7 +41,7 @@
 // those with the same rows) finishes last.
 //
 // What bounds it: of 256 sequences of 11,200 tokens on average and 8 heads (3.3 GB)
-// the reading, 541 us, 6.1 TB/s; of 64 of 1,500 (111 MB, 32 us, 3.5 TB/s) the start
+// the reading, 531 us, 6.2 TB/s; of 64 of 1,500 (111 MB, 32 us, 3.5 TB/s) the start
 // (5 us until the first tiles land) and the unequal ends of the ranges; the matrix
 // products and what feeds them, 2,300 cycles for 64 tokens of 4 heads, fill three
 // quarters of the time between.
@@ -68,9 +68,10 @@ constexpr int kProducers = 2;  // producer i copies every tile whose place in th
 static_assert(kStages % kSubs == 0 && kStages % kProducers == 0, "each stage is always the same producer's");
 constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + kProducers * 32;
-// Work partition: what a run costs beyond its tiles, in tiles (200 sequences of one
-// KV head: 21.6 us with 1, 20.7 with 3, 19.4 with 4).
-constexpr int kRunCost = 4;
+// Work partition: what a run costs beyond its tiles, in tiles (for 64 sequences /
+// 256 / 200 of one KV head 32.1 / 532.7 / 20.6 us with 4, 32.0 / 530.7 / 19.7 with
+// 6, 31.4 / 532.3 / 20.4 with 10; 1 and 3 were slower by 2 to 5 percent).
+constexpr int kRunCost = 6;
 // Runs of more pieces than this are combined in two levels, each of up to 32.
 constexpr int kMergeGroup = 16;
 // Counters of a launch, 64 bits with one byte a warp, in the workspace's region
@@ -394,11 +395,13 @@ __device__ __forceinline__ float* partial(const Decode& p, int cta, int last, in
 // `count` (at most 32) partial results of rows row, row + step, ... (`rows` of them),
 // `stride` CTAs apart from CTA `first` on, combined; emit(row, four dims from 4 lane
 // on, max, sum). Lane k holds partial result k's maxima and sums of all rows, which
-// come first; then four results of four rows are on their way at a time.
+// come first; then six results of four rows are on their way at a time (256
+// sequences: 533 us, 541 with four, which leaves the kernel's other values less room
+// in registers).
 template <class Emit>
 __device__ __forceinline__ void combine(const Decode& p, int first, int stride, int count, int last, int row, int step, int rows,
                                         int lane, Emit emit) {
-    constexpr int kAhead = 4, kAbreast = 4;
+    constexpr int kAhead = 6, kAbreast = 4;
     const int cta = first + min(lane, count - 1) * stride;
 #pragma unroll 1
     for (int j = 0; j < rows; j += kAbreast) {
