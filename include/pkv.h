@@ -477,11 +477,11 @@ pkv_status pkv_attn_decode_int4(const void* q, const void* cache, const int32_t*
  *   history_out, lengths_out : [num_groups][num_candidates][max_length] and
  *                  [num_groups][num_candidates]: the parent's tokens, then the
  *                  new one unless the parent was finished; what lies behind
- *                  them stays as it was, a missing candidate has length 0. Must
- *                  not overlap history. A parent that has max_length tokens
- *                  takes no more and sets PKV_DEVERR_CONTEXT in device_error
- *                  (which may be NULL); so does a length outside [0, max_length],
- *                  which is clamped
+ *                  them stays as it was, a missing candidate has length 0. A
+ *                  parent that has max_length tokens takes no more and sets
+ *                  PKV_DEVERR_CONTEXT in device_error (which may be NULL); so
+ *                  does a length outside [0, max_length], which is clamped.
+ *                  No output may overlap an input (PKV_EINVAL)
  *   workspace    : device scratch of pkv_beam_workspace_size bytes for the same
  *                  four sizes, 256-byte aligned; it holds nothing between calls.
  *                  Calls that share one must not overlap on the GPU

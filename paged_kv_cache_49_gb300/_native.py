@@ -987,8 +987,8 @@ def beam_select(logits, scores, finished=None, eos: int = -1, history=None, leng
             raise ValueError(f"out must hold {groups} groups of {n} candidates on cuda:{device}")
         if room and out.shape[2] != room:
             raise ValueError("out's histories must be [groups, candidates, max_length], as the beams'")
-        if room and out._ptrs[5] == history.data_ptr():
-            raise ValueError("out's histories must not be the beams'")
+        if out._ptrs[0] == scores.data_ptr():
+            raise ValueError("out must not be the beams' own buffers")
     if workspace is not None and workspace.device != device:
         raise ValueError(f"the workspace is on cuda:{workspace.device}, the tensors on cuda:{device}")
     if device_error is not None:

@@ -646,6 +646,15 @@ pkv_status check(int groups, int beams, int candidates, int vocab) {
     return PKV_OK;
 }
 
+struct Range {
+    const void* at;  // NULL: none
+    size_t bytes;
+    bool overlaps(const Range& b) const {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(at), y = reinterpret_cast<uintptr_t>(b.at);
+        return at && b.at && x < y + b.bytes && y < x + bytes;
+    }
+};
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t workspace_for(long long rows, int candidates, int chunks) {
@@ -688,6 +697,16 @@ pkv_status pkv_beam_select(const void* logits, int64_t row_stride, int logits_by
     beam::Params p = {};
     p.chunks = beam::chunks_for(rows, vocab, logits_bytes, &vectors, &p.chunk_tokens);
     if (workspace_bytes < beam::workspace_for(rows, num_candidates, p.chunks)) return PKV_EINVAL;
+    // Several blocks read a group's inputs, and one writes its results while the
+    // others may still read.
+    const size_t in = static_cast<size_t>(rows), out = static_cast<size_t>(num_groups) * num_candidates, room = max_length;
+    const beam::Range inputs[] = {{logits, ((in - 1) * row_stride + vocab) * logits_bytes}, {scores, in * 4}, {finished, in},
+                                  {lengths, in * 4}, {history, in * room * 4}};
+    const beam::Range outputs[] = {{scores_out, out * 4}, {tokens_out, out * 4}, {parents_out, out * 4}, {finished_out, out},
+                                   {lengths_out, out * 4}, {history_out, out * room * 4}};
+    for (const beam::Range& a : inputs)
+        for (const beam::Range& b : outputs)
+            if (a.overlaps(b)) return PKV_EINVAL;
     p.logits = logits;
     p.row_stride = row_stride;
     p.scores = scores;

@@ -202,6 +202,22 @@ def test_c_calls_refuse(pkv):
         assert L.pkv_beam_workspace_size(*shape) == 0
 
 
+def test_outputs_on_inputs_are_refused(pkv):
+    """Whole, by their last byte and by their first."""
+    from paged_kv_cache_49_gb300 import _native as nat
+    g, k, n, v, room = 2, 4, 8, 100, 5
+    inputs = {"x": (g * k - 1) * 128 * 2 + v * 2, "s": g * k * 4, "fin": g * k, "h": g * k * room * 4, "ln": g * k * 4}
+    outputs = {"so": g * n * 4, "to": g * n * 4, "po": g * n * 4, "fo": g * n, "lo": g * n * 4, "ho": g * n * room * 4}
+    at = {name: (i + 1) << 20 for i, name in enumerate([*inputs, *outputs])}
+    for i, size in inputs.items():
+        for o, length in outputs.items():
+            for place in (at[i], at[i] + (size - 1) // 4 * 4, at[i] - length + 1):
+                w = dict(at, **{o: place})
+                got = nat.lib.pkv_beam_select(w["x"], 128, 2, w["s"], w["fin"], 1, g, k, n, v, w["h"], w["ln"], room, w["so"],
+                                              w["to"], w["po"], w["fo"], w["lo"], w["ho"], 1 << 28, 1 << 20, None, None)
+                assert got == nat.PKV_EINVAL, (i, o, place)
+
+
 def test_python_calls_refuse(pkv):
     logits, scores = torch.zeros((4, 50)), torch.zeros((2, 2))
     with pytest.raises(ValueError, match="scores"):  # host tensors

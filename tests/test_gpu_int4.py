@@ -464,6 +464,48 @@ def test_calls_in_turn_without_a_wait(pkv):
         assert torch.equal(a, b)
 
 
+def test_captured_behind_two_streams(pkv):
+    """Every call captured where two streams meet: what they wrote is there."""
+    rng = np.random.default_rng(22)
+    args, ws, _ = _decode(pkv, rng, [500, 70], 8, 2, poison=False)
+    q, cache, tables, ctx, scale = args
+    kv = [torch.zeros((64, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    given = [torch.randn_like(t) for t in kv]
+    slots = torch.arange(64, device="cuda")
+    pairs = torch.tensor([[i, i] for i in range(4)], dtype=torch.int32, device="cuda")
+    pools = [torch.zeros((4, 2, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    lens, out = torch.zeros_like(ctx), torch.zeros_like(q)
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        kv[0].copy_(given[0])
+        with torch.cuda.stream(side):
+            kv[1].copy_(given[1])
+            lens.copy_(ctx)
+        main.wait_stream(side)
+        pkv.append_int4(*kv, slots, cache)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            pkv.load_int4(cache, pairs, *pools)
+        pkv.attn_decode_int4(q, cache, tables, lens, scale, out=out, workspace=ws)
+        main.wait_stream(side)
+    for _ in range(3):
+        for t in given:
+            t.copy_(torch.randn_like(t))
+        g.replay()
+        pkv.append_int4(*given, slots, cache)
+        assert torch.equal(out, pkv.attn_decode_int4(*args))
+        again = [torch.zeros_like(p) for p in pools]
+        pkv.load_int4(cache, pairs, *again)
+        for a, b in zip(pools, again):
+            assert torch.equal(a, b)
+            a.zero_()
+        out.zero_()
+        lens.zero_()
+    assert ws.read_error() == 0
+
+
 def test_a_pool_past_four_gigabytes(pkv):
     """Offsets beyond 32 bits: blocks at both ends of a pool of 5.4 GB."""
     rng = np.random.default_rng(19)
