@@ -258,6 +258,23 @@ def test_repeats_are_equal_to_the_bit(pkv):
         assert torch.equal(first.scores, again.scores) and torch.equal(first.tokens, again.tokens)
 
 
+def test_two_calls_at_once(pkv):
+    """On two streams, each with a workspace and buffers of its own, on one input."""
+    rng = np.random.default_rng(12)
+    logits = _logits(rng, 24, 30011, torch.bfloat16)
+    scores = torch.from_numpy(-rng.random((6, 4), np.float32)).cuda()
+    want = pkv.beam_select(logits, scores, candidates=8)
+    streams, spaces = [torch.cuda.Stream() for _ in range(2)], [pkv.BeamWorkspace(6, 4, 8, 30011) for _ in range(2)]
+    outs = [[pkv.BeamBuffers(6, 8) for _ in range(10)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for st, w, o in zip(streams, spaces, outs):
+            pkv.beam_select(logits, scores, out=o[i], workspace=w, stream=st)
+    torch.cuda.synchronize()
+    for x in (x for o in outs for x in o):
+        assert torch.equal(x.scores, want.scores) and torch.equal(x.tokens, want.tokens) and torch.equal(x.parents, want.parents)
+
+
 def test_refusals_on_the_gpu(pkv):
     z = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype, device="cuda")
     logits, scores, i32 = z(4, 50), z(2, 2), torch.int32

@@ -506,6 +506,21 @@ def test_captured_behind_two_streams(pkv):
     assert ws.read_error() == 0
 
 
+def test_two_calls_at_once(pkv):
+    """On two streams, each with a workspace of its own, over one cache."""
+    rng = np.random.default_rng(23)
+    args, ws, first = _decode(pkv, rng, [3000, 64, 1, 900, 2000], 8, 2)
+    first, other = first.clone(), pkv.AttentionWorkspace(5, 2)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.zeros_like(first) for _ in range(20)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for st, w, o in zip(streams, (ws, other), outs):
+            pkv.attn_decode_int4(*args, out=o[i], workspace=w, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, x) for o in outs for x in o) and ws.read_error() == other.read_error() == 0
+
+
 def test_a_pool_past_four_gigabytes(pkv):
     """Offsets beyond 32 bits: blocks at both ends of a pool of 5.4 GB."""
     rng = np.random.default_rng(19)
