@@ -756,6 +756,8 @@ pkv_status pkv_beam_select(const void* logits, int64_t row_stride, int logits_by
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, scan, p);
     if (e == cudaSuccess) {
+        // every share of a group merges the lists, and copies its part of the histories (12
+        // groups of 32 histories of 1,000 tokens: 29.7 us with 25 shares, 31.3 with 2)
         cfg.gridDim = dim3(num_groups, static_cast<unsigned>(std::max(1, std::min(num_candidates, beam::kWantCtas / num_groups))));
         e = cudaLaunchKernelEx(&cfg, beam::join_kernel, p);
     }
