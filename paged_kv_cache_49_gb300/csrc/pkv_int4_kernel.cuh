@@ -41,7 +41,7 @@
 // those with the same rows) finishes last.
 //
 // What bounds it: of 256 sequences of 11,200 tokens on average and 8 heads (3.3 GB)
-// the reading, 531 us, 6.2 TB/s; of 64 of 1,500 (111 MB, 32 us, 3.5 TB/s) the start
+// the reading, 525 us, 6.3 TB/s; of 64 of 1,500 (111 MB, 32 us, 3.5 TB/s) the start
 // (5 us until the first tiles land) and the unequal ends of the ranges; the matrix
 // products and what feeds them, 2,300 cycles for 64 tokens of 4 heads, fill three
 // quarters of the time between.
@@ -450,8 +450,9 @@ __device__ __forceinline__ void combine(const Decode& p, int first, int stride, 
 }
 
 // A row from the results of the warps that share its head, `stride` floats apart:
-// four dims from 4 lane on. (All loads at once: 200 sequences of one KV head 17.3 us,
-// 18.8 one after the other; a call, so that its registers are not the kernel's.)
+// four dims from 4 lane on. (All loads at once: 200 sequences of one KV head 18.3 us,
+// 18.9 one after the other; a call, so that its registers are not the kernel's: 256
+// of 8 heads 525 us, 542 without.)
 struct Row {
     float4 o;
     float max, sum;
