@@ -71,14 +71,18 @@ __device__ __forceinline__ bool row_live(const Params& p, int row) {
     return !done & some;
 }
 
-// A sum of powers of two counts from its largest logit, times kLog2e in fp32: one
-// from s.x on as one from `top` on. (Products that overflow stand for logits of
-// more than 2e38, whose differences count alone.) One without a logit above -inf
-// is 0, or NaN.
+// A sum of powers of two counts from the largest of its logits, times kLog2e: from
+// fl(x * kLog2e) up to kLarge, where the rounding is 1 at most, and from the product
+// itself beyond, where the rounding may be any power of two. off() is the product
+// less what the sum counts from.
+constexpr float kLarge = 0x1p24f;
+__device__ __forceinline__ float off(float x) { return fabsf(x) < kLarge ? __fmaf_rn(x, kLog2e, -__fmul_rn(x, kLog2e)) : 0.f; }
+// A sum that counts from s.x as one that counts from `top`, which is no less. One
+// without a logit above -inf is 0, or NaN.
 __device__ __forceinline__ float scaled(float2 s, float top) {
     if (!(s.x > -INFINITY)) return s.y;
-    const float a = __fmul_rn(s.x, kLog2e), b = __fmul_rn(top, kLog2e);
-    return s.y * exp2f(fabsf(b) < INFINITY ? a - b : (s.x - top) * kLog2e);
+    if (fabsf(s.x) < kLarge && fabsf(top) < kLarge) return s.y * exp2f(__fmul_rn(s.x, kLog2e) - __fmul_rn(top, kLog2e));
+    return s.y * exp2f(__fmaf_rn(s.x - top, kLog2e, off(top) - off(s.x)));
 }
 
 // Numbers that compare as unsigned integers as the keys do as floats (-0 as 0).
@@ -357,15 +361,14 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
     for (int i = 0; i < kVectors; ++i) best = fmaxf(best, v[i].largest());
     // Each warp sums from its own largest logit on, with no barrier before it:
     // sum 2^(x log2(e) - from), whose only error beside the sum's is that of the
-    // fp32 constant, by which the join divides again. A NaN makes the row's sum
-    // NaN, and then none of its scores is a number.
+    // fp32 constant, by which the join divides again; two at a time. A NaN makes the
+    // row's sum NaN, and then none of its scores is a number.
     const float top = unordered(__reduce_max_sync(0xffffffffu, ordered(best)));
-    const float from = top > -INFINITY ? top * kLog2e : 0.f;
-    float sum = 0.f;
-    if (fabsf(from) < INFINITY || fabsf(top) == INFINITY) {
-        // two at a time: x log2(e) - from, and the sums
-        uint64_t part[2] = {0, 0};
-        const uint64_t by = pair(kLog2e, kLog2e), less = pair(-from, -from);
+    uint64_t part[2] = {0, 0};
+    const uint64_t by = pair(kLog2e, kLog2e);
+    if (fabsf(top) < kLarge || top == -INFINITY) {
+        const float from = top > -INFINITY ? top * kLog2e : 0.f;
+        const uint64_t less = pair(-from, -from);
 #pragma unroll
         for (int i = 0; i < kVectors; ++i)
 #pragma unroll
@@ -374,18 +377,20 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
                 unpair(fma2(pair(v[i].get(e), v[i].get(e + 1)), by, less), a, b);
                 part[e / 2 % 2] = add2(part[e / 2 % 2], pair(ex2(a), ex2(b)));
             }
-        float a, b;
-        unpair(add2(part[0], part[1]), a, b);
-        sum = a + b;
-    } else {  // logits of more than 2e38
+    } else {  // differences first, which are exact where they count
+        const uint64_t less = pair(-top, -top);
 #pragma unroll
         for (int i = 0; i < kVectors; ++i)
-#pragma unroll 1
-            for (int e = 0; e < kN; ++e) {
-                const int at = first + i * kThreads * kN + e;
-                if (at < hi) sum += ex2((static_cast<float>(logits[at]) - top) * kLog2e);
+#pragma unroll
+            for (int e = 0; e < kN; e += 2) {
+                float a, b;
+                unpair(mul2(add2(pair(v[i].get(e), v[i].get(e + 1)), less), by), a, b);
+                part[e / 2 % 2] = add2(part[e / 2 % 2], pair(ex2(a), ex2(b)));
             }
     }
+    float sum, more;
+    unpair(add2(part[0], part[1]), sum, more);
+    sum += more;
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane == 0) sel.part[warp] = make_float2(top, sum);
@@ -466,7 +471,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
         float top = first.x;
         for (int i = lane + 32; i < p.chunks; i += 32) top = fmaxf(top, stats[i].x);
         top = unordered(__reduce_max_sync(0xffffffffu, ordered(top)));
-        const bool large = fabsf(top * kLog2e) == INFINITY;
         float sum = lane < p.chunks ? scaled(first, top) : 0.f;
         for (int i = lane + 32; i < p.chunks; i += 32) sum += scaled(stats[i], top);
 #pragma unroll
@@ -477,8 +481,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
             const float rest = log2f(ldexpf(sum, -e));
             const Pair by = {0x1.62e43p-1f, 0x1.f8ff94p-28f};
             Pair l;
-            if (large) l = two_sum(top, 0.f);
-            else l = mul(add(two_sum(__fmul_rn(top, kLog2e), static_cast<float>(e)), rest), by);
+            if (fabsf(top) < kLarge) l = mul(add(two_sum(__fmul_rn(top, kLog2e), static_cast<float>(e)), rest), by);
+            else l = add(mul(two_sum(static_cast<float>(e), rest), by), top);
             if (!(sum < INFINITY) || !(fabsf(top) < INFINITY)) l.hi = l.lo = NAN;
             lse[k] = {0.25f * l.hi, 0.25f * l.lo};
             less[k] = score[k] - lse[k].hi;

@@ -2,6 +2,7 @@
 manager's reorder against the oracle's, and what the calls refuse."""
 import math
 import random
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -53,6 +54,26 @@ def test_selection_of_ties_bars_and_missing_candidates():
                       np.array([[1, 2]], np.int32), np.full((1, 2, 3), 9, np.int32))
     assert got[1].tolist() == [[3, -1]] and got[3].tolist() == [[True, False]]
     assert got[4].tolist() == [[2, 0]] and got[5].tolist() == [[[3, 4, 9], [9, 9, 9]]]
+
+
+def test_selection_of_large_logits():
+    """Against sums of fractions: rows of masks alone, masks behind other logits, and
+    logits so large that float64 does not hold what the beams' scores add."""
+    rng = np.random.default_rng(3)
+    for size in (1e9, 1e20, 1e30, 3e38):
+        logits, scores = rng.standard_normal((4, 6)).astype(np.float32).astype(np.float64), -rng.random((2, 2))
+        size = float(np.float32(size))
+        logits[0, 2:], logits[1], logits[2, 1], logits[3, ::2] = -size, -size, size, size
+        got = beam.select(logits, scores, np.zeros((2, 2), bool), -1, 12)
+        for b in range(2):
+            every = []
+            for k in range(2):
+                x = [Fraction(v) for v in logits[2 * b + k]]
+                rest = math.log(sum(math.exp(float(v - max(x))) for v in x))
+                every += [(-(v - max(x) + Fraction(scores[b, k] - rest)), k * 6 + i) for i, v in enumerate(x)]
+            every.sort()
+            assert (got[2][b] * 6 + got[1][b]).tolist() == [at for _, at in every]
+            assert np.allclose(got[0][b], [-float(s) for s, _ in every])
 
 
 # ---- reorder --------------------------------------------------------------------

@@ -171,6 +171,65 @@ def test_nan_and_infinite_logits(pkv):
     assert (out.parents[0] == 1).all() and (out.parents[1] == 0).all()
 
 
+MASKS = [-1.0e4, -65504.0, -1.0e9, -5.0e9, -1.0e10, -1.0e12, -1.0e18, -1.0e20, -1.0e30, -1.0e37, -3.3e38]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("mask", MASKS)
+def test_tokens_barred_by_a_large_finite_logit(pkv, mask, dtype):
+    """Single tokens, the shares of whole warps, threads and chunks, all tokens but
+    three, and whole rows."""
+    rng = np.random.default_rng(13)
+    vocab = 20_011
+    for kept in (None, [17, 4000, 20_010]):
+        logits = _logits(rng, 8, vocab, dtype)
+        if kept is None:
+            logits[:, rng.integers(0, vocab, 40)] = mask
+            logits[1, :256] = mask
+            logits[2, 4096:9001] = mask
+            logits[3, 700:] = mask
+        else:
+            held = logits[:, kept].clone()
+            logits[:] = mask
+            logits[:, kept] = held
+        logits[5] = mask
+        logits[6:] = mask
+        _check(pkv, logits, _scores(rng, 4, 2), n=8, room=3)
+        _check(pkv, logits[:, 1:], _scores(rng, 2, 4), n=20)
+    # many chunks a row
+    logits = _logits(rng, 3, 400_000, dtype)
+    logits[:, 1000:390_000] = mask
+    logits[2] = mask
+    _check(pkv, logits, _scores(rng, 1, 3), n=9)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size", [2.0e9, 1.0e20, 1.0e38, 3.0e38])
+def test_rows_whose_largest_logit_is_large(pkv, size, dtype):
+    rng = np.random.default_rng(14)
+    logits = _logits(rng, 8, 9001, dtype)
+    logits[0, 5000], logits[1, 8], logits[1, 7000] = size, size, size
+    logits[2] += size
+    logits[3] -= size
+    logits[4], logits[4, ::3] = -size, -size / 2
+    logits[5, 300:600] = -size
+    logits[6], logits[6, 77] = size, size / 4
+    _check(pkv, logits, _scores(rng, 4, 2), n=8)
+    _check(pkv, logits, _scores(rng, 1, 8), n=30)
+
+
+@pytest.mark.parametrize("at", [2.0 ** 24, -(2.0 ** 24), 2.0 ** 22, -(2.0 ** 22), 2.0 ** 23])
+def test_logits_near_where_sums_are_formed_otherwise(pkv, at):
+    """Neighbours of 2^24, of either sign, whose differences count: chunks and warps
+    whose largest is below it beside others."""
+    rng = np.random.default_rng(15)
+    x = at + rng.integers(-9, 10, (6, 30_003))
+    x[:, ::2] -= 40
+    x[3:, 2048:] -= 8
+    x[4, 25_000:] -= 30
+    _check(pkv, torch.from_numpy(x).float().cuda(), _scores(rng, 3, 2), n=7)
+
+
 def test_all_beams_finished(pkv):
     rng = np.random.default_rng(7)
     logits = torch.full((4, 300), float("nan"), dtype=torch.bfloat16, device="cuda")
