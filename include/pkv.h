@@ -460,6 +460,8 @@ pkv_status pkv_attn_decode_int4(const void* q, const void* cache, const int32_t*
  * with the highest scores are taken, equal scores in the order of k * vocab + v.
  * A candidate whose score is NaN or -inf is none: barred tokens have logits of
  * -inf, beams that do not exist yet scores of -inf (their logits are not read).
+ * A beam whose score is +inf comes first: all its tokens with logits above -inf
+ * have that score, so the lowest of them are taken.
  *   logits       : device, bf16 (logits_bytes = 2) or fp32 (4); num_groups *
  *                  num_beams rows of vocab contiguous values, one every
  *                  row_stride >= vocab values; any alignment

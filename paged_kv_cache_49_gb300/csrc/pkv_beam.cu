@@ -407,7 +407,12 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
     }
     // index `at` of the chunk's candidates, counted down, so that the lower is the larger
     auto packed = [&](float x, int at) { return static_cast<uint64_t>(ordered(x)) << 32 | static_cast<uint32_t>(~at); };
-    if (best >= cut) {
+    // Of a beam whose score is +inf all scores are, so its logits above -inf are equal
+    // here: more than a list holds, as far as finish() is told.
+    const bool pinned = p.scores[row] == INFINITY;
+    if (pinned) {
+        if (threadIdx.x == 0) sel.count = kList + 1;
+    } else if (best >= cut) {
         uint64_t hits = reach(v, cut);
         int slot = atomicAdd(&sel.count, __popcll(hits));
         for (; hits; hits &= hits - 1, ++slot) {
@@ -424,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const Params p) {
         sel, p.n, hi - lo,
         [&](int i, uint64_t& k, int&) {
             const float x = static_cast<float>(logits[lo + i]);
-            k = packed(x, lo + i);
+            k = packed(pinned ? 0.f : x, lo + i);
             return x > -INFINITY;
         },
         [&](int rank, uint64_t k, int) {
@@ -521,9 +526,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
         const uint2 c = ended ? make_uint2(0u, static_cast<uint32_t>(p.eos)) : lists[from.at];
         at = k * p.vocab + static_cast<int>(c.y);
         const Pair l = lse[k];
-        const Pair s = ended ? Pair{score[k], 0.f} : add(add(two_sum(0.25f * __uint_as_float(c.x), -l.hi), -l.lo), score[k]);
+        // (no pair holds an infinity: less[k] is NaN where the row's logits make it none)
+        const bool pinned = score[k] == INFINITY;
+        const Pair s = ended || pinned ? Pair{ended ? score[k] : less[k], 0.f}
+                                       : add(add(two_sum(0.25f * __uint_as_float(c.x), -l.hi), -l.lo), score[k]);
         key = static_cast<uint64_t>(ordered(s.hi)) << 32 | ordered(s.lo);
-        return static_cast<int>(c.y) >= 0 && s.hi > -INFINITY && s.hi < INFINITY;  // (false for NaN)
+        return static_cast<int>(c.y) >= 0 && s.hi > -INFINITY;  // (false for NaN)
     };
     // The cut is from the lists' first entries: a turn of the threads takes 256
     // candidates, and the first turns take those of every list.
@@ -551,7 +559,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p) {
     // these.
     const float t = lane < p.beams ? fabsf(score[lane]) + fabsf(lse[lane].hi) : 0.f;
     const float terms = __uint_as_float(__reduce_max_sync(0xffffffffu, t < INFINITY ? __float_as_uint(t) : 0u));
-    cut -= 0x1p-21f * (2.f * terms + fabsf(cut));
+    if (cut < INFINITY) cut -= 0x1p-21f * (2.f * terms + fabsf(cut));
     cut = fmaxf(cut, -0x1.fffffep127f);  // (-inf is no candidate)
     auto take = [&](int i) {
         uint64_t key;

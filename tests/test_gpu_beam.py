@@ -230,6 +230,31 @@ def test_logits_near_where_sums_are_formed_otherwise(pkv, at):
     _check(pkv, torch.from_numpy(x).float().cuda(), _scores(rng, 3, 2), n=7)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_beams_with_scores_of_plus_infinity(pkv, dtype):
+    """They come first, live and finished ones; of a live one the lowest tokens that are
+    not barred, unless its logits are no numbers."""
+    rng = np.random.default_rng(16)
+    inf = np.inf
+    scores = np.array([[-1.0, inf, -2.0], [inf, inf, -1.0], [inf, -3.0, inf], [-1.0, -2.0, inf], [inf, -inf, inf]], np.float32)
+    finished = np.array([[0, 0, 0], [0, 1, 0], [0, 0, 0], [0, 1, 1], [1, 0, 1]], bool)
+    for vocab in (5, 3000, 30_011):
+        for n in (3, 20, 64):
+            logits = _logits(rng, 15, vocab, dtype)
+            logits[1, : vocab // 2] = -inf
+            logits[3] = -inf
+            logits[3, vocab - 1], logits[3, vocab // 2] = 1.0, -2.0
+            logits[6, vocab // 3] = float("nan")
+            logits[8] = -inf
+            out = pkv.beam_select(logits, torch.from_numpy(scores).cuda(), torch.from_numpy(finished).cuda(), 2, candidates=n)
+            want = beam.select(logits.double().cpu().numpy(), scores, finished, 2, n)
+            for got, w in zip((out.tokens, out.parents, out.finished), want[1:]):
+                assert np.array_equal(got.cpu().numpy(), w)
+            got, large = out.scores.cpu().numpy(), want[0] == inf
+            assert (got[large] == inf).all() and large.any(axis=1).tolist() == [True, True, False, True, True]
+            _near(np.where(large, 0, got), np.where(large, 0, want[0]))
+
+
 def test_all_beams_finished(pkv):
     rng = np.random.default_rng(7)
     logits = torch.full((4, 300), float("nan"), dtype=torch.bfloat16, device="cuda")
