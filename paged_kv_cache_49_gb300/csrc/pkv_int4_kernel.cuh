@@ -23,9 +23,10 @@
 //    The queries are scaled by a power of two per head so that fp16 holds them
 //    without loss.
 //  * Weights are 2^(x - max + 10), so what fp16 drops of them is below 2^-35 of
-//    the largest; where a value's scale is 32 or more, 2^(x - max + 2), for
-//    weight times scale to stay in range. A third product with rows of the
-//    values' minima and of ones gives sum p m and the softmax's denominator.
+//    the largest (less room where fp32 holds no max - 10, from 2^24 on); where a
+//    value's scale is 32 or more, 2^(x - max + 2), for weight times scale to stay
+//    in range. A third product with rows of the values' minima and of ones gives
+//    sum p m and the softmax's denominator.
 //
 // Work. A run is one sequence and up to 4 of its KV heads (the most of 4, 2, 1
 // that divide their number), in tiles of 16 tokens a consumer warp: with 4 heads a
@@ -336,7 +337,9 @@ __device__ __forceinline__ void add_tiles(uint8_t* const (&at)[kSubs], const int
         for (int d = 4; d < 32; d <<= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], d));
     }
     if (__any_sync(0xffffffffu, (scales & 0xffffu) >= 0x5000u || (scales >> 16) >= 0x5000u)) st.offset = 2.f;  // 32 in fp16
-    const float base[2] = {top[0] - st.offset, top[1] - st.offset};
+    // rounded up: where fp32 numbers are 16 apart (tops of 2^27 and more), one below the
+    // difference would have the largest weight 2^16, which is none in fp16
+    const float base[2] = {__fsub_ru(top[0], st.offset), __fsub_ru(top[1], st.offset)};
     if (__any_sync(0xffffffffu, base[0] != st.base[0] || base[1] != st.base[1])) {
         const float f[2] = {ex2(st.base[0] - base[0]), ex2(st.base[1] - base[1])};
 #pragma unroll

@@ -336,6 +336,48 @@ def test_values_of_any_size(pkv, size):
     _decode(pkv, rng, [300, 33], 8, 2, pool=Pool(pkv, rng, 25, 2, 16, 64, v=v))
 
 
+def _attend(pkv, pool, tables, lens, q, scale, **kw):
+    """(out float64, the oracle's) of q float64, which bf16 holds."""
+    ws = pkv.AttentionWorkspace(len(lens), pool.cache.num_kv_heads)
+    got = pkv.attn_decode_int4(torch.from_numpy(q).to(torch.bfloat16).cuda(), pool.cache, torch.from_numpy(tables).cuda(),
+                               torch.tensor(lens, dtype=torch.int32, device="cuda"), scale, workspace=ws, **kw)
+    assert ws.read_error() == 0
+    return _f32(pkv.bits_from_bf16(got)).astype(np.float64), int4.decode(q, pool.k, pool.v, tables, lens, scale)
+
+
+def _bf16_rows(x):
+    return torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("size", [1.0, 60000.0])
+def test_scores_of_any_size(pkv, size, sign):
+    """Scores from 2^15 to 2^34, a factor of 1.4 at a time, so far apart that each row
+    is one token's value: no weight leaves fp16 where fp32 scores are 16 apart. What
+    may differ: the output's rounding, 2^-8 of it, and that of weight times scale,
+    2^-11 of the value's terms."""
+    rng = np.random.default_rng(24)
+    lens = [40, 333]
+    v = size * np.clip(rng.standard_normal((30 * 16, 2, 128)), -1.05, 1.05)
+    pool = Pool(pkv, rng, 30, 2, 16, 64, v=_bf16_rows(v).view(torch.int16).numpy().view(np.uint16))
+    tables = _batch(rng, lens, 30, 16)
+    q = _bf16_rows(rng.standard_normal((2, 16, 128))).double().numpy()
+    for step in range(38):
+        scale = sign * 2.0 ** (10 + step / 2)
+        got, (want, a, e) = _attend(pkv, pool, tables, lens, q, scale)
+        # rows whose two best scores differ by less than fp32's rounding of their terms could be either's
+        clear = np.ones(want.shape[:2], bool)
+        for b, n in enumerate(lens):
+            t = np.arange(n)
+            for h in range(16):
+                key = int4.values(*(x[tables[b][t // 16], h // 8, t % 16] for x in pool.k))
+                best = np.sort(scale * (key @ q[b, h]))[-2:]
+                clear[b, h] = best[1] - best[0] > 2.0 ** -16 * abs(e).max() + 20
+        assert clear.mean() > 0.9
+        assert np.isfinite(got).all(), (scale, np.isnan(got).any(axis=-1))
+        assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -11 * a)[clear].all(), scale
+
+
 def test_nan_where_it_is_seen(pkv):
     """A NaN in a key reaches its heads, one in a group of a value those dims."""
     rng = np.random.default_rng(14)
