@@ -421,8 +421,11 @@ pkv_status pkv_attn_tree(const void* q, const void* k_draft, const void* v_draft
  *   the batch (0 when no device is present); fewer bytes are taken as they are
  *   and make fewer CTAs do the work, less than one CTA's share is refused
  *   (PKV_EINVAL). num_ctas: as there, at most 512. fp32 sums and softmax; the
- *   weights enter the product with the values in fp16. What lies behind a
- *   context in its last block, NaN scales included, never reaches the output.
+ *   weights, and their products with the values' scales, enter the product with
+ *   the values in fp16: each rounded by 2^-11 of itself at most, and by less than
+ *   2^-29 of the largest weight times the largest scale where that is more (from
+ *   scales of 2^-17 on; of scales of 2^-24, 2^-22). What lies behind a context in
+ *   its last block, NaN scales included, never reaches the output.
  */
 size_t pkv_int4_block_bytes(int num_kv_heads, int block_tokens, int group_dims);
 

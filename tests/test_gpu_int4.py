@@ -378,6 +378,72 @@ def test_scores_of_any_size(pkv, size, sign):
         assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -11 * a)[clear].all(), scale
 
 
+def _dropped(scale):
+    """What fp16 drops of a weight (of 1 at most) times a value's scale, given the largest
+    scale up to a factor of 2: 2^-25 of products that are held times 2^10, and times
+    2^11 more where all scales are below 2^-6; times 2^2 where they reach 32."""
+    return 2.0 ** -46 if scale < 2.0 ** -7 else 2.0 ** -35 if scale < 16 else 2.0 ** -27
+
+
+@pytest.mark.parametrize("gd", [32, 64, 128])
+@pytest.mark.parametrize("top", [2.0 ** -16, 2.0 ** -13, 2.0 ** -8, 1.0])
+def test_many_small_weights_beside_a_large_one(pkv, top, gd):
+    """One token of weight 1 and 2^15 of 2^-15, all in one warp's piece, with values up
+    to `top`: half of the output is theirs, weight times scale far below 2^-14."""
+    rng = np.random.default_rng(25)
+    n, hkv = 1 + (1 << 15), 4
+    blocks = -(-n // 64)
+    k, v = np.zeros((blocks * 64, hkv, 128), np.float32), np.zeros((blocks * 64, hkv, 128), np.float32)
+    v[:] = top * (np.arange(128) * 37 % 128) / 127
+    bits = lambda x: _bf16_rows(x).view(torch.int16).numpy().view(np.uint16)
+    at = 7001  # the token of weight 1: value zero
+    pool = Pool(pkv, rng, blocks, hkv, 64, gd, bits(k), bits(v))
+    tables = np.arange(blocks, dtype=np.int32)[None]
+    key = np.zeros((1, hkv, 128), np.float32)
+    key[:, :, 0] = 1.0
+    kb, vb = _bf16_rows(key), _bf16_rows(0 * key)
+    pkv.append_int4(kb.cuda(), vb.cuda(), torch.tensor([at], device="cuda"), pool.cache)
+    for held, x in ((pool.k, kb), (pool.v, vb)):
+        for dst, src in zip(held, int4.quantise(x.float().numpy(), gd)):
+            dst[at // 64, :, at % 64] = src[0]
+    q = np.zeros((1, 2 * hkv, 128))
+    q[:, ::2, 0], q[:, 1::2, 0] = 8.0, 16.0  # (and of 2^-30)
+    got, (want, a, e) = _attend(pkv, pool, tables, [n], q, 15 * np.log(2) / 8, num_ctas=1)
+    # roundings as in _near(), and what fp16 drops: of n weights 2^-25 of 2^10 each, times
+    # value and output; of n products as _dropped() says, times codes up to 15.
+    tol = 2.0 ** -8 * np.abs(want) + a * (3 * 2.0 ** -11 + 2.0 ** -16 * e[..., None] + 2.0 ** -14)
+    tol += n * (15 * _dropped(top / 15) + 2.0 ** -34 * top)
+    assert want[0, 0].max() > 0.45 * top and (np.abs(got - want) <= tol).all(), (np.abs(got - want) - tol).max() / top
+
+
+@pytest.mark.parametrize("num_ctas", [0, 1])
+@pytest.mark.parametrize("growing", [True, False])
+def test_values_that_grow_along_a_context(pkv, growing, num_ctas):
+    """Tiles whose values' scales rise or fall from 2^-19 to 2^12 along a context of
+    equal weights, so that what the sums are held in units of changes on the way."""
+    rng = np.random.default_rng(26)
+    n = 4001
+    blocks = -(-n // 16) + 3
+    tables = _batch(rng, [n], blocks, 16)
+    v = np.clip(rng.standard_normal((blocks * 16, 2, 128)), -1, 1).astype(np.float32)
+    size = 2.0 ** (-19 + 34 * np.arange(n) / n)
+    slot = tables[0][np.arange(n) // 16].astype(np.int64) * 16 + np.arange(n) % 16
+    pool = Pool(pkv, rng, blocks, 2, 16, 64)
+    v[:n] *= (size if growing else size[::-1])[:, None, None].astype(np.float32)
+    k0, v0 = torch.zeros((n, 2, 128)).to(torch.bfloat16), _bf16_rows(v[:n])
+    pkv.append_int4(k0.cuda(), v0.cuda(), torch.from_numpy(slot).cuda(), pool.cache)
+    for held, x in ((pool.k, k0), (pool.v, v0)):
+        for dst, src in zip(held, int4.quantise(x.float().numpy(), 64)):
+            dst[slot // 16, :, slot % 16] = src
+    q = _bf16_rows(rng.standard_normal((1, 8, 128))).double().numpy()
+    for m in (n, 16, 100, 1000, 3000):  # (growing: of the small ones alone)
+        got, (want, a, e) = _attend(pkv, pool, tables, [m], q, 0.1, num_ctas=num_ctas)
+        tol = 2.0 ** -8 * np.abs(want) + a * (3 * 2.0 ** -11 + 2.0 ** -14)
+        big = (size if growing else size[::-1])[:m].max()
+        tol += 15 * _dropped(big / 7.5)  # of m products, each of weight 1 / m
+        assert (np.abs(got - want) <= tol).all(), (m, (np.abs(got - want) - tol).max())
+
+
 def test_nan_where_it_is_seen(pkv):
     """A NaN in a key reaches its heads, one in a group of a value those dims."""
     rng = np.random.default_rng(14)
