@@ -444,6 +444,55 @@ def test_values_that_grow_along_a_context(pkv, growing, num_ctas):
         assert (np.abs(got - want) <= tol).all(), (m, (np.abs(got - want) - tol).max())
 
 
+@pytest.mark.parametrize("lens,hq,hkv,num_ctas", [([40_001], 8, 1, 0), ([40_001], 8, 1, 512), ([131_072], 16, 4, 0),
+                                                  ([4097, 0, 1500], 8, 2, 7), ([4097, 0, 1500], 8, 2, 64),
+                                                  ([4097, 0, 1500], 8, 2, 152), ([4097, 0, 1500], 8, 2, 304)])
+def test_no_stretch_of_a_context_is_lost(pkv, lens, hq, hkv, num_ctas):
+    """Each of the values' dims stands for a stretch of the context: a result that leaves
+    out, or counts twice, 1/300 of it is far from the bounds."""
+    rng = np.random.default_rng(27)
+    bt, gd = 16, 64
+    blocks = sum(-(-n // bt) for n in lens) + 3
+    pool = Pool(pkv, rng, blocks, hkv, bt, gd)
+    tables = _batch(rng, lens, blocks, bt)
+    slots, rows = [], []
+    for b, n in enumerate(lens):
+        t = np.arange(n)
+        slots.append(tables[b][t // bt].astype(np.int64) * bt + t % bt)
+        rows.append(0.2 * rng.random((n, hkv, 128)))
+        rows[b][t, :, t * 128 // max(n, 1)] += 3.0
+    slots, v = np.concatenate(slots), _bf16_rows(np.concatenate(rows))
+    order = np.argsort(pool.slots)
+    k_bits = pool.k_bits[order][slots]
+    pkv.append_int4(_dev(pkv, k_bits), v.cuda(), torch.from_numpy(slots).cuda(), pool.cache)
+    for dst, src in zip(pool.v, int4.quantise(v.float().numpy(), gd)):
+        dst[slots // bt, :, slots % bt] = src
+    q = _bf16_rows(0.3 * rng.standard_normal((len(lens), hq, 128))).double().numpy()
+    got, (want, a, e) = _attend(pkv, pool, tables, lens, q, 0.09, num_ctas=num_ctas)
+    # roundings as in _near(), and what fp16 drops of n weights and products
+    most, span = float(pool.v[1].max()), float(np.abs(v.float().numpy()).max())
+    tol = 2.0 ** -8 * np.abs(want) + a * (3 * 2.0 ** -11 + 2.0 ** -16 * e[..., None] + 2.0 ** -14)
+    tol += np.array(lens)[:, None, None] * (15 * _dropped(most) + 2.0 ** -34 * span)
+    assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) - tol).max()
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        t = np.arange(n)
+        at = tables[b][t // bt]
+        for lo in (0, n // 2, n - n // 300):
+            lost = (t >= lo) & (t < lo + n // 300)
+            for times in (0.0, 2.0):  # left out, counted twice
+                worst = 0.0
+                for g in range(hkv):
+                    key, val = (int4.values(*(x[at, g, t % bt] for x in kv)) for kv in (pool.k, pool.v))
+                    h = slice(g * hq // hkv, (g + 1) * hq // hkv)
+                    x = 0.09 * (q[b, h] @ key.T)
+                    w = np.exp(x - x.max(axis=-1, keepdims=True)) * np.where(lost, times, 1.0)
+                    wrong = w @ val / w.sum(axis=-1, keepdims=True)
+                    worst = max(worst, (np.abs(wrong - want[b, h]) / tol[b, h]).max())
+                assert worst > 5, (b, lo, times, worst)
+
+
 def test_nan_where_it_is_seen(pkv):
     """A NaN in a key reaches its heads, one in a group of a value those dims."""
     rng = np.random.default_rng(14)
@@ -650,6 +699,38 @@ def test_a_pool_past_four_gigabytes(pkv):
                                torch.tensor(lens, dtype=torch.int32, device="cuda"), 0.1)
     want, a, e = int4.decode(q.double().numpy(), *held, [[0, 1, 2, 3]], lens, 0.1)
     _near(pkv.bits_from_bf16(got), want, a, e, lens)
+
+
+def test_grids_and_workspaces_at_their_limits(pkv):
+    """512 CTAs and no more; as many as the bytes hold, fewer where the call may choose,
+    and a share at least."""
+    from paged_kv_cache_49_gb300 import _native as nat
+    rng = np.random.default_rng(28)
+    lens = [700, 0, 333]
+    pool = Pool(pkv, rng, 70, 4, 16, 64)
+    (q, cache, tables, ctx, scale), _, _ = _decode(pkv, rng, lens, 8, 4, pool=pool)
+    oracle = int4.decode(q.double().cpu().numpy(), pool.k, pool.v, tables.cpu().numpy(), lens, scale)
+    fixed, share = pkv.AttentionWorkspace.fixed_bytes(), 2 * 8 * 132 * 4  # (8 query rows a run)
+    space = torch.zeros(fixed + 512 * share + 256, dtype=torch.uint8, device="cuda")
+    at = -(-space.data_ptr() // 256) * 256
+
+    def call(num_ctas, nbytes):
+        out = torch.full_like(q, 9.0)
+        st = nat.lib.pkv_attn_decode_int4(q.data_ptr(), cache.data.data_ptr(), tables.data_ptr(), tables.shape[1], ctx.data_ptr(), 3,
+                                          8, 4, 128, cache.num_blocks, 16, 64, scale, num_ctas, at, nbytes, out.data_ptr(),
+                                          torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert not space[at - space.data_ptr():][:256].any()  # the error word
+        return st, out
+
+    for num_ctas, shares in ((512, 512), (3, 3), (0, 3), (0, 1), (1, 1), (0, 512)):
+        st, out = call(num_ctas, fixed + shares * share)
+        assert st == nat.PKV_OK
+        _near(pkv.bits_from_bf16(out), *oracle, lens)
+    for num_ctas, nbytes in ((513, fixed + 512 * share), (4, fixed + 3 * share), (4, fixed + 4 * share - 1), (0, fixed + share - 1),
+                             (1, fixed), (0, 0)):
+        st, out = call(num_ctas, nbytes)
+        assert st == nat.PKV_EINVAL and (out == 9).all()
 
 
 def test_refusals_on_the_gpu(pkv):
