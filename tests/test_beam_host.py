@@ -223,6 +223,42 @@ def test_c_calls_refuse(pkv):
         assert L.pkv_beam_workspace_size(*shape) == 0
 
 
+def _apart():
+    """Arguments that the call takes, each at an address of its own."""
+    names = ("x", "s", "fin", "h", "ln", "so", "to", "po", "fo", "lo", "ho", "ws")
+    a = {name: (i + 1) << 24 for i, name in enumerate(names)}
+    return dict(a, stride=100, size=2, eos=1, g=2, k=4, n=8, v=100, room=5, nb=1 << 20)
+
+
+def _select(a):
+    from paged_kv_cache_49_gb300 import _native as nat
+    return nat.lib.pkv_beam_select(a["x"], a["stride"], a["size"], a["s"], a["fin"], a["eos"], a["g"], a["k"], a["n"], a["v"],
+                                   a["h"], a["ln"], a["room"], a["so"], a["to"], a["po"], a["fo"], a["lo"], a["ho"], a["ws"],
+                                   a["nb"], None, None)
+
+
+@pytest.mark.parametrize("told", [True, False])
+def test_each_argument_is_refused_by_its_own_check(pkv, told):
+    """One argument at a time is wrong, the others are such as the call takes (as
+    test_gpu_beam.py shows); each checked bound from its refused side."""
+    from paged_kv_cache_49_gb300 import _native as nat
+    ok = _apart()
+    if not told:
+        ok.update(h=None, ln=None, lo=None, ho=None, room=0)
+    need = 256 * ((2 * 4 * 8 + 255) // 256) + 256 * ((2 * 4 * 8 * 8 + 255) // 256)  # one chunk a row
+    bad = [dict(x=None), dict(s=None), dict(so=None), dict(to=None), dict(po=None), dict(fo=None), dict(ws=None), dict(g=0),
+           dict(k=0), dict(n=0), dict(v=0), dict(g=-1), dict(stride=99), dict(stride=-100), dict(eos=100), dict(eos=-2), dict(eos=-1),
+           dict(room=-1), dict(x=ok["x"] + 1), dict(x=ok["x"] + 2, size=4), dict(ws=ok["ws"] + 128), dict(nb=need - 1), dict(nb=0)]
+    if told:
+        bad += [dict(h=None), dict(ln=None), dict(lo=None), dict(ho=None), dict(room=0)]
+    else:
+        bad += [dict(h=1 << 26, room=5), dict(ln=1 << 26, room=5), dict(lo=1 << 26, room=5), dict(ho=1 << 26, room=5)]
+    for change in bad:
+        assert _select({**ok, **change}) == nat.PKV_EINVAL, change
+    for change in (dict(k=33), dict(n=65), dict(size=1), dict(size=8)):
+        assert _select({**ok, **change}) == nat.PKV_EUNSUPPORTED, change
+
+
 def test_outputs_on_inputs_are_refused(pkv):
     """Whole, by their last byte and by their first."""
     from paged_kv_cache_49_gb300 import _native as nat

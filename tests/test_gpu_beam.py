@@ -359,6 +359,46 @@ def test_two_calls_at_once(pkv):
         assert torch.equal(x.scores, want.scores) and torch.equal(x.tokens, want.tokens) and torch.equal(x.parents, want.parents)
 
 
+@pytest.mark.parametrize("told", [True, False])
+def test_arguments_next_to_one_another_are_taken(pkv, told):
+    """Inputs and outputs in one allocation, each output directly before or behind an
+    input, with the least workspace: what the refusals' tests change one by one."""
+    from paged_kv_cache_49_gb300 import _native as nat
+    rng = np.random.default_rng(17)
+    g, k, n, v, room = 2, 4, 8, 100, 5
+    logits, scores = _logits(rng, g * k, v), _scores(rng, g, k)
+    fin = rng.random((g, k)) < 0.3
+    hist, lens = rng.integers(0, v, (g, k, room)).astype(np.int32), rng.integers(0, room, (g, k)).astype(np.int32)
+    given = {"x": logits, "s": torch.from_numpy(scores), "fin": torch.from_numpy(fin), "h": torch.from_numpy(hist),
+             "ln": torch.from_numpy(lens)}
+    sizes = {"x": g * k * v * 2, "s": g * k * 4, "fin": g * k, "h": g * k * room * 4, "ln": g * k * 4, "so": g * n * 4, "to": g * n * 4,
+             "po": g * n * 4, "fo": g * n, "lo": g * n * 4, "ho": g * n * room * 4}
+    # sizes are multiples of 8 here; every output lies between two inputs or beside one
+    order = ["so", "x", "to", "s", "po", "h", "fo", "fin", "lo", "ln", "ho"]
+    space, at = torch.zeros(sum(sizes.values()), dtype=torch.uint8, device="cuda"), {}
+    for name in order:
+        at[name] = sum(sizes[o] for o in at)
+    view = lambda name, dtype: space[at[name]:at[name] + sizes[name]].view(dtype)
+    for name, t in given.items():
+        view(name, t.dtype).copy_(t.reshape(-1))
+    view("ho", torch.int32).fill_(-9)
+    need = 256 * ((g * k * 8 + 255) // 256) + 256 * ((g * k * n * 8 + 255) // 256)
+    ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+    p = {name: space.data_ptr() + at[name] if told or name not in ("h", "ln", "lo", "ho") else None for name in order}
+    st = nat.lib.pkv_beam_select(p["x"], v, 2, p["s"], p["fin"], 1, g, k, n, v, p["h"], p["ln"], room if told else 0, p["so"], p["to"],
+                                 p["po"], p["fo"], p["lo"], p["ho"], -(-ws.data_ptr() // 256) * 256, need, None,
+                                 torch.cuda.current_stream().cuda_stream)
+    assert st == nat.PKV_OK
+    want = beam.select(logits.double().cpu().numpy(), scores, fin, 1, n, hist, lens, np.full((g, n, room), -9, np.int32))
+    got = [view(name, dtype).cpu().numpy().reshape(g, n, -1) for name, dtype in (
+        ("so", torch.float32), ("to", torch.int32), ("po", torch.int32), ("fo", torch.bool), ("lo", torch.int32), ("ho", torch.int32))]
+    _near(got[0][..., 0], want[0])
+    for a, b in list(zip(got[1:], want[1:]))[:5 if told else 3]:
+        assert np.array_equal(a, b.reshape(a.shape))
+    for name, t in given.items():  # as they were
+        assert torch.equal(view(name, t.dtype).cpu(), t.reshape(-1).cpu())
+
+
 def test_refusals_on_the_gpu(pkv):
     z = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype, device="cuda")
     logits, scores, i32 = z(4, 50), z(2, 2), torch.int32
