@@ -275,20 +275,39 @@ def launch_ctas(num_seqs: int, num_kv_heads: int, max_blocks_per_seq: int, block
 class AttentionWorkspace:
     """Device scratch for attn_decode: error word, merge counters and per-CTA
     partials, zeroed once at creation. One workspace serves calls of any
-    batch and grid whose partial slots fit in it."""
+    batch and grid whose partial slots fit in it. attn_decode_int4 leaves more
+    partial results a CTA, behind the same counters: with int4 the workspace has
+    room for them from the start, else its first such call moves it to a larger
+    buffer (not while a graph is captured: fewer CTAs do the work then, as in a
+    workspace of fewer bytes)."""
 
-    def __init__(self, num_seqs: int, num_kv_heads: int, device=None, stream=None):
+    def __init__(self, num_seqs: int, num_kv_heads: int, device=None, stream=None, int4: bool = False):
         nbytes = int(_lib.pkv_attn_workspace_size(num_seqs, num_kv_heads))
         if nbytes == 0:
             raise PkvError(PKV_EINVAL, "pkv_attn_workspace_size")
         self.num_seqs, self.num_kv_heads, self.nbytes = num_seqs, num_kv_heads, nbytes
-        # attn_decode_int4 leaves more partial results a CTA, behind the same counters
-        self.int4_nbytes = max(nbytes, int(_lib.pkv_attn_int4_workspace_size()))
-        self.buffer = torch.empty(self.int4_nbytes + 256, dtype=torch.uint8, device=device or "cuda")
+        self.int4_nbytes = 0  # of the buffer, where it has room for attn_decode_int4's results
+        self._before: list[torch.Tensor] = []  # buffers that captured graphs may still use
+        device = torch.device(device or "cuda")
+        if int4:
+            with torch.cuda.device(device):
+                self.int4_nbytes = max(nbytes, int(_lib.pkv_attn_int4_workspace_size()))
+        self._take(self.int4_nbytes or nbytes, device, _stream(stream))
+
+    def _take(self, nbytes: int, device, stream: int) -> None:
+        self.buffer = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
         off = (-self.buffer.data_ptr()) % 256
-        self.tensor = self.buffer[off : off + nbytes]
-        _check(_lib.pkv_attn_workspace_init(self.tensor.data_ptr(), nbytes, _stream(stream)),
-               "pkv_attn_workspace_init")
+        self.tensor = self.buffer[off : off + self.nbytes]
+        _check(_lib.pkv_attn_workspace_init(self.tensor.data_ptr(), self.nbytes, stream), "pkv_attn_workspace_init")
+
+    def for_int4(self, stream: int) -> int:
+        """Bytes of the workspace for a call of attn_decode_int4 on the current device
+        and stream."""
+        if not self.int4_nbytes and not torch.cuda.is_current_stream_capturing():
+            self._before.append(self.tensor)
+            self.int4_nbytes = max(self.nbytes, int(_lib.pkv_attn_int4_workspace_size()))
+            self._take(self.int4_nbytes, self.tensor.device, stream)
+        return self.int4_nbytes or self.nbytes
 
     @property
     def ptr(self) -> int:
@@ -304,7 +323,10 @@ class AttentionWorkspace:
         return self.tensor[:4].view(torch.int32)
 
     def read_error(self, clear: bool = True, stream=None) -> int:
-        return read_device_error(self.error_word(), clear, stream)
+        error = read_device_error(self.error_word(), clear, stream)
+        for tensor in self._before:
+            error |= read_device_error(tensor[:4], clear, stream)
+        return error
 
 
 def attn_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out=None, workspace=None,
@@ -875,8 +897,8 @@ def block_copy_int4(cache: Int4Cache, pairs, device_error=None, stream=None) -> 
 def attn_decode_int4(q, cache: Int4Cache, block_tables, context_lens, scale, out=None, workspace=None, num_ctas: int = 0,
                      stream=None):
     """attn_decode over a cache held in 4 bits; returns out [B, Hq, 128] bf16.
-    workspace: an AttentionWorkspace; without one the call makes it, and device
-    errors are not reported."""
+    workspace: an AttentionWorkspace (made with int4 where the first call is a
+    captured one); without one the call makes it, and device errors are not reported."""
     device = q.get_device()
     _need_all(device, ((q, _BF16, "q"), (block_tables, _I32, "block_tables"), (context_lens, _I32, "context_lens")))
     st = _here(device, stream)
@@ -899,12 +921,13 @@ def attn_decode_int4(q, cache: Int4Cache, block_tables, context_lens, scale, out
         if out.shape != shape:
             raise ValueError("out must be shaped like q")
     if workspace is None:
-        workspace = AttentionWorkspace(B, hkv, device=q.device)
+        workspace = AttentionWorkspace(B, hkv, device=q.device, int4=True)
     elif workspace.tensor.get_device() != device:
         raise ValueError(f"the workspace is on {workspace.tensor.device}, the tensors on cuda:{device}")
+    nbytes = workspace.for_int4(st)
     _check(_lib.pkv_attn_decode_int4(q.data_ptr(), cache._ptr, block_tables.data_ptr(), tables[1], context_lens.data_ptr(), B,
                                      hq, hkv, d, cache.num_blocks, bt, gd, scale, num_ctas, workspace.ptr,
-                                     workspace.int4_nbytes, out.data_ptr(), st), "pkv_attn_decode_int4")
+                                     nbytes, out.data_ptr(), st), "pkv_attn_decode_int4")
     return out
 
 

@@ -475,7 +475,7 @@ class PagedKVEngine:
             tables=tables.to(dev), ctx=ctx.to(dev), q=q,
             k=bf16_from_bits(k_bits).to(dev), v=bf16_from_bits(v_bits).to(dev),
             out=torch.empty_like(q),
-            workspace=nat.AttentionWorkspace(len(seq_ids), self.num_kv_heads, device=dev))
+            workspace=nat.AttentionWorkspace(len(seq_ids), self.num_kv_heads, device=dev, int4=self.cache is not None))
 
     def run_step(self, sb: StepBuffers, scale: float, num_ctas: int = 0, stream=None) -> torch.Tensor:
         """The device part of a decode step -- copy-on-write copies, append,

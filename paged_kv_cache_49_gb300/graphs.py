@@ -43,7 +43,7 @@ class _Bucket:
         self.ctx = torch.zeros((size,), dtype=torch.int32, device=dev)
         self.out = torch.zeros((size, hq, d), dtype=torch.bfloat16, device=dev)
         self.no_pairs = torch.zeros((0, 2), dtype=torch.int32, device=dev)
-        self.ws = nat.AttentionWorkspace(size, hkv, device=dev)
+        self.ws = nat.AttentionWorkspace(size, hkv, device=dev, int4=eng.cache is not None)
         # pinned staging for the host-side inputs of a step
         self.h_slots = torch.full((size,), -1, dtype=torch.int64).pin_memory()
         self.h_tables = torch.full((size, width), -1, dtype=torch.int32).pin_memory()

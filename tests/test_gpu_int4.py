@@ -733,6 +733,81 @@ def test_grids_and_workspaces_at_their_limits(pkv):
         assert st == nat.PKV_EINVAL and (out == 9).all()
 
 
+def test_room_for_4_bit_calls_is_taken_by_them_alone(pkv):
+    """A workspace has the bf16 calls' bytes until its first call over a 4-bit cache;
+    what was captured before goes on in the bytes that it had, errors are read of both."""
+    from paged_kv_cache_49_gb300 import _native as nat
+    rng = np.random.default_rng(29)
+    small = nat.lib.pkv_attn_workspace_size(3, 2) + 256
+    large = max(small, nat.lib.pkv_attn_int4_workspace_size() + 256)
+    args, _, want = _decode(pkv, rng, [900, 20, 333], 8, 2)
+    want = want.clone()
+    k = torch.randn((90, 2, 16, 128), device="cuda").to(torch.bfloat16)
+    tables = torch.arange(90, dtype=torch.int32, device="cuda").view(3, 30)
+    ctx = torch.tensor([480, 1, 77], dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(want)
+    ws = pkv.AttentionWorkspace(3, 2)
+    bf16 = lambda **kw: pkv.attn_decode(args[0], k, k, tables, ctx, 0.1, workspace=ws, **kw)
+    first = bf16().clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bf16(out=out)
+    assert ws.buffer.numel() == small
+    bad = ctx.clone()
+    ctx[0] = 481  # past the table
+    bf16()
+    ctx.copy_(bad)
+    assert torch.equal(want, pkv.attn_decode_int4(*args, workspace=ws)) and ws.buffer.numel() == large
+    bad_tables = args[2].clone()
+    bad_tables[1, 0] = -1
+    pkv.attn_decode_int4(args[0], args[1], bad_tables, *args[3:], workspace=ws)
+    assert ws.read_error() == pkv.DEVERR_CONTEXT | pkv.DEVERR_BLOCK_ID and ws.read_error() == 0
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, first) and torch.equal(bf16(), first)
+        assert torch.equal(want, pkv.attn_decode_int4(*args, workspace=ws))
+    # made with room: the same results, captured by the first call too
+    ws = pkv.AttentionWorkspace(3, 2, int4=True)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkv.attn_decode_int4(*args, out=out, workspace=ws)
+    out.zero_()
+    g.replay()
+    assert ws.buffer.numel() == large and torch.equal(out, want) and torch.equal(bf16(), first)
+    # made without, and captured by the first call: in the bytes at hand, so of another
+    # cut (two results off by 2^-8 of up to 1 and by 2^-9 of their terms each: under 0.02)
+    ws = pkv.AttentionWorkspace(3, 2)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkv.attn_decode_int4(*args, out=out, workspace=ws)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert ws.buffer.numel() == small and (out.float() - want.float()).abs().max() < 0.02 and torch.equal(bf16(), first)
+    assert torch.equal(want, pkv.attn_decode_int4(*args, workspace=ws)) and ws.buffer.numel() == large
+    out.zero_()
+    g.replay()
+    assert (out.float() - want.float()).abs().max() < 0.02 and ws.read_error() == 0
+    assert small <= 256 + nat.lib.pkv_attn_workspace_size(3, 2) < large
+
+
+def test_engines_take_room_for_their_cache_alone(pkv):
+    """Of 16 and of 4 bits: the workspaces of steps and of captured steps."""
+    from paged_kv_cache_49_gb300 import _native as nat
+    for bits in (16, 4):
+        eng = pkv.PagedKVEngine(20, 8, 2, cache_bits=bits)
+        seq = eng.bm.admit(20, 8)
+        zeros = np.zeros((1, 8, 128), np.uint16)
+        step = eng.prepare_step([seq], zeros, zeros[:, :2], zeros[:, :2])
+        graphed = pkv.GraphedDecoder(eng, 1, 4, 0.1)
+        want = nat.lib.pkv_attn_workspace_size(1, 2)
+        if bits == 4:
+            want = max(want, nat.lib.pkv_attn_int4_workspace_size())
+        for ws in (step.workspace, graphed.buckets[1].ws):
+            assert ws.buffer.numel() == want + 256
+
+
 def test_refusals_on_the_gpu(pkv):
     c = pkv.Int4Cache(4, 2)
     z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device="cuda")
