@@ -450,6 +450,16 @@ pkv_status pkv_attn_decode_int4(const void* q, const void* cache, const int32_t*
                                 int block_tokens, int group_dims, float scale, int num_ctas, void* workspace,
                                 size_t workspace_bytes, void* out, void* stream);
 
+/* pkv_attn_decode_int4, of groups of 64, for tests of its bounded waits only, as
+ * pkv_attn_decode_wait_test: CTA 0's producers copy the first stop_tiles (>= 0) tiles
+ * of 16 tokens a warp and no more. Zero the workspace's fixed bytes before its next use. */
+pkv_status pkv_attn_decode_int4_wait_test(const void* q, const void* cache, const int32_t* block_tables,
+                                          int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                                          int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
+                                          int block_tokens, int group_dims, float scale, int num_ctas,
+                                          void* workspace, size_t workspace_bytes, void* out, int stop_tiles,
+                                          void* stream);
+
 /*
  * pkv_beam_select -- beam search's selection: of each group of beams (the
  * hypotheses of one request, whose sequences share blocks: cs2680 Lecture 10,

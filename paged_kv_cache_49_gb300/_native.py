@@ -50,7 +50,8 @@ EXPORTED = [
     "pkv_attn_decode_wait_test", "pkv_attn_decode_cuda_cores", "pkv_attn_workspace_fixed_bytes",
     "pkv_attn_launch_ctas", "pkv_attn_prefill", "pkv_attn_prefill_workspace_size", "pkv_attn_tree",
     "pkv_qk_norm_rope_append", "pkv_int4_block_bytes", "pkv_append_int4", "pkv_load_int4", "pkv_block_copy_int4",
-    "pkv_attn_decode_int4", "pkv_attn_int4_workspace_size", "pkv_beam_select", "pkv_beam_workspace_size", "pkv_bm_reorder",
+    "pkv_attn_decode_int4", "pkv_attn_decode_int4_wait_test", "pkv_attn_int4_workspace_size", "pkv_beam_select",
+    "pkv_beam_workspace_size", "pkv_bm_reorder",
 ]
 BLOCK_SIZES = (8, 16, 32, 64)
 INT4_GROUP_DIMS = (32, 64, 128)
@@ -158,6 +159,8 @@ def _load() -> ctypes.CDLL:
         "pkv_block_copy_int4": (i32, [vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]),
         "pkv_attn_decode_int4": (i32, [vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz, vp,
                                        vp]),
+        "pkv_attn_decode_int4_wait_test": (i32, [vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz,
+                                                 vp, i32, vp]),
         "pkv_beam_workspace_size": (sz, [i32, i32, i32, i32]),
         "pkv_beam_select": (i32, [vp, i64, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp,
                                   sz, vp, vp]),

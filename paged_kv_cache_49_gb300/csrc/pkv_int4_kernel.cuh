@@ -118,6 +118,13 @@ struct Decode {
     float* partials;                     // [grid][2][rows][kORow]
 };
 
+// For tests of the bounded waits: CTA 0 copies no tiles from stop_tiles on.
+struct StoppedDecode : Decode {
+    int stop_tiles;
+};
+__device__ __forceinline__ bool stopped(const Decode&, int) { return false; }
+__device__ __forceinline__ bool stopped(const StoppedDecode& p, int tile) { return blockIdx.x == 0 && tile >= p.stop_tiles; }
+
 __device__ __forceinline__ uint64_t atom_add_acq_rel_gpu(unsigned long long* addr, uint64_t v) {
     uint64_t old;
     asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;" : "=l"(old) : "l"(addr), "l"(v) : "memory");
@@ -534,8 +541,8 @@ __device__ __forceinline__ uint2 rounded(float4 o, float inv) {
     return make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
-template <int kGroups>
-__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
+template <int kGroups, class Params>
+__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Params p) {
     using U = Unit<kGroups>;
     using L = Smem<kGroups>;
     extern __shared__ uint8_t smem_raw[];
@@ -677,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Decode p) {
                     src = reinterpret_cast<uint64_t>(p.cache) + unit_of(slot, pc.g * p.heads, p.hkv, blocks_of_8) * U::kBytes;
                 }
                 for (int j = 0; j < n; ++j, ++gi) {
-                    if (gi % kProducers != warp - kWarps) continue;
+                    if (gi % kProducers != warp - kWarps || stopped(p, gi)) continue;
                     const int st = gi % kStages;
                     // whole slabs: 16 tokens (8 in blocks of 8)
                     const int left = min(tile_tokens, ctx - (pc.blk + j0 + j) * tile_tokens);

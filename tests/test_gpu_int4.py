@@ -808,6 +808,34 @@ def test_engines_take_room_for_their_cache_alone(pkv):
             assert ws.buffer.numel() == want + 256
 
 
+@pytest.mark.parametrize("hkv,stop_tiles", [(4, 0), (4, 5), (4, 14), (1, 3)])
+def test_wait_runs_out_and_the_next_call_is_exact(pkv, hkv, stop_tiles):
+    """CTA 0's tiles from stop_tiles on never come: the call ends after a second, with the
+    error set, and the same calls as before give the same results."""
+    from paged_kv_cache_49_gb300 import _native as nat
+    rng = np.random.default_rng(30)
+    args, ws, want = _decode(pkv, rng, [1500, 300, 45], 2 * hkv, hkv, num_ctas=4)
+    want = want.clone()
+    q, cache, tables, ctx, scale = args
+    out, stream = torch.zeros_like(q), torch.cuda.current_stream().cuda_stream
+    call = lambda stop: nat.lib.pkv_attn_decode_int4_wait_test(
+        q.data_ptr(), cache.data.data_ptr(), tables.data_ptr(), tables.shape[1], ctx.data_ptr(), 3, 2 * hkv, hkv, 128, cache.num_blocks,
+        16, 64, scale, 4, ws.ptr, ws.for_int4(stream), out.data_ptr(), stop, stream)
+    assert call(-1) == nat.PKV_EINVAL
+    assert call(stop_tiles) == nat.PKV_OK
+    torch.cuda.synchronize()  # returns: the wait gave up instead of hanging
+    assert ws.read_error(clear=False) == pkv.DEVERR_TIMEOUT
+    nat.lib.pkv_attn_workspace_init(ws.ptr, ws.fixed_bytes(), stream)
+    for _ in range(2):
+        assert torch.equal(want, pkv.attn_decode_int4(*args, workspace=ws, num_ctas=4)) and ws.read_error() == 0
+    rows = _dev(pkv, _rows(rng, (5, hkv, 128)))
+    new = pkv.Int4Cache(2, hkv)
+    pkv.append_int4(rows, rows, torch.arange(5, device="cuda"), new)
+    k, v = (torch.zeros((2, hkv, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pkv.load_int4(new, torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"), k, v)
+    assert torch.equal(k, v) and k[1, :, :5].any() and not k[0].any() and not k[1, :, 5:].any()
+
+
 def test_refusals_on_the_gpu(pkv):
     c = pkv.Int4Cache(4, 2)
     z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device="cuda")

@@ -62,6 +62,13 @@ def test_c_calls_refuse(pkv):
         assert decode(**bad) == nat.PKV_ERANGE, bad
 
 
+def test_the_wait_test_refuses(pkv):
+    from paged_kv_cache_49_gb300 import _native as nat
+    call = lambda stop=0, gd=64, q=4096: nat.lib.pkv_attn_decode_int4_wait_test(
+        q, 4096, 4096, 4, 4096, 2, 32, 8, 128, 8, 16, gd, 0.1, 0, 4096, 1 << 20, 4096, stop, None)
+    assert call(stop=-1) == call(q=None) == nat.PKV_EINVAL and call(gd=32) == call(gd=128) == nat.PKV_EUNSUPPORTED
+
+
 def _cache(pkv, blocks=4, hkv=2, bt=16, gd=64):
     return pkv.Int4Cache(blocks, hkv, bt, gd, device="cpu")
 
