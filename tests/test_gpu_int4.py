@@ -493,6 +493,37 @@ def test_no_stretch_of_a_context_is_lost(pkv, lens, hq, hkv, num_ctas):
                 assert worst > 5, (b, lo, times, worst)
 
 
+@pytest.mark.parametrize("gd", [32, 64, 128])
+@pytest.mark.parametrize("lens,hkv", [([131_072], 4), ([131_072], 1), ([60_000, 50_001], 2)])
+def test_sums_of_long_pieces(pkv, lens, hkv, gd):
+    """A whole context in one piece, of values about zero whose codes and minima are two
+    large sums: the error over all outputs is that of independent roundings."""
+    rng = np.random.default_rng(31)
+    blocks = sum(-(-n // 64) for n in lens)
+    pool = Pool(pkv, rng, blocks, hkv, 64, gd)
+    tables = _batch(rng, lens, blocks, 64)
+    q = _bf16_rows(rng.standard_normal((len(lens), 2 * hkv, 128))).double().numpy()
+    got, (want, a, e) = _attend(pkv, pool, tables, lens, q, 0.05, num_ctas=1)
+    # bf16: 2^-8 of an output at most, evenly spread. Weights, and their products with the
+    # scales, in fp16: 2^-11 at most each, of terms whose squares' sum is that of n equal ones
+    # times at most max p / mean p; three such roundings. What the matrix unit cuts off of an
+    # fp32 sum: half a step of 2^-24 of it each time, over 8 turns of 4 tiles at most 32
+    # times, the sum being half of its last value on average.
+    for b, n in enumerate(lens):
+        t = np.arange(n)
+        spread = 0.0
+        for g in range(hkv):
+            key = int4.values(*(x[tables[b][t // 64], g, t % 64] for x in pool.k))
+            x = 0.05 * (q[b, 2 * g:2 * g + 2] @ key.T)
+            w = np.exp(x - x.max(axis=-1, keepdims=True))
+            w /= w.sum(axis=-1, keepdims=True)
+            spread = max(spread, np.sqrt((w ** 2).sum(axis=-1)).max())
+        rms = lambda x: np.sqrt((x ** 2).mean())
+        size = np.abs(a[b]).max()
+        bound = np.hypot(2.0 ** -8 / 3 ** 0.5 * rms(want[b]), 3 * 2.0 ** -11 / 3 ** 0.5 * spread * size) + 32 * 2.0 ** -26 * size
+        assert rms(got[b] - want[b]) <= bound, (rms(got[b] - want[b]), bound, rms(want[b]))
+
+
 def test_nan_where_it_is_seen(pkv):
     """A NaN in a key reaches its heads, one in a group of a value those dims."""
     rng = np.random.default_rng(14)
