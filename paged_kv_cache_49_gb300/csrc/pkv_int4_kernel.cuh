@@ -44,7 +44,7 @@
 // those with the same rows) finishes last.
 //
 // What bounds it: of 256 sequences of 11,200 tokens on average and 8 heads (3.3 GB)
-// the reading, 525 us, 6.3 TB/s; of 64 of 1,500 (111 MB, 32 us, 3.5 TB/s) the start
+// the reading, 547 us, 6.0 TB/s; of 64 of 1,500 (111 MB, 32 us, 3.5 TB/s) the start
 // (5 us until the first tiles land) and the unequal ends of the ranges; the matrix
 // products and what feeds them, 2,300 cycles for 64 tokens of 4 heads, fill three
 // quarters of the time between.
@@ -61,7 +61,8 @@ namespace pkv {
 namespace kv4 {
 
 constexpr int kMaxG = PKV_ATTN_MAX_GROUP;
-// With both sides measured, in us for one sequence / 64 / 256 / 200 of one KV head:
+// With both sides measured, each as the kernel was then, in us for one sequence / 64 /
+// 256 / 200 of one KV head:
 // 8 warps and heads take 128 registers a thread at most and spill (10.5 / 34.3 /
 // 558 / 22.9 with 4, 13.3 / 52.9 / 965 / 29.7 with 8); two tiles at a time overlap
 // less (10.5 / 33.8 / 594 / 21.5); a second producer gives 10.4 / 33.5 / 542 / 21.9;
@@ -75,9 +76,9 @@ static_assert(kStages % kSubs == 0 && kStages % kProducers == 0, "each stage is 
 constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + kProducers * 32;
 // Work partition: what a run costs beyond its tiles, in tiles (for 64 sequences /
-// 256 / 200 of one KV head 32.1 / 532.7 / 20.6 us with 4, 32.0 / 530.7 / 19.7 with
-// 6, 31.4 / 532.3 / 20.4 with 10; 1 and 3 were slower by 2 to 5 percent).
-constexpr int kRunCost = 6;
+// 256 / 200 of one KV head 32.9 / 551 / 21.2 us with 4, 32.9 / 546 / 20.4 with 6,
+// 32.0 / 547 / 20.5 with 10, 33.9 / 550 / 21.6 with 14).
+constexpr int kRunCost = 10;
 // Runs of more pieces than this are combined in two levels, each of up to 32.
 constexpr int kMergeGroup = 16;
 // Counters of a launch, 64 bits with one byte a warp, in the workspace's region
@@ -495,7 +496,7 @@ __device__ __forceinline__ float* partial(const Decode& p, int cta, int last, in
 // `stride` CTAs apart from CTA `first` on, combined; emit(row, four dims from 4 lane
 // on, max, sum). Lane k holds partial result k's maxima and sums of all rows, which
 // come first; then six results of four rows are on their way at a time (256
-// sequences: 533 us, 541 with four, which leaves the kernel's other values less room
+// sequences: 546 us, 553 with four, which leaves the kernel's other values less room
 // in registers).
 template <class Emit>
 __device__ __forceinline__ void combine(const Decode& p, int first, int stride, int count, int last, int row, int step, int rows,
@@ -550,8 +551,8 @@ __device__ __forceinline__ void combine(const Decode& p, int first, int stride, 
 
 // A row from the results of the warps that share its head, `stride` floats apart:
 // four dims from 4 lane on. (All loads at once: 200 sequences of one KV head 18.3 us,
-// 18.9 one after the other; a call, so that its registers are not the kernel's: 256
-// of 8 heads 525 us, 542 without.)
+// 18.9 one after the other. A call, so that its registers are not the kernel's: 256
+// of 8 heads 546 us, 552 without, though 200 of one KV head 20.4 and 19.0.)
 struct Row {
     float4 o;
     float max, sum;
@@ -762,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Params p) {
 
     // ======================= consumer warps =======================
     // The walk stays in shared memory between pieces: the registers are the sums'. (128
-    // sequences of 8,000 tokens: 224 us, 227 without.)
+    // sequences of 8,000 tokens, 32 turns held: 224 us, 227 without.)
     attn::PieceWalk* place = reinterpret_cast<attn::PieceWalk*>(smem + L::kWalks + warp * 64);
     static_assert(sizeof(attn::PieceWalk) <= 64, "a walk fits its place");
     {
@@ -795,8 +796,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Params p) {
         bool some = false;  // whether the warp has tokens of the piece
         // The piece's tiles from j to `stop`; false, with the last ones not yet given back,
         // where they are for the other kind of turn: the first ones, if their scales are all small,
-        // are taken again with lifted scales (`lift`), until there is one that is not. (A look
-        // at the scales ahead of every turn: 256 sequences 541 us, 532 with this.)
+        // are taken again with lifted scales (`lift`), until there is one that is not. (One
+        // loop for both, with a branch: 256 sequences 565 us, 547 with two.)
         int j = 0, stop = 0;
         auto tiles = [&](auto lift) {
             for (; j < stop; j += kSubs) {
