@@ -18,9 +18,10 @@
 // precision: neighbours of the last one taken may differ by less than fp32 holds.
 //
 // What bounds it: the scan of 64 groups of 4 beams over 131,072 tokens in bf16 (60
-// MB read) the exponentials, at 16 a cycle and SM two thirds of the time of
-// reading, and the instructions around them (11 for 32 logits, many of them a
-// CTA's for its cut and list): 14 us; the join, 6 us, a chain of latencies.
+// MB read, 14 us) that a CTA's phases do not overlap: it loads, then sums, then finds
+// its cut and list. Nothing is full (issue slots 58%, memory 38%, the exponentials'
+// unit 26%; 11 warp instructions for 32 logits, many of them a CTA's for its cut and
+// list). The join, 6 us, is a chain of latencies.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -92,7 +93,8 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 __device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
 // A number as the sum of two, the second below half a step of the first: 48 bits
-// or more from fp32 operations (64-bit ones run at 1/64 of their rate here).
+// or more from fp32 operations (64-bit ones run at 1/64 of their rate here). Knuth's
+// sum and Dekker's sums and products of such pairs.
 struct Pair {
     float hi, lo;
 };
