@@ -15,8 +15,11 @@ namespace kv4 {
 
 using KernelFn = void (*)(Decode);
 
-KernelFn kernel_for(int groups) {
-    return groups == 1 ? decode_kernel<1, Decode> : groups == 2 ? decode_kernel<2, Decode> : decode_kernel<4, Decode>;
+// shared: runs of fewer heads than warps.
+KernelFn kernel_for(int groups, bool shared) {
+    if (shared)
+        return groups == 1 ? decode_kernel<1, true, Decode> : groups == 2 ? decode_kernel<2, true, Decode> : decode_kernel<4, true, Decode>;
+    return groups == 1 ? decode_kernel<1, false, Decode> : groups == 2 ? decode_kernel<2, false, Decode> : decode_kernel<4, false, Decode>;
 }
 
 size_t smem_for(int groups, int num_seqs) {
@@ -38,11 +41,16 @@ int resident_ctas(int groups, int num_seqs) {
     std::lock_guard<std::mutex> lock(mu);
     for (const Entry& e : cache)
         if (e.dev == dev && e.groups == groups && e.smem == smem) return e.ctas;
-    const KernelFn fn = kernel_for(groups);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem_for(groups, PKV_ATTN_MAX_SEQS)));
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, smem);
+    cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    for (const bool shared : {false, true}) {  // (two CTAs an SM of either, as they are compiled for)
+        const KernelFn fn = kernel_for(groups, shared);
+        int here = 0;
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(smem_for(groups, PKV_ATTN_MAX_SEQS)));
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&here, fn, kThreads, smem);
+        per_sm = shared ? std::min(per_sm, here) : here;
+    }
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return 0;
@@ -127,15 +135,16 @@ pkv_status decode(const void* q, const void* cache, const int32_t* block_tables,
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t e = cudaSuccess;
+    const bool shared = p.heads < kWarps;
     if (stop_tiles < 0) {
-        e = cudaLaunchKernelEx(&cfg, kernel_for(groups), p);
+        e = cudaLaunchKernelEx(&cfg, kernel_for(groups, shared), p);
     } else {
         StoppedDecode stopped;
         static_cast<Decode&>(stopped) = p;
         stopped.stop_tiles = stop_tiles;
-        e = cudaFuncSetAttribute(decode_kernel<2, StoppedDecode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(cfg.dynamicSmemBytes));
-        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, decode_kernel<2, StoppedDecode>, stopped);
+        const auto fn = shared ? decode_kernel<2, true, StoppedDecode> : decode_kernel<2, false, StoppedDecode>;
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(cfg.dynamicSmemBytes));
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, fn, stopped);
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {

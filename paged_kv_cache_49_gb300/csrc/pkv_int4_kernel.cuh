@@ -551,13 +551,12 @@ __device__ __forceinline__ void combine(const Decode& p, int first, int stride, 
 
 // A row from the results of the warps that share its head, `stride` floats apart:
 // four dims from 4 lane on. (All loads at once: 200 sequences of one KV head 18.3 us,
-// 18.9 one after the other. A call, so that its registers are not the kernel's: 256
-// of 8 heads 546 us, 552 without, though 200 of one KV head 20.4 and 19.0.)
+// 18.9 one after the other.)
 struct Row {
     float4 o;
     float max, sum;
 };
-__device__ __noinline__ Row of_parts(const float* state, int stride, int parts, int lane) {
+__device__ __forceinline__ Row of_parts(const float* state, int stride, int parts, int lane) {
     float2 ml[kWarps];
     float4 v[kWarps];
     Row x = {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
@@ -582,7 +581,10 @@ __device__ __forceinline__ uint2 rounded(float4 o, float inv) {
     return make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
-template <int kGroups, class Params>
+// kShared: runs of fewer than kWarps heads, whose warps share them. (Compiled apart, since
+// either takes the registers that the other would have: 200 sequences of one KV head 19.4
+// us, 20.5 in one kernel, 64 of two 26.0 and 27.1; 256 of 8 heads 547 in both.)
+template <int kGroups, bool kShared, class Params>
 __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Params p) {
     using U = Unit<kGroups>;
     using L = Smem<kGroups>;
@@ -590,7 +592,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Params p) {
     uint8_t* smem = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = p.num_seqs, runs = p.runs;
-    const int parts = kWarps / p.heads, tile_tokens = kTok * parts;  // warps of a head, tokens of a tile
+    const int heads = kShared ? p.heads : kWarps;
+    const int parts = kWarps / heads, tile_tokens = kTok * parts;  // warps of a head, tokens of a tile
     int* scan = reinterpret_cast<int*>(smem + L::kScan);
     int* misc = reinterpret_cast<int*>(smem + L::kMisc);
     volatile int* abort_flag = misc;
@@ -706,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Params p) {
         attn::PieceWalk walk(scan, B, runs, range_lo, range_hi, first_piece);
         const uint64_t policy = policy_evict_first();
         const int ahead = 32 / p.copies;  // tiles whose copies' places the lanes hold
-        const uint32_t unit_row = static_cast<uint32_t>(p.heads) * U::kBytes;  // a unit of every head of the run
+        const uint32_t unit_row = static_cast<uint32_t>(heads) * U::kBytes;  // a unit of every head of the run
         int gi = 0, last_issued = -1;
         while (walk.next(pc)) {
             const int ctx = min(__ldg(p.context_lens + pc.s), p.cap);
@@ -722,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Params p) {
                         id = 0;  // a valid block in its place; the output is flagged invalid
                     }
                     const long long slot = (static_cast<long long>(id) << p.bt_shift) + (token & ((1 << p.bt_shift) - 1));
-                    src = reinterpret_cast<uint64_t>(p.cache) + unit_of(slot, pc.g * p.heads, p.hkv, blocks_of_8) * U::kBytes;
+                    src = reinterpret_cast<uint64_t>(p.cache) + unit_of(slot, pc.g * heads, p.hkv, blocks_of_8) * U::kBytes;
                 }
                 for (int j = 0; j < n; ++j, ++gi) {
                     if (gi % kProducers != warp - kWarps || stopped(p, gi)) continue;
@@ -772,10 +775,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Params p) {
         __syncwarp();
     }
     const int r = lane >> 2, c = lane & 3;
-    const int head = warp & (p.heads - 1), part = warp / p.heads;
+    const int head = warp & (heads - 1), part = warp / heads;
     // the warp's two units in a stage
-    const int second = blocks_of_8 ? p.heads * U::kBytes : U::kBytes;
-    const int own = blocks_of_8 ? (part * 2 * p.heads + head) * U::kBytes : (part * p.heads + head) * 2 * U::kBytes;
+    const int second = blocks_of_8 ? heads * U::kBytes : U::kBytes;
+    const int own = blocks_of_8 ? (part * 2 * heads + head) * U::kBytes : (part * heads + head) * 2 * U::kBytes;
     float* states = reinterpret_cast<float*>(smem + L::kStates);
     float4* kept = reinterpret_cast<float4*>(states + warp * kKeptFloats * 32) + lane;
     const int cta = static_cast<int>(blockIdx.x);
@@ -789,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Params p) {
         const int s = pc.s, nb = pc.nb;
         const int ctx = min(__ldg(p.context_lens + s), p.cap);
         Queries<kGroups> q;
-        q.load(p, s, pc.g * p.heads + head, r, c);
+        q.load(p, s, pc.g * heads + head, r, c);
         State<kGroups> st;
         st.clear();
         const int left = ctx - pc.blk * tile_tokens - part * kTok;  // of the context, from the warp's first token on
@@ -843,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Params p) {
             if (__builtin_expect(lifted, 0)) st.unlift();
             if (__builtin_expect(stop > kHold * kSubs, 0)) st.add_kept(kept);
             if (__builtin_expect(stop == pc.len, 1)) break;
-            if (stop == kHold * kSubs && parts > 1) named_barrier_sync(1, kConsumers);  // all have read the last piece's states
+            if (stop == kHold * kSubs && kShared) named_barrier_sync(1, kConsumers);  // all have read the last piece's states
             st.keep(kept);
         }
         gidx += pc.len;
@@ -856,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Params p) {
         int row = head * p.group, step = 1, rows = p.group;
         float mins[kGroups][2], sums[2];
         st.rows(c, mins, sums);
-        if (parts == 1) {
+        if (!kShared) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (2 * c + h >= p.group) continue;
@@ -895,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const Params p) {
             rows = (p.rows - warp + kWarps - 1) / kWarps;
             for (int j = 0; j < rows; ++j) {
                 const int mine = row + j * step, of = mine / p.group, h = mine - of * p.group;
-                const Row x = of_parts(states + (of * kMaxG + h) * kORow, p.heads * kMaxG * kORow, parts, lane);
+                const Row x = of_parts(states + (of * kMaxG + h) * kORow, heads * kMaxG * kORow, parts, lane);
                 if (pieces == 1) {
                     reinterpret_cast<uint2*>(out + mine * kDim)[lane] = rounded(x.o, 1.f / x.sum);
                 } else {
