@@ -79,7 +79,7 @@ def decode(q, k, v, tables, ctx, scale):
     """Decode attention over such a cache. q float64 [B, Hq, 128]; k, v: (codes, s,
     m) of the pool's rows [blocks, Hkv, block tokens, 128]. Returns float64 (out,
     a, e): a = sum_j softmax(x)_j (s c + |m|)_j, the size of the values' terms,
-    and e [B, Hq] = max_j scale * sum_d |q_d| (s c + |m|)_jd, that of the keys'."""
+    and e [B, Hq] = max_j |scale| * sum_d |q_d| (s c + |m|)_jd, that of the keys'."""
     B, Hq, _ = q.shape
     Hkv, bt = k[0].shape[1:3]
     G = Hq // Hkv
@@ -100,5 +100,5 @@ def decode(q, k, v, tables, ctx, scale):
                 w = np.exp(x - x.max(axis=-1, keepdims=True))
                 w /= w.sum(axis=-1, keepdims=True)
                 out[b, h], a[b, h] = w @ val, w @ vsz
-                e[b, h] = (scale * (np.abs(q[b, h]) @ ksz.T)).max(axis=-1)
+                e[b, h] = (abs(scale) * (np.abs(q[b, h]) @ ksz.T)).max(axis=-1)
     return out, a, e
